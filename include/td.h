@@ -71,7 +71,14 @@ typedef enum {
 #define TD_FLAG_SEQ_LEN_OUT_OF_RANGE 0x2u /* seq_lens[b] < 0 or > max_seq_len: clamped */
 #define TD_FLAG_WAIT_TIMEOUT 0x4u         /* a staged kernel's bounded wait for its copies gave up;
                                              that (batch, KV head)'s output lacks the tokens of
-                                             the CTA that gave up (the workspace stays usable) */
+                                             the CTA that gave up (the workspace stays usable).
+                                             td_tree_*: the rows of the CTA that gave up are not
+                                             valid */
+#define TD_FLAG_TREE_OUT_OF_RANGE 0x8u    /* tree_lens[b], accepted_lens[b] or an accepted node
+                                             outside its range: clamped / skipped */
+#define TD_FLAG_PAGE_OUT_OF_RANGE 0x10u   /* a page number, page count or slot outside the cache:
+                                             its tokens are skipped */
+#define TD_FLAG_PAGES_EXHAUSTED 0x20u     /* td_block_tables ran out of free pages or of slots */
 
 typedef struct {
     int32_t batch;          /* B  >= 1                                         */
@@ -346,6 +353,174 @@ td_status td_plan_create_append(td_plan **plan, const td_shape *shape, int32_t n
                                 const int32_t *seq_lens, int32_t top_k, int32_t *idx_buf,
                                 int32_t idx_valid, void *const *outs, float *const *outs_f32,
                                 void *ws, size_t ws_bytes);
+
+/*
+ * ---- Speculative decoding over the step's cache ----------------------------
+ *
+ * A draft model proposes several tokens per request, arranged as a tree; the
+ * target model attends for all of them in one step and keeps one root-to-leaf
+ * path.  One step of a batch is
+ *     td_block_tables        pages and slots for every request's new tokens
+ *     per layer:
+ *       td_kv_append_slots   the drafted tokens' K/V rows into the cache
+ *       td_tree_attn / td_tree_sparse_attn
+ *     td_tree_commit         the accepted rows of all layers, and the new lengths
+ *
+ * td_cache: one layer's K/V rows.
+ *   k, v     device bf16 [num_pages][num_kv_heads][page_size][128], 16-byte aligned.
+ *   block_table  device int32 [batch][max_blocks]: position p of request b is
+ *            row p % page_size of page block_table[b][p / page_size].  NULL: a
+ *            contiguous cache, request b owns page b (num_pages >= batch,
+ *            page_size = the max_seq_len of the other calls' k_cache).
+ *   Any page_size >= 1; num_pages * num_kv_heads * page_size < 2^31.  The
+ *   tree attention is fastest where a page divides 128 tokens (16, 32, 64,
+ *   128) or is a multiple of 128.
+ *   A page number outside [0, num_pages) is never followed: its tokens are
+ *   skipped and TD_FLAG_PAGE_OUT_OF_RANGE is set.  Entries of a table row
+ *   beyond its request's length are not read.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    int32_t num_pages;
+    int32_t page_size;
+    const int32_t *block_table;
+    int32_t max_blocks;
+} td_cache;
+
+#define TD_MAX_TREE 128   /* drafted tokens per request */
+
+/* Bytes of workspace td_tree_attn and td_tree_sparse_attn need for up to
+ * tree_size drafted tokens per request, beside what td_workspace_size asks
+ * for: a buffer that serves both kinds of calls holds the sum, one that serves
+ * only the tree calls just these.  The tree calls use the last bytes of the
+ * buffer and the status word at its start.  0 for an invalid shape or
+ * tree_size.  Does not touch the GPU. */
+size_t td_tree_workspace_size(const td_shape *shape, int32_t tree_size);
+
+/*
+ * Attention of a tree of drafted tokens, one layer.  Of request b's
+ * seq_lens[b] cached tokens the last n = tree_lens[b] are its drafted ones
+ * (their K/V rows are already in the cache); c = seq_lens[b] - n precede them.
+ * Drafted token t < n attends to the positions
+ *     { 0 .. c - 1 }  and  { c + j : j < n and bit j of tree_mask[b][t] set },
+ * in one softmax:  out[b][t][h] = sum_p softmax(scale * q[b][t][h] . K[p]) V[p].
+ *   tree_size  T, 1 .. TD_MAX_TREE: rows per request of q, out and tree_mask.
+ *   tree_lens  device int32 [batch], 0 <= tree_lens[b] <= min(T, seq_lens[b]);
+ *              NULL: T drafted tokens in every request.
+ *   tree_mask  device [batch][T][ceil(T / 32)] words: bit j % 32 of word j / 32
+ *              lets the row see drafted token j (a token sees itself only where
+ *              its own bit is set; bits j >= n are ignored).  NULL: a chain,
+ *              token t sees 0 .. t.
+ *   q, out     device bf16 [batch][T][num_q_heads][128], 16-byte aligned.
+ *   Rows t >= n of out are left as they were.  A row that sees no position
+ *   gets 0.  T = 1 with a NULL mask is plain decoding over the cache.
+ *   shape      max_seq_len bounds seq_lens (a longer one is clamped and
+ *              flagged); it must fit max_blocks * page_size (page_size for a
+ *              NULL block_table).
+ * K/V values at positions a row does not see never reach it, whatever they
+ * hold (infinities and NaN included).  The probabilities enter the second
+ * product as bf16 (relative error 2^-9 each); scores, softmax statistics and
+ * sums are fp32.
+ */
+td_status td_tree_attn(const td_shape *shape, const td_cache *cache, int32_t tree_size,
+                       const int32_t *tree_lens, const uint32_t *tree_mask, const void *q,
+                       const int32_t *seq_lens, void *out, void *ws, size_t ws_bytes,
+                       void *stream);
+
+/*
+ * The same for a PPSA layer: the positions { 0 .. c - 1 } above are replaced
+ * by the persisted set { idx[b][g][i] } of the row's KV head g (as for
+ * td_sparse_attn: distinct, any order, -1 is padding).  An entry outside
+ * [-1, c) is skipped and sets TD_FLAG_INDEX_OUT_OF_RANGE.  The drafted tokens
+ * stay visible as the mask says.
+ *   idx  device int32 [batch][num_kv_heads][top_k], 1 <= top_k <= max_seq_len.
+ */
+td_status td_tree_sparse_attn(const td_shape *shape, const td_cache *cache, int32_t tree_size,
+                              const int32_t *tree_lens, const uint32_t *tree_mask, const void *q,
+                              const int32_t *seq_lens, const int32_t *idx, int32_t top_k,
+                              void *out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Keep the accepted tokens of a drafted tree, in every layer: with c as above,
+ * cache row c + i becomes what row c + accepted[b][i] held before the call,
+ * for i < accepted_lens[b], and seq_lens_out[b] = c + accepted_lens[b].  Other
+ * rows keep their values.
+ *   caches         HOST array of num_layers caches: the same geometry and the
+ *                  same block_table, distinct k and v.
+ *   accepted       device int32 [batch][tree_size]: drafted token numbers, in
+ *                  the order they are kept, each in [0, tree_lens[b]) (any
+ *                  order; one outside is flagged and its row kept as it was).
+ *   accepted_lens  device int32 [batch], 0 .. tree_lens[b].
+ *   seq_lens_out   device int32 [batch], not overlapping seq_lens, tree_lens,
+ *                  accepted or accepted_lens.
+ *   Requests must not share the pages of their drafted tokens.
+ * The workspace is used for its status word only.
+ */
+td_status td_tree_commit(const td_shape *shape, int32_t num_layers, const td_cache *caches,
+                         int32_t tree_size, const int32_t *tree_lens, const int32_t *accepted,
+                         const int32_t *accepted_lens, const int32_t *seq_lens,
+                         int32_t *seq_lens_out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * New K/V rows of a packed batch into one layer's cache: row i goes to page
+ * slot_map[i] / page_size, row slot_map[i] % page_size of every KV head.
+ *   k_new, v_new  device bf16, row i at k_new + i * new_stride values: the
+ *                 num_kv_heads * 128 values of token i; 16-byte aligned.
+ *   new_stride    values between two tokens' rows, a multiple of 8 and at
+ *                 least num_kv_heads * 128 (packed projections have more).
+ *   slot_map      device int32 [num_tokens]; a negative entry writes nothing,
+ *                 one at or beyond num_pages * page_size neither (no flag: the
+ *                 call has no workspace).  Slots must be distinct.
+ *   num_tokens >= 0.  shape gives num_kv_heads and head_dim; the cache's
+ *   block_table is not read.
+ */
+td_status td_kv_append_slots(const td_shape *shape, const td_cache *cache, int32_t num_tokens,
+                             const void *k_new, const void *v_new, int64_t new_stride,
+                             const int32_t *slot_map, void *stream);
+
+/*
+ * Block tables and the slot map of a batch, from its lengths: request b is to
+ * hold target = ceil(seq_lens[b] / page_size) pages, the last new_lens[b] of
+ * its tokens are new.  Deterministic:
+ *   1. pages a request holds beyond its target (table entries target ..
+ *      num_blocks[b] - 1) are pushed on the free stack, requests and entries
+ *      ascending; the table keeps the stale entries.
+ *   2. entries num_blocks[b] .. target - 1 are filled by popping, requests and
+ *      entries ascending: the r-th page popped is the r-th from the top.
+ *   3. without enough free pages, the first request that does not get all of
+ *      its pages and every later one that needs any get none
+ *      (TD_FLAG_PAGES_EXHAUSTED): they keep what they hold.
+ *   4. cu_new[b] = new_lens[0] + .. + new_lens[b - 1]; new token i of request
+ *      b, at position p = seq_lens[b] - new_lens[b] + i, gets
+ *      slot_map[cu_new[b] + i] = table[b][p / page_size] * page_size + p % page_size,
+ *      or -1 where the request holds no page for it.
+ * A request that finished has seq_lens[b] = 0: all of its pages return.
+ *   block_table    device int32 [batch][max_blocks], updated.
+ *   num_blocks     device int32 [batch]: pages held on entry.
+ *   num_blocks_out device int32 [batch]: pages held after; may be num_blocks.
+ *   free_pages     device int32 [num_pages]: the stack, entries 0 .. free_count - 1;
+ *                  updated.  Entries beyond the new top are unspecified.
+ *   free_count     device int32 [1]; free_count_out [1] may be free_count.
+ *   cu_new         device int32 [batch + 1], written.
+ *   slot_map       device int32 [max_new], written whole: -1 beyond the last
+ *                  new token.  More than max_new new tokens: the rest is left
+ *                  out and TD_FLAG_PAGES_EXHAUSTED is set.
+ * With separate out arrays a call can be repeated with the same result.  A
+ * length outside [0, max_blocks * page_size], or new_lens[b] outside
+ * [0, seq_lens[b]], is clamped (TD_FLAG_SEQ_LEN_OUT_OF_RANGE); a page count
+ * outside its range is clamped and a page number outside [0, num_pages) gives
+ * slot -1 (TD_FLAG_PAGE_OUT_OF_RANGE).
+ *   1 <= batch <= 65535, max_blocks * page_size and num_pages * page_size
+ *   < 2^31.  Arrays other than the two out pairs must not overlap.
+ * The workspace is used for its status word only.
+ */
+td_status td_block_tables(int32_t batch, int32_t page_size, int32_t max_blocks, int32_t num_pages,
+                          const int32_t *seq_lens, const int32_t *new_lens, int32_t *block_table,
+                          const int32_t *num_blocks, int32_t *num_blocks_out,
+                          int32_t *free_pages, const int32_t *free_count,
+                          int32_t *free_count_out, int32_t *cu_new, int32_t *slot_map,
+                          int32_t max_new, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Measurement aid (not part of the decode step): reads exactly the K/V rows

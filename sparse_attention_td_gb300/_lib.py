@@ -13,6 +13,10 @@ MODE_SPARSE = 2
 FLAG_INDEX_OUT_OF_RANGE = 0x1
 FLAG_SEQ_LEN_OUT_OF_RANGE = 0x2
 FLAG_WAIT_TIMEOUT = 0x4
+FLAG_TREE_OUT_OF_RANGE = 0x8
+FLAG_PAGE_OUT_OF_RANGE = 0x10
+FLAG_PAGES_EXHAUSTED = 0x20
+MAX_TREE = 128                   # TD_MAX_TREE: drafted tokens per request of a tree call
 NOALLOC_SCRATCH_BYTES = 8 << 20  # TD_NOALLOC_SCRATCH_BYTES: td_sparse_attn_noalloc's fixed scratch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +40,12 @@ class Shape(ctypes.Structure):
     @property
     def group(self) -> int:
         return self.num_q_heads // self.num_kv_heads
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("block_table", ctypes.c_void_p),
+                ("max_blocks", ctypes.c_int32)]
 
 
 def default_scale(head_dim: int) -> float:
@@ -94,6 +104,19 @@ def lib():
                                       i32, vp, i32, vp, vpp, vp, vp, sz]
     L.td_index_overlap.restype = ctypes.c_int
     L.td_index_overlap.argtypes = [shp, vp, vp, i32, vp, vp]
+    cch, i64 = ctypes.POINTER(_Cache), ctypes.c_int64
+    L.td_tree_workspace_size.restype = sz
+    L.td_tree_workspace_size.argtypes = [shp, i32]
+    L.td_tree_attn.restype = ctypes.c_int
+    L.td_tree_attn.argtypes = [shp, cch, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.td_tree_sparse_attn.restype = ctypes.c_int
+    L.td_tree_sparse_attn.argtypes = [shp, cch, i32, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    L.td_tree_commit.restype = ctypes.c_int
+    L.td_tree_commit.argtypes = [shp, i32, cch, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.td_kv_append_slots.restype = ctypes.c_int
+    L.td_kv_append_slots.argtypes = [shp, cch, i32, vp, vp, i64, vp, vp]
+    L.td_block_tables.restype = ctypes.c_int
+    L.td_block_tables.argtypes = [i32, i32, i32, i32] + [vp] * 10 + [i32, vp, sz, vp]
     L.td_sparse_attn.restype = ctypes.c_int
     L.td_sparse_attn.argtypes = [shp, vp, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
     L.td_sparse_attn_noalloc.restype = ctypes.c_int
@@ -175,13 +198,23 @@ def td_workspace_status(ws: torch.Tensor, stream=None) -> int:
     return flags.value
 
 
-class Workspace:
-    """A zero-initialised device workspace of td_workspace_size bytes."""
+def td_tree_workspace_size(shape: Shape, tree_size: int) -> int:
+    return int(lib().td_tree_workspace_size(ctypes.byref(shape), int(tree_size)))
 
-    def __init__(self, shape: Shape, top_k: int, device=None, stream=None):
+
+class Workspace:
+    """A zero-initialised device workspace of td_workspace_size bytes; with
+    tree_size also td_tree_workspace_size bytes, for the tree calls."""
+
+    def __init__(self, shape: Shape, top_k: int, device=None, stream=None, tree_size: int = 0):
         n = td_workspace_size(shape, top_k)
         if n == 0:
             raise TdError(1, "td_workspace_size")
+        if tree_size:
+            more = td_tree_workspace_size(shape, tree_size)
+            if more == 0:
+                raise TdError(1, "td_tree_workspace_size")
+            n += more
         self.tensor = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
         td_workspace_init(self.tensor, stream)
 
@@ -284,6 +317,148 @@ def td_sparse_attn_noalloc(shape: Shape, q, k_cache, v_cache, seq_lens, idx, top
 def _ptr_array(tensors, name, dtype, numel, optional=False):
     ptrs = [_dev(t, f"{name}[{i}]", dtype, numel, optional) or 0 for i, t in enumerate(tensors)]
     return (ctypes.c_void_p * max(len(ptrs), 1))(*ptrs)
+
+
+def _here(tensors, stream=None):
+    """The call launches on the current device: every tensor has to live there."""
+    dev = torch.cuda.current_device()
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{dev}")
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+class Cache:
+    """One layer's K/V rows (td_cache): k, v [pages][Hkv][page_size][128] and a
+    block table [B][max_blocks], or without a table a contiguous cache
+    [B][Hkv][max_seq_len][128]."""
+
+    def __init__(self, k, v, block_table=None):
+        for name, t in (("k", k), ("v", v)):
+            if t.dim() != 4 or t.shape[3] != 128:
+                raise ValueError(f"{name} must be [pages][kv heads][page size][128], got {tuple(t.shape)}")
+        if k.shape != v.shape:
+            raise ValueError(f"k and v differ: {tuple(k.shape)} and {tuple(v.shape)}")
+        if block_table is not None and block_table.dim() != 2:
+            raise ValueError("block_table must be [batch][max_blocks]")
+        self.k, self.v, self.block_table = k, v, block_table
+        self.num_pages, self.kv_heads, self.page_size = (int(x) for x in k.shape[:3])
+        self.c = _Cache(_dev(k, "k", torch.bfloat16), _dev(v, "v", torch.bfloat16), self.num_pages,
+                        self.page_size, _dev(block_table, "block_table", torch.int32, optional=True),
+                        0 if block_table is None else int(block_table.shape[1]))
+
+    def check(self, shape: Shape):
+        if self.kv_heads != shape.num_kv_heads:
+            raise ValueError(f"the cache has {self.kv_heads} KV heads, the shape {shape.num_kv_heads}")
+        if self.block_table is not None and self.block_table.shape[0] < shape.batch:
+            raise ValueError(f"block_table has {self.block_table.shape[0]} rows, needs {shape.batch}")
+        return self
+
+    def tensors(self):
+        return {"k": self.k, "v": self.v, "block_table": self.block_table}
+
+
+def make_cache(k, v, block_table=None) -> Cache:
+    return Cache(k, v, block_table)
+
+
+def _tree(shape, cache, tree_size, tree_lens, tree_mask, q, seq_lens, out, ws, stream, **more):
+    cache.check(shape)
+    _here({**cache.tensors(), "tree_lens": tree_lens, "tree_mask": tree_mask, "q": q,
+           "seq_lens": seq_lens, "out": out, "ws": ws.tensor, **more}, stream)
+    nb, T = shape.batch, int(tree_size)
+    n = nb * T * shape.num_q_heads * shape.head_dim
+    return (ctypes.byref(shape), ctypes.byref(cache.c), T,
+            _dev(tree_lens, "tree_lens", torch.int32, nb, True),
+            _dev(tree_mask, "tree_mask", torch.int32, nb * T * ((T + 31) // 32), True),
+            _dev(q, "q", torch.bfloat16, n), _dev(seq_lens, "seq_lens", torch.int32, nb),
+            _dev(out, "out", torch.bfloat16, n))
+
+
+def td_tree_attn(shape: Shape, cache: Cache, tree_size, tree_lens, tree_mask, q, seq_lens, out,
+                 ws: Workspace = None, stream=None):
+    """Attention of tree_size drafted tokens per request over the cache;
+    tree_mask int32 words [B][T][ceil(T / 32)] (None: a chain)."""
+    a = _tree(shape, cache, tree_size, tree_lens, tree_mask, q, seq_lens, out, ws, stream)
+    _check(lib().td_tree_attn(*a, ws.ptr, ws.nbytes, _stream(stream)), "td_tree_attn")
+
+
+def td_tree_sparse_attn(shape: Shape, cache: Cache, tree_size, tree_lens, tree_mask, q, seq_lens,
+                        idx, top_k, out, ws: Workspace = None, stream=None):
+    """td_tree_attn over the persisted index set of a PPSA layer and the tree."""
+    *a, po = _tree(shape, cache, tree_size, tree_lens, tree_mask, q, seq_lens, out, ws, stream,
+                   idx=idx)
+    pi = _dev(idx, "idx", torch.int32, shape.batch * shape.num_kv_heads * int(top_k))
+    _check(lib().td_tree_sparse_attn(*a, pi, int(top_k), po, ws.ptr, ws.nbytes, _stream(stream)),
+           "td_tree_sparse_attn")
+
+
+def td_tree_commit(shape: Shape, caches: Sequence[Cache], tree_size, tree_lens, accepted,
+                   accepted_lens, seq_lens, seq_lens_out, ws: Workspace = None, stream=None):
+    """Move the accepted drafted rows of every layer to the front of their tree."""
+    nb, T = shape.batch, int(tree_size)
+    for c in caches:
+        c.check(shape)
+        _here(c.tensors(), stream)
+    _here({"tree_lens": tree_lens, "accepted": accepted, "accepted_lens": accepted_lens,
+           "seq_lens": seq_lens, "seq_lens_out": seq_lens_out, "ws": ws.tensor}, stream)
+    arr = (_Cache * max(len(caches), 1))(*[c.c for c in caches])
+    st = lib().td_tree_commit(
+        ctypes.byref(shape), len(caches), arr, T, _dev(tree_lens, "tree_lens", torch.int32, nb, True),
+        _dev(accepted, "accepted", torch.int32, nb * T),
+        _dev(accepted_lens, "accepted_lens", torch.int32, nb),
+        _dev(seq_lens, "seq_lens", torch.int32, nb),
+        _dev(seq_lens_out, "seq_lens_out", torch.int32, nb), ws.ptr, ws.nbytes, _stream(stream))
+    _check(st, "td_tree_commit")
+
+
+def _token_rows(t, name, heads):
+    """A [tokens][heads][128] tensor whose token rows may lie apart (a column
+    block of a packed projection): its pointer and token stride in values."""
+    if not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or t.stride(2) != 1 or \
+            (heads > 1 and t.stride(1) != 128):
+        raise ValueError(f"{name} must be [tokens][{heads}][128] with whole token rows")
+    return t.data_ptr(), int(t.stride(0)) if t.shape[0] > 1 else heads * 128
+
+
+def td_kv_append_slots(shape: Shape, cache: Cache, k_new, v_new, slot_map, stream=None):
+    """New K/V rows [tokens][Hkv][128] into the cache at slot_map [tokens]."""
+    cache.check(shape)
+    _here({**cache.tensors(), "k_new": k_new, "v_new": v_new, "slot_map": slot_map}, stream)
+    pk, sk = _token_rows(k_new, "k_new", shape.num_kv_heads)
+    pv, sv = _token_rows(v_new, "v_new", shape.num_kv_heads)
+    n = int(k_new.shape[0])
+    if v_new.shape[0] != n or sk != sv:
+        raise ValueError("k_new and v_new must have the same tokens and token stride")
+    st = lib().td_kv_append_slots(ctypes.byref(shape), ctypes.byref(cache.c), n, pk, pv, sk,
+                                  _dev(slot_map, "slot_map", torch.int32, n), _stream(stream))
+    _check(st, "td_kv_append_slots")
+
+
+def td_block_tables(seq_lens, new_lens, page_size, block_table, num_blocks, num_blocks_out,
+                    free_pages, free_count, free_count_out, cu_new, slot_map,
+                    ws: Workspace = None, stream=None):
+    """Block tables and slot map of a batch from its lengths; sizes come from
+    block_table [B][max_blocks], free_pages [num_pages] and slot_map [max_new]."""
+    _here({"seq_lens": seq_lens, "new_lens": new_lens, "block_table": block_table,
+           "num_blocks": num_blocks, "num_blocks_out": num_blocks_out, "free_pages": free_pages,
+           "free_count": free_count, "free_count_out": free_count_out, "cu_new": cu_new,
+           "slot_map": slot_map, "ws": ws.tensor}, stream)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][max_blocks]")
+    B, blocks = (int(x) for x in block_table.shape)
+    i32 = torch.int32
+    st = lib().td_block_tables(
+        B, int(page_size), blocks, int(free_pages.numel()), _dev(seq_lens, "seq_lens", i32, B),
+        _dev(new_lens, "new_lens", i32, B), _dev(block_table, "block_table", i32),
+        _dev(num_blocks, "num_blocks", i32, B), _dev(num_blocks_out, "num_blocks_out", i32, B),
+        _dev(free_pages, "free_pages", i32), _dev(free_count, "free_count", i32, 1),
+        _dev(free_count_out, "free_count_out", i32, 1), _dev(cu_new, "cu_new", i32, B + 1),
+        _dev(slot_map, "slot_map", i32), int(slot_map.numel()), ws.ptr, ws.nbytes, _stream(stream))
+    _check(st, "td_block_tables")
 
 
 class _StepArgs:

@@ -19,6 +19,7 @@
 
 #include "../../include/td.h"
 #include "td_internal.h"
+#include "td_spec.h"
 
 namespace {
 
@@ -981,6 +982,13 @@ td_status create_plan(td_plan **plan, const td_shape *shape, int32_t num_layers,
 }
 
 }  // namespace
+
+// Host helpers shared with the speculative-decoding entry points.
+namespace td {
+td_status host_check_shape(const td_shape *s) { return check_shape(s); }
+float host_scale(const td_shape &s) { return effective_scale(s); }
+int host_sm_count() { return device_sm_count(); }
+}  // namespace td
 
 extern "C" {
 

@@ -1,0 +1,98 @@
+// td_spec.h -- kernel arguments, launchers and host helpers of the
+// speculative-decoding operators (tree attention, commit, slot append, block
+// tables), shared by td_tree.cu, td_pages.cu, td_spec_api.cu and td_api.cu
+// (not part of the public C ABI).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/td.h"
+#include "td_internal.h"
+
+namespace td {
+
+constexpr uint32_t kFlagTreeOutOfRange = 0x8u;
+constexpr uint32_t kFlagPageOutOfRange = 0x10u;
+constexpr uint32_t kFlagPagesExhausted = 0x20u;
+
+// One layer's rows: k / v [num_pages][Hkv][page_size][128]; table null: request b owns page b.
+struct CacheArgs {
+    uint16_t *k, *v;
+    const int32_t *table;    // [B][max_blocks]
+    int num_pages, page_size, max_blocks;
+};
+
+struct TreeArgs {
+    CacheArgs c;
+    const uint16_t *q;          // [B][T][Hq][128]
+    uint16_t *out;              // [B][T][Hq][128]
+    const int32_t *seq_lens;    // [B]
+    const int32_t *tree_lens;   // [B], or null: T everywhere
+    const uint32_t *mask;       // [B][T][W], or null: chain
+    const int32_t *idx;         // sparse layer: [B][Hkv][top_k], or null
+    uint32_t *status;
+    int B, T, W, Hq, Hkv, Nmax, top_k;
+    float scale;                // softmax scale (natural-log units)
+};
+cudaError_t launch_tree_attention(const TreeArgs &a, cudaStream_t stream);
+
+// Accepted rows of up to kAppendLayers layers in one launch.
+struct CommitArgs {
+    uint16_t *k[kAppendLayers];
+    uint16_t *v[kAppendLayers];
+    const int32_t *table;
+    const int32_t *seq_lens, *tree_lens, *accepted, *accepted_lens;
+    int32_t *seq_lens_out;      // null: not this launch
+    uint32_t *status;
+    int B, T, Hkv, Nmax, num_pages, page_size, max_blocks;
+};
+cudaError_t launch_tree_commit(const CommitArgs &a, int num_layers, cudaStream_t stream);
+
+struct AppendSlotsArgs {
+    uint16_t *k, *v;
+    const uint16_t *k_new, *v_new;
+    const int32_t *slots;
+    int64_t new_stride;
+    int tokens, Hkv, num_pages, page_size;
+};
+cudaError_t launch_append_slots(const AppendSlotsArgs &a, cudaStream_t stream);
+
+struct TablesArgs {
+    const int32_t *seq_lens, *new_lens, *held, *count;
+    int32_t *table, *held_out, *free_pages, *count_out, *cu_new, *slots;
+    uint32_t *status;
+    int B, page_size, max_blocks, num_pages, max_new;
+};
+cudaError_t launch_block_tables(const TablesArgs &a, cudaStream_t stream);
+
+// Request b's lengths as every kernel of this family reads them: seq_lens
+// clamped to [0, Nmax], tree_lens to [0, min(T, n)].  `bad` collects the
+// status bits of what was clamped.
+struct TreeLens {
+    int n;      // cached tokens, drafted ones included
+    int nt;     // drafted tokens
+};
+__device__ __forceinline__ TreeLens tree_lens_of(const int32_t *seq_lens, const int32_t *tree_lens,
+                                                 int b, int T, int Nmax, uint32_t &bad)
+{
+    const int raw = seq_lens[b];
+    TreeLens r;
+    r.n = raw < 0 ? 0 : (raw > Nmax ? Nmax : raw);
+    if (r.n != raw)
+        bad |= kFlagSeqLenOutOfRange;
+    const int t = tree_lens ? tree_lens[b] : T;
+    const int most = T < r.n ? T : r.n;
+    r.nt = t < 0 ? 0 : (t > most ? most : t);
+    if (r.nt != t)
+        bad |= kFlagTreeOutOfRange;
+    return r;
+}
+
+// Host helpers of td_api.cu.
+td_status host_check_shape(const td_shape *s);
+float host_scale(const td_shape &s);
+int host_sm_count();
+
+}  // namespace td
