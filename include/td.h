@@ -416,8 +416,8 @@ size_t td_tree_workspace_size(const td_shape *shape, int32_t tree_size);
  *   Rows t >= n of out are left as they were.  A row that sees no position
  *   gets 0.  T = 1 with a NULL mask is plain decoding over the cache.
  *   shape      max_seq_len bounds seq_lens (a longer one is clamped and
- *              flagged); it must fit max_blocks * page_size (page_size for a
- *              NULL block_table).
+ *              flagged); at most 2^30, and it must fit max_blocks * page_size
+ *              (page_size for a NULL block_table).
  * K/V values at positions a row does not see never reach it, whatever they
  * hold (infinities and NaN included).  The probabilities enter the second
  * product as bf16 (relative error 2^-9 each); scores, softmax statistics and

@@ -988,6 +988,20 @@ namespace td {
 td_status host_check_shape(const td_shape *s) { return check_shape(s); }
 float host_scale(const td_shape &s) { return effective_scale(s); }
 int host_sm_count() { return device_sm_count(); }
+bool host_box_map(TmaDesc *out, const void *base, long rows, int box_rows)
+{
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn || rows < 1 || rows >= (1L << 31) || !aligned(base, 16))
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t elem[2] = {1, 1};
+    return fn(reinterpret_cast<CUtensorMap *>(out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace td
 
 extern "C" {

@@ -24,7 +24,12 @@ struct CacheArgs {
     int num_pages, page_size, max_blocks;
 };
 
+// CTAs of a tree attention launch: one per SM, at most this many (it sizes the partials).
+constexpr int kMaxTreeCtas = 160;
+
 struct TreeArgs {
+    TmaDesc box_k, box_v;       // rows as boxes of 64 values x box_rows rows, 128-byte swizzle
+    TmaDesc row_k, row_v;       // the same rows as boxes of one row, for row gathers
     CacheArgs c;
     const uint16_t *q;          // [B][T][Hq][128]
     uint16_t *out;              // [B][T][Hq][128]
@@ -33,10 +38,18 @@ struct TreeArgs {
     const uint32_t *mask;       // [B][T][W], or null: chain
     const int32_t *idx;         // sparse layer: [B][Hkv][top_k], or null
     uint32_t *status;
-    int B, T, W, Hq, Hkv, Nmax, top_k;
+    long long *prefix;          // [B + 1] work items before each request (written by the kernel)
+    float *part_m, *part_l;     // [2 * ctas][part_rows]
+    float *part_o;              // [2 * ctas][part_rows][128]
+    int B, T, W, Hq, Hkv, G, Nmax, top_k;
+    int box_rows;               // 0: no boxes, every tile is gathered
+    int oob_row;                // first row past the maps (reads zeros)
+    int part_rows;
     float scale;                // softmax scale (natural-log units)
 };
-cudaError_t launch_tree_attention(const TreeArgs &a, cudaStream_t stream);
+// Rows one work unit of a launch with T * G query rows per KV head can have.
+inline int tree_part_rows(int rows) { return rows <= 128 ? rows : 256; }
+cudaError_t launch_tree_attention(const TreeArgs &a, int sms, cudaStream_t stream);
 
 // Accepted rows of up to kAppendLayers layers in one launch.
 struct CommitArgs {
@@ -94,5 +107,8 @@ __device__ __forceinline__ TreeLens tree_lens_of(const int32_t *seq_lens, const 
 td_status host_check_shape(const td_shape *s);
 float host_scale(const td_shape &s);
 int host_sm_count();
+// Tensor map over `rows` rows of 128 bf16 values: boxes of 64 values x box_rows
+// rows, 128-byte swizzle, zero fill past the end.
+bool host_box_map(TmaDesc *out, const void *base, long rows, int box_rows);
 
 }  // namespace td

@@ -47,6 +47,31 @@ td_status check_cache(const td_shape &s, const td_cache *c, bool positions)
     return TD_OK;
 }
 
+// Workspace of the tree attention: the status word at the buffer's start, the
+// rest at its end (offsets from the start of that part).
+struct TreeWs {
+    size_t prefix, part_m, part_l, part_o, total;
+};
+
+TreeWs tree_ws(const td_shape &s, int tree_size)
+{
+    const size_t align = kAlign - 1;
+    const size_t rows = 2 * (size_t)td::kMaxTreeCtas *
+                        td::tree_part_rows(tree_size * (s.num_q_heads / s.num_kv_heads));
+    TreeWs w{};
+    size_t off = 0;
+    w.prefix = off;
+    off += (((size_t)s.batch + 1) * sizeof(long long) + align) & ~align;
+    w.part_m = off;
+    off += (rows * sizeof(float) + align) & ~align;
+    w.part_l = off;
+    off += (rows * sizeof(float) + align) & ~align;
+    w.part_o = off;
+    off += rows * kHeadDim * sizeof(float);
+    w.total = kAlign + off;
+    return w;
+}
+
 td::CacheArgs cache_args(const td_cache &c)
 {
     return td::CacheArgs{(uint16_t *)c.k, (uint16_t *)c.v, c.block_table, c.num_pages, c.page_size,
@@ -63,6 +88,8 @@ td_status run_tree(const td_shape *shape, const td_cache *cache, int32_t tree_si
         return st;
     if (tree_size < 1 || tree_size > TD_MAX_TREE)
         return TD_ERR_INVALID_ARG;
+    if (shape->max_seq_len > (1 << 30))     // positions stay below 2^31 when rounded up to tiles
+        return TD_ERR_UNSUPPORTED_SHAPE;
     st = check_cache(*shape, cache, true);
     if (st)
         return st;
@@ -82,6 +109,23 @@ td_status run_tree(const td_shape *shape, const td_cache *cache, int32_t tree_si
     a.mask = tree_mask;
     a.idx = idx;
     a.status = (uint32_t *)ws;
+    a.G = shape->num_q_heads / shape->num_kv_heads;
+    a.part_rows = td::tree_part_rows(tree_size * a.G);
+    const TreeWs w = tree_ws(*shape, tree_size);
+    char *base = (char *)ws + (ws_bytes - (w.total - kAlign)) / kAlign * kAlign;
+    a.prefix = (long long *)(base + w.prefix);
+    a.part_m = (float *)(base + w.part_m);
+    a.part_l = (float *)(base + w.part_l);
+    a.part_o = (float *)(base + w.part_o);
+    const long rows = (long)cache->num_pages * shape->num_kv_heads * cache->page_size;
+    const int ps = cache->page_size;
+    a.box_rows = !cache->block_table || ps % 128 == 0 ? 128 : ps >= 8 && 128 % ps == 0 ? ps : 0;
+    a.oob_row = (int)rows;
+    if (!td::host_box_map(&a.box_k, cache->k, rows, a.box_rows ? a.box_rows : 1) ||
+        !td::host_box_map(&a.box_v, cache->v, rows, a.box_rows ? a.box_rows : 1) ||
+        !td::host_box_map(&a.row_k, cache->k, rows, 1) ||
+        !td::host_box_map(&a.row_v, cache->v, rows, 1))
+        return TD_ERR_CUDA;
     a.B = shape->batch;
     a.T = tree_size;
     a.W = (tree_size + 31) / 32;
@@ -90,7 +134,7 @@ td_status run_tree(const td_shape *shape, const td_cache *cache, int32_t tree_si
     a.Nmax = shape->max_seq_len;
     a.top_k = top_k;
     a.scale = td::host_scale(*shape);
-    return td::launch_tree_attention(a, (cudaStream_t)stream) == cudaSuccess ? TD_OK : TD_ERR_CUDA;
+    return td::launch_tree_attention(a, td::host_sm_count(), (cudaStream_t)stream) == cudaSuccess ? TD_OK : TD_ERR_CUDA;
 }
 
 }  // namespace
@@ -101,7 +145,7 @@ size_t td_tree_workspace_size(const td_shape *shape, int32_t tree_size)
 {
     if (td::host_check_shape(shape) != TD_OK || tree_size < 1 || tree_size > TD_MAX_TREE)
         return 0;
-    return kAlign;
+    return tree_ws(*shape, tree_size).total;
 }
 
 td_status td_tree_attn(const td_shape *shape, const td_cache *cache, int32_t tree_size,
