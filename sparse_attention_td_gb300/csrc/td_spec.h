@@ -27,9 +27,22 @@ struct CacheArgs {
 // CTAs of a tree attention launch: one per SM, at most this many (it sizes the partials).
 constexpr int kMaxTreeCtas = 160;
 
+// A unit whose tiles several CTAs shared, left by the CTA whose range starts
+// at the unit's first cut (rows 0: nothing to join there).
+struct JoinPlan {
+    int rows, b, h, row0;   // query rows of the unit, the first one's number
+    int last;               // the last CTA that has a part
+    int late;               // the first part is its CTA's second one
+};
+struct JoinArgs {
+    const JoinPlan *plan;
+    const float *part_m, *part_l, *part_o;
+    uint16_t *out;
+    int T, Hq, G, part_rows;
+};
+
 struct TreeArgs {
     TmaDesc box_k, box_v;       // rows as boxes of 64 values x box_rows rows, 128-byte swizzle
-    TmaDesc row_k, row_v;       // the same rows as boxes of one row, for row gathers
     CacheArgs c;
     const uint16_t *q;          // [B][T][Hq][128]
     uint16_t *out;              // [B][T][Hq][128]
@@ -38,12 +51,11 @@ struct TreeArgs {
     const uint32_t *mask;       // [B][T][W], or null: chain
     const int32_t *idx;         // sparse layer: [B][Hkv][top_k], or null
     uint32_t *status;
-    long long *prefix;          // [B + 1] work items before each request (written by the kernel)
+    JoinPlan *plan;             // [ctas] (written by the kernel)
     float *part_m, *part_l;     // [2 * ctas][part_rows]
     float *part_o;              // [2 * ctas][part_rows][128]
     int B, T, W, Hq, Hkv, G, Nmax, top_k;
-    int box_rows;               // 0: no boxes, every tile is gathered
-    int oob_row;                // first row past the maps (reads zeros)
+    int box_rows;               // 0: no boxes, every tile goes row by row
     int part_rows;
     float scale;                // softmax scale (natural-log units)
 };

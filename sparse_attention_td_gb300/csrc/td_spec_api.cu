@@ -50,7 +50,7 @@ td_status check_cache(const td_shape &s, const td_cache *c, bool positions)
 // Workspace of the tree attention: the status word at the buffer's start, the
 // rest at its end (offsets from the start of that part).
 struct TreeWs {
-    size_t prefix, part_m, part_l, part_o, total;
+    size_t plan, part_m, part_l, part_o, total;
 };
 
 TreeWs tree_ws(const td_shape &s, int tree_size)
@@ -60,8 +60,8 @@ TreeWs tree_ws(const td_shape &s, int tree_size)
                         td::tree_part_rows(tree_size * (s.num_q_heads / s.num_kv_heads));
     TreeWs w{};
     size_t off = 0;
-    w.prefix = off;
-    off += (((size_t)s.batch + 1) * sizeof(long long) + align) & ~align;
+    w.plan = off;
+    off += (td::kMaxTreeCtas * sizeof(td::JoinPlan) + align) & ~align;
     w.part_m = off;
     off += (rows * sizeof(float) + align) & ~align;
     w.part_l = off;
@@ -113,18 +113,15 @@ td_status run_tree(const td_shape *shape, const td_cache *cache, int32_t tree_si
     a.part_rows = td::tree_part_rows(tree_size * a.G);
     const TreeWs w = tree_ws(*shape, tree_size);
     char *base = (char *)ws + (ws_bytes - (w.total - kAlign)) / kAlign * kAlign;
-    a.prefix = (long long *)(base + w.prefix);
+    a.plan = (td::JoinPlan *)(base + w.plan);
     a.part_m = (float *)(base + w.part_m);
     a.part_l = (float *)(base + w.part_l);
     a.part_o = (float *)(base + w.part_o);
     const long rows = (long)cache->num_pages * shape->num_kv_heads * cache->page_size;
     const int ps = cache->page_size;
     a.box_rows = !cache->block_table || ps % 128 == 0 ? 128 : ps >= 8 && 128 % ps == 0 ? ps : 0;
-    a.oob_row = (int)rows;
     if (!td::host_box_map(&a.box_k, cache->k, rows, a.box_rows ? a.box_rows : 1) ||
-        !td::host_box_map(&a.box_v, cache->v, rows, a.box_rows ? a.box_rows : 1) ||
-        !td::host_box_map(&a.row_k, cache->k, rows, 1) ||
-        !td::host_box_map(&a.row_v, cache->v, rows, 1))
+        !td::host_box_map(&a.box_v, cache->v, rows, a.box_rows ? a.box_rows : 1))
         return TD_ERR_CUDA;
     a.B = shape->batch;
     a.T = tree_size;

@@ -32,19 +32,22 @@ constexpr int kTile = 128;                       // tokens per tile, and query r
 constexpr int kHalfBytes = kTile * 128;          // one 64-value half of a tile's rows
 constexpr int kTileBytes = 2 * kHalfBytes;       // 128 rows of 128 bf16 values
 constexpr int kMaskRing = 8;                     // tiles whose validity masks are alive (see producer)
-constexpr uint64_t kTreeWaitNs = 1000000000ull;  // a wait gives up after 1 s
+constexpr long long kTreeWaitCycles = 2000000000ll;  // a wait gives up after about 1 s
 
 // Shared memory: Q row tiles, then the ring of K and V tiles.
 template <int MT> struct Cfg {
     static constexpr int kSlots = MT == 1 ? 6 : 5;
     static constexpr int kSoftWarps = 4 * MT;
-    static constexpr int kThreads = 32 * (kSoftWarps + 2);
+    // softmax, two producers, the MMA issuer and a spare warp (whole warpgroups)
+    static constexpr int kThreads = 32 * (kSoftWarps + 4);
+    static constexpr int kProducer = kSoftWarps, kIssuer = kSoftWarps + 2;
     static constexpr size_t kSmem = (size_t)(MT + kSlots) * kTileBytes + 1024;
 };
-// Tensor memory columns (32-bit): two S tiles (P overwrites the lower half of
+// Tensor memory columns (32-bit): two S tiles (P overwrites the upper half of
 // its S), then the O tiles.
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
+constexpr uint32_t kColP = 64;
 
 __device__ __forceinline__ uint32_t smem_of(const void *p)
 {
@@ -68,12 +71,12 @@ __device__ __forceinline__ void bar_expect(uint64_t *bar, unsigned bytes)
                  : "memory");
 }
 
-// Waits for the phase of the given parity.  Gives up after kTreeWaitNs, or when
-// another role has (then the CTA leaves as a whole and reports the timeout).
+// Waits for the phase of the given parity.  Gives up after kTreeWaitCycles, or
+// when another role has (then the CTA leaves as a whole and reports the timeout).
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, unsigned parity, volatile int *gave_up)
 {
     const uint32_t addr = smem_of(bar);
-    uint64_t t0 = 0;
+    long long t0 = 0;
     for (int polls = 0;; ++polls) {
         uint32_t done;
         asm volatile(
@@ -85,14 +88,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, unsigned parity, volatil
             : "memory");
         if (done)
             return true;
-        if ((polls & 15) == 15) {
-            uint64_t t;
-            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+        if ((polls & 63) == 63) {
+            const long long t = clock64();
             if (t0 == 0)
                 t0 = t;
             if (*gave_up)
                 return false;
-            if (t - t0 > kTreeWaitNs) {
+            if (t - t0 > kTreeWaitCycles) {
                 *gave_up = 1;
                 return false;
             }
@@ -109,44 +111,43 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const TmaDesc *map, int x,
         : "memory");
 }
 
-__device__ __forceinline__ void tma_rows4(uint32_t dst, const TmaDesc *map, int x, const int (&r)[4],
-                                          uint64_t *bar)
+// 16 bytes global -> shared, through L2 only; zeros where `there` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(smem_of(bar))
-        : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
 }
 
 // Shared-memory operand of tcgen05.mma, 128-byte swizzle.  K-major (rows of
 // 128 bytes, groups of 8 rows 1024 bytes apart) or, for V, MN-major: 64-value
 // blocks of the dims `lead` bytes apart, groups of 8 tokens 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead)
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead)   // low word
 {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 |
-           (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+    return ((addr & 0x3ffff) >> 4) | (lead >> 4) << 16;
 }
+constexpr uint32_t kOperandHigh = 1024 >> 4 | 1u << 14 | 2u << 29;   // high word
 
 // kind::f16, fp32 accumulator, bf16 operands, M = N = 128; bit 16: B is MN-major.
 constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (128u >> 3) << 17 | (128u >> 4) << 24;
 constexpr uint32_t kIdescV = kIdesc | 1u << 16;
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, bool add)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(kIdesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kIdesc), "r"((uint32_t)add), "r"(kOperandHigh)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, bool add)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(kIdescV), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kIdescV), "r"((uint32_t)add), "r"(kOperandHigh)
         : "memory");
 }
 
@@ -227,6 +228,13 @@ __device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint
                  : "memory");
 }
 
+__device__ __forceinline__ void store32(void *p, const uint32_t *x)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -234,11 +242,24 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// x / y of numbers >= 0, y > 0; short where both are short.
+__device__ __forceinline__ long long quotient(long long x, long long y)
+{
+    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
 // ---- work: units (request, KV head, block of query rows), each a run of
@@ -262,23 +283,13 @@ __device__ __forceinline__ Work work_of(const TreeArgs &a, int b, uint32_t &bad)
 
 // A CTA's range of tiles, unit after unit: every role of the CTA walks it alike.
 template <int MT> struct Walk {
-    const TreeArgs &a;
-    long long left;
+    const TreeArgs *args;
+    int left;                     // tiles left of the CTA's range
     int b, h, m, t;               // current request, KV head, row block and first tile
     bool first;                   // the segment starts at the CTA's range start
     Work w;
 
-    __device__ Walk(const TreeArgs &args, int b0, long long off, long long n)
-        : a(args), left(n), b(b0), first(true)
-    {
-        uint32_t bad = 0;
-        w = work_of<MT>(a, b, bad);
-        const long long unit = off / w.tiles;
-        t = (int)(off % w.tiles);
-        h = (int)(unit / w.blocks);
-        m = (int)(unit % w.blocks);
-    }
-    __device__ int count() const { return (int)min(left, (long long)(w.tiles - t)); }
+    __device__ int count() const { return min(left, w.tiles - t); }
     __device__ void next(int n)
     {
         first = false;
@@ -290,15 +301,15 @@ template <int MT> struct Walk {
         if (++m < w.blocks)
             return;
         m = 0;
-        if (++h < a.Hkv)
+        if (++h < args->Hkv)
             return;
         h = 0;
         uint32_t bad = 0;
         do {
-            w = work_of<MT>(a, ++b, bad);
-        } while (w.tiles == 0 && b + 1 < a.B);
+            w = work_of<MT>(*args, ++b, bad);
+        } while (w.tiles == 0 && b + 1 < args->B);
     }
-    __device__ int rows() const { return min(w.nt * a.G - m * MT * kTile, MT * kTile); }
+    __device__ int rows() const { return min(w.nt * args->G - m * MT * kTile, MT * kTile); }
 };
 
 // One CTA per SM; each takes an equal, contiguous range of the batch's tiles
@@ -312,12 +323,11 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     using C = Cfg<MT>;
     extern __shared__ unsigned char sm_raw[];
     __shared__ __align__(8) uint64_t bar_full[C::kSlots], bar_empty[C::kSlots];
-    __shared__ __align__(8) uint64_t bar_q[MT], bar_s[2], bar_p[2], bar_o[MT], bar_scan, bar_drain;
+    __shared__ __align__(8) uint64_t bar_q[MT], bar_s[2], bar_p[2], bar_p2[2], bar_o[MT], bar_scan, bar_drain;
     __shared__ uint32_t sm_valid[kMaskRing][4];   // tokens of a tile that exist
     __shared__ uint32_t sm_badv[MT][4];           // drafted tokens with non-finite V values
     __shared__ long long sm_scan[C::kThreads / 32];
-    __shared__ long long sm_off;
-    __shared__ int sm_b0;
+    __shared__ Walk<MT> sm_start;
     __shared__ uint32_t sm_tmem;
     __shared__ int sm_gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -325,16 +335,49 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     const uint32_t sm_ring = sm_q + MT * kTileBytes;
     volatile int *gave_up = &sm_gave_up;
 
-    // ---- the CTA's range: requests in equal runs per thread, prefix sums
-    long long start, end;
+    // ---- the CTA's range: requests in equal runs per thread, prefix sums.  The
+    // barriers, the tensor memory and the tensor maps are made ready meanwhile.
     {
         const int run = (a.B + C::kThreads - 1) / C::kThreads;
         const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
         uint32_t bad = 0;
         long long mine = 0;
+        Work w{};
         for (int b = b0; b < b1; ++b) {
-            const Work w = work_of<MT>(a, b, bad);
+            w = work_of<MT>(a, b, bad);
             mine += (long long)w.tiles * w.blocks * a.Hkv;
+        }
+        if (tid == 0) {
+            sm_gave_up = 0;
+            sm_start.left = 0;
+            for (int i = 0; i < C::kSlots; ++i) {
+                bar_init(&bar_full[i], 64);
+                bar_init(&bar_empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                bar_init(&bar_s[i], 1);
+                bar_init(&bar_p[i], 4);
+                bar_init(&bar_p2[i], 4);
+            }
+            for (int i = 0; i < MT; ++i) {
+                bar_init(&bar_q[i], 4);
+                bar_init(&bar_o[i], 1);
+            }
+            bar_init(&bar_scan, 4);
+            bar_init(&bar_drain, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        if (tid == 32 * C::kProducer) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_k) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_v) : "memory");
+        }
+        if (warp == C::kIssuer) {
+            __syncwarp();
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_of(&sm_tmem)),
+                         "r"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
         if (bad && blockIdx.x == 0)
             atomicOr(a.status, bad);
@@ -347,293 +390,348 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         }
         if (lane == 31)
             sm_scan[warp] = inc;
-        if (tid == 0) {
-            sm_gave_up = 0;
-            for (int i = 0; i < C::kSlots; ++i) {
-                bar_init(&bar_full[i], 1);
-                bar_init(&bar_empty[i], 1);
-            }
-            for (int i = 0; i < 2; ++i) {
-                bar_init(&bar_s[i], 1);
-                bar_init(&bar_p[i], 4);
-            }
-            for (int i = 0; i < MT; ++i) {
-                bar_init(&bar_q[i], 4);
-                bar_init(&bar_o[i], 1);
-            }
-            bar_init(&bar_scan, 4);
-            bar_init(&bar_drain, 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        }
         __syncthreads();
         long long total = 0, at = inc - mine;
+#pragma unroll
         for (int i = 0; i < C::kThreads / 32; ++i) {
             if (i < warp)
                 at += sm_scan[i];
             total += sm_scan[i];
         }
-        const long long per = (total + gridDim.x - 1) / gridDim.x;
-        start = blockIdx.x * per;
-        end = min(start + per, total);
-        if (blockIdx.x == 0) {
-            long long p = at;
-            for (int b = b0; b < b1; ++b) {
-                const Work w = work_of<MT>(a, b, bad);
-                a.prefix[b] = p;
-                p += (long long)w.tiles * w.blocks * a.Hkv;
-            }
-            if (tid == 0)
-                a.prefix[a.B] = total;
-        }
-        pdl_launch_dependents();
-        if (start >= end)
-            return;
-        if (at <= start && start < at + mine) {
-            long long p = at;
-            for (int b = b0; b < b1; ++b) {
-                const Work w = work_of<MT>(a, b, bad);
-                const long long n = (long long)w.tiles * w.blocks * a.Hkv;
-                if (start < p + n) {
-                    sm_b0 = b;
-                    sm_off = start - p;
-                    break;
+        const long long per = quotient(total + gridDim.x - 1, gridDim.x);
+        const long long start = blockIdx.x * per;
+        if (start < total && at <= start && start < at + mine) {
+            int b = b0;
+            if (run > 1) {
+                for (long long p = at; b < b1; ++b, at = p) {
+                    w = work_of<MT>(a, b, bad);
+                    p += (long long)w.tiles * w.blocks * a.Hkv;
+                    if (start < p)
+                        break;
                 }
-                p += n;
             }
+            const long long off = start - at;
+            const long long unit = quotient(off, w.tiles);
+            const int first = (int)(off - unit * w.tiles);
+            Walk<MT> s;
+            s.args = &a;
+            s.left = (int)min(per, total - start);
+            s.b = b;
+            s.h = (int)unit / w.blocks;
+            s.m = (int)unit % w.blocks;
+            s.t = first;
+            s.first = true;
+            s.w = w;
+            sm_start = s;
+            // The unit that this cut goes through, if it is the unit's first cut.
+            const bool joins = first > 0 && first <= per;
+            JoinPlan j{};
+            if (joins) {
+                j.rows = s.rows();
+                j.b = b;
+                j.h = s.h;
+                j.row0 = s.m * MT * kTile;
+                // the last range that meets the unit
+                j.last = (int)quotient(start - first + w.tiles - 1, per);
+                j.late = first < per;
+            }
+            a.plan[blockIdx.x] = j;
         }
-        __syncwarp();
-        if (warp == C::kSoftWarps + 1) {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                             smem_of(&sm_tmem)),
-                         "r"(kTmemCols)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        }
+        if (start >= total && tid == 0)
+            a.plan[blockIdx.x] = JoinPlan{};
         tmem_before();
         __syncthreads();
         tmem_after();
+        pdl_launch_dependents();
     }
     const uint32_t tmem = sm_tmem;
-    Walk<MT> walk(a, sm_b0, sm_off, end - start);
+    Walk<MT> walk = sm_start;
 
-    if (warp == C::kSoftWarps) {
-        // ---- producer: K then V tile of every tile in turn, into the ring.
-        // A tile whose tokens all exist comes as boxes of whole rows (of a page);
-        // any other (ragged end, index set, drafted tokens, a bad page) row by
-        // row, four per copy, where a token that does not exist reads the zero
-        // row past the map: its V row is then 0, and the validity mask keeps its
-        // score out.  The mask ring: the producer is at most kSlots / 2 tiles
-        // ahead of the last S = Q K^T, itself at most 2 ahead of the softmax.
-        uint32_t e = 0, tile_no = 0;
-        bool ok = true;
-        while (ok && walk.left > 0) {
-            const int n = walk.count();
-            const int h = walk.h, b = walk.b;
-            for (int i = 0; ok && i < n; ++i, ++tile_no) {
-                const int t = walk.t + i;
-                const bool tree = t == walk.w.tiles - 1;
-                const int base = t * kTile;
-                int rows[4];
-                int box = -1;               // this lane's box row
-                uint32_t flags = 0;
-                bool boxes = false;
-                if (!tree && !a.idx && a.box_rows && base + kTile <= walk.w.ctx) {
-                    const int nbox = kTile / a.box_rows;
-                    if (lane < nbox) {
-                        const int p = base + lane * a.box_rows;
-                        int page = b, r = p;
-                        if (a.c.table) {
-                            page = a.c.table[(size_t)b * a.c.max_blocks + p / a.c.page_size];
-                            r = p % a.c.page_size;
-                        }
-                        if (page >= 0 && page < a.c.num_pages)
-                            box = (page * a.Hkv + h) * a.c.page_size + r;
-                    }
-                    boxes = __all_sync(kFull, lane >= nbox || box >= 0);
-                }
-                uint32_t valid = 0xf;
-                if (!boxes) {
-                    valid = 0;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int j = 4 * lane + u;
-                        int p = -1;
-                        if (tree) {
-                            p = j < walk.w.nt ? walk.w.ctx + j : -1;
-                        } else if (a.idx) {
-                            if (base + j < a.top_k) {
-                                p = a.idx[((size_t)b * a.Hkv + h) * a.top_k + base + j];
-                                if (p < -1 || p >= walk.w.ctx) {
-                                    flags |= kFlagIndexOutOfRange;
-                                    p = -1;
-                                }
-                            }
-                        } else {
-                            p = base + j < walk.w.ctx ? base + j : -1;
-                        }
-                        rows[u] = a.oob_row;
-                        if (p >= 0) {
-                            int page = b, r = p;
-                            if (a.c.table) {
-                                page = a.c.table[(size_t)b * a.c.max_blocks + p / a.c.page_size];
-                                r = p % a.c.page_size;
-                            }
-                            if (page >= 0 && page < a.c.num_pages) {
-                                rows[u] = (page * a.Hkv + h) * a.c.page_size + r;
-                                valid |= 1u << u;
-                            } else {
-                                flags |= kFlagPageOutOfRange;
-                            }
-                        }
-                    }
-                    if (flags)
-                        atomicOr(a.status, flags);
-                }
-                const uint32_t word = __reduce_or_sync(0xffu << (lane & 24), valid << (4 * (lane & 7)));
-                for (int kv = 0; ok && kv < 2; ++kv, ++e) {
-                    const uint32_t slot = e % C::kSlots, use = e / C::kSlots;
-                    if (use > 0)
-                        ok = bar_wait(&bar_empty[slot], (use - 1) & 1, gave_up);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok)
-                        break;
-                    if (kv == 0 && (lane & 7) == 0)
-                        sm_valid[tile_no % kMaskRing][lane >> 3] = word;
-                    __syncwarp();
-                    if (lane == 0)
-                        bar_expect(&bar_full[slot], kTileBytes);
-                    __syncwarp();
-                    const uint32_t dst = sm_ring + slot * kTileBytes;
-                    if (boxes) {
-                        if (box >= 0) {
-                            const TmaDesc *map = kv ? &a.box_v : &a.box_k;
-                            const uint32_t d = dst + lane * a.box_rows * 128;
-                            tma_box(d, map, 0, box, &bar_full[slot]);
-                            tma_box(d + kHalfBytes, map, 64, box, &bar_full[slot]);
-                        }
-                    } else {
-                        const TmaDesc *map = kv ? &a.row_v : &a.row_k;
-                        const uint32_t d = dst + lane * 4 * 128;
-                        tma_rows4(d, map, 0, rows, &bar_full[slot]);
-                        tma_rows4(d + kHalfBytes, map, 64, rows, &bar_full[slot]);
-                    }
+    if (warp == C::kProducer || warp == C::kProducer + 1) {
+        // ---- producers: K then V tile of every tile in turn, into the ring.
+        // A tile whose tokens all exist comes as boxes of whole rows (of a page),
+        // by one warp for K and the other for V.  Any other (ragged end, index
+        // set, drafted tokens, a bad page) row by row with cp.async, 64 rows per
+        // warp, half a warp per 256-byte row: a token that does not exist is
+        // filled with zeros (no stale V value meets its zero probability), and
+        // the validity mask keeps its score out.  Row gathers by TMA instead
+        // took 60 ns per four half rows, 7.7 us a tile.
+        // The lookups run ahead: positions two tiles, page numbers one.
+        // The mask ring: a producer is at most kSlots / 2 tiles ahead of the last
+        // S = Q K^T, itself at most 2 ahead of the softmax.
+        const int pw = warp - C::kProducer;
+        struct Cursor {
+            Walk<MT> walk;
+            int i, n;             // tile of the segment, tiles of the segment
+            __device__ Cursor(const Walk<MT> &w) : walk(w), i(0), n(w.count()) {}
+            __device__ bool more() const { return walk.left > 0; }
+            __device__ void step()
+            {
+                if (++i == n) {
+                    walk.next(n);
+                    i = 0;
+                    n = walk.count();
                 }
             }
-            walk.next(n);
+        };
+        // what is known of a tile so far: positions (-1: none), their pages
+        struct Tile {
+            int pos[2], page[2];
+            bool whole;           // candidate for boxes: pos[0] is this lane's box
+        };
+        auto positions = [&](const Cursor &c, Tile &x, uint32_t &flags) {
+            const Work &w = c.walk.w;
+            const int t = c.walk.t + c.i, base = t * kTile;
+            const bool tree = t == w.tiles - 1;
+            x.whole = !tree && !a.idx && a.box_rows && base + kTile <= w.ctx;
+            if (x.whole) {
+                x.pos[0] = lane * a.box_rows < kTile ? base + lane * a.box_rows : -1;
+                x.pos[1] = -1;
+                return;
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int j = pw * 64 + u * 32 + lane;
+                int p = -1;
+                if (tree) {
+                    p = j < w.nt ? w.ctx + j : -1;
+                } else if (a.idx) {
+                    if (base + j < a.top_k)
+                        p = __ldg(a.idx + ((size_t)c.walk.b * a.Hkv + c.walk.h) * a.top_k + base + j);
+                } else {
+                    p = base + j < w.ctx ? base + j : -1;
+                }
+                x.pos[u] = p;
+            }
+        };
+        // index entries are checked here, a tile after they were requested
+        auto pages = [&](const Cursor &c, Tile &x, uint32_t &flags) {
+            const Work &w = c.walk.w;
+            const bool listed = a.idx && c.walk.t + c.i != w.tiles - 1;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (listed && x.pos[u] != -1 && (x.pos[u] < 0 || x.pos[u] >= w.ctx)) {
+                    flags |= kFlagIndexOutOfRange;
+                    x.pos[u] = -1;
+                }
+                x.page[u] = c.walk.b;
+                if (a.c.table && x.pos[u] >= 0)
+                    x.page[u] = __ldg(a.c.table + (size_t)c.walk.b * a.c.max_blocks +
+                                      x.pos[u] / a.c.page_size);
+            }
+        };
+        auto row_of = [&](const Cursor &c, int pos, int page) {   // -1: no such row
+            if (pos < 0 || page < 0 || page >= a.c.num_pages)
+                return -1;
+            return (page * a.Hkv + c.walk.h) * a.c.page_size + (a.c.table ? pos % a.c.page_size : pos);
+        };
+        uint32_t e = 0, tile_no = 0, flags = 0;
+        bool ok = true;
+        Cursor c0(walk), c1(walk), c2(walk);      // tiles issued, with pages, with positions
+        Tile x0{}, x1{}, x2{};
+        if (c0.more()) {
+            positions(c0, x0, flags);
+            pages(c0, x0, flags);
+            c1.step();
+            if (c1.more())
+                positions(c1, x1, flags);
+            c2 = c1;
         }
+        for (; ok && c0.more(); ++tile_no) {
+            if (c1.more()) {
+                c2.step();
+                if (c2.more())
+                    positions(c2, x2, flags);
+                pages(c1, x1, flags);
+            }
+            int row[2];
+            row[0] = row_of(c0, x0.pos[0], x0.page[0]);
+            row[1] = row_of(c0, x0.pos[1], x0.page[1]);
+            bool boxes = x0.whole;
+            if (boxes && __any_sync(kFull, x0.pos[0] >= 0 && row[0] < 0)) {
+                boxes = false;                    // a bad page: token by token
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    x0.pos[u] = (c0.walk.t + c0.i) * kTile + pw * 64 + u * 32 + lane;
+                    x0.page[u] = a.c.table ? a.c.table[(size_t)c0.walk.b * a.c.max_blocks +
+                                                       x0.pos[u] / a.c.page_size]
+                                           : c0.walk.b;
+                    row[u] = row_of(c0, x0.pos[u], x0.page[u]);
+                }
+            }
+            uint32_t word[2] = {0xffffffffu, 0xffffffffu};
+            if (!boxes) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    word[u] = __ballot_sync(kFull, row[u] >= 0);
+                    if (x0.pos[u] >= 0 && row[u] < 0)
+                        flags |= kFlagPageOutOfRange;
+                }
+            }
+            for (int kv = 0; ok && kv < 2; ++kv, ++e) {
+                const uint32_t slot = e % C::kSlots, use = e / C::kSlots;
+                if (use > 0)
+                    ok = bar_wait(&bar_empty[slot], (use - 1) & 1, gave_up);
+                ok = __all_sync(kFull, ok);
+                if (!ok)
+                    break;
+                if (kv == 0 && lane < 2)
+                    sm_valid[tile_no % kMaskRing][pw * 2 + lane] = word[lane];
+                __syncwarp();
+                const uint32_t dst = sm_ring + slot * kTileBytes;
+                if (boxes) {
+                    if (pw == kv) {
+                        if (lane == 0)
+                            bar_expect(&bar_full[slot], kTileBytes);
+                        else
+                            bar_arrive(&bar_full[slot]);
+                        __syncwarp();
+                        if (row[0] >= 0) {
+                            const TmaDesc *map = kv ? &a.box_v : &a.box_k;
+                            const uint32_t d = dst + lane * a.box_rows * 128;
+                            tma_box(d, map, 0, row[0], &bar_full[slot]);
+                            tma_box(d + kHalfBytes, map, 64, row[0], &bar_full[slot]);
+                        }
+                    } else {
+                        bar_arrive(&bar_full[slot]);
+                    }
+                } else {
+                    const uint16_t *base = kv ? a.c.v : a.c.k;
+                    const int c = lane & 15;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int it = 0; it < 16; ++it) {
+                            const int src = it * 2 + (lane >> 4);
+                            const int rr = __shfl_sync(kFull, row[u], src);
+                            const int x = pw * 64 + u * 32 + src;
+                            copy16(dst + (c >> 3) * kHalfBytes + x * 128 + (((c ^ x) & 7) << 4),
+                                   base + (size_t)max(rr, 0) * kHeadDim + c * 8, rr >= 0);
+                        }
+                    // an arrival per thread once its copies have landed
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                                     smem_of(&bar_full[slot]))
+                                 : "memory");
+                }
+                __syncwarp();
+            }
+            c0 = c1;
+            x0 = x1;
+            c1 = c2;
+            x1 = x2;
+        }
+        if (flags)
+            atomicOr(a.status, flags);
         if (!ok) {
             // leave no copy in flight: the last ones issued, each with a limit of its own
+            asm volatile("cp.async.wait_all;" ::: "memory");
             int own_limit = 0;
             for (uint32_t k = e > C::kSlots ? e - C::kSlots : 0; k < e; ++k)
                 bar_wait(&bar_full[k % C::kSlots], (k / C::kSlots) & 1, &own_limit);
         }
-    } else if (warp == C::kSoftWarps + 1) {
-        // ---- MMA issue.  One row tile: S of tile i + 1 is issued before P V of
-        // tile i, so the tensor cores work while the softmax does.  Two row
-        // tiles: they take turns.
-        uint32_t e = 0;                  // ring entries consumed: 2 * tile (K), 2 * tile + 1 (V)
-        uint32_t done_p[2] = {0, 0};     // P V issued per row tile (two row tiles)
-        uint32_t segs[MT] = {};          // segments begun per row tile
-        bool ok = true;
-        auto issue_s = [&](uint32_t entry, int m, int buf, bool last) {
-            if (lane == 0) {
-                const uint32_t k = sm_ring + entry % C::kSlots * kTileBytes, q = sm_q + m * kTileBytes;
+    } else if (warp == C::kIssuer) {
+        // ---- MMA issue, by one thread.  One row tile: S of tile i + 1 is issued
+        // before P V of tile i, so the tensor cores work while the softmax does.
+        // Two row tiles: they take turns.  P comes in halves (tokens 64 .. 127
+        // first), so half of P V overlaps the rest of the exponentials.
+        if (lane == 0) {
+            uint32_t e = 0;              // ring entries consumed: 2 * tile (K), 2 * tile + 1 (V)
+            uint32_t done_p[2] = {0, 0}; // P V issued per row tile (two row tiles)
+            uint32_t segs[MT] = {};      // segments begun per row tile
+            bool ok = true;
+            auto issue_s = [&](uint32_t entry, int m, int buf, bool last) {
+                const uint32_t k = operand(sm_ring + entry % C::kSlots * kTileBytes, 16);
+                const uint32_t q = operand(sm_q + m * kTileBytes, 16);
 #pragma unroll
                 for (int s = 0; s < 8; ++s) {
                     const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
-                    mma_ss(tmem + buf * kTile, operand(q + o, 16), operand(k + o, 16), s > 0);
+                    mma_ss(tmem + buf * kTile, q + (o >> 4), k + (o >> 4), s > 0);
                 }
                 mma_commit(&bar_s[buf]);
                 if (last)
                     mma_commit(&bar_empty[entry % C::kSlots]);
-            }
-            __syncwarp();
-        };
-        auto issue_o = [&](uint32_t entry, int m, int buf, bool first, bool last) {
-            if (lane == 0) {
-                const uint32_t v = sm_ring + entry % C::kSlots * kTileBytes;
+            };
+            auto issue_o = [&](uint32_t entry, int m, int buf, int half, bool first) {
+                const uint32_t v = operand(sm_ring + entry % C::kSlots * kTileBytes, kHalfBytes);
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_ts(tmem + kColO + m * kTile, tmem + buf * kTile + s * 8,
-                           operand(v + s * 16 * 128, kHalfBytes), !(first && s == 0));
+                for (int s = 0; s < 4; ++s)
+                    mma_ts(tmem + kColO + m * kTile, tmem + buf * kTile + kColP + (4 * half + s) * 8,
+                           v + ((4 * half + s) * 16 * 128 >> 4), !(first && s == 0));
+            };
+            auto wait_full = [&](uint32_t entry) {
+                ok = ok && bar_wait(&bar_full[entry % C::kSlots], (entry / C::kSlots) & 1, gave_up);
+                // rows copied by cp.async are read by the MMA through the async proxy
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                return ok;
+            };
+            auto wait_bar = [&](uint64_t *bar, uint32_t phase) {
+                ok = ok && bar_wait(bar, phase & 1, gave_up);
+                tmem_after();
+                return ok;
+            };
+            // P V of one row tile, V already there; false: gave up
+            auto do_o = [&](uint32_t entry, int m, int buf, uint32_t phase, bool first, bool last) {
+                if (!wait_bar(&bar_p[buf], phase))
+                    return false;
+                issue_o(entry, m, buf, 1, first);
+                if (!wait_bar(&bar_p2[buf], phase))
+                    return false;
+                issue_o(entry, m, buf, 0, false);
                 mma_commit(&bar_o[m]);
                 if (last)
                     mma_commit(&bar_empty[entry % C::kSlots]);
-            }
-            __syncwarp();
-        };
-        auto wait_full = [&](uint32_t entry) {
-            ok = ok && bar_wait(&bar_full[entry % C::kSlots], (entry / C::kSlots) & 1, gave_up);
-            ok = __all_sync(kFull, ok);
-            tmem_after();
-        };
-        auto wait_bar = [&](uint64_t *bar, uint32_t phase) {
-            ok = ok && bar_wait(bar, phase & 1, gave_up);
-            ok = __all_sync(kFull, ok);
-            tmem_after();
-        };
-        while (ok && walk.left > 0) {
-            const int n = walk.count();
-            const int nm = MT == 1 ? 1 : (walk.rows() + kTile - 1) / kTile;
-            for (int m = 0; m < nm; ++m)
-                wait_bar(&bar_q[m], segs[m]++);
-            if (!ok)
-                break;
-            if constexpr (MT == 1) {
-                // tile i uses S buffer (global tile number) & 1
-                const uint32_t g0 = e >> 1;
-                wait_full(e);
-                if (ok)
+                return true;
+            };
+            while (ok && walk.left > 0) {
+                const int n = walk.count();
+                const int nm = MT == 1 ? 1 : (walk.rows() + kTile - 1) / kTile;
+                for (int m = 0; m < nm; ++m)
+                    wait_bar(&bar_q[m], segs[m]++);
+                if (!wait_full(e))
+                    break;
+                if constexpr (MT == 1) {
+                    // tile i uses S buffer (global tile number) & 1
+                    const uint32_t g0 = e >> 1;
                     issue_s(e, 0, g0 & 1, true);
-                for (int i = 0; ok && i < n; ++i) {
-                    const uint32_t g = g0 + i;
-                    if (i + 1 < n) {
-                        wait_full(2 * (g + 1));
-                        if (!ok)
+                    for (int i = 0; ok && i < n; ++i) {
+                        const uint32_t g = g0 + i;
+                        if (i + 1 < n) {
+                            if (!wait_full(2 * (g + 1)))
+                                break;
+                            issue_s(2 * (g + 1), 0, (g + 1) & 1, true);
+                        }
+                        if (!wait_full(2 * g + 1))
                             break;
-                        issue_s(2 * (g + 1), 0, (g + 1) & 1, true);
+                        do_o(2 * g + 1, 0, g & 1, g >> 1, i == 0, true);
                     }
-                    wait_bar(&bar_p[g & 1], g >> 1);
-                    wait_full(2 * g + 1);
-                    if (!ok)
-                        break;
-                    issue_o(2 * g + 1, 0, g & 1, i == 0, true);
-                }
-                e += 2 * n;
-            } else {
-                wait_full(e);
-                if (ok)
+                    e += 2 * n;
+                } else {
                     for (int m = 0; m < nm; ++m)
                         issue_s(e, m, m, m == nm - 1);
-                for (int i = 0; ok && i < n; ++i, e += 2) {
-                    for (int m = 0; ok && m < nm; ++m) {
-                        wait_bar(&bar_p[m], done_p[m]);
-                        if (m == 0)
-                            wait_full(e + 1);
-                        if (!ok)
+                    for (int i = 0; ok && i < n; ++i, e += 2) {
+                        if (!wait_full(e + 1))
                             break;
-                        ++done_p[m];
-                        issue_o(e + 1, m, m, i == 0, m == nm - 1);
-                        if (i + 1 < n) {
-                            if (m == 0)
-                                wait_full(e + 2);
-                            if (!ok)
+                        for (int m = 0; ok && m < nm; ++m) {
+                            if (!do_o(e + 1, m, m, done_p[m]++, i == 0, m == nm - 1))
                                 break;
-                            issue_s(e + 2, m, m, m == nm - 1);
+                            if (i + 1 < n) {
+                                if (m == 0 && !wait_full(e + 2))
+                                    break;
+                                issue_s(e + 2, m, m, m == nm - 1);
+                            }
                         }
                     }
                 }
+                walk.next(n);
             }
-            walk.next(n);
-        }
-        if (!ok) {
-            int own_limit = 0;
-            if (lane == 0)
+            if (!ok) {
+                int own_limit = 0;
                 mma_commit(&bar_drain);
-            __syncwarp();
-            bar_wait(&bar_drain, 0, &own_limit);
+                bar_wait(&bar_drain, 0, &own_limit);
+            }
         }
-    } else {
+        __syncwarp();
+    } else if (warp < C::kSoftWarps) {
         // ---- softmax: thread r of a row tile owns query row r
         const int m = MT == 1 ? 0 : warp >> 2;
         const int r = (warp & 3) * 32 + lane;                 // row of the row tile, TMEM lane
@@ -768,47 +866,41 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     }
                     const bool masked = (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu;
                     // One row tile: the row's 128 scores stay in registers.  Two
-                    // row tiles (12 warps' worth of registers): 32 at a time, read
-                    // from tensor memory once for the maximum and once for the
-                    // exponentials.
-                    constexpr int kHeld = MT == 1 ? kTile : 32;
-                    float s[kHeld];
-                    auto fetch = [&](int c) {     // scores 32c .. 32c + 31 to s
-                        float *d = s + (MT == 1 ? 32 * c : 0);
-                        tmem_ld32(at + 32 * c, reinterpret_cast<uint32_t *>(d));
+                    // row tiles (384 threads, 168 registers each): 64 at a time; the
+                    // second half stays for the exponentials and the first half is
+                    // read from tensor memory again, while P goes over the second.
+                    float s[MT == 1 ? kTile : 64];
+                    auto half = [&](int c) { return s + (MT == 1 ? 64 * c : 0); };
+                    auto fetch = [&](int c) {
+                        tmem_ld32(at + 64 * c, reinterpret_cast<uint32_t *>(half(c)));
+                        tmem_ld32(at + 64 * c + 32, reinterpret_cast<uint32_t *>(half(c)) + 32);
                     };
-                    auto hide = [&](int c) {
-                        float *d = s + (MT == 1 ? 32 * c : 0);
+                    auto arrived = [&](int c) {
+                        tmem_wait_ld();
+                        float *d = half(c);
+                        tmem_loaded(reinterpret_cast<uint32_t *>(d));
+                        tmem_loaded(reinterpret_cast<uint32_t *>(d) + 32);
                         if (masked) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(w[c] >> k & 1u))
+                            for (int k = 0; k < 64; ++k)
+                                if (!(w[2 * c + (k >> 5)] >> (k & 31) & 1u))
                                     d[k] = -CUDART_INF_F;
                         }
                     };
                     float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
                     __syncwarp();
-                    if constexpr (MT == 1) {
+                    fetch(0);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            fetch(c);
-                        tmem_wait_ld();
+                    for (int c = 0; c < 2; ++c) {
+                        arrived(c);
+                        if (MT == 1 && c == 0)
+                            fetch(1);
+                        const float *d = half(c);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32 * c);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if constexpr (MT > 1) {
-                            fetch(c);
-                            tmem_wait_ld();
-                            tmem_loaded(reinterpret_cast<uint32_t *>(s));
-                        }
-                        hide(c);
-                        const float *d = s + (MT == 1 ? 32 * c : 0);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            mx[k & 3] = fmaxf(mx[k & 3], d[k]);
+                        for (int k = 0; k < 64; k += 2)
+                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], d[k], d[k + 1]);
+                        if (MT > 1 && c == 0)
+                            fetch(1);
                     }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                     if (mref == -CUDART_INF_F)
@@ -839,34 +931,45 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         }
                     }
                     const float off = mref == -CUDART_INF_F ? 0.0f : -mref;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float2 off2 = make_float2(off, off), sl22 = make_float2(sl2, sl2);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if constexpr (MT > 1) {
-                            fetch(c);
-                            tmem_wait_ld();
-                            tmem_loaded(reinterpret_cast<uint32_t *>(s));
-                            hide(c);
+                    for (int c = 1; c >= 0; --c) {
+                        if (MT > 1 && c == 0) {
+                            fetch(0);
+                            arrived(0);
                         }
-                        const float *d = s + (MT == 1 ? 32 * c : 0);
-                        uint32_t p[16];
+                        const float *d = half(c);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float p0 = ex2(fmaf(d[2 * k], sl2, off));
-                            const float p1 = ex2(fmaf(d[2 * k + 1], sl2, off));
-                            sum[(2 * k) & 3] += p0;
-                            sum[(2 * k + 1) & 3] += p1;
-                            p[k] = pack_bf16(p0, p1);
+                        for (int y = 0; y < 2; ++y) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float2 x = __ffma2_rn(
+                                    make_float2(d[32 * y + 2 * k], d[32 * y + 2 * k + 1]), sl22, off2);
+                                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                                sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+                                p[k] = pack_bf16(e.x, e.y);
+                            }
+                            tmem_st16(at + kColP + 32 * c + 16 * y, p);
                         }
-                        tmem_st16(at + 16 * c, p);   // over scores that have been read
+                        if (c == 1) {
+                            tmem_wait_st();
+                            tmem_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                bar_arrive(&bar_p[buf]);
+                        }
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
+                } else if (lane == 0) {
+                    bar_arrive(&bar_p[buf]);
                 }
                 tmem_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(&bar_p[buf]);
+                    bar_arrive(&bar_p2[buf]);
             }
             if (!ok)
                 break;
@@ -914,22 +1017,20 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         }
                     }
                     if (live && whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(
-                            a.out + (q0 + (size_t)tok * a.Hq + row % a.G) * kHeadDim + 32 * c);
+                        uint16_t *dst = a.out + (q0 + (size_t)tok * a.Hq + row % a.G) * kHeadDim + 32 * c;
+                        uint32_t y[16];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint4 y;
-                            y.x = pack_bf16(__uint_as_float(x[8 * k]) * inv, __uint_as_float(x[8 * k + 1]) * inv);
-                            y.y = pack_bf16(__uint_as_float(x[8 * k + 2]) * inv, __uint_as_float(x[8 * k + 3]) * inv);
-                            y.z = pack_bf16(__uint_as_float(x[8 * k + 4]) * inv, __uint_as_float(x[8 * k + 5]) * inv);
-                            y.w = pack_bf16(__uint_as_float(x[8 * k + 6]) * inv, __uint_as_float(x[8 * k + 7]) * inv);
-                            dst[k] = y;
-                        }
+                        for (int k = 0; k < 16; ++k)
+                            y[k] = pack_bf16(__uint_as_float(x[2 * k]) * inv, __uint_as_float(x[2 * k + 1]) * inv);
+                        const uint4 *v = reinterpret_cast<const uint4 *>(y);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            reinterpret_cast<uint4 *>(dst)[k] = v[k];
                     } else if (live) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + prow * kHeadDim + 32 * c);
+                        float *dst = a.part_o + prow * kHeadDim + 32 * c;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                        for (int k = 0; k < 4; ++k)
+                            store32(dst + 8 * k, x + 8 * k);
                     }
                     __syncwarp();
                 }
@@ -948,82 +1049,79 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     __syncthreads();
     if (tid == 0 && sm_gave_up)
         atomicOr(a.status, kFlagWaitTimeout);
-    if (warp == C::kSoftWarps + 1) {
+    if (warp == C::kIssuer) {
         tmem_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                      : "memory");
     }
 }
 
-// Joins the parts of the units that several CTAs shared.  CTA x is given the
-// unit, if any, whose first cut is the end of range x; its warps take the
-// unit's rows in turn: o = sum_s o_s 2^(m_s - m) / sum_s l_s 2^(m_s - m).
+// Joins the parts of the units that several CTAs shared.  Block x belongs to
+// the cut at the start of CTA x + 1's range, which left a plan of the unit that
+// it goes through (rows 0: none, or another cut's unit).  A warp per query row:
+// o = sum_s o_s 2^(m_s - m) / sum_s l_s 2^(m_s - m).
 constexpr int kJoinWarps = 4;
 
-template <int MT>
-__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ TreeArgs a,
-                                                                     int ctas)
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ JoinArgs a)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const long long total = a.prefix[a.B];
-    const long long per = (total + ctas - 1) / ctas;
     const int c = blockIdx.x + 1;
-    const long long pos = c * per;
-    if (pos >= total)
+    const JoinPlan j = a.plan[c];
+    const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    if (r >= j.rows)
         return;
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.prefix[mid] <= pos)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    uint32_t bad = 0;
-    const Work w = work_of<MT>(a, lo, bad);
-    const long long unit = (pos - a.prefix[lo]) / w.tiles;
-    const long long u0 = a.prefix[lo] + unit * w.tiles;
-    if (u0 == pos || u0 / per != c - 1)
-        return;
-    const int c0 = c - 1, c1 = (int)((u0 + w.tiles - 1) / per);
-    const int h = (int)(unit / w.blocks), m = (int)(unit % w.blocks);
-    const int rows = min(w.nt * a.G - m * MT * kTile, MT * kTile);
-    auto part_row = [&](int cc, int r) {
-        const int part = 2 * cc + (u0 > cc * per ? 1 : 0);
-        return (size_t)part * a.part_rows + r;
+    // part s of the unit: CTA c - 1 + s's; its second one where the unit starts inside its range
+    auto part_row = [&](int s) {
+        return (size_t)(2 * (c - 1 + s) + (s == 0 && j.late ? 1 : 0)) * a.part_rows + r;
     };
-    for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < rows; r += gridDim.y * kJoinWarps) {
-        float top = -CUDART_INF_F;
-        for (int cc = c0 + lane; cc <= c1; cc += 32)
-            top = fmaxf(top, a.part_m[part_row(cc, r)]);
+    const int parts = j.last - c + 2;
+    constexpr int kAhead = 8;
+    float top = -CUDART_INF_F, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = 0; s0 < parts; s0 += kAhead) {
+        float ms[kAhead], ls[kAhead];
+        float4 x[kAhead];
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-        float l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int cc = c0; cc <= c1; ++cc) {
-            const size_t p = part_row(cc, r);
-            const float ms = a.part_m[p];
-            const float4 x = *reinterpret_cast<const float4 *>(a.part_o + p * kHeadDim + lane * 4);
-            const float f = ms == -CUDART_INF_F ? 0.0f : exp2f(ms - top);
-            if (f != 0.0f) {      // an empty part has nothing to add
-                l += a.part_l[p] * f;
-                o.x += x.x * f;
-                o.y += x.y * f;
-                o.z += x.z * f;
-                o.w += x.w * f;
+        for (int u = 0; u < kAhead; ++u) {
+            ms[u] = -CUDART_INF_F;
+            if (s0 + u < parts) {
+                const size_t p = part_row(s0 + u);
+                ms[u] = a.part_m[p];
+                ls[u] = a.part_l[p];
+                x[u] = *reinterpret_cast<const float4 *>(a.part_o + p * kHeadDim + lane * 4);
             }
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int row = m * MT * kTile + r;
-        uint2 y;
-        y.x = pack_bf16(o.x * inv, o.y * inv);
-        y.y = pack_bf16(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2 *>(
-            a.out + (((size_t)lo * a.T + row / a.G) * a.Hq + h * a.G + row % a.G) * kHeadDim + lane * 4) = y;
+        float mn = top;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            mn = fmaxf(mn, ms[u]);
+        const float keep = safe_exp2_diff(top, mn);
+        l *= keep;
+        o.x *= keep;
+        o.y *= keep;
+        o.z *= keep;
+        o.w *= keep;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const float f = safe_exp2_diff(ms[u], mn);
+            if (f != 0.0f) {      // an empty part has nothing to add
+                l += ls[u] * f;
+                o.x += x[u].x * f;
+                o.y += x[u].y * f;
+                o.z += x[u].z * f;
+                o.w += x[u].w * f;
+            }
+        }
+        top = mn;
     }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int row = j.row0 + r;
+    uint2 y;
+    y.x = pack_bf16(o.x * inv, o.y * inv);
+    y.y = pack_bf16(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2 *>(
+        a.out + (((size_t)j.b * a.T + row / a.G) * a.Hq + j.h * a.G + row % a.G) * kHeadDim + lane * 4) = y;
 }
 
 template <int MT>
@@ -1061,7 +1159,8 @@ cudaError_t launch(const TreeArgs &a, int sms, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<MT>, a, ctas);
+    const JoinArgs j{a.plan, a.part_m, a.part_l, a.part_o, a.out, a.T, a.Hq, a.G, a.part_rows};
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel, j);
 }
 
 }  // namespace
