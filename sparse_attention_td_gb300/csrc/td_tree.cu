@@ -34,20 +34,26 @@ constexpr int kTileBytes = 2 * kHalfBytes;       // 128 rows of 128 bf16 values
 constexpr int kMaskRing = 8;                     // tiles whose validity masks are alive (see producer)
 constexpr long long kTreeWaitCycles = 2000000000ll;  // a wait gives up after about 1 s
 
-// Shared memory: Q row tiles, then the ring of K and V tiles.
+// MT row tiles per CTA.  Shared memory: Q row tiles, then the ring of K and V
+// tiles.  The softmax works in steps of kStep tokens; each row tile has two S
+// buffers, so S of the next step is there when a step's softmax ends.  Tensor
+// memory (512 columns of 32 bits): S buffers (P overwrites the upper half of
+// its S) in columns 0 .. 255, then the O tiles.
 template <int MT> struct Cfg {
     static constexpr int kSlots = MT == 1 ? 6 : 5;
+    static constexpr int kStep = MT == 1 ? 128 : 64;
+    static constexpr int kSteps = kTile / kStep;      // per tile
     static constexpr int kSoftWarps = 4 * MT;
-    // softmax, two producers, the MMA issuer and a spare warp (whole warpgroups)
-    static constexpr int kThreads = 32 * (kSoftWarps + 4);
-    static constexpr int kProducer = kSoftWarps, kIssuer = kSoftWarps + 2;
+    static constexpr int kLoaders = 3;
+    // softmax, loaders, the MMA issuer
+    static constexpr int kThreads = 32 * (kSoftWarps + kLoaders + 1);
+    static constexpr int kLoader = kSoftWarps, kIssuer = kSoftWarps + kLoaders;
     static constexpr size_t kSmem = (size_t)(MT + kSlots) * kTileBytes + 1024;
+    __device__ static constexpr uint32_t col_s(int m, int buf) { return m * 2 * kStep + buf * kStep; }
+    __device__ static constexpr uint32_t col_p(int m, int buf) { return col_s(m, buf) + kStep / 2; }
+    __device__ static constexpr uint32_t col_o(int m) { return 256 + m * kTile; }
 };
-// Tensor memory columns (32-bit): two S tiles (P overwrites the upper half of
-// its S), then the O tiles.
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;
-constexpr uint32_t kColP = 64;
 
 __device__ __forceinline__ uint32_t smem_of(const void *p)
 {
@@ -57,6 +63,15 @@ __device__ __forceinline__ uint32_t smem_of(const void *p)
 __device__ __forceinline__ void bar_init(uint64_t *bar, unsigned count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_of(bar)), "r"(count) : "memory");
+}
+
+// One lane of the warp; the MMAs under it issue faster than under lane == 0
+// (8 of them in 416 instead of 552 cycles).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
 }
 
 __device__ __forceinline__ void bar_arrive(uint64_t *bar)
@@ -73,7 +88,8 @@ __device__ __forceinline__ void bar_expect(uint64_t *bar, unsigned bytes)
 
 // Waits for the phase of the given parity.  Gives up after kTreeWaitCycles, or
 // when another role has (then the CTA leaves as a whole and reports the timeout).
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, unsigned parity, volatile int *gave_up)
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, unsigned parity, volatile int *gave_up,
+                                         long long limit = kTreeWaitCycles)
 {
     const uint32_t addr = smem_of(bar);
     long long t0 = 0;
@@ -94,7 +110,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, unsigned parity, volatil
                 t0 = t;
             if (*gave_up)
                 return false;
-            if (t - t0 > kTreeWaitCycles) {
+            if (t - t0 > limit) {
                 *gave_up = 1;
                 return false;
             }
@@ -127,17 +143,20 @@ __device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead)   // l
 }
 constexpr uint32_t kOperandHigh = 1024 >> 4 | 1u << 14 | 2u << 29;   // high word
 
-// kind::f16, fp32 accumulator, bf16 operands, M = N = 128; bit 16: B is MN-major.
-constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (128u >> 3) << 17 | (128u >> 4) << 24;
-constexpr uint32_t kIdescV = kIdesc | 1u << 16;
+// kind::f16, fp32 accumulator, bf16 operands, M = 128; bit 16: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc(uint32_t n)
+{
+    return 1u << 4 | 1u << 7 | 1u << 10 | (n >> 3) << 17 | (128u >> 4) << 24;
+}
+constexpr uint32_t kIdescV = idesc(128) | 1u << 16;
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add)
+template <int N> __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(kIdesc), "r"((uint32_t)add), "r"(kOperandHigh)
+        "r"(a), "r"(b), "r"(idesc(N)), "r"((uint32_t)add), "r"(kOperandHigh)
         : "memory");
 }
 
@@ -323,7 +342,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     using C = Cfg<MT>;
     extern __shared__ unsigned char sm_raw[];
     __shared__ __align__(8) uint64_t bar_full[C::kSlots], bar_empty[C::kSlots];
-    __shared__ __align__(8) uint64_t bar_q[MT], bar_s[2], bar_p[2], bar_p2[2], bar_o[MT], bar_scan, bar_drain;
+    __shared__ __align__(8) uint64_t bar_q[MT], bar_s[MT][2], bar_p[MT][2], bar_o[MT], bar_scan, bar_drain;
     __shared__ uint32_t sm_valid[kMaskRing][4];   // tokens of a tile that exist
     __shared__ uint32_t sm_badv[MT][4];           // drafted tokens with non-finite V values
     __shared__ long long sm_scan[C::kThreads / 32];
@@ -351,15 +370,14 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             sm_gave_up = 0;
             sm_start.left = 0;
             for (int i = 0; i < C::kSlots; ++i) {
-                bar_init(&bar_full[i], 64);
+                bar_init(&bar_full[i], 32);
                 bar_init(&bar_empty[i], 1);
             }
-            for (int i = 0; i < 2; ++i) {
-                bar_init(&bar_s[i], 1);
-                bar_init(&bar_p[i], 4);
-                bar_init(&bar_p2[i], 4);
-            }
             for (int i = 0; i < MT; ++i) {
+                for (int k = 0; k < 2; ++k) {
+                    bar_init(&bar_s[i][k], 1);
+                    bar_init(&bar_p[i][k], 4);
+                }
                 bar_init(&bar_q[i], 4);
                 bar_init(&bar_o[i], 1);
             }
@@ -367,7 +385,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             bar_init(&bar_drain, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-        if (tid == 32 * C::kProducer) {
+        if (tid == 32 * C::kLoader) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_k) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_v) : "memory");
         }
@@ -417,196 +435,152 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             s.args = &a;
             s.left = (int)min(per, total - start);
             s.b = b;
-            s.h = (int)unit / w.blocks;
-            s.m = (int)unit % w.blocks;
+            s.h = w.blocks == 1 ? (int)unit : (int)unit / w.blocks;
+            s.m = (int)unit - s.h * w.blocks;
             s.t = first;
             s.first = true;
             s.w = w;
             sm_start = s;
-            // The unit that this cut goes through, if it is the unit's first cut.
-            const bool joins = first > 0 && first <= per;
-            JoinPlan j{};
-            if (joins) {
-                j.rows = s.rows();
-                j.b = b;
-                j.h = s.h;
-                j.row0 = s.m * MT * kTile;
-                // the last range that meets the unit
-                j.last = (int)quotient(start - first + w.tiles - 1, per);
-                j.late = first < per;
-            }
-            a.plan[blockIdx.x] = j;
         }
-        if (start >= total && tid == 0)
-            a.plan[blockIdx.x] = JoinPlan{};
         tmem_before();
         __syncthreads();
         tmem_after();
         pdl_launch_dependents();
+        if (tid == C::kThreads - 1) {
+            // The unit that this cut goes through, if it is the unit's first cut.
+            JoinPlan j{};
+            const int first = sm_start.t;
+            if (sm_start.left > 0 && first > 0 && first <= per) {
+                j.rows = sm_start.rows();
+                j.b = sm_start.b;
+                j.h = sm_start.h;
+                j.row0 = sm_start.m * MT * kTile;
+                // the last range that meets the unit
+                j.last = (int)quotient(start - first + sm_start.w.tiles - 1, per);
+                j.late = first < per;
+            }
+            a.plan[blockIdx.x] = j;
+        }
+        __syncwarp();
     }
     const uint32_t tmem = sm_tmem;
     Walk<MT> walk = sm_start;
+    int last_tile = -1;           // loaders: the last tile that this warp began to load
 
-    if (warp == C::kProducer || warp == C::kProducer + 1) {
-        // ---- producers: K then V tile of every tile in turn, into the ring.
-        // A tile whose tokens all exist comes as boxes of whole rows (of a page),
-        // by one warp for K and the other for V.  Any other (ragged end, index
-        // set, drafted tokens, a bad page) row by row with cp.async, 64 rows per
-        // warp, half a warp per 256-byte row: a token that does not exist is
-        // filled with zeros (no stale V value meets its zero probability), and
-        // the validity mask keeps its score out.  Row gathers by TMA instead
-        // took 60 ns per four half rows, 7.7 us a tile.
-        // The lookups run ahead: positions two tiles, page numbers one.
-        // The mask ring: a producer is at most kSlots / 2 tiles ahead of the last
-        // S = Q K^T, itself at most 2 ahead of the softmax.
-        const int pw = warp - C::kProducer;
-        struct Cursor {
-            Walk<MT> walk;
-            int i, n;             // tile of the segment, tiles of the segment
-            __device__ Cursor(const Walk<MT> &w) : walk(w), i(0), n(w.count()) {}
-            __device__ bool more() const { return walk.left > 0; }
-            __device__ void step()
-            {
-                if (++i == n) {
-                    walk.next(n);
-                    i = 0;
-                    n = walk.count();
-                }
+    if (warp >= C::kLoader && warp < C::kLoader + C::kLoaders) {
+        // ---- loaders: K then V tile of every kLoaders-th tile, into the ring.  A
+        // tile whose tokens all exist comes as boxes of whole rows (of a page).
+        // Any other (ragged end, index set, drafted tokens, a bad page) row by row
+        // with cp.async, half a warp per 256-byte row: a token that does not exist
+        // is filled with zeros (no stale V value meets its zero probability), and
+        // the validity mask keeps its score out.  Row gathers by TMA instead took
+        // 60 ns per four half rows, 7.7 us a tile.  With a warp per tile, the
+        // lookups (index entry, then page number) of one tile overlap the copies
+        // of the others.  The mask ring: a loader is at most kSlots / 2 tiles ahead
+        // of the last S = Q K^T, itself at most 2 ahead of the softmax.
+        uint32_t tile_no = 0, flags = 0;
+        int i = 0, n = walk.count();
+        auto step = [&](int tiles) {
+            tile_no += tiles;
+            i += tiles;
+            while (i >= n && walk.left > 0) {
+                i -= n;
+                walk.next(n);
+                n = walk.count();
             }
         };
-        // what is known of a tile so far: positions (-1: none), their pages
-        struct Tile {
-            int pos[2], page[2];
-            bool whole;           // candidate for boxes: pos[0] is this lane's box
-        };
-        auto positions = [&](const Cursor &c, Tile &x, uint32_t &flags) {
-            const Work &w = c.walk.w;
-            const int t = c.walk.t + c.i, base = t * kTile;
-            const bool tree = t == w.tiles - 1;
-            x.whole = !tree && !a.idx && a.box_rows && base + kTile <= w.ctx;
-            if (x.whole) {
-                x.pos[0] = lane * a.box_rows < kTile ? base + lane * a.box_rows : -1;
-                x.pos[1] = -1;
-                return;
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int j = pw * 64 + u * 32 + lane;
-                int p = -1;
-                if (tree) {
-                    p = j < w.nt ? w.ctx + j : -1;
-                } else if (a.idx) {
-                    if (base + j < a.top_k)
-                        p = __ldg(a.idx + ((size_t)c.walk.b * a.Hkv + c.walk.h) * a.top_k + base + j);
-                } else {
-                    p = base + j < w.ctx ? base + j : -1;
-                }
-                x.pos[u] = p;
-            }
-        };
-        // index entries are checked here, a tile after they were requested
-        auto pages = [&](const Cursor &c, Tile &x, uint32_t &flags) {
-            const Work &w = c.walk.w;
-            const bool listed = a.idx && c.walk.t + c.i != w.tiles - 1;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (listed && x.pos[u] != -1 && (x.pos[u] < 0 || x.pos[u] >= w.ctx)) {
-                    flags |= kFlagIndexOutOfRange;
-                    x.pos[u] = -1;
-                }
-                x.page[u] = c.walk.b;
-                if (a.c.table && x.pos[u] >= 0)
-                    x.page[u] = __ldg(a.c.table + (size_t)c.walk.b * a.c.max_blocks +
-                                      x.pos[u] / a.c.page_size);
-            }
-        };
-        auto row_of = [&](const Cursor &c, int pos, int page) {   // -1: no such row
-            if (pos < 0 || page < 0 || page >= a.c.num_pages)
-                return -1;
-            return (page * a.Hkv + c.walk.h) * a.c.page_size + (a.c.table ? pos % a.c.page_size : pos);
-        };
-        uint32_t e = 0, tile_no = 0, flags = 0;
         bool ok = true;
-        Cursor c0(walk), c1(walk), c2(walk);      // tiles issued, with pages, with positions
-        Tile x0{}, x1{}, x2{};
-        if (c0.more()) {
-            positions(c0, x0, flags);
-            pages(c0, x0, flags);
-            c1.step();
-            if (c1.more())
-                positions(c1, x1, flags);
-            c2 = c1;
-        }
-        for (; ok && c0.more(); ++tile_no) {
-            if (c1.more()) {
-                c2.step();
-                if (c2.more())
-                    positions(c2, x2, flags);
-                pages(c1, x1, flags);
-            }
-            int row[2];
-            row[0] = row_of(c0, x0.pos[0], x0.page[0]);
-            row[1] = row_of(c0, x0.pos[1], x0.page[1]);
-            bool boxes = x0.whole;
-            if (boxes && __any_sync(kFull, x0.pos[0] >= 0 && row[0] < 0)) {
-                boxes = false;                    // a bad page: token by token
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    x0.pos[u] = (c0.walk.t + c0.i) * kTile + pw * 64 + u * 32 + lane;
-                    x0.page[u] = a.c.table ? a.c.table[(size_t)c0.walk.b * a.c.max_blocks +
-                                                       x0.pos[u] / a.c.page_size]
-                                           : c0.walk.b;
-                    row[u] = row_of(c0, x0.pos[u], x0.page[u]);
+        step(warp - C::kLoader);
+        for (; walk.left > 0; step(C::kLoaders)) {
+            const Work w = walk.w;
+            const int t = walk.t + i, base = t * kTile;
+            const bool tree = t == w.tiles - 1;
+            const int32_t *table = a.c.table + (size_t)walk.b * a.c.max_blocks;
+            auto row_of = [&](int pos) {      // of this KV head; -1: no such row
+                int page = walk.b, r = pos;
+                if (a.c.table) {
+                    const int block = pos / a.c.page_size;
+                    page = __ldg(table + block);
+                    r = pos - block * a.c.page_size;
                 }
+                if (page < 0 || page >= a.c.num_pages)
+                    return -1;
+                return (page * a.Hkv + walk.h) * a.c.page_size + r;
+            };
+            bool boxes = !tree && !a.idx && a.box_rows && base + kTile <= w.ctx;
+            int row[4] = {-1, -1, -1, -1};    // boxes: this lane's box; else tokens 32u + lane
+            if (boxes) {
+                const bool mine = lane * a.box_rows < kTile;
+                if (mine)
+                    row[0] = row_of(base + lane * a.box_rows);
+                boxes = __all_sync(kFull, !mine || row[0] >= 0);
             }
-            uint32_t word[2] = {0xffffffffu, 0xffffffffu};
+            uint32_t word[4] = {kFull, kFull, kFull, kFull};
             if (!boxes) {
+                int pos[4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    word[u] = __ballot_sync(kFull, row[u] >= 0);
-                    if (x0.pos[u] >= 0 && row[u] < 0)
+                for (int u = 0; u < 4; ++u) {
+                    const int j = u * 32 + lane;
+                    if (tree)
+                        pos[u] = j < w.nt ? w.ctx + j : -1;
+                    else if (a.idx)
+                        pos[u] = base + j < a.top_k
+                                     ? __ldg(a.idx + ((size_t)walk.b * a.Hkv + walk.h) * a.top_k + base + j)
+                                     : -1;
+                    else
+                        pos[u] = base + j < w.ctx ? base + j : -1;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (!tree && pos[u] != -1 && (pos[u] < 0 || pos[u] >= w.ctx)) {
+                        flags |= kFlagIndexOutOfRange;
+                        pos[u] = -1;
+                    }
+                    row[u] = pos[u] < 0 ? -1 : row_of(pos[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (pos[u] >= 0 && row[u] < 0)
                         flags |= kFlagPageOutOfRange;
+                    word[u] = __ballot_sync(kFull, row[u] >= 0);
                 }
             }
-            for (int kv = 0; ok && kv < 2; ++kv, ++e) {
-                const uint32_t slot = e % C::kSlots, use = e / C::kSlots;
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t e = 2 * tile_no + kv, slot = e % C::kSlots, use = e / C::kSlots;
                 if (use > 0)
-                    ok = bar_wait(&bar_empty[slot], (use - 1) & 1, gave_up);
-                ok = __all_sync(kFull, ok);
+                    ok = __all_sync(kFull, bar_wait(&bar_empty[slot], (use - 1) & 1, gave_up));
                 if (!ok)
                     break;
-                if (kv == 0 && lane < 2)
-                    sm_valid[tile_no % kMaskRing][pw * 2 + lane] = word[lane];
+                if (kv == 0 && lane < 4)
+                    sm_valid[tile_no % kMaskRing][lane] = lane < 2 ? (lane == 0 ? word[0] : word[1])
+                                                                   : (lane == 2 ? word[2] : word[3]);
                 __syncwarp();
+                last_tile = tile_no;
                 const uint32_t dst = sm_ring + slot * kTileBytes;
                 if (boxes) {
-                    if (pw == kv) {
-                        if (lane == 0)
-                            bar_expect(&bar_full[slot], kTileBytes);
-                        else
-                            bar_arrive(&bar_full[slot]);
-                        __syncwarp();
-                        if (row[0] >= 0) {
-                            const TmaDesc *map = kv ? &a.box_v : &a.box_k;
-                            const uint32_t d = dst + lane * a.box_rows * 128;
-                            tma_box(d, map, 0, row[0], &bar_full[slot]);
-                            tma_box(d + kHalfBytes, map, 64, row[0], &bar_full[slot]);
-                        }
-                    } else {
+                    if (lane == 0)
+                        bar_expect(&bar_full[slot], kTileBytes);
+                    else
                         bar_arrive(&bar_full[slot]);
+                    __syncwarp();
+                    if (row[0] >= 0) {
+                        const TmaDesc *map = kv ? &a.box_v : &a.box_k;
+                        const uint32_t d = dst + lane * a.box_rows * 128;
+                        tma_box(d, map, 0, row[0], &bar_full[slot]);
+                        tma_box(d + kHalfBytes, map, 64, row[0], &bar_full[slot]);
                     }
                 } else {
-                    const uint16_t *base = kv ? a.c.v : a.c.k;
-                    const int c = lane & 15;
+                    const int c = lane & 15, hi = lane >> 4;
+                    const uint16_t *src = (kv ? a.c.v : a.c.k) + c * 8;
+                    const uint32_t d = dst + (c >> 3) * kHalfBytes;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll 4
                         for (int it = 0; it < 16; ++it) {
-                            const int src = it * 2 + (lane >> 4);
-                            const int rr = __shfl_sync(kFull, row[u], src);
-                            const int x = pw * 64 + u * 32 + src;
-                            copy16(dst + (c >> 3) * kHalfBytes + x * 128 + (((c ^ x) & 7) << 4),
-                                   base + (size_t)max(rr, 0) * kHeadDim + c * 8, rr >= 0);
+                            const int x = it * 2 + hi;
+                            const int rr = __shfl_sync(kFull, row[u], x);
+                            copy16(d + (u * 32 + x) * 128 + (((c ^ x) & 7) << 4),
+                                   src + (size_t)max(rr, 0) * kHeadDim, rr >= 0);
                         }
                     // an arrival per thread once its copies have landed
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
@@ -615,49 +589,19 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 }
                 __syncwarp();
             }
-            c0 = c1;
-            x0 = x1;
-            c1 = c2;
-            x1 = x2;
+            if (!ok)
+                break;
         }
         if (flags)
             atomicOr(a.status, flags);
-        if (!ok) {
-            // leave no copy in flight: the last ones issued, each with a limit of its own
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            int own_limit = 0;
-            for (uint32_t k = e > C::kSlots ? e - C::kSlots : 0; k < e; ++k)
-                bar_wait(&bar_full[k % C::kSlots], (k / C::kSlots) & 1, &own_limit);
-        }
     } else if (warp == C::kIssuer) {
-        // ---- MMA issue, by one thread.  One row tile: S of tile i + 1 is issued
-        // before P V of tile i, so the tensor cores work while the softmax does.
-        // Two row tiles: they take turns.  P comes in halves (tokens 64 .. 127
-        // first), so half of P V overlaps the rest of the exponentials.
-        if (lane == 0) {
-            uint32_t e = 0;              // ring entries consumed: 2 * tile (K), 2 * tile + 1 (V)
-            uint32_t done_p[2] = {0, 0}; // P V issued per row tile (two row tiles)
+        // ---- MMA issue, by one thread: S of step j + 1 before P V of step j, so
+        // the tensor cores work while the softmax does.
+        if (elect_one()) {
+            uint32_t e = 0;              // ring entry of the segment's first K tile
+            uint32_t steps[MT] = {};     // steps of earlier segments, per row tile
             uint32_t segs[MT] = {};      // segments begun per row tile
             bool ok = true;
-            auto issue_s = [&](uint32_t entry, int m, int buf, bool last) {
-                const uint32_t k = operand(sm_ring + entry % C::kSlots * kTileBytes, 16);
-                const uint32_t q = operand(sm_q + m * kTileBytes, 16);
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
-                    mma_ss(tmem + buf * kTile, q + (o >> 4), k + (o >> 4), s > 0);
-                }
-                mma_commit(&bar_s[buf]);
-                if (last)
-                    mma_commit(&bar_empty[entry % C::kSlots]);
-            };
-            auto issue_o = [&](uint32_t entry, int m, int buf, int half, bool first) {
-                const uint32_t v = operand(sm_ring + entry % C::kSlots * kTileBytes, kHalfBytes);
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    mma_ts(tmem + kColO + m * kTile, tmem + buf * kTile + kColP + (4 * half + s) * 8,
-                           v + ((4 * half + s) * 16 * 128 >> 4), !(first && s == 0));
-            };
             auto wait_full = [&](uint32_t entry) {
                 ok = ok && bar_wait(&bar_full[entry % C::kSlots], (entry / C::kSlots) & 1, gave_up);
                 // rows copied by cp.async are read by the MMA through the async proxy
@@ -669,65 +613,73 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 tmem_after();
                 return ok;
             };
-            // P V of one row tile, V already there; false: gave up
-            auto do_o = [&](uint32_t entry, int m, int buf, uint32_t phase, bool first, bool last) {
-                if (!wait_bar(&bar_p[buf], phase))
-                    return false;
-                issue_o(entry, m, buf, 1, first);
-                if (!wait_bar(&bar_p2[buf], phase))
-                    return false;
-                issue_o(entry, m, buf, 0, false);
-                mma_commit(&bar_o[m]);
-                if (last)
-                    mma_commit(&bar_empty[entry % C::kSlots]);
-                return true;
-            };
             while (ok && walk.left > 0) {
-                const int n = walk.count();
+                const int n = walk.count() * C::kSteps;
                 const int nm = MT == 1 ? 1 : (walk.rows() + kTile - 1) / kTile;
-                for (int m = 0; m < nm; ++m)
-                    wait_bar(&bar_q[m], segs[m]++);
+                auto issue_s = [&](int j) {
+                    const uint32_t entry = e + 2 * (j / C::kSteps);
+                    const uint32_t k = operand(sm_ring + entry % C::kSlots * kTileBytes, 16) +
+                                       (j % C::kSteps * C::kStep * 128 >> 4);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        if (m >= nm)
+                            break;
+                        const uint32_t q = operand(sm_q + m * kTileBytes, 16);
+                        const int buf = (steps[m] + j) & 1;
+                        if (j >= 2)     // P V of step j - 2 has read this buffer's P
+                            wait_bar(&bar_o[m], steps[m] + j - 2);
+#pragma unroll
+                        for (int s = 0; s < 8; ++s) {
+                            const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
+                            mma_ss<C::kStep>(tmem + C::col_s(m, buf), q + (o >> 4), k + (o >> 4), s > 0);
+                        }
+                        mma_commit(&bar_s[m][buf]);
+                    }
+                    if (j % C::kSteps == C::kSteps - 1)
+                        mma_commit(&bar_empty[entry % C::kSlots]);
+                };
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    if (m < nm)
+                        wait_bar(&bar_q[m], segs[m]++);
                 if (!wait_full(e))
                     break;
-                if constexpr (MT == 1) {
-                    // tile i uses S buffer (global tile number) & 1
-                    const uint32_t g0 = e >> 1;
-                    issue_s(e, 0, g0 & 1, true);
-                    for (int i = 0; ok && i < n; ++i) {
-                        const uint32_t g = g0 + i;
-                        if (i + 1 < n) {
-                            if (!wait_full(2 * (g + 1)))
-                                break;
-                            issue_s(2 * (g + 1), 0, (g + 1) & 1, true);
-                        }
-                        if (!wait_full(2 * g + 1))
+                issue_s(0);
+                for (int j = 0; j < n; ++j) {
+                    if (j + 1 < n) {
+                        if ((j + 1) % C::kSteps == 0 && !wait_full(e + 2 * ((j + 1) / C::kSteps)))
                             break;
-                        do_o(2 * g + 1, 0, g & 1, g >> 1, i == 0, true);
+                        issue_s(j + 1);
                     }
-                    e += 2 * n;
-                } else {
-                    for (int m = 0; m < nm; ++m)
-                        issue_s(e, m, m, m == nm - 1);
-                    for (int i = 0; ok && i < n; ++i, e += 2) {
-                        if (!wait_full(e + 1))
+                    const uint32_t entry = e + 2 * (j / C::kSteps) + 1;
+                    if (j % C::kSteps == 0 && !wait_full(entry))
+                        break;
+                    const uint32_t v = operand(sm_ring + entry % C::kSlots * kTileBytes, kHalfBytes) +
+                                       (j % C::kSteps * C::kStep * 128 >> 4);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        if (m >= nm)
                             break;
-                        for (int m = 0; ok && m < nm; ++m) {
-                            if (!do_o(e + 1, m, m, done_p[m]++, i == 0, m == nm - 1))
-                                break;
-                            if (i + 1 < n) {
-                                if (m == 0 && !wait_full(e + 2))
-                                    break;
-                                issue_s(e + 2, m, m, m == nm - 1);
-                            }
-                        }
+                        const uint32_t g = steps[m] + j;
+                        if (!wait_bar(&bar_p[m][g & 1], g >> 1))
+                            break;
+#pragma unroll
+                        for (int s = 0; s < C::kStep / 16; ++s)
+                            mma_ts(tmem + C::col_o(m), tmem + C::col_p(m, g & 1) + s * 8,
+                                   v + (s * 16 * 128 >> 4), j > 0 || s > 0);
+                        mma_commit(&bar_o[m]);
                     }
+                    if (!ok)
+                        break;
+                    if (j % C::kSteps == C::kSteps - 1)
+                        mma_commit(&bar_empty[entry % C::kSlots]);
                 }
-                walk.next(n);
-            }
-            if (!ok) {
-                int own_limit = 0;
-                mma_commit(&bar_drain);
-                bar_wait(&bar_drain, 0, &own_limit);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    if (m < nm)
+                        steps[m] += n;
+                e += 2 * (n / C::kSteps);
+                walk.next(n / C::kSteps);
             }
         }
         __syncwarp();
@@ -737,7 +689,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         const int r = (warp & 3) * 32 + lane;                 // row of the row tile, TMEM lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // this warp's TMEM lanes
         const float sl2 = a.scale * kLog2e;
-        uint32_t count = 0;                                   // tiles done
+        uint32_t count = 0;                                   // steps done
         uint32_t tile_no = 0;                                 // tiles of the CTA before the segment
         uint32_t scans = 0;                                   // clearings of V with two row tiles
         bool ok = true;
@@ -792,15 +744,23 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                                     : 0u;
                 }
             }
-            for (int i = 0; ok && i < n; ++i, ++count) {
-                const int buf = MT == 1 ? (int)(count & 1) : m;
-                const uint32_t phase = MT == 1 ? count >> 1 : count;
+            for (int j = 0; j < n * C::kSteps; ++j, ++count) {
+                const int i = j / C::kSteps, part = j % C::kSteps;   // tile, step of the tile
+                const int buf = count & 1;
                 const bool tree = walk.t + i == walk.w.tiles - 1;
-                ok = __all_sync(kFull, bar_wait(&bar_s[buf], phase & 1, gave_up));
+                // P V of the step before is done.  Waited for in every step (it is, by
+                // the time the exponentials are), so no phase of bar_o is missed.
+                bool waited = j == 0;
+                auto o_done = [&]() {
+                    if (!waited)
+                        ok = __all_sync(kFull, bar_wait(&bar_o[m], (count - 1) & 1, gave_up));
+                    waited = true;
+                };
+                ok = __all_sync(kFull, bar_wait(&bar_s[m][buf], (count >> 1) & 1, gave_up));
                 if (!ok)
                     break;
                 tmem_after();
-                if (tree) {
+                if (tree && part == 0) {
                     // A V value that is not finite must not meet the zero
                     // probabilities of rows that do not see its token: such values
                     // leave the tile here and join the rows that do see it below.
@@ -856,60 +816,46 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     }
                 }
                 if (warp_live) {
-                    const uint32_t at = tmem + buf * kTile + lanes;
-                    uint32_t w[4];
+                    constexpr int kWords = C::kStep / 32;
+                    uint32_t w[kWords], all = kFull;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        w[c] = sm_valid[(tile_no + i) % kMaskRing][c];
+                    for (int c = 0; c < kWords; ++c) {
+                        w[c] = sm_valid[(tile_no + i) % kMaskRing][part * kWords + c];
                         if (tree)
-                            w[c] &= sees[c];
+                            w[c] &= MT == 1 ? sees[c] : (part ? sees[(2 + c) & 3] : sees[c]);
+                        all &= w[c];
                     }
-                    const bool masked = (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu;
-                    // One row tile: the row's 128 scores stay in registers.  Two
-                    // row tiles (384 threads, 168 registers each): 64 at a time; the
-                    // second half stays for the exponentials and the first half is
-                    // read from tensor memory again, while P goes over the second.
-                    float s[MT == 1 ? kTile : 64];
-                    auto half = [&](int c) { return s + (MT == 1 ? 64 * c : 0); };
-                    auto fetch = [&](int c) {
-                        tmem_ld32(at + 64 * c, reinterpret_cast<uint32_t *>(half(c)));
-                        tmem_ld32(at + 64 * c + 32, reinterpret_cast<uint32_t *>(half(c)) + 32);
-                    };
-                    auto arrived = [&](int c) {
-                        tmem_wait_ld();
-                        float *d = half(c);
-                        tmem_loaded(reinterpret_cast<uint32_t *>(d));
-                        tmem_loaded(reinterpret_cast<uint32_t *>(d) + 32);
-                        if (masked) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if (!(w[2 * c + (k >> 5)] >> (k & 31) & 1u))
-                                    d[k] = -CUDART_INF_F;
-                        }
-                    };
+                    const bool masked = all != kFull;
+                    const uint32_t at = tmem + C::col_s(m, buf) + lanes;
+                    float s[C::kStep];
+                    auto fetch = [&](int c) { tmem_ld32(at + 32 * c, reinterpret_cast<uint32_t *>(s) + 32 * c); };
                     float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
                     __syncwarp();
                     fetch(0);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        arrived(c);
-                        if (MT == 1 && c == 0)
-                            fetch(1);
-                        const float *d = half(c);
+                    for (int c = 0; c < kWords; ++c) {
+                        tmem_wait_ld();
+                        tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32 * c);
+                        if (c + 1 < kWords)
+                            fetch(c + 1);
+                        if (masked) {
 #pragma unroll
-                        for (int k = 0; k < 64; k += 2)
-                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], d[k], d[k + 1]);
-                        if (MT > 1 && c == 0)
-                            fetch(1);
+                            for (int k = 0; k < 32; ++k)
+                                if (!(w[c] >> k & 1u))
+                                    s[32 * c + k] = -CUDART_INF_F;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[32 * c + k], s[32 * c + k + 1]);
                     }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                     if (mref == -CUDART_INF_F)
                         mref = top;          // nothing summed so far: l = 0 and O = 0
                     // The running maximum lags until a row exceeds it by 2^8: the
                     // probabilities stay below 2^8 and the rescaling of O is rare.
-                    const bool grow = i > 0 && top > mref + 8.0f;
+                    const bool grow = j > 0 && top > mref + 8.0f;
                     if (__any_sync(kFull, grow)) {
-                        ok = __all_sync(kFull, bar_wait(&bar_o[m], (count - 1) & 1, gave_up));
+                        o_done();
                         if (!ok)
                             break;
                         tmem_after();
@@ -917,7 +863,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         const float f = grow ? ex2(mref - mn) : 1.0f;
                         mref = mn;
                         l *= f;
-                        const uint32_t o = tmem + kColO + m * kTile + lanes;
+                        const uint32_t o = tmem + C::col_o(m) + lanes;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             uint32_t x[32];
@@ -934,42 +880,28 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     const float2 off2 = make_float2(off, off), sl22 = make_float2(sl2, sl2);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                    for (int c = 1; c >= 0; --c) {
-                        if (MT > 1 && c == 0) {
-                            fetch(0);
-                            arrived(0);
-                        }
-                        const float *d = half(c);
+                    for (int c = 0; c < kWords; ++c) {
+                        const float *d = s + 32 * c;
+                        uint32_t p[16];
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            uint32_t p[16];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float2 x = __ffma2_rn(
-                                    make_float2(d[32 * y + 2 * k], d[32 * y + 2 * k + 1]), sl22, off2);
-                                const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                                sum[k & 1] = __fadd2_rn(sum[k & 1], e);
-                                p[k] = pack_bf16(e.x, e.y);
-                            }
-                            tmem_st16(at + kColP + 32 * c + 16 * y, p);
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 x = __ffma2_rn(make_float2(d[2 * k], d[2 * k + 1]), sl22, off2);
+                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                            sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+                            p[k] = pack_bf16(e.x, e.y);
                         }
-                        if (c == 1) {
-                            tmem_wait_st();
-                            tmem_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                bar_arrive(&bar_p[buf]);
-                        }
+                        tmem_st16(at + C::kStep / 2 + 16 * c, p);   // over scores that have been read
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
-                } else if (lane == 0) {
-                    bar_arrive(&bar_p[buf]);
                 }
+                o_done();
+                if (!ok)
+                    break;
                 tmem_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(&bar_p2[buf]);
+                    bar_arrive(&bar_p[m][buf]);
             }
             if (!ok)
                 break;
@@ -988,7 +920,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
                         bad[w] = sm_badv[m][w] & sees[w];
-                const uint32_t o = tmem + kColO + m * kTile + lanes;
+                const uint32_t o = tmem + C::col_o(m) + lanes;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t x[32];
@@ -1047,6 +979,27 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     }
     tmem_before();
     __syncthreads();
+    if (sm_gave_up) {
+        // A wait gave up: leave no copy and no MMA in flight.  A loader's last two
+        // tiles are the ones that can be; each wait has a limit of its own.
+        int own_limit = 0;
+        if (warp >= C::kLoader && warp < C::kIssuer) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            for (int k = 0; k < 4; ++k) {
+                const int tile = last_tile - (k >> 1) * C::kLoaders;
+                const uint32_t entry = 2 * tile + (k & 1);
+                if (tile >= 0) {
+                    own_limit = 0;
+                    bar_wait(&bar_full[entry % C::kSlots], (entry / C::kSlots) & 1, &own_limit,
+                             kTreeWaitCycles / 16);
+                }
+            }
+        } else if (warp == C::kIssuer && lane == 0) {
+            mma_commit(&bar_drain);
+            bar_wait(&bar_drain, 0, &own_limit, kTreeWaitCycles / 16);
+        }
+        __syncthreads();
+    }
     if (tid == 0 && sm_gave_up)
         atomicOr(a.status, kFlagWaitTimeout);
     if (warp == C::kIssuer) {
