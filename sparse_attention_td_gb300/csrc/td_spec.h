@@ -55,6 +55,7 @@ struct TreeArgs {
     float *part_m, *part_l;     // [2 * ctas][part_rows]
     float *part_o;              // [2 * ctas][part_rows][128]
     int B, T, W, Hq, Hkv, G, Nmax, top_k;
+    int g_shift;                // log2(G)
     int box_rows;               // 0: no boxes, every tile goes row by row
     int part_rows;
     float scale;                // softmax scale (natural-log units)

@@ -110,6 +110,7 @@ td_status run_tree(const td_shape *shape, const td_cache *cache, int32_t tree_si
     a.idx = idx;
     a.status = (uint32_t *)ws;
     a.G = shape->num_q_heads / shape->num_kv_heads;
+    a.g_shift = a.G == 1 ? 0 : a.G == 2 ? 1 : a.G == 4 ? 2 : 3;
     a.part_rows = td::tree_part_rows(tree_size * a.G);
     const TreeWs w = tree_ws(*shape, tree_size);
     char *base = (char *)ws + (ws_bytes - (w.total - kAlign)) / kAlign * kAlign;

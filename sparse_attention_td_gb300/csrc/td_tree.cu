@@ -45,6 +45,11 @@ template <int MT> struct Cfg {
     static constexpr int kSteps = kTile / kStep;      // per tile
     static constexpr int kSoftWarps = 4 * MT;
     static constexpr int kLoaders = 3;
+    // A loader's waits see a slot's phases by their parity, so when it waits for
+    // the last use of a slot, the use before that one has to be over.  It is once
+    // the loader's own last wait is: that was for entry e - 2 * kLoaders + 1 - kSlots
+    // to be read, at or behind e - 2 * kSlots.
+    static_assert(2 * kLoaders - 1 <= kSlots, "a loader could be two uses of a slot ahead");
     // softmax, loaders, the MMA issuer
     static constexpr int kThreads = 32 * (kSoftWarps + kLoaders + 1);
     static constexpr int kLoader = kSoftWarps, kIssuer = kSoftWarps + kLoaders;
@@ -134,6 +139,36 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there
                  : "memory");
 }
 
+// The barrier gets this thread's arrival once all of its copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+
+// The rows of a tile by one warp, half a warp per 256-byte row: token 32u + x
+// is row r[u] of lane x; bit x of w[u] says whether it exists (else zeros).
+// Chunk c of row x goes to x * 128 + ((c ^ x) & 7) * 16 of its half.
+__device__ __forceinline__ void copy_rows(uint32_t dst, const uint16_t *src, const int (&r)[4],
+                                          const uint32_t (&w)[4], int lane)
+{
+    const int c = lane & 15, hi = lane >> 4;
+    const uint16_t *s = src + c * 8;
+    uint32_t at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        at[i] = dst + (c >> 3) * kHalfBytes + (2 * i + hi) * 128 + (((c ^ (2 * i + hi)) & 7) << 4);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t bits = w[u] >> hi;
+#pragma unroll 4
+        for (int it = 0; it < 16; ++it) {
+            const int row = __shfl_sync(kFull, r[u], 2 * it + hi);
+            copy16(at[it & 3] + (u * 32 + (it & ~3) * 2) * 128, s + (size_t)row * kHeadDim,
+                   bits >> (2 * it) & 1u);
+        }
+    }
+}
+
 // Shared-memory operand of tcgen05.mma, 128-byte swizzle.  K-major (rows of
 // 128 bytes, groups of 8 rows 1024 bytes apart) or, for V, MN-major: 64-value
 // blocks of the dims `lead` bytes apart, groups of 8 tokens 1024 bytes apart.
@@ -220,16 +255,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
         "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
         "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -342,7 +367,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     using C = Cfg<MT>;
     extern __shared__ unsigned char sm_raw[];
     __shared__ __align__(8) uint64_t bar_full[C::kSlots], bar_empty[C::kSlots];
-    __shared__ __align__(8) uint64_t bar_q[MT], bar_s[MT][2], bar_p[MT][2], bar_o[MT], bar_scan, bar_drain;
+    __shared__ __align__(8) uint64_t bar_q[2], bar_q0, bar_qfree[2], bar_s[MT][2], bar_p[MT][2], bar_o[MT], bar_scan, bar_drain;
     __shared__ uint32_t sm_valid[kMaskRing][4];   // tokens of a tile that exist
     __shared__ uint32_t sm_badv[MT][4];           // drafted tokens with non-finite V values
     __shared__ long long sm_scan[C::kThreads / 32];
@@ -378,9 +403,13 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     bar_init(&bar_s[i][k], 1);
                     bar_init(&bar_p[i][k], 4);
                 }
-                bar_init(&bar_q[i], 4);
                 bar_init(&bar_o[i], 1);
             }
+            bar_init(&bar_q[0], 32);
+            bar_init(&bar_q[1], 32);
+            bar_init(&bar_q0, 32 * C::kLoaders);
+            bar_init(&bar_qfree[0], 1);
+            bar_init(&bar_qfree[1], 1);
             bar_init(&bar_scan, 4);
             bar_init(&bar_drain, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -465,6 +494,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     }
     const uint32_t tmem = sm_tmem;
     Walk<MT> walk = sm_start;
+    // Up to 64 query rows per unit: Q has two buffers of 64 rows, and the next
+    // segment's comes in during this one.  (The MMA reads 128 rows from either;
+    // the rows that are not Q's end in S and O rows that nobody reads.)
+    const bool two_q = MT == 1 && a.part_rows <= 64;
     int last_tile = -1;           // loaders: the last tile that this warp began to load
 
     if (warp >= C::kLoader && warp < C::kLoader + C::kLoaders) {
@@ -478,7 +511,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         // lookups (index entry, then page number) of one tile overlap the copies
         // of the others.  The mask ring: a loader is at most kSlots / 2 tiles ahead
         // of the last S = Q K^T, itself at most 2 ahead of the softmax.
-        uint32_t tile_no = 0, flags = 0;
+        uint32_t tile_no = 0, flags = 0, seg = 0;
         int i = 0, n = walk.count();
         auto step = [&](int tiles) {
             tile_no += tiles;
@@ -487,110 +520,169 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 i -= n;
                 walk.next(n);
                 n = walk.count();
+                ++seg;
+            }
+        };
+        // Q rows of a segment, by the loader of its first tile (the first segment's:
+        // by all loaders, before anything else).  Rows that are not Q's are left
+        // as they are: they end in S and O rows that nobody reads.
+        auto load_q = [&](int b, int h, int row0, int rows, uint32_t s, int from, int stride) {
+            const int c = lane & 15, hi = lane >> 4;
+            const uint16_t *src = a.q + ((size_t)b * a.T * a.Hq + h * a.G) * kHeadDim + c * 8;
+            const uint32_t dst = sm_q + (two_q ? s & 1 : 0) * 64 * 128 + (c >> 3) * kHalfBytes;
+#pragma unroll 4
+            for (int x = 2 * from + hi; x < rows; x += 2 * stride) {
+                const int row = row0 + x, tk = row >> a.g_shift, g = row & (a.G - 1);
+                copy16(dst + (x >> 7) * kTileBytes + (x & 127) * 128 + (((c ^ x) & 7) << 4),
+                       src + ((size_t)tk * a.Hq + g) * kHeadDim, true);
+            }
+        };
+        if (walk.left > 0) {
+            load_q(walk.b, walk.h, walk.m * MT * kTile, walk.rows(), 0, warp - C::kLoader, C::kLoaders);
+            copies_arrive(&bar_q0);
+        }
+        // A tile's rows are found in three steps, each before one of the copies of
+        // the tile before (memory is slow to answer while every SM's ring fills):
+        // positions, pages, rows.
+        bool boxes = false;
+        int pos[4], page[4], row[4];      // boxes: [0] is this lane's box; else tokens 32u + lane
+        uint32_t word[4];
+        auto page_of = [&](int p) {
+            return a.c.table ? __ldg(a.c.table + (size_t)walk.b * a.c.max_blocks + p / a.c.page_size)
+                             : walk.b;
+        };
+        auto find_positions = [&]() {
+            const int t = walk.t + i, base = t * kTile;
+            const bool tree = t == walk.w.tiles - 1;
+            boxes = !tree && !a.idx && a.box_rows && base + kTile <= walk.w.ctx;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = u * 32 + lane;
+                if (boxes)
+                    pos[u] = u == 0 && lane * a.box_rows < kTile ? base + lane * a.box_rows : -1;
+                else if (tree)
+                    pos[u] = j < walk.w.nt ? walk.w.ctx + j : -1;
+                else if (a.idx)
+                    pos[u] = base + j < a.top_k
+                                 ? __ldg(a.idx + ((size_t)walk.b * a.Hkv + walk.h) * a.top_k + base + j)
+                                 : -1;
+                else
+                    pos[u] = base + j < walk.w.ctx ? base + j : -1;
+            }
+        };
+        auto find_pages = [&]() {
+            const bool listed = a.idx && walk.t + i != walk.w.tiles - 1;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (listed && pos[u] != -1 && (pos[u] < 0 || pos[u] >= walk.w.ctx)) {
+                    flags |= kFlagIndexOutOfRange;
+                    pos[u] = -1;
+                }
+                page[u] = pos[u] < 0 ? 0 : page_of(pos[u]);
+            }
+        };
+        auto find_rows = [&]() {
+            auto row_of = [&](int u) {
+                if (pos[u] < 0 || page[u] < 0 || page[u] >= a.c.num_pages)
+                    return -1;
+                return (page[u] * a.Hkv + walk.h) * a.c.page_size +
+                       (a.c.table ? pos[u] % a.c.page_size : pos[u]);
+            };
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                row[u] = row_of(u);
+            if (boxes && __any_sync(kFull, pos[0] >= 0 && row[0] < 0)) {
+                boxes = false;            // a bad page: token by token
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    pos[u] = (walk.t + i) * kTile + u * 32 + lane;
+                    page[u] = page_of(pos[u]);
+                    row[u] = row_of(u);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (pos[u] >= 0 && row[u] < 0)
+                    flags |= kFlagPageOutOfRange;
+                word[u] = boxes ? kFull : __ballot_sync(kFull, row[u] >= 0);
+                if (!boxes)
+                    row[u] = max(row[u], 0);
             }
         };
         bool ok = true;
         step(warp - C::kLoader);
-        for (; walk.left > 0; step(C::kLoaders)) {
-            const Work w = walk.w;
-            const int t = walk.t + i, base = t * kTile;
-            const bool tree = t == w.tiles - 1;
-            const int32_t *table = a.c.table + (size_t)walk.b * a.c.max_blocks;
-            auto row_of = [&](int pos) {      // of this KV head; -1: no such row
-                int page = walk.b, r = pos;
-                if (a.c.table) {
-                    const int block = pos / a.c.page_size;
-                    page = __ldg(table + block);
-                    r = pos - block * a.c.page_size;
-                }
-                if (page < 0 || page >= a.c.num_pages)
-                    return -1;
-                return (page * a.Hkv + walk.h) * a.c.page_size + r;
-            };
-            bool boxes = !tree && !a.idx && a.box_rows && base + kTile <= w.ctx;
-            int row[4] = {-1, -1, -1, -1};    // boxes: this lane's box; else tokens 32u + lane
-            if (boxes) {
-                const bool mine = lane * a.box_rows < kTile;
-                if (mine)
-                    row[0] = row_of(base + lane * a.box_rows);
-                boxes = __all_sync(kFull, !mine || row[0] >= 0);
+        if (walk.left > 0) {
+            find_positions();
+            find_pages();
+            find_rows();
+        }
+        while (walk.left > 0) {
+            const uint32_t tile = tile_no;
+            const bool box = boxes;
+            int r[4];
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                r[u] = row[u];
+                w[u] = word[u];
             }
-            uint32_t word[4] = {kFull, kFull, kFull, kFull};
-            if (!boxes) {
-                int pos[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int j = u * 32 + lane;
-                    if (tree)
-                        pos[u] = j < w.nt ? w.ctx + j : -1;
-                    else if (a.idx)
-                        pos[u] = base + j < a.top_k
-                                     ? __ldg(a.idx + ((size_t)walk.b * a.Hkv + walk.h) * a.top_k + base + j)
-                                     : -1;
-                    else
-                        pos[u] = base + j < w.ctx ? base + j : -1;
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (!tree && pos[u] != -1 && (pos[u] < 0 || pos[u] >= w.ctx)) {
-                        flags |= kFlagIndexOutOfRange;
-                        pos[u] = -1;
-                    }
-                    row[u] = pos[u] < 0 ? -1 : row_of(pos[u]);
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (pos[u] >= 0 && row[u] < 0)
-                        flags |= kFlagPageOutOfRange;
-                    word[u] = __ballot_sync(kFull, row[u] >= 0);
-                }
-            }
+            const bool new_q = i == 0 && seg > 0;
+            const int qb = walk.b, qh = walk.h, qrow = walk.m * MT * kTile, qrows = walk.rows();
+            const uint32_t qseg = seg;
+            step(C::kLoaders);
+#pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
-                const uint32_t e = 2 * tile_no + kv, slot = e % C::kSlots, use = e / C::kSlots;
+                if (walk.left > 0) {
+                    if (kv == 0)
+                        find_positions();
+                    else
+                        find_pages();
+                }
+                const uint32_t e = 2 * tile + kv, slot = e % C::kSlots, use = e / C::kSlots;
                 if (use > 0)
                     ok = __all_sync(kFull, bar_wait(&bar_empty[slot], (use - 1) & 1, gave_up));
                 if (!ok)
                     break;
                 if (kv == 0 && lane < 4)
-                    sm_valid[tile_no % kMaskRing][lane] = lane < 2 ? (lane == 0 ? word[0] : word[1])
-                                                                   : (lane == 2 ? word[2] : word[3]);
+                    sm_valid[tile % kMaskRing][lane] = lane < 2 ? (lane == 0 ? w[0] : w[1])
+                                                                : (lane == 2 ? w[2] : w[3]);
                 __syncwarp();
-                last_tile = tile_no;
+                last_tile = tile;
                 const uint32_t dst = sm_ring + slot * kTileBytes;
-                if (boxes) {
+                uint64_t *full = &bar_full[slot];
+                if (box) {
                     if (lane == 0)
-                        bar_expect(&bar_full[slot], kTileBytes);
+                        bar_expect(full, kTileBytes);
                     else
-                        bar_arrive(&bar_full[slot]);
+                        bar_arrive(full);
                     __syncwarp();
-                    if (row[0] >= 0) {
+                    if (r[0] >= 0) {
                         const TmaDesc *map = kv ? &a.box_v : &a.box_k;
                         const uint32_t d = dst + lane * a.box_rows * 128;
-                        tma_box(d, map, 0, row[0], &bar_full[slot]);
-                        tma_box(d + kHalfBytes, map, 64, row[0], &bar_full[slot]);
+                        tma_box(d, map, 0, r[0], full);
+                        tma_box(d + kHalfBytes, map, 64, r[0], full);
                     }
                 } else {
-                    const int c = lane & 15, hi = lane >> 4;
-                    const uint16_t *src = (kv ? a.c.v : a.c.k) + c * 8;
-                    const uint32_t d = dst + (c >> 3) * kHalfBytes;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-#pragma unroll 4
-                        for (int it = 0; it < 16; ++it) {
-                            const int x = it * 2 + hi;
-                            const int rr = __shfl_sync(kFull, row[u], x);
-                            copy16(d + (u * 32 + x) * 128 + (((c ^ x) & 7) << 4),
-                                   src + (size_t)max(rr, 0) * kHeadDim, rr >= 0);
-                        }
+                    copy_rows(dst, (kv ? a.c.v : a.c.k), r, w, lane);
                     // an arrival per thread once its copies have landed
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                                     smem_of(&bar_full[slot]))
-                                 : "memory");
+                    copies_arrive(full);
                 }
                 __syncwarp();
             }
+            if (ok && new_q) {
+                // its buffer was the last segment's, or with two the one before's
+                const int last = (int)qseg - (two_q ? 2 : 1);
+                if (last >= 0)
+                    ok = __all_sync(kFull, bar_wait(&bar_qfree[last & 1], (last >> 1) & 1, gave_up));
+                if (ok) {
+                    load_q(qb, qh, qrow, qrows, qseg, 0, 1);
+                    copies_arrive(&bar_q[qseg & 1]);
+                }
+            }
             if (!ok)
                 break;
+            if (walk.left > 0)
+                find_rows();
         }
         if (flags)
             atomicOr(a.status, flags);
@@ -600,7 +692,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         if (elect_one()) {
             uint32_t e = 0;              // ring entry of the segment's first K tile
             uint32_t steps[MT] = {};     // steps of earlier segments, per row tile
-            uint32_t segs[MT] = {};      // segments begun per row tile
+            uint32_t seg = 0;            // segments begun
             bool ok = true;
             auto wait_full = [&](uint32_t entry) {
                 ok = ok && bar_wait(&bar_full[entry % C::kSlots], (entry / C::kSlots) & 1, gave_up);
@@ -624,7 +716,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     for (int m = 0; m < MT; ++m) {
                         if (m >= nm)
                             break;
-                        const uint32_t q = operand(sm_q + m * kTileBytes, 16);
+                        const uint32_t q = operand(sm_q + m * kTileBytes + (two_q ? seg & 1 : 0) * 64 * 128, 16);
                         const int buf = (steps[m] + j) & 1;
                         if (j >= 2)     // P V of step j - 2 has read this buffer's P
                             wait_bar(&bar_o[m], steps[m] + j - 2);
@@ -637,12 +729,14 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     }
                     if (j % C::kSteps == C::kSteps - 1)
                         mma_commit(&bar_empty[entry % C::kSlots]);
+                    if (j == n - 1)
+                        mma_commit(&bar_qfree[seg & 1]);   // the segment's Q has been read
                 };
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    if (m < nm)
-                        wait_bar(&bar_q[m], segs[m]++);
-                if (!wait_full(e))
+                if (seg == 0)
+                    wait_bar(&bar_q0, 0);
+                else
+                    wait_bar(&bar_q[seg & 1], (seg - 1) >> 1);
+                if (!wait_full(e))     // (its proxy fence covers Q, too)
                     break;
                 issue_s(0);
                 for (int j = 0; j < n; ++j) {
@@ -678,6 +772,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 for (int m = 0; m < MT; ++m)
                     if (m < nm)
                         steps[m] += n;
+                ++seg;
                 e += 2 * (n / C::kSteps);
                 walk.next(n / C::kSteps);
             }
@@ -706,26 +801,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             const int row0 = walk.m * MT * kTile + m * kTile;   // first query row of the row tile
             const int total_rows = walk.w.nt * a.G;
             const size_t q0 = (size_t)b * a.T * a.Hq + h * a.G;
-            // Q row tile: chunk c of row x at x * 128 + ((c ^ x) & 7) * 16 of its half
-            {
-                const int x0 = (warp & 3) * 32;
-#pragma unroll 4
-                for (int it = 0; it < 16; ++it) {
-                    const int x = x0 + it * 2 + (lane >> 4), c = lane & 15;
-                    const int row = row0 + x;
-                    uint4 val = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < total_rows)
-                        val = *reinterpret_cast<const uint4 *>(
-                            a.q + (q0 + (size_t)(row / a.G) * a.Hq + row % a.G) * kHeadDim + c * 8);
-                    const uint32_t dst = sm_q + m * kTileBytes + (c >> 3) * kHalfBytes + x * 128 +
-                                         (((c ^ x) & 7) << 4);
-                    sts4(dst, val.x, val.y, val.z, val.w);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0)
-                    bar_arrive(&bar_q[m]);
-            }
             const int row = row0 + r;
             const int tok = row / a.G;                         // drafted token of this row
             const bool live = row < total_rows;
@@ -773,7 +848,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     const uint32_t v = sm_ring + entry % C::kSlots * kTileBytes + r * 128;
                     bool any = false;
                     if (r < walk.w.nt) {
-#pragma unroll
+#pragma unroll 2
                         for (int c = 0; c < 16; ++c) {
                             uint32_t x[4];
                             lds4(v + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4), x);
@@ -816,37 +891,46 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     }
                 }
                 if (warp_live) {
-                    constexpr int kWords = C::kStep / 32;
-                    uint32_t w[kWords], all = kFull;
-#pragma unroll
-                    for (int c = 0; c < kWords; ++c) {
-                        w[c] = sm_valid[(tile_no + i) % kMaskRing][part * kWords + c];
-                        if (tree)
-                            w[c] &= MT == 1 ? sees[c] : (part ? sees[(2 + c) & 3] : sees[c]);
-                        all &= w[c];
-                    }
-                    const bool masked = all != kFull;
+                    // The row's scores pass through 64 registers, in blocks of 64
+                    // tokens: every block once for the maximum, then the last block
+                    // from the registers and the others again for the exponentials.
+                    // Loops that stay rolled: with the step unrolled over 128
+                    // registers the roles' code no longer fitted the instruction
+                    // cache (100K: 261 us against 314).
+                    constexpr int kBlocks = C::kStep / 64;
                     const uint32_t at = tmem + C::col_s(m, buf) + lanes;
-                    float s[C::kStep];
-                    auto fetch = [&](int c) { tmem_ld32(at + 32 * c, reinterpret_cast<uint32_t *>(s) + 32 * c); };
-                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-                    __syncwarp();
-                    fetch(0);
-#pragma unroll
-                    for (int c = 0; c < kWords; ++c) {
-                        tmem_wait_ld();
-                        tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32 * c);
-                        if (c + 1 < kWords)
-                            fetch(c + 1);
-                        if (masked) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(w[c] >> k & 1u))
-                                    s[32 * c + k] = -CUDART_INF_F;
+                    const uint32_t *valid = sm_valid[(tile_no + i) % kMaskRing] + part * 2;
+                    float s[64];
+                    auto fetch = [&](int block) {
+                        __syncwarp();
+                        tmem_ld32(at + 64 * block, reinterpret_cast<uint32_t *>(s));
+                        tmem_ld32(at + 64 * block + 32, reinterpret_cast<uint32_t *>(s) + 32);
+                        uint32_t w0 = valid[2 * block], w1 = valid[2 * block + 1];
+                        if (tree) {
+                            const bool upper = part + block > 0;      // drafted tokens 64 .. 127
+                            w0 &= upper ? sees[2] : sees[0];
+                            w1 &= upper ? sees[3] : sees[1];
                         }
+                        tmem_wait_ld();
+                        tmem_loaded(reinterpret_cast<uint32_t *>(s));
+                        tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32);
+                        if ((w0 & w1) != kFull) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2)
-                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[32 * c + k], s[32 * c + k + 1]);
+                            for (int k = 0; k < 32; ++k) {
+                                if (!(w0 >> k & 1u))
+                                    s[k] = -CUDART_INF_F;
+                                if (!(w1 >> k & 1u))
+                                    s[32 + k] = -CUDART_INF_F;
+                            }
+                        }
+                    };
+                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll 1
+                    for (int block = 0; block < kBlocks; ++block) {
+                        fetch(block);
+#pragma unroll
+                        for (int k = 0; k < 64; k += 2)
+                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
                     }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                     if (mref == -CUDART_INF_F)
@@ -864,7 +948,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         mref = mn;
                         l *= f;
                         const uint32_t o = tmem + C::col_o(m) + lanes;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t x[32];
                             tmem_ld32(o + 32 * c, x);
@@ -879,18 +963,20 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     const float off = mref == -CUDART_INF_F ? 0.0f : -mref;
                     const float2 off2 = make_float2(off, off), sl22 = make_float2(sl2, sl2);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+                    for (int block = kBlocks - 1; block >= 0; --block) {
+                        if (block < kBlocks - 1)
+                            fetch(block);
+                        uint32_t p[32];
 #pragma unroll
-                    for (int c = 0; c < kWords; ++c) {
-                        const float *d = s + 32 * c;
-                        uint32_t p[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float2 x = __ffma2_rn(make_float2(d[2 * k], d[2 * k + 1]), sl22, off2);
+                        for (int k = 0; k < 32; ++k) {
+                            const float2 x = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), sl22, off2);
                             const float2 e = make_float2(ex2(x.x), ex2(x.y));
                             sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                             p[k] = pack_bf16(e.x, e.y);
                         }
-                        tmem_st16(at + C::kStep / 2 + 16 * c, p);   // over scores that have been read
+                        // over scores of this or a later block, which have been read
+                        tmem_st32(at + C::kStep / 2 + 32 * block, p);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
@@ -921,7 +1007,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     for (int w = 0; w < 4; ++w)
                         bad[w] = sm_badv[m][w] & sees[w];
                 const uint32_t o = tmem + C::col_o(m) + lanes;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t x[32];
                     tmem_ld32(o + 32 * c, x);
