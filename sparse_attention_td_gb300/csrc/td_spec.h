@@ -56,6 +56,7 @@ struct TreeArgs {
     float *part_o;              // [2 * ctas][part_rows][128]
     int B, T, W, Hq, Hkv, G, Nmax, top_k;
     int g_shift;                // log2(G)
+    int page_shift;             // log2(page_size), or -1
     int box_rows;               // 0: no boxes, every tile goes row by row
     int part_rows;
     float scale;                // softmax scale (natural-log units)

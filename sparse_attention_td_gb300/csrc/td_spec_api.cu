@@ -93,6 +93,12 @@ td_status run_tree(const td_shape *shape, const td_cache *cache, int32_t tree_si
     st = check_cache(*shape, cache, true);
     if (st)
         return st;
+    {   // the kernel counts its tiles of work in 31 bits
+        const int64_t rows = (int64_t)tree_size * (shape->num_q_heads / shape->num_kv_heads);
+        const int64_t tiles = (idx ? top_k : shape->max_seq_len) / 128 + 2;
+        if ((int64_t)shape->batch * shape->num_kv_heads * ((rows + 127) / 128) * tiles > (int64_t(1) << 30))
+            return TD_ERR_UNSUPPORTED_SHAPE;
+    }
     if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !i32(seq_lens))
         return TD_ERR_INVALID_ARG;
     if ((tree_lens && !aligned(tree_lens, 4)) || (tree_mask && !aligned(tree_mask, 4)))
@@ -111,6 +117,10 @@ td_status run_tree(const td_shape *shape, const td_cache *cache, int32_t tree_si
     a.status = (uint32_t *)ws;
     a.G = shape->num_q_heads / shape->num_kv_heads;
     a.g_shift = a.G == 1 ? 0 : a.G == 2 ? 1 : a.G == 4 ? 2 : 3;
+    a.page_shift = -1;
+    for (int s = 0; s < 31; ++s)
+        if (cache->page_size == 1 << s)
+            a.page_shift = s;
     a.part_rows = td::tree_part_rows(tree_size * a.G);
     const TreeWs w = tree_ws(*shape, tree_size);
     char *base = (char *)ws + (ws_bytes - (w.total - kAlign)) / kAlign * kAlign;

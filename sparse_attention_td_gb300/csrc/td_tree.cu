@@ -31,6 +31,7 @@ namespace {
 constexpr int kTile = 128;                       // tokens per tile, and query rows per row tile
 constexpr int kHalfBytes = kTile * 128;          // one 64-value half of a tile's rows
 constexpr int kTileBytes = 2 * kHalfBytes;       // 128 rows of 128 bf16 values
+constexpr int kRowRing = 4;                      // tiles whose row lists are alive
 constexpr int kMaskRing = 8;                     // tiles whose validity masks are alive (see producer)
 constexpr long long kTreeWaitCycles = 2000000000ll;  // a wait gives up after about 1 s
 
@@ -44,16 +45,11 @@ template <int MT> struct Cfg {
     static constexpr int kStep = MT == 1 ? 128 : 64;
     static constexpr int kSteps = kTile / kStep;      // per tile
     static constexpr int kSoftWarps = 4 * MT;
-    static constexpr int kLoaders = 3;
-    // A loader's waits see a slot's phases by their parity, so when it waits for
-    // the last use of a slot, the use before that one has to be over.  It is once
-    // the loader's own last wait is: that was for entry e - 2 * kLoaders + 1 - kSlots
-    // to be read, at or behind e - 2 * kSlots.
-    static_assert(2 * kLoaders - 1 <= kSlots, "a loader could be two uses of a slot ahead");
-    // softmax, loaders, the MMA issuer
-    static constexpr int kThreads = 32 * (kSoftWarps + kLoaders + 1);
-    static constexpr int kLoader = kSoftWarps, kIssuer = kSoftWarps + kLoaders;
-    static constexpr size_t kSmem = (size_t)(MT + kSlots) * kTileBytes + 1024;
+    // softmax, the loader, the MMA issuer, copy warps: 12 warps, 168 registers a thread
+    static constexpr int kLoader = kSoftWarps, kIssuer = kSoftWarps + 1, kCopier = kSoftWarps + 2;
+    static constexpr int kCopiers = 10 - kSoftWarps;
+    static constexpr int kThreads = 32 * (kCopier + kCopiers);
+    static constexpr size_t kSmem = (size_t)(MT + kSlots) * kTileBytes + 3072;
     __device__ static constexpr uint32_t col_s(int m, int buf) { return m * 2 * kStep + buf * kStep; }
     __device__ static constexpr uint32_t col_p(int m, int buf) { return col_s(m, buf) + kStep / 2; }
     __device__ static constexpr uint32_t col_o(int m) { return 256 + m * kTile; }
@@ -82,6 +78,11 @@ __device__ __forceinline__ bool elect_one()
 __device__ __forceinline__ void bar_arrive(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive_n(uint64_t *bar, unsigned n)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(bar)), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void bar_expect(uint64_t *bar, unsigned bytes)
@@ -145,28 +146,13 @@ __device__ __forceinline__ void copies_arrive(uint64_t *bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
 }
 
-// The rows of a tile by one warp, half a warp per 256-byte row: token 32u + x
-// is row r[u] of lane x; bit x of w[u] says whether it exists (else zeros).
-// Chunk c of row x goes to x * 128 + ((c ^ x) & 7) * 16 of its half.
-__device__ __forceinline__ void copy_rows(uint32_t dst, const uint16_t *src, const int (&r)[4],
-                                          const uint32_t (&w)[4], int lane)
+// Row `tok` of a tile from cache row `row` (below 0: zeros), by half a warp: chunk
+// c at tok * 128 + ((c ^ tok) & 7) * 16 of its half.
+__device__ __forceinline__ void copy_row(uint32_t dst, int tok, const uint16_t *src, int row, int lane)
 {
-    const int c = lane & 15, hi = lane >> 4;
-    const uint16_t *s = src + c * 8;
-    uint32_t at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        at[i] = dst + (c >> 3) * kHalfBytes + (2 * i + hi) * 128 + (((c ^ (2 * i + hi)) & 7) << 4);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const uint32_t bits = w[u] >> hi;
-#pragma unroll 4
-        for (int it = 0; it < 16; ++it) {
-            const int row = __shfl_sync(kFull, r[u], 2 * it + hi);
-            copy16(at[it & 3] + (u * 32 + (it & ~3) * 2) * 128, s + (size_t)row * kHeadDim,
-                   bits >> (2 * it) & 1u);
-        }
-    }
+    const int c = lane & 15;
+    copy16(dst + (c >> 3) * kHalfBytes + tok * 128 + (((c ^ tok) & 7) << 4),
+           src + (size_t)max(row, 0) * kHeadDim + c * 8, row >= 0);
 }
 
 // Shared-memory operand of tcgen05.mma, 128-byte swizzle.  K-major (rows of
@@ -300,16 +286,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-// x / y of numbers >= 0, y > 0; short where both are short.
-__device__ __forceinline__ long long quotient(long long x, long long y)
-{
-    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
-}
-
-// ---- work: units (request, KV head, block of query rows), each a run of
-// tiles: the context's (or the index set's), then one tile of drafted tokens.
+// ---- work: units (request, KV head, block of query rows), each a run of tiles
+// of 128 tokens: the context's (or the index set's), then the drafted tokens,
+// which share the last context tile where both fit.
 struct Work {
     int ctx, nt, tiles, blocks;   // of the current request; tiles 0: no drafted token, no work
+    int entries;                  // context tokens, or index entries
+    int off;                      // the drafted tokens' first row in the last tile
+
+    // Tokens of tile t; rows behind them are not read.
+    __device__ int tokens(int t) const { return t == tiles - 1 ? off + nt : min(kTile, entries - t * kTile); }
 };
 
 template <int MT>
@@ -319,8 +305,10 @@ __device__ __forceinline__ Work work_of(const TreeArgs &a, int b, uint32_t &bad)
     Work w;
     w.nt = len.nt;
     w.ctx = len.n - len.nt;
-    const int entries = a.idx ? a.top_k : w.ctx;
-    w.tiles = w.nt ? (int)(((long long)entries + kTile - 1) / kTile) + 1 : 0;
+    w.entries = a.idx ? a.top_k : w.ctx;
+    const int rest = w.entries & (kTile - 1);
+    w.off = rest + w.nt <= kTile ? rest : 0;
+    w.tiles = w.nt ? (w.entries >> 7) + (w.off == 0 && rest > 0 ? 1 : 0) + 1 : 0;
     w.blocks = (w.nt * a.G + MT * kTile - 1) / (MT * kTile);
     return w;
 }
@@ -356,336 +344,409 @@ template <int MT> struct Walk {
     __device__ int rows() const { return min(w.nt * args->G - m * MT * kTile, MT * kTile); }
 };
 
+// Shared memory behind the Q tiles and the ring.
+template <int MT> struct Extra {
+    using C = Cfg<MT>;
+    uint64_t full[C::kSlots], empty[C::kSlots];   // ring: filled, read
+    uint64_t q[2], q_free[2];                     // Q of a segment: there, read (by segment parity)
+    uint64_t s[MT][2], p[MT][2], o[MT];           // S there, P there, P V done
+    uint64_t go[kRowRing][2], rows_read[kRowRing];  // a tile's K / V rows may be copied; row list read
+    uint64_t scan, drain;
+    int rows[kRowRing][kTile];                    // cache rows of a tile's tokens, -1: none
+    uint32_t valid[kMaskRing][4];                 // tokens of a tile that exist
+    uint32_t badv[MT][4];                         // drafted tokens with non-finite V values
+    int sums[C::kThreads / 32];
+    Walk<MT> start;
+    uint32_t tmem;
+    int gave_up;
+};
+
 // One CTA per SM; each takes an equal, contiguous range of the batch's tiles
 // (a range may cover several units and end inside one: those units' partial
 // results are joined by tree_join_kernel).  Roles: 4 * MT softmax warps (one
-// query row per thread), a warp that fills the ring, a warp that issues MMAs.
+// query row per thread), the loader, the copy warps, the MMA issuer.
 template <int MT>
 __global__ void __launch_bounds__(Cfg<MT>::kThreads, 1)
 tree_attention_kernel(const __grid_constant__ TreeArgs a)
 {
     using C = Cfg<MT>;
-    extern __shared__ unsigned char sm_raw[];
-    __shared__ __align__(8) uint64_t bar_full[C::kSlots], bar_empty[C::kSlots];
-    __shared__ __align__(8) uint64_t bar_q[2], bar_q0, bar_qfree[2], bar_s[MT][2], bar_p[MT][2], bar_o[MT], bar_scan, bar_drain;
-    __shared__ uint32_t sm_valid[kMaskRing][4];   // tokens of a tile that exist
-    __shared__ uint32_t sm_badv[MT][4];           // drafted tokens with non-finite V values
-    __shared__ long long sm_scan[C::kThreads / 32];
-    __shared__ Walk<MT> sm_start;
-    __shared__ uint32_t sm_tmem;
-    __shared__ int sm_gave_up;
+    extern __shared__ __align__(1024) unsigned char sm_raw[];
+    Extra<MT> &x = *reinterpret_cast<Extra<MT> *>(sm_raw + (MT + C::kSlots) * kTileBytes);
+    static_assert((MT + C::kSlots) * kTileBytes + sizeof(Extra<MT>) <= C::kSmem, "shared memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t sm_q = (smem_of(sm_raw) + 1023) & ~1023u;
+    const uint32_t sm_q = smem_of(sm_raw);        // 1024-byte aligned: nothing static lies before it
     const uint32_t sm_ring = sm_q + MT * kTileBytes;
-    volatile int *gave_up = &sm_gave_up;
+    volatile int *gave_up = &x.gave_up;
+    if (sm_q & 1023) {            // (cannot be: the swizzled tiles need it)
+        if (tid == 0)
+            atomicOr(a.status, kFlagWaitTimeout);
+        return;
+    }
 
-    // ---- the CTA's range: requests in equal runs per thread, prefix sums.  The
-    // barriers, the tensor memory and the tensor maps are made ready meanwhile.
+    // ---- the CTA's range: requests in equal runs per thread, prefix sums.  (The
+    // host has made sure that the number of tiles fits 31 bits.)
     {
         const int run = (a.B + C::kThreads - 1) / C::kThreads;
         const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
         uint32_t bad = 0;
-        long long mine = 0;
+        int mine = 0;
         Work w{};
         for (int b = b0; b < b1; ++b) {
             w = work_of<MT>(a, b, bad);
-            mine += (long long)w.tiles * w.blocks * a.Hkv;
-        }
-        if (tid == 0) {
-            sm_gave_up = 0;
-            sm_start.left = 0;
-            for (int i = 0; i < C::kSlots; ++i) {
-                bar_init(&bar_full[i], 32);
-                bar_init(&bar_empty[i], 1);
-            }
-            for (int i = 0; i < MT; ++i) {
-                for (int k = 0; k < 2; ++k) {
-                    bar_init(&bar_s[i][k], 1);
-                    bar_init(&bar_p[i][k], 4);
-                }
-                bar_init(&bar_o[i], 1);
-            }
-            bar_init(&bar_q[0], 32);
-            bar_init(&bar_q[1], 32);
-            bar_init(&bar_q0, 32 * C::kLoaders);
-            bar_init(&bar_qfree[0], 1);
-            bar_init(&bar_qfree[1], 1);
-            bar_init(&bar_scan, 4);
-            bar_init(&bar_drain, 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            mine += w.tiles * w.blocks * a.Hkv;
         }
         if (tid == 32 * C::kLoader) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_k) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_v) : "memory");
         }
-        if (warp == C::kIssuer) {
-            __syncwarp();
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                             smem_of(&sm_tmem)),
-                         "r"(kTmemCols)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (tid == 32 * C::kIssuer) {
+            x.gave_up = 0;
+            x.start.left = 0;
+            for (int i = 0; i < C::kSlots; ++i) {
+                bar_init(&x.full[i], 32 * C::kCopiers);
+                bar_init(&x.empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                bar_init(&x.q[i], 32 * C::kCopiers);
+                bar_init(&x.q_free[i], 1);
+            }
+            for (int i = 0; i < MT; ++i) {
+                for (int k = 0; k < 2; ++k) {
+                    bar_init(&x.s[i][k], 1);
+                    bar_init(&x.p[i][k], 4);
+                }
+                bar_init(&x.o[i], 1);
+            }
+            for (int i = 0; i < kRowRing; ++i) {
+                bar_init(&x.go[i][0], 1);
+                bar_init(&x.go[i][1], 1);
+                bar_init(&x.rows_read[i], C::kCopiers);
+            }
+            bar_init(&x.scan, 4);
+            bar_init(&x.drain, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         if (bad && blockIdx.x == 0)
             atomicOr(a.status, bad);
-        long long inc = mine;
+        int inc = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(kFull, inc, d);
+            const int y = __shfl_up_sync(kFull, inc, d);
             if (lane >= d)
                 inc += y;
         }
         if (lane == 31)
-            sm_scan[warp] = inc;
+            x.sums[warp] = inc;
         __syncthreads();
-        long long total = 0, at = inc - mine;
+        int total = 0, at = inc - mine;
 #pragma unroll
         for (int i = 0; i < C::kThreads / 32; ++i) {
+            const int y = x.sums[i];
             if (i < warp)
-                at += sm_scan[i];
-            total += sm_scan[i];
+                at += y;
+            total += y;
         }
-        const long long per = quotient(total + gridDim.x - 1, gridDim.x);
-        const long long start = blockIdx.x * per;
-        if (start < total && at <= start && start < at + mine) {
+        const int per = (uint32_t)(total + gridDim.x - 1) / gridDim.x;
+        const int start = blockIdx.x * per;
+        if (start < total && at <= start && start - at < mine) {
             int b = b0;
             if (run > 1) {
-                for (long long p = at; b < b1; ++b, at = p) {
+                for (int p = at; b < b1; ++b, at = p) {
                     w = work_of<MT>(a, b, bad);
-                    p += (long long)w.tiles * w.blocks * a.Hkv;
+                    p += w.tiles * w.blocks * a.Hkv;
                     if (start < p)
                         break;
                 }
             }
-            const long long off = start - at;
-            const long long unit = quotient(off, w.tiles);
-            const int first = (int)(off - unit * w.tiles);
+            const int unit = (uint32_t)(start - at) / (uint32_t)w.tiles;
             Walk<MT> s;
             s.args = &a;
-            s.left = (int)min(per, total - start);
+            s.left = min(per, total - start);
             s.b = b;
-            s.h = w.blocks == 1 ? (int)unit : (int)unit / w.blocks;
-            s.m = (int)unit - s.h * w.blocks;
-            s.t = first;
+            s.h = w.blocks == 1 ? unit : unit / w.blocks;
+            s.m = unit - s.h * w.blocks;
+            s.t = start - at - unit * w.tiles;
             s.first = true;
             s.w = w;
-            sm_start = s;
+            x.start = s;
         }
-        tmem_before();
         __syncthreads();
-        tmem_after();
         pdl_launch_dependents();
         if (tid == C::kThreads - 1) {
             // The unit that this cut goes through, if it is the unit's first cut.
             JoinPlan j{};
-            const int first = sm_start.t;
-            if (sm_start.left > 0 && first > 0 && first <= per) {
-                j.rows = sm_start.rows();
-                j.b = sm_start.b;
-                j.h = sm_start.h;
-                j.row0 = sm_start.m * MT * kTile;
+            const int first = x.start.t;
+            if (x.start.left > 0 && first > 0 && first <= per) {
+                j.rows = x.start.rows();
+                j.b = x.start.b;
+                j.h = x.start.h;
+                j.row0 = x.start.m * MT * kTile;
                 // the last range that meets the unit
-                j.last = (int)quotient(start - first + sm_start.w.tiles - 1, per);
+                j.last = (uint32_t)(start - first + x.start.w.tiles - 1) / (uint32_t)per;
                 j.late = first < per;
             }
             a.plan[blockIdx.x] = j;
         }
         __syncwarp();
     }
-    const uint32_t tmem = sm_tmem;
-    Walk<MT> walk = sm_start;
+    Walk<MT> walk = x.start;
     // Up to 64 query rows per unit: Q has two buffers of 64 rows, and the next
     // segment's comes in during this one.  (The MMA reads 128 rows from either;
     // the rows that are not Q's end in S and O rows that nobody reads.)
     const bool two_q = MT == 1 && a.part_rows <= 64;
-    int last_tile = -1;           // loaders: the last tile that this warp began to load
-
-    if (warp >= C::kLoader && warp < C::kLoader + C::kLoaders) {
-        // ---- loaders: K then V tile of every kLoaders-th tile, into the ring.  A
-        // tile whose tokens all exist comes as boxes of whole rows (of a page).
-        // Any other (ragged end, index set, drafted tokens, a bad page) row by row
-        // with cp.async, half a warp per 256-byte row: a token that does not exist
-        // is filled with zeros (no stale V value meets its zero probability), and
-        // the validity mask keeps its score out.  Row gathers by TMA instead took
-        // 60 ns per four half rows, 7.7 us a tile.  With a warp per tile, the
-        // lookups (index entry, then page number) of one tile overlap the copies
-        // of the others.  The mask ring: a loader is at most kSlots / 2 tiles ahead
-        // of the last S = Q K^T, itself at most 2 ahead of the softmax.
-        uint32_t tile_no = 0, flags = 0, seg = 0;
-        int i = 0, n = walk.count();
-        auto step = [&](int tiles) {
-            tile_no += tiles;
-            i += tiles;
-            while (i >= n && walk.left > 0) {
-                i -= n;
-                walk.next(n);
-                n = walk.count();
-                ++seg;
-            }
-        };
-        // Q rows of a segment, by the loader of its first tile (the first segment's:
-        // by all loaders, before anything else).  Rows that are not Q's are left
-        // as they are: they end in S and O rows that nobody reads.
-        auto load_q = [&](int b, int h, int row0, int rows, uint32_t s, int from, int stride) {
-            const int c = lane & 15, hi = lane >> 4;
-            const uint16_t *src = a.q + ((size_t)b * a.T * a.Hq + h * a.G) * kHeadDim + c * 8;
-            const uint32_t dst = sm_q + (two_q ? s & 1 : 0) * 64 * 128 + (c >> 3) * kHalfBytes;
-#pragma unroll 4
-            for (int x = 2 * from + hi; x < rows; x += 2 * stride) {
-                const int row = row0 + x, tk = row >> a.g_shift, g = row & (a.G - 1);
-                copy16(dst + (x >> 7) * kTileBytes + (x & 127) * 128 + (((c ^ x) & 7) << 4),
-                       src + ((size_t)tk * a.Hq + g) * kHeadDim, true);
-            }
-        };
-        if (walk.left > 0) {
-            load_q(walk.b, walk.h, walk.m * MT * kTile, walk.rows(), 0, warp - C::kLoader, C::kLoaders);
-            copies_arrive(&bar_q0);
+    uint32_t loaded = 0;          // loader: ring entries begun
+    uint32_t tmem = 0;
+    if (warp < C::kSoftWarps || warp == C::kIssuer) {
+        // tensor memory for the roles that use it, while the others begin
+        if (warp == C::kIssuer) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_of(&x.tmem)),
+                         "r"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
-        // A tile's rows are found in three steps, each before one of the copies of
-        // the tile before (memory is slow to answer while every SM's ring fills):
-        // positions, pages, rows.
-        bool boxes = false;
-        int pos[4], page[4], row[4];      // boxes: [0] is this lane's box; else tokens 32u + lane
-        uint32_t word[4];
-        auto page_of = [&](int p) {
-            return a.c.table ? __ldg(a.c.table + (size_t)walk.b * a.c.max_blocks + p / a.c.page_size)
-                             : walk.b;
+        tmem_before();
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * (C::kSoftWarps + 1)) : "memory");
+        tmem_after();
+        tmem = x.tmem;
+    }
+
+    // A tile that comes as boxes of whole rows (of a page): all of its tokens exist.
+    auto is_box = [&](const Work &w, int t) {
+        return t < w.tiles - 1 && !a.idx && a.box_rows && (t + 1) * kTile <= w.ctx;
+    };
+
+    if (warp == C::kLoader) {
+        // ---- loader: waits for the ring's slots, in order, and fills them: box tiles
+        // by TMA itself; of any other tile (ragged end, index set, drafted tokens) it
+        // finds the rows and lets the copy warps go.  (Row gathers by TMA took 60 ns
+        // per four half rows, 7.7 us a tile.)  Memory is slow to answer while every
+        // SM's ring fills, so positions are asked for two tiles ahead and page numbers
+        // one.  The mask ring: the loader is at most kSlots / 2 tiles ahead of the last
+        // S = Q K^T, itself at most 2 ahead of the softmax.
+        struct Cursor {
+            Walk<MT> walk;
+            int i, n;             // tile of the segment, tiles of the segment
+            __device__ void step()
+            {
+                if (++i == n) {
+                    walk.next(n);
+                    i = 0;
+                    n = walk.count();
+                }
+            }
+            __device__ int tile() const { return walk.t + i; }
         };
-        auto find_positions = [&]() {
-            const int t = walk.t + i, base = t * kTile;
-            const bool tree = t == walk.w.tiles - 1;
-            boxes = !tree && !a.idx && a.box_rows && base + kTile <= walk.w.ctx;
+        struct Found {
+            int pos[4], page[4];  // boxes: [0] is this lane's box; else tokens 32u + lane
+        };
+        uint32_t flags = 0;
+        auto page_of = [&](int b, int p) {
+            const int block = a.page_shift >= 0 ? p >> a.page_shift : p / a.c.page_size;
+            return __ldg(a.c.table + (size_t)b * a.c.max_blocks + block);
+        };
+        auto find_positions = [&](const Cursor &c, Found &f) {
+            const Work &w = c.walk.w;
+            const int t = c.tile(), base = t * kTile;
+            if (is_box(w, t)) {
+                f.pos[0] = lane * a.box_rows < kTile ? base + lane * a.box_rows : -1;
+                f.pos[1] = f.pos[2] = f.pos[3] = -1;
+                return;
+            }
+            const bool last = t == w.tiles - 1;
+            const int listed = last ? w.off : min(kTile, w.entries - base);   // context entries
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int j = u * 32 + lane;
-                if (boxes)
-                    pos[u] = u == 0 && lane * a.box_rows < kTile ? base + lane * a.box_rows : -1;
-                else if (tree)
-                    pos[u] = j < walk.w.nt ? walk.w.ctx + j : -1;
-                else if (a.idx)
-                    pos[u] = base + j < a.top_k
-                                 ? __ldg(a.idx + ((size_t)walk.b * a.Hkv + walk.h) * a.top_k + base + j)
-                                 : -1;
+                if (j < listed)
+                    f.pos[u] = a.idx ? __ldg(a.idx + ((size_t)c.walk.b * a.Hkv + c.walk.h) * a.top_k + base + j)
+                                     : base + j;
                 else
-                    pos[u] = base + j < walk.w.ctx ? base + j : -1;
+                    f.pos[u] = last && j - w.off < w.nt ? w.ctx + j - w.off : -1;
             }
         };
-        auto find_pages = [&]() {
-            const bool listed = a.idx && walk.t + i != walk.w.tiles - 1;
+        auto find_pages = [&](const Cursor &c, Found &f) {
+            const Work &w = c.walk.w;
+            const int t = c.tile();
+            const int listed = !a.idx ? 0 : t == w.tiles - 1 ? w.off : kTile;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (listed && pos[u] != -1 && (pos[u] < 0 || pos[u] >= walk.w.ctx)) {
+                if (u * 32 + lane < listed && f.pos[u] != -1 && (f.pos[u] < 0 || f.pos[u] >= w.ctx)) {
                     flags |= kFlagIndexOutOfRange;
-                    pos[u] = -1;
+                    f.pos[u] = -1;
                 }
-                page[u] = pos[u] < 0 ? 0 : page_of(pos[u]);
+                f.page[u] = f.pos[u] < 0 ? -1 : a.c.table ? page_of(c.walk.b, f.pos[u]) : c.walk.b;
             }
         };
-        auto find_rows = [&]() {
-            auto row_of = [&](int u) {
-                if (pos[u] < 0 || page[u] < 0 || page[u] >= a.c.num_pages)
-                    return -1;
-                return (page[u] * a.Hkv + walk.h) * a.c.page_size +
-                       (a.c.table ? pos[u] % a.c.page_size : pos[u]);
-            };
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                row[u] = row_of(u);
-            if (boxes && __any_sync(kFull, pos[0] >= 0 && row[0] < 0)) {
-                boxes = false;            // a bad page: token by token
+        auto row_of = [&](const Cursor &c, int pos, int page) {
+            if (pos < 0 || page < 0 || page >= a.c.num_pages)
+                return -1;
+            const int in = !a.c.table          ? pos
+                           : a.page_shift >= 0 ? pos & (a.c.page_size - 1)
+                                               : pos % a.c.page_size;
+            return (page * a.Hkv + c.walk.h) * a.c.page_size + in;
+        };
+        Cursor c0{walk, 0, walk.count()};
+        Found f0{}, f1{}, f2{};
+        bool ok = true;
+        if (walk.left > 0) {
+            find_positions(c0, f0);
+            find_pages(c0, f0);
+        }
+        Cursor c1 = c0;
+        if (walk.left > 0)
+            c1.step();
+        if (c1.walk.left > 0)
+            find_positions(c1, f1);
+        Cursor c2 = c1;
+        uint32_t tile_no = 0, copied = 0;         // tiles, tiles for the copy warps
+        for (; c0.walk.left > 0; ++tile_no) {
+            if (c1.walk.left > 0) {
+                find_pages(c1, f1);
+                c2.step();
+                if (c2.walk.left > 0)
+                    find_positions(c2, f2);
+            }
+            bool box = is_box(c0.walk.w, c0.tile());
+            int row[4];
+            uint32_t word[4] = {kFull, kFull, kFull, kFull};
+            bool alone = false;                   // a box tile with a bad page: row by row, here
+            row[0] = row_of(c0, f0.pos[0], f0.page[0]);
+            if (box && __any_sync(kFull, f0.pos[0] >= 0 && row[0] < 0)) {
+                box = false;
+                alone = true;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    pos[u] = (walk.t + i) * kTile + u * 32 + lane;
-                    page[u] = page_of(pos[u]);
-                    row[u] = row_of(u);
+                    f0.pos[u] = c0.tile() * kTile + u * 32 + lane;
+                    f0.page[u] = a.c.table ? page_of(c0.walk.b, f0.pos[u]) : c0.walk.b;
+                }
+                row[0] = row_of(c0, f0.pos[0], f0.page[0]);
+            }
+            const uint32_t ring = copied % kRowRing;
+            if (!box) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    row[u] = row_of(c0, f0.pos[u], f0.page[u]);
+                    if (f0.pos[u] >= 0 && row[u] < 0)
+                        flags |= kFlagPageOutOfRange;
+                    word[u] = __ballot_sync(kFull, row[u] >= 0);
+                }
+                if (!alone) {
+                    if (copied >= kRowRing)       // the list of four copied tiles before has been read
+                        ok = __all_sync(kFull, bar_wait(&x.rows_read[ring], (copied / kRowRing - 1) & 1, gave_up));
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        x.rows[ring][u * 32 + lane] = row[u];
                 }
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (pos[u] >= 0 && row[u] < 0)
-                    flags |= kFlagPageOutOfRange;
-                word[u] = boxes ? kFull : __ballot_sync(kFull, row[u] >= 0);
-                if (!boxes)
-                    row[u] = max(row[u], 0);
-            }
-        };
-        bool ok = true;
-        step(warp - C::kLoader);
-        if (walk.left > 0) {
-            find_positions();
-            find_pages();
-            find_rows();
-        }
-        while (walk.left > 0) {
-            const uint32_t tile = tile_no;
-            const bool box = boxes;
-            int r[4];
-            uint32_t w[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                r[u] = row[u];
-                w[u] = word[u];
-            }
-            const bool new_q = i == 0 && seg > 0;
-            const int qb = walk.b, qh = walk.h, qrow = walk.m * MT * kTile, qrows = walk.rows();
-            const uint32_t qseg = seg;
-            step(C::kLoaders);
-#pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
-                if (walk.left > 0) {
-                    if (kv == 0)
-                        find_positions();
-                    else
-                        find_pages();
-                }
-                const uint32_t e = 2 * tile + kv, slot = e % C::kSlots, use = e / C::kSlots;
+                const uint32_t e = 2 * tile_no + kv, slot = e % C::kSlots, use = e / C::kSlots;
                 if (use > 0)
-                    ok = __all_sync(kFull, bar_wait(&bar_empty[slot], (use - 1) & 1, gave_up));
+                    ok = __all_sync(kFull, bar_wait(&x.empty[slot], (use - 1) & 1, gave_up));
                 if (!ok)
                     break;
                 if (kv == 0 && lane < 4)
-                    sm_valid[tile % kMaskRing][lane] = lane < 2 ? (lane == 0 ? w[0] : w[1])
-                                                                : (lane == 2 ? w[2] : w[3]);
+                    x.valid[tile_no % kMaskRing][lane] = lane < 2 ? (lane == 0 ? word[0] : word[1])
+                                                                  : (lane == 2 ? word[2] : word[3]);
                 __syncwarp();
-                last_tile = tile;
+                loaded = e + 1;
                 const uint32_t dst = sm_ring + slot * kTileBytes;
-                uint64_t *full = &bar_full[slot];
                 if (box) {
-                    if (lane == 0)
-                        bar_expect(full, kTileBytes);
-                    else
-                        bar_arrive(full);
+                    if (lane == 0) {
+                        bar_expect(&x.full[slot], kTileBytes);
+                        bar_arrive_n(&x.full[slot], 32 * C::kCopiers - 1);
+                    }
                     __syncwarp();
-                    if (r[0] >= 0) {
+                    if (row[0] >= 0) {
                         const TmaDesc *map = kv ? &a.box_v : &a.box_k;
                         const uint32_t d = dst + lane * a.box_rows * 128;
-                        tma_box(d, map, 0, r[0], full);
-                        tma_box(d + kHalfBytes, map, 64, r[0], full);
+                        tma_box(d, map, 0, row[0], &x.full[slot]);
+                        tma_box(d + kHalfBytes, map, 64, row[0], &x.full[slot]);
                     }
+                } else if (!alone) {
+                    if (lane == 0)
+                        bar_arrive(&x.go[ring][kv]);
                 } else {
-                    copy_rows(dst, (kv ? a.c.v : a.c.k), r, w, lane);
-                    // an arrival per thread once its copies have landed
-                    copies_arrive(full);
+                    for (int j = 0; j < kTile / 2; ++j) {
+                        const int tok = 2 * j + (lane >> 4);
+                        const int at = __shfl_sync(kFull, j < 16 ? row[0] : j < 32 ? row[1] : j < 48 ? row[2] : row[3],
+                                                   tok & 31);
+                        copy_row(dst, tok, kv ? a.c.v : a.c.k, at, lane);
+                    }
+                    copies_arrive(&x.full[slot]);
+                    if (lane == 0)
+                        bar_arrive_n(&x.full[slot], 32 * C::kCopiers - 32);
                 }
                 __syncwarp();
-            }
-            if (ok && new_q) {
-                // its buffer was the last segment's, or with two the one before's
-                const int last = (int)qseg - (two_q ? 2 : 1);
-                if (last >= 0)
-                    ok = __all_sync(kFull, bar_wait(&bar_qfree[last & 1], (last >> 1) & 1, gave_up));
-                if (ok) {
-                    load_q(qb, qh, qrow, qrows, qseg, 0, 1);
-                    copies_arrive(&bar_q[qseg & 1]);
-                }
             }
             if (!ok)
                 break;
-            if (walk.left > 0)
-                find_rows();
+            copied += box || alone ? 0 : 1;
+            c0 = c1;
+            f0 = f1;
+            c1 = c2;
+            f1 = f2;
         }
         if (flags)
             atomicOr(a.status, flags);
+    } else if (warp >= C::kCopier) {
+        // ---- copy warps: a segment's Q, then the rows of its tiles that are not
+        // boxes, with cp.async, half a warp per 256-byte row; a token that does not
+        // exist is filled with zeros (no stale V value meets its zero probability).
+        const int me = warp - C::kCopier;
+        uint32_t e = 0, seg = 0, copied = 0;
+        bool ok = true;
+        for (; ok && walk.left > 0; ++seg) {
+            const int n = walk.count();
+            // Q: its buffer was the last segment's, or with two the one before's.  Rows
+            // that are not Q's are left as they are.
+            const int last = (int)seg - (two_q ? 2 : 1);
+            if (last >= 0)
+                ok = __all_sync(kFull, bar_wait(&x.q_free[last & 1], (last >> 1) & 1, gave_up));
+            if (!ok)
+                break;
+            {
+                const int rows = walk.rows(), row0 = walk.m * MT * kTile;
+                const int c = lane & 15;
+                const uint16_t *src = a.q + ((size_t)walk.b * a.T * a.Hq + walk.h * a.G) * kHeadDim + c * 8;
+                const uint32_t dst = sm_q + (two_q ? seg & 1 : 0) * 64 * 128 + (c >> 3) * kHalfBytes;
+#pragma unroll 2
+                for (int r = 2 * me + (lane >> 4); r < rows; r += 2 * C::kCopiers) {
+                    const int row = row0 + r, tk = row >> a.g_shift, g = row & (a.G - 1);
+                    copy16(dst + (r >> 7) * kTileBytes + (r & 127) * 128 + (((c ^ r) & 7) << 4),
+                           src + ((size_t)tk * a.Hq + g) * kHeadDim, true);
+                }
+                copies_arrive(&x.q[seg & 1]);
+            }
+            for (int i = 0; ok && i < n; ++i, e += 2) {
+                const int t = walk.t + i;
+                if (is_box(walk.w, t))
+                    continue;
+                const uint32_t ring = copied % kRowRing, phase = copied / kRowRing & 1;
+                const int tokens = walk.w.tokens(t);
+                for (int kv = 0; kv < 2; ++kv) {
+                    ok = __all_sync(kFull, bar_wait(&x.go[ring][kv], phase, gave_up));
+                    if (!ok)
+                        break;
+                    const uint32_t slot = (e + kv) % C::kSlots;
+                    // scores of rows behind the tokens are masked; P V takes tokens by 16
+                    const int end = kv ? (tokens + 15) & ~15 : tokens;
+                    const uint16_t *src = kv ? a.c.v : a.c.k;
+                    const uint32_t dst = sm_ring + slot * kTileBytes;
+#pragma unroll 4
+                    for (int tok = 2 * me + (lane >> 4); tok < end; tok += 2 * C::kCopiers)
+                        copy_row(dst, tok, src, x.rows[ring][tok], lane);
+                    copies_arrive(&x.full[slot]);
+                }
+                __syncwarp();
+                if (ok && lane == 0)
+                    bar_arrive(&x.rows_read[ring]);
+                ++copied;
+            }
+            walk.next(n);
+        }
     } else if (warp == C::kIssuer) {
         // ---- MMA issue, by one thread: S of step j + 1 before P V of step j, so
         // the tensor cores work while the softmax does.
@@ -695,7 +756,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             uint32_t seg = 0;            // segments begun
             bool ok = true;
             auto wait_full = [&](uint32_t entry) {
-                ok = ok && bar_wait(&bar_full[entry % C::kSlots], (entry / C::kSlots) & 1, gave_up);
+                ok = ok && bar_wait(&x.full[entry % C::kSlots], (entry / C::kSlots) & 1, gave_up);
                 // rows copied by cp.async are read by the MMA through the async proxy
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 return ok;
@@ -719,23 +780,20 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         const uint32_t q = operand(sm_q + m * kTileBytes + (two_q ? seg & 1 : 0) * 64 * 128, 16);
                         const int buf = (steps[m] + j) & 1;
                         if (j >= 2)     // P V of step j - 2 has read this buffer's P
-                            wait_bar(&bar_o[m], steps[m] + j - 2);
+                            wait_bar(&x.o[m], steps[m] + j - 2);
 #pragma unroll
                         for (int s = 0; s < 8; ++s) {
                             const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
                             mma_ss<C::kStep>(tmem + C::col_s(m, buf), q + (o >> 4), k + (o >> 4), s > 0);
                         }
-                        mma_commit(&bar_s[m][buf]);
+                        mma_commit(&x.s[m][buf]);
                     }
                     if (j % C::kSteps == C::kSteps - 1)
-                        mma_commit(&bar_empty[entry % C::kSlots]);
+                        mma_commit(&x.empty[entry % C::kSlots]);
                     if (j == n - 1)
-                        mma_commit(&bar_qfree[seg & 1]);   // the segment's Q has been read
+                        mma_commit(&x.q_free[seg & 1]);   // the segment's Q has been read
                 };
-                if (seg == 0)
-                    wait_bar(&bar_q0, 0);
-                else
-                    wait_bar(&bar_q[seg & 1], (seg - 1) >> 1);
+                wait_bar(&x.q[seg & 1], seg >> 1);
                 if (!wait_full(e))     // (its proxy fence covers Q, too)
                     break;
                 issue_s(0);
@@ -750,23 +808,26 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         break;
                     const uint32_t v = operand(sm_ring + entry % C::kSlots * kTileBytes, kHalfBytes) +
                                        (j % C::kSteps * C::kStep * 128 >> 4);
+                    // tokens by 16, as far as the tile has any
+                    const int tokens = walk.w.tokens(walk.t + j / C::kSteps) - j % C::kSteps * C::kStep;
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         if (m >= nm)
                             break;
                         const uint32_t g = steps[m] + j;
-                        if (!wait_bar(&bar_p[m][g & 1], g >> 1))
+                        if (!wait_bar(&x.p[m][g & 1], g >> 1))
                             break;
 #pragma unroll
                         for (int s = 0; s < C::kStep / 16; ++s)
-                            mma_ts(tmem + C::col_o(m), tmem + C::col_p(m, g & 1) + s * 8,
-                                   v + (s * 16 * 128 >> 4), j > 0 || s > 0);
-                        mma_commit(&bar_o[m]);
+                            if (s * 16 < tokens)
+                                mma_ts(tmem + C::col_o(m), tmem + C::col_p(m, g & 1) + s * 8,
+                                       v + (s * 16 * 128 >> 4), j > 0 || s > 0);
+                        mma_commit(&x.o[m]);
                     }
                     if (!ok)
                         break;
                     if (j % C::kSteps == C::kSteps - 1)
-                        mma_commit(&bar_empty[entry % C::kSlots]);
+                        mma_commit(&x.empty[entry % C::kSlots]);
                 }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
@@ -778,7 +839,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             }
         }
         __syncwarp();
-    } else if (warp < C::kSoftWarps) {
+    } else {
         // ---- softmax: thread r of a row tile owns query row r
         const int m = MT == 1 ? 0 : warp >> 2;
         const int r = (warp & 3) * 32 + lane;                 // row of the row tile, TMEM lane
@@ -818,6 +879,18 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                   : tok >= 32 * w   ? 0xffffffffu >> (31 - (tok & 31))
                                                     : 0u;
                 }
+                // the last tile's bits: its context tokens, then the drafted ones
+                const int up = walk.w.off >> 5, by = walk.w.off & 31;
+#pragma unroll
+                for (int w = 3; w >= 0; --w) {
+                    const uint32_t hi = w >= up ? (up == 0 ? sees[w] : up == 1 ? sees[w > 0 ? w - 1 : 0]
+                                                   : up == 2 ? sees[w > 1 ? w - 2 : 0] : sees[0]) : 0u;
+                    const uint32_t lo = w >= up + 1 ? (up == 0 ? sees[w > 0 ? w - 1 : 0] : up == 1 ? sees[w > 1 ? w - 2 : 0]
+                                                       : sees[0]) : 0u;
+                    const int below = walk.w.off - 32 * w;
+                    sees[w] = __funnelshift_l(lo, hi, by) |
+                              (below >= 32 ? kFull : below > 0 ? (1u << below) - 1 : 0u);
+                }
             }
             for (int j = 0; j < n * C::kSteps; ++j, ++count) {
                 const int i = j / C::kSteps, part = j % C::kSteps;   // tile, step of the tile
@@ -828,10 +901,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 bool waited = j == 0;
                 auto o_done = [&]() {
                     if (!waited)
-                        ok = __all_sync(kFull, bar_wait(&bar_o[m], (count - 1) & 1, gave_up));
+                        ok = __all_sync(kFull, bar_wait(&x.o[m], (count - 1) & 1, gave_up));
                     waited = true;
                 };
-                ok = __all_sync(kFull, bar_wait(&bar_s[m][buf], (count >> 1) & 1, gave_up));
+                ok = __all_sync(kFull, bar_wait(&x.s[m][buf], (count >> 1) & 1, gave_up));
                 if (!ok)
                     break;
                 tmem_after();
@@ -841,30 +914,30 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     // leave the tile here and join the rows that do see it below.
                     // With two row tiles both look, then the first one clears.
                     const uint32_t entry = 2 * (tile_no + i) + 1;
-                    ok = __all_sync(kFull, bar_wait(&bar_full[entry % C::kSlots],
+                    ok = __all_sync(kFull, bar_wait(&x.full[entry % C::kSlots],
                                                     (entry / C::kSlots) & 1, gave_up));
                     if (!ok)
                         break;
                     const uint32_t v = sm_ring + entry % C::kSlots * kTileBytes + r * 128;
                     bool any = false;
-                    if (r < walk.w.nt) {
+                    if (r >= walk.w.off && r < walk.w.off + walk.w.nt) {
 #pragma unroll 2
                         for (int c = 0; c < 16; ++c) {
-                            uint32_t x[4];
-                            lds4(v + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4), x);
+                            uint32_t y4[4];
+                            lds4(v + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4), y4);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                any |= (x[k] & 0x7f80u) == 0x7f80u || (x[k] & 0x7f800000u) == 0x7f800000u;
+                                any |= (y4[k] & 0x7f80u) == 0x7f80u || (y4[k] & 0x7f800000u) == 0x7f800000u;
                         }
                     }
                     const uint32_t bits = __ballot_sync(kFull, any);
                     if (lane == 0)
-                        sm_badv[m][warp & 3] = bits;
+                        x.badv[m][warp & 3] = bits;
                     if constexpr (MT > 1) {
                         if (nm > 1 && m == 1 && lane == 0)
-                            bar_arrive(&bar_scan);
+                            bar_arrive(&x.scan);
                         if (nm > 1 && m == 0) {
-                            ok = __all_sync(kFull, bar_wait(&bar_scan, scans & 1, gave_up));
+                            ok = __all_sync(kFull, bar_wait(&x.scan, scans & 1, gave_up));
                             if (!ok)
                                 break;
                             ++scans;
@@ -873,17 +946,17 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     if (m == 0 && bits) {
                         if (any) {
                             for (int c = 0; c < 16; ++c) {
-                                uint32_t x[4];
+                                uint32_t y4[4];
                                 const uint32_t at = v + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4);
-                                lds4(at, x);
+                                lds4(at, y4);
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
-                                    if ((x[k] & 0x7f80u) == 0x7f80u)
-                                        x[k] &= 0xffff0000u;
-                                    if ((x[k] & 0x7f800000u) == 0x7f800000u)
-                                        x[k] &= 0xffffu;
+                                    if ((y4[k] & 0x7f80u) == 0x7f80u)
+                                        y4[k] &= 0xffff0000u;
+                                    if ((y4[k] & 0x7f800000u) == 0x7f800000u)
+                                        y4[k] &= 0xffffu;
                                 }
-                                sts4(at, x[0], x[1], x[2], x[3]);
+                                sts4(at, y4[0], y4[1], y4[2], y4[3]);
                             }
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -899,7 +972,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     // cache (100K: 261 us against 314).
                     constexpr int kBlocks = C::kStep / 64;
                     const uint32_t at = tmem + C::col_s(m, buf) + lanes;
-                    const uint32_t *valid = sm_valid[(tile_no + i) % kMaskRing] + part * 2;
+                    const uint32_t *valid = x.valid[(tile_no + i) % kMaskRing] + part * 2;
                     float s[64];
                     auto fetch = [&](int block) {
                         __syncwarp();
@@ -950,14 +1023,14 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         const uint32_t o = tmem + C::col_o(m) + lanes;
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            uint32_t x[32];
-                            tmem_ld32(o + 32 * c, x);
+                            uint32_t ov[32];
+                            tmem_ld32(o + 32 * c, ov);
                             tmem_wait_ld();
-                            tmem_loaded(x);
+                            tmem_loaded(ov);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-                            tmem_st32(o + 32 * c, x);
+                                ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+                            tmem_st32(o + 32 * c, ov);
                         }
                     }
                     const float off = mref == -CUDART_INF_F ? 0.0f : -mref;
@@ -970,8 +1043,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         uint32_t p[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
-                            const float2 x = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), sl22, off2);
-                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                            const float2 z = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), sl22, off2);
+                            const float2 e = make_float2(ex2(z.x), ex2(z.y));
                             sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                             p[k] = pack_bf16(e.x, e.y);
                         }
@@ -987,12 +1060,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 tmem_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(&bar_p[m][buf]);
+                    bar_arrive(&x.p[m][buf]);
             }
             if (!ok)
                 break;
             // ---- the segment's result
-            ok = __all_sync(kFull, bar_wait(&bar_o[m], (count - 1) & 1, gave_up));
+            ok = __all_sync(kFull, bar_wait(&x.o[m], (count - 1) & 1, gave_up));
             if (!ok)
                 break;
             tmem_after();
@@ -1005,19 +1078,19 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 if (has_tree)
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        bad[w] = sm_badv[m][w] & sees[w];
+                        bad[w] = x.badv[m][w] & sees[w];
                 const uint32_t o = tmem + C::col_o(m) + lanes;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    tmem_ld32(o + 32 * c, x);
+                    uint32_t ov[32];
+                    tmem_ld32(o + 32 * c, ov);
                     tmem_wait_ld();
-                    tmem_loaded(x);
+                    tmem_loaded(ov);
                     if (live && (bad[0] | bad[1] | bad[2] | bad[3])) {
-                        for (int j = 0; j < walk.w.nt; ++j) {
-                            if (!(bad[j >> 5] >> (j & 31) & 1u))
+                        for (int j = walk.w.off; j < walk.w.off + walk.w.nt; ++j) {
+                            if (!((j < 64 ? (j < 32 ? bad[0] : bad[1]) : (j < 96 ? bad[2] : bad[3])) >> (j & 31) & 1u))
                                 continue;
-                            const int p = walk.w.ctx + j;
+                            const int p = walk.w.ctx + j - walk.w.off;
                             int page = b, rr = p;
                             if (a.c.table) {
                                 page = a.c.table[(size_t)b * a.c.max_blocks + p / a.c.page_size];
@@ -1030,7 +1103,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 if ((v[k] & 0x7f80) == 0x7f80)
-                                    x[k] = __float_as_uint(__uint_as_float(x[k]) +
+                                    ov[k] = __float_as_uint(__uint_as_float(ov[k]) +
                                                            __uint_as_float((uint32_t)v[k] << 16));
                         }
                     }
@@ -1039,7 +1112,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         uint32_t y[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
-                            y[k] = pack_bf16(__uint_as_float(x[2 * k]) * inv, __uint_as_float(x[2 * k + 1]) * inv);
+                            y[k] = pack_bf16(__uint_as_float(ov[2 * k]) * inv, __uint_as_float(ov[2 * k + 1]) * inv);
                         const uint4 *v = reinterpret_cast<const uint4 *>(y);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -1048,7 +1121,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         float *dst = a.part_o + prow * kHeadDim + 32 * c;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            store32(dst + 8 * k, x + 8 * k);
+                            store32(dst + 8 * k, ov + 8 * k);
                     }
                     __syncwarp();
                 }
@@ -1065,28 +1138,23 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     }
     tmem_before();
     __syncthreads();
-    if (sm_gave_up) {
-        // A wait gave up: leave no copy and no MMA in flight.  A loader's last two
-        // tiles are the ones that can be; each wait has a limit of its own.
+    if (x.gave_up) {
+        // A wait gave up: leave no copy and no MMA in flight.  The ring's last
+        // entries are the ones that can be; each wait has a limit of its own.
         int own_limit = 0;
-        if (warp >= C::kLoader && warp < C::kIssuer) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            for (int k = 0; k < 4; ++k) {
-                const int tile = last_tile - (k >> 1) * C::kLoaders;
-                const uint32_t entry = 2 * tile + (k & 1);
-                if (tile >= 0) {
-                    own_limit = 0;
-                    bar_wait(&bar_full[entry % C::kSlots], (entry / C::kSlots) & 1, &own_limit,
-                             kTreeWaitCycles / 16);
-                }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (warp == C::kLoader) {
+            for (uint32_t e = loaded > C::kSlots ? loaded - C::kSlots : 0; e < loaded; ++e) {
+                own_limit = 0;
+                bar_wait(&x.full[e % C::kSlots], (e / C::kSlots) & 1, &own_limit, kTreeWaitCycles / 16);
             }
         } else if (warp == C::kIssuer && lane == 0) {
-            mma_commit(&bar_drain);
-            bar_wait(&bar_drain, 0, &own_limit, kTreeWaitCycles / 16);
+            mma_commit(&x.drain);
+            bar_wait(&x.drain, 0, &own_limit, kTreeWaitCycles / 16);
         }
         __syncthreads();
     }
-    if (tid == 0 && sm_gave_up)
+    if (tid == 0 && x.gave_up)
         atomicOr(a.status, kFlagWaitTimeout);
     if (warp == C::kIssuer) {
         tmem_after();
