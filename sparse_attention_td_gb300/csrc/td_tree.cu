@@ -31,7 +31,6 @@ namespace {
 constexpr int kTile = 128;                       // tokens per tile, and query rows per row tile
 constexpr int kHalfBytes = kTile * 128;          // one 64-value half of a tile's rows
 constexpr int kTileBytes = 2 * kHalfBytes;       // 128 rows of 128 bf16 values
-constexpr int kRowRing = 4;                      // tiles whose row lists are alive
 constexpr int kMaskRing = 8;                     // tiles whose validity masks are alive (see producer)
 constexpr long long kTreeWaitCycles = 2000000000ll;  // a wait gives up after about 1 s
 
@@ -45,10 +44,19 @@ template <int MT> struct Cfg {
     static constexpr int kStep = MT == 1 ? 128 : 64;
     static constexpr int kSteps = kTile / kStep;      // per tile
     static constexpr int kSoftWarps = 4 * MT;
-    // softmax, the loader, the MMA issuer, copy warps: 12 warps, 168 registers a thread
-    static constexpr int kLoader = kSoftWarps, kIssuer = kSoftWarps + 1, kCopier = kSoftWarps + 2;
-    static constexpr int kCopiers = 10 - kSoftWarps;
-    static constexpr int kThreads = 32 * (kCopier + kCopiers);
+    // softmax, the loader, the MMA issuer, row finders, copy warps: 12 or 16 warps
+    // Copy warps in the third and fourth sub-partition (warp % 4): their queue of
+    // copies slows the other warps there, and the first two have the first 64 rows.
+    static constexpr int kLoader = kSoftWarps, kIssuer = kSoftWarps + 1;
+    static constexpr int kFinder = kSoftWarps + 4, kFinders = 2, kCopiers = 4;
+    static constexpr int kRowRing = 4;                // tiles whose row lists are alive
+    static constexpr int kThreads = 32 * (kSoftWarps + 8);
+    // number of a copy warp, or -1
+    __device__ static int copier(int warp)
+    {
+        const int w = warp - kSoftWarps;
+        return w < 0 || (w & 2) == 0 ? -1 : (w & 1) + (w >> 2) * 2;
+    }
     static constexpr size_t kSmem = (size_t)(MT + kSlots) * kTileBytes + 3072;
     __device__ static constexpr uint32_t col_s(int m, int buf) { return m * 2 * kStep + buf * kStep; }
     __device__ static constexpr uint32_t col_p(int m, int buf) { return col_s(m, buf) + kStep / 2; }
@@ -144,6 +152,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there
 __device__ __forceinline__ void copies_arrive(uint64_t *bar)
 {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 // Row `tok` of a tile from cache row `row` (below 0: zeros), by half a warp: chunk
@@ -350,9 +363,11 @@ template <int MT> struct Extra {
     uint64_t full[C::kSlots], empty[C::kSlots];   // ring: filled, read
     uint64_t q[2], q_free[2];                     // Q of a segment: there, read (by segment parity)
     uint64_t s[MT][2], p[MT][2], o[MT];           // S there, P there, P V done
-    uint64_t go[kRowRing][2], rows_read[kRowRing];  // a tile's K / V rows may be copied; row list read
+    uint64_t rows_there[C::kRowRing], rows_read[C::kRowRing];   // a tile's row list: written, read
+    uint64_t go[C::kRowRing][2];                  // the tile's K / V rows may be copied
     uint64_t scan, drain;
-    int rows[kRowRing][kTile];                    // cache rows of a tile's tokens, -1: none
+    int rows[C::kRowRing][kTile];                 // cache rows of a tile's tokens, -1: none
+    uint32_t rows_valid[C::kRowRing][4];          // which tokens have one
     uint32_t valid[kMaskRing][4];                 // tokens of a tile that exist
     uint32_t badv[MT][4];                         // drafted tokens with non-finite V values
     int sums[C::kThreads / 32];
@@ -417,7 +432,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 }
                 bar_init(&x.o[i], 1);
             }
-            for (int i = 0; i < kRowRing; ++i) {
+            for (int i = 0; i < C::kRowRing; ++i) {
+                bar_init(&x.rows_there[i], 1);
                 bar_init(&x.go[i][0], 1);
                 bar_init(&x.go[i][1], 1);
                 bar_init(&x.rows_read[i], C::kCopiers);
@@ -511,194 +527,219 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         tmem = x.tmem;
     }
 
-    // A tile that comes as boxes of whole rows (of a page): all of its tokens exist.
-    auto is_box = [&](const Work &w, int t) {
-        return t < w.tiles - 1 && !a.idx && a.box_rows && (t + 1) * kTile <= w.ctx;
+    // The first tiles of a unit, whose tokens all exist, come as boxes of whole rows
+    // (of a page) by TMA; the others (ragged end, index set, drafted tokens) row by
+    // row by the copy warps.
+    auto boxes_of = [&](const Work &w) { return a.idx || !a.box_rows ? 0 : w.ctx >> 7; };
+    auto page_of = [&](int b, int p) {
+        if (!a.c.table)
+            return b;
+        const int block = a.page_shift >= 0 ? p >> a.page_shift : p / a.c.page_size;
+        return __ldg(a.c.table + (size_t)b * a.c.max_blocks + block);
+    };
+    auto row_of = [&](int h, int pos, int page) {       // -1: no such row
+        if (pos < 0 || page < 0 || page >= a.c.num_pages)
+            return -1;
+        const int in = !a.c.table          ? pos
+                       : a.page_shift >= 0 ? pos & (a.c.page_size - 1)
+                                           : pos % a.c.page_size;
+        return (page * a.Hkv + h) * a.c.page_size + in;
     };
 
     if (warp == C::kLoader) {
-        // ---- loader: waits for the ring's slots, in order, and fills them: box tiles
-        // by TMA itself; of any other tile (ragged end, index set, drafted tokens) it
-        // finds the rows and lets the copy warps go.  (Row gathers by TMA took 60 ns
-        // per four half rows, 7.7 us a tile.)  Memory is slow to answer while every
-        // SM's ring fills, so positions are asked for two tiles ahead and page numbers
-        // one.  The mask ring: the loader is at most kSlots / 2 tiles ahead of the last
-        // S = Q K^T, itself at most 2 ahead of the softmax.
-        struct Cursor {
-            Walk<MT> walk;
-            int i, n;             // tile of the segment, tiles of the segment
-            __device__ void step()
-            {
-                if (++i == n) {
-                    walk.next(n);
-                    i = 0;
-                    n = walk.count();
-                }
-            }
-            __device__ int tile() const { return walk.t + i; }
-        };
-        struct Found {
-            int pos[4], page[4];  // boxes: [0] is this lane's box; else tokens 32u + lane
-        };
-        uint32_t flags = 0;
-        auto page_of = [&](int b, int p) {
-            const int block = a.page_shift >= 0 ? p >> a.page_shift : p / a.c.page_size;
-            return __ldg(a.c.table + (size_t)b * a.c.max_blocks + block);
-        };
-        auto find_positions = [&](const Cursor &c, Found &f) {
-            const Work &w = c.walk.w;
-            const int t = c.tile(), base = t * kTile;
-            if (is_box(w, t)) {
-                f.pos[0] = lane * a.box_rows < kTile ? base + lane * a.box_rows : -1;
-                f.pos[1] = f.pos[2] = f.pos[3] = -1;
-                return;
-            }
-            const bool last = t == w.tiles - 1;
-            const int listed = last ? w.off : min(kTile, w.entries - base);   // context entries
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int j = u * 32 + lane;
-                if (j < listed)
-                    f.pos[u] = a.idx ? __ldg(a.idx + ((size_t)c.walk.b * a.Hkv + c.walk.h) * a.top_k + base + j)
-                                     : base + j;
-                else
-                    f.pos[u] = last && j - w.off < w.nt ? w.ctx + j - w.off : -1;
-            }
-        };
-        auto find_pages = [&](const Cursor &c, Found &f) {
-            const Work &w = c.walk.w;
-            const int t = c.tile();
-            const int listed = !a.idx ? 0 : t == w.tiles - 1 ? w.off : kTile;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (u * 32 + lane < listed && f.pos[u] != -1 && (f.pos[u] < 0 || f.pos[u] >= w.ctx)) {
-                    flags |= kFlagIndexOutOfRange;
-                    f.pos[u] = -1;
-                }
-                f.page[u] = f.pos[u] < 0 ? -1 : a.c.table ? page_of(c.walk.b, f.pos[u]) : c.walk.b;
-            }
-        };
-        auto row_of = [&](const Cursor &c, int pos, int page) {
-            if (pos < 0 || page < 0 || page >= a.c.num_pages)
-                return -1;
-            const int in = !a.c.table          ? pos
-                           : a.page_shift >= 0 ? pos & (a.c.page_size - 1)
-                                               : pos % a.c.page_size;
-            return (page * a.Hkv + c.walk.h) * a.c.page_size + in;
-        };
-        Cursor c0{walk, 0, walk.count()};
-        Found f0{}, f1{}, f2{};
+        // ---- loader: waits for the ring's slots, in order, and fills them with boxes
+        // or lets the copy warps go.  (Row gathers by TMA took 60 ns per four half
+        // rows, 7.7 us a tile.)  Page numbers of the boxes are read 32 at a time, a
+        // batch ahead.  The mask ring: the loader is at most kSlots / 2 tiles ahead of
+        // the last S = Q K^T, itself at most 2 ahead of the softmax.
+        const int shift = a.box_rows ? __ffs(kTile / a.box_rows) - 1 : 0;     // log2(boxes per tile)
+        const int batch = 32 >> shift;                                        // tiles per 32 boxes
+        auto box_pos = [&](int t, int box) { return t * kTile + box * a.box_rows; };
+        uint32_t tile_no = 0, copied = 0, flags = 0;       // tiles; tiles for the copy warps
         bool ok = true;
-        if (walk.left > 0) {
-            find_positions(c0, f0);
-            find_pages(c0, f0);
-        }
-        Cursor c1 = c0;
-        if (walk.left > 0)
-            c1.step();
-        if (c1.walk.left > 0)
-            find_positions(c1, f1);
-        Cursor c2 = c1;
-        uint32_t tile_no = 0, copied = 0;         // tiles, tiles for the copy warps
-        for (; c0.walk.left > 0; ++tile_no) {
-            if (c1.walk.left > 0) {
-                find_pages(c1, f1);
-                c2.step();
-                if (c2.walk.left > 0)
-                    find_positions(c2, f2);
+        while (ok && walk.left > 0) {
+            const int n = walk.count(), boxes = boxes_of(walk.w);
+            auto read_pages = [&](int t) {      // of the boxes of tiles t .. t + batch - 1
+                const int tile = t + (lane >> shift);
+                return tile < boxes ? page_of(walk.b, box_pos(tile, lane & ((1 << shift) - 1))) : 0;
+            };
+            int first = walk.t, pages = 0, pages2 = 0;
+            if (first < boxes) {
+                pages = read_pages(first);
+                pages2 = read_pages(first + batch);
             }
-            bool box = is_box(c0.walk.w, c0.tile());
-            int row[4];
-            uint32_t word[4] = {kFull, kFull, kFull, kFull};
-            bool alone = false;                   // a box tile with a bad page: row by row, here
-            row[0] = row_of(c0, f0.pos[0], f0.page[0]);
-            if (box && __any_sync(kFull, f0.pos[0] >= 0 && row[0] < 0)) {
-                box = false;
-                alone = true;
+            for (int i = 0; i < n; ++i, ++tile_no) {
+                const int t = walk.t + i;
+                const bool box = t < boxes;
+                const uint32_t ring = copied % C::kRowRing;
+                int row[4] = {-1, -1, -1, -1};
+                uint32_t word = kFull;                      // lane < 4: tokens 32 * lane ..
+                bool alone = false;                         // a box tile with a bad page: row by row, here
+                if (box) {
+                    if (t == first + batch) {
+                        first = t;
+                        pages = pages2;
+                        pages2 = read_pages(t + batch);
+                    }
+                    const int mine = lane & ((1 << shift) - 1);
+                    const int page = __shfl_sync(kFull, pages, ((t - first) << shift) + mine);
+                    row[0] = row_of(walk.h, box_pos(t, mine), page);
+                    alone = __any_sync(kFull, row[0] < 0);
+                    if (alone) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    f0.pos[u] = c0.tile() * kTile + u * 32 + lane;
-                    f0.page[u] = a.c.table ? page_of(c0.walk.b, f0.pos[u]) : c0.walk.b;
-                }
-                row[0] = row_of(c0, f0.pos[0], f0.page[0]);
-            }
-            const uint32_t ring = copied % kRowRing;
-            if (!box) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    row[u] = row_of(c0, f0.pos[u], f0.page[u]);
-                    if (f0.pos[u] >= 0 && row[u] < 0)
+                        for (int u = 0; u < 4; ++u) {
+                            const int p = t * kTile + u * 32 + lane;
+                            row[u] = row_of(walk.h, p, page_of(walk.b, p));
+                            const uint32_t there = __ballot_sync(kFull, row[u] >= 0);
+                            word = lane == u ? there : word;
+                        }
                         flags |= kFlagPageOutOfRange;
-                    word[u] = __ballot_sync(kFull, row[u] >= 0);
-                }
-                if (!alone) {
-                    if (copied >= kRowRing)       // the list of four copied tiles before has been read
-                        ok = __all_sync(kFull, bar_wait(&x.rows_read[ring], (copied / kRowRing - 1) & 1, gave_up));
+                    }
+                } else {
+                    ok = __all_sync(kFull, bar_wait(&x.rows_there[ring], copied / C::kRowRing & 1, gave_up));
                     if (!ok)
                         break;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        x.rows[ring][u * 32 + lane] = row[u];
+                    word = x.rows_valid[ring][lane & 3];
                 }
-            }
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint32_t e = 2 * tile_no + kv, slot = e % C::kSlots, use = e / C::kSlots;
-                if (use > 0)
-                    ok = __all_sync(kFull, bar_wait(&x.empty[slot], (use - 1) & 1, gave_up));
-                if (!ok)
-                    break;
-                if (kv == 0 && lane < 4)
-                    x.valid[tile_no % kMaskRing][lane] = lane < 2 ? (lane == 0 ? word[0] : word[1])
-                                                                  : (lane == 2 ? word[2] : word[3]);
-                __syncwarp();
-                loaded = e + 1;
-                const uint32_t dst = sm_ring + slot * kTileBytes;
-                if (box) {
-                    if (lane == 0) {
-                        bar_expect(&x.full[slot], kTileBytes);
-                        bar_arrive_n(&x.full[slot], 32 * C::kCopiers - 1);
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t e = 2 * tile_no + kv, slot = e % C::kSlots, use = e / C::kSlots;
+                    if (use > 0)
+                        ok = __all_sync(kFull, bar_wait(&x.empty[slot], (use - 1) & 1, gave_up));
+                    if (!ok)
+                        break;
+                    if (kv == 0 && lane < 4)
+                        x.valid[tile_no % kMaskRing][lane] = word;
+                    __syncwarp();
+                    loaded = e + 1;
+                    const uint32_t dst = sm_ring + slot * kTileBytes;
+                    if (!box) {
+                        if (lane == 0)
+                            bar_arrive(&x.go[ring][kv]);
+                    } else if (!alone) {
+                        if (lane == 0) {
+                            bar_expect(&x.full[slot], kTileBytes);
+                            bar_arrive_n(&x.full[slot], 32 * C::kCopiers - 1);
+                        }
+                        __syncwarp();
+                        if (lane < 1 << shift) {
+                            const TmaDesc *map = kv ? &a.box_v : &a.box_k;
+                            const uint32_t d = dst + lane * a.box_rows * 128;
+                            tma_box(d, map, 0, row[0], &x.full[slot]);
+                            tma_box(d + kHalfBytes, map, 64, row[0], &x.full[slot]);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int j = 0; j < kTile / 2; ++j) {
+                            const int tok = 2 * j + (lane >> 4);
+                            const int from = j < 16 ? row[0] : j < 32 ? row[1] : j < 48 ? row[2] : row[3];
+                            copy_row(dst, tok, kv ? a.c.v : a.c.k, __shfl_sync(kFull, from, tok & 31), lane);
+                        }
+                        copies_arrive(&x.full[slot]);
+                        if (lane == 0)
+                            bar_arrive_n(&x.full[slot], 32 * C::kCopiers - 32);
                     }
                     __syncwarp();
-                    if (row[0] >= 0) {
-                        const TmaDesc *map = kv ? &a.box_v : &a.box_k;
-                        const uint32_t d = dst + lane * a.box_rows * 128;
-                        tma_box(d, map, 0, row[0], &x.full[slot]);
-                        tma_box(d + kHalfBytes, map, 64, row[0], &x.full[slot]);
+                }
+                if (!ok)
+                    break;
+                copied += box ? 0 : 1;
+            }
+            walk.next(n);
+        }
+        if (flags && lane == 0)
+            atomicOr(a.status, flags);
+    } else if (warp == C::kFinder || warp == C::kFinder + 1) {
+        // ---- finders: the cache rows of every kFinders-th tile for the copy warps, as
+        // far ahead as there are lists.  (Memory is slow to answer while every SM's
+        // ring fills: found by the copy warps themselves, between two tiles, the rows
+        // cost 1500 to 3000 cycles a tile.)
+        const int me = warp - C::kFinder;
+        constexpr uint32_t kRing = C::kRowRing;
+        // Index entries and page numbers of a segment into L2 before they are needed.
+        auto prefetch = [&](const Walk<MT> &at) {
+            const int first = at.t * kTile, tokens = at.count() * kTile;
+            if (a.idx) {
+                const int32_t *p = a.idx + ((size_t)at.b * a.Hkv + at.h) * a.top_k;
+                for (int j = first + lane * 32; j < min(first + tokens, a.top_k); j += 32 * 32)
+                    prefetch_l2(p + j);
+            }
+            if (a.c.table) {
+                const int32_t *p = a.c.table + (size_t)at.b * a.c.max_blocks;
+                const int blocks = (at.w.ctx + at.w.nt + a.c.page_size - 1) / a.c.page_size;
+                for (int j = lane * 32; j < blocks; j += 32 * 32)
+                    prefetch_l2(p + j);
+            }
+        };
+        uint32_t flags = 0, tile = 0;      // tile: number of the copied tile
+        bool ok = true;
+        for (bool first = true; ok && walk.left > 0; first = false) {
+            const Work &w = walk.w;
+            const int n = walk.count();
+            if (me == 0) {
+                Walk<MT> next = walk;
+                next.next(n);
+                if (next.left > 0)
+                    prefetch(next);
+            } else if (first) {
+                prefetch(walk);
+            }
+            for (int i = max(0, boxes_of(w) - walk.t); i < n; ++i, ++tile) {
+                if (tile % C::kFinders != (uint32_t)me)
+                    continue;
+                const int t = walk.t + i, base = t * kTile;
+                const bool last = t == w.tiles - 1;
+                const int listed = last ? w.off : min(kTile, w.entries - base);   // context entries
+                int pos[4], row[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int j = u * 32 + lane;
+                    if (j < listed)
+                        pos[u] = a.idx ? __ldg(a.idx + ((size_t)walk.b * a.Hkv + walk.h) * a.top_k + base + j)
+                                       : base + j;
+                    else
+                        pos[u] = last && j - w.off < w.nt ? w.ctx + j - w.off : -1;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (u * 32 + lane < listed && pos[u] != -1 && (pos[u] < 0 || pos[u] >= w.ctx)) {
+                        flags |= kFlagIndexOutOfRange;
+                        pos[u] = -1;
                     }
-                } else if (!alone) {
+                    row[u] = pos[u] < 0 ? -1 : page_of(walk.b, pos[u]);
+                }
+                const uint32_t ring = tile % kRing;
+                if (tile >= kRing)        // every copy warp has read the list before
+                    ok = __all_sync(kFull, bar_wait(&x.rows_read[ring], (tile / kRing - 1) & 1, gave_up));
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    row[u] = row_of(walk.h, pos[u], row[u]);
+                    if (pos[u] >= 0 && row[u] < 0)
+                        flags |= kFlagPageOutOfRange;
+                    const uint32_t there = __ballot_sync(kFull, row[u] >= 0);
                     if (lane == 0)
-                        bar_arrive(&x.go[ring][kv]);
-                } else {
-                    for (int j = 0; j < kTile / 2; ++j) {
-                        const int tok = 2 * j + (lane >> 4);
-                        const int at = __shfl_sync(kFull, j < 16 ? row[0] : j < 32 ? row[1] : j < 48 ? row[2] : row[3],
-                                                   tok & 31);
-                        copy_row(dst, tok, kv ? a.c.v : a.c.k, at, lane);
-                    }
-                    copies_arrive(&x.full[slot]);
-                    if (lane == 0)
-                        bar_arrive_n(&x.full[slot], 32 * C::kCopiers - 32);
+                        x.rows_valid[ring][u] = there;
+                    x.rows[ring][u * 32 + lane] = row[u];
                 }
                 __syncwarp();
+                if (lane == 0)
+                    bar_arrive(&x.rows_there[ring]);
             }
-            if (!ok)
-                break;
-            copied += box || alone ? 0 : 1;
-            c0 = c1;
-            f0 = f1;
-            c1 = c2;
-            f1 = f2;
+            walk.next(n);
         }
         if (flags)
             atomicOr(a.status, flags);
-    } else if (warp >= C::kCopier) {
+    } else if (C::copier(warp) >= 0) {
         // ---- copy warps: a segment's Q, then the rows of its tiles that are not
         // boxes, with cp.async, half a warp per 256-byte row; a token that does not
         // exist is filled with zeros (no stale V value meets its zero probability).
-        const int me = warp - C::kCopier;
-        uint32_t e = 0, seg = 0, copied = 0;
+        const int me = C::copier(warp);
+        constexpr uint32_t kRing = C::kRowRing;
+        uint32_t e = 0, copied = 0;
         bool ok = true;
-        for (; ok && walk.left > 0; ++seg) {
+        for (uint32_t seg = 0; ok && walk.left > 0; ++seg) {
             const int n = walk.count();
             // Q: its buffer was the last segment's, or with two the one before's.  Rows
             // that are not Q's are left as they are.
@@ -720,17 +761,15 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 }
                 copies_arrive(&x.q[seg & 1]);
             }
-            for (int i = 0; ok && i < n; ++i, e += 2) {
-                const int t = walk.t + i;
-                if (is_box(walk.w, t))
-                    continue;
-                const uint32_t ring = copied % kRowRing, phase = copied / kRowRing & 1;
-                const int tokens = walk.w.tokens(t);
+            for (int i = max(0, boxes_of(walk.w) - walk.t); i < n; ++i, ++copied) {
+                const uint32_t ring = copied % kRing, phase = copied / kRing & 1;
+                const int tokens = walk.w.tokens(walk.t + i);
+#pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
                     ok = __all_sync(kFull, bar_wait(&x.go[ring][kv], phase, gave_up));
                     if (!ok)
                         break;
-                    const uint32_t slot = (e + kv) % C::kSlots;
+                    const uint32_t slot = (e + 2 * i + kv) % C::kSlots;
                     // scores of rows behind the tokens are masked; P V takes tokens by 16
                     const int end = kv ? (tokens + 15) & ~15 : tokens;
                     const uint16_t *src = kv ? a.c.v : a.c.k;
@@ -741,10 +780,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     copies_arrive(&x.full[slot]);
                 }
                 __syncwarp();
-                if (ok && lane == 0)
+                if (!ok)
+                    break;
+                if (lane == 0)
                     bar_arrive(&x.rows_read[ring]);
-                ++copied;
             }
+            e += 2 * n;
             walk.next(n);
         }
     } else if (warp == C::kIssuer) {
