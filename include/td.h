@@ -511,8 +511,8 @@ td_status td_kv_append_slots(const td_shape *shape, const td_cache *cache, int32
  * [0, seq_lens[b]], is clamped (TD_FLAG_SEQ_LEN_OUT_OF_RANGE); a page count
  * outside its range is clamped and a page number outside [0, num_pages) gives
  * slot -1 (TD_FLAG_PAGE_OUT_OF_RANGE).
- *   1 <= batch <= 65535, max_blocks * page_size and num_pages * page_size
- *   < 2^31.  Arrays other than the two out pairs must not overlap.
+ *   1 <= batch <= 65535; batch * max_blocks, max_blocks * page_size and
+ *   num_pages * page_size < 2^31.  Arrays other than the two out pairs must not overlap.
  * The workspace is used for its status word only.
  */
 td_status td_block_tables(int32_t batch, int32_t page_size, int32_t max_blocks, int32_t num_pages,

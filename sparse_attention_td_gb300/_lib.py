@@ -319,14 +319,35 @@ def _ptr_array(tensors, name, dtype, numel, optional=False):
     return (ctypes.c_void_p * max(len(ptrs), 1))(*ptrs)
 
 
-def _here(tensors, stream=None):
-    """The call launches on the current device: every tensor has to live there."""
-    dev = torch.cuda.current_device()
-    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
-        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{dev}")
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+# The calls below run once or more per layer, so their marshalling is kept short:
+# one look at each tensor (_on), the raw stream handle.
+
+def _launch(stream):
+    """(device, raw stream): a call launches on the current device."""
+    dev = torch._C._cuda_getDevice()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is cuda:{dev}")
+    return dev, _stream(stream)
+
+
+def _on(dev, t, name, dtype, numel):
+    """Pointer of a contiguous tensor of at least numel values on device dev."""
+    if t is not None and t.get_device() == dev and t.dtype is dtype and t.is_contiguous() and \
+            t.numel() >= numel:
+        return t.data_ptr()
+    _dev(t, name, dtype, numel)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _ws(dev, ws):
+    if ws is None:
+        raise ValueError("ws is required")
+    t = ws.tensor
+    if t.get_device() != dev:
+        raise ValueError(f"ws is on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr(), t.numel()
 
 
 class Cache:
@@ -347,95 +368,118 @@ class Cache:
         self.c = _Cache(_dev(k, "k", torch.bfloat16), _dev(v, "v", torch.bfloat16), self.num_pages,
                         self.page_size, _dev(block_table, "block_table", torch.int32, optional=True),
                         0 if block_table is None else int(block_table.shape[1]))
+        self.device = k.get_device()
+        for name, t in (("v", v), ("block_table", block_table)):
+            if t is not None and t.get_device() != self.device:
+                raise ValueError(f"k is on {k.device}, {name} on {t.device}")
+        self.ref = ctypes.byref(self.c)
+        self.raw = bytes(self.c)
+        # what a call has to agree with: device, KV heads, requests (None: any)
+        self.fits = (self.device, self.kv_heads, None if block_table is None else int(block_table.shape[0]))
 
-    def check(self, shape: Shape):
-        if self.kv_heads != shape.num_kv_heads:
-            raise ValueError(f"the cache has {self.kv_heads} KV heads, the shape {shape.num_kv_heads}")
-        if self.block_table is not None and self.block_table.shape[0] < shape.batch:
-            raise ValueError(f"block_table has {self.block_table.shape[0]} rows, needs {shape.batch}")
-        return self
+    def check(self, shape: Shape, dev: int):
+        _fits(self.fits, shape, dev)
+        return self.ref
 
-    def tensors(self):
-        return {"k": self.k, "v": self.v, "block_table": self.block_table}
+
+def _fits(fits, shape, dev):
+    device, heads, rows = fits
+    if device != dev:
+        raise ValueError(f"the cache is on cuda:{device}, the current device is cuda:{dev}")
+    if heads != shape.num_kv_heads:
+        raise ValueError(f"the cache has {heads} KV heads, the shape {shape.num_kv_heads}")
+    if rows is not None and rows < shape.batch:
+        raise ValueError(f"block_table has {rows} rows, needs {shape.batch}")
 
 
 def make_cache(k, v, block_table=None) -> Cache:
     return Cache(k, v, block_table)
 
 
-def _tree(shape, cache, tree_size, tree_lens, tree_mask, q, seq_lens, out, ws, stream, **more):
-    cache.check(shape)
-    _here({**cache.tensors(), "tree_lens": tree_lens, "tree_mask": tree_mask, "q": q,
-           "seq_lens": seq_lens, "out": out, "ws": ws.tensor, **more}, stream)
-    nb, T = shape.batch, int(tree_size)
-    n = nb * T * shape.num_q_heads * shape.head_dim
-    return (ctypes.byref(shape), ctypes.byref(cache.c), T,
-            _dev(tree_lens, "tree_lens", torch.int32, nb, True),
-            _dev(tree_mask, "tree_mask", torch.int32, nb * T * ((T + 31) // 32), True),
-            _dev(q, "q", torch.bfloat16, n), _dev(seq_lens, "seq_lens", torch.int32, nb),
-            _dev(out, "out", torch.bfloat16, n))
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
 def td_tree_attn(shape: Shape, cache: Cache, tree_size, tree_lens, tree_mask, q, seq_lens, out,
                  ws: Workspace = None, stream=None):
     """Attention of tree_size drafted tokens per request over the cache;
     tree_mask int32 words [B][T][ceil(T / 32)] (None: a chain)."""
-    a = _tree(shape, cache, tree_size, tree_lens, tree_mask, q, seq_lens, out, ws, stream)
-    _check(lib().td_tree_attn(*a, ws.ptr, ws.nbytes, _stream(stream)), "td_tree_attn")
+    dev, st = _launch(stream)
+    wp, wn = _ws(dev, ws)
+    nb, T = shape.batch, int(tree_size)
+    n = nb * T * shape.num_q_heads * 128
+    rc = lib().td_tree_attn(
+        shape, cache.check(shape, dev), T,
+        None if tree_lens is None else _on(dev, tree_lens, "tree_lens", _I32, nb),
+        None if tree_mask is None else _on(dev, tree_mask, "tree_mask", _I32, nb * T * ((T + 31) // 32)),
+        _on(dev, q, "q", _BF16, n), _on(dev, seq_lens, "seq_lens", _I32, nb),
+        _on(dev, out, "out", _BF16, n), wp, wn, st)
+    if rc:
+        _check(rc, "td_tree_attn")
 
 
 def td_tree_sparse_attn(shape: Shape, cache: Cache, tree_size, tree_lens, tree_mask, q, seq_lens,
                         idx, top_k, out, ws: Workspace = None, stream=None):
     """td_tree_attn over the persisted index set of a PPSA layer and the tree."""
-    *a, po = _tree(shape, cache, tree_size, tree_lens, tree_mask, q, seq_lens, out, ws, stream,
-                   idx=idx)
-    pi = _dev(idx, "idx", torch.int32, shape.batch * shape.num_kv_heads * int(top_k))
-    _check(lib().td_tree_sparse_attn(*a, pi, int(top_k), po, ws.ptr, ws.nbytes, _stream(stream)),
-           "td_tree_sparse_attn")
+    dev, st = _launch(stream)
+    wp, wn = _ws(dev, ws)
+    nb, T, k = shape.batch, int(tree_size), int(top_k)
+    n = nb * T * shape.num_q_heads * 128
+    rc = lib().td_tree_sparse_attn(
+        shape, cache.check(shape, dev), T,
+        None if tree_lens is None else _on(dev, tree_lens, "tree_lens", _I32, nb),
+        None if tree_mask is None else _on(dev, tree_mask, "tree_mask", _I32, nb * T * ((T + 31) // 32)),
+        _on(dev, q, "q", _BF16, n), _on(dev, seq_lens, "seq_lens", _I32, nb),
+        _on(dev, idx, "idx", _I32, nb * shape.num_kv_heads * k), k, _on(dev, out, "out", _BF16, n),
+        wp, wn, st)
+    if rc:
+        _check(rc, "td_tree_sparse_attn")
 
 
 def td_tree_commit(shape: Shape, caches: Sequence[Cache], tree_size, tree_lens, accepted,
                    accepted_lens, seq_lens, seq_lens_out, ws: Workspace = None, stream=None):
     """Move the accepted drafted rows of every layer to the front of their tree."""
+    dev, st = _launch(stream)
+    wp, wn = _ws(dev, ws)
     nb, T = shape.batch, int(tree_size)
-    for c in caches:
-        c.check(shape)
-        _here(c.tensors(), stream)
-    _here({"tree_lens": tree_lens, "accepted": accepted, "accepted_lens": accepted_lens,
-           "seq_lens": seq_lens, "seq_lens_out": seq_lens_out, "ws": ws.tensor}, stream)
-    arr = (_Cache * max(len(caches), 1))(*[c.c for c in caches])
-    st = lib().td_tree_commit(
-        ctypes.byref(shape), len(caches), arr, T, _dev(tree_lens, "tree_lens", torch.int32, nb, True),
-        _dev(accepted, "accepted", torch.int32, nb * T),
-        _dev(accepted_lens, "accepted_lens", torch.int32, nb),
-        _dev(seq_lens, "seq_lens", torch.int32, nb),
-        _dev(seq_lens_out, "seq_lens_out", torch.int32, nb), ws.ptr, ws.nbytes, _stream(stream))
-    _check(st, "td_tree_commit")
+    for fits in {c.fits for c in caches}:
+        _fits(fits, shape, dev)
+    arr = ctypes.create_string_buffer(b"".join([c.raw for c in caches]))   # the td_cache array
+    rc = lib().td_tree_commit(
+        shape, len(caches), ctypes.cast(arr, ctypes.POINTER(_Cache)), T,
+        None if tree_lens is None else _on(dev, tree_lens, "tree_lens", _I32, nb),
+        _on(dev, accepted, "accepted", _I32, nb * T), _on(dev, accepted_lens, "accepted_lens", _I32, nb),
+        _on(dev, seq_lens, "seq_lens", _I32, nb), _on(dev, seq_lens_out, "seq_lens_out", _I32, nb),
+        wp, wn, st)
+    if rc:
+        _check(rc, "td_tree_commit")
 
 
-def _token_rows(t, name, heads):
+def _token_rows(dev, t, name, heads):
     """A [tokens][heads][128] tensor whose token rows may lie apart (a column
-    block of a packed projection): its pointer and token stride in values."""
-    if not t.is_cuda or t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or t.stride(2) != 1 or \
-            (heads > 1 and t.stride(1) != 128):
+    block of a packed projection): its pointer, tokens and token stride."""
+    if t.get_device() != dev or t.dtype is not _BF16:
+        raise ValueError(f"{name} must be a bfloat16 tensor on cuda:{dev}")
+    size, step = t.shape, t.stride()
+    if len(size) != 3 or size[1] != heads or size[2] != 128 or step[2] != 1 or \
+            (heads > 1 and step[1] != 128):
         raise ValueError(f"{name} must be [tokens][{heads}][128] with whole token rows")
-    return t.data_ptr(), int(t.stride(0)) if t.shape[0] > 1 else heads * 128
+    return t.data_ptr(), size[0], step[0] if size[0] > 1 else heads * 128
 
 
 def td_kv_append_slots(shape: Shape, cache: Cache, k_new, v_new, slot_map, stream=None):
     """New K/V rows [tokens][Hkv][128] into the cache at slot_map [tokens]."""
-    cache.check(shape)
-    _here({**cache.tensors(), "k_new": k_new, "v_new": v_new, "slot_map": slot_map}, stream)
-    pk, sk = _token_rows(k_new, "k_new", shape.num_kv_heads)
-    pv, sv = _token_rows(v_new, "v_new", shape.num_kv_heads)
-    n = int(k_new.shape[0])
-    if v_new.shape[0] != n or sk != sv:
+    dev, st = _launch(stream)
+    heads = shape.num_kv_heads
+    ref = cache.ref
+    if cache.device != dev or cache.kv_heads != heads:
+        cache.check(shape, dev)
+    pk, n, sk = _token_rows(dev, k_new, "k_new", heads)
+    pv, nv, sv = _token_rows(dev, v_new, "v_new", heads)
+    if n != nv or sk != sv:
         raise ValueError("k_new and v_new must have the same tokens and token stride")
-    st = lib().td_kv_append_slots(ctypes.byref(shape), ctypes.byref(cache.c), n, pk, pv, sk,
-                                  _dev(slot_map, "slot_map", torch.int32, n), _stream(stream))
-    _check(st, "td_kv_append_slots")
+    rc = lib().td_kv_append_slots(shape, ref, n, pk, pv, sk, _on(dev, slot_map, "slot_map", _I32, n), st)
+    if rc:
+        _check(rc, "td_kv_append_slots")
 
 
 def td_block_tables(seq_lens, new_lens, page_size, block_table, num_blocks, num_blocks_out,
@@ -443,22 +487,22 @@ def td_block_tables(seq_lens, new_lens, page_size, block_table, num_blocks, num_
                     ws: Workspace = None, stream=None):
     """Block tables and slot map of a batch from its lengths; sizes come from
     block_table [B][max_blocks], free_pages [num_pages] and slot_map [max_new]."""
-    _here({"seq_lens": seq_lens, "new_lens": new_lens, "block_table": block_table,
-           "num_blocks": num_blocks, "num_blocks_out": num_blocks_out, "free_pages": free_pages,
-           "free_count": free_count, "free_count_out": free_count_out, "cu_new": cu_new,
-           "slot_map": slot_map, "ws": ws.tensor}, stream)
+    dev, st = _launch(stream)
+    wp, wn = _ws(dev, ws)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch][max_blocks]")
-    B, blocks = (int(x) for x in block_table.shape)
-    i32 = torch.int32
-    st = lib().td_block_tables(
-        B, int(page_size), blocks, int(free_pages.numel()), _dev(seq_lens, "seq_lens", i32, B),
-        _dev(new_lens, "new_lens", i32, B), _dev(block_table, "block_table", i32),
-        _dev(num_blocks, "num_blocks", i32, B), _dev(num_blocks_out, "num_blocks_out", i32, B),
-        _dev(free_pages, "free_pages", i32), _dev(free_count, "free_count", i32, 1),
-        _dev(free_count_out, "free_count_out", i32, 1), _dev(cu_new, "cu_new", i32, B + 1),
-        _dev(slot_map, "slot_map", i32), int(slot_map.numel()), ws.ptr, ws.nbytes, _stream(stream))
-    _check(st, "td_block_tables")
+    B, blocks = block_table.shape
+    pages, slots = free_pages.numel(), slot_map.numel()
+    rc = lib().td_block_tables(
+        B, int(page_size), blocks, pages, _on(dev, seq_lens, "seq_lens", _I32, B),
+        _on(dev, new_lens, "new_lens", _I32, B), _on(dev, block_table, "block_table", _I32, 0),
+        _on(dev, num_blocks, "num_blocks", _I32, B),
+        _on(dev, num_blocks_out, "num_blocks_out", _I32, B),
+        _on(dev, free_pages, "free_pages", _I32, 0), _on(dev, free_count, "free_count", _I32, 1),
+        _on(dev, free_count_out, "free_count_out", _I32, 1), _on(dev, cu_new, "cu_new", _I32, B + 1),
+        _on(dev, slot_map, "slot_map", _I32, 0), slots, wp, wn, st)
+    if rc:
+        _check(rc, "td_block_tables")
 
 
 class _StepArgs:

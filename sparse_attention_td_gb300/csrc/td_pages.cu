@@ -16,37 +16,38 @@ constexpr int kRowChunks = kHeadDim / 8;      // 16-byte chunks of one row
 
 // ------------------------------------------------------------ block tables
 constexpr int kTableThreads = 1024;
+// Up to this many slots the block-table CTA writes the slot map itself; more are
+// a second kernel's.  Measured on GB300 (256 requests): see launch_block_tables.
+constexpr int kOwnSlots = 4096;
 
-// Exclusive prefix sum over the CTA's threads, and its total.
-__device__ __forceinline__ long long block_scan(long long x, long long *sm_warp, long long &total)
+template <typename T> __device__ __forceinline__ T scan_warp(T x, int lane)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long inc = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(kAll, inc, d);
+        const T y = __shfl_up_sync(kAll, x, d);
         if (lane >= d)
-            inc += y;
+            x += y;
     }
+    return x;
+}
+
+// Exclusive prefix sum over the CTA's threads, and its total.
+template <typename T> __device__ __forceinline__ T scan_block(T x, T *sm_warp, T &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T inc = scan_warp(x, lane);
     if (lane == 31)
         sm_warp[warp] = inc;
     __syncthreads();
-    long long w = sm_warp[lane];
-    long long winc = w;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(kAll, winc, d);
-        if (lane >= d)
-            winc += y;
-    }
+    const T w = sm_warp[lane], winc = scan_warp(w, lane);
     total = __shfl_sync(kAll, winc, 31);
-    const long long before = __shfl_sync(kAll, winc - w, warp);
+    const T before = __shfl_sync(kAll, winc - w, warp);
     __syncthreads();
     return before + inc - x;
 }
 
-// The last request of the chunk whose prefix is <= e (prefix[0] = 0, ascending).
-__device__ __forceinline__ int owner_of(const long long *prefix, int n, long long e)
+// The last of n ascending values that is <= e (the first one is).
+template <typename T> __device__ __forceinline__ int owner_of(const T *prefix, int n, T e)
 {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
@@ -66,103 +67,140 @@ struct Want {
 __device__ __forceinline__ Want want_of(const TablesArgs &a, int b, uint32_t &bad)
 {
     const int cap = a.max_blocks * a.page_size;
+    const int n = a.seq_lens[b], fresh = a.new_lens[b], held = a.held[b];
     Want w;
-    int raw = a.seq_lens[b];
-    w.n = raw < 0 ? 0 : (raw > cap ? cap : raw);
-    if (w.n != raw)
+    w.n = min(max(n, 0), cap);
+    w.fresh = min(max(fresh, 0), w.n);
+    w.held = min(max(held, 0), a.max_blocks);
+    if (w.n != n || w.fresh != fresh)
         bad |= kFlagSeqLenOutOfRange;
-    raw = a.new_lens[b];
-    w.fresh = raw < 0 ? 0 : (raw > w.n ? w.n : raw);
-    if (w.fresh != raw)
-        bad |= kFlagSeqLenOutOfRange;
-    raw = a.held[b];
-    w.held = raw < 0 ? 0 : (raw > a.max_blocks ? a.max_blocks : raw);
-    if (w.held != raw)
+    if (w.held != held)
         bad |= kFlagPageOutOfRange;
-    w.target = (int)(((long long)w.n + a.page_size - 1) / a.page_size);
+    w.target = (int)((w.n + a.page_size - 1u) / (unsigned)a.page_size);
     return w;
+}
+
+// Slot of position p of request b, which holds `held` pages.
+__device__ __forceinline__ int slot_of(const TablesArgs &a, int b, int p, int held, uint32_t &bad)
+{
+    const int j = p / a.page_size;
+    if (j >= held)
+        return -1;
+    const int page = a.table[(size_t)b * a.max_blocks + j];
+    if (page < 0 || page >= a.num_pages) {
+        bad |= kFlagPageOutOfRange;
+        return -1;
+    }
+    return page * a.page_size + (p - j * a.page_size);
 }
 
 // Pages: one CTA, requests in chunks of its threads.  Pass 1 pushes what
 // requests give back, pass 2 pops what they need, so a page given back in a
 // call can be taken in the same call.  Each changed table entry is one
 // thread's work (its request found by a search of the chunk's prefix sums), so
-// one long prompt does not make one thread walk all of its pages.
+// one long prompt does not make one thread walk all of its pages.  What bounds
+// it is the chain of dependent loads and barriers (about 4 us).
 __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const TablesArgs a)
 {
-    __shared__ long long sm_warp[32];
-    __shared__ long long sm_prefix[kTableThreads];
-    __shared__ int sm_first[kTableThreads];
+    __shared__ long long sm_warp64[32];
+    __shared__ int sm_warp[32];
+    __shared__ int sm_prefix[kTableThreads], sm_first[kTableThreads], sm_cu[kTableThreads];
+    __shared__ int sm_fit;
     const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the slot map's blocks may come
     uint32_t bad = 0;
     int count = *a.count;
     if (count < 0 || count > a.num_pages) {
         count = count < 0 ? 0 : a.num_pages;
         bad |= kFlagPageOutOfRange;
     }
+    const bool single = a.B <= kTableThreads;
+    Want w{};
     long long top = count;
     for (int b0 = 0; b0 < a.B; b0 += kTableThreads) {
         const int b = b0 + tid;
-        Want w{};
+        w = Want{};
         if (b < a.B)
             w = want_of(a, b, bad);
-        long long total;
-        const long long at = block_scan(w.held > w.target ? w.held - w.target : 0, sm_warp, total);
-        if (total == 0)
+        const int back = w.held > w.target ? w.held - w.target : 0;
+        if (!__syncthreads_or(back))
             continue;
+        int total;
+        const int at = scan_block(back, sm_warp, total);
         sm_prefix[tid] = at;
         sm_first[tid] = w.target;
         __syncthreads();
         const int n = min(kTableThreads, a.B - b0);
-        for (long long e = tid; e < total; e += kTableThreads) {
+        for (int e = tid; e < total; e += kTableThreads) {
             const int i = owner_of(sm_prefix, n, e);
-            const int j = sm_first[i] + (int)(e - sm_prefix[i]);
+            const int j = sm_first[i] + e - sm_prefix[i];
             if (top + e < a.num_pages)
                 a.free_pages[top + e] = a.table[(size_t)(b0 + i) * a.max_blocks + j];
             else
                 bad |= kFlagPageOutOfRange;   // more pages given back than there are
         }
-        top += total;
-        if (top > a.num_pages)
-            top = a.num_pages;
-        __syncthreads();
+        top = min(top + total, (long long)a.num_pages);
+        __syncthreads();      // the pushes are visible to the pops
     }
-    __syncthreads();      // the pushes are visible to the pops
     long long taken = 0, used = 0, fresh = 0;
     for (int b0 = 0; b0 < a.B; b0 += kTableThreads) {
         const int b = b0 + tid;
-        Want w{};
-        if (b < a.B)
-            w = want_of(a, b, bad);
-        const int need = w.target > w.held ? w.target - w.held : 0;
-        long long total, total_new;
-        const long long at = taken + block_scan(need, sm_warp, total);
-        const long long cu = fresh + block_scan(w.fresh, sm_warp, total_new);
-        const bool fits = at + need <= top;
-        if (need && !fits)
-            bad |= kFlagPagesExhausted;
-        sm_prefix[tid] = at - taken;
-        sm_first[tid] = w.held;
-        long long fit_end = 0, dummy;
-        // pages popped in this chunk: the prefix up to its last request that fits
-        {
-            long long mine = need && fits ? need : 0;
-            block_scan(mine, sm_warp, dummy);
-            fit_end = dummy;
+        if (!single) {
+            w = Want{};
+            if (b < a.B)
+                w = want_of(a, b, bad);
         }
+        const int need = w.target > w.held ? w.target - w.held : 0;
+        int total;
+        long long total_new;
+        const int rel = scan_block(need, sm_warp, total);
+        const long long cu = fresh + scan_block((long long)w.fresh, sm_warp64, total_new);
+        const bool fits = taken + rel + need <= top;
+        sm_prefix[tid] = rel;
+        sm_first[tid] = w.held;
+        sm_cu[tid] = (int)min(cu, 0x7fffffffLL);
+        // pages popped in this chunk: up to the first request that does not fit
+        int fit_end = total;
+        if (taken + total > top) {            // (the same for all threads)
+            if (tid == 0)
+                sm_fit = total;
+            __syncthreads();
+            if (need && !fits) {
+                bad |= kFlagPagesExhausted;
+                atomicMin(&sm_fit, rel);
+            }
+            __syncthreads();
+            fit_end = sm_fit;
+        }
+        if (need && fits)
+            w.held = w.target;
+        else if (!need)
+            w.held = w.target;
         if (b < a.B) {
-            a.held_out[b] = need && !fits ? w.held : w.target;
-            a.cu_new[b] = (int)min(cu, 0x7fffffffLL);
+            a.held_out[b] = w.held;
+            a.cu_new[b] = sm_cu[tid];
         }
         __syncthreads();
         const int n = min(kTableThreads, a.B - b0);
-        for (long long e = tid; e < fit_end; e += kTableThreads) {
-            const int i = owner_of(sm_prefix, n, e);
-            const int j = sm_first[i] + (int)(e - sm_prefix[i]);
-            const int page = a.free_pages[top - 1 - (taken + e)];
-            if (page < 0 || page >= a.num_pages)
-                bad |= kFlagPageOutOfRange;
-            a.table[(size_t)(b0 + i) * a.max_blocks + j] = page;
+        constexpr int kAhead = 4;      // pops in flight per thread
+        for (int e0 = tid; e0 < fit_end; e0 += kAhead * kTableThreads) {
+            int page[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int e = e0 + u * kTableThreads;
+                page[u] = e < fit_end ? a.free_pages[top - 1 - (taken + e)] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int e = e0 + u * kTableThreads;
+                if (e >= fit_end)
+                    break;
+                const int i = owner_of(sm_prefix, n, e);
+                const int j = sm_first[i] + e - sm_prefix[i];
+                if (page[u] < 0 || page[u] >= a.num_pages)
+                    bad |= kFlagPageOutOfRange;
+                a.table[(size_t)(b0 + i) * a.max_blocks + j] = page[u];
+            }
         }
         taken += total;
         used += fit_end;
@@ -175,41 +213,60 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
         if (fresh > a.max_new)
             bad |= kFlagPagesExhausted;
     }
+    if (single && a.max_new <= kOwnSlots) {
+        // the slots of a decode step: the chunk's sums are still in shared memory
+        sm_prefix[tid] = w.held;
+        sm_first[tid] = w.n - w.fresh;
+        __syncthreads();
+        for (int i = tid; i < a.max_new; i += kTableThreads) {
+            int slot = -1;
+            if (i < fresh) {
+                const int b = owner_of(sm_cu, a.B, i);
+                slot = slot_of(a, b, sm_first[b] + i - sm_cu[b], sm_prefix[b], bad);
+            }
+            a.slots[i] = slot;
+        }
+    }
     if (bad)
         atomicOr(a.status, bad);
 }
 
 constexpr int kSlotThreads = 256;
+constexpr int kSlotsPerThread = 4;
 
+// The slots of prompts: what a block's tokens need of the batch's prefix sums is
+// searched in shared memory where it fits.
 __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const TablesArgs a)
 {
-    const int i = blockIdx.x * kSlotThreads + threadIdx.x;
-    if (i >= a.max_new)
-        return;
-    int slot = -1;
-    if (i < a.cu_new[a.B]) {
-        int lo = 0, hi = a.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.cu_new[mid] <= i)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        const int cap = a.max_blocks * a.page_size;
-        const int raw = a.seq_lens[lo];
-        const int n = raw < 0 ? 0 : (raw > cap ? cap : raw);
-        const int p = n - (a.cu_new[lo + 1] - a.cu_new[lo]) + (i - a.cu_new[lo]);
-        const int j = p / a.page_size;
-        if (j < a.held_out[lo]) {
-            const int page = a.table[(size_t)lo * a.max_blocks + j];
-            if (page >= 0 && page < a.num_pages)
-                slot = page * a.page_size + p % a.page_size;
-            else
-                atomicOr(a.status, kFlagPageOutOfRange);
-        }
+    __shared__ int sm_cu[1024];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int *cu = a.cu_new;
+    const int total = a.cu_new[a.B];
+    const int base = blockIdx.x * kSlotThreads * kSlotsPerThread;
+    if (a.B <= 1024 && base < total) {
+        for (int b = threadIdx.x; b < a.B; b += kSlotThreads)
+            sm_cu[b] = a.cu_new[b];
+        __syncthreads();
+        cu = sm_cu;
     }
-    a.slots[i] = slot;
+    const int cap = a.max_blocks * a.page_size;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int u = 0; u < kSlotsPerThread; ++u) {
+        const int i = base + u * kSlotThreads + threadIdx.x;
+        if (i >= a.max_new)
+            break;
+        int slot = -1;
+        if (i < total) {
+            const int b = owner_of(cu, a.B, i);
+            const int n = min(max(a.seq_lens[b], 0), cap);
+            const int end = b + 1 < a.B ? cu[b + 1] : total;
+            slot = slot_of(a, b, n - (end - cu[b]) + i - cu[b], a.held_out[b], bad);
+        }
+        a.slots[i] = slot;
+    }
+    if (bad)
+        atomicOr(a.status, bad);
 }
 
 // -------------------------------------------------------------- slot append
@@ -241,69 +298,121 @@ __global__ void __launch_bounds__(kAppendThreads) append_slots_kernel(const Appe
 }
 
 // ------------------------------------------------------------------- commit
-// One CTA per (request, KV head, layer): it alone reads and writes that head's
-// drafted rows, and holds all of them in registers before it writes any, so a
-// row may be both a source and a destination.
-constexpr int kCommitThreads = 256;
+// A CTA takes the accepted rows of one request for up to kCommitTasks (layer, KV
+// head, K or V) tasks per warp, fewer where the launch has few CTAs: the rows are found once, then each warp moves its tasks'
+// rows, half a warp per 256-byte row.  A row may be both a source and a
+// destination.  Where no accepted token comes before its place (a path of a tree
+// whose parents have lower numbers), sixteen rows at a time can be read and then
+// written in order: a later source lies behind every earlier destination.  In any
+// other order the whole CTA holds all rows of a task before it writes any.
+constexpr int kCommitWarps = 8;
+constexpr int kCommitTasks = 4;
+constexpr int kCommitRows = 16;       // rows a warp holds at a time
 
-__global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitArgs a)
+__global__ void __launch_bounds__(32 * kCommitWarps) tree_commit_kernel(const CommitArgs a, int tasks, int per_warp)
 {
-    const int g = blockIdx.x, b = blockIdx.y, l = blockIdx.z, tid = threadIdx.x;
+    __shared__ long long sm_src[TD_MAX_TREE], sm_dst[TD_MAX_TREE];   // cache rows of KV head 0, -1: stays
+    __shared__ int sm_behind, sm_moves;
+    const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t bad = 0;
     const TreeLens len = tree_lens_of(a.seq_lens, a.tree_lens, b, a.T, a.Nmax, bad);
     const int ctx = len.n - len.nt;
     const int raw = a.accepted_lens[b];
-    const int acc = raw < 0 ? 0 : (raw > len.nt ? len.nt : raw);
+    const int acc = min(max(raw, 0), len.nt);
     if (acc != raw)
         bad |= kFlagTreeOutOfRange;
-    if (g == 0 && l == 0 && tid == 0 && a.seq_lens_out)
-        a.seq_lens_out[b] = ctx + acc;
-    auto row_of = [&](int p) -> long long {   // -1: no such page
+    if (tid == 0) {
+        sm_behind = sm_moves = 0;
+        if (blockIdx.x == 0 && a.seq_lens_out)
+            a.seq_lens_out[b] = ctx + acc;
+    }
+    __syncthreads();
+    auto row_of = [&](int p) -> long long {   // of KV head 0; -1: no such page
         long long page = b;
         int r = p;
         if (a.table) {
             page = a.table[(size_t)b * a.max_blocks + p / a.page_size];
             r = p % a.page_size;
         }
-        if (page < 0 || page >= a.num_pages)
-            return -1;
-        return ((page * a.Hkv + g) * a.page_size + r) * kHeadDim;
+        return page < 0 || page >= a.num_pages ? -1 : page * a.Hkv * a.page_size + r;
     };
-    constexpr int kPer = TD_MAX_TREE * kRowChunks / kCommitThreads;
-    uint4 kr[kPer], vr[kPer];
-    long long to[kPer];
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-        const int e = tid + u * kCommitThreads;
-        const int i = e / kRowChunks, c = e % kRowChunks;
-        to[u] = -1;
-        if (i < acc) {
-            const int j = a.accepted[(size_t)b * a.T + i];
-            if (j < 0 || j >= len.nt) {
-                bad |= kFlagTreeOutOfRange;
-                continue;
-            }
-            const long long src = row_of(ctx + j), dst = row_of(ctx + i);
-            if (src < 0 || dst < 0) {
+    for (int i = tid; i < acc; i += 32 * kCommitWarps) {
+        const int j = a.accepted[(size_t)b * a.T + i];
+        long long src = -1, dst = -1;
+        if (j < 0 || j >= len.nt) {
+            bad |= kFlagTreeOutOfRange;
+        } else {
+            src = row_of(ctx + j);
+            dst = row_of(ctx + i);
+            if (src < 0 || dst < 0)
                 bad |= kFlagPageOutOfRange;
-                continue;
-            }
-            if (j == i)
-                continue;
-            kr[u] = *reinterpret_cast<const uint4 *>(a.k[l] + src + c * 8);
-            vr[u] = *reinterpret_cast<const uint4 *>(a.v[l] + src + c * 8);
-            to[u] = dst + c * 8;
+            if (j == i || src < 0 || dst < 0)
+                dst = -1;
+            else if (j < i)
+                sm_behind = 1;
         }
+        sm_src[i] = src;
+        sm_dst[i] = dst;
+        if (dst >= 0)
+            sm_moves = 1;
     }
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kPer; ++u)
-        if (to[u] >= 0) {
-            *reinterpret_cast<uint4 *>(a.k[l] + to[u]) = kr[u];
-            *reinterpret_cast<uint4 *>(a.v[l] + to[u]) = vr[u];
-        }
-    if (bad)
+    if (bad && blockIdx.x == 0)
         atomicOr(a.status, bad);
+    if (!sm_moves)
+        return;
+    const int hi = lane >> 4, c = lane & 15;
+    const int task0 = (blockIdx.x * kCommitWarps + warp) * per_warp;
+    const bool in_order = !sm_behind;
+    // task: layer, then K or V, then head (neighbouring warps read neighbouring rows)
+    auto rows_of = [&](int task, int c) {
+        const int g = task % a.Hkv, kv = task / a.Hkv & 1, l = task / a.Hkv >> 1;
+        return (kv ? a.v[l] : a.k[l]) + (size_t)g * a.page_size * kHeadDim + c * 8;
+    };
+    if (in_order) {
+        for (int task = task0; task < min(task0 + per_warp, tasks); ++task) {
+            uint16_t *rows = rows_of(task, c);
+#pragma unroll 1
+            for (int i0 = 0; i0 < acc; i0 += kCommitRows) {
+                uint4 x[kCommitRows / 2];
+#pragma unroll
+                for (int u = 0; u < kCommitRows / 2; ++u) {
+                    const int i = i0 + 2 * u + hi;
+                    if (i < acc && sm_dst[i] >= 0)
+                        x[u] = *reinterpret_cast<const uint4 *>(rows + sm_src[i] * kHeadDim);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < kCommitRows / 2; ++u) {
+                    const int i = i0 + 2 * u + hi;
+                    if (i < acc && sm_dst[i] >= 0)
+                        *reinterpret_cast<uint4 *>(rows + sm_dst[i] * kHeadDim) = x[u];
+                }
+                __syncwarp();
+            }
+        }
+        return;
+    }
+    const int first = blockIdx.x * kCommitWarps * per_warp;
+    constexpr int kHold = TD_MAX_TREE / (2 * kCommitWarps);
+    for (int task = first; task < min(first + kCommitWarps * per_warp, tasks); ++task) {
+        uint16_t *rows = rows_of(task, c);
+        uint4 x[kHold];
+#pragma unroll
+        for (int u = 0; u < kHold; ++u) {
+            const int i = 2 * (u * kCommitWarps + warp) + hi;
+            if (i < acc && sm_dst[i] >= 0)
+                x[u] = *reinterpret_cast<const uint4 *>(rows + sm_src[i] * kHeadDim);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kHold; ++u) {
+            const int i = 2 * (u * kCommitWarps + warp) + hi;
+            if (i < acc && sm_dst[i] >= 0)
+                *reinterpret_cast<uint4 *>(rows + sm_dst[i] * kHeadDim) = x[u];
+        }
+        __syncthreads();
+    }
 }
 
 }  // namespace
@@ -311,9 +420,20 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
 cudaError_t launch_block_tables(const TablesArgs &a, cudaStream_t stream)
 {
     block_tables_kernel<<<1, kTableThreads, 0, stream>>>(a);
-    if (a.max_new > 0)
-        slot_map_kernel<<<(a.max_new + kSlotThreads - 1) / kSlotThreads, kSlotThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess || a.max_new == 0 || (a.B <= kTableThreads && a.max_new <= kOwnSlots))
+        return err;
+    constexpr int kPer = kSlotThreads * kSlotsPerThread;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)a.max_new + kPer - 1) / kPer));
+    cfg.blockDim = dim3(kSlotThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, slot_map_kernel, a);
 }
 
 cudaError_t launch_append_slots(const AppendSlotsArgs &a, cudaStream_t stream)
@@ -329,7 +449,12 @@ cudaError_t launch_append_slots(const AppendSlotsArgs &a, cudaStream_t stream)
 
 cudaError_t launch_tree_commit(const CommitArgs &a, int num_layers, cudaStream_t stream)
 {
-    tree_commit_kernel<<<dim3(a.Hkv, a.B, num_layers), kCommitThreads, 0, stream>>>(a);
+    const int tasks = num_layers * 2 * a.Hkv;
+    const long long fill = (long long)host_sm_count() * 2 * kCommitWarps;   // two CTAs per SM
+    int per_warp = (int)((long long)tasks * a.B / fill);
+    per_warp = per_warp < 1 ? 1 : per_warp > kCommitTasks ? kCommitTasks : per_warp;
+    const int per = kCommitWarps * per_warp;
+    tree_commit_kernel<<<dim3((tasks + per - 1) / per, a.B), 32 * kCommitWarps, 0, stream>>>(a, tasks, per_warp);
     return cudaGetLastError();
 }
 

@@ -266,7 +266,8 @@ td_status td_block_tables(int32_t batch, int32_t page_size, int32_t max_blocks, 
 {
     if (batch < 1 || page_size < 1 || max_blocks < 1 || num_pages < 1 || max_new < 0)
         return TD_ERR_INVALID_ARG;
-    if (batch > 65535 || (int64_t)max_blocks * page_size >= (int64_t(1) << 31) ||
+    if (batch > 65535 || (int64_t)batch * max_blocks >= (int64_t(1) << 31) ||
+        (int64_t)max_blocks * page_size >= (int64_t(1) << 31) ||
         (int64_t)num_pages * page_size >= (int64_t(1) << 31))
         return TD_ERR_UNSUPPORTED_SHAPE;
     if (!i32(seq_lens) || !i32(new_lens) || !i32(block_table) || !i32(num_blocks) ||

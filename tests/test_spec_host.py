@@ -156,6 +156,7 @@ def test_block_tables_refusals(L):
     assert tables(L, B=65536) == UNSUPPORTED
     assert tables(L, blocks=1 << 27) == UNSUPPORTED
     assert tables(L, pages=1 << 27) == UNSUPPORTED
+    assert tables(L, B=65535, blocks=1 << 16) == UNSUPPORTED
     for name in ("seq", "new", "table", "held", "held_out", "free", "count", "count_out", "cu",
                  "slots", "ws"):
         assert tables(L, **{name: None}) == INVALID
