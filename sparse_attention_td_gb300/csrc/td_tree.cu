@@ -35,10 +35,13 @@ constexpr int kMaskRing = 8;                     // tiles whose validity masks a
 constexpr long long kTreeWaitCycles = 2000000000ll;  // a wait gives up after about 1 s
 
 // MT row tiles per CTA.  Shared memory: Q row tiles, then the ring of K and V
-// tiles.  The softmax works in steps of kStep tokens; each row tile has two S
-// buffers, so S of the next step is there when a step's softmax ends.  Tensor
-// memory (512 columns of 32 bits): S buffers (P overwrites the upper half of
-// its S) in columns 0 .. 255, then the O tiles.
+// tiles.  The softmax works in steps of kStep tokens.  Tensor memory (512 columns
+// of 32 bits): in columns 0 .. 255 S and P, then the O tiles.  One row tile: two S
+// buffers of 128 columns, P over the upper half of its S, so S of the next step is
+// there when a step's softmax ends.  Two row tiles, 128 columns each: one S of 64
+// columns, which is free again as soon as the softmax has its values in registers,
+// and two P buffers.  (Two S buffers with P over them, S of a step waiting for P V
+// of the one before the last: 136 us instead of 129 for 4 x 32K tokens, 64 nodes.)
 template <int MT> struct Cfg {
     static constexpr int kSlots = MT == 1 ? 6 : 5;
     static constexpr int kStep = MT == 1 ? 128 : 64;
@@ -48,18 +51,26 @@ template <int MT> struct Cfg {
     // Copy warps in the third and fourth sub-partition (warp % 4): their queue of
     // copies slows the other warps there, and the first two have the first 64 rows.
     static constexpr int kLoader = kSoftWarps, kIssuer = kSoftWarps + 1;
-    static constexpr int kFinder = kSoftWarps + 4, kFinders = 2, kCopiers = 4;
+    // An issuer per row tile, in sub-partitions of their own: both in one slowed its
+    // softmax warps to 2300 cycles a step, and with them the row tiles.
+    static constexpr int kIssuer1 = kSoftWarps + 7;
+    static constexpr int kFinder = kSoftWarps + 4, kFinders = MT == 1 ? 2 : 1, kCopiers = 4;
     static constexpr int kRowRing = 4;                // tiles whose row lists are alive
     static constexpr int kThreads = 32 * (kSoftWarps + 8);
     // number of a copy warp, or -1
     __device__ static int copier(int warp)
     {
         const int w = warp - kSoftWarps;
+        if (MT > 1 && w >= 5)
+            return w == 7 ? -1 : w == 6 ? 2 : 3;
         return w < 0 || (w & 2) == 0 ? -1 : (w & 1) + (w >> 2) * 2;
     }
     static constexpr size_t kSmem = (size_t)(MT + kSlots) * kTileBytes + 3072;
-    __device__ static constexpr uint32_t col_s(int m, int buf) { return m * 2 * kStep + buf * kStep; }
-    __device__ static constexpr uint32_t col_p(int m, int buf) { return col_s(m, buf) + kStep / 2; }
+    // of step number g of a row tile: S and P columns, phase of the S barrier
+    __device__ static uint32_t col_s(int m, uint32_t g) { return m * 128 + (MT == 1 ? (g & 1) * 128 : 0); }
+    __device__ static uint32_t col_p(int m, uint32_t g) { return m * 128 + 64 + (g & 1) * (MT == 1 ? 128 : 32); }
+    __device__ static int buf_s(uint32_t g) { return MT == 1 ? g & 1 : 0; }
+    __device__ static uint32_t phase_s(uint32_t g) { return MT == 1 ? g >> 1 : g; }
     __device__ static constexpr uint32_t col_o(int m) { return 256 + m * kTile; }
 };
 constexpr uint32_t kTmemCols = 512;
@@ -365,7 +376,8 @@ template <int MT> struct Extra {
     uint64_t s[MT][2], p[MT][2], o[MT];           // S there, P there, P V done
     uint64_t rows_there[C::kRowRing], rows_read[C::kRowRing];   // a tile's row list: written, read
     uint64_t go[C::kRowRing][2];                  // the tile's K / V rows may be copied
-    uint64_t scan, drain;
+    uint64_t s_read[MT];                          // two row tiles: S is in registers
+    uint64_t scan, clear, drain;
     int rows[C::kRowRing][kTile];                 // cache rows of a tile's tokens, -1: none
     uint32_t rows_valid[C::kRowRing][4];          // which tokens have one
     uint32_t valid[kMaskRing][4];                 // tokens of a tile that exist
@@ -419,11 +431,11 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             x.start.left = 0;
             for (int i = 0; i < C::kSlots; ++i) {
                 bar_init(&x.full[i], 32 * C::kCopiers);
-                bar_init(&x.empty[i], 1);
+                bar_init(&x.empty[i], MT);
             }
             for (int i = 0; i < 2; ++i) {
                 bar_init(&x.q[i], 32 * C::kCopiers);
-                bar_init(&x.q_free[i], 1);
+                bar_init(&x.q_free[i], MT);
             }
             for (int i = 0; i < MT; ++i) {
                 for (int k = 0; k < 2; ++k) {
@@ -431,6 +443,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     bar_init(&x.p[i][k], 4);
                 }
                 bar_init(&x.o[i], 1);
+                bar_init(&x.s_read[i], 4);
             }
             for (int i = 0; i < C::kRowRing; ++i) {
                 bar_init(&x.rows_there[i], 1);
@@ -439,7 +452,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 bar_init(&x.rows_read[i], C::kCopiers);
             }
             bar_init(&x.scan, 4);
-            bar_init(&x.drain, 1);
+            bar_init(&x.clear, 4);
+            bar_init(&x.drain, MT);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         if (bad && blockIdx.x == 0)
@@ -512,7 +526,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     const bool two_q = MT == 1 && a.part_rows <= 64;
     uint32_t loaded = 0;          // loader: ring entries begun
     uint32_t tmem = 0;
-    if (warp < C::kSoftWarps || warp == C::kIssuer) {
+    const bool issuer = warp == C::kIssuer || (MT > 1 && warp == C::kIssuer1);
+    if (warp < C::kSoftWarps || issuer) {
         // tensor memory for the roles that use it, while the others begin
         if (warp == C::kIssuer) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -522,7 +537,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
         tmem_before();
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * (C::kSoftWarps + 1)) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * (C::kSoftWarps + MT)) : "memory");
         tmem_after();
         tmem = x.tmem;
     }
@@ -653,7 +668,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         }
         if (flags && lane == 0)
             atomicOr(a.status, flags);
-    } else if (warp == C::kFinder || warp == C::kFinder + 1) {
+    } else if (warp >= C::kFinder && warp < C::kFinder + C::kFinders) {
         // ---- finders: the cache rows of every kFinders-th tile for the copy warps, as
         // far ahead as there are lists.  (Memory is slow to answer while every SM's
         // ring fills: found by the copy warps themselves, between two tiles, the rows
@@ -792,18 +807,22 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             e += 2 * n;
             walk.next(n);
         }
-    } else if (warp == C::kIssuer) {
-        // ---- MMA issue, by one thread: S of step j + 1 before P V of step j, so
-        // the tensor cores work while the softmax does.
+    } else if (issuer) {
+        // ---- MMA issue of one row tile, by one thread: S of step j + 1 before P V of
+        // step j, so the tensor cores work while the softmax does.
         if (elect_one()) {
+            const int m = warp == C::kIssuer ? 0 : 1;
             uint32_t e = 0;              // ring entry of the segment's first K tile
-            uint32_t steps[MT] = {};     // steps of earlier segments, per row tile
+            uint32_t steps = 0;          // steps of earlier segments
             uint32_t seg = 0;            // segments begun
             bool ok = true;
-            auto wait_full = [&](uint32_t entry) {
+            // Rows copied by cp.async are read by the MMA through the async proxy.  (The
+            // fence is not cheap: boxes come through that proxy and go without.)
+            auto proxy_fence = [] { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); };
+            auto wait_full = [&](uint32_t entry, bool copied) {
                 ok = ok && bar_wait(&x.full[entry % C::kSlots], (entry / C::kSlots) & 1, gave_up);
-                // rows copied by cp.async are read by the MMA through the async proxy
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (copied)
+                    proxy_fence();
                 return ok;
             };
             auto wait_bar = [&](uint64_t *bar, uint32_t phase) {
@@ -811,76 +830,75 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 tmem_after();
                 return ok;
             };
-            while (ok && walk.left > 0) {
-                const int n = walk.count() * C::kSteps;
-                const int nm = MT == 1 ? 1 : (walk.rows() + kTile - 1) / kTile;
+            for (; ok && walk.left > 0; ++seg) {
+                const int tiles = walk.count(), n = tiles * C::kSteps;
+                if (MT > 1 && m * kTile >= walk.rows()) {
+                    // no rows here: the slots are free as far as this row tile goes
+                    for (int i = 0; ok && i < 2 * tiles; ++i)
+                        if (wait_full(e + i, false))
+                            bar_arrive(&x.empty[(e + i) % C::kSlots]);
+                    if (ok)
+                        bar_arrive(&x.q_free[seg & 1]);
+                    e += 2 * tiles;
+                    walk.next(tiles);
+                    continue;
+                }
+                const uint32_t q = operand(sm_q + m * kTileBytes + (two_q ? seg & 1 : 0) * 64 * 128, 16);
                 auto issue_s = [&](int j) {
                     const uint32_t entry = e + 2 * (j / C::kSteps);
                     const uint32_t k = operand(sm_ring + entry % C::kSlots * kTileBytes, 16) +
                                        (j % C::kSteps * C::kStep * 128 >> 4);
+                    const uint32_t g = steps + j;
+                    if (MT > 1 && j >= 1)       // the softmax has read the step before
+                        wait_bar(&x.s_read[m], g - 1);
+                    if (MT == 1 && j >= 2)      // P V of step j - 2 has read this buffer's P
+                        wait_bar(&x.o[m], g - 2);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (m >= nm)
-                            break;
-                        const uint32_t q = operand(sm_q + m * kTileBytes + (two_q ? seg & 1 : 0) * 64 * 128, 16);
-                        const int buf = (steps[m] + j) & 1;
-                        if (j >= 2)     // P V of step j - 2 has read this buffer's P
-                            wait_bar(&x.o[m], steps[m] + j - 2);
-#pragma unroll
-                        for (int s = 0; s < 8; ++s) {
-                            const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
-                            mma_ss<C::kStep>(tmem + C::col_s(m, buf), q + (o >> 4), k + (o >> 4), s > 0);
-                        }
-                        mma_commit(&x.s[m][buf]);
+                    for (int s = 0; s < 8; ++s) {
+                        const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
+                        mma_ss<C::kStep>(tmem + C::col_s(m, g), q + (o >> 4), k + (o >> 4), s > 0);
                     }
+                    mma_commit(&x.s[m][C::buf_s(g)]);
                     if (j % C::kSteps == C::kSteps - 1)
                         mma_commit(&x.empty[entry % C::kSlots]);
                     if (j == n - 1)
                         mma_commit(&x.q_free[seg & 1]);   // the segment's Q has been read
                 };
+                const int boxes = boxes_of(walk.w) - walk.t;     // tiles before this one are boxes
                 wait_bar(&x.q[seg & 1], seg >> 1);
-                if (!wait_full(e))     // (its proxy fence covers Q, too)
+                proxy_fence();
+                if (!wait_full(e, boxes <= 0))
                     break;
                 issue_s(0);
                 for (int j = 0; j < n; ++j) {
                     if (j + 1 < n) {
-                        if ((j + 1) % C::kSteps == 0 && !wait_full(e + 2 * ((j + 1) / C::kSteps)))
+                        if ((j + 1) % C::kSteps == 0 &&
+                            !wait_full(e + 2 * ((j + 1) / C::kSteps), (j + 1) / C::kSteps >= boxes))
                             break;
                         issue_s(j + 1);
                     }
                     const uint32_t entry = e + 2 * (j / C::kSteps) + 1;
-                    if (j % C::kSteps == 0 && !wait_full(entry))
+                    if (j % C::kSteps == 0 && !wait_full(entry, j / C::kSteps >= boxes))
                         break;
                     const uint32_t v = operand(sm_ring + entry % C::kSlots * kTileBytes, kHalfBytes) +
                                        (j % C::kSteps * C::kStep * 128 >> 4);
                     // tokens by 16, as far as the tile has any
                     const int tokens = walk.w.tokens(walk.t + j / C::kSteps) - j % C::kSteps * C::kStep;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (m >= nm)
-                            break;
-                        const uint32_t g = steps[m] + j;
-                        if (!wait_bar(&x.p[m][g & 1], g >> 1))
-                            break;
-#pragma unroll
-                        for (int s = 0; s < C::kStep / 16; ++s)
-                            if (s * 16 < tokens)
-                                mma_ts(tmem + C::col_o(m), tmem + C::col_p(m, g & 1) + s * 8,
-                                       v + (s * 16 * 128 >> 4), j > 0 || s > 0);
-                        mma_commit(&x.o[m]);
-                    }
-                    if (!ok)
+                    const uint32_t g = steps + j;
+                    if (!wait_bar(&x.p[m][g & 1], g >> 1))
                         break;
+#pragma unroll
+                    for (int s = 0; s < C::kStep / 16; ++s)
+                        if (s * 16 < tokens)
+                            mma_ts(tmem + C::col_o(m), tmem + C::col_p(m, g) + s * 8,
+                                   v + (s * 16 * 128 >> 4), j > 0 || s > 0);
+                    mma_commit(&x.o[m]);
                     if (j % C::kSteps == C::kSteps - 1)
                         mma_commit(&x.empty[entry % C::kSlots]);
                 }
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    if (m < nm)
-                        steps[m] += n;
-                ++seg;
-                e += 2 * (n / C::kSteps);
-                walk.next(n / C::kSteps);
+                steps += n;
+                e += 2 * tiles;
+                walk.next(tiles);
             }
         }
         __syncwarp();
@@ -939,7 +957,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             }
             for (int j = 0; j < n * C::kSteps; ++j, ++count) {
                 const int i = j / C::kSteps, part = j % C::kSteps;   // tile, step of the tile
-                const int buf = count & 1;
                 const bool tree = walk.t + i == walk.w.tiles - 1;
                 // P V of the step before is done.  Waited for in every step (it is, by
                 // the time the exponentials are), so no phase of bar_o is missed.
@@ -949,7 +966,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         ok = __all_sync(kFull, bar_wait(&x.o[m], (count - 1) & 1, gave_up));
                     waited = true;
                 };
-                ok = __all_sync(kFull, bar_wait(&x.s[m][buf], (count >> 1) & 1, gave_up));
+                ok = __all_sync(kFull, bar_wait(&x.s[m][C::buf_s(count)], C::phase_s(count) & 1, gave_up));
                 if (!ok)
                     break;
                 tmem_after();
@@ -979,10 +996,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     if (lane == 0)
                         x.badv[m][warp & 3] = bits;
                     if constexpr (MT > 1) {
-                        if (nm > 1 && m == 1 && lane == 0)
-                            bar_arrive(&x.scan);
-                        if (nm > 1 && m == 0) {
-                            ok = __all_sync(kFull, bar_wait(&x.scan, scans & 1, gave_up));
+                        if (nm > 1) {
+                            if (m == 1 && lane == 0)
+                                bar_arrive(&x.scan);
+                            ok = __all_sync(kFull, bar_wait(m == 0 ? &x.scan : &x.clear, scans & 1, gave_up));
                             if (!ok)
                                 break;
                             ++scans;
@@ -1005,8 +1022,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                             }
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
                     }
+                    __syncwarp();
+                    if (MT > 1 && nm > 1 && m == 0 && lane == 0)
+                        bar_arrive(&x.clear);
                 }
                 if (warp_live) {
                     // The row's scores pass through 64 registers, in blocks of 64
@@ -1016,7 +1035,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     // registers the roles' code no longer fitted the instruction
                     // cache (100K: 261 us against 314).
                     constexpr int kBlocks = C::kStep / 64;
-                    const uint32_t at = tmem + C::col_s(m, buf) + lanes;
+                    const uint32_t at = tmem + C::col_s(m, count) + lanes;
                     const uint32_t *valid = x.valid[(tile_no + i) % kMaskRing] + part * 2;
                     float s[64];
                     auto fetch = [&](int block) {
@@ -1046,6 +1065,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
 #pragma unroll 1
                     for (int block = 0; block < kBlocks; ++block) {
                         fetch(block);
+                        if constexpr (MT > 1) {
+                            tmem_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                bar_arrive(&x.s_read[m]);
+                        }
 #pragma unroll
                         for (int k = 0; k < 64; k += 2)
                             mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
@@ -1093,11 +1118,14 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                             sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                             p[k] = pack_bf16(e.x, e.y);
                         }
-                        // over scores of this or a later block, which have been read
-                        tmem_st32(at + C::kStep / 2 + 32 * block, p);
+                        // (one row tile: over scores of this or a later block, which have been
+                        // read; two: P V of the step before the last is done)
+                        tmem_st32(tmem + C::col_p(m, count) + lanes + 32 * block, p);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
+                } else if (MT > 1 && lane == 0) {
+                    bar_arrive(&x.s_read[m]);
                 }
                 o_done();
                 if (!ok)
@@ -1105,7 +1133,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 tmem_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(&x.p[m][buf]);
+                    bar_arrive(&x.p[m][count & 1]);
             }
             if (!ok)
                 break;
@@ -1193,7 +1221,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 own_limit = 0;
                 bar_wait(&x.full[e % C::kSlots], (e / C::kSlots) & 1, &own_limit, kTreeWaitCycles / 16);
             }
-        } else if (warp == C::kIssuer && lane == 0) {
+        } else if (issuer && elect_one()) {      // (the lane that issued them)
             mma_commit(&x.drain);
             bar_wait(&x.drain, 0, &own_limit, kTreeWaitCycles / 16);
         }
