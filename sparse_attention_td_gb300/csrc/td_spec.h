@@ -56,7 +56,8 @@ struct TreeArgs {
     float *part_o;              // [2 * ctas][part_rows][128]
     int B, T, W, Hq, Hkv, G, Nmax, top_k;
     int g_shift;                // log2(G)
-    int page_shift;             // log2(page_size), or -1
+    uint32_t page_magic;        // p / page_size = p * page_magic >> page_shift, 0 <= p < 2^31
+    int page_shift;
     int box_rows;               // 0: no boxes, every tile goes row by row
     int part_rows;
     float scale;                // softmax scale (natural-log units)

@@ -117,10 +117,14 @@ td_status run_tree(const td_shape *shape, const td_cache *cache, int32_t tree_si
     a.status = (uint32_t *)ws;
     a.G = shape->num_q_heads / shape->num_kv_heads;
     a.g_shift = a.G == 1 ? 0 : a.G == 2 ? 1 : a.G == 4 ? 2 : 3;
-    a.page_shift = -1;
-    for (int s = 0; s < 31; ++s)
-        if (cache->page_size == 1 << s)
-            a.page_shift = s;
+    {
+        const uint32_t d = (uint32_t)cache->page_size;
+        int s = 0;
+        while ((uint32_t(1) << s) < d)
+            ++s;
+        a.page_shift = 31 + s;
+        a.page_magic = (uint32_t)(((uint64_t(1) << (31 + s)) + d - 1) / d);
+    }
     a.part_rows = td::tree_part_rows(tree_size * a.G);
     const TreeWs w = tree_ws(*shape, tree_size);
     char *base = (char *)ws + (ws_bytes - (w.total - kAlign)) / kAlign * kAlign;

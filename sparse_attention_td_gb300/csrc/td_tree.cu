@@ -310,6 +310,30 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
+// Block of a request that position p >= 0 lies in: p / page_size by a product.
+__device__ __forceinline__ int block_of(const TreeArgs &a, int p)
+{
+    return (int)((uint64_t)(uint32_t)p * a.page_magic >> a.page_shift);
+}
+
+// What a drafted token's V values that are not finite add to 32 dims of the
+// output rows that see it (rare; kept out of the caller's code).
+__device__ __noinline__ void add_not_finite(const TreeArgs &a, int b, int h, int pos, int dim, uint32_t *o)
+{
+    int page = b, r = pos;
+    if (a.c.table) {
+        const int block = block_of(a, pos);
+        page = a.c.table[(size_t)b * a.c.max_blocks + block];
+        r = pos - block * a.c.page_size;
+    }
+    if (page < 0 || page >= a.c.num_pages)
+        return;
+    const uint16_t *v = a.c.v + (((size_t)page * a.Hkv + h) * a.c.page_size + r) * kHeadDim + dim;
+    for (int k = 0; k < 32; ++k)
+        if ((v[k] & 0x7f80) == 0x7f80)
+            o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float((uint32_t)v[k] << 16));
+}
+
 // ---- work: units (request, KV head, block of query rows), each a run of tiles
 // of 128 tokens: the context's (or the index set's), then the drafted tokens,
 // which share the last context tile where both fit.
@@ -549,15 +573,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     auto page_of = [&](int b, int p) {
         if (!a.c.table)
             return b;
-        const int block = a.page_shift >= 0 ? p >> a.page_shift : p / a.c.page_size;
-        return __ldg(a.c.table + (size_t)b * a.c.max_blocks + block);
+        return __ldg(a.c.table + (size_t)b * a.c.max_blocks + block_of(a, p));
     };
     auto row_of = [&](int h, int pos, int page) {       // -1: no such row
         if (pos < 0 || page < 0 || page >= a.c.num_pages)
             return -1;
-        const int in = !a.c.table          ? pos
-                       : a.page_shift >= 0 ? pos & (a.c.page_size - 1)
-                                           : pos % a.c.page_size;
+        const int in = a.c.table ? pos - block_of(a, pos) * a.c.page_size : pos;
         return (page * a.Hkv + h) * a.c.page_size + in;
     };
 
@@ -1163,21 +1184,14 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         for (int j = walk.w.off; j < walk.w.off + walk.w.nt; ++j) {
                             if (!((j < 64 ? (j < 32 ? bad[0] : bad[1]) : (j < 96 ? bad[2] : bad[3])) >> (j & 31) & 1u))
                                 continue;
-                            const int p = walk.w.ctx + j - walk.w.off;
-                            int page = b, rr = p;
-                            if (a.c.table) {
-                                page = a.c.table[(size_t)b * a.c.max_blocks + p / a.c.page_size];
-                                rr = p % a.c.page_size;
-                            }
-                            if (page < 0 || page >= a.c.num_pages)
-                                continue;
-                            const uint16_t *v =
-                                a.c.v + (((size_t)page * a.Hkv + h) * a.c.page_size + rr) * kHeadDim + 32 * c;
+                            uint32_t add[32];
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if ((v[k] & 0x7f80) == 0x7f80)
-                                    ov[k] = __float_as_uint(__uint_as_float(ov[k]) +
-                                                           __uint_as_float((uint32_t)v[k] << 16));
+                                add[k] = ov[k];
+                            add_not_finite(a, b, h, walk.w.ctx + j - walk.w.off, 32 * c, add);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                ov[k] = add[k];
                         }
                     }
                     if (live && whole) {

@@ -1,0 +1,132 @@
+"""Tree attention where its work is cut unevenly: many small requests, few long
+ones, several blocks of query rows, and drafted tokens around a tile's end."""
+import pytest
+import torch
+
+import sparse_attention_td_gb300 as td
+from spec_util import D
+from test_spec_gpu import _built, check_tree, run_tree, tree_case  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("k", [0, 20])
+def test_many_small_requests(page, k):
+    """More requests than threads in a block, many units per SM, some without work."""
+    gen = torch.Generator().manual_seed(page + k)
+    B = 700
+    lens = torch.randint(0, 60, (B,), generator=gen).tolist()
+    sizes = [min(n, int(s)) for n, s in zip(lens, torch.randint(0, 4, (B,), generator=gen))]
+    c = tree_case(page + k, 2, 1, lens, sizes, 3, page, "tree", k, max_len=64)
+    out, ws = run_tree(c)
+    check_tree(c, out)
+    assert ws.status() == 0
+
+
+@pytest.mark.parametrize("page", [0, 64])
+@pytest.mark.parametrize("G,T", [(1, 2), (8, 3), (8, 20)])
+def test_one_long_request_on_every_sm(page, G, T):
+    """One (request, KV head) in parts on all SMs."""
+    c = tree_case(G, G, 1, [40003], [T], T, page, "tree")
+    out, ws = run_tree(c)
+    check_tree(c, out)
+    assert ws.status() == 0
+    assert torch.equal(run_tree(c)[0], out)
+
+
+@pytest.mark.parametrize("ctx", [1, 63, 64, 65, 100, 120, 126, 127, 128, 129, 200, 256])
+@pytest.mark.parametrize("nt", [1, 2, 8, 28, 64, 65, 127, 128])
+def test_drafted_tokens_around_a_tiles_end(ctx, nt):
+    """Sharing the last context tile, just fitting it, or in one of their own."""
+    c = tree_case(ctx * 131 + nt, 1, 1, [ctx + nt], [nt], 128, 32, "random")
+    c["seen"][0, :, 0] = True
+    out, ws = run_tree(c)
+    check_tree(c, out)
+    assert ws.status() == 0
+
+
+@pytest.mark.parametrize("G,T", [(4, 64), (8, 64), (8, 128), (2, 100), (1, 128)])
+@pytest.mark.parametrize("page,k", [(0, 0), (16, 0), (128, 0), (0, 150), (16, 150)])
+def test_blocks_of_query_rows(G, T, page, k):
+    """Over 128 rows per KV head: two row tiles per block, up to four blocks; requests whose
+    trees fill one row tile only lie between them."""
+    lens = [T + 400, 5, T + 131, 40, T + 7]
+    sizes = [T, 3, T - 1, min(T, 17), T // 2 + 1]
+    c = tree_case(G * T + page + k, G, 1, lens, sizes, T, page, "tree", k)
+    out, ws = run_tree(c)
+    check_tree(c, out)
+    assert ws.status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("ctx", [0, 70, 256])
+def test_non_finite_values_with_two_row_tiles(bad, ctx):
+    T, G = 50, 4
+    c = tree_case(ctx, G, 1, [ctx + T, ctx + T], [T, T], T, 0, "random")
+    c["seen"][0, :, 7] = False
+    c["seen"][0, (3, 40), 7] = True            # a row of each row tile sees the token
+    cc = dict(c, V=c["V"].clone())
+    cc["V"][0, 0, ctx + 7, 100] = bad
+    cc["vc"] = cc["V"]
+    out, ws = run_tree(cc)
+    clean, _ = run_tree(c)
+    check_tree(c, clean)
+    got = out.cpu()
+    for t in (3, 40):
+        assert not torch.isfinite(got[0, t, :, 100]).any()
+        other = [d for d in range(D) if d != 100]
+        assert torch.equal(got[0, t][:, other], clean[0, t].cpu()[:, other])
+    rows = [t for t in range(T) if t not in (3, 40)]
+    assert torch.equal(got[0, rows], clean[0, rows].cpu()) and torch.equal(got[1], clean[1].cpu())
+    assert ws.status() == 0
+
+
+@pytest.mark.parametrize("page", [16, 24])
+def test_bad_pages_of_a_sparse_layer(page):
+    """Index entries on a page outside the cache count as absent."""
+    c = tree_case(5, 4, 2, [300, 200], [6, 6], 6, page, "chain", 40)
+    c["table"][0, 3] = -4
+    out, ws = run_tree(c)
+    assert ws.status() == td.FLAG_PAGE_OUT_OF_RANGE
+    gone = dict(c, idx=c["idx"].clone())
+    hit = (gone["idx"][0] >= 3 * page) & (gone["idx"][0] < 4 * page)
+    gone["idx"][0][hit] = -1
+    assert hit.any()
+    check_tree(gone, out)
+
+
+def test_two_captured_graphs_share_a_workspace():
+    """Replayed one after the other on one stream, in any order."""
+    a = tree_case(1, 4, 2, [3000, 1500], [8, 5], 8, 16, "tree")
+    b = tree_case(2, 4, 2, [700, 2600], [40, 33], 40, 0, "tree", 300)
+    from test_spec_gpu import i32
+    from spec_util import pack_mask
+    shape = [td.make_shape(2, 8, 2, c["N"]) for c in (a, b)]
+    big = max(shape, key=lambda s: td.td_tree_workspace_size(s, 40))
+    ws = td.Workspace(big, 0, tree_size=40)
+    graphs, outs, keep = [], [], []
+    for c, s in zip((a, b), shape):
+        table = None if c["table"] is None else c["table"].cuda()
+        x = dict(cache=td.make_cache(c["kc"].cuda(), c["vc"].cuda(), table), q=c["q"].cuda(),
+                 mask=pack_mask(c["seen"]).cuda(), lens=i32(c["lens"]), sizes=i32(c["sizes"]),
+                 idx=None if c["idx"] is None else c["idx"].cuda())
+        x["out"] = torch.full_like(x["q"], 7.0)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if x["idx"] is None:
+                td.td_tree_attn(s, x["cache"], c["T"], x["sizes"], x["mask"], x["q"], x["lens"], x["out"], ws)
+            else:
+                td.td_tree_sparse_attn(s, x["cache"], c["T"], x["sizes"], x["mask"], x["q"], x["lens"],
+                                       x["idx"], c["idx"].shape[-1], x["out"], ws)
+        graphs.append(g), outs.append(x["out"]), keep.append(x)
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1, 0)):
+        for o in outs:
+            o.fill_(7.0)
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        check_tree(a, outs[0])
+        check_tree(b, outs[1])
+    assert ws.status() == 0
