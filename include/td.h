@@ -620,14 +620,18 @@ td_status td_probe_layer_reads(const td_shape *shape, const void *k_cache, const
  *          streamed); 0 one contiguous chunk each; negative restores the
  *          default
  *   "wait_limit_us": microseconds after which a staged full-layer CTA stops
- *          waiting for a bulk copy (default 1 s).  A CTA that gives up waits
+ *          waiting for a bulk copy, or a tree-attention CTA for its copies and
+ *          products (default 1 s; a tree-attention CTA that gives up waits, with
+ *          limits, for what it has in flight, sets TD_FLAG_WAIT_TIMEOUT and leaves:
+ *          its rows are not valid, the next launch is not affected).  A CTA that gives up waits
  *          (at the default limit) for every copy it issued, then joins the
  *          split merge with an empty partial and sets TD_FLAG_WAIT_TIMEOUT:
  *          the layer's output lacks that CTA's tokens and the workspace stays
  *          consistent for the next launch
  *   "wait_test": 1 makes the first stage wait of every staged full-layer CTA
  *          poll a barrier that nothing arrives on, so it runs out after
- *          "wait_limit_us" (tests of the failure report; no fault, no hang);
+ *          "wait_limit_us" (tests of the failure report; no fault, no hang); the
+ *          tree attention's softmax likewise;
  *          0 (default) in normal use
  * Otherwise value <= 0 restores the default.  Unknown key -> TD_ERR_INVALID_ARG.
  */

@@ -61,6 +61,8 @@ struct TreeArgs {
     int box_rows;               // 0: no boxes, every tile goes row by row
     int part_rows;
     float scale;                // softmax scale (natural-log units)
+    long long wait_cycles;      // SM clock cycles before a wait gives up
+    int wait_test;              // the softmax waits for what nothing arrives on (tests); 0 in normal use
 };
 // Rows one work unit of a launch with T * G query rows per KV head can have.
 inline int tree_part_rows(int rows) { return rows <= 128 ? rows : 256; }
@@ -122,6 +124,9 @@ __device__ __forceinline__ TreeLens tree_lens_of(const int32_t *seq_lens, const 
 td_status host_check_shape(const td_shape *s);
 float host_scale(const td_shape &s);
 int host_sm_count();
+// The tuning keys "wait_limit_us" (1 s by default) and "wait_test".
+int host_wait_limit_us();
+bool host_wait_test();
 // Tensor map over `rows` rows of 128 bf16 values: boxes of 64 values x box_rows
 // rows, 128-byte swizzle, zero fill past the end.
 bool host_box_map(TmaDesc *out, const void *base, long rows, int box_rows);

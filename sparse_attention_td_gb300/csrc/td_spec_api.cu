@@ -146,6 +146,8 @@ td_status run_tree(const td_shape *shape, const td_cache *cache, int32_t tree_si
     a.Nmax = shape->max_seq_len;
     a.top_k = top_k;
     a.scale = td::host_scale(*shape);
+    a.wait_cycles = td::host_wait_limit_us() * 2000ll;      // of about 2 GHz
+    a.wait_test = td::host_wait_test();
     return td::launch_tree_attention(a, td::host_sm_count(), (cudaStream_t)stream) == cudaSuccess ? TD_OK : TD_ERR_CUDA;
 }
 

@@ -32,7 +32,6 @@ constexpr int kTile = 128;                       // tokens per tile, and query r
 constexpr int kHalfBytes = kTile * 128;          // one 64-value half of a tile's rows
 constexpr int kTileBytes = 2 * kHalfBytes;       // 128 rows of 128 bf16 values
 constexpr int kMaskRing = 8;                     // tiles whose validity masks are alive (see producer)
-constexpr long long kTreeWaitCycles = 2000000000ll;  // a wait gives up after about 1 s
 
 // MT row tiles per CTA.  Shared memory: Q row tiles, then the ring of K and V
 // tiles.  The softmax works in steps of kStep tokens.  Tensor memory (512 columns
@@ -111,10 +110,10 @@ __device__ __forceinline__ void bar_expect(uint64_t *bar, unsigned bytes)
                  : "memory");
 }
 
-// Waits for the phase of the given parity.  Gives up after kTreeWaitCycles, or
-// when another role has (then the CTA leaves as a whole and reports the timeout).
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, unsigned parity, volatile int *gave_up,
-                                         long long limit = kTreeWaitCycles)
+// Waits for the phase of the given parity.  Gives up after `limit` cycles of the SM
+// clock, or when another role has (then the CTA leaves as a whole and reports the
+// timeout).
+__device__ __forceinline__ bool bar_wait_for(uint64_t *bar, unsigned parity, volatile int *gave_up, long long limit)
 {
     const uint32_t addr = smem_of(bar);
     long long t0 = 0;
@@ -402,6 +401,7 @@ template <int MT> struct Extra {
     uint64_t go[C::kRowRing][2];                  // the tile's K / V rows may be copied
     uint64_t s_read[MT];                          // two row tiles: S is in registers
     uint64_t scan, clear, drain;
+    uint64_t never;                               // nothing arrives (tests of the failure report)
     int rows[C::kRowRing][kTile];                 // cache rows of a tile's tokens, -1: none
     uint32_t rows_valid[C::kRowRing][4];          // which tokens have one
     uint32_t valid[kMaskRing][4];                 // tokens of a tile that exist
@@ -425,6 +425,9 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     Extra<MT> &x = *reinterpret_cast<Extra<MT> *>(sm_raw + (MT + C::kSlots) * kTileBytes);
     static_assert((MT + C::kSlots) * kTileBytes + sizeof(Extra<MT>) <= C::kSmem, "shared memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar_wait = [&](uint64_t *bar, unsigned parity, volatile int *up) {
+        return bar_wait_for(bar, parity, up, a.wait_cycles);
+    };
     const uint32_t sm_q = smem_of(sm_raw);        // 1024-byte aligned: nothing static lies before it
     const uint32_t sm_ring = sm_q + MT * kTileBytes;
     volatile int *gave_up = &x.gave_up;
@@ -478,6 +481,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             bar_init(&x.scan, 4);
             bar_init(&x.clear, 4);
             bar_init(&x.drain, MT);
+            bar_init(&x.never, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         if (bad && blockIdx.x == 0)
@@ -549,6 +553,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     // the rows that are not Q's end in S and O rows that nobody reads.)
     const bool two_q = MT == 1 && a.part_rows <= 64;
     uint32_t loaded = 0;          // loader: ring entries begun
+    uint32_t loaded_boxes = 0;    // which of the last ones came as boxes (bit 0: the last)
     uint32_t tmem = 0;
     const bool issuer = warp == C::kIssuer || (MT > 1 && warp == C::kIssuer1);
     if (warp < C::kSoftWarps || issuer) {
@@ -648,6 +653,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         x.valid[tile_no % kMaskRing][lane] = word;
                     __syncwarp();
                     loaded = e + 1;
+                    loaded_boxes = loaded_boxes << 1 | (box && !alone ? 1u : 0u);
                     const uint32_t dst = sm_ring + slot * kTileBytes;
                     if (!box) {
                         if (lane == 0)
@@ -987,7 +993,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         ok = __all_sync(kFull, bar_wait(&x.o[m], (count - 1) & 1, gave_up));
                     waited = true;
                 };
-                ok = __all_sync(kFull, bar_wait(&x.s[m][C::buf_s(count)], C::phase_s(count) & 1, gave_up));
+                ok = __all_sync(kFull, a.wait_test ? bar_wait(&x.never, 0, gave_up)
+                                                   : bar_wait(&x.s[m][C::buf_s(count)], C::phase_s(count) & 1, gave_up));
                 if (!ok)
                     break;
                 tmem_after();
@@ -1226,18 +1233,20 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     tmem_before();
     __syncthreads();
     if (x.gave_up) {
-        // A wait gave up: leave no copy and no MMA in flight.  The ring's last
-        // entries are the ones that can be; each wait has a limit of its own.
+        // A wait gave up: leave no copy and no MMA in flight.  Of the boxes the ring's
+        // last entries can be; what was issued does complete, and these waits have
+        // the default limit.
+        constexpr long long kLimit = 2000000000ll;
         int own_limit = 0;
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (warp == C::kLoader) {
             for (uint32_t e = loaded > C::kSlots ? loaded - C::kSlots : 0; e < loaded; ++e) {
-                own_limit = 0;
-                bar_wait(&x.full[e % C::kSlots], (e / C::kSlots) & 1, &own_limit, kTreeWaitCycles / 16);
+                if (loaded_boxes >> (loaded - 1 - e) & 1)
+                    bar_wait_for(&x.full[e % C::kSlots], (e / C::kSlots) & 1, &own_limit, kLimit);
             }
         } else if (issuer && elect_one()) {      // (the lane that issued them)
             mma_commit(&x.drain);
-            bar_wait(&x.drain, 0, &own_limit, kTreeWaitCycles / 16);
+            bar_wait_for(&x.drain, 0, &own_limit, kLimit);
         }
         __syncthreads();
     }
