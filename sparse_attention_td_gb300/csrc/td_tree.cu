@@ -11,10 +11,23 @@
 //
 // All n * G query rows of a (request, KV head) share its K/V rows, so they are
 // the M side of two matrix products per tile of 128 tokens: S = Q K^T and
-// O += P V, on the tensor cores (tcgen05.mma, 128 x 128 tiles; S, P and O in
-// tensor memory, K and V tiles in shared memory).  A K/V byte then takes part
-// in up to 128 (one row tile) or 256 (two) multiply-adds, and the layer is
-// bound by reading the cache.
+// O += P V, on the tensor cores (tcgen05.mma, 128 query rows; S, P and O in
+// tensor memory, K and V tiles in shared memory).  P is rounded to bf16, the
+// products' operand type (relative error 2^-9, as the value rows carry already);
+// S, O, m and l are fp32.
+//
+// What bounds it, measured on GB300 (a copy of the same bytes runs at 6.7 TB/s):
+//   reading the cache once, where a KV head has at most 128 query rows:
+//     32 requests of 8K-16K, 8 KV heads, G = 4, 16 nodes, 64-token pages: 248 us, 6.6 TB/s
+//     one request of 100K, 32 KV heads, G = 1, 32 nodes:                  242 us, 6.9 TB/s
+//   the softmax, where it has more (two row tiles):
+//     4 x 32K, 8 KV heads, G = 4, 64 nodes:            129 us, 4.1 TB/s, 1.0 PFLOP/s
+//   launch, first loads and the join, where a step is short:
+//     4 x 257-2050, 8 KV heads, G = 8, one node, 16-token pages:  16 us
+//     4 x 32K, G = 4, 2048 index entries, 5 nodes:                18 us
+//     (the two launches alone, every CTA leaving at once:         4.5 us)
+//   copies of single rows, where an index set names them:
+//     32 requests, G = 4, 1024 index entries, 16 nodes:  45 to 49 us, 3.1 TB/s
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -64,7 +77,7 @@ template <int MT> struct Cfg {
             return w == 7 ? -1 : w == 6 ? 2 : 3;
         return w < 0 || (w & 2) == 0 ? -1 : (w & 1) + (w >> 2) * 2;
     }
-    static constexpr size_t kSmem = (size_t)(MT + kSlots) * kTileBytes + 3072;
+    static constexpr size_t kSmem = (size_t)(MT + kSlots) * kTileBytes + 3 * 1024;   // + Extra
     // of step number g of a row tile: S and P columns, phase of the S barrier
     __device__ static uint32_t col_s(int m, uint32_t g) { return m * 128 + (MT == 1 ? (g & 1) * 128 : 0); }
     __device__ static uint32_t col_p(int m, uint32_t g) { return m * 128 + 64 + (g & 1) * (MT == 1 ? 128 : 32); }
@@ -405,7 +418,10 @@ template <int MT> struct Extra {
     int rows[C::kRowRing][kTile];                 // cache rows of a tile's tokens, -1: none
     uint32_t rows_valid[C::kRowRing][4];          // which tokens have one
     uint32_t valid[kMaskRing][4];                 // tokens of a tile that exist
-    uint32_t badv[MT][4];                         // drafted tokens with non-finite V values
+    // Drafted tokens with non-finite V values, by the number of their tile: a warp may
+    // look at the next segment's, if it has one or two tiles, while another still
+    // reads this one's (behind more, P V has waited for both).
+    uint32_t badv[MT][4][4];
     int sums[C::kThreads / 32];
     Walk<MT> start;
     uint32_t tmem;
@@ -843,8 +859,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             uint32_t steps = 0;          // steps of earlier segments
             uint32_t seg = 0;            // segments begun
             bool ok = true;
-            // Rows copied by cp.async are read by the MMA through the async proxy.  (The
-            // fence is not cheap: boxes come through that proxy and go without.)
+            // Rows copied by cp.async are read by the MMA through the async proxy; boxes
+            // come through it and need no fence.
             auto proxy_fence = [] { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); };
             auto wait_full = [&](uint32_t entry, bool copied) {
                 ok = ok && bar_wait(&x.full[entry % C::kSlots], (entry / C::kSlots) & 1, gave_up);
@@ -864,7 +880,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     for (int i = 0; ok && i < 2 * tiles; ++i)
                         if (wait_full(e + i, false))
                             bar_arrive(&x.empty[(e + i) % C::kSlots]);
-                    if (ok)
+                    if (wait_bar(&x.q[seg & 1], seg >> 1))     // (no phase is missed)
                         bar_arrive(&x.q_free[seg & 1]);
                     e += 2 * tiles;
                     walk.next(tiles);
@@ -1022,7 +1038,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     }
                     const uint32_t bits = __ballot_sync(kFull, any);
                     if (lane == 0)
-                        x.badv[m][warp & 3] = bits;
+                        x.badv[m][(tile_no + i) & 3][warp & 3] = bits;
                     if constexpr (MT > 1) {
                         if (nm > 1) {
                             if (m == 1 && lane == 0)
@@ -1179,7 +1195,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 if (has_tree)
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        bad[w] = x.badv[m][w] & sees[w];
+                        bad[w] = x.badv[m][(tile_no + n - 1) & 3][w] & sees[w];
                 const uint32_t o = tmem + C::col_o(m) + lanes;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {

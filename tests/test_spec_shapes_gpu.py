@@ -130,3 +130,79 @@ def test_two_captured_graphs_share_a_workspace():
         check_tree(a, outs[0])
         check_tree(b, outs[1])
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("page,k", [(0, 0), (16, 0), (16, 40)])
+def test_small_and_large_trees_in_turn(page, k):
+    """Two row tiles per block, most requests with rows for one only and one tile of tokens:
+    a row tile leaves many units out between two that it has."""
+    gen = torch.Generator().manual_seed(page + k)
+    B, T = 220, 40
+    sizes = [40 if b % 7 == 3 else int(s) for b, s in enumerate(torch.randint(0, 20, (B,), generator=gen))]
+    lens = [n + int(c) for n, c in zip(sizes, torch.randint(0, 150, (B,), generator=gen))]
+    c = tree_case(page + k, 4, 2, lens, sizes, T, page, "tree", k, max_len=192)
+    out, ws = run_tree(c)
+    check_tree(c, out)
+    assert ws.status() == 0
+    assert torch.equal(run_tree(c)[0], out)
+
+
+def test_non_finite_values_of_neighbouring_units():
+    """One-tile units, every second one with values that are not finite in its tree: they stay
+    with the rows that see them and with their unit."""
+    B, T, page = 400, 4, 16
+    gen = torch.Generator().manual_seed(5)
+    lens = (T + torch.randint(0, 100, (B,), generator=gen)).tolist()
+    c = tree_case(9, 2, 2, lens, [T] * B, T, page, "tree", max_len=112)
+    c["seen"][:, :, 2] = False
+    c["seen"][:, 3, 2] = True                     # only the last row sees token 2
+    for b in range(0, B, 2):
+        p = lens[b] - T + 2
+        c["vc"][c["table"][b, p // page], :, p % page, 5] = float("inf")
+        c["V"][b, :, p, 5] = 0.0                  # what the rows that do not see it get is unchanged
+    out, ws = run_tree(c)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0::2, 3, :, 5] = True
+    assert torch.all(out[hit] == float("inf"))
+    out[hit] = 0.0
+    from spec_util import reference
+    ref, tol = reference(c["q"], c["K"], c["V"], c["lens"], c["sizes"], c["seen"])
+    ref[0::2, 3, :, 5] = 0.0
+    err = (out.cpu().double() - ref).abs()
+    assert torch.all(err <= tol) and ws.status() == 0
+
+
+def test_rows_behind_32_bit_offsets():
+    """A cache of more than 2^32 bytes and values: pages, slots and committed rows at its end."""
+    B, Hkv, G, page, T = 2, 8, 1, 64, 5
+    pages = (1 << 32) // (Hkv * page * D) + 64           # values per tensor over 2^32
+    c = tree_case(21, G, Hkv, [300, 130], [T, T], T, page, "tree")
+    blocks = c["table"].shape[1]
+    table = torch.arange(pages - 2 * blocks, pages, dtype=torch.int32).view(2, blocks)
+    shape = td.make_shape(B, Hkv * G, Hkv, c["N"])
+    kc = torch.empty(pages, Hkv, page, D, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    cache = td.make_cache(kc, vc, table.cuda())
+    ws = td.Workspace(shape, 0, tree_size=T)
+    pos = [(b, p) for b in range(B) for p in range(c["lens"][b])]
+    slots = torch.tensor([int(table[b, p // page]) * page + p % page for b, p in pos], dtype=torch.int32)
+    new = [torch.stack([x[b, :, p] for b, p in pos]).cuda() for x in (c["K"], c["V"])]
+    td.td_kv_append_slots(shape, cache, new[0], new[1], slots.cuda())
+    q, out = c["q"].cuda(), torch.full_like(c["q"], 7.0).cuda()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    from spec_util import pack_mask
+    td.td_tree_attn(shape, cache, T, None, pack_mask(c["seen"]).cuda(), q, i32(c["lens"]), out, ws)
+    torch.cuda.synchronize()
+    check_tree(c, out)
+    kept = [0, 2, 4]
+    new_lens = i32([0, 0])
+    td.td_tree_commit(shape, [cache], T, None, i32([kept + [0, 0]] * B), i32([3] * B), i32(c["lens"]), new_lens, ws)
+    torch.cuda.synchronize()
+    assert new_lens.tolist() == [n - T + 3 for n in c["lens"]] and ws.status() == 0
+    for b, n in enumerate(c["lens"]):
+        for i, j in enumerate(kept):
+            at, src = n - T + i, n - T + j
+            for got, x in ((kc, c["K"]), (vc, c["V"])):
+                assert torch.equal(got[int(table[b, at // page]), :, at % page].cpu(), x[b, :, src])
+    del kc, vc, cache
+    torch.cuda.empty_cache()
