@@ -123,36 +123,42 @@ __device__ __forceinline__ void bar_expect(uint64_t *bar, unsigned bytes)
                  : "memory");
 }
 
+__device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // Waits for the phase of the given parity.  Gives up after `limit` cycles of the SM
 // clock, or when another role has (then the CTA leaves as a whole and reports the
-// timeout).
-__device__ __forceinline__ bool bar_wait_for(uint64_t *bar, unsigned parity, volatile int *gave_up, long long limit)
+// timeout).  Out of line: the roles' code has to stay in the instruction cache.
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, unsigned parity, volatile int *gave_up, long long limit)
 {
-    const uint32_t addr = smem_of(bar);
-    long long t0 = 0;
-    for (int polls = 0;; ++polls) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(addr), "r"(parity)
-            : "memory");
-        if (done)
+    const long long t0 = clock64();
+    for (int polls = 1;; ++polls) {
+        if (bar_try(bar, parity))
             return true;
-        if ((polls & 63) == 63) {
-            const long long t = clock64();
-            if (t0 == 0)
-                t0 = t;
+        if ((polls & 63) == 0) {
             if (*gave_up)
                 return false;
-            if (t - t0 > limit) {
+            if (clock64() - t0 > limit) {
                 *gave_up = 1;
                 return false;
             }
         }
     }
+}
+
+__device__ __forceinline__ bool bar_wait_for(uint64_t *bar, unsigned parity, volatile int *gave_up, long long limit)
+{
+    return bar_try(smem_of(bar), parity) || bar_wait_long(smem_of(bar), parity, gave_up, limit);
 }
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const TmaDesc *map, int x, int row, uint64_t *bar)
@@ -358,10 +364,8 @@ struct Work {
     __device__ int tokens(int t) const { return t == tiles - 1 ? off + nt : min(kTile, entries - t * kTile); }
 };
 
-template <int MT>
-__device__ __forceinline__ Work work_of(const TreeArgs &a, int b, uint32_t &bad)
+template <int MT> __device__ __forceinline__ Work work_of(const TreeArgs &a, const TreeLens &len)
 {
-    const TreeLens len = tree_lens_of(a.seq_lens, a.tree_lens, b, a.T, a.Nmax, bad);
     Work w;
     w.nt = len.nt;
     w.ctx = len.n - len.nt;
@@ -371,6 +375,30 @@ __device__ __forceinline__ Work work_of(const TreeArgs &a, int b, uint32_t &bad)
     w.tiles = w.nt ? (w.entries >> 7) + (w.off == 0 && rest > 0 ? 1 : 0) + 1 : 0;
     w.blocks = (w.nt * a.G + MT * kTile - 1) / (MT * kTile);
     return w;
+}
+
+template <int MT> __device__ __forceinline__ Work work_of(const TreeArgs &a, int b, uint32_t &bad)
+{
+    return work_of<MT>(a, tree_lens_of(a.seq_lens, a.tree_lens, b, a.T, a.Nmax, bad));
+}
+
+// The first request behind b that has drafted tokens (or the last one) and its
+// lengths.  Out of line, once for all roles: their code has to stay in the
+// instruction cache.
+struct NextRequest {
+    TreeLens len;
+    int b;
+};
+__device__ __noinline__ NextRequest next_request(const TreeArgs &a, int b)
+{
+    NextRequest r;
+    uint32_t bad = 0;
+#pragma unroll 1
+    do {
+        r.len = tree_lens_of(a.seq_lens, a.tree_lens, ++b, a.T, a.Nmax, bad);
+    } while (r.len.nt == 0 && b + 1 < a.B);
+    r.b = b;
+    return r;
 }
 
 // A CTA's range of tiles, unit after unit: every role of the CTA walks it alike.
@@ -396,10 +424,9 @@ template <int MT> struct Walk {
         if (++h < args->Hkv)
             return;
         h = 0;
-        uint32_t bad = 0;
-        do {
-            w = work_of<MT>(*args, ++b, bad);
-        } while (w.tiles == 0 && b + 1 < args->B);
+        const NextRequest r = next_request(*args, b);
+        b = r.b;
+        w = work_of<MT>(*args, r.len);
     }
     __device__ int rows() const { return min(w.nt * args->G - m * MT * kTile, MT * kTile); }
 };
@@ -415,9 +442,9 @@ template <int MT> struct Extra {
     uint64_t s_read[MT];                          // two row tiles: S is in registers
     uint64_t scan, clear, drain;
     uint64_t never;                               // nothing arrives (tests of the failure report)
-    int rows[C::kRowRing][kTile];                 // cache rows of a tile's tokens, -1: none
+    alignas(16) int rows[C::kRowRing][kTile];     // cache rows of a tile's tokens, -1: none
     uint32_t rows_valid[C::kRowRing][4];          // which tokens have one
-    uint32_t valid[kMaskRing][4];                 // tokens of a tile that exist
+    alignas(16) uint32_t valid[kMaskRing][4];     // tokens of a tile that exist
     // Drafted tokens with non-finite V values, by the number of their tile: a warp may
     // look at the next segment's, if it has one or two tiles, while another still
     // reads this one's (behind more, P V has waited for both).
@@ -439,6 +466,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     using C = Cfg<MT>;
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     Extra<MT> &x = *reinterpret_cast<Extra<MT> *>(sm_raw + (MT + C::kSlots) * kTileBytes);
+    static_assert(C::kCopiers == 4, "copy warps' rows of a tile");
     static_assert((MT + C::kSlots) * kTileBytes + sizeof(Extra<MT>) <= C::kSmem, "shared memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto bar_wait = [&](uint64_t *bar, unsigned parity, volatile int *up) {
@@ -461,6 +489,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         uint32_t bad = 0;
         int mine = 0;
         Work w{};
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             w = work_of<MT>(a, b, bad);
             mine += w.tiles * w.blocks * a.Hkv;
@@ -525,6 +554,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         if (start < total && at <= start && start - at < mine) {
             int b = b0;
             if (run > 1) {
+#pragma unroll 1
                 for (int p = at; b < b1; ++b, at = p) {
                     w = work_of<MT>(a, b, bad);
                     p += w.tiles * w.blocks * a.Hkv;
@@ -614,6 +644,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         auto box_pos = [&](int t, int box) { return t * kTile + box * a.box_rows; };
         uint32_t tile_no = 0, copied = 0, flags = 0;       // tiles; tiles for the copy warps
         bool ok = true;
+#pragma unroll 1
         while (ok && walk.left > 0) {
             const int n = walk.count(), boxes = boxes_of(walk.w);
             auto read_pages = [&](int t) {      // of the boxes of tiles t .. t + batch - 1
@@ -625,6 +656,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 pages = read_pages(first);
                 pages2 = read_pages(first + batch);
             }
+#pragma unroll 1
             for (int i = 0; i < n; ++i, ++tile_no) {
                 const int t = walk.t + i;
                 const bool box = t < boxes;
@@ -723,18 +755,21 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             const int first = at.t * kTile, tokens = at.count() * kTile;
             if (a.idx) {
                 const int32_t *p = a.idx + ((size_t)at.b * a.Hkv + at.h) * a.top_k;
+#pragma unroll 1
                 for (int j = first + lane * 32; j < min(first + tokens, a.top_k); j += 32 * 32)
                     prefetch_l2(p + j);
             }
             if (a.c.table) {
                 const int32_t *p = a.c.table + (size_t)at.b * a.c.max_blocks;
                 const int blocks = (at.w.ctx + at.w.nt + a.c.page_size - 1) / a.c.page_size;
+#pragma unroll 1
                 for (int j = lane * 32; j < blocks; j += 32 * 32)
                     prefetch_l2(p + j);
             }
         };
         uint32_t flags = 0, tile = 0;      // tile: number of the copied tile
         bool ok = true;
+#pragma unroll 1
         for (bool first = true; ok && walk.left > 0; first = false) {
             const Work &w = walk.w;
             const int n = walk.count();
@@ -746,6 +781,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             } else if (first) {
                 prefetch(walk);
             }
+#pragma unroll 1
             for (int i = max(0, boxes_of(w) - walk.t); i < n; ++i, ++tile) {
                 if (tile % C::kFinders != (uint32_t)me)
                     continue;
@@ -801,6 +837,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         constexpr uint32_t kRing = C::kRowRing;
         uint32_t e = 0, copied = 0;
         bool ok = true;
+#pragma unroll 1
         for (uint32_t seg = 0; ok && walk.left > 0; ++seg) {
             const int n = walk.count();
             // Q: its buffer was the last segment's, or with two the one before's.  Rows
@@ -823,9 +860,13 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 }
                 copies_arrive(&x.q[seg & 1]);
             }
+#pragma unroll 1
             for (int i = max(0, boxes_of(walk.w) - walk.t); i < n; ++i, ++copied) {
                 const uint32_t ring = copied % kRing, phase = copied / kRing & 1;
                 const int tokens = walk.w.tokens(walk.t + i);
+                // Half a warp takes four neighbouring rows of every 32; their numbers are
+                // loaded ahead, as loads from shared memory queue behind the copies.
+                const int tok0 = 8 * me + 4 * (lane >> 4);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
                     ok = __all_sync(kFull, bar_wait(&x.go[ring][kv], phase, gave_up));
@@ -836,9 +877,20 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     const int end = kv ? (tokens + 15) & ~15 : tokens;
                     const uint16_t *src = kv ? a.c.v : a.c.k;
                     const uint32_t dst = sm_ring + slot * kTileBytes;
-#pragma unroll 4
-                    for (int tok = 2 * me + (lane >> 4); tok < end; tok += 2 * C::kCopiers)
-                        copy_row(dst, tok, src, x.rows[ring][tok], lane);
+                    uint32_t rows[4], ahead[4];
+                    lds4(smem_of(&x.rows[ring][tok0]), ahead);
+#pragma unroll 1
+                    for (int tok = tok0; tok < end; tok += 32) {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            rows[v] = ahead[v];
+                        if (tok + 32 < end)
+                            lds4(smem_of(&x.rows[ring][tok + 32]), ahead);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            if (tok + v < end)
+                                copy_row(dst, tok + v, src, (int)rows[v], lane);
+                    }
                     copies_arrive(&x.full[slot]);
                 }
                 __syncwarp();
@@ -873,10 +925,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 tmem_after();
                 return ok;
             };
+#pragma unroll 1
             for (; ok && walk.left > 0; ++seg) {
                 const int tiles = walk.count(), n = tiles * C::kSteps;
                 if (MT > 1 && m * kTile >= walk.rows()) {
                     // no rows here: the slots are free as far as this row tile goes
+#pragma unroll 1
                     for (int i = 0; ok && i < 2 * tiles; ++i)
                         if (wait_full(e + i, false))
                             bar_arrive(&x.empty[(e + i) % C::kSlots]);
@@ -913,6 +967,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 if (!wait_full(e, boxes <= 0))
                     break;
                 issue_s(0);
+#pragma unroll 1
                 for (int j = 0; j < n; ++j) {
                     if (j + 1 < n) {
                         if ((j + 1) % C::kSteps == 0 &&
@@ -955,6 +1010,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         uint32_t tile_no = 0;                                 // tiles of the CTA before the segment
         uint32_t scans = 0;                                   // clearings of V with two row tiles
         bool ok = true;
+#pragma unroll 1
         while (ok && walk.left > 0) {
             const int n = walk.count();
             const int unit_rows = walk.rows();
@@ -969,7 +1025,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             const int total_rows = walk.w.nt * a.G;
             const size_t q0 = (size_t)b * a.T * a.Hq + h * a.G;
             const int row = row0 + r;
-            const int tok = row / a.G;                         // drafted token of this row
+            const int tok = row >> a.g_shift;                  // drafted token of this row
             const bool live = row < total_rows;
             const bool warp_live = row0 + (warp & 3) * 32 < total_rows;
             float mref = -CUDART_INF_F, l = 0.0f;
@@ -986,31 +1042,34 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                                     : 0u;
                 }
                 // the last tile's bits: its context tokens, then the drafted ones
-                const int up = walk.w.off >> 5, by = walk.w.off & 31;
-#pragma unroll
-                for (int w = 3; w >= 0; --w) {
-                    const uint32_t hi = w >= up ? (up == 0 ? sees[w] : up == 1 ? sees[w > 0 ? w - 1 : 0]
-                                                   : up == 2 ? sees[w > 1 ? w - 2 : 0] : sees[0]) : 0u;
-                    const uint32_t lo = w >= up + 1 ? (up == 0 ? sees[w > 0 ? w - 1 : 0] : up == 1 ? sees[w > 1 ? w - 2 : 0]
-                                                       : sees[0]) : 0u;
-                    const int below = walk.w.off - 32 * w;
-                    sees[w] = __funnelshift_l(lo, hi, by) |
-                              (below >= 32 ? kFull : below > 0 ? (1u << below) - 1 : 0u);
-                }
+                uint64_t lo = sees[0] | (uint64_t)sees[1] << 32, hi = sees[2] | (uint64_t)sees[3] << 32;
+                const int off = walk.w.off;
+                const uint64_t below = (1ull << (off & 63)) - 1;
+                hi = off >= 64 ? lo << (off & 63) | below : off > 0 ? hi << off | lo >> (64 - off) : hi;
+                lo = off >= 64 ? ~0ull : lo << off | below;
+                sees[0] = (uint32_t)lo;
+                sees[1] = (uint32_t)(lo >> 32);
+                sees[2] = (uint32_t)hi;
+                sees[3] = (uint32_t)(hi >> 32);
             }
+#pragma unroll 1
             for (int j = 0; j < n * C::kSteps; ++j, ++count) {
                 const int i = j / C::kSteps, part = j % C::kSteps;   // tile, step of the tile
                 const bool tree = walk.t + i == walk.w.tiles - 1;
-                // P V of the step before is done.  Waited for in every step (it is, by
-                // the time the exponentials are), so no phase of bar_o is missed.
+                // P V of the step before is done.  Two row tiles: waited for in every step
+                // (it is, by the time the exponentials are), as P of the step before the
+                // last is overwritten.  One: only to rescale, and in the last step; S of
+                // this step was issued after P V of the step before the last.  Either way
+                // this comes before P of this step is handed over, behind which P V of
+                // this step may end and the phase of the one before be past.
                 bool waited = j == 0;
                 auto o_done = [&]() {
                     if (!waited)
                         ok = __all_sync(kFull, bar_wait(&x.o[m], (count - 1) & 1, gave_up));
                     waited = true;
                 };
-                ok = __all_sync(kFull, a.wait_test ? bar_wait(&x.never, 0, gave_up)
-                                                   : bar_wait(&x.s[m][C::buf_s(count)], C::phase_s(count) & 1, gave_up));
+                ok = __all_sync(kFull, bar_wait(a.wait_test ? &x.never : &x.s[m][C::buf_s(count)],
+                                                a.wait_test ? 0 : C::phase_s(count) & 1, gave_up));
                 if (!ok)
                     break;
                 tmem_after();
@@ -1075,23 +1134,35 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     // The row's scores pass through 64 registers, in blocks of 64
                     // tokens: every block once for the maximum, then the last block
                     // from the registers and the others again for the exponentials.
-                    // Loops that stay rolled: with the step unrolled over 128
+                    // A loop that stays rolled: with the step unrolled over 128
                     // registers the roles' code no longer fitted the instruction
                     // cache (100K: 261 us against 314).
                     constexpr int kBlocks = C::kStep / 64;
                     const uint32_t at = tmem + C::col_s(m, count) + lanes;
-                    const uint32_t *valid = x.valid[(tile_no + i) % kMaskRing] + part * 2;
-                    float s[64];
-                    auto fetch = [&](int block) {
+                    uint32_t seen[4];     // of the step's tokens, 32 a word (two row tiles: two words)
+                    lds4(smem_of(x.valid[(tile_no + i) % kMaskRing]), seen);
+                    if (tree) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            seen[w] &= sees[w];
+                    }
+                    if (MT > 1 && part > 0) {
+                        seen[0] = seen[2];
+                        seen[1] = seen[3];
+                    }
+                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                    float2 off2 = make_float2(0.0f, 0.0f);
+                    float2 sum[2] = {off2, off2};
+                    // passes: block 0 (maximum), block 1 (maximum, probabilities), block 0
+                    // (probabilities); with one block both in one pass
+#pragma unroll 1
+                    for (int pass = 0; pass < 2 * kBlocks - 1; ++pass) {
+                        const int block = kBlocks > 1 ? pass & 1 : 0;
+                        const uint32_t w0 = block > 0 ? seen[2] : seen[0], w1 = block > 0 ? seen[3] : seen[1];
+                        float s[64];
                         __syncwarp();
                         tmem_ld32(at + 64 * block, reinterpret_cast<uint32_t *>(s));
                         tmem_ld32(at + 64 * block + 32, reinterpret_cast<uint32_t *>(s) + 32);
-                        uint32_t w0 = valid[2 * block], w1 = valid[2 * block + 1];
-                        if (tree) {
-                            const bool upper = part + block > 0;      // drafted tokens 64 .. 127
-                            w0 &= upper ? sees[2] : sees[0];
-                            w1 &= upper ? sees[3] : sees[1];
-                        }
                         tmem_wait_ld();
                         tmem_loaded(reinterpret_cast<uint32_t *>(s));
                         tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32);
@@ -1104,74 +1175,73 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                     s[32 + k] = -CUDART_INF_F;
                             }
                         }
-                    };
-                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll 1
-                    for (int block = 0; block < kBlocks; ++block) {
-                        fetch(block);
-                        if constexpr (MT > 1) {
-                            tmem_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                bar_arrive(&x.s_read[m]);
-                        }
+                        if (pass < kBlocks) {
+                            if constexpr (MT > 1) {
+                                tmem_before();
+                                __syncwarp();
+                                if (lane == 0)
+                                    bar_arrive(&x.s_read[m]);
+                            }
 #pragma unroll
-                        for (int k = 0; k < 64; k += 2)
-                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-                    if (mref == -CUDART_INF_F)
-                        mref = top;          // nothing summed so far: l = 0 and O = 0
-                    // The running maximum lags until a row exceeds it by 2^8: the
-                    // probabilities stay below 2^8 and the rescaling of O is rare.
-                    const bool grow = j > 0 && top > mref + 8.0f;
-                    if (__any_sync(kFull, grow)) {
-                        o_done();
-                        if (!ok)
-                            break;
-                        tmem_after();
-                        const float mn = grow ? top : mref;
-                        const float f = grow ? ex2(mref - mn) : 1.0f;
-                        mref = mn;
-                        l *= f;
-                        const uint32_t o = tmem + C::col_o(m) + lanes;
+                            for (int k = 0; k < 64; k += 2)
+                                mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
+                        }
+                        if (pass == kBlocks - 1) {
+                            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                            if (mref == -CUDART_INF_F)
+                                mref = top;          // nothing summed so far: l = 0 and O = 0
+                            // The running maximum lags until a row exceeds it by 2^8: the
+                            // probabilities stay below 2^8 and the rescaling of O is rare.
+                            const bool grow = j > 0 && top > mref + 8.0f;
+                            if (__any_sync(kFull, grow)) {
+                                o_done();
+                                if (!ok)
+                                    break;
+                                tmem_after();
+                                const float mn = grow ? top : mref;
+                                const float f = grow ? ex2(mref - mn) : 1.0f;
+                                mref = mn;
+                                l *= f;
+                                const uint32_t o = tmem + C::col_o(m) + lanes;
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t ov[32];
-                            tmem_ld32(o + 32 * c, ov);
-                            tmem_wait_ld();
-                            tmem_loaded(ov);
+                                for (int c = 0; c < 4; ++c) {
+                                    uint32_t ov[32];
+                                    tmem_ld32(o + 32 * c, ov);
+                                    tmem_wait_ld();
+                                    tmem_loaded(ov);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
-                            tmem_st32(o + 32 * c, ov);
+                                    for (int k = 0; k < 32; ++k)
+                                        ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+                                    tmem_st32(o + 32 * c, ov);
+                                }
+                            }
+                            const float off = mref == -CUDART_INF_F ? 0.0f : -mref;
+                            off2 = make_float2(off, off);
+                        }
+                        if (pass >= kBlocks - 1) {
+                            const float2 sl22 = make_float2(sl2, sl2);
+                            uint32_t p[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const float2 z = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), sl22, off2);
+                                const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                                sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+                                p[k] = pack_bf16(e.x, e.y);
+                            }
+                            // (one row tile: over scores of this or a later block, which have been
+                            // read; two: P V of the step before the last is done)
+                            tmem_st32(tmem + C::col_p(m, count) + lanes + 32 * block, p);
                         }
                     }
-                    const float off = mref == -CUDART_INF_F ? 0.0f : -mref;
-                    const float2 off2 = make_float2(off, off), sl22 = make_float2(sl2, sl2);
-                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll 1
-                    for (int block = kBlocks - 1; block >= 0; --block) {
-                        if (block < kBlocks - 1)
-                            fetch(block);
-                        uint32_t p[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float2 z = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), sl22, off2);
-                            const float2 e = make_float2(ex2(z.x), ex2(z.y));
-                            sum[k & 1] = __fadd2_rn(sum[k & 1], e);
-                            p[k] = pack_bf16(e.x, e.y);
-                        }
-                        // (one row tile: over scores of this or a later block, which have been
-                        // read; two: P V of the step before the last is done)
-                        tmem_st32(tmem + C::col_p(m, count) + lanes + 32 * block, p);
-                    }
+                    if (!ok)
+                        break;
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                 } else if (MT > 1 && lane == 0) {
                     bar_arrive(&x.s_read[m]);
                 }
-                o_done();
+                if (MT > 1 || j == n - 1)
+                    o_done();
                 if (!ok)
                     break;
                 tmem_before();
@@ -1204,6 +1274,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     tmem_wait_ld();
                     tmem_loaded(ov);
                     if (live && (bad[0] | bad[1] | bad[2] | bad[3])) {
+#pragma unroll 1
                         for (int j = walk.w.off; j < walk.w.off + walk.w.nt; ++j) {
                             if (!((j < 64 ? (j < 32 ? bad[0] : bad[1]) : (j < 96 ? bad[2] : bad[3])) >> (j & 31) & 1u))
                                 continue;
@@ -1218,7 +1289,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         }
                     }
                     if (live && whole) {
-                        uint16_t *dst = a.out + (q0 + (size_t)tok * a.Hq + row % a.G) * kHeadDim + 32 * c;
+                        uint16_t *dst = a.out + (q0 + (size_t)tok * a.Hq + (row & (a.G - 1))) * kHeadDim + 32 * c;
                         uint32_t y[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
