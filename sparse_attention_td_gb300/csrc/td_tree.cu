@@ -481,6 +481,43 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         return;
     }
 
+    // ---- what needs no input, while the kernel before this one ends
+    if (tid == 32 * C::kLoader) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_v) : "memory");
+    }
+    if (tid == 32 * C::kIssuer) {
+        x.gave_up = 0;
+        x.start.left = 0;
+        for (int i = 0; i < C::kSlots; ++i) {
+            bar_init(&x.full[i], 32 * C::kCopiers);
+            bar_init(&x.empty[i], MT);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&x.q[i], 32 * C::kCopiers);
+            bar_init(&x.q_free[i], MT);
+        }
+        for (int i = 0; i < MT; ++i) {
+            for (int k = 0; k < 2; ++k) {
+                bar_init(&x.s[i][k], 1);
+                bar_init(&x.p[i][k], 4);
+            }
+            bar_init(&x.o[i], 1);
+            bar_init(&x.s_read[i], 4);
+        }
+        for (int i = 0; i < C::kRowRing; ++i) {
+            bar_init(&x.rows_there[i], 1);
+            bar_init(&x.go[i][0], 1);
+            bar_init(&x.go[i][1], 1);
+            bar_init(&x.rows_read[i], C::kCopiers);
+        }
+        bar_init(&x.scan, 4);
+        bar_init(&x.clear, 4);
+        bar_init(&x.drain, MT);
+        bar_init(&x.never, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    pdl_wait();
     // ---- the CTA's range: requests in equal runs per thread, prefix sums.  (The
     // host has made sure that the number of tiles fits 31 bits.)
     {
@@ -493,41 +530,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         for (int b = b0; b < b1; ++b) {
             w = work_of<MT>(a, b, bad);
             mine += w.tiles * w.blocks * a.Hkv;
-        }
-        if (tid == 32 * C::kLoader) {
-            asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_k) : "memory");
-            asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_v) : "memory");
-        }
-        if (tid == 32 * C::kIssuer) {
-            x.gave_up = 0;
-            x.start.left = 0;
-            for (int i = 0; i < C::kSlots; ++i) {
-                bar_init(&x.full[i], 32 * C::kCopiers);
-                bar_init(&x.empty[i], MT);
-            }
-            for (int i = 0; i < 2; ++i) {
-                bar_init(&x.q[i], 32 * C::kCopiers);
-                bar_init(&x.q_free[i], MT);
-            }
-            for (int i = 0; i < MT; ++i) {
-                for (int k = 0; k < 2; ++k) {
-                    bar_init(&x.s[i][k], 1);
-                    bar_init(&x.p[i][k], 4);
-                }
-                bar_init(&x.o[i], 1);
-                bar_init(&x.s_read[i], 4);
-            }
-            for (int i = 0; i < C::kRowRing; ++i) {
-                bar_init(&x.rows_there[i], 1);
-                bar_init(&x.go[i][0], 1);
-                bar_init(&x.go[i][1], 1);
-                bar_init(&x.rows_read[i], C::kCopiers);
-            }
-            bar_init(&x.scan, 4);
-            bar_init(&x.clear, 4);
-            bar_init(&x.drain, MT);
-            bar_init(&x.never, 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         if (bad && blockIdx.x == 0)
             atomicOr(a.status, bad);
@@ -1436,19 +1438,22 @@ cudaError_t launch(const TreeArgs &a, int sms, cudaStream_t stream)
         }
     }
     const int ctas = sms < kMaxTreeCtas ? sms : kMaxTreeCtas;
-    tree_attention_kernel<MT><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
-    err = cudaGetLastError();
-    if (err != cudaSuccess || ctas < 2)
-        return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas - 1, (a.part_rows + kJoinWarps - 1) / kJoinWarps);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    err = cudaLaunchKernelEx(&cfg, tree_attention_kernel<MT>, a);
+    if (err != cudaSuccess || ctas < 2)
+        return err;
+    cfg.gridDim = dim3(ctas - 1, (a.part_rows + kJoinWarps - 1) / kJoinWarps);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.dynamicSmemBytes = 0;
     const JoinArgs j{a.plan, a.part_m, a.part_l, a.part_o, a.out, a.T, a.Hq, a.G, a.part_rows};
     return cudaLaunchKernelEx(&cfg, tree_join_kernel, j);
 }
