@@ -950,7 +950,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     const uint32_t g = steps + j;
                     if (MT > 1 && j >= 1)       // the softmax has read the step before
                         wait_bar(&x.s_read[m], g - 1);
-                    if (MT == 1 && j >= 2)      // P V of step j - 2 has read this buffer's P
+                    if (j >= 2)                 // P V of step j - 2 has read the P that goes next
                         wait_bar(&x.o[m], g - 2);
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
@@ -1058,12 +1058,11 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             for (int j = 0; j < n * C::kSteps; ++j, ++count) {
                 const int i = j / C::kSteps, part = j % C::kSteps;   // tile, step of the tile
                 const bool tree = walk.t + i == walk.w.tiles - 1;
-                // P V of the step before is done.  Two row tiles: waited for in every step
-                // (it is, by the time the exponentials are), as P of the step before the
-                // last is overwritten.  One: only to rescale, and in the last step; S of
-                // this step was issued after P V of the step before the last.  Either way
-                // this comes before P of this step is handed over, behind which P V of
-                // this step may end and the phase of the one before be past.
+                // P V of the step before is done: waited for to rescale O, and in the last
+                // step.  (P V of the step before the last was done when S of this step was
+                // issued, so no phase is missed.)  Both waits come before P of this step is
+                // handed over, behind which P V of this step may end and the phase of the
+                // one before be past.
                 bool waited = j == 0;
                 auto o_done = [&]() {
                     if (!waited)
@@ -1156,10 +1155,11 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     float2 off2 = make_float2(0.0f, 0.0f);
                     float2 sum[2] = {off2, off2};
                     // passes: block 0 (maximum), block 1 (maximum, probabilities), block 0
-                    // (probabilities); with one block both in one pass
+                    // (probabilities); with one block (of a step, or of tokens) both in one
+                    const int blocks = kBlocks > 1 && walk.w.tokens(walk.t + i) > 64 ? 2 : 1;
 #pragma unroll 1
-                    for (int pass = 0; pass < 2 * kBlocks - 1; ++pass) {
-                        const int block = kBlocks > 1 ? pass & 1 : 0;
+                    for (int pass = 0; pass < 2 * blocks - 1; ++pass) {
+                        const int block = blocks > 1 ? pass & 1 : 0;
                         const uint32_t w0 = block > 0 ? seen[2] : seen[0], w1 = block > 0 ? seen[3] : seen[1];
                         float s[64];
                         __syncwarp();
@@ -1177,7 +1177,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                     s[32 + k] = -CUDART_INF_F;
                             }
                         }
-                        if (pass < kBlocks) {
+                        if (pass < blocks) {
                             if constexpr (MT > 1) {
                                 tmem_before();
                                 __syncwarp();
@@ -1188,7 +1188,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                             for (int k = 0; k < 64; k += 2)
                                 mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
                         }
-                        if (pass == kBlocks - 1) {
+                        if (pass == blocks - 1) {
                             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                             if (mref == -CUDART_INF_F)
                                 mref = top;          // nothing summed so far: l = 0 and O = 0
@@ -1220,7 +1220,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                             const float off = mref == -CUDART_INF_F ? 0.0f : -mref;
                             off2 = make_float2(off, off);
                         }
-                        if (pass >= kBlocks - 1) {
+                        if (pass >= blocks - 1) {
                             const float2 sl22 = make_float2(sl2, sl2);
                             uint32_t p[32];
 #pragma unroll
@@ -1230,8 +1230,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                 sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                                 p[k] = pack_bf16(e.x, e.y);
                             }
-                            // (one row tile: over scores of this or a later block, which have been
-                            // read; two: P V of the step before the last is done)
+                            // (one row tile: over scores of this or a later block, which have been read)
                             tmem_st32(tmem + C::col_p(m, count) + lanes + 32 * block, p);
                         }
                     }
@@ -1242,7 +1241,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 } else if (MT > 1 && lane == 0) {
                     bar_arrive(&x.s_read[m]);
                 }
-                if (MT > 1 || j == n - 1)
+                if (j == n * C::kSteps - 1)
                     o_done();
                 if (!ok)
                     break;
