@@ -1043,16 +1043,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                   : tok >= 32 * w   ? 0xffffffffu >> (31 - (tok & 31))
                                                     : 0u;
                 }
-                // the last tile's bits: its context tokens, then the drafted ones
-                uint64_t lo = sees[0] | (uint64_t)sees[1] << 32, hi = sees[2] | (uint64_t)sees[3] << 32;
-                const int off = walk.w.off;
-                const uint64_t below = (1ull << (off & 63)) - 1;
-                hi = off >= 64 ? lo << (off & 63) | below : off > 0 ? hi << off | lo >> (64 - off) : hi;
-                lo = off >= 64 ? ~0ull : lo << off | below;
-                sees[0] = (uint32_t)lo;
-                sees[1] = (uint32_t)(lo >> 32);
-                sees[2] = (uint32_t)hi;
-                sees[3] = (uint32_t)(hi >> 32);
             }
 #pragma unroll 1
             for (int j = 0; j < n * C::kSteps; ++j, ++count) {
@@ -1075,6 +1065,16 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     break;
                 tmem_after();
                 if (tree && part == 0) {
+                    // the last tile's bits: its context tokens, then the drafted ones
+                    uint64_t lo = sees[0] | (uint64_t)sees[1] << 32, hi = sees[2] | (uint64_t)sees[3] << 32;
+                    const int off = walk.w.off;
+                    const uint64_t below = (1ull << (off & 63)) - 1;
+                    hi = off >= 64 ? lo << (off & 63) | below : off > 0 ? hi << off | lo >> (64 - off) : hi;
+                    lo = off >= 64 ? ~0ull : lo << off | below;
+                    sees[0] = (uint32_t)lo;
+                    sees[1] = (uint32_t)(lo >> 32);
+                    sees[2] = (uint32_t)hi;
+                    sees[3] = (uint32_t)(hi >> 32);
                     // A V value that is not finite must not meet the zero
                     // probabilities of rows that do not see its token: such values
                     // leave the tile here and join the rows that do see it below.
