@@ -286,12 +286,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
         : "memory");
 }
 
-__device__ __forceinline__ void lds4(uint32_t addr, uint32_t (&x)[4])
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&x)[4])
 {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                  : "r"(addr)
                  : "memory");
+}
+
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&x)[2])
+{
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
@@ -403,14 +408,13 @@ __device__ __noinline__ NextRequest next_request(const TreeArgs &a, int b)
 
 // A CTA's range of tiles, unit after unit: every role of the CTA walks it alike.
 template <int MT> struct Walk {
-    const TreeArgs *args;
     int left;                     // tiles left of the CTA's range
     int b, h, m, t;               // current request, KV head, row block and first tile
     bool first;                   // the segment starts at the CTA's range start
     Work w;
 
     __device__ int count() const { return min(left, w.tiles - t); }
-    __device__ void next(int n)
+    __device__ void next(const TreeArgs &a, int n)
     {
         first = false;
         left -= n;
@@ -421,14 +425,14 @@ template <int MT> struct Walk {
         if (++m < w.blocks)
             return;
         m = 0;
-        if (++h < args->Hkv)
+        if (++h < a.Hkv)
             return;
         h = 0;
-        const NextRequest r = next_request(*args, b);
+        const NextRequest r = next_request(a, b);
         b = r.b;
-        w = work_of<MT>(*args, r.len);
+        w = work_of<MT>(a, r.len);
     }
-    __device__ int rows() const { return min(w.nt * args->G - m * MT * kTile, MT * kTile); }
+    __device__ int rows(const TreeArgs &a) const { return min(w.nt * a.G - m * MT * kTile, MT * kTile); }
 };
 
 // Shared memory behind the Q tiles and the ring.
@@ -566,7 +570,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             }
             const int unit = (uint32_t)(start - at) / (uint32_t)w.tiles;
             Walk<MT> s;
-            s.args = &a;
             s.left = min(per, total - start);
             s.b = b;
             s.h = w.blocks == 1 ? unit : unit / w.blocks;
@@ -583,7 +586,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             JoinPlan j{};
             const int first = x.start.t;
             if (x.start.left > 0 && first > 0 && first <= per) {
-                j.rows = x.start.rows();
+                j.rows = x.start.rows(a);
                 j.b = x.start.b;
                 j.h = x.start.h;
                 j.row0 = x.start.m * MT * kTile;
@@ -741,7 +744,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     break;
                 copied += box ? 0 : 1;
             }
-            walk.next(n);
+            walk.next(a, n);
         }
         if (flags && lane == 0)
             atomicOr(a.status, flags);
@@ -777,7 +780,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             const int n = walk.count();
             if (me == 0) {
                 Walk<MT> next = walk;
-                next.next(n);
+                next.next(a, n);
                 if (next.left > 0)
                     prefetch(next);
             } else if (first) {
@@ -827,7 +830,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 if (lane == 0)
                     bar_arrive(&x.rows_there[ring]);
             }
-            walk.next(n);
+            walk.next(a, n);
         }
         if (flags)
             atomicOr(a.status, flags);
@@ -850,7 +853,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             if (!ok)
                 break;
             {
-                const int rows = walk.rows(), row0 = walk.m * MT * kTile;
+                const int rows = walk.rows(a), row0 = walk.m * MT * kTile;
                 const int c = lane & 15;
                 const uint16_t *src = a.q + ((size_t)walk.b * a.T * a.Hq + walk.h * a.G) * kHeadDim + c * 8;
                 const uint32_t dst = sm_q + (two_q ? seg & 1 : 0) * 64 * 128 + (c >> 3) * kHalfBytes;
@@ -880,14 +883,14 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     const uint16_t *src = kv ? a.c.v : a.c.k;
                     const uint32_t dst = sm_ring + slot * kTileBytes;
                     uint32_t rows[4], ahead[4];
-                    lds4(smem_of(&x.rows[ring][tok0]), ahead);
+                    lds_words(smem_of(&x.rows[ring][tok0]), ahead);
 #pragma unroll 1
                     for (int tok = tok0; tok < end; tok += 32) {
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
                             rows[v] = ahead[v];
                         if (tok + 32 < end)
-                            lds4(smem_of(&x.rows[ring][tok + 32]), ahead);
+                            lds_words(smem_of(&x.rows[ring][tok + 32]), ahead);
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
                             if (tok + v < end)
@@ -902,7 +905,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     bar_arrive(&x.rows_read[ring]);
             }
             e += 2 * n;
-            walk.next(n);
+            walk.next(a, n);
         }
     } else if (issuer) {
         // ---- MMA issue of one row tile, by one thread: S of step j + 1 before P V of
@@ -930,7 +933,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
 #pragma unroll 1
             for (; ok && walk.left > 0; ++seg) {
                 const int tiles = walk.count(), n = tiles * C::kSteps;
-                if (MT > 1 && m * kTile >= walk.rows()) {
+                if (MT > 1 && m * kTile >= walk.rows(a)) {
                     // no rows here: the slots are free as far as this row tile goes
 #pragma unroll 1
                     for (int i = 0; ok && i < 2 * tiles; ++i)
@@ -939,7 +942,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     if (wait_bar(&x.q[seg & 1], seg >> 1))     // (no phase is missed)
                         bar_arrive(&x.q_free[seg & 1]);
                     e += 2 * tiles;
-                    walk.next(tiles);
+                    walk.next(a, tiles);
                     continue;
                 }
                 const uint32_t q = operand(sm_q + m * kTileBytes + (two_q ? seg & 1 : 0) * 64 * 128, 16);
@@ -998,7 +1001,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 }
                 steps += n;
                 e += 2 * tiles;
-                walk.next(tiles);
+                walk.next(a, tiles);
             }
         }
         __syncwarp();
@@ -1015,11 +1018,11 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
 #pragma unroll 1
         while (ok && walk.left > 0) {
             const int n = walk.count();
-            const int unit_rows = walk.rows();
+            const int unit_rows = walk.rows(a);
             const int nm = MT == 1 ? 1 : (unit_rows + kTile - 1) / kTile;
             if (m >= nm) {
                 tile_no += n;
-                walk.next(n);
+                walk.next(a, n);
                 continue;
             }
             const int b = walk.b, h = walk.h;
@@ -1090,7 +1093,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
 #pragma unroll 2
                         for (int c = 0; c < 16; ++c) {
                             uint32_t y4[4];
-                            lds4(v + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4), y4);
+                            lds_words(v + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4), y4);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 any |= (y4[k] & 0x7f80u) == 0x7f80u || (y4[k] & 0x7f800000u) == 0x7f800000u;
@@ -1114,7 +1117,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                             for (int c = 0; c < 16; ++c) {
                                 uint32_t y4[4];
                                 const uint32_t at = v + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4);
-                                lds4(at, y4);
+                                lds_words(at, y4);
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     if ((y4[k] & 0x7f80u) == 0x7f80u)
@@ -1140,16 +1143,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     // cache (100K: 261 us against 314).
                     constexpr int kBlocks = C::kStep / 64;
                     const uint32_t at = tmem + C::col_s(m, count) + lanes;
-                    uint32_t seen[4];     // of the step's tokens, 32 a word (two row tiles: two words)
-                    lds4(smem_of(x.valid[(tile_no + i) % kMaskRing]), seen);
+                    uint32_t seen[C::kStep / 32];     // of the step's tokens, 32 a word
+                    lds_words(smem_of(x.valid[(tile_no + i) % kMaskRing] + part * (C::kStep / 32)), seen);
                     if (tree) {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w)
-                            seen[w] &= sees[w];
-                    }
-                    if (MT > 1 && part > 0) {
-                        seen[0] = seen[2];
-                        seen[1] = seen[3];
+                        for (int w = 0; w < C::kStep / 32; ++w)
+                            seen[w] &= MT > 1 && part > 0 ? sees[(w + 2) & 3] : sees[w];
                     }
                     float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
                     float2 off2 = make_float2(0.0f, 0.0f);
@@ -1160,7 +1159,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
 #pragma unroll 1
                     for (int pass = 0; pass < 2 * blocks - 1; ++pass) {
                         const int block = blocks > 1 ? pass & 1 : 0;
-                        const uint32_t w0 = block > 0 ? seen[2] : seen[0], w1 = block > 0 ? seen[3] : seen[1];
+                        constexpr int kUp = kBlocks > 1 ? 2 : 0;
+                        const uint32_t w0 = block > 0 ? seen[kUp] : seen[0], w1 = block > 0 ? seen[kUp + 1] : seen[1];
                         float s[64];
                         __syncwarp();
                         tmem_ld32(at + 64 * block, reinterpret_cast<uint32_t *>(s));
@@ -1315,7 +1315,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             }
             __syncwarp();
             tile_no += n;
-            walk.next(n);
+            walk.next(a, n);
         }
     }
     tmem_before();
