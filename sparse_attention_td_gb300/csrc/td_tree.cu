@@ -333,6 +333,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
+// The same value, which the compiler knows nothing of: a test of it inside a loop
+// does not make two loops (the roles' code has to stay in the instruction cache).
+template <typename T> __device__ __forceinline__ T opaque(T x)
+{
+    if constexpr (sizeof(T) == 8)
+        asm volatile("" : "+l"(x));
+    else
+        asm volatile("" : "+r"(x));
+    return x;
+}
+
 // Block of a request that position p >= 0 lies in: p / page_size by a product.
 __device__ __forceinline__ int block_of(const TreeArgs &a, int p)
 {
@@ -627,14 +638,15 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     // row by the copy warps.
     auto boxes_of = [&](const Work &w) { return a.idx || !a.box_rows ? 0 : w.ctx >> 7; };
     auto page_of = [&](int b, int p) {
-        if (!a.c.table)
+        const int32_t *table = opaque(a.c.table);
+        if (!table)
             return b;
-        return __ldg(a.c.table + (size_t)b * a.c.max_blocks + block_of(a, p));
+        return __ldg(table + (size_t)b * a.c.max_blocks + block_of(a, p));
     };
     auto row_of = [&](int h, int pos, int page) {       // -1: no such row
         if (pos < 0 || page < 0 || page >= a.c.num_pages)
             return -1;
-        const int in = a.c.table ? pos - block_of(a, pos) * a.c.page_size : pos;
+        const int in = opaque(a.c.table) ? pos - block_of(a, pos) * a.c.page_size : pos;
         return (page * a.Hkv + h) * a.c.page_size + in;
     };
 
@@ -708,10 +720,11 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     loaded = e + 1;
                     loaded_boxes = loaded_boxes << 1 | (box && !alone ? 1u : 0u);
                     const uint32_t dst = sm_ring + slot * kTileBytes;
-                    if (!box) {
+                    const int how = opaque(!box ? 0 : alone ? 2 : 1);
+                    if (how == 0) {
                         if (lane == 0)
                             bar_arrive(&x.go[ring][kv]);
-                    } else if (!alone) {
+                    } else if (how == 1) {
                         if (lane == 0) {
                             bar_expect(&x.full[slot], kTileBytes);
                             bar_arrive_n(&x.full[slot], 32 * C::kCopiers - 1);
@@ -766,7 +779,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             }
             if (a.c.table) {
                 const int32_t *p = a.c.table + (size_t)at.b * a.c.max_blocks;
-                const int blocks = (at.w.ctx + at.w.nt + a.c.page_size - 1) / a.c.page_size;
+                const int blocks = block_of(a, at.w.ctx + at.w.nt - 1) + 1;
 #pragma unroll 1
                 for (int j = lane * 32; j < blocks; j += 32 * 32)
                     prefetch_l2(p + j);
@@ -778,13 +791,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         for (bool first = true; ok && walk.left > 0; first = false) {
             const Work &w = walk.w;
             const int n = walk.count();
-            if (me == 0) {
-                Walk<MT> next = walk;
-                next.next(a, n);
-                if (next.left > 0)
-                    prefetch(next);
-            } else if (first) {
-                prefetch(walk);
+            {
+                Walk<MT> at = walk;
+                if (me == 0)
+                    at.next(a, n);
+                if (me == 0 ? at.left > 0 : first)
+                    prefetch(at);
             }
 #pragma unroll 1
             for (int i = max(0, boxes_of(w) - walk.t); i < n; ++i, ++tile) {
@@ -793,23 +805,28 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 const int t = walk.t + i, base = t * kTile;
                 const bool last = t == w.tiles - 1;
                 const int listed = last ? w.off : min(kTile, w.entries - base);   // context entries
-                int pos[4], row[4];
+                // Loads from valid places whether or not their value counts: no branches.
+                const int32_t *set = a.idx + ((size_t)walk.b * a.Hkv + walk.h) * a.top_k;
+                const int32_t *table = a.c.table + (size_t)walk.b * a.c.max_blocks;
+                const bool sparse = opaque((int)(a.idx != nullptr)), paged = opaque((int)(a.c.table != nullptr));
+                int pos[4], page[4], in[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int j = u * 32 + lane;
-                    if (j < listed)
-                        pos[u] = a.idx ? __ldg(a.idx + ((size_t)walk.b * a.Hkv + walk.h) * a.top_k + base + j)
-                                       : base + j;
-                    else
-                        pos[u] = last && j - w.off < w.nt ? w.ctx + j - w.off : -1;
+                    const int j = base + u * 32 + lane;
+                    pos[u] = sparse ? __ldg(set + min(j, a.top_k - 1)) : j;
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    if (u * 32 + lane < listed && pos[u] != -1 && (pos[u] < 0 || pos[u] >= w.ctx)) {
+                    const int j = u * 32 + lane;
+                    if (j >= listed)
+                        pos[u] = last && j - w.off < w.nt ? w.ctx + j - w.off : -1;
+                    else if (sparse && pos[u] != -1 && (uint32_t)pos[u] >= (uint32_t)w.ctx) {
                         flags |= kFlagIndexOutOfRange;
                         pos[u] = -1;
                     }
-                    row[u] = pos[u] < 0 ? -1 : page_of(walk.b, pos[u]);
+                    const int block = paged ? block_of(a, max(pos[u], 0)) : 0;
+                    in[u] = pos[u] - block * a.c.page_size;
+                    page[u] = paged ? __ldg(table + block) : walk.b;
                 }
                 const uint32_t ring = tile % kRing;
                 if (tile >= kRing)        // every copy warp has read the list before
@@ -818,13 +835,13 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     break;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    row[u] = row_of(walk.h, pos[u], row[u]);
-                    if (pos[u] >= 0 && row[u] < 0)
+                    const bool valid = pos[u] >= 0 && (uint32_t)page[u] < (uint32_t)a.c.num_pages;
+                    if (pos[u] >= 0 && !valid)
                         flags |= kFlagPageOutOfRange;
-                    const uint32_t there = __ballot_sync(kFull, row[u] >= 0);
+                    const uint32_t there = __ballot_sync(kFull, valid);
                     if (lane == 0)
                         x.rows_valid[ring][u] = there;
-                    x.rows[ring][u * 32 + lane] = row[u];
+                    x.rows[ring][u * 32 + lane] = valid ? (page[u] * a.Hkv + walk.h) * a.c.page_size + in[u] : -1;
                 }
                 __syncwarp();
                 if (lane == 0)
