@@ -333,6 +333,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
+// Two fp32 values times f.
+__device__ __forceinline__ void scale2(uint32_t *x, float f)
+{
+    const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(f, f));
+    x[0] = __float_as_uint(y.x);
+    x[1] = __float_as_uint(y.y);
+}
+
 // The same value, which the compiler knows nothing of: a test of it inside a loop
 // does not make two loops (the roles' code has to stay in the instruction cache).
 template <typename T> __device__ __forceinline__ T opaque(T x)
@@ -1107,14 +1115,17 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     const uint32_t v = sm_ring + entry % C::kSlots * kTileBytes + r * 128;
                     bool any = false;
                     if (r >= walk.w.off && r < walk.w.off + walk.w.nt) {
-#pragma unroll 2
+                        // largest magnitude bits of the row's even and odd values
+                        uint32_t top = 0;
+#pragma unroll 8
                         for (int c = 0; c < 16; ++c) {
                             uint32_t y4[4];
                             lds_words(v + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4), y4);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                any |= (y4[k] & 0x7f80u) == 0x7f80u || (y4[k] & 0x7f800000u) == 0x7f800000u;
+                                top = __vmaxu2(top, y4[k] & 0x7fff7fffu);
                         }
+                        any = (top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u;
                     }
                     const uint32_t bits = __ballot_sync(kFull, any);
                     if (lane == 0)
@@ -1229,8 +1240,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                     tmem_wait_ld();
                                     tmem_loaded(ov);
 #pragma unroll
-                                    for (int k = 0; k < 32; ++k)
-                                        ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+                                    for (int k = 0; k < 32; k += 2)
+                                        scale2(ov + k, f);
                                     tmem_st32(o + 32 * c, ov);
                                 }
                             }
@@ -1310,8 +1321,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         uint16_t *dst = a.out + (q0 + (size_t)tok * a.Hq + (row & (a.G - 1))) * kHeadDim + 32 * c;
                         uint32_t y[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            y[k] = pack_bf16(__uint_as_float(ov[2 * k]) * inv, __uint_as_float(ov[2 * k + 1]) * inv);
+                        for (int k = 0; k < 16; ++k) {
+                            scale2(ov + 2 * k, inv);
+                            y[k] = pack_bf16(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1]));
+                        }
                         const uint4 *v = reinterpret_cast<const uint4 *>(y);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
