@@ -739,14 +739,17 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         }
                         __syncwarp();
                         const TmaDesc *map = kv ? &a.box_v : &a.box_k;
+                        int next = __shfl_sync(kFull, row[0], 0);
+                        uint32_t d = dst;
 #pragma unroll 1
-                        for (int k = 0; k < 1 << shift; ++k) {     // (each lane its own: 20% slower)
-                            const int r = __shfl_sync(kFull, row[0], k);
-                            const uint32_t d = dst + k * a.box_rows * 128;
+                        for (int k = 1; k <= 1 << shift; ++k) {    // (each lane its own: 20% slower)
+                            const int r = next;
+                            next = __shfl_sync(kFull, row[0], k & 31);
                             if (elect_one()) {
                                 tma_box(d, map, 0, r, &x.full[slot]);
                                 tma_box(d + kHalfBytes, map, 64, r, &x.full[slot]);
                             }
+                            d += a.box_rows * 128;
                         }
                     } else {
 #pragma unroll 1
