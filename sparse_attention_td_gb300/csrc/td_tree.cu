@@ -622,10 +622,18 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     // segment's comes in during this one.  (The MMA reads 128 rows from either;
     // the rows that are not Q's end in S and O rows that nobody reads.)
     const bool two_q = MT == 1 && a.part_rows <= 64;
-    uint32_t loaded = 0;          // loader: ring entries begun
+    uint32_t loaded = 0;          // loaders: ring entries begun
     uint32_t loaded_boxes = 0;    // which of the last ones came as boxes (bit 0: the last)
     uint32_t tmem = 0;
     const bool issuer = warp == C::kIssuer || (MT > 1 && warp == C::kIssuer1);
+    // Boxes of 8 or 16 rows are more than one warp can issue (80 cycles each).  In full
+    // layers with one row tile the second finder has little to do and loads V, the
+    // loader K; the ring's number of slots is even, so each has slots of its own.
+    // 32 requests of 8K-16K, G = 4, 16 nodes, one / two loaders: 8-token pages 412 /
+    // 258 us, 16: 279 / 253, 32: 251 / 253, 64: 250 / 257 (K then runs ahead of V).
+    const bool split = MT == 1 && !a.idx && a.box_rows && a.box_rows <= 16;
+    const bool loads_v = split && warp == C::kFinder + 1;
+    static_assert(MT > 1 || C::kSlots % 2 == 0, "slots of K and of V");
     if (warp < C::kSoftWarps || issuer) {
         // tensor memory for the roles that use it, while the others begin
         if (warp == C::kIssuer) {
@@ -658,7 +666,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         return (page * a.Hkv + h) * a.c.page_size + in;
     };
 
-    if (warp == C::kLoader) {
+    if (warp == C::kLoader || loads_v) {
         // ---- loader: waits for the ring's slots, in order, and fills them with boxes
         // or lets the copy warps go.  (Row gathers by TMA took 60 ns per four half
         // rows, 7.7 us a tile.)  Page numbers of the boxes are read 32 at a time, a
@@ -667,6 +675,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         const int shift = a.box_rows ? __ffs(kTile / a.box_rows) - 1 : 0;     // log2(boxes per tile)
         const int batch = 32 >> shift;                                        // tiles per 32 boxes
         auto box_pos = [&](int t, int box) { return t * kTile + box * a.box_rows; };
+        const int kv0 = loads_v ? 1 : 0, kv1 = split ? kv0 + 1 : 2;
         uint32_t tile_no = 0, copied = 0, flags = 0;       // tiles; tiles for the copy warps
         bool ok = true;
 #pragma unroll 1
@@ -716,7 +725,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     word = x.rows_valid[ring][lane & 3];
                 }
 #pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv) {
+                for (int kv = kv0; kv < kv1; ++kv) {
                     const uint32_t e = 2 * tile_no + kv, slot = e % C::kSlots, use = e / C::kSlots;
                     if (use > 0)
                         ok = __all_sync(kFull, bar_wait(&x.empty[slot], (use - 1) & 1, gave_up));
@@ -725,7 +734,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     if (kv == 0 && lane < 4)
                         x.valid[tile_no % kMaskRing][lane] = word;
                     __syncwarp();
-                    loaded = e + 1;
+                    ++loaded;
                     loaded_boxes = loaded_boxes << 1 | (box && !alone ? 1u : 0u);
                     const uint32_t dst = sm_ring + slot * kTileBytes;
                     const int how = opaque(!box ? 0 : alone ? 2 : 1);
@@ -773,11 +782,11 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         if (flags && lane == 0)
             atomicOr(a.status, flags);
     } else if (warp >= C::kFinder && warp < C::kFinder + C::kFinders) {
-        // ---- finders: the cache rows of every kFinders-th tile for the copy warps, as
+        // ---- finders (one or two): the cache rows of the tiles for the copy warps, as
         // far ahead as there are lists.  (Memory is slow to answer while every SM's
         // ring fills: found by the copy warps themselves, between two tiles, the rows
         // cost 1500 to 3000 cycles a tile.)
-        const int me = warp - C::kFinder;
+        const int me = warp - C::kFinder, finders = split ? 1 : C::kFinders;
         constexpr uint32_t kRing = C::kRowRing;
         // Index entries and page numbers of a segment into L2 before they are needed.
         auto prefetch = [&](const Walk<MT> &at) {
@@ -811,7 +820,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             }
 #pragma unroll 1
             for (int i = max(0, boxes_of(w) - walk.t); i < n; ++i, ++tile) {
-                if (tile % C::kFinders != (uint32_t)me)
+                if (finders > 1 && (tile & 1) != (uint32_t)me)
                     continue;
                 const int t = walk.t + i, base = t * kTile;
                 const bool last = t == w.tiles - 1;
@@ -1354,15 +1363,17 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     tmem_before();
     __syncthreads();
     if (x.gave_up) {
-        // A wait gave up: leave no copy and no MMA in flight.  Of the boxes the ring's
-        // last entries can be; what was issued does complete, and these waits have
-        // the default limit.
+        // A wait gave up: leave no copy and no MMA in flight.  Of the boxes the last
+        // entries of a loader's slots can be; what was issued does complete, and these
+        // waits have the default limit.
         constexpr long long kLimit = 2000000000ll;
         int own_limit = 0;
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (warp == C::kLoader) {
-            for (uint32_t e = loaded > C::kSlots ? loaded - C::kSlots : 0; e < loaded; ++e) {
-                if (loaded_boxes >> (loaded - 1 - e) & 1)
+        if (warp == C::kLoader || loads_v) {
+            const uint32_t slots = split ? C::kSlots / 2 : C::kSlots;
+            for (uint32_t n = loaded > slots ? loaded - slots : 0; n < loaded; ++n) {
+                const uint32_t e = split ? 2 * n + (loads_v ? 1 : 0) : n;
+                if (loaded_boxes >> (loaded - 1 - n) & 1)
                     bar_wait_for(&x.full[e % C::kSlots], (e / C::kSlots) & 1, &own_limit, kLimit);
             }
         } else if (issuer && elect_one()) {      // (the lane that issued them)

@@ -206,3 +206,52 @@ def test_rows_behind_32_bit_offsets():
                 assert torch.equal(got[int(table[b, at // page]), :, at % page].cpu(), x[b, :, src])
     del kc, vc, cache
     torch.cuda.empty_cache()
+
+
+def test_captured_behind_other_work():
+    """The calls of a step captured behind a fill, a copy and another stream's work, each of which
+    writes what the call reads."""
+    from test_spec_gpu import i32
+    from spec_util import pack_mask
+    c = tree_case(31, 4, 2, [900, 333], [8, 5], 8, 16, "tree")
+    shape = td.make_shape(2, 8, 2, c["N"])
+    ws = td.Workspace(shape, 0, tree_size=8)
+    pages, _, page, _ = c["kc"].shape
+    rows = [x.permute(0, 2, 1, 3).reshape(pages * page, 2, D).contiguous().cuda() for x in (c["kc"], c["vc"])]
+    k, v = torch.zeros_like(c["kc"]).cuda(), torch.zeros_like(c["vc"]).cuda()
+    cache = td.make_cache(k, v, c["table"].cuda())
+    slots = torch.full((pages * page,), -1, dtype=torch.int32, device="cuda")
+    staged = torch.arange(pages * page, dtype=torch.int32, device="cuda")
+    q, q_in = torch.zeros_like(c["q"]).cuda(), c["q"].cuda()
+    lens, lens_in, sizes = i32([0, 0]), i32(c["lens"]), i32(c["sizes"])
+    mask, out = pack_mask(c["seen"]).cuda(), torch.full_like(q, 7.0)
+    kept, kept_lens, after = i32([[1, 3, 4, 0, 0, 0, 0, 0]] * 2), i32([3, 2]), i32([0, 0])
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        k.zero_(), v.zero_(), out.fill_(7.0)                # fills
+        slots.copy_(staged)                                 # a copy right before the call
+        td.td_kv_append_slots(shape, cache, rows[0], rows[1], slots)
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            q.copy_(q_in)
+            lens.copy_(lens_in)
+        main.wait_stream(other)                             # the call's inputs come from another stream
+        td.td_tree_attn(shape, cache, 8, sizes, mask, q, lens, out, ws)
+        td.td_tree_commit(shape, [cache], 8, sizes, kept, kept_lens, lens, after, ws)
+        lens.zero_()                                        # what the calls read, right behind them
+        q.zero_()
+    for _ in range(5):
+        out.zero_()
+        after.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    check_tree(c, out)
+    assert after.tolist() == [900 - 8 + 3, 333 - 5 + 2] and ws.status() == 0
+    for b, n in enumerate(c["lens"]):
+        ctx = n - c["sizes"][b]
+        for i, j in enumerate([1, 3, 4][:3 if b == 0 else 2]):
+            at = ctx + i
+            assert torch.equal(k[int(c["table"][b, at // page]), :, at % page].cpu(), c["K"][b, :, ctx + j])
