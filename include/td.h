@@ -420,7 +420,7 @@ size_t td_tree_workspace_size(const td_shape *shape, int32_t tree_size);
  *              (page_size for a NULL block_table).
  * K/V values at positions a row does not see never reach it, whatever they
  * hold (infinities and NaN included).  The probabilities enter the second
- * product as bf16 (relative error 2^-9 each); scores, softmax statistics and
+ * product as bf16 (relative error at most 2^-8 each); scores, softmax statistics and
  * sums are fp32.
  */
 td_status td_tree_attn(const td_shape *shape, const td_cache *cache, int32_t tree_size,

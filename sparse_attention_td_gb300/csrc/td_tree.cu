@@ -13,7 +13,7 @@
 // the M side of two matrix products per tile of 128 tokens: S = Q K^T and
 // O += P V, on the tensor cores (tcgen05.mma, 128 query rows; S, P and O in
 // tensor memory, K and V tiles in shared memory).  P is rounded to bf16, the
-// products' operand type (relative error 2^-9, as the value rows carry already);
+// products' operand type (relative error at most 2^-8, as in the rows themselves);
 // S, O, m and l are fp32.
 //
 // What bounds it, measured on GB300 (a copy of the same bytes runs at 6.7 TB/s):
@@ -21,13 +21,17 @@
 //     32 requests of 8K-16K, 8 KV heads, G = 4, 16 nodes, 64-token pages: 248 us, 6.6 TB/s
 //     one request of 100K, 32 KV heads, G = 1, 32 nodes:                  242 us, 6.9 TB/s
 //   the softmax, where it has more (two row tiles):
-//     4 x 32K, 8 KV heads, G = 4, 64 nodes:            129 us, 4.1 TB/s, 1.0 PFLOP/s
+//     4 x 32K, 8 KV heads, G = 4, 64 nodes:            124 us, 4.2 TB/s, 1.1 PFLOP/s
 //   launch, first loads and the join, where a step is short:
-//     4 x 257-2050, 8 KV heads, G = 8, one node, 16-token pages:  16 us
-//     4 x 32K, G = 4, 2048 index entries, 5 nodes:                18 us
+//     4 x 257-2050, 8 KV heads, G = 8, one node, 16-token pages:  15 us
+//     4 x 32K, G = 4, 2048 index entries, 5 nodes:                17 us
 //     (the two launches alone, every CTA leaving at once:         4.5 us)
-//   copies of single rows, where an index set names them:
-//     32 requests, G = 4, 1024 index entries, 16 nodes:  45 to 49 us, 3.1 TB/s
+//   copies of single rows, where an index set names them, and the ends of units:
+//     32 requests, G = 4, 1024 index entries, 16 nodes:  39 us, 3.7 TB/s
+// The roles' code together does not fit an SM's instruction cache: on the last of
+// these 18% of its requests missed with 100 KB of code, and with 80 KB (waits and
+// unit changes out of line, loops left rolled, no branches where a selection does)
+// it takes 39 us instead of 50.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -53,18 +57,18 @@ constexpr int kMaskRing = 8;                     // tiles whose validity masks a
 // there when a step's softmax ends.  Two row tiles, 128 columns each: one S of 64
 // columns, which is free again as soon as the softmax has its values in registers,
 // and two P buffers.  (Two S buffers with P over them, S of a step waiting for P V
-// of the one before the last: 136 us instead of 129 for 4 x 32K tokens, 64 nodes.)
+// of the one before the last: 5% slower for 4 x 32K tokens, 64 nodes.)
 template <int MT> struct Cfg {
     static constexpr int kSlots = MT == 1 ? 6 : 5;
     static constexpr int kStep = MT == 1 ? 128 : 64;
     static constexpr int kSteps = kTile / kStep;      // per tile
     static constexpr int kSoftWarps = 4 * MT;
-    // softmax, the loader, the MMA issuer, row finders, copy warps: 12 or 16 warps
-    // Copy warps in the third and fourth sub-partition (warp % 4): their queue of
-    // copies slows the other warps there, and the first two have the first 64 rows.
+    // Warps: softmax, the loader, an MMA issuer per row tile, row finders, copy warps;
+    // 12 or 16.  Copy warps in the third and fourth sub-partition (warp % 4): their
+    // queue of copies slows the other warps there, and the first two have the first 64
+    // rows.  The two issuers in different ones: both in one slowed its softmax warps,
+    // and with them the row tiles (136 us instead of 129 at the time).
     static constexpr int kLoader = kSoftWarps, kIssuer = kSoftWarps + 1;
-    // An issuer per row tile, in sub-partitions of their own: both in one slowed its
-    // softmax warps to 2300 cycles a step, and with them the row tiles.
     static constexpr int kIssuer1 = kSoftWarps + 7;
     static constexpr int kFinder = kSoftWarps + 4, kFinders = MT == 1 ? 2 : 1, kCopiers = 4;
     static constexpr int kRowRing = 4;                // tiles whose row lists are alive
@@ -480,8 +484,10 @@ template <int MT> struct Extra {
 
 // One CTA per SM; each takes an equal, contiguous range of the batch's tiles
 // (a range may cover several units and end inside one: those units' partial
-// results are joined by tree_join_kernel).  Roles: 4 * MT softmax warps (one
-// query row per thread), the loader, the copy warps, the MMA issuer.
+// results are joined by tree_join_kernel): the longest request decides nothing, and
+// the SMs end together.  Roles: 4 * MT softmax warps (one query row per thread), the
+// loader, the row finders and copy warps for tiles that no box holds, and an MMA
+// issuer per row tile; they meet at barriers in shared memory only.
 template <int MT>
 __global__ void __launch_bounds__(Cfg<MT>::kThreads, 1)
 tree_attention_kernel(const __grid_constant__ TreeArgs a)
@@ -657,7 +663,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         const int32_t *table = opaque(a.c.table);
         if (!table)
             return b;
-        return __ldg(table + (size_t)b * a.c.max_blocks + block_of(a, p));
+        return table[(size_t)b * a.c.max_blocks + block_of(a, p)];
     };
     auto row_of = [&](int h, int pos, int page) {       // -1: no such row
         if (pos < 0 || page < 0 || page >= a.c.num_pages)
@@ -826,6 +832,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 const bool last = t == w.tiles - 1;
                 const int listed = last ? w.off : min(kTile, w.entries - base);   // context entries
                 // Loads from valid places whether or not their value counts: no branches.
+                // (Plain ones: the kernel before may have written these while this one began.)
                 const int32_t *set = a.idx + ((size_t)walk.b * a.Hkv + walk.h) * a.top_k;
                 const int32_t *table = a.c.table + (size_t)walk.b * a.c.max_blocks;
                 const bool sparse = opaque((int)(a.idx != nullptr)), paged = opaque((int)(a.c.table != nullptr));
@@ -833,7 +840,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int j = base + u * 32 + lane;
-                    pos[u] = sparse ? __ldg(set + min(j, a.top_k - 1)) : j;
+                    pos[u] = sparse ? set[min(j, a.top_k - 1)] : j;
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -846,7 +853,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     }
                     const int block = paged ? block_of(a, max(pos[u], 0)) : 0;
                     in[u] = pos[u] - block * a.c.page_size;
-                    page[u] = paged ? __ldg(table + block) : walk.b;
+                    page[u] = paged ? table[block] : walk.b;
                 }
                 const uint32_t ring = tile % kRing;
                 if (tile >= kRing)        // every copy warp has read the list before
