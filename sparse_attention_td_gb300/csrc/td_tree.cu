@@ -547,6 +547,13 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_wait();
+    {   // the batch's page numbers and index entries into L2, a line per thread of the grid
+        const size_t at = ((size_t)blockIdx.x * C::kThreads + tid) * 32;
+        if (a.c.table && at < (size_t)a.B * a.c.max_blocks)
+            prefetch_l2(a.c.table + at);
+        if (a.idx && at < (size_t)a.B * a.Hkv * a.top_k)
+            prefetch_l2(a.idx + at);
+    }
     // ---- the CTA's range: requests in equal runs per thread, prefix sums.  (The
     // host has made sure that the number of tiles fits 31 bits.)
     {
@@ -701,9 +708,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 const int t = walk.t + i;
                 const bool box = t < boxes;
                 const uint32_t ring = copied % C::kRowRing;
-                int row[4] = {-1, -1, -1, -1};
+                int row = 0;                                // of the lane's box
                 uint32_t word = kFull;                      // lane < 4: tokens 32 * lane ..
-                bool alone = false;                         // a box tile with a bad page: row by row, here
                 if (box) {
                     if (t == first + batch) {
                         first = t;
@@ -712,16 +718,16 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     }
                     const int mine = lane & ((1 << shift) - 1);
                     const int page = __shfl_sync(kFull, pages, ((t - first) << shift) + mine);
-                    row[0] = row_of(walk.h, box_pos(t, mine), page);
-                    alone = __any_sync(kFull, row[0] < 0);
-                    if (alone) {
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int p = t * kTile + u * 32 + lane;
-                            row[u] = row_of(walk.h, p, page_of(walk.b, p));
-                            const uint32_t there = __ballot_sync(kFull, row[u] >= 0);
-                            word = lane == u ? there : word;
-                        }
+                    row = row_of(walk.h, box_pos(t, mine), page);
+                    const uint32_t there = __ballot_sync(kFull, row >= 0);
+                    if (there != kFull) {
+                        // a box of a page that does not exist lies behind the cache's rows,
+                        // where the map fills with zeros; its tokens do not exist
+                        row = row >= 0 ? row : a.c.num_pages * a.Hkv * a.c.page_size;
+                        word = 0;
+                        for (int k = 0; k < 4; ++k)
+                            if (there >> ((32 * (lane & 3) + 8 * k) >> (7 - shift)) & 1u)
+                                word |= 0xffu << 8 * k;
                         flags |= kFlagPageOutOfRange;
                     }
                 } else {
@@ -741,41 +747,30 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         x.valid[tile_no % kMaskRing][lane] = word;
                     __syncwarp();
                     ++loaded;
-                    loaded_boxes = loaded_boxes << 1 | (box && !alone ? 1u : 0u);
+                    loaded_boxes = loaded_boxes << 1 | (box ? 1u : 0u);
                     const uint32_t dst = sm_ring + slot * kTileBytes;
-                    const int how = opaque(!box ? 0 : alone ? 2 : 1);
-                    if (how == 0) {
+                    if (!box) {
                         if (lane == 0)
                             bar_arrive(&x.go[ring][kv]);
-                    } else if (how == 1) {
+                    } else {
                         if (lane == 0) {
                             bar_expect(&x.full[slot], kTileBytes);
                             bar_arrive_n(&x.full[slot], 32 * C::kCopiers - 1);
                         }
                         __syncwarp();
                         const TmaDesc *map = kv ? &a.box_v : &a.box_k;
-                        int next = __shfl_sync(kFull, row[0], 0);
+                        int next = __shfl_sync(kFull, row, 0);
                         uint32_t d = dst;
 #pragma unroll 1
                         for (int k = 1; k <= 1 << shift; ++k) {    // (each lane its own: 20% slower)
                             const int r = next;
-                            next = __shfl_sync(kFull, row[0], k & 31);
+                            next = __shfl_sync(kFull, row, k & 31);
                             if (elect_one()) {
                                 tma_box(d, map, 0, r, &x.full[slot]);
                                 tma_box(d + kHalfBytes, map, 64, r, &x.full[slot]);
                             }
                             d += a.box_rows * 128;
                         }
-                    } else {
-#pragma unroll 1
-                        for (int j = 0; j < kTile / 2; ++j) {
-                            const int tok = 2 * j + (lane >> 4);
-                            const int from = j < 16 ? row[0] : j < 32 ? row[1] : j < 48 ? row[2] : row[3];
-                            copy_row(dst, tok, kv ? a.c.v : a.c.k, __shfl_sync(kFull, from, tok & 31), lane);
-                        }
-                        copies_arrive(&x.full[slot]);
-                        if (lane == 0)
-                            bar_arrive_n(&x.full[slot], 32 * C::kCopiers - 32);
                     }
                     __syncwarp();
                 }
@@ -794,36 +789,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         // cost 1500 to 3000 cycles a tile.)
         const int me = warp - C::kFinder, finders = split ? 1 : C::kFinders;
         constexpr uint32_t kRing = C::kRowRing;
-        // Index entries and page numbers of a segment into L2 before they are needed.
-        auto prefetch = [&](const Walk<MT> &at) {
-            const int first = at.t * kTile, tokens = at.count() * kTile;
-            if (a.idx) {
-                const int32_t *p = a.idx + ((size_t)at.b * a.Hkv + at.h) * a.top_k;
-#pragma unroll 1
-                for (int j = first + lane * 32; j < min(first + tokens, a.top_k); j += 32 * 32)
-                    prefetch_l2(p + j);
-            }
-            if (a.c.table) {
-                const int32_t *p = a.c.table + (size_t)at.b * a.c.max_blocks;
-                const int blocks = block_of(a, at.w.ctx + at.w.nt - 1) + 1;
-#pragma unroll 1
-                for (int j = lane * 32; j < blocks; j += 32 * 32)
-                    prefetch_l2(p + j);
-            }
-        };
         uint32_t flags = 0, tile = 0;      // tile: number of the copied tile
         bool ok = true;
 #pragma unroll 1
-        for (bool first = true; ok && walk.left > 0; first = false) {
+        while (ok && walk.left > 0) {
             const Work &w = walk.w;
             const int n = walk.count();
-            {
-                Walk<MT> at = walk;
-                if (me == 0)
-                    at.next(a, n);
-                if (me == 0 ? at.left > 0 : first)
-                    prefetch(at);
-            }
 #pragma unroll 1
             for (int i = max(0, boxes_of(w) - walk.t); i < n; ++i, ++tile) {
                 if (finders > 1 && (tile & 1) != (uint32_t)me)
