@@ -362,9 +362,10 @@ __device__ __forceinline__ int block_of(const TreeArgs &a, int p)
     return (int)((uint64_t)(uint32_t)p * a.page_magic >> a.page_shift);
 }
 
-// What a drafted token's V values that are not finite add to 32 dims of the
-// output rows that see it (rare; kept out of the caller's code).
-__device__ __noinline__ void add_not_finite(const TreeArgs &a, int b, int h, int pos, int dim, uint32_t *o)
+// What a drafted token's V values that are not finite add to an output row that
+// sees it, written already, as fp32 partial sums or (part null) as the result.
+// Rare; out of line, as is the next one, to keep the roles' code short.
+__device__ __noinline__ void add_not_finite(const TreeArgs &a, int b, int h, int pos, float *part, uint16_t *out)
 {
     int page = b, r = pos;
     if (a.c.table) {
@@ -374,10 +375,36 @@ __device__ __noinline__ void add_not_finite(const TreeArgs &a, int b, int h, int
     }
     if (page < 0 || page >= a.c.num_pages)
         return;
-    const uint16_t *v = a.c.v + (((size_t)page * a.Hkv + h) * a.c.page_size + r) * kHeadDim + dim;
-    for (int k = 0; k < 32; ++k)
-        if ((v[k] & 0x7f80) == 0x7f80)
-            o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float((uint32_t)v[k] << 16));
+    const uint16_t *v = a.c.v + (((size_t)page * a.Hkv + h) * a.c.page_size + r) * kHeadDim;
+#pragma unroll 1
+    for (int k = 0; k < kHeadDim; ++k) {
+        if ((v[k] & 0x7f80) != 0x7f80)
+            continue;
+        const float x = __uint_as_float((uint32_t)v[k] << 16);
+        if (part)
+            part[k] += x;
+        else
+            out[k] = (uint16_t)pack_bf16(__uint_as_float((uint32_t)out[k] << 16) + x, 0.0f);
+    }
+}
+
+// Takes the values that are not finite out of row r of a V tile.
+__device__ __noinline__ void clear_not_finite(uint32_t row, int r)
+{
+#pragma unroll 1
+    for (int c = 0; c < 16; ++c) {
+        uint32_t x[4];
+        const uint32_t at = row + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4);
+        lds_words(at, x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if ((x[k] & 0x7f80u) == 0x7f80u)
+                x[k] &= 0xffff0000u;
+            if ((x[k] & 0x7f800000u) == 0x7f800000u)
+                x[k] &= 0xffffu;
+        }
+        sts4(at, x[0], x[1], x[2], x[3]);
+    }
 }
 
 // ---- work: units (request, KV head, block of query rows), each a run of tiles
@@ -1131,21 +1158,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         }
                     }
                     if (m == 0 && bits) {
-                        if (any) {
-                            for (int c = 0; c < 16; ++c) {
-                                uint32_t y4[4];
-                                const uint32_t at = v + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4);
-                                lds_words(at, y4);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    if ((y4[k] & 0x7f80u) == 0x7f80u)
-                                        y4[k] &= 0xffff0000u;
-                                    if ((y4[k] & 0x7f800000u) == 0x7f800000u)
-                                        y4[k] &= 0xffffu;
-                                }
-                                sts4(at, y4[0], y4[1], y4[2], y4[3]);
-                            }
-                        }
+                        if (any)
+                            clear_not_finite(v, r);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
                     __syncwarp();
@@ -1280,11 +1294,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 const int part = 2 * blockIdx.x + (walk.first ? 0 : 1);
                 const size_t prow = (size_t)part * a.part_rows + m * kTile + r;
-                uint32_t bad[4] = {0, 0, 0, 0};
-                if (has_tree)
-#pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        bad[w] = x.badv[m][(tile_no + n - 1) & 3][w] & sees[w];
+                uint16_t *out = a.out + (q0 + (size_t)tok * a.Hq + (row & (a.G - 1))) * kHeadDim;
+                float *part_o = a.part_o + prow * kHeadDim;
                 const uint32_t o = tmem + C::col_o(m) + lanes;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -1292,23 +1303,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     tmem_ld32(o + 32 * c, ov);
                     tmem_wait_ld();
                     tmem_loaded(ov);
-                    if (live && (bad[0] | bad[1] | bad[2] | bad[3])) {
-#pragma unroll 1
-                        for (int j = walk.w.off; j < walk.w.off + walk.w.nt; ++j) {
-                            if (!((j < 64 ? (j < 32 ? bad[0] : bad[1]) : (j < 96 ? bad[2] : bad[3])) >> (j & 31) & 1u))
-                                continue;
-                            uint32_t add[32];
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                add[k] = ov[k];
-                            add_not_finite(a, b, h, walk.w.ctx + j - walk.w.off, 32 * c, add);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                ov[k] = add[k];
-                        }
-                    }
                     if (live && whole) {
-                        uint16_t *dst = a.out + (q0 + (size_t)tok * a.Hq + (row & (a.G - 1))) * kHeadDim + 32 * c;
+                        uint16_t *dst = out + 32 * c;
                         uint32_t y[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
@@ -1320,7 +1316,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         for (int k = 0; k < 4; ++k)
                             reinterpret_cast<uint4 *>(dst)[k] = v[k];
                     } else if (live) {
-                        float *dst = a.part_o + prow * kHeadDim + 32 * c;
+                        float *dst = part_o + 32 * c;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             store32(dst + 8 * k, ov + 8 * k);
@@ -1331,6 +1327,16 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     a.part_m[prow] = mref;
                     a.part_l[prow] = l;
                 }
+                if (has_tree && live) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t bad = x.badv[m][(tile_no + n - 1) & 3][w] & sees[w];
+                        for (; bad; bad &= bad - 1)
+                            add_not_finite(a, b, h, walk.w.ctx + 32 * w + __ffs(bad) - 1 - walk.w.off,
+                                           whole ? nullptr : part_o, out);
+                    }
+                }
+                __syncwarp();
                 tmem_before();
             }
             __syncwarp();
