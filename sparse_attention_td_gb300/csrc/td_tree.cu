@@ -23,15 +23,15 @@
 //   the softmax, where it has more (two row tiles):
 //     4 x 32K, 8 KV heads, G = 4, 64 nodes:            124 us, 4.2 TB/s, 1.1 PFLOP/s
 //   launch, first loads and the join, where a step is short:
-//     4 x 257-2050, 8 KV heads, G = 8, one node, 16-token pages:  15 us
-//     4 x 32K, G = 4, 2048 index entries, 5 nodes:                17 us
+//     4 x 257-2050, 8 KV heads, G = 8, one node, 16-token pages:  14.4 us
+//     4 x 32K, G = 4, 2048 index entries, 5 nodes:                16.6 us
 //     (the two launches alone, every CTA leaving at once:         4.5 us)
 //   copies of single rows, where an index set names them, and the ends of units:
-//     32 requests, G = 4, 1024 index entries, 16 nodes:  39 us, 3.7 TB/s
+//     32 requests, G = 4, 1024 index entries, 16 nodes:  37.4 us, 3.9 TB/s
 // The roles' code together does not fit an SM's instruction cache: on the last of
-// these 18% of its requests missed with 100 KB of code, and with 80 KB (waits and
-// unit changes out of line, loops left rolled, no branches where a selection does)
-// it takes 39 us instead of 50.
+// these 18% of its requests missed with 100 KB of code, and with 70 KB (waits, unit
+// changes and rare cases out of line, loops left rolled, no branches where a selection
+// does) it takes 37 us instead of 50.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
