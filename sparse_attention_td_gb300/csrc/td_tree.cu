@@ -573,6 +573,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         bar_init(&x.never, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    __syncthreads();
     pdl_wait();
     {   // the batch's page numbers and index entries into L2, a line per thread of the grid
         const size_t at = ((size_t)blockIdx.x * C::kThreads + tid) * 32;
@@ -581,12 +582,14 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         if (a.idx && at < (size_t)a.B * a.Hkv * a.top_k)
             prefetch_l2(a.idx + at);
     }
-    // ---- the CTA's range: requests in equal runs per thread, prefix sums.  (The
-    // host has made sure that the number of tiles fits 31 bits.)
+    // ---- the CTA's range: requests in equal runs per thread, prefix sums of their
+    // tiles.  (The host has made sure that the number of tiles fits 31 bits.)
+    Walk<MT> walk;
+    uint32_t bad = 0;
+    int per, start;
     {
         const int run = (a.B + C::kThreads - 1) / C::kThreads;
         const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
-        uint32_t bad = 0;
         int mine = 0;
         Work w{};
 #pragma unroll 1
@@ -594,8 +597,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             w = work_of<MT>(a, b, bad);
             mine += w.tiles * w.blocks * a.Hkv;
         }
-        if (bad && blockIdx.x == 0)
-            atomicOr(a.status, bad);
         int inc = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -614,8 +615,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 at += y;
             total += y;
         }
-        const int per = (uint32_t)(total + gridDim.x - 1) / gridDim.x;
-        const int start = blockIdx.x * per;
+        per = (uint32_t)(total + gridDim.x - 1) / gridDim.x;
+        start = blockIdx.x * per;
         if (start < total && at <= start && start - at < mine) {
             int b = b0;
             if (run > 1) {
@@ -639,25 +640,27 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             x.start = s;
         }
         __syncthreads();
-        pdl_launch_dependents();
-        if (tid == C::kThreads - 1) {
-            // The unit that this cut goes through, if it is the unit's first cut.
-            JoinPlan j{};
-            const int first = x.start.t;
-            if (x.start.left > 0 && first > 0 && first <= per) {
-                j.rows = x.start.rows(a);
-                j.b = x.start.b;
-                j.h = x.start.h;
-                j.row0 = x.start.m * MT * kTile;
-                // the last range that meets the unit
-                j.last = (uint32_t)(start - first + x.start.w.tiles - 1) / (uint32_t)per;
-                j.late = first < per;
-            }
-            a.plan[blockIdx.x] = j;
-        }
-        __syncwarp();
+        walk = x.start;
     }
-    Walk<MT> walk = x.start;
+    pdl_launch_dependents();
+    if (bad && blockIdx.x == 0)
+        atomicOr(a.status, bad);
+    if (tid == C::kThreads - 1) {
+        // The unit that this cut goes through, if it is the unit's first cut.
+        JoinPlan j{};
+        const int first = walk.t;
+        if (walk.left > 0 && first > 0 && first <= per) {
+            j.rows = walk.rows(a);
+            j.b = walk.b;
+            j.h = walk.h;
+            j.row0 = walk.m * MT * kTile;
+            // the last range that meets the unit
+            j.last = (uint32_t)(start - first + walk.w.tiles - 1) / (uint32_t)per;
+            j.late = first < per;
+        }
+        a.plan[blockIdx.x] = j;
+    }
+    __syncwarp();
     // Up to 64 query rows per unit: Q has two buffers of 64 rows, and the next
     // segment's comes in during this one.  (The MMA reads 128 rows from either;
     // the rows that are not Q's end in S and O rows that nobody reads.)
@@ -1404,6 +1407,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             ms[u] = -CUDART_INF_F;
+            ls[u] = 0.0f;
             if (s0 + u < parts) {
                 const size_t p = part_row(s0 + u);
                 ms[u] = a.part_m[p];
@@ -1424,7 +1428,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const float f = safe_exp2_diff(ms[u], mn);
-            if (f != 0.0f) {      // an empty part has nothing to add
+            // an empty part has nothing to add; one whose scores are all NaN has no maximum
+            if (f != 0.0f || ls[u] != ls[u]) {
                 l += ls[u] * f;
                 o.x += x[u].x * f;
                 o.y += x[u].y * f;

@@ -255,3 +255,17 @@ def test_captured_behind_other_work():
         for i, j in enumerate([1, 3, 4][:3 if b == 0 else 2]):
             at = ctx + i
             assert torch.equal(k[int(c["table"][b, at // page]), :, at % page].cpu(), c["K"][b, :, ctx + j])
+
+
+@pytest.mark.parametrize("n", [40, 9000])
+def test_a_query_row_that_is_not_a_number_says_so(n):
+    """In a request that one block does, and in one that is joined from the parts of many."""
+    c = tree_case(17, 4, 1, [n], [6], 6, 0, "tree")
+    q = c["q"].clone()
+    c["q"][0, 2, 1, 7] = float("nan")
+    out, ws = run_tree(c)
+    row = out[0, 2, 1].clone()
+    assert torch.isnan(row).all() and ws.status() == 0
+    c["q"] = q
+    out[0, 2, 1] = run_tree(c)[0][0, 2, 1]
+    check_tree(c, out)
