@@ -990,6 +990,7 @@ float host_scale(const td_shape &s) { return effective_scale(s); }
 int host_sm_count() { return device_sm_count(); }
 int host_wait_limit_us() { return g_tuning.wait_limit_us > 0 ? g_tuning.wait_limit_us : 1000000; }
 bool host_wait_test() { return g_tuning.wait_test != 0; }
+bool host_pdl() { return g_tuning.pdl != 0; }
 bool host_box_map(TmaDesc *out, const void *base, long rows, int box_rows)
 {
     EncodeTiledFn fn = encode_tiled();

@@ -124,9 +124,10 @@ __device__ __forceinline__ TreeLens tree_lens_of(const int32_t *seq_lens, const 
 td_status host_check_shape(const td_shape *s);
 float host_scale(const td_shape &s);
 int host_sm_count();
-// The tuning keys "wait_limit_us" (1 s by default) and "wait_test".
+// The tuning keys "wait_limit_us" (1 s by default), "wait_test" and "pdl".
 int host_wait_limit_us();
 bool host_wait_test();
+bool host_pdl();
 // Tensor map over `rows` rows of 128 bf16 values: boxes of 64 values x box_rows
 // rows, 128-byte swizzle, zero fill past the end.
 bool host_box_map(TmaDesc *out, const void *base, long rows, int box_rows);

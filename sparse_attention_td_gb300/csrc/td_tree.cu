@@ -48,7 +48,7 @@ namespace {
 constexpr int kTile = 128;                       // tokens per tile, and query rows per row tile
 constexpr int kHalfBytes = kTile * 128;          // one 64-value half of a tile's rows
 constexpr int kTileBytes = 2 * kHalfBytes;       // 128 rows of 128 bf16 values
-constexpr int kMaskRing = 8;                     // tiles whose validity masks are alive (see producer)
+constexpr int kMaskRing = 8;                     // tiles whose validity masks are alive (see the loader)
 
 // MT row tiles per CTA.  Shared memory: Q row tiles, then the ring of K and V
 // tiles.  The softmax works in steps of kStep tokens.  Tensor memory (512 columns
@@ -495,6 +495,7 @@ template <int MT> struct Extra {
     uint64_t go[C::kRowRing][2];                  // the tile's K / V rows may be copied
     uint64_t s_read[MT];                          // two row tiles: S is in registers
     uint64_t scan, clear, drain;
+    uint64_t done[MT];                            // everything an issuer has issued is done
     uint64_t never;                               // nothing arrives (tests of the failure report)
     alignas(16) int rows[C::kRowRing][kTile];     // cache rows of a tile's tokens, -1: none
     uint32_t rows_valid[C::kRowRing][4];          // which tokens have one
@@ -537,7 +538,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         return;
     }
 
-    // ---- what needs no input, while the kernel before this one ends
     if (tid == 32 * C::kLoader) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_k) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_v) : "memory");
@@ -560,6 +560,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             }
             bar_init(&x.o[i], 1);
             bar_init(&x.s_read[i], 4);
+            bar_init(&x.done[i], 1);
         }
         for (int i = 0; i < C::kRowRing; ++i) {
             bar_init(&x.rows_there[i], 1);
@@ -573,8 +574,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         bar_init(&x.never, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    __syncthreads();
-    pdl_wait();
     {   // the batch's page numbers and index entries into L2, a line per thread of the grid
         const size_t at = ((size_t)blockIdx.x * C::kThreads + tid) * 32;
         if (a.c.table && at < (size_t)a.B * a.c.max_blocks)
@@ -1048,6 +1047,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 e += 2 * tiles;
                 walk.next(a, tiles);
             }
+            // Nobody waits for the last commits to the ring's slots and Q: no arrival of
+            // theirs may be left when the CTA ends.
+            mma_commit(&x.done[m]);
+            bar_wait(&x.done[m], 0, gave_up);
         }
         __syncwarp();
     } else {
@@ -1470,22 +1473,19 @@ cudaError_t launch(const TreeArgs &a, int sms, cudaStream_t stream)
         }
     }
     const int ctas = sms < kMaxTreeCtas ? sms : kMaxTreeCtas;
+    tree_attention_kernel<MT><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
+    err = cudaGetLastError();
+    if (err != cudaSuccess || ctas < 2)
+        return err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = host_pdl();
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.stream = stream;
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    err = cudaLaunchKernelEx(&cfg, tree_attention_kernel<MT>, a);
-    if (err != cudaSuccess || ctas < 2)
-        return err;
     cfg.gridDim = dim3(ctas - 1, (a.part_rows + kJoinWarps - 1) / kJoinWarps);
     cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.dynamicSmemBytes = 0;
     const JoinArgs j{a.plan, a.part_m, a.part_l, a.part_o, a.out, a.T, a.Hq, a.G, a.part_rows};
     return cudaLaunchKernelEx(&cfg, tree_join_kernel, j);
 }

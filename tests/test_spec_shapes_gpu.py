@@ -269,3 +269,22 @@ def test_a_query_row_that_is_not_a_number_says_so(n):
     c["q"] = q
     out[0, 2, 1] = run_tree(c)[0][0, 2, 1]
     check_tree(c, out)
+
+
+@pytest.mark.parametrize("sparse", [0, 150])
+def test_launches_in_plain_stream_order_give_the_same(sparse):
+    """With and without programmatic launches, many calls in a row into each other's inputs."""
+    c = tree_case(23, 4, 2, [2100, 77, 640], [8, 3, 8], 8, 16, "tree", sparse)
+    outs = []
+    for pdl in (1, 0):
+        td.td_set_tuning("pdl", pdl)
+        try:
+            out, ws = run_tree(c)
+            for _ in range(20):
+                run_tree(c, out=out, ws=ws)
+            assert ws.status() == 0
+        finally:
+            td.td_set_tuning("pdl", 1)
+        outs.append(out)
+    check_tree(c, outs[0])
+    assert torch.equal(outs[0], outs[1])
