@@ -65,7 +65,7 @@ struct TreeArgs {
     int wait_test;              // the softmax waits for what nothing arrives on (tests); 0 in normal use
 };
 // Rows one work unit of a launch with T * G query rows per KV head can have.
-inline int tree_part_rows(int rows) { return rows <= 128 ? rows : 256; }
+inline int tree_part_rows(int rows) { return rows <= 128 ? rows : 128; }
 cudaError_t launch_tree_attention(const TreeArgs &a, int sms, cudaStream_t stream);
 
 // Accepted rows of up to kAppendLayers layers in one launch.

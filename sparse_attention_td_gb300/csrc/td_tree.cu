@@ -45,49 +45,34 @@
 namespace td {
 namespace {
 
-constexpr int kTile = 128;                       // tokens per tile, and query rows per row tile
+constexpr int kTile = 128;                       // tokens per tile, and query rows per unit
 constexpr int kHalfBytes = kTile * 128;          // one 64-value half of a tile's rows
 constexpr int kTileBytes = 2 * kHalfBytes;       // 128 rows of 128 bf16 values
 constexpr int kMaskRing = 8;                     // tiles whose validity masks are alive (see the loader)
 
-// MT row tiles per CTA.  Shared memory: Q row tiles, then the ring of K and V
-// tiles.  The softmax works in steps of kStep tokens.  Tensor memory (512 columns
-// of 32 bits): in columns 0 .. 255 S and P, then the O tiles.  One row tile: two S
-// buffers of 128 columns, P over the upper half of its S, so S of the next step is
-// there when a step's softmax ends.  Two row tiles, 128 columns each: one S of 64
-// columns, which is free again as soon as the softmax has its values in registers,
-// and two P buffers.  (Two S buffers with P over them, S of a step waiting for P V
-// of the one before the last: 5% slower for 4 x 32K tokens, 64 nodes.)
-template <int MT> struct Cfg {
-    static constexpr int kSlots = MT == 1 ? 6 : 5;
-    static constexpr int kStep = MT == 1 ? 128 : 64;
-    static constexpr int kSteps = kTile / kStep;      // per tile
-    static constexpr int kSoftWarps = 4 * MT;
-    // Warps: softmax, the loader, an MMA issuer per row tile, row finders, copy warps;
-    // 12 or 16.  Copy warps in the third and fourth sub-partition (warp % 4): their
-    // queue of copies slows the other warps there, and the first two have the first 64
-    // rows.  The two issuers in different ones: both in one slowed its softmax warps,
-    // and with them the row tiles (136 us instead of 129 at the time).
-    static constexpr int kLoader = kSoftWarps, kIssuer = kSoftWarps + 1;
-    static constexpr int kIssuer1 = kSoftWarps + 7;
-    static constexpr int kFinder = kSoftWarps + 4, kFinders = MT == 1 ? 2 : 1, kCopiers = 4;
+// Layout of a CTA.  Shared memory: the Q tile, then the ring of K and V tiles.  Tensor
+// memory (512 columns of 32 bits): two S buffers of 128 columns, P over the upper half
+// of its S, so S of the next tile is there when a tile's softmax ends, then O.
+struct Cfg {
+    static constexpr int kSlots = 6;
+    static constexpr int kSoftWarps = 4;
+    // Warps: softmax, the loader, the MMA issuer, two row finders, copy warps.  Copy
+    // warps in the third and fourth sub-partition (warp % 4): their queue of copies
+    // slows the other warps there, and the first two have the first 64 rows.
+    static constexpr int kLoader = 4, kIssuer = 5, kFinder = 8, kFinders = 2, kCopiers = 4;
     static constexpr int kRowRing = 4;                // tiles whose row lists are alive
-    static constexpr int kThreads = 32 * (kSoftWarps + 8);
-    // number of a copy warp, or -1
+    static constexpr int kThreads = 32 * 12;
+    // number of a copy warp (6, 7, 10, 11), or -1
     __device__ static int copier(int warp)
     {
         const int w = warp - kSoftWarps;
-        if (MT > 1 && w >= 5)
-            return w == 7 ? -1 : w == 6 ? 2 : 3;
         return w < 0 || (w & 2) == 0 ? -1 : (w & 1) + (w >> 2) * 2;
     }
-    static constexpr size_t kSmem = (size_t)(MT + kSlots) * kTileBytes + 3 * 1024;   // + Extra
-    // of step number g of a row tile: S and P columns, phase of the S barrier
-    __device__ static uint32_t col_s(int m, uint32_t g) { return m * 128 + (MT == 1 ? (g & 1) * 128 : 0); }
-    __device__ static uint32_t col_p(int m, uint32_t g) { return m * 128 + 64 + (g & 1) * (MT == 1 ? 128 : 32); }
-    __device__ static int buf_s(uint32_t g) { return MT == 1 ? g & 1 : 0; }
-    __device__ static uint32_t phase_s(uint32_t g) { return MT == 1 ? g >> 1 : g; }
-    __device__ static constexpr uint32_t col_o(int m) { return 256 + m * kTile; }
+    static constexpr size_t kSmem = (size_t)(1 + kSlots) * kTileBytes + 3 * 1024;   // + Extra
+    // of tile number g: S and P columns
+    __device__ static uint32_t col_s(uint32_t g) { return (g & 1) * 128; }
+    __device__ static uint32_t col_p(uint32_t g) { return (g & 1) * 128 + 64; }
+    static constexpr uint32_t kColO = 256;
 };
 constexpr uint32_t kTmemCols = 512;
 
@@ -298,11 +283,6 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&x)[4])
                  : "memory");
 }
 
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&x)[2])
-{
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(addr) : "memory");
-}
-
 __device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
@@ -419,7 +399,7 @@ struct Work {
     __device__ int tokens(int t) const { return t == tiles - 1 ? off + nt : min(kTile, entries - t * kTile); }
 };
 
-template <int MT> __device__ __forceinline__ Work work_of(const TreeArgs &a, const TreeLens &len)
+__device__ __forceinline__ Work work_of(const TreeArgs &a, const TreeLens &len)
 {
     Work w;
     w.nt = len.nt;
@@ -428,13 +408,13 @@ template <int MT> __device__ __forceinline__ Work work_of(const TreeArgs &a, con
     const int rest = w.entries & (kTile - 1);
     w.off = rest + w.nt <= kTile ? rest : 0;
     w.tiles = w.nt ? (w.entries >> 7) + (w.off == 0 && rest > 0 ? 1 : 0) + 1 : 0;
-    w.blocks = (w.nt * a.G + MT * kTile - 1) / (MT * kTile);
+    w.blocks = (w.nt * a.G + kTile - 1) / kTile;
     return w;
 }
 
-template <int MT> __device__ __forceinline__ Work work_of(const TreeArgs &a, int b, uint32_t &bad)
+__device__ __forceinline__ Work work_of(const TreeArgs &a, int b, uint32_t &bad)
 {
-    return work_of<MT>(a, tree_lens_of(a.seq_lens, a.tree_lens, b, a.T, a.Nmax, bad));
+    return work_of(a, tree_lens_of(a.seq_lens, a.tree_lens, b, a.T, a.Nmax, bad));
 }
 
 // The first request behind b that has drafted tokens (or the last one) and its
@@ -457,7 +437,7 @@ __device__ __noinline__ NextRequest next_request(const TreeArgs &a, int b)
 }
 
 // A CTA's range of tiles, unit after unit: every role of the CTA walks it alike.
-template <int MT> struct Walk {
+struct Walk {
     int left;                     // tiles left of the CTA's range
     int b, h, m, t;               // current request, KV head, row block and first tile
     bool first;                   // the segment starts at the CTA's range start
@@ -480,22 +460,21 @@ template <int MT> struct Walk {
         h = 0;
         const NextRequest r = next_request(a, b);
         b = r.b;
-        w = work_of<MT>(a, r.len);
+        w = work_of(a, r.len);
     }
-    __device__ int rows(const TreeArgs &a) const { return min(w.nt * a.G - m * MT * kTile, MT * kTile); }
+    __device__ int rows(const TreeArgs &a) const { return min(w.nt * a.G - m * kTile, kTile); }
 };
 
 // Shared memory behind the Q tiles and the ring.
-template <int MT> struct Extra {
-    using C = Cfg<MT>;
+struct Extra {
+    using C = Cfg;
     uint64_t full[C::kSlots], empty[C::kSlots];   // ring: filled, read
     uint64_t q[2], q_free[2];                     // Q of a segment: there, read (by segment parity)
-    uint64_t s[MT][2], p[MT][2], o[MT];           // S there, P there, P V done
+    uint64_t s[2], p[2], o;                       // S there, P there, P V done
     uint64_t rows_there[C::kRowRing], rows_read[C::kRowRing];   // a tile's row list: written, read
     uint64_t go[C::kRowRing][2];                  // the tile's K / V rows may be copied
-    uint64_t s_read[MT];                          // two row tiles: S is in registers
-    uint64_t scan, clear, drain;
-    uint64_t done[MT];                            // everything an issuer has issued is done
+    uint64_t drain;                               // everything issued is done (a CTA that gave up)
+    uint64_t done;                                // everything issued is done
     uint64_t never;                               // nothing arrives (tests of the failure report)
     alignas(16) int rows[C::kRowRing][kTile];     // cache rows of a tile's tokens, -1: none
     uint32_t rows_valid[C::kRowRing][4];          // which tokens have one
@@ -503,9 +482,9 @@ template <int MT> struct Extra {
     // Drafted tokens with non-finite V values, by the number of their tile: a warp may
     // look at the next segment's, if it has one or two tiles, while another still
     // reads this one's (behind more, P V has waited for both).
-    uint32_t badv[MT][4][4];
+    uint32_t badv[4][4];
     int sums[C::kThreads / 32];
-    Walk<MT> start;
+    Walk start;
     uint32_t tmem;
     int gave_up;
 };
@@ -513,24 +492,23 @@ template <int MT> struct Extra {
 // One CTA per SM; each takes an equal, contiguous range of the batch's tiles
 // (a range may cover several units and end inside one: those units' partial
 // results are joined by tree_join_kernel): the longest request decides nothing, and
-// the SMs end together.  Roles: 4 * MT softmax warps (one query row per thread), the
-// loader, the row finders and copy warps for tiles that no box holds, and an MMA
-// issuer per row tile; they meet at barriers in shared memory only.
-template <int MT>
-__global__ void __launch_bounds__(Cfg<MT>::kThreads, 1)
+// the SMs end together.  Roles: softmax warps (one query row per thread), the
+// loader, the row finders and copy warps for tiles that no box holds, and the MMA
+// issuer; they meet at barriers in shared memory only.
+__global__ void __launch_bounds__(Cfg::kThreads, 1)
 tree_attention_kernel(const __grid_constant__ TreeArgs a)
 {
-    using C = Cfg<MT>;
+    using C = Cfg;
     extern __shared__ __align__(1024) unsigned char sm_raw[];
-    Extra<MT> &x = *reinterpret_cast<Extra<MT> *>(sm_raw + (MT + C::kSlots) * kTileBytes);
+    Extra &x = *reinterpret_cast<Extra *>(sm_raw + (1 + C::kSlots) * kTileBytes);
     static_assert(C::kCopiers == 4, "copy warps' rows of a tile");
-    static_assert((MT + C::kSlots) * kTileBytes + sizeof(Extra<MT>) <= C::kSmem, "shared memory");
+    static_assert((1 + C::kSlots) * kTileBytes + sizeof(Extra) <= C::kSmem, "shared memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto bar_wait = [&](uint64_t *bar, unsigned parity, volatile int *up) {
         return bar_wait_for(bar, parity, up, a.wait_cycles);
     };
     const uint32_t sm_q = smem_of(sm_raw);        // 1024-byte aligned: nothing static lies before it
-    const uint32_t sm_ring = sm_q + MT * kTileBytes;
+    const uint32_t sm_ring = sm_q + kTileBytes;
     volatile int *gave_up = &x.gave_up;
     if (sm_q & 1023) {            // (cannot be: the swizzled tiles need it)
         if (tid == 0)
@@ -547,30 +525,23 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         x.start.left = 0;
         for (int i = 0; i < C::kSlots; ++i) {
             bar_init(&x.full[i], 32 * C::kCopiers);
-            bar_init(&x.empty[i], MT);
+            bar_init(&x.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&x.q[i], 32 * C::kCopiers);
-            bar_init(&x.q_free[i], MT);
+            bar_init(&x.q_free[i], 1);
+            bar_init(&x.s[i], 1);
+            bar_init(&x.p[i], 4);
         }
-        for (int i = 0; i < MT; ++i) {
-            for (int k = 0; k < 2; ++k) {
-                bar_init(&x.s[i][k], 1);
-                bar_init(&x.p[i][k], 4);
-            }
-            bar_init(&x.o[i], 1);
-            bar_init(&x.s_read[i], 4);
-            bar_init(&x.done[i], 1);
-        }
+        bar_init(&x.o, 1);
         for (int i = 0; i < C::kRowRing; ++i) {
             bar_init(&x.rows_there[i], 1);
             bar_init(&x.go[i][0], 1);
             bar_init(&x.go[i][1], 1);
             bar_init(&x.rows_read[i], C::kCopiers);
         }
-        bar_init(&x.scan, 4);
-        bar_init(&x.clear, 4);
-        bar_init(&x.drain, MT);
+        bar_init(&x.drain, 1);
+        bar_init(&x.done, 1);
         bar_init(&x.never, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -581,21 +552,21 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         if (a.idx && at < (size_t)a.B * a.Hkv * a.top_k)
             prefetch_l2(a.idx + at);
     }
-    // ---- the CTA's range: requests in equal runs per thread, prefix sums of their
-    // tiles.  (The host has made sure that the number of tiles fits 31 bits.)
-    Walk<MT> walk;
-    uint32_t bad = 0;
-    int per, start;
+    // ---- the CTA's range: requests in equal runs per thread, prefix sums.  (The
+    // host has made sure that the number of tiles fits 31 bits.)
     {
         const int run = (a.B + C::kThreads - 1) / C::kThreads;
         const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
+        uint32_t bad = 0;
         int mine = 0;
         Work w{};
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            w = work_of<MT>(a, b, bad);
+            w = work_of(a, b, bad);
             mine += w.tiles * w.blocks * a.Hkv;
         }
+        if (bad && blockIdx.x == 0)
+            atomicOr(a.status, bad);
         int inc = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -614,21 +585,21 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 at += y;
             total += y;
         }
-        per = (uint32_t)(total + gridDim.x - 1) / gridDim.x;
-        start = blockIdx.x * per;
+        const int per = (uint32_t)(total + gridDim.x - 1) / gridDim.x;
+        const int start = blockIdx.x * per;
         if (start < total && at <= start && start - at < mine) {
             int b = b0;
             if (run > 1) {
 #pragma unroll 1
                 for (int p = at; b < b1; ++b, at = p) {
-                    w = work_of<MT>(a, b, bad);
+                    w = work_of(a, b, bad);
                     p += w.tiles * w.blocks * a.Hkv;
                     if (start < p)
                         break;
                 }
             }
             const int unit = (uint32_t)(start - at) / (uint32_t)w.tiles;
-            Walk<MT> s;
+            Walk s;
             s.left = min(per, total - start);
             s.b = b;
             s.h = w.blocks == 1 ? unit : unit / w.blocks;
@@ -639,44 +610,41 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             x.start = s;
         }
         __syncthreads();
-        walk = x.start;
-    }
-    pdl_launch_dependents();
-    if (bad && blockIdx.x == 0)
-        atomicOr(a.status, bad);
-    if (tid == C::kThreads - 1) {
-        // The unit that this cut goes through, if it is the unit's first cut.
-        JoinPlan j{};
-        const int first = walk.t;
-        if (walk.left > 0 && first > 0 && first <= per) {
-            j.rows = walk.rows(a);
-            j.b = walk.b;
-            j.h = walk.h;
-            j.row0 = walk.m * MT * kTile;
-            // the last range that meets the unit
-            j.last = (uint32_t)(start - first + walk.w.tiles - 1) / (uint32_t)per;
-            j.late = first < per;
+        pdl_launch_dependents();
+        if (tid == C::kThreads - 1) {
+            // The unit that this cut goes through, if it is the unit's first cut.
+            JoinPlan j{};
+            const int first = x.start.t;
+            if (x.start.left > 0 && first > 0 && first <= per) {
+                j.rows = x.start.rows(a);
+                j.b = x.start.b;
+                j.h = x.start.h;
+                j.row0 = x.start.m * kTile;
+                // the last range that meets the unit
+                j.last = (uint32_t)(start - first + x.start.w.tiles - 1) / (uint32_t)per;
+                j.late = first < per;
+            }
+            a.plan[blockIdx.x] = j;
         }
-        a.plan[blockIdx.x] = j;
+        __syncwarp();
     }
-    __syncwarp();
+    Walk walk = x.start;
     // Up to 64 query rows per unit: Q has two buffers of 64 rows, and the next
     // segment's comes in during this one.  (The MMA reads 128 rows from either;
     // the rows that are not Q's end in S and O rows that nobody reads.)
-    const bool two_q = MT == 1 && a.part_rows <= 64;
+    const bool two_q = a.part_rows <= 64;
     uint32_t loaded = 0;          // loaders: ring entries begun
     uint32_t loaded_boxes = 0;    // which of the last ones came as boxes (bit 0: the last)
     uint32_t tmem = 0;
-    const bool issuer = warp == C::kIssuer || (MT > 1 && warp == C::kIssuer1);
     // Boxes of 8 or 16 rows are more than one warp can issue (80 cycles each).  In full
-    // layers with one row tile the second finder has little to do and loads V, the
+    // layers the second finder has little to do and loads V, the
     // loader K; the ring's number of slots is even, so each has slots of its own.
     // 32 requests of 8K-16K, G = 4, 16 nodes, one / two loaders: 8-token pages 412 /
     // 258 us, 16: 279 / 253, 32: 251 / 253, 64: 250 / 257 (K then runs ahead of V).
-    const bool split = MT == 1 && !a.idx && a.box_rows && a.box_rows <= 16;
+    const bool split = !a.idx && a.box_rows && a.box_rows <= 16;
     const bool loads_v = split && warp == C::kFinder + 1;
-    static_assert(MT > 1 || C::kSlots % 2 == 0, "slots of K and of V");
-    if (warp < C::kSoftWarps || issuer) {
+    static_assert(C::kSlots % 2 == 0, "slots of K and of V");
+    if (warp < C::kSoftWarps || warp == C::kIssuer) {
         // tensor memory for the roles that use it, while the others begin
         if (warp == C::kIssuer) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -686,7 +654,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
         tmem_before();
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * (C::kSoftWarps + MT)) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * (C::kSoftWarps + 1)) : "memory");
         tmem_after();
         tmem = x.tmem;
     }
@@ -897,14 +865,14 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             if (!ok)
                 break;
             {
-                const int rows = walk.rows(a), row0 = walk.m * MT * kTile;
+                const int rows = walk.rows(a), row0 = walk.m * kTile;
                 const int c = lane & 15;
                 const uint16_t *src = a.q + ((size_t)walk.b * a.T * a.Hq + walk.h * a.G) * kHeadDim + c * 8;
                 const uint32_t dst = sm_q + (two_q ? seg & 1 : 0) * 64 * 128 + (c >> 3) * kHalfBytes;
 #pragma unroll 2
                 for (int r = 2 * me + (lane >> 4); r < rows; r += 2 * C::kCopiers) {
                     const int row = row0 + r, tk = row >> a.g_shift, g = row & (a.G - 1);
-                    copy16(dst + (r >> 7) * kTileBytes + (r & 127) * 128 + (((c ^ r) & 7) << 4),
+                    copy16(dst + r * 128 + (((c ^ r) & 7) << 4),
                            src + ((size_t)tk * a.Hq + g) * kHeadDim, true);
                 }
                 copies_arrive(&x.q[seg & 1]);
@@ -951,13 +919,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             e += 2 * n;
             walk.next(a, n);
         }
-    } else if (issuer) {
-        // ---- MMA issue of one row tile, by one thread: S of step j + 1 before P V of
-        // step j, so the tensor cores work while the softmax does.
+    } else if (warp == C::kIssuer) {
+        // ---- MMA issue, by one thread: S of tile j + 1 before P V of tile j, so the
+        // tensor cores work while the softmax does.
         if (elect_one()) {
-            const int m = warp == C::kIssuer ? 0 : 1;
             uint32_t e = 0;              // ring entry of the segment's first K tile
-            uint32_t steps = 0;          // steps of earlier segments
+            uint32_t tiles = 0;          // tiles of earlier segments
             uint32_t seg = 0;            // segments begun
             bool ok = true;
             // Rows copied by cp.async are read by the MMA through the async proxy; boxes
@@ -976,37 +943,20 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             };
 #pragma unroll 1
             for (; ok && walk.left > 0; ++seg) {
-                const int tiles = walk.count(), n = tiles * C::kSteps;
-                if (MT > 1 && m * kTile >= walk.rows(a)) {
-                    // no rows here: the slots are free as far as this row tile goes
-#pragma unroll 1
-                    for (int i = 0; ok && i < 2 * tiles; ++i)
-                        if (wait_full(e + i, false))
-                            bar_arrive(&x.empty[(e + i) % C::kSlots]);
-                    if (wait_bar(&x.q[seg & 1], seg >> 1))     // (no phase is missed)
-                        bar_arrive(&x.q_free[seg & 1]);
-                    e += 2 * tiles;
-                    walk.next(a, tiles);
-                    continue;
-                }
-                const uint32_t q = operand(sm_q + m * kTileBytes + (two_q ? seg & 1 : 0) * 64 * 128, 16);
+                const int n = walk.count();
+                const uint32_t q = operand(sm_q + (two_q ? seg & 1 : 0) * 64 * 128, 16);
                 auto issue_s = [&](int j) {
-                    const uint32_t entry = e + 2 * (j / C::kSteps);
-                    const uint32_t k = operand(sm_ring + entry % C::kSlots * kTileBytes, 16) +
-                                       (j % C::kSteps * C::kStep * 128 >> 4);
-                    const uint32_t g = steps + j;
-                    if (MT > 1 && j >= 1)       // the softmax has read the step before
-                        wait_bar(&x.s_read[m], g - 1);
-                    if (j >= 2)                 // P V of step j - 2 has read the P that goes next
-                        wait_bar(&x.o[m], g - 2);
+                    const uint32_t slot = (e + 2 * j) % C::kSlots, g = tiles + j;
+                    const uint32_t k = operand(sm_ring + slot * kTileBytes, 16);
+                    if (j >= 2)                 // P V of tile j - 2 has read the P that goes next
+                        wait_bar(&x.o, g - 2);
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
                         const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
-                        mma_ss<C::kStep>(tmem + C::col_s(m, g), q + (o >> 4), k + (o >> 4), s > 0);
+                        mma_ss<kTile>(tmem + C::col_s(g), q + (o >> 4), k + (o >> 4), s > 0);
                     }
-                    mma_commit(&x.s[m][C::buf_s(g)]);
-                    if (j % C::kSteps == C::kSteps - 1)
-                        mma_commit(&x.empty[entry % C::kSlots]);
+                    mma_commit(&x.s[g & 1]);
+                    mma_commit(&x.empty[slot]);
                     if (j == n - 1)
                         mma_commit(&x.q_free[seg & 1]);   // the segment's Q has been read
                 };
@@ -1019,68 +969,53 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
 #pragma unroll 1
                 for (int j = 0; j < n; ++j) {
                     if (j + 1 < n) {
-                        if ((j + 1) % C::kSteps == 0 &&
-                            !wait_full(e + 2 * ((j + 1) / C::kSteps), (j + 1) / C::kSteps >= boxes))
+                        if (!wait_full(e + 2 * (j + 1), j + 1 >= boxes))
                             break;
                         issue_s(j + 1);
                     }
-                    const uint32_t entry = e + 2 * (j / C::kSteps) + 1;
-                    if (j % C::kSteps == 0 && !wait_full(entry, j / C::kSteps >= boxes))
+                    const uint32_t entry = e + 2 * j + 1, slot = entry % C::kSlots, g = tiles + j;
+                    if (!wait_full(entry, j >= boxes))
                         break;
-                    const uint32_t v = operand(sm_ring + entry % C::kSlots * kTileBytes, kHalfBytes) +
-                                       (j % C::kSteps * C::kStep * 128 >> 4);
-                    // tokens by 16, as far as the tile has any
-                    const int tokens = walk.w.tokens(walk.t + j / C::kSteps) - j % C::kSteps * C::kStep;
-                    const uint32_t g = steps + j;
-                    if (!wait_bar(&x.p[m][g & 1], g >> 1))
+                    const uint32_t v = operand(sm_ring + slot * kTileBytes, kHalfBytes);
+                    const int tokens = walk.w.tokens(walk.t + j);    // by 16, as far as there are any
+                    if (!wait_bar(&x.p[g & 1], g >> 1))
                         break;
 #pragma unroll
-                    for (int s = 0; s < C::kStep / 16; ++s)
+                    for (int s = 0; s < kTile / 16; ++s)
                         if (s * 16 < tokens)
-                            mma_ts(tmem + C::col_o(m), tmem + C::col_p(m, g) + s * 8,
-                                   v + (s * 16 * 128 >> 4), j > 0 || s > 0);
-                    mma_commit(&x.o[m]);
-                    if (j % C::kSteps == C::kSteps - 1)
-                        mma_commit(&x.empty[entry % C::kSlots]);
+                            mma_ts(tmem + C::kColO, tmem + C::col_p(g) + s * 8, v + (s * 16 * 128 >> 4),
+                                   j > 0 || s > 0);
+                    mma_commit(&x.o);
+                    mma_commit(&x.empty[slot]);
                 }
-                steps += n;
-                e += 2 * tiles;
-                walk.next(a, tiles);
+                tiles += n;
+                e += 2 * n;
+                walk.next(a, n);
             }
             // Nobody waits for the last commits to the ring's slots and Q: no arrival of
             // theirs may be left when the CTA ends.
-            mma_commit(&x.done[m]);
-            bar_wait(&x.done[m], 0, gave_up);
+            mma_commit(&x.done);
+            bar_wait(&x.done, 0, gave_up);
         }
         __syncwarp();
     } else {
-        // ---- softmax: thread r of a row tile owns query row r
-        const int m = MT == 1 ? 0 : warp >> 2;
-        const int r = (warp & 3) * 32 + lane;                 // row of the row tile, TMEM lane
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // this warp's TMEM lanes
+        // ---- softmax: thread r owns query row r of the unit
+        const int r = warp * 32 + lane;                       // also the TMEM lane
+        const uint32_t lanes = (uint32_t)warp << 21;          // this warp's TMEM lanes
         const float sl2 = a.scale * kLog2e;
-        uint32_t count = 0;                                   // steps done
-        uint32_t tile_no = 0;                                 // tiles of the CTA before the segment
-        uint32_t scans = 0;                                   // clearings of V with two row tiles
+        uint32_t count = 0;                                   // tiles done
         bool ok = true;
 #pragma unroll 1
         while (ok && walk.left > 0) {
             const int n = walk.count();
-            const int unit_rows = walk.rows(a);
-            const int nm = MT == 1 ? 1 : (unit_rows + kTile - 1) / kTile;
-            if (m >= nm) {
-                tile_no += n;
-                walk.next(a, n);
-                continue;
-            }
             const int b = walk.b, h = walk.h;
-            const int row0 = walk.m * MT * kTile + m * kTile;   // first query row of the row tile
+            const int row0 = walk.m * kTile;                   // first query row of the unit
             const int total_rows = walk.w.nt * a.G;
             const size_t q0 = (size_t)b * a.T * a.Hq + h * a.G;
             const int row = row0 + r;
             const int tok = row >> a.g_shift;                  // drafted token of this row
             const bool live = row < total_rows;
-            const bool warp_live = row0 + (warp & 3) * 32 < total_rows;
+            const bool warp_live = row0 + warp * 32 < total_rows;
             float mref = -CUDART_INF_F, l = 0.0f;
             uint32_t sees[4] = {0, 0, 0, 0};
             const bool has_tree = walk.t + n == walk.w.tiles;
@@ -1096,26 +1031,25 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 }
             }
 #pragma unroll 1
-            for (int j = 0; j < n * C::kSteps; ++j, ++count) {
-                const int i = j / C::kSteps, part = j % C::kSteps;   // tile, step of the tile
-                const bool tree = walk.t + i == walk.w.tiles - 1;
-                // P V of the step before is done: waited for to rescale O, and in the last
-                // step.  (P V of the step before the last was done when S of this step was
-                // issued, so no phase is missed.)  Both waits come before P of this step is
-                // handed over, behind which P V of this step may end and the phase of the
-                // one before be past.
+            for (int j = 0; j < n; ++j, ++count) {
+                const bool tree = walk.t + j == walk.w.tiles - 1;
+                // P V of the tile before is done: waited for to rescale O, and at the last
+                // tile.  (P V of the tile before that was done when S of this one was
+                // issued, so no phase is missed.)  Both waits come before P of this tile is
+                // handed over, behind which its P V may end and the phase of the one before
+                // be past.
                 bool waited = j == 0;
                 auto o_done = [&]() {
                     if (!waited)
-                        ok = __all_sync(kFull, bar_wait(&x.o[m], (count - 1) & 1, gave_up));
+                        ok = __all_sync(kFull, bar_wait(&x.o, (count - 1) & 1, gave_up));
                     waited = true;
                 };
-                ok = __all_sync(kFull, bar_wait(a.wait_test ? &x.never : &x.s[m][C::buf_s(count)],
-                                                a.wait_test ? 0 : C::phase_s(count) & 1, gave_up));
+                ok = __all_sync(kFull, bar_wait(a.wait_test ? &x.never : &x.s[count & 1],
+                                                a.wait_test ? 0 : count >> 1 & 1, gave_up));
                 if (!ok)
                     break;
                 tmem_after();
-                if (tree && part == 0) {
+                if (tree) {
                     // the last tile's bits: its context tokens, then the drafted ones
                     uint64_t lo = sees[0] | (uint64_t)sees[1] << 32, hi = sees[2] | (uint64_t)sees[3] << 32;
                     const int off = walk.w.off;
@@ -1129,8 +1063,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     // A V value that is not finite must not meet the zero
                     // probabilities of rows that do not see its token: such values
                     // leave the tile here and join the rows that do see it below.
-                    // With two row tiles both look, then the first one clears.
-                    const uint32_t entry = 2 * (tile_no + i) + 1;
+                    const uint32_t entry = 2 * count + 1;
                     ok = __all_sync(kFull, bar_wait(&x.full[entry % C::kSlots],
                                                     (entry / C::kSlots) & 1, gave_up));
                     if (!ok)
@@ -1152,25 +1085,13 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     }
                     const uint32_t bits = __ballot_sync(kFull, any);
                     if (lane == 0)
-                        x.badv[m][(tile_no + i) & 3][warp & 3] = bits;
-                    if constexpr (MT > 1) {
-                        if (nm > 1) {
-                            if (m == 1 && lane == 0)
-                                bar_arrive(&x.scan);
-                            ok = __all_sync(kFull, bar_wait(m == 0 ? &x.scan : &x.clear, scans & 1, gave_up));
-                            if (!ok)
-                                break;
-                            ++scans;
-                        }
-                    }
-                    if (m == 0 && bits) {
+                        x.badv[count & 3][warp] = bits;
+                    if (bits) {
                         if (any)
                             clear_not_finite(v, r);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
                     __syncwarp();
-                    if (MT > 1 && nm > 1 && m == 0 && lane == 0)
-                        bar_arrive(&x.clear);
                 }
                 if (warp_live) {
                     // The row's scores pass through 64 registers, in blocks of 64
@@ -1179,26 +1100,24 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     // A loop that stays rolled: with the step unrolled over 128
                     // registers the roles' code no longer fitted the instruction
                     // cache (100K: 261 us against 314).
-                    constexpr int kBlocks = C::kStep / 64;
-                    const uint32_t at = tmem + C::col_s(m, count) + lanes;
-                    uint32_t seen[C::kStep / 32];     // of the step's tokens, 32 a word
-                    lds_words(smem_of(x.valid[(tile_no + i) % kMaskRing] + part * (C::kStep / 32)), seen);
+                    const uint32_t at = tmem + C::col_s(count) + lanes;
+                    uint32_t seen[4];                 // of the tile's tokens, 32 a word
+                    lds_words(smem_of(x.valid[count % kMaskRing]), seen);
                     if (tree) {
 #pragma unroll
-                        for (int w = 0; w < C::kStep / 32; ++w)
-                            seen[w] &= MT > 1 && part > 0 ? sees[(w + 2) & 3] : sees[w];
+                        for (int w = 0; w < 4; ++w)
+                            seen[w] &= sees[w];
                     }
                     float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
                     float2 off2 = make_float2(0.0f, 0.0f);
                     float2 sum[2] = {off2, off2};
                     // passes: block 0 (maximum), block 1 (maximum, probabilities), block 0
-                    // (probabilities); with one block (of a step, or of tokens) both in one
-                    const int blocks = kBlocks > 1 && walk.w.tokens(walk.t + i) > 64 ? 2 : 1;
+                    // (probabilities); with one block of tokens both in one
+                    const int blocks = walk.w.tokens(walk.t + j) > 64 ? 2 : 1;
 #pragma unroll 1
                     for (int pass = 0; pass < 2 * blocks - 1; ++pass) {
                         const int block = blocks > 1 ? pass & 1 : 0;
-                        constexpr int kUp = kBlocks > 1 ? 2 : 0;
-                        const uint32_t w0 = block > 0 ? seen[kUp] : seen[0], w1 = block > 0 ? seen[kUp + 1] : seen[1];
+                        const uint32_t w0 = block > 0 ? seen[2] : seen[0], w1 = block > 0 ? seen[3] : seen[1];
                         float s[64];
                         __syncwarp();
                         tmem_ld32(at + 64 * block, reinterpret_cast<uint32_t *>(s));
@@ -1216,12 +1135,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                             }
                         }
                         if (pass < blocks) {
-                            if constexpr (MT > 1) {
-                                tmem_before();
-                                __syncwarp();
-                                if (lane == 0)
-                                    bar_arrive(&x.s_read[m]);
-                            }
 #pragma unroll
                             for (int k = 0; k < 64; k += 2)
                                 mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
@@ -1242,7 +1155,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                 const float f = grow ? ex2(mref - mn) : 1.0f;
                                 mref = mn;
                                 l *= f;
-                                const uint32_t o = tmem + C::col_o(m) + lanes;
+                                const uint32_t o = tmem + C::kColO + lanes;
 #pragma unroll 1
                                 for (int c = 0; c < 4; ++c) {
                                     uint32_t ov[32];
@@ -1268,30 +1181,28 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                 sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                                 p[k] = pack_bf16(e.x, e.y);
                             }
-                            // (one row tile: over scores of this or a later block, which have been read)
-                            tmem_st32(tmem + C::col_p(m, count) + lanes + 32 * block, p);
+                            // (over scores of this or a later block, which have been read)
+                            tmem_st32(tmem + C::col_p(count) + lanes + 32 * block, p);
                         }
                     }
                     if (!ok)
                         break;
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
-                } else if (MT > 1 && lane == 0) {
-                    bar_arrive(&x.s_read[m]);
                 }
-                if (j == n * C::kSteps - 1)
+                if (j == n - 1)
                     o_done();
                 if (!ok)
                     break;
                 tmem_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(&x.p[m][count & 1]);
+                    bar_arrive(&x.p[count & 1]);
             }
             if (!ok)
                 break;
             // ---- the segment's result
-            ok = __all_sync(kFull, bar_wait(&x.o[m], (count - 1) & 1, gave_up));
+            ok = __all_sync(kFull, bar_wait(&x.o, (count - 1) & 1, gave_up));
             if (!ok)
                 break;
             tmem_after();
@@ -1299,10 +1210,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 const bool whole = n == walk.w.tiles;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 const int part = 2 * blockIdx.x + (walk.first ? 0 : 1);
-                const size_t prow = (size_t)part * a.part_rows + m * kTile + r;
+                const size_t prow = (size_t)part * a.part_rows + r;
                 uint16_t *out = a.out + (q0 + (size_t)tok * a.Hq + (row & (a.G - 1))) * kHeadDim;
                 float *part_o = a.part_o + prow * kHeadDim;
-                const uint32_t o = tmem + C::col_o(m) + lanes;
+                const uint32_t o = tmem + C::kColO + lanes;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t ov[32];
@@ -1336,7 +1247,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 if (has_tree && live) {
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        uint32_t bad = x.badv[m][(tile_no + n - 1) & 3][w] & sees[w];
+                        uint32_t bad = x.badv[(count - 1) & 3][w] & sees[w];
                         for (; bad; bad &= bad - 1)
                             add_not_finite(a, b, h, walk.w.ctx + 32 * w + __ffs(bad) - 1 - walk.w.off,
                                            whole ? nullptr : part_o, out);
@@ -1346,7 +1257,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 tmem_before();
             }
             __syncwarp();
-            tile_no += n;
             walk.next(a, n);
         }
     }
@@ -1366,7 +1276,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 if (loaded_boxes >> (loaded - 1 - n) & 1)
                     bar_wait_for(&x.full[e % C::kSlots], (e / C::kSlots) & 1, &own_limit, kLimit);
             }
-        } else if (issuer && elect_one()) {      // (the lane that issued them)
+        } else if (warp == C::kIssuer && elect_one()) {      // (the lane that issued them)
             mma_commit(&x.drain);
             bar_wait_for(&x.drain, 0, &own_limit, kLimit);
         }
@@ -1451,10 +1361,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
         a.out + (((size_t)j.b * a.T + row / a.G) * a.Hq + j.h * a.G + row % a.G) * kHeadDim + lane * 4) = y;
 }
 
-template <int MT>
-cudaError_t launch(const TreeArgs &a, int sms, cudaStream_t stream)
+}  // namespace
+
+cudaError_t launch_tree_attention(const TreeArgs &a, int sms, cudaStream_t stream)
 {
-    using C = Cfg<MT>;
+    using C = Cfg;
     static std::mutex mu;
     static bool ready[64] = {false};
     int dev = 0;
@@ -1464,7 +1375,7 @@ cudaError_t launch(const TreeArgs &a, int sms, cudaStream_t stream)
     {
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64 || !ready[dev]) {
-            err = cudaFuncSetAttribute(tree_attention_kernel<MT>,
+            err = cudaFuncSetAttribute(tree_attention_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
             if (err != cudaSuccess)
                 return err;
@@ -1473,7 +1384,7 @@ cudaError_t launch(const TreeArgs &a, int sms, cudaStream_t stream)
         }
     }
     const int ctas = sms < kMaxTreeCtas ? sms : kMaxTreeCtas;
-    tree_attention_kernel<MT><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
+    tree_attention_kernel<<<ctas, C::kThreads, C::kSmem, stream>>>(a);
     err = cudaGetLastError();
     if (err != cudaSuccess || ctas < 2)
         return err;
@@ -1488,13 +1399,6 @@ cudaError_t launch(const TreeArgs &a, int sms, cudaStream_t stream)
     cfg.blockDim = dim3(32 * kJoinWarps);
     const JoinArgs j{a.plan, a.part_m, a.part_l, a.part_o, a.out, a.T, a.Hq, a.G, a.part_rows};
     return cudaLaunchKernelEx(&cfg, tree_join_kernel, j);
-}
-
-}  // namespace
-
-cudaError_t launch_tree_attention(const TreeArgs &a, int sms, cudaStream_t stream)
-{
-    return a.T * a.G <= kTile ? launch<1>(a, sms, stream) : launch<2>(a, sms, stream);
 }
 
 }  // namespace td
