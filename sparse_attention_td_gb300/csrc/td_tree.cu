@@ -17,17 +17,16 @@
 // S, O, m and l are fp32.
 //
 // What bounds it, measured on GB300 (a copy of the same bytes runs at 6.7 TB/s):
-//   reading the cache once, where a KV head has at most 128 query rows:
+//   reading the cache, once per 128 query rows of a KV head:
 //     32 requests of 8K-16K, 8 KV heads, G = 4, 16 nodes, 64-token pages: 248 us, 6.6 TB/s
 //     one request of 100K, 32 KV heads, G = 1, 32 nodes:                  242 us, 6.9 TB/s
-//   the softmax, where it has more (two row tiles):
-//     4 x 32K, 8 KV heads, G = 4, 64 nodes:            124 us, 4.2 TB/s, 1.1 PFLOP/s
+//     4 x 32K, 8 KV heads, G = 4, 64 nodes (256 rows, two reads):         157 us, 6.7 TB/s
 //   launch, first loads and the join, where a step is short:
-//     4 x 257-2050, 8 KV heads, G = 8, one node, 16-token pages:  14.4 us
+//     4 x 257-2050, 8 KV heads, G = 8, one node, 16-token pages:  14.5 us
 //     4 x 32K, G = 4, 2048 index entries, 5 nodes:                16.6 us
 //     (the two launches alone, every CTA leaving at once:         4.5 us)
 //   copies of single rows, where an index set names them, and the ends of units:
-//     32 requests, G = 4, 1024 index entries, 16 nodes:  37.4 us, 3.9 TB/s
+//     32 requests, G = 4, 1024 index entries, 16 nodes:  37.7 us, 3.9 TB/s
 // The roles' code together does not fit an SM's instruction cache: on the last of
 // these 18% of its requests missed with 100 KB of code, and with 70 KB (waits, unit
 // changes and rare cases out of line, loops left rolled, no branches where a selection

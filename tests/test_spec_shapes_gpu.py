@@ -49,8 +49,8 @@ def test_drafted_tokens_around_a_tiles_end(ctx, nt):
 @pytest.mark.parametrize("G,T", [(4, 64), (8, 64), (8, 128), (2, 100), (1, 128)])
 @pytest.mark.parametrize("page,k", [(0, 0), (16, 0), (128, 0), (0, 150), (16, 150)])
 def test_blocks_of_query_rows(G, T, page, k):
-    """Over 128 rows per KV head: two row tiles per block, up to four blocks; requests whose
-    trees fill one row tile only lie between them."""
+    """Over 128 rows per KV head: several blocks of rows; requests whose trees fill one block
+    only lie between them."""
     lens = [T + 400, 5, T + 131, 40, T + 7]
     sizes = [T, 3, T - 1, min(T, 17), T // 2 + 1]
     c = tree_case(G * T + page + k, G, 1, lens, sizes, T, page, "tree", k)
@@ -134,8 +134,7 @@ def test_two_captured_graphs_share_a_workspace():
 
 @pytest.mark.parametrize("page,k", [(0, 0), (16, 0), (16, 40)])
 def test_small_and_large_trees_in_turn(page, k):
-    """Two row tiles per block, most requests with rows for one only and one tile of tokens:
-    a row tile leaves many units out between two that it has."""
+    """Two blocks of rows in some requests, most with rows for one only and one tile of tokens."""
     gen = torch.Generator().manual_seed(page + k)
     B, T = 220, 40
     sizes = [40 if b % 7 == 3 else int(s) for b, s in enumerate(torch.randint(0, 20, (B,), generator=gen))]
