@@ -598,7 +598,8 @@ td_status td_probe_layer_reads(const td_shape *shape, const void *k_cache, const
  *          which rows x cluster fits one wave of SMs with at least 16384
  *          positions per CTA; else 1)
  *   "pdl", "topk_pdl": 0 turns off programmatic dependent launch between a
- *                   call's kernels / before the top-k kernel (default 1)
+ *                   call's kernels (the speculative-decoding calls: and behind
+ *                   the kernel before) / before the top-k kernel (default 1)
  *   "mma_full_tokens", "mma_sparse_tokens": tokens each warp of a
  *          tensor-core full (and full+select) / sparse kernel takes per round:
  *          8 (CTAs of 8 warps) or 16 (CTAs of 4 warps, both row groups of the

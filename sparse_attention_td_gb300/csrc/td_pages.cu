@@ -13,6 +13,26 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
+// Every kernel here is launched while the one before it in the stream may still
+// end (programmatic serialization) and waits for it before it touches memory.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename Args, typename... More>
+cudaError_t launch_behind(void (*kernel)(Args, More...), dim3 grid, int threads, cudaStream_t stream,
+                          const Args &a, More... more)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = host_pdl();
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, more...);
+}
+
 constexpr int kRowChunks = kHeadDim / 8;      // 16-byte chunks of one row
 
 // ------------------------------------------------------------ block tables
@@ -111,6 +131,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
     __shared__ int sm_prefix[kTableThreads], sm_first[kTableThreads], sm_cu[kTableThreads];
     __shared__ int sm_fit;
     const int tid = threadIdx.x;
+    wait_before();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the slot map's blocks may come
     uint32_t bad = 0;
     int count = *a.count;
@@ -243,7 +264,7 @@ constexpr int kSlotsPerThread = 4;
 __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const TablesArgs a)
 {
     __shared__ int sm_cu[1024];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_before();
     const int *cu = a.cu_new;
     const int total = a.cu_new[a.B];
     const int base = blockIdx.x * kSlotThreads * kSlotsPerThread;
@@ -275,11 +296,12 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const TablesArgs
 // -------------------------------------------------------------- slot append
 // One thread per 16 bytes: consecutive threads take consecutive chunks of a
 // token's K row (all heads), then of its V row.  32749 tokens of 8 KV heads (268 MB
-// read and written) take 44 us, 6.0 TB/s, bound by HBM; 257 tokens 2.0 us, a launch.
+// read and written) take 44 us, 6.0 TB/s, bound by HBM; 257 tokens 1.6 us, a launch.
 constexpr int kAppendThreads = 256;
 
 __global__ void __launch_bounds__(kAppendThreads) append_slots_kernel(const AppendSlotsArgs a)
 {
+    wait_before();
     const int per = a.Hkv * kRowChunks;                 // chunks of one token's K (or V)
     const long long total = (long long)a.tokens * 2 * per;
     const long long limit = (long long)a.num_pages * a.page_size;
@@ -310,9 +332,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_slots_kernel(const Appe
 // written in order: a later source lies behind every earlier destination.  In any
 // other order the whole CTA holds all rows of a task before it writes any.
 // Bound by latency: one dependent read behind the row search, then the write.
-// 32 requests x 32 layers x 8 KV heads, trees of 32 (71 MB): 15.4 us, 4.6 TB/s;
-// 3 requests x 4 layers 2.6 us.  The first at 4 / 3 / 2 tasks per warp: 15.4 /
-// 16.9 / 15.7 us.
+// 32 requests x 32 layers x 8 KV heads, trees of 32 (71 MB): 14.8 us, 4.8 TB/s;
+// 3 requests x 4 layers 2.3 us.  The first at 4 / 3 / 2 tasks per warp: 15.4 /
+// 16.9 / 15.7 us (launched in plain stream order).
 constexpr int kCommitWarps = 8;
 constexpr int kCommitTasks = 4;
 constexpr int kCommitRows = 16;       // rows a warp holds at a time
@@ -323,6 +345,7 @@ __global__ void __launch_bounds__(32 * kCommitWarps) tree_commit_kernel(const Co
     __shared__ int sm_behind, sm_moves;
     const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t bad = 0;
+    wait_before();
     const TreeLens len = tree_lens_of(a.seq_lens, a.tree_lens, b, a.T, a.Nmax, bad);
     const int ctx = len.n - len.nt;
     const int raw = a.accepted_lens[b];
@@ -427,21 +450,12 @@ __global__ void __launch_bounds__(32 * kCommitWarps) tree_commit_kernel(const Co
 
 cudaError_t launch_block_tables(const TablesArgs &a, cudaStream_t stream)
 {
-    block_tables_kernel<<<1, kTableThreads, 0, stream>>>(a);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_behind(block_tables_kernel, dim3(1), kTableThreads, stream, a);
     if (err != cudaSuccess || a.max_new == 0 || (a.B <= kTableThreads && a.max_new <= kOwnSlots))
         return err;
     constexpr int kPer = kSlotThreads * kSlotsPerThread;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)a.max_new + kPer - 1) / kPer));
-    cfg.blockDim = dim3(kSlotThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = host_pdl();
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, slot_map_kernel, a);
+    const dim3 grid((unsigned)(((long long)a.max_new + kPer - 1) / kPer));
+    return launch_behind(slot_map_kernel, grid, kSlotThreads, stream, a);
 }
 
 cudaError_t launch_append_slots(const AppendSlotsArgs &a, cudaStream_t stream)
@@ -451,8 +465,7 @@ cudaError_t launch_append_slots(const AppendSlotsArgs &a, cudaStream_t stream)
     long long grid = (total + kAppendThreads - 1) / kAppendThreads;
     if (grid > most)
         grid = most;
-    append_slots_kernel<<<(unsigned)grid, kAppendThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_behind(append_slots_kernel, dim3((unsigned)grid), kAppendThreads, stream, a);
 }
 
 cudaError_t launch_tree_commit(const CommitArgs &a, int num_layers, cudaStream_t stream)
@@ -462,8 +475,8 @@ cudaError_t launch_tree_commit(const CommitArgs &a, int num_layers, cudaStream_t
     int per_warp = (int)((long long)tasks * a.B / fill);
     per_warp = per_warp < 1 ? 1 : per_warp > kCommitTasks ? kCommitTasks : per_warp;
     const int per = kCommitWarps * per_warp;
-    tree_commit_kernel<<<dim3((tasks + per - 1) / per, a.B), 32 * kCommitWarps, 0, stream>>>(a, tasks, per_warp);
-    return cudaGetLastError();
+    return launch_behind(tree_commit_kernel, dim3((tasks + per - 1) / per, a.B), 32 * kCommitWarps, stream, a,
+                         tasks, per_warp);
 }
 
 }  // namespace td

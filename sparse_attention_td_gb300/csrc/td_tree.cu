@@ -515,6 +515,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         return;
     }
 
+    // ---- what needs no input, while the kernel before this one ends
     if (tid == 32 * C::kLoader) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_k) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_v) : "memory");
@@ -544,6 +545,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         bar_init(&x.never, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    pdl_wait();
     {   // the batch's page numbers and index entries into L2, a line per thread of the grid
         const size_t at = ((size_t)blockIdx.x * C::kThreads + tid) * 32;
         if (a.c.table && at < (size_t)a.B * a.c.max_blocks)
@@ -1383,10 +1385,6 @@ cudaError_t launch_tree_attention(const TreeArgs &a, int sms, cudaStream_t strea
         }
     }
     const int ctas = sms < kMaxTreeCtas ? sms : kMaxTreeCtas;
-    tree_attention_kernel<<<ctas, C::kThreads, C::kSmem, stream>>>(a);
-    err = cudaGetLastError();
-    if (err != cudaSuccess || ctas < 2)
-        return err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1394,8 +1392,15 @@ cudaError_t launch_tree_attention(const TreeArgs &a, int sms, cudaStream_t strea
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.stream = stream;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    err = cudaLaunchKernelEx(&cfg, tree_attention_kernel, a);
+    if (err != cudaSuccess || ctas < 2)
+        return err;
     cfg.gridDim = dim3(ctas - 1, (a.part_rows + kJoinWarps - 1) / kJoinWarps);
     cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.dynamicSmemBytes = 0;
     const JoinArgs j{a.plan, a.part_m, a.part_l, a.part_o, a.out, a.T, a.Hq, a.G, a.part_rows};
     return cudaLaunchKernelEx(&cfg, tree_join_kernel, j);
 }
