@@ -949,7 +949,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 auto issue_s = [&](int j) {
                     const uint32_t slot = (e + 2 * j) % C::kSlots, g = tiles + j;
                     const uint32_t k = operand(sm_ring + slot * kTileBytes, 16);
-                    if (j >= 2)                 // P V of tile j - 2 has read the P that goes next
+                    // P V of tile g - 2 has read the P that goes next.  (j = 0: its softmax has
+                    // waited for that before it handed over P of tile g - 1.  The phase before is
+                    // over by then, and P V of tile g - 1 is issued later: no phase is missed.)
+                    if (j >= 1 && g >= 2)
                         wait_bar(&x.o, g - 2);
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
