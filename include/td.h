@@ -93,7 +93,8 @@ typedef struct {
 const char *td_status_string(td_status status);
 
 /* Bytes of workspace needed by every call below for this shape and top_k
- * (top_k = 0 when no call selects or runs sparse attention).  Returns 0 for
+ * (top_k = 0 when no call selects or runs sparse attention), td_tree_attn and
+ * td_tree_sparse_attn apart (td_tree_workspace_size).  Returns 0 for
  * an invalid shape.  Does not touch the GPU. */
 size_t td_workspace_size(const td_shape *shape, int32_t top_k);
 
@@ -394,8 +395,12 @@ typedef struct {
  * tree_size drafted tokens per request, beside what td_workspace_size asks
  * for: a buffer that serves both kinds of calls holds the sum, one that serves
  * only the tree calls just these.  The tree calls use the last bytes of the
- * buffer and the status word at its start.  0 for an invalid shape or
- * tree_size.  Does not touch the GPU. */
+ * buffer and the status word at its start; the other calls keep counts that have
+ * to stay zero up to the last byte that td_workspace_size asks for.  So do not
+ * give the tree calls a buffer of td_workspace_size bytes alone, even where it
+ * is large enough: the size check cannot tell, and later selections would start
+ * from damaged counts.  0 for an invalid shape or tree_size.  Does not touch the
+ * GPU. */
 size_t td_tree_workspace_size(const td_shape *shape, int32_t tree_size);
 
 /*

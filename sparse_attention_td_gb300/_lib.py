@@ -204,18 +204,22 @@ def td_tree_workspace_size(shape: Shape, tree_size: int) -> int:
 
 class Workspace:
     """A zero-initialised device workspace of td_workspace_size bytes; with
-    tree_size also td_tree_workspace_size bytes, for the tree calls."""
+    tree_size also td_tree_workspace_size bytes, for the tree calls.  Those write
+    the buffer's last bytes, which the other calls must find as they left them: the
+    tree calls take only a workspace with a tree part of their size, the others see
+    the buffer without it."""
 
     def __init__(self, shape: Shape, top_k: int, device=None, stream=None, tree_size: int = 0):
         n = td_workspace_size(shape, top_k)
         if n == 0:
             raise TdError(1, "td_workspace_size")
+        self.tree_bytes = 0
         if tree_size:
-            more = td_tree_workspace_size(shape, tree_size)
-            if more == 0:
+            self.tree_bytes = td_tree_workspace_size(shape, tree_size)
+            if self.tree_bytes == 0:
                 raise TdError(1, "td_tree_workspace_size")
-            n += more
-        self.tensor = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        self._trees = set()          # (query heads, KV heads, tree size) known to fit
+        self.tensor = torch.empty(n + self.tree_bytes, dtype=torch.uint8, device=device or "cuda")
         td_workspace_init(self.tensor, stream)
 
     @property
@@ -224,7 +228,19 @@ class Workspace:
 
     @property
     def nbytes(self) -> int:
-        return self.tensor.numel()
+        """Bytes without the tree part."""
+        return self.tensor.numel() - self.tree_bytes
+
+    def check_tree(self, shape: Shape, tree_size: int):
+        key = (shape.num_q_heads, shape.num_kv_heads, tree_size)
+        if key in self._trees:
+            return
+        need = td_tree_workspace_size(shape, tree_size)
+        if need > self.tree_bytes:
+            raise ValueError(f"ws has {self.tree_bytes} bytes for tree calls, needs {need} "
+                             f"(Workspace(..., tree_size={tree_size}))")
+        if need:                     # (0: the call refuses the shape or tree_size)
+            self._trees.add(key)
 
     def status(self, stream=None) -> int:
         return td_workspace_status(self.tensor, stream)
@@ -350,6 +366,12 @@ def _ws(dev, ws):
     return t.data_ptr(), t.numel()
 
 
+def _tree_ws(dev, ws, shape, tree_size):
+    where = _ws(dev, ws)
+    ws.check_tree(shape, tree_size)
+    return where
+
+
 class Cache:
     """One layer's K/V rows (td_cache): k, v [pages][Hkv][page_size][128] and a
     block table [B][max_blocks], or without a table a contiguous cache
@@ -404,8 +426,8 @@ def td_tree_attn(shape: Shape, cache: Cache, tree_size, tree_lens, tree_mask, q,
     """Attention of tree_size drafted tokens per request over the cache;
     tree_mask int32 words [B][T][ceil(T / 32)] (None: a chain)."""
     dev, st = _launch(stream)
-    wp, wn = _ws(dev, ws)
     nb, T = shape.batch, int(tree_size)
+    wp, wn = _tree_ws(dev, ws, shape, T)
     n = nb * T * shape.num_q_heads * 128
     rc = lib().td_tree_attn(
         shape, cache.check(shape, dev), T,
@@ -421,8 +443,8 @@ def td_tree_sparse_attn(shape: Shape, cache: Cache, tree_size, tree_lens, tree_m
                         idx, top_k, out, ws: Workspace = None, stream=None):
     """td_tree_attn over the persisted index set of a PPSA layer and the tree."""
     dev, st = _launch(stream)
-    wp, wn = _ws(dev, ws)
     nb, T, k = shape.batch, int(tree_size), int(top_k)
+    wp, wn = _tree_ws(dev, ws, shape, T)
     n = nb * T * shape.num_q_heads * 128
     rc = lib().td_tree_sparse_attn(
         shape, cache.check(shape, dev), T,
