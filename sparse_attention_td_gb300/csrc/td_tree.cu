@@ -176,13 +176,14 @@ __device__ __forceinline__ void prefetch_l2(const void *p)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// Row `tok` of a tile from cache row `row` (below 0: zeros), by half a warp: chunk
-// c at tok * 128 + ((c ^ tok) & 7) * 16 of its half.
-__device__ __forceinline__ void copy_row(uint32_t dst, int tok, const uint16_t *src, int row, int lane)
+// Row `tok` of a tile from cache row `row` (none of the cache's `rows`: zeros), by half
+// a warp: chunk c at tok * 128 + ((c ^ tok) & 7) * 16 of its half.
+__device__ __forceinline__ void copy_row(uint32_t dst, int tok, const uint16_t *src, uint32_t row, uint32_t rows,
+                                         int lane)
 {
     const int c = lane & 15;
     copy16(dst + (c >> 3) * kHalfBytes + tok * 128 + (((c ^ tok) & 7) << 4),
-           src + (size_t)max(row, 0) * kHeadDim + c * 8, row >= 0);
+           src + (size_t)(row < rows ? row : 0) * kHeadDim + c * 8, row < rows);
 }
 
 // Shared-memory operand of tcgen05.mma, 128-byte swizzle.  K-major (rows of
@@ -464,7 +465,28 @@ struct Walk {
     __device__ int rows(const TreeArgs &a) const { return min(w.nt * a.G - m * kTile, kTile); }
 };
 
-// Shared memory behind the Q tiles and the ring.
+// Shared memory behind the Q tile and the ring.
+//
+// Who arrives at a barrier and who waits.  A wait looks at a phase's parity only, so
+// each must come when the phase before is over and the one after cannot be:
+//   full     a slot's use: the copy warps (as their copies land), or its loader with the
+//            boxes' bytes.  The issuer waits for every use in order.  The softmax, at a
+//            unit's last tile, for V of tile g: S of g was issued behind P V of g - 3, the
+//            use before; the use after needs P V of g, which needs this warp's P.
+//   empty    the commit behind the MMAs that read the slot.  The one loader that owns the
+//            slot waits for every use in order.
+//   rows_there, go, rows_read   a row list, one finder each: written (loaders), then the
+//            slots for its K and V free (copy warps), then read (the finder, before it
+//            writes the next one there).  Every party waits for every use in order, and
+//            the next use needs all of them: its finder all copy warps, these every go,
+//            which a loader gives after it has seen rows_there and read rows_valid.
+//   q, q_free   as full and empty, per segment, copy warps and issuer.
+//   s        S of tile g, every softmax warp waits for every one.  S of g + 2 is issued
+//            behind the issuer's wait for p of g, to which every softmax warp arrives.
+//   p        all four softmax warps; the issuer waits for every one.
+//   o        P V of tile g.  Waited for by the softmax (see o_done) and before S of g + 2
+//            (see issue_s): the reasons stand there.
+//   drain, done   once, by the issuer.
 struct Extra {
     using C = Cfg;
     uint64_t full[C::kSlots], empty[C::kSlots];   // ring: filled, read
@@ -486,6 +508,7 @@ struct Extra {
     Walk start;
     uint32_t tmem;
     int gave_up;
+    int last_waits[C::kThreads / 32];             // a warp's waits after that: run out
 };
 
 // One CTA per SM; each takes an equal, contiguous range of the batch's tiles
@@ -522,6 +545,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     }
     if (tid == 32 * C::kIssuer) {
         x.gave_up = 0;
+        for (int i = 0; i < C::kThreads / 32; ++i)
+            x.last_waits[i] = 0;
         x.start.left = 0;
         for (int i = 0; i < C::kSlots; ++i) {
             bar_init(&x.full[i], 32 * C::kCopiers);
@@ -853,6 +878,9 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         // exist is filled with zeros (no stale V value meets its zero probability).
         const int me = C::copier(warp);
         constexpr uint32_t kRing = C::kRowRing;
+        // No list holds a row outside the cache; one that did would be reported, not followed.
+        const uint32_t cache_rows = (uint32_t)(a.c.num_pages * a.Hkv * a.c.page_size);
+        bool strange = false;
         uint32_t e = 0, copied = 0;
         bool ok = true;
 #pragma unroll 1
@@ -906,8 +934,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                             lds_words(smem_of(&x.rows[ring][tok + 32]), ahead);
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
-                            if (tok + v < end)
-                                copy_row(dst, tok + v, src, (int)rows[v], lane);
+                            if (tok + v < end) {
+                                copy_row(dst, tok + v, src, rows[v], cache_rows, lane);
+                                strange |= rows[v] >= cache_rows && rows[v] != 0xffffffffu;
+                            }
                     }
                     copies_arrive(&x.full[slot]);
                 }
@@ -920,6 +950,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             e += 2 * n;
             walk.next(a, n);
         }
+        if (strange)
+            atomicOr(a.status, kFlagPageOutOfRange);
     } else if (warp == C::kIssuer) {
         // ---- MMA issue, by one thread: S of tile j + 1 before P V of tile j, so the
         // tensor cores work while the softmax does.
@@ -1271,18 +1303,18 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         // entries of a loader's slots can be; what was issued does complete, and these
         // waits have the default limit.
         constexpr long long kLimit = 2000000000ll;
-        int own_limit = 0;
+        volatile int *own_limit = &x.last_waits[warp];
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (warp == C::kLoader || loads_v) {
             const uint32_t slots = split ? C::kSlots / 2 : C::kSlots;
             for (uint32_t n = loaded > slots ? loaded - slots : 0; n < loaded; ++n) {
                 const uint32_t e = split ? 2 * n + (loads_v ? 1 : 0) : n;
                 if (loaded_boxes >> (loaded - 1 - n) & 1)
-                    bar_wait_for(&x.full[e % C::kSlots], (e / C::kSlots) & 1, &own_limit, kLimit);
+                    bar_wait_for(&x.full[e % C::kSlots], (e / C::kSlots) & 1, own_limit, kLimit);
             }
         } else if (warp == C::kIssuer && elect_one()) {      // (the lane that issued them)
             mma_commit(&x.drain);
-            bar_wait_for(&x.drain, 0, &own_limit, kLimit);
+            bar_wait_for(&x.drain, 0, own_limit, kLimit);
         }
         __syncthreads();
     }
