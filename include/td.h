@@ -626,8 +626,9 @@ td_status td_probe_layer_reads(const td_shape *shape, const void *k_cache, const
  *          streamed); 0 one contiguous chunk each; negative restores the
  *          default
  *   "wait_limit_us": microseconds after which a staged full-layer CTA stops
- *          waiting for a bulk copy, or a tree-attention CTA for its copies and
- *          products (default 1 s; a tree-attention CTA that gives up waits, with
+ *          waiting for a bulk copy, or a tree-attention CTA that has finished no
+ *          tile of 128 tokens meanwhile for its copies and products (default 1 s;
+ *          a tree-attention CTA that gives up waits, with
  *          limits, for what it has in flight, sets TD_FLAG_WAIT_TIMEOUT and leaves:
  *          its rows are not valid, the next launch is not affected).  A CTA that gives up waits
  *          (at the default limit) for every copy it issued, then joins the

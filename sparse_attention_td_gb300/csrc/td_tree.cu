@@ -124,29 +124,41 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity)
     return done != 0;
 }
 
+// What waits look at before they give up: whether another role has, and the tiles done
+// by the CTA so far.
+struct Progress {
+    int gave_up;
+    uint32_t tiles;
+};
+
 // Waits for the phase of the given parity.  Gives up after `limit` cycles of the SM
-// clock, or when another role has (then the CTA leaves as a whole and reports the
+// clock without a tile done (a role may have nothing to do for most of a long unit),
+// or when another role has (then the CTA leaves as a whole and reports the
 // timeout).  Out of line: the roles' code has to stay in the instruction cache.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, unsigned parity, volatile int *gave_up, long long limit)
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, unsigned parity, volatile Progress *at, long long limit)
 {
-    const long long t0 = clock64();
+    long long t0 = clock64();
+    uint32_t tiles = at->tiles;
     for (int polls = 1;; ++polls) {
         if (bar_try(bar, parity))
             return true;
         if ((polls & 63) == 0) {
-            if (*gave_up)
+            if (at->gave_up)
                 return false;
-            if (clock64() - t0 > limit) {
-                *gave_up = 1;
+            if (at->tiles != tiles) {
+                tiles = at->tiles;
+                t0 = clock64();
+            } else if (clock64() - t0 > limit) {
+                at->gave_up = 1;
                 return false;
             }
         }
     }
 }
 
-__device__ __forceinline__ bool bar_wait_for(uint64_t *bar, unsigned parity, volatile int *gave_up, long long limit)
+__device__ __forceinline__ bool bar_wait_for(uint64_t *bar, unsigned parity, volatile Progress *at, long long limit)
 {
-    return bar_try(smem_of(bar), parity) || bar_wait_long(smem_of(bar), parity, gave_up, limit);
+    return bar_try(smem_of(bar), parity) || bar_wait_long(smem_of(bar), parity, at, limit);
 }
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const TmaDesc *map, int x, int row, uint64_t *bar)
@@ -507,8 +519,8 @@ struct Extra {
     int sums[C::kThreads / 32];
     Walk start;
     uint32_t tmem;
-    int gave_up;
-    int last_waits[C::kThreads / 32];             // a warp's waits after that: run out
+    Progress progress;
+    Progress last_waits[C::kThreads / 32];        // of a warp's waits after the CTA gave up
 };
 
 // One CTA per SM; each takes an equal, contiguous range of the batch's tiles
@@ -526,12 +538,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     static_assert(C::kCopiers == 4, "copy warps' rows of a tile");
     static_assert((1 + C::kSlots) * kTileBytes + sizeof(Extra) <= C::kSmem, "shared memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    auto bar_wait = [&](uint64_t *bar, unsigned parity, volatile int *up) {
-        return bar_wait_for(bar, parity, up, a.wait_cycles);
+    auto bar_wait = [&](uint64_t *bar, unsigned parity, volatile Progress *at) {
+        return bar_wait_for(bar, parity, at, a.wait_cycles);
     };
     const uint32_t sm_q = smem_of(sm_raw);        // 1024-byte aligned: nothing static lies before it
     const uint32_t sm_ring = sm_q + kTileBytes;
-    volatile int *gave_up = &x.gave_up;
+    volatile Progress *progress = &x.progress;
     if (sm_q & 1023) {            // (cannot be: the swizzled tiles need it)
         if (tid == 0)
             atomicOr(a.status, kFlagWaitTimeout);
@@ -544,9 +556,9 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.box_v) : "memory");
     }
     if (tid == 32 * C::kIssuer) {
-        x.gave_up = 0;
+        x.progress = Progress{};
         for (int i = 0; i < C::kThreads / 32; ++i)
-            x.last_waits[i] = 0;
+            x.last_waits[i] = Progress{};
         x.start.left = 0;
         for (int i = 0; i < C::kSlots; ++i) {
             bar_init(&x.full[i], 32 * C::kCopiers);
@@ -754,7 +766,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                         flags |= kFlagPageOutOfRange;
                     }
                 } else {
-                    ok = __all_sync(kFull, bar_wait(&x.rows_there[ring], copied / C::kRowRing & 1, gave_up));
+                    ok = __all_sync(kFull, bar_wait(&x.rows_there[ring], copied / C::kRowRing & 1, progress));
                     if (!ok)
                         break;
                     word = x.rows_valid[ring][lane & 3];
@@ -763,7 +775,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 for (int kv = kv0; kv < kv1; ++kv) {
                     const uint32_t e = 2 * tile_no + kv, slot = e % C::kSlots, use = e / C::kSlots;
                     if (use > 0)
-                        ok = __all_sync(kFull, bar_wait(&x.empty[slot], (use - 1) & 1, gave_up));
+                        ok = __all_sync(kFull, bar_wait(&x.empty[slot], (use - 1) & 1, progress));
                     if (!ok)
                         break;
                     if (kv == 0 && lane < 4)
@@ -851,7 +863,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 }
                 const uint32_t ring = tile % kRing;
                 if (tile >= kRing)        // every copy warp has read the list before
-                    ok = __all_sync(kFull, bar_wait(&x.rows_read[ring], (tile / kRing - 1) & 1, gave_up));
+                    ok = __all_sync(kFull, bar_wait(&x.rows_read[ring], (tile / kRing - 1) & 1, progress));
                 if (!ok)
                     break;
 #pragma unroll
@@ -890,7 +902,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             // that are not Q's are left as they are.
             const int last = (int)seg - (two_q ? 2 : 1);
             if (last >= 0)
-                ok = __all_sync(kFull, bar_wait(&x.q_free[last & 1], (last >> 1) & 1, gave_up));
+                ok = __all_sync(kFull, bar_wait(&x.q_free[last & 1], (last >> 1) & 1, progress));
             if (!ok)
                 break;
             {
@@ -915,7 +927,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 const int tok0 = 8 * me + 4 * (lane >> 4);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
-                    ok = __all_sync(kFull, bar_wait(&x.go[ring][kv], phase, gave_up));
+                    ok = __all_sync(kFull, bar_wait(&x.go[ring][kv], phase, progress));
                     if (!ok)
                         break;
                     const uint32_t slot = (e + 2 * i + kv) % C::kSlots;
@@ -964,13 +976,13 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             // come through it and need no fence.
             auto proxy_fence = [] { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); };
             auto wait_full = [&](uint32_t entry, bool copied) {
-                ok = ok && bar_wait(&x.full[entry % C::kSlots], (entry / C::kSlots) & 1, gave_up);
+                ok = ok && bar_wait(&x.full[entry % C::kSlots], (entry / C::kSlots) & 1, progress);
                 if (copied)
                     proxy_fence();
                 return ok;
             };
             auto wait_bar = [&](uint64_t *bar, uint32_t phase) {
-                ok = ok && bar_wait(bar, phase & 1, gave_up);
+                ok = ok && bar_wait(bar, phase & 1, progress);
                 tmem_after();
                 return ok;
             };
@@ -1023,6 +1035,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                                    j > 0 || s > 0);
                     mma_commit(&x.o);
                     mma_commit(&x.empty[slot]);
+                    progress->tiles = g + 1;
                 }
                 tiles += n;
                 e += 2 * n;
@@ -1031,7 +1044,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             // Nobody waits for the last commits to the ring's slots and Q: no arrival of
             // theirs may be left when the CTA ends.
             mma_commit(&x.done);
-            bar_wait(&x.done, 0, gave_up);
+            bar_wait(&x.done, 0, progress);
         }
         __syncwarp();
     } else {
@@ -1077,11 +1090,11 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                 bool waited = j == 0;
                 auto o_done = [&]() {
                     if (!waited)
-                        ok = __all_sync(kFull, bar_wait(&x.o, (count - 1) & 1, gave_up));
+                        ok = __all_sync(kFull, bar_wait(&x.o, (count - 1) & 1, progress));
                     waited = true;
                 };
                 ok = __all_sync(kFull, bar_wait(a.wait_test ? &x.never : &x.s[count & 1],
-                                                a.wait_test ? 0 : count >> 1 & 1, gave_up));
+                                                a.wait_test ? 0 : count >> 1 & 1, progress));
                 if (!ok)
                     break;
                 tmem_after();
@@ -1101,7 +1114,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
                     // leave the tile here and join the rows that do see it below.
                     const uint32_t entry = 2 * count + 1;
                     ok = __all_sync(kFull, bar_wait(&x.full[entry % C::kSlots],
-                                                    (entry / C::kSlots) & 1, gave_up));
+                                                    (entry / C::kSlots) & 1, progress));
                     if (!ok)
                         break;
                     const uint32_t v = sm_ring + entry % C::kSlots * kTileBytes + r * 128;
@@ -1238,7 +1251,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
             if (!ok)
                 break;
             // ---- the segment's result
-            ok = __all_sync(kFull, bar_wait(&x.o, (count - 1) & 1, gave_up));
+            ok = __all_sync(kFull, bar_wait(&x.o, (count - 1) & 1, progress));
             if (!ok)
                 break;
             tmem_after();
@@ -1298,27 +1311,27 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     }
     tmem_before();
     __syncthreads();
-    if (x.gave_up) {
+    if (x.progress.gave_up) {
         // A wait gave up: leave no copy and no MMA in flight.  Of the boxes the last
         // entries of a loader's slots can be; what was issued does complete, and these
         // waits have the default limit.
         constexpr long long kLimit = 2000000000ll;
-        volatile int *own_limit = &x.last_waits[warp];
+        volatile Progress *own = &x.last_waits[warp];
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (warp == C::kLoader || loads_v) {
             const uint32_t slots = split ? C::kSlots / 2 : C::kSlots;
             for (uint32_t n = loaded > slots ? loaded - slots : 0; n < loaded; ++n) {
                 const uint32_t e = split ? 2 * n + (loads_v ? 1 : 0) : n;
                 if (loaded_boxes >> (loaded - 1 - n) & 1)
-                    bar_wait_for(&x.full[e % C::kSlots], (e / C::kSlots) & 1, own_limit, kLimit);
+                    bar_wait_for(&x.full[e % C::kSlots], (e / C::kSlots) & 1, own, kLimit);
             }
         } else if (warp == C::kIssuer && elect_one()) {      // (the lane that issued them)
             mma_commit(&x.drain);
-            bar_wait_for(&x.drain, 0, own_limit, kLimit);
+            bar_wait_for(&x.drain, 0, own, kLimit);
         }
         __syncthreads();
     }
-    if (tid == 0 && x.gave_up)
+    if (tid == 0 && x.progress.gave_up)
         atomicOr(a.status, kFlagWaitTimeout);
     if (warp == C::kIssuer) {
         tmem_after();
