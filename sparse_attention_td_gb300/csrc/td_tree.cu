@@ -1359,6 +1359,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
     auto part_row = [&](int s) {
         return (size_t)(2 * (c - 1 + s) + (s == 0 && j.late ? 1 : 0)) * a.part_rows + r;
     };
+    auto not_finite = [](float v) { return fabsf(v) < CUDART_INF_F ? 0.0f : v; };
     const int parts = j.last - c + 2;
     constexpr int kAhead = 8;
     float top = -CUDART_INF_F, l = 0.0f;
@@ -1397,6 +1398,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
                 o.y += x[u].y * f;
                 o.z += x[u].z * f;
                 o.w += x[u].w * f;
+            } else if (ls[u] != 0.0f) {
+                // a weight too small for fp32 is not zero: what is not finite stays so
+                o.x += not_finite(x[u].x);
+                o.y += not_finite(x[u].y);
+                o.z += not_finite(x[u].z);
+                o.w += not_finite(x[u].w);
             }
         }
         top = mn;
