@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from spec_util import D
 from test_spec_gpu import _built, check_tree, run_tree, tree_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
