@@ -122,7 +122,7 @@ __device__ __forceinline__ int slot_of(const TablesArgs &a, int b, int p, int he
 // thread's work (its request found by a search of the chunk's prefix sums), so
 // one long prompt does not make one thread walk all of its pages.  What bounds
 // it is the chain of dependent loads and barriers, not its bytes: 256 requests that
-// grow by up to 9 tokens each 6.2 us, slot map included; 61 prompts of 1K to 8K
+// grow by up to 9 tokens each 6.1 us, slot map included; 61 prompts of 1K to 8K
 // tokens 10.0 us with the slot map's kernel.
 __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const TablesArgs a)
 {
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_slots_kernel(const Appe
 // written in order: a later source lies behind every earlier destination.  In any
 // other order the whole CTA holds all rows of a task before it writes any.
 // Bound by latency: one dependent read behind the row search, then the write.
-// 32 requests x 32 layers x 8 KV heads, trees of 32 (71 MB): 14.8 us, 4.8 TB/s;
+// 32 requests x 32 layers x 8 KV heads, trees of 32 (71 MB): 14.9 us, 4.8 TB/s;
 // 3 requests x 4 layers 2.3 us.  The first at 4 / 3 / 2 tasks per warp: 15.4 /
 // 16.9 / 15.7 us (launched in plain stream order).
 constexpr int kCommitWarps = 8;

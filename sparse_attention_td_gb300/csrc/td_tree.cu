@@ -14,23 +14,29 @@
 // O += P V, on the tensor cores (tcgen05.mma, 128 query rows; S, P and O in
 // tensor memory, K and V tiles in shared memory).  P is rounded to bf16, the
 // products' operand type (relative error at most 2^-8, as in the rows themselves);
-// S, O, m and l are fp32.
+// S, O, m and l are fp32.  (A second bf16 term of P, 16 bits together, makes P V and
+// the softmax longer by more than the loads hide: the cases below 248 -> 270, 241 ->
+// 266, 38.4 -> 41.3 and 14.4 -> 15.1 us.  Not taken: the output's own rounding is as
+// coarse as one term's.)
 //
 // What bounds it, measured on GB300 (a copy of the same bytes runs at 6.7 TB/s):
 //   reading the cache, once per 128 query rows of a KV head:
 //     32 requests of 8K-16K, 8 KV heads, G = 4, 16 nodes, 64-token pages: 248 us, 6.6 TB/s
 //     one request of 100K, 32 KV heads, G = 1, 32 nodes:                  242 us, 6.9 TB/s
-//     4 x 32K, 8 KV heads, G = 4, 64 nodes (256 rows, two reads):         157 us, 6.7 TB/s
+//     4 x 32K, 8 KV heads, G = 4, 64 nodes (256 rows, two reads): 144-166 us, by where the
+//     cache lies, 6.3-7.2 TB/s: twice the time that one read takes
 //   launch, first loads and the join, where a step is short:
-//     4 x 257-2050, 8 KV heads, G = 8, one node, 16-token pages:  14.5 us
-//     4 x 32K, G = 4, 2048 index entries, 5 nodes:                16.6 us
+//     4 x 257-2050, 8 KV heads, G = 8, one node, 16-token pages:  14.6 us
+//     (a contiguous cache: 15.0; td_full_attn_select there:       17.9 us)
+//     4 x 32K, G = 4, 2048 index entries, 5 nodes:                16.8 us
+//     (reads of the same rows alone, call after call:             8.8 us)
 //     (the two launches alone, every CTA leaving at once:         4.5 us)
 //   copies of single rows, where an index set names them, and the ends of units:
-//     32 requests, G = 4, 1024 index entries, 16 nodes:  37.7 us, 3.9 TB/s
+//     32 requests, G = 4, 1024 index entries, 16 nodes:  38.2 us, 3.8 TB/s
 // The roles' code together does not fit an SM's instruction cache: on the last of
-// these 18% of its requests missed with 100 KB of code, and with 70 KB (waits, unit
-// changes and rare cases out of line, loops left rolled, no branches where a selection
-// does) it takes 37 us instead of 50.
+// these 18% of its requests missed with 100 KB of code and 15% do with 70 KB (waits,
+// unit changes and rare cases out of line, loops left rolled, no branches where a
+// selection does), which took it from 50 us to 37.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -671,7 +677,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
     // segment's comes in during this one.  (The MMA reads 128 rows from either;
     // the rows that are not Q's end in S and O rows that nobody reads.)
     const bool two_q = a.part_rows <= 64;
-    uint32_t loaded = 0;          // loaders: ring entries begun
+    uint32_t loaded = 0;          // a loader's ring entries begun
     uint32_t loaded_boxes = 0;    // which of the last ones came as boxes (bit 0: the last)
     uint32_t tmem = 0;
     // Boxes of 8 or 16 rows are more than one warp can issue (80 cycles each).  In full
@@ -818,8 +824,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a)
         if (flags && lane == 0)
             atomicOr(a.status, flags);
     } else if (warp >= C::kFinder && warp < C::kFinder + C::kFinders) {
-        // ---- finders (one or two): the cache rows of the tiles for the copy warps, as
-        // far ahead as there are lists.  (Memory is slow to answer while every SM's
+        // ---- finders, both of them, or the first where the second loads V: the cache rows
+        // of the tiles for the copy warps, as far ahead as there are lists.  (Memory is slow to answer while every SM's
         // ring fills: found by the copy warps themselves, between two tiles, the rows
         // cost 1500 to 3000 cycles a tile.)
         const int me = warp - C::kFinder, finders = split ? 1 : C::kFinders;
