@@ -72,8 +72,8 @@ typedef enum {
 #define TD_FLAG_WAIT_TIMEOUT 0x4u         /* a staged kernel's bounded wait for its copies gave up;
                                              that (batch, KV head)'s output lacks the tokens of
                                              the CTA that gave up (the workspace stays usable).
-                                             td_tree_*: the rows of the CTA that gave up are not
-                                             valid */
+                                             td_tree_*, td_window_attn and td_q4_attn with cu_new:
+                                             the rows of the CTA that gave up are not valid */
 #define TD_FLAG_TREE_OUT_OF_RANGE 0x8u    /* tree_lens[b], accepted_lens[b] or an accepted node
                                              outside its range: clamped / skipped */
 #define TD_FLAG_PAGE_OUT_OF_RANGE 0x10u   /* a page number, page count or slot outside the cache:
@@ -94,7 +94,8 @@ const char *td_status_string(td_status status);
 
 /* Bytes of workspace needed by every call below for this shape and top_k
  * (top_k = 0 when no call selects or runs sparse attention), td_tree_attn and
- * td_tree_sparse_attn apart (td_tree_workspace_size).  Returns 0 for
+ * td_tree_sparse_attn (td_tree_workspace_size) and the calls on small caches
+ * (td_cache_workspace_size) apart.  Returns 0 for
  * an invalid shape.  Does not touch the GPU. */
 size_t td_workspace_size(const td_shape *shape, int32_t top_k);
 
@@ -528,6 +529,144 @@ td_status td_block_tables(int32_t batch, int32_t page_size, int32_t max_blocks, 
                           int32_t max_new, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * ---- Small caches: windows, 4-bit rows, eviction -----------------------------
+ *
+ * A decode step is bound by reading the cache.  These calls keep that small:
+ * layers that see a window and a few first tokens, rows held in 4 bits, and
+ * caches from which the positions with the least attention weight are taken.
+ * They work on td_cache (pages or contiguous) and on its 4-bit form:
+ *
+ * td_q4_cache: one layer's K/V rows in 4 bits.  16 neighbouring values of a row share
+ * a scale:  value = code * scale,  code one of +-{0, .5, 1, 1.5, 2, 3, 4, 6} (e2m1),
+ * scale an e4m3 value.  144 bytes per token and KV head instead of 512.
+ *   k, v     device bytes [num_pages][num_kv_heads][page_size][64], 16-byte aligned:
+ *            value 2i in the low half of byte i, value 2i + 1 in the high half.
+ *   scales   device bytes [num_pages][num_kv_heads][page_size][16], 16-byte aligned:
+ *            the 8 scales of the token's K row, then those of its V row.
+ *   block_table, max_blocks, num_pages, page_size   as in td_cache.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    void *scales;
+    int32_t num_pages;
+    int32_t page_size;
+    const int32_t *block_table;
+    int32_t max_blocks;
+} td_q4_cache;
+
+/* Bytes of workspace td_window_attn, td_q4_attn, td_q4_sparse_attn and td_weights_attn need
+ * for this shape, beside what td_workspace_size and td_tree_workspace_size ask for: a buffer
+ * that serves several kinds of calls holds the sum.  These calls use the status word at
+ * the buffer's start and its last bytes, some of which they must find as they left
+ * them: give them a buffer (or a part of one that begins at its start) whose last bytes
+ * no other kind of call writes, and always of the same size.  td_evict needs the
+ * status word alone.  0 for an invalid shape.  Does not touch the GPU. */
+size_t td_cache_workspace_size(const td_shape *shape);
+
+/*
+ * Attention of new tokens over a cache, one layer, with a sliding window and a few first
+ * tokens that stay visible.  The new tokens' K/V rows are in the cache already: request
+ * b's n_b new tokens are the last of its seq_lens[b] cached ones.  The token at position p
+ * sees
+ *     { j <= p : j < sinks  or  p - j < window }        (window = 0: every j <= p)
+ * in one softmax:  out[i][h] = sum_j softmax(scale * q[i][h] . K[j]) V[j].
+ *   cu_new     device int32 [batch + 1]: request b's new tokens are rows cu_new[b] ..
+ *              cu_new[b + 1] - 1 of q and out (td_block_tables writes it); ascending, between
+ *              0 and num_tokens.  Any mix of prompts, chunks and single tokens.  Rows that
+ *              belong to no request are left as they were.  NULL: one new token per
+ *              request, row b; num_tokens = batch (the form for decoding: one request's
+ *              tokens are shared out over many SMs).
+ *   q, out     device bf16 [num_tokens][num_q_heads][128], 16-byte aligned.
+ *   window, sinks >= 0.
+ * A token that sees no position (seq_lens[b] = 0; more new tokens than cached ones, which also
+ * sets TD_FLAG_SEQ_LEN_OUT_OF_RANGE) gets 0.  K/V values that a token does not see never reach
+ * it, whatever they hold.  (Where a unit of 256 query rows meets V values that are not
+ * finite, its rows are computed again one by one: right, but slow.)  Scores, statistics and
+ * sums are fp32; with cu_new the probabilities enter the second product as bf16 (relative
+ * error at most 2^-8 each), without as two bf16 terms.
+ *   shape      max_seq_len bounds seq_lens (a longer one is clamped and flagged); at most
+ *              2^30, and it must fit the cache's positions per request.
+ */
+td_status td_window_attn(const td_shape *shape, const td_cache *cache, int32_t window, int32_t sinks,
+                         int32_t num_tokens, const int32_t *cu_new, const void *q,
+                         const int32_t *seq_lens, void *out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The same over a 4-bit cache.  Its values enter the products exactly, as fp16; q enters as fp16 too,
+ * each row times a power of two (a value below 2^-22 times the row's largest loses bits),
+ * the probabilities as fp16 (relative error at most 2^-11; below 2^-14 of the largest one,
+ * an absolute 2^-25 of it).
+ */
+td_status td_q4_attn(const td_shape *shape, const td_q4_cache *cache, int32_t window, int32_t sinks,
+                     int32_t num_tokens, const int32_t *cu_new, const void *q,
+                     const int32_t *seq_lens, void *out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * A PPSA layer over a 4-bit cache: one token per request over the persisted set (as
+ * td_sparse_attn: distinct positions, any order, -1 is padding; an entry outside
+ * [-1, seq_lens[b]) is skipped and sets TD_FLAG_INDEX_OUT_OF_RANGE).
+ *   q, out   device bf16 [batch][num_q_heads][128], 16-byte aligned.
+ *   idx      device int32 [batch][num_kv_heads][top_k], 1 <= top_k <= max_seq_len.
+ */
+td_status td_q4_sparse_attn(const td_shape *shape, const td_q4_cache *cache, const void *q,
+                            const int32_t *seq_lens, const int32_t *idx, int32_t top_k, void *out,
+                            void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * New K/V rows of a packed batch into one layer's 4-bit cache (arguments as td_kv_append_slots).
+ * Per 16 values:  scale = the e4m3 value nearest to max |x| / 6, at most 448;
+ * code = the one nearest to x / scale, ties to the even code (0, 1, 2, 4, ..), at most 6.  Both are
+ * decided exactly.  Larger values than 6 * 448 are held as that; a scale of 0 holds
+ * zeros; 16 values of which one is NaN are held as NaN (a NaN scale).
+ */
+td_status td_q4_append(const td_shape *shape, const td_q4_cache *cache, int32_t num_tokens,
+                       const void *k_new, const void *v_new, int64_t new_stride,
+                       const int32_t *slot_map, void *stream);
+
+/*
+ * Full attention of one token per request over a td_cache (out as td_window_attn without
+ * a window), which also adds up how much weight each cached position gets: for n <
+ * seq_lens[b], with p_h the probabilities of query head h,
+ *     weights[b][g][n] = (n < seq_lens[b] - fresh ? weights[b][g][n] : 0) + sum_{h of g} p_h[n].
+ *   fresh     the last `fresh` positions have no sum yet: 1 in a decode step that appended
+ *             one token, max_seq_len for a cache without sums.
+ *   weights   device fp32 [batch][num_kv_heads][max_seq_len]; entries from seq_lens[b] on are
+ *             left as they were.
+ *   logits    device fp32 [batch][num_q_heads][max_seq_len]: receives the scaled scores
+ *             (entries below seq_lens[b]; -inf where the page is none).  Not overlapping
+ *             weights.
+ */
+td_status td_weights_attn(const td_shape *shape, const td_cache *cache, int32_t fresh, const void *q,
+                          const int32_t *seq_lens, float *weights, float *logits, void *out, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/*
+ * Eviction: of a request with seq_lens[b] > budget positions each KV head keeps `budget`: the
+ * first `sinks`, the last `recent`, and of the others those with the most weight (ties: the lower
+ * position; a NaN counts as the most).  Kept rows stay in order and become rows 0 .. budget - 1 of
+ * `to`; their weights become weights_out[b][g][0 .. budget - 1], and seq_lens_out[b] =
+ * min(seq_lens[b], budget).  A request with no more than budget positions keeps them all.  (Heads keep
+ * different positions, so the rows of one position are not those of one token afterwards.)
+ *   cache, to  `to` may be the same cache (in place: rows behind the last kept one are left
+ *              as they were), hold other pages of the same pool, or be a cache of its own. Both
+ *              with shape's num_kv_heads; `to` holds at least min(budget, max_seq_len)
+ *              positions per request.  Requests must not share pages that are written.
+ *   budget     >= 1, sinks + recent <= budget, sinks, recent >= 0.
+ *   weights    device fp32 [batch][num_kv_heads][max_seq_len] (td_weights_attn).
+ *   weights_out  device fp32 [batch][num_kv_heads][weights_out_row], weights_out_row >=
+ *              min(budget, max_seq_len); may be weights (then weights_out_row = max_seq_len).
+ *   seq_lens_out  device int32 [batch], not seq_lens.
+ *   kept       device int32 [batch][num_kv_heads][budget]: the kept positions, ascending, -1 padded.
+ *   batch * num_kv_heads <= 2^24.
+ * A row on a page that is none (of either cache) is not moved (TD_FLAG_PAGE_OUT_OF_RANGE).
+ */
+td_status td_evict(const td_shape *shape, const td_cache *cache, const td_cache *to, int32_t budget,
+                   int32_t sinks, int32_t recent, const float *weights, float *weights_out,
+                   int32_t weights_out_row, const int32_t *seq_lens, int32_t *seq_lens_out,
+                   int32_t *kept, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Measurement aid (not part of the decode step): reads exactly the K/V rows
  * one full layer (idx == NULL) or one sparse layer (idx = its index set)
  * reads, with the same split plan, launch shape and 16-byte row loads as the
@@ -626,9 +765,9 @@ td_status td_probe_layer_reads(const td_shape *shape, const void *k_cache, const
  *          streamed); 0 one contiguous chunk each; negative restores the
  *          default
  *   "wait_limit_us": microseconds after which a staged full-layer CTA stops
- *          waiting for a bulk copy, or a tree-attention CTA that has finished no
- *          tile of 128 tokens meanwhile for its copies and products (default 1 s;
- *          a tree-attention CTA that gives up waits, with
+ *          waiting for a bulk copy, or a tree-attention CTA (or one of td_window_attn or td_q4_attn
+ *          with cu_new) that has finished no tile of 128 tokens meanwhile for its copies and products (default 1 s;
+ *          such a CTA that gives up waits, with
  *          limits, for what it has in flight, sets TD_FLAG_WAIT_TIMEOUT and leaves:
  *          its rows are not valid, the next launch is not affected).  A CTA that gives up waits
  *          (at the default limit) for every copy it issued, then joins the
@@ -638,7 +777,7 @@ td_status td_probe_layer_reads(const td_shape *shape, const void *k_cache, const
  *   "wait_test": 1 makes the first stage wait of every staged full-layer CTA
  *          poll a barrier that nothing arrives on, so it runs out after
  *          "wait_limit_us" (tests of the failure report; no fault, no hang); the
- *          tree attention's softmax likewise;
+ *          tree attention's softmax likewise, and that of new tokens with cu_new;
  *          0 (default) in normal use
  * Otherwise value <= 0 restores the default.  Unknown key -> TD_ERR_INVALID_ARG.
  */

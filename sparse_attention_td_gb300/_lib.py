@@ -48,6 +48,12 @@ class _Cache(ctypes.Structure):
                 ("max_blocks", ctypes.c_int32)]
 
 
+class _Q4Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int32)]
+
+
 def default_scale(head_dim: int) -> float:
     """The library's scale when Shape.scale == 0: 1/sqrtf(head_dim) in fp32."""
     import numpy as np
@@ -117,6 +123,20 @@ def lib():
     L.td_kv_append_slots.argtypes = [shp, cch, i32, vp, vp, i64, vp, vp]
     L.td_block_tables.restype = ctypes.c_int
     L.td_block_tables.argtypes = [i32, i32, i32, i32] + [vp] * 10 + [i32, vp, sz, vp]
+    q4 = ctypes.POINTER(_Q4Cache)
+    L.td_cache_workspace_size.restype = sz
+    L.td_cache_workspace_size.argtypes = [shp]
+    for call, cache in ((L.td_window_attn, cch), (L.td_q4_attn, q4)):
+        call.restype = ctypes.c_int
+        call.argtypes = [shp, cache, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.td_q4_sparse_attn.restype = ctypes.c_int
+    L.td_q4_sparse_attn.argtypes = [shp, q4, vp, vp, vp, i32, vp, vp, sz, vp]
+    L.td_q4_append.restype = ctypes.c_int
+    L.td_q4_append.argtypes = [shp, q4, i32, vp, vp, i64, vp, vp]
+    L.td_weights_attn.restype = ctypes.c_int
+    L.td_weights_attn.argtypes = [shp, cch, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.td_evict.restype = ctypes.c_int
+    L.td_evict.argtypes = [shp, cch, cch, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, sz, vp]
     L.td_sparse_attn.restype = ctypes.c_int
     L.td_sparse_attn.argtypes = [shp, vp, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
     L.td_sparse_attn_noalloc.restype = ctypes.c_int
@@ -202,17 +222,27 @@ def td_tree_workspace_size(shape: Shape, tree_size: int) -> int:
     return int(lib().td_tree_workspace_size(ctypes.byref(shape), int(tree_size)))
 
 
+def td_cache_workspace_size(shape: Shape) -> int:
+    return int(lib().td_cache_workspace_size(ctypes.byref(shape)))
+
+
 class Workspace:
     """A zero-initialised device workspace of td_workspace_size bytes; with
     tree_size also td_tree_workspace_size bytes, for the tree calls.  Those write
     the buffer's last bytes, which the other calls must find as they left them: the
     tree calls take only a workspace with a tree part of their size, the others see
-    the buffer without it."""
+    the buffer without it.  cache_calls adds td_cache_workspace_size bytes, between
+    the two, for the calls on small caches (td_window_attn and those behind it), which
+    likewise take only a workspace with a part large enough and write no other."""
 
-    def __init__(self, shape: Shape, top_k: int, device=None, stream=None, tree_size: int = 0):
+    def __init__(self, shape: Shape, top_k: int, device=None, stream=None, tree_size: int = 0,
+                 cache_calls: bool = False):
         n = td_workspace_size(shape, top_k)
         if n == 0:
             raise TdError(1, "td_workspace_size")
+        self.cache_bytes = (td_cache_workspace_size(shape) + 255) // 256 * 256 if cache_calls else 0
+        self._cache_shapes = set()   # (batch, query heads, KV heads) known to fit
+        n = (n + 255) // 256 * 256 + self.cache_bytes if cache_calls else n
         self.tree_bytes = 0
         if tree_size:
             self.tree_bytes = td_tree_workspace_size(shape, tree_size)
@@ -228,8 +258,19 @@ class Workspace:
 
     @property
     def nbytes(self) -> int:
-        """Bytes without the tree part."""
-        return self.tensor.numel() - self.tree_bytes
+        """Bytes without the parts of the tree calls and of the calls on small caches."""
+        return self.tensor.numel() - self.tree_bytes - self.cache_bytes
+
+    def check_cache(self, shape: Shape):
+        key = (shape.batch, shape.num_q_heads, shape.num_kv_heads)
+        if key in self._cache_shapes:
+            return
+        need = td_cache_workspace_size(shape)
+        if need > self.cache_bytes:
+            raise ValueError(f"ws has {self.cache_bytes} bytes for calls on small caches, needs {need} "
+                             f"(Workspace(..., cache_calls=True))")
+        if need:                     # (0: the call refuses the shape)
+            self._cache_shapes.add(key)
 
     def check_tree(self, shape: Shape, tree_size: int):
         key = (shape.num_q_heads, shape.num_kv_heads, tree_size)
@@ -418,7 +459,7 @@ def make_cache(k, v, block_table=None) -> Cache:
     return Cache(k, v, block_table)
 
 
-_BF16, _I32 = torch.bfloat16, torch.int32
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
 def td_tree_attn(shape: Shape, cache: Cache, tree_size, tree_lens, tree_mask, q, seq_lens, out,
@@ -525,6 +566,157 @@ def td_block_tables(seq_lens, new_lens, page_size, block_table, num_blocks, num_
         _on(dev, slot_map, "slot_map", _I32, 0), slots, wp, wn, st)
     if rc:
         _check(rc, "td_block_tables")
+
+
+def _cache_ws(dev, ws, shape):
+    """The buffer up to the end of the part for calls on small caches."""
+    p, n = _ws(dev, ws)
+    ws.check_cache(shape)
+    return p, n - ws.tree_bytes
+
+
+class Q4Cache:
+    """One layer's K/V rows in 4 bits (td_q4_cache): k, v uint8 [pages][Hkv][page_size][64],
+    scales uint8 [pages][Hkv][page_size][16] (K's 8 e4m3 scales of a token, then V's) and a
+    block table [B][max_blocks], or without a table a contiguous cache."""
+
+    def __init__(self, k, v, scales, block_table=None):
+        for name, t, width in (("k", k, 64), ("v", v, 64), ("scales", scales, 16)):
+            if t.dim() != 4 or t.shape[3] != width:
+                raise ValueError(f"{name} must be [pages][kv heads][page size][{width}], got {tuple(t.shape)}")
+            if t.shape[:3] != k.shape[:3]:
+                raise ValueError(f"k and {name} differ: {tuple(k.shape)} and {tuple(t.shape)}")
+        if block_table is not None and block_table.dim() != 2:
+            raise ValueError("block_table must be [batch][max_blocks]")
+        self.k, self.v, self.scales, self.block_table = k, v, scales, block_table
+        self.num_pages, self.kv_heads, self.page_size = (int(x) for x in k.shape[:3])
+        self.c = _Q4Cache(_dev(k, "k", torch.uint8), _dev(v, "v", torch.uint8),
+                          _dev(scales, "scales", torch.uint8), self.num_pages, self.page_size,
+                          _dev(block_table, "block_table", torch.int32, optional=True),
+                          0 if block_table is None else int(block_table.shape[1]))
+        self.device = k.get_device()
+        for name, t in (("v", v), ("scales", scales), ("block_table", block_table)):
+            if t is not None and t.get_device() != self.device:
+                raise ValueError(f"k is on {k.device}, {name} on {t.device}")
+        self.ref = ctypes.byref(self.c)
+        self.fits = (self.device, self.kv_heads, None if block_table is None else int(block_table.shape[0]))
+
+    check = Cache.check
+
+
+def make_q4_cache(k, v, scales, block_table=None) -> Q4Cache:
+    return Q4Cache(k, v, scales, block_table)
+
+
+def _kind(cache, cls, call):
+    if not isinstance(cache, cls):
+        raise ValueError(f"{call} takes a {cls.__name__}, got {type(cache).__name__}")
+
+
+def _new_tokens(name, kind, shape, cache, window, sinks, cu_new, q, seq_lens, out, ws, stream):
+    dev, st = _launch(stream)
+    _kind(cache, kind, name)
+    wp, wn = _cache_ws(dev, ws, shape)
+    if q.dim() != 3 or q.shape[1] != shape.num_q_heads or q.shape[2] != 128:
+        raise ValueError(f"q must be [tokens][{shape.num_q_heads}][128], got {tuple(q.shape)}")
+    nb, tokens = shape.batch, int(q.shape[0])
+    n = tokens * shape.num_q_heads * 128
+    rc = getattr(lib(), name)(
+        shape, cache.check(shape, dev), int(window), int(sinks), tokens,
+        None if cu_new is None else _on(dev, cu_new, "cu_new", _I32, nb + 1),
+        _on(dev, q, "q", _BF16, n), _on(dev, seq_lens, "seq_lens", _I32, nb),
+        _on(dev, out, "out", _BF16, n), wp, wn, st)
+    if rc:
+        _check(rc, name)
+
+
+def td_window_attn(shape: Shape, cache: Cache, window, sinks, cu_new, q, seq_lens, out,
+                   ws: Workspace = None, stream=None):
+    """Attention of the new tokens q [tokens][Hq][128] over the cache with a sliding window
+    (0: none) and the first `sinks` tokens; request b's rows are cu_new[b] .. cu_new[b + 1] - 1
+    (None: one new token per request)."""
+    _new_tokens("td_window_attn", Cache, shape, cache, window, sinks, cu_new, q, seq_lens, out, ws, stream)
+
+
+def td_q4_attn(shape: Shape, cache: Q4Cache, window, sinks, cu_new, q, seq_lens, out,
+               ws: Workspace = None, stream=None):
+    """td_window_attn over a 4-bit cache."""
+    _new_tokens("td_q4_attn", Q4Cache, shape, cache, window, sinks, cu_new, q, seq_lens, out, ws, stream)
+
+
+def td_q4_sparse_attn(shape: Shape, cache: Q4Cache, q, seq_lens, idx, top_k, out,
+                      ws: Workspace = None, stream=None):
+    """One PPSA layer over a 4-bit cache: the persisted set idx [B][Hkv][top_k]."""
+    dev, st = _launch(stream)
+    _kind(cache, Q4Cache, "td_q4_sparse_attn")
+    wp, wn = _cache_ws(dev, ws, shape)
+    nb, k = shape.batch, int(top_k)
+    n = nb * shape.num_q_heads * 128
+    rc = lib().td_q4_sparse_attn(
+        shape, cache.check(shape, dev), _on(dev, q, "q", _BF16, n),
+        _on(dev, seq_lens, "seq_lens", _I32, nb),
+        _on(dev, idx, "idx", _I32, nb * shape.num_kv_heads * k), k, _on(dev, out, "out", _BF16, n),
+        wp, wn, st)
+    if rc:
+        _check(rc, "td_q4_sparse_attn")
+
+
+def td_q4_append(shape: Shape, cache: Q4Cache, k_new, v_new, slot_map, stream=None):
+    """New K/V rows [tokens][Hkv][128] into the 4-bit cache at slot_map [tokens]."""
+    dev, st = _launch(stream)
+    _kind(cache, Q4Cache, "td_q4_append")
+    heads = shape.num_kv_heads
+    ref = cache.ref
+    if cache.device != dev or cache.kv_heads != heads:
+        cache.check(shape, dev)
+    pk, n, sk = _token_rows(dev, k_new, "k_new", heads)
+    pv, nv, sv = _token_rows(dev, v_new, "v_new", heads)
+    if n != nv or sk != sv:
+        raise ValueError("k_new and v_new must have the same tokens and token stride")
+    rc = lib().td_q4_append(shape, ref, n, pk, pv, sk, _on(dev, slot_map, "slot_map", _I32, n), st)
+    if rc:
+        _check(rc, "td_q4_append")
+
+
+def td_weights_attn(shape: Shape, cache: Cache, fresh, q, seq_lens, weights, logits, out,
+                    ws: Workspace = None, stream=None):
+    """Full attention of one token per request that adds its probabilities, summed over each KV
+    head's query heads, to weights [B][Hkv][max_seq_len] (the last `fresh` positions are set)."""
+    dev, st = _launch(stream)
+    _kind(cache, Cache, "td_weights_attn")
+    wp, wn = _cache_ws(dev, ws, shape)
+    nb, nq, N = shape.batch, shape.num_q_heads, shape.max_seq_len
+    rc = lib().td_weights_attn(
+        shape, cache.check(shape, dev), int(fresh), _on(dev, q, "q", _BF16, nb * nq * 128),
+        _on(dev, seq_lens, "seq_lens", _I32, nb),
+        _on(dev, weights, "weights", _F32, nb * shape.num_kv_heads * N),
+        _on(dev, logits, "logits", _F32, nb * nq * N), _on(dev, out, "out", _BF16, nb * nq * 128),
+        wp, wn, st)
+    if rc:
+        _check(rc, "td_weights_attn")
+
+
+def td_evict(shape: Shape, cache: Cache, to: Cache, budget, sinks, recent, weights, weights_out,
+             seq_lens, seq_lens_out, kept, ws: Workspace = None, stream=None):
+    """Each KV head of a request with more than budget positions keeps its first `sinks`, its last
+    `recent` and the heaviest others, as rows 0 .. budget - 1 of `to` (which may be cache);
+    weights_out [B][Hkv][row], kept int32 [B][Hkv][budget]."""
+    dev, st = _launch(stream)
+    _kind(cache, Cache, "td_evict")
+    _kind(to, Cache, "td_evict")
+    wp, wn = _ws(dev, ws)
+    nb, units, budget = shape.batch, shape.batch * shape.num_kv_heads, int(budget)
+    if weights_out.dim() != 3:
+        raise ValueError("weights_out must be [batch][kv heads][positions]")
+    row = int(weights_out.shape[2])
+    rc = lib().td_evict(
+        shape, cache.check(shape, dev), to.check(shape, dev), budget, int(sinks), int(recent),
+        _on(dev, weights, "weights", _F32, units * shape.max_seq_len),
+        _on(dev, weights_out, "weights_out", _F32, units * row), row,
+        _on(dev, seq_lens, "seq_lens", _I32, nb), _on(dev, seq_lens_out, "seq_lens_out", _I32, nb),
+        _on(dev, kept, "kept", _I32, units * max(budget, 0)), wp, wn, st)
+    if rc:
+        _check(rc, "td_evict")
 
 
 class _StepArgs:

@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtd.so")
 SOURCES = ["td_api.cu", "td_attn.cu", "td_attn_mma.cu", "td_topk.cu", "td_noalloc.cu", "td_diag.cu",
-           "td_tree.cu", "td_pages.cu", "td_spec_api.cu"]
+           "td_tree.cu", "td_pages.cu", "td_spec_api.cu", "td_cache_attn.cu", "td_cache_rows.cu",
+           "td_prompt.cu", "td_cache_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,7 +47,8 @@ def _stale(out: str, deps: list) -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    headers = [os.path.join(CSRC, h) for h in ("td_internal.h", "td_spec.h", "td_attn_common.cuh")]
+    headers = [os.path.join(CSRC, h) for h in ("td_internal.h", "td_spec.h", "td_cache.h", "td_attn_common.cuh",
+                                                "td_tc.cuh")]
     headers.append(os.path.join(ROOT, "include", "td.h"))
     objs, jobs = [], []
     for src in SOURCES:

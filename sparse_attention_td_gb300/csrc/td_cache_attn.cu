@@ -1,0 +1,769 @@
+// td_cache_attn.cu -- attention of one new token per request over a small cache:
+// a window with sinks, rows of 16 or of 4 bits, a persisted index set; and the sums
+// of its probabilities per cached position.
+//
+// Request b, KV head g, its G query heads h, positions S (a window with the first
+// tokens, everything, or an index set):
+//     x_j = scale q_h . K_j,   out_h = sum_{j in S} softmax(x)_j V_j   (0 for empty S)
+// in one pass with a running maximum m, denominator l and output o per head.
+//
+// A 4-bit value is code * scale, a code of 0 .5 1 1.5 2 3 4 6 with a sign (e2m1) and an e4m3
+// scale for 16 of them: 2 + 4 significant bits between 2^-10 and 2688, so fp16 holds
+// it exactly and the products below see the cached values themselves.
+//
+// Both products run on mma.sync m16n8k16: a KV head has at most 8 query heads here, an
+// eighth of a tcgen05 tile's rows, and the operands come out of registers, where
+// 4-bit rows have to be decoded anyway (a tcgen05 operand would go through shared or
+// tensor memory first).  S: 16 tokens x 8 heads, dims summed; O: dims x 8 heads,
+// tokens summed.  The order in which a sum takes its terms is free, so a lane's dims are
+// those that its loads bring: 16 bytes of a K row, of V rows 16 (8 of a 4-bit row, the
+// dims of one scale).  P turns from S's layout to the second product's by a transposing
+// move of 8 x 8 blocks.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "td_attn_common.cuh"
+#include "td_cache.h"
+
+namespace td {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kHeads = 8;             // columns of the products; heads behind G are zero
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
+{
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1)
+{
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 block of 16-bit values held as mma fragments.
+__device__ __forceinline__ uint32_t turned(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Loads of rows, which are read once: no L1 allocation.  Zeros where `there` is false.
+__device__ __forceinline__ uint4 load16(const void *p, bool there = true)
+{
+    uint4 r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                 "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+                 "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p), "r"((uint32_t)there));
+    return r;
+}
+
+__device__ __forceinline__ uint2 load8(const void *p)
+{
+    uint2 r;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+
+// Four codes' worth of halves: two bytes of codes (those of byte `at` and at + 1 of x) as
+// two pairs of fp16 values, the low half of a byte first.
+__device__ __forceinline__ void decode2(uint32_t x, int at, uint32_t &lo, uint32_t &hi)
+{
+    if (at == 0)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %2;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(x));
+    else
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %2;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, c;\n\tcvt.rn.f16x2.e2m1x2 %1, d;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(x));
+}
+
+// Two e4m3 scales (low 16 bits of x) as fp16, each twice.
+__device__ __forceinline__ void scales2(uint32_t x, uint32_t &s0, uint32_t &s1)
+{
+    uint32_t s;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s) : "r"(x));
+    s0 = prmt(s, s, 0x1010);
+    s1 = prmt(s, s, 0x3232);
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_b16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// Rows of 16 tokens of a warp: lane (r, c) = (lane / 4, lane % 4) holds of K the tokens r and
+// r + 8, of V the tokens 2c, 2c + 1, 2c + 8 and 2c + 9.
+template <bool Q4> struct Tokens;
+
+// 16 bits.  K: dims 8 (c + 4 i) .. + 7 in word group i; V: dims 8 r .. + 7 and 64 + 8 r .. + 7.
+template <> struct Tokens<false> {
+    uint4 k[2][4], v[4][2];
+
+    __device__ void load_k(const RowsArgs &a, int r, int c, const int (&row)[2])
+    {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t *p = a.k + (size_t)(uint32_t)max(row[t], 0) * (kHeadDim * 2) + 16 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                k[t][i] = load16(p + 64 * i);
+        }
+    }
+    __device__ void load_v(const RowsArgs &a, int r, int c, const int (&row)[4])
+    {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint8_t *p = a.v + (size_t)(uint32_t)max(row[t], 0) * (kHeadDim * 2) + 16 * r;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                v[t][i] = load16(p + 128 * i, row[t] >= 0);    // P of such a token is zero; V has to be finite
+        }
+    }
+    __device__ void s(float (&d)[4], const uint32_t (&q)[16]) const
+    {
+        float odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mma<false>(d, k[0][i].x, k[1][i].x, k[0][i].y, k[1][i].y, q[4 * i], q[4 * i + 1]);
+            mma<false>(odd, k[0][i].z, k[1][i].z, k[0][i].w, k[1][i].w, q[4 * i + 2], q[4 * i + 3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            d[e] += odd[e];
+    }
+    __device__ static uint32_t word(const uint4 (&x)[2], int i)
+    {
+        const uint4 &y = x[i >> 2];
+        return (i & 3) == 0 ? y.x : (i & 3) == 1 ? y.y : (i & 3) == 2 ? y.z : y.w;
+    }
+    // P as two bf16 terms, 16 bits together, so that the result has the accuracy of fp32
+    // sums behind its one rounding.  (p[t]: of token r + 8 t, heads 2c and 2c + 1.)
+    __device__ void pv(float (&o)[8][4], const float (&p)[2][2]) const
+    {
+        uint32_t b[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t hi = pack_b16(p[t][0], p[t][1]);
+            b[0][t] = turned(hi);
+            b[1][t] = turned(pack_b16(p[t][0] - bf_lo(hi), p[t][1] - bf_hi(hi)));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w0 = word(v[0], i), w1 = word(v[1], i), w2 = word(v[2], i), w3 = word(v[3], i);
+            const uint32_t a0 = prmt(w0, w1, 0x5410), a1 = prmt(w0, w1, 0x7632);
+            const uint32_t a2 = prmt(w2, w3, 0x5410), a3 = prmt(w2, w3, 0x7632);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                mma<false>(o[i], a0, a1, a2, a3, b[k][0], b[k][1]);
+        }
+    }
+    __device__ static int dim(int i, int r) { return (i < 4 ? 8 * r : 64 + 8 * r) + 2 * (i & 3); }
+    __device__ static int qdim(int c, int w) { return 8 * (c + 4 * (w >> 2)) + 2 * (w & 3); }   // of q word w
+};
+
+// 4 bits.  K: dims 32 c .. + 31, two scales; V: dims 16 r .. + 15, one scale.
+template <> struct Tokens<true> {
+    uint4 k[2];
+    uint2 v[4];
+    uint32_t ks[2], vs[4];
+
+    __device__ void load_k(const RowsArgs &a, int r, int c, const int (&row)[2])
+    {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const size_t at = (uint32_t)max(row[t], 0);
+            k[t] = load16(a.k + at * kCodeBytes + 16 * c);
+            ks[t] = *reinterpret_cast<const uint16_t *>(a.scales + at * kScaleBytes + 2 * c);
+        }
+    }
+    __device__ void load_v(const RowsArgs &a, int r, int c, const int (&row)[4])
+    {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const size_t at = (uint32_t)max(row[t], 0);
+            v[t] = load8(a.v + at * kCodeBytes + 8 * r);
+            vs[t] = a.scales[at * kScaleBytes + 8 + r];
+            if (row[t] < 0)
+                vs[t] = 0;         // P of such a token is zero; V has to be finite
+        }
+    }
+    __device__ void s(float (&d)[4], const uint32_t (&q)[16]) const
+    {
+        uint32_t sc[2][2];
+        scales2(ks[0], sc[0][0], sc[0][1]);
+        scales2(ks[1], sc[1][0], sc[1][1]);
+        float odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t x[2][2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t w = (j >> 1) == 0 ? k[t].x : (j >> 1) == 1 ? k[t].y : (j >> 1) == 2 ? k[t].z : k[t].w;
+                decode2(w, 2 * (j & 1), x[t][0], x[t][1]);
+                x[t][0] = mul2(x[t][0], sc[t][j >> 2]);
+                x[t][1] = mul2(x[t][1], sc[t][j >> 2]);
+            }
+            mma<true>((j & 1) ? odd : d, x[0][0], x[1][0], x[0][1], x[1][1], q[2 * j], q[2 * j + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            d[e] += odd[e];
+    }
+    // P in fp16: half a step is 2^-12 of a probability, an eighth of the output's own
+    // rounding (below 2^-14 of the largest, an absolute 2^-25).
+    __device__ void pv(float (&o)[8][4], const float (&p)[2][2]) const
+    {
+        uint32_t sc[4];
+        scales2(vs[0] | vs[1] << 8, sc[0], sc[1]);
+        scales2(vs[2] | vs[3] << 8, sc[2], sc[3]);
+        const uint32_t b0 = turned(pack_f16(p[0][0], p[0][1])), b1 = turned(pack_f16(p[1][0], p[1][1]));
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            uint32_t x[4][2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                decode2(i < 4 ? v[t].x : v[t].y, i & 2, x[t][0], x[t][1]);
+                x[t][0] = mul2(x[t][0], sc[t]);
+                x[t][1] = mul2(x[t][1], sc[t]);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                mma<true>(o[i + u], prmt(x[0][u], x[1][u], 0x5410), prmt(x[0][u], x[1][u], 0x7632),
+                          prmt(x[2][u], x[3][u], 0x5410), prmt(x[2][u], x[3][u], 0x7632), b0, b1);
+        }
+    }
+    __device__ static int dim(int i, int r) { return 16 * r + 2 * i; }
+    __device__ static int qdim(int c, int w) { return 32 * c + 2 * w; }
+};
+
+// What a CTA does: an equal, contiguous range of the batch's groups of tokens, unit
+// (request, KV head) after unit, so that the longest request decides nothing.  A unit that
+// several CTAs share is joined by the last of them to come.  A unit without tokens
+// has one group, of which no token exists: its result is zero.
+struct Seen {
+    int n, count, groups;
+    Range w;
+};
+
+template <int MODE, int GT> __device__ __forceinline__ Seen seen_of(const CacheAttnArgs &a, int b, uint32_t &bad)
+{
+    Seen s;
+    s.n = seq_len_of(a.seq_lens, b, a.Nmax, bad);
+    s.w = window_range(s.n, a.window, a.sinks);
+    s.count = MODE == 1 ? a.top_k : s.n - s.w.low + s.w.first;
+    s.groups = max(1, (s.count + GT - 1) / GT);
+    return s;
+}
+
+// MODE 0: a window or everything; 1: an index set; 2: everything, the logits are kept.
+// U: 16-token blocks that a warp takes at a time.
+template <bool Q4, int MODE, int U, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const __grid_constant__ CacheAttnArgs a)
+{
+    constexpr int GT = 16 * U;
+    using Block = Tokens<Q4>;
+    __shared__ int sm_sums[kWarps];
+    __shared__ int sm_start[3];                   // b, KV head, group that the CTA's range starts at
+    __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
+    __shared__ __align__(16) float sm_o[kWarps][kHeads][kHeadDim];
+    __shared__ int sm_last;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r = lane >> 2, c = lane & 3;
+    pdl_wait();
+
+    // ---- the CTA's range: requests in equal runs per thread, prefix sums
+    uint32_t bad = 0;
+    int total = 0, per;
+    {
+        const int run = (a.B + kThreads - 1) / kThreads;
+        const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
+        int mine = 0;
+        for (int b = b0; b < b1; ++b)
+            mine += seen_of<MODE, GT>(a, b, bad).groups * a.Hkv;
+        if (bad && blockIdx.x == 0)
+            atomicOr(a.status, bad);
+        bad = 0;
+        int inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(kFull, inc, d);
+            if (lane >= d)
+                inc += y;
+        }
+        if (lane == 31)
+            sm_sums[warp] = inc;
+        __syncthreads();
+        int at = inc - mine;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp)
+                at += sm_sums[i];
+            total += sm_sums[i];
+        }
+        // (at least a group for each warp)
+        per = max(kWarps, (int)((uint32_t)(total + gridDim.x - 1) / gridDim.x));
+        const int64_t start = (int64_t)blockIdx.x * per;
+        if (start < total && at <= start && start < at + mine) {
+            for (int b = b0; b < b1; ++b) {
+                const int g = seen_of<MODE, GT>(a, b, bad).groups;
+                if (start < at + (int64_t)g * a.Hkv) {
+                    sm_start[0] = b;
+                    sm_start[1] = (int)(start - at) / g;
+                    sm_start[2] = (int)(start - at) % g;
+                    break;
+                }
+                at += g * a.Hkv;
+            }
+        }
+        __syncthreads();
+        if (start >= total)
+            return;
+    }
+    const int begin = blockIdx.x * per;
+    int left = min(per, total - begin);
+    int b = sm_start[0], h = sm_start[1], grp = sm_start[2];
+    Seen seen = seen_of<MODE, GT>(a, b, bad);
+    pdl_launch_dependents();
+    uint32_t flags = 0;
+
+    for (bool first_seg = true; left > 0; first_seg = false) {
+        const int count = min(left, seen.groups - grp);
+        const int32_t *set = MODE == 1 ? a.idx + ((size_t)b * a.Hkv + h) * a.top_k : nullptr;
+
+        // Where a token of group i lies, in three steps that are taken for later groups
+        // while earlier ones are computed: its position, its page, its row.  A lane
+        // has token lane % GT of the group.
+        auto position = [&](int i) {
+            const int t = (grp + i) * GT + (lane & (GT - 1));
+            if (i >= count || t >= seen.count)
+                return -1;
+            if (MODE == 1)
+                return set[t];
+            return t < seen.w.first ? t : seen.w.low + t - seen.w.first;
+        };
+        auto checked = [&](int p) {
+            if (MODE == 1 && (p < -1 || p >= seen.n)) {
+                flags |= kFlagIndexOutOfRange;
+                return -1;
+            }
+            return p;
+        };
+        auto page = [&](int p) { return p >= 0 ? page_of(a.rows, b, p) : 0; };
+        auto find = [&](int p, int pg) {
+            if (p < 0)
+                return -1;
+            const int row = row_of(a.rows, a.Hkv, h, p, pg);
+            if (row < 0)
+                flags |= kFlagPageOutOfRange;
+            return row;
+        };
+        Block blk[U];
+        auto load_k = [&](int row) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int rows[2] = {__shfl_sync(kFull, row, 16 * u + r), __shfl_sync(kFull, row, 16 * u + 8 + r)};
+                blk[u].load_k(a.rows, r, c, rows);
+            }
+        };
+        auto load_v = [&](int row) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = 16 * u + 2 * c;
+                const int rows[4] = {__shfl_sync(kFull, row, at), __shfl_sync(kFull, row, at + 1),
+                                     __shfl_sync(kFull, row, at + 8), __shfl_sync(kFull, row, at + 9)};
+                blk[u].load_v(a.rows, r, c, rows);
+            }
+        };
+
+        int i = warp;
+        int p0 = checked(position(i)), p1 = checked(position(i + kWarps)), p2 = position(i + 2 * kWarps);
+        int pg0 = page(p0), pg1 = page(p1);
+        int row = find(p0, pg0);
+        if (i < count) {
+            load_k(row);
+            load_v(row);
+        }
+
+        // q of head r; a 4-bit cache's products are of fp16 values: the head's q, times a power
+        // of two that brings its largest value to 2^8 (values 2^-22 times as large keep all bits)
+        uint32_t q[16];
+        float x2[2];             // logits to exponents of 2, heads 2c and 2c + 1
+        {
+            const uint16_t *src = a.q + ((size_t)b * a.Hq + (size_t)h * a.G + r) * kHeadDim;
+#pragma unroll
+            for (int w = 0; w < 16; w += 2) {
+                const uint2 y = r < a.G ? *reinterpret_cast<const uint2 *>(src + Block::qdim(c, w)) : make_uint2(0, 0);
+                q[w] = y.x;
+                q[w + 1] = y.y;
+            }
+            x2[0] = x2[1] = a.scale * kLog2e;
+            if constexpr (Q4) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int w = 0; w < 16; ++w)
+                    top = __vmaxu2(top, q[w] & 0x7fff7fffu);
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(kFull, top, 1));
+                top = max(top, __shfl_xor_sync(kFull, top, 2));
+                const int e = top >> 7;                            // exponent bits of the largest
+                const int up = e == 0 || e == 255 ? 0 : max(-120, min(120, 135 - e));
+                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                const float inv = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+                for (int w = 0; w < 16; ++w)
+                    q[w] = pack_f16(bf_lo(q[w]) * f, bf_hi(q[w]) * f);
+                x2[0] *= __shfl_sync(kFull, inv, 8 * c);
+                x2[1] *= __shfl_sync(kFull, inv, 8 * c + 4);
+            }
+        }
+
+        float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.0f, 0.0f};    // l: this lane's tokens
+        float o[8][4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[k][e] = 0.0f;
+
+        for (; i < count; i += kWarps) {
+            const uint32_t there = __ballot_sync(kFull, row >= 0);
+            p2 = checked(p2);
+            const int pg2 = page(p2), p3 = position(i + 3 * kWarps);
+            const int next = find(p1, pg1);
+            float s[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[u][e] = 0.0f;
+                blk[u].s(s[u], q);
+            }
+            if (i + kWarps < count)
+                load_k(next);
+            // s[u][2 t + e]: token 16 u + 8 t + r, head 2c + e
+            float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const bool ok = there >> (16 * u + 8 * t + r) & 1u;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &x = s[u][2 * t + e];
+                        if constexpr (MODE == 2) {
+                            const float z = x * a.scale;
+                            const int at = (grp + i) * GT + 16 * u + 8 * t + r;
+                            if (2 * c + e < a.G && at < seen.count)
+                                a.logits[((size_t)b * a.Hq + (size_t)h * a.G + 2 * c + e) * a.Nmax + at] =
+                                    ok ? z : -CUDART_INF_F;
+                            x = z * kLog2e;
+                        } else {
+                            x *= x2[e];
+                        }
+                        x = ok ? x : -CUDART_INF_F;
+                        top[e] = fmaxf(top[e], x);
+                    }
+                }
+            float ref[2];
+            bool grows = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], 4));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], 8));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], 16));
+                grows |= top[e] > m[e];
+            }
+            if (__any_sync(kFull, grows)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mn = fmaxf(m[e], top[e]);
+                    const float f = safe_exp2_diff(m[e], mn);
+                    m[e] = mn;
+                    l[e] *= f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        o[k][e] *= f;
+                        o[k][e + 2] *= f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                ref[e] = m[e] == -CUDART_INF_F ? 0.0f : m[e];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float p[2][2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        p[t][e] = exp2f(s[u][2 * t + e] - ref[e]);
+                        l[e] += p[t][e];
+                    }
+                blk[u].pv(o, p);
+            }
+            if (i + kWarps < count)
+                load_v(next);
+            row = next;
+            p1 = p2;
+            pg1 = pg2;
+            p2 = p3;
+        }
+
+        // ---- the segment's result: the warps' sums joined in shared memory
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(kFull, l[e], 4);
+            l[e] += __shfl_xor_sync(kFull, l[e], 8);
+            l[e] += __shfl_xor_sync(kFull, l[e], 16);
+            const int hd = 2 * c + e;
+            if (hd < a.G) {
+                if (r == 0) {
+                    sm_m[warp][hd] = m[e];
+                    sm_l[warp][hd] = l[e];
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<float2 *>(&sm_o[warp][hd][Block::dim(k, r)]) = make_float2(o[k][e], o[k][e + 2]);
+            }
+        }
+        __syncthreads();
+        // This unit's groups in the whole batch's order, and the CTAs that share them.
+        const int u0 = begin + (min(per, total - begin) - left) - grp, u1 = u0 + seen.groups;
+        const int c0 = u0 / per, c1 = (u1 - 1) / per;
+        const bool whole = c0 == c1;
+        const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
+        const size_t row0 = (size_t)b * a.Hq + (size_t)h * a.G;
+        static_assert(kThreads == kHeadDim, "a thread per dim");
+        auto weight = [](float ms, float M) { return ms == -CUDART_INF_F ? 1.0f : exp2f(ms - M); };
+        for (int hd = 0; hd < a.G; ++hd) {
+            float M = -CUDART_INF_F, L = 0.0f, O = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                M = fmaxf(M, sm_m[w][hd]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = weight(sm_m[w][hd], M);     // (without a maximum: zeros, or NaN)
+                L += sm_l[w][hd] * f;
+                O += sm_o[w][hd][tid] * f;
+            }
+            if (whole) {
+                a.out[(row0 + hd) * kHeadDim + tid] = f32_to_bf16_rn(L == 0.0f ? 0.0f : O / L);
+                if (MODE == 2 && tid == 0) {
+                    a.stat_m[row0 + hd] = M;
+                    a.stat_l[row0 + hd] = L;
+                }
+            } else {
+                a.ws->part_o[slot][hd][tid] = O;
+                if (tid == 0) {
+                    a.ws->part_m[slot][hd] = M;
+                    a.ws->part_l[slot][hd] = L;
+                }
+            }
+        }
+        __syncthreads();
+        if (!whole) {
+            // The barrier orders the CTA's stores before the ticket's release; in the last
+            // CTA to come the acquire and the next barrier order the loads behind the others'.
+            if (tid == 0) {
+                unsigned ticket;
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                             : "=r"(ticket)
+                             : "l"(a.ws->tickets + c0)
+                             : "memory");
+                sm_last = ticket == (unsigned)(c1 - c0);
+            }
+            __syncthreads();
+            if (sm_last) {
+                if (tid == 0)
+                    a.ws->tickets[c0] = 0;
+                // CTA c0's part is its second one where the unit starts inside its range.
+                const int late = (int64_t)c0 * per < u0 ? 1 : 0;
+                for (int hd = 0; hd < a.G; ++hd) {
+                    float M = -CUDART_INF_F, L = 0.0f, O = 0.0f;
+                    constexpr int kAhead = 8;
+                    for (int s0 = c0; s0 <= c1; s0 += kAhead) {
+                        float ms[kAhead], ls[kAhead], os[kAhead], mn = M;
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k) {
+                            ms[k] = -CUDART_INF_F;
+                            ls[k] = os[k] = 0.0f;
+                            if (s0 + k <= c1) {
+                                const int at = 2 * (s0 + k) + (s0 + k == c0 ? late : 0);
+                                ms[k] = __ldcg(&a.ws->part_m[at][hd]);
+                                ls[k] = __ldcg(&a.ws->part_l[at][hd]);
+                                os[k] = __ldcg(&a.ws->part_o[at][hd][tid]);
+                            }
+                            mn = fmaxf(mn, ms[k]);
+                        }
+                        const float keep = weight(M, mn);
+                        L *= keep;
+                        O *= keep;
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k) {
+                            const float f = weight(ms[k], mn);
+                            L += ls[k] * f;
+                            O += os[k] * f;
+                        }
+                        M = mn;
+                    }
+                    a.out[(row0 + hd) * kHeadDim + tid] = f32_to_bf16_rn(L == 0.0f ? 0.0f : O / L);
+                    if (MODE == 2 && tid == 0) {
+                        a.stat_m[row0 + hd] = M;
+                        a.stat_l[row0 + hd] = L;
+                    }
+                }
+            }
+        }
+        // ---- the next unit
+        left -= count;
+        grp = 0;
+        if (left > 0 && ++h == a.Hkv) {
+            h = 0;
+            ++b;
+            seen = seen_of<MODE, GT>(a, b, bad);
+        }
+    }
+    if (flags)
+        atomicOr(a.status, flags);
+}
+
+template <bool Q4, int MODE, int U, int CTAS>
+cudaError_t launch(const CacheAttnArgs &a, int sms, cudaStream_t stream)
+{
+    int64_t most = 0;      // groups, if every request had the most
+    {
+        const int count = MODE == 1 ? a.top_k : a.window > 0 && a.Nmax > a.window ? a.window + a.sinks : a.Nmax;
+        most = (int64_t)a.B * a.Hkv * ((count + 16 * U - 1) / (16 * U) + 1);
+    }
+    int64_t ctas = (int64_t)sms * CTAS;
+    if (ctas > (most + kWarps - 1) / kWarps)
+        ctas = (most + kWarps - 1) / kWarps;
+    if (ctas > kMaxCacheCtas)
+        ctas = kMaxCacheCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = host_pdl();
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_attention_kernel<Q4, MODE, U, CTAS>, a);
+}
+
+// ---- weights: a thread per position and KV head, the logits of its G heads
+constexpr int kWeightThreads = 256;
+constexpr int kWeightPer = 4;
+
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightsArgs a, int chunks)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int unit = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+    const int b = unit / a.Hkv, g = unit % a.Hkv;
+    uint32_t bad = 0;
+    const int n = seq_len_of(a.seq_lens, b, a.Nmax, bad);
+    const int n0 = chunk * kWeightThreads * kWeightPer + threadIdx.x;
+    if (n0 >= n)
+        return;
+    const size_t row0 = (size_t)b * a.Hq + (size_t)g * a.G;
+    float *w = a.weights + (size_t)unit * a.Nmax;
+    float sum[kWeightPer];
+#pragma unroll
+    for (int k = 0; k < kWeightPer; ++k) {
+        const int at = n0 + k * kWeightThreads;
+        sum[k] = at < n - a.fresh ? w[at] : 0.0f;
+    }
+    for (int hd = 0; hd < a.G; ++hd) {
+        const float m = a.stat_m[row0 + hd], l = a.stat_l[row0 + hd];
+        const float ref = m == -CUDART_INF_F ? 0.0f : m, inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float *x = a.logits + (row0 + hd) * a.Nmax;
+#pragma unroll
+        for (int k = 0; k < kWeightPer; ++k) {
+            const int at = n0 + k * kWeightThreads;
+            if (at < n)
+                sum[k] += exp2f(x[at] * kLog2e - ref) * inv;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kWeightPer; ++k) {
+        const int at = n0 + k * kWeightThreads;
+        if (at < n)
+            w[at] = sum[k];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attention(const CacheAttnArgs &a, int sms, cudaStream_t stream)
+{
+    if (a.logits)
+        return launch<false, 2, 1, 3>(a, sms, stream);
+    if (a.rows.scales)
+        return a.idx ? launch<true, 1, 2, 4>(a, sms, stream) : launch<true, 0, 2, 4>(a, sms, stream);
+    return launch<false, 0, 1, 3>(a, sms, stream);
+}
+
+cudaError_t launch_weights(const WeightsArgs &a, cudaStream_t stream)
+{
+    const int per = kWeightThreads * kWeightPer;
+    const int chunks = (a.Nmax + per - 1) / per;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hkv * chunks));
+    cfg.blockDim = dim3(kWeightThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = host_pdl();
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, weights_kernel, a, chunks);
+}
+
+}  // namespace td

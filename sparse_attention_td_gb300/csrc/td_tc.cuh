@@ -1,0 +1,280 @@
+// td_tc.cuh -- device helpers of the kernels on the tcgen05 tensor cores:
+// barriers in shared memory with limited waits, copies, operand descriptors,
+// MMA issue and tensor-memory transfers (td_tree.cu, td_prompt.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "td_internal.h"
+
+namespace td {
+namespace {
+
+__device__ __forceinline__ uint32_t smem_of(const void *p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+__device__ __forceinline__ void bar_init(uint64_t *bar, unsigned count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_of(bar)), "r"(count) : "memory");
+}
+
+// One lane of the warp; the MMAs under it issue faster than under lane == 0
+// (8 of them in 416 instead of 552 cycles).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
+__device__ __forceinline__ void bar_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive_n(uint64_t *bar, unsigned n)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(bar)), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect(uint64_t *bar, unsigned bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// What waits look at before they give up: whether another role has, and the tiles done
+// by the CTA so far.
+struct Progress {
+    int gave_up;
+    uint32_t tiles;
+};
+
+// Waits for the phase of the given parity.  Gives up after `limit` cycles of the SM
+// clock without a tile done (a role may have nothing to do for most of a long unit),
+// or when another role has (then the CTA leaves as a whole and reports the
+// timeout).  Out of line: the roles' code has to stay in the instruction cache.
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, unsigned parity, volatile Progress *at, long long limit)
+{
+    long long t0 = clock64();
+    uint32_t tiles = at->tiles;
+    for (int polls = 1;; ++polls) {
+        if (bar_try(bar, parity))
+            return true;
+        if ((polls & 63) == 0) {
+            if (at->gave_up)
+                return false;
+            if (at->tiles != tiles) {
+                tiles = at->tiles;
+                t0 = clock64();
+            } else if (clock64() - t0 > limit) {
+                at->gave_up = 1;
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ bool bar_wait_for(uint64_t *bar, unsigned parity, volatile Progress *at, long long limit)
+{
+    return bar_try(smem_of(bar), parity) || bar_wait_long(smem_of(bar), parity, at, limit);
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const TmaDesc *map, int x, int row, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(row), "r"(smem_of(bar))
+        : "memory");
+}
+
+// 16 bytes global -> shared, through L2 only; zeros where `there` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+// The barrier gets this thread's arrival once all of its copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// Shared-memory operand of tcgen05.mma, 128-byte swizzle.  K-major (rows of
+// 128 bytes, groups of 8 rows 1024 bytes apart) or, for V, MN-major: 64-value
+// blocks of the dims `lead` bytes apart, groups of 8 tokens 1024 bytes apart.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead)   // low word
+{
+    return ((addr & 0x3ffff) >> 4) | (lead >> 4) << 16;
+}
+constexpr uint32_t kOperandHigh = 1024 >> 4 | 1u << 14 | 2u << 29;   // high word
+
+// kind::f16, fp32 accumulator, operands both bf16 (or both fp16), M = 128; bit 16: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc(uint32_t n, bool fp16 = false)
+{
+    return 1u << 4 | (fp16 ? 0u : 1u << 7 | 1u << 10) | (n >> 3) << 17 | (128u >> 4) << 24;
+}
+__host__ __device__ constexpr uint32_t idesc_v(bool fp16 = false) { return idesc(128, fp16) | 1u << 16; }
+
+template <int N, bool FP16 = false> __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc(N, FP16)), "r"((uint32_t)add), "r"(kOperandHigh)
+        : "memory");
+}
+
+template <bool FP16 = false> __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc_v(FP16)), "r"((uint32_t)add), "r"(kOperandHigh)
+        : "memory");
+}
+
+// The barrier gets an arrival when every MMA issued so far by this thread is done.
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_of(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Values that tmem_ld32 loads are used after a tmem_wait_ld and this, which
+// keeps their first use behind the wait.
+__device__ __forceinline__ void tmem_loaded(uint32_t *r)
+{
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this warp's 32 lanes: thread i gets lane i's values.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&x)[4])
+{
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void store32(void *p, const uint32_t *x)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two fp32 values times f.
+__device__ __forceinline__ void scale2(uint32_t *x, float f)
+{
+    const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(f, f));
+    x[0] = __float_as_uint(y.x);
+    x[1] = __float_as_uint(y.y);
+}
+
+// The same value, which the compiler knows nothing of: a test of it inside a loop
+// does not make two loops (the roles' code has to stay in the instruction cache).
+template <typename T> __device__ __forceinline__ T opaque(T x)
+{
+    if constexpr (sizeof(T) == 8)
+        asm volatile("" : "+l"(x));
+    else
+        asm volatile("" : "+r"(x));
+    return x;
+}
+
+}  // namespace
+}  // namespace td
