@@ -32,16 +32,31 @@ struct RowsArgs {
 // CTAs of a launch of the single-token kernel, at most (it sizes the partials).
 constexpr int kMaxCacheCtas = 1024;
 
+// CTAs of a launch of the kernel for many new tokens, one per SM, at most; query rows of a unit
+// of its work.
+constexpr int kMaxPromptCtas = 160;
+constexpr int kPromptRows = 256;
+
+// A unit whose tiles several CTAs shared, left by the CTA whose range begins at the unit's first
+// cut (rows 0: nothing to join there).
+struct PromptJoin {
+    int b, h, q0, row0, rows, pos0;
+    int last;                             // the last CTA that has a part
+    int late;                             // the first part is its CTA's second one
+};
+
 // Fixed part of the workspace, at the buffer's end whatever the shape is, so that the
 // counters that have to stay zero never lie where a call of another shape writes.
 struct CacheWs {
-    uint32_t units;                       // prompts: units handed out (zero between launches)
-    uint32_t done;                        // prompts: CTAs that have ended (zero between launches)
-    uint32_t pad[62];
     uint32_t tickets[kMaxCacheCtas];      // parts of a cut unit that have come (zero between launches)
     float part_m[2 * kMaxCacheCtas][8];   // running maxima (log2 units)
     float part_l[2 * kMaxCacheCtas][8];   // denominators
     float part_o[2 * kMaxCacheCtas][8][kHeadDim];
+    // many new tokens
+    PromptJoin join[kMaxPromptCtas];
+    float prompt_m[2 * kMaxPromptCtas][kPromptRows];
+    float prompt_l[2 * kMaxPromptCtas][kPromptRows];
+    float prompt_o[2 * kMaxPromptCtas][kPromptRows][kHeadDim];
 };
 
 // One token per request: the last one of its seq_lens[b] positions.

@@ -34,18 +34,30 @@ namespace {
 constexpr int kTile = 128;                       // tokens per tile, query rows per row tile
 constexpr int kHalfBytes = kTile * 128;          // one 64-value half of a tile's rows
 constexpr int kTileBytes = 2 * kHalfBytes;
-constexpr int kUnitRows = 2 * kTile;
-constexpr int kSlots = 5;                        // ring of K and V tiles
+constexpr int kUnitRows = kPromptRows;
+static_assert(kUnitRows == 2 * kTile, "two row tiles");
+// A unit's begin and end cost as much as two tiles: it counts as so many more.  (Prompts of 1K-6K,
+// window 1024, ranges cut by tiles alone: 230 us with 10 units per CTA, 344 with 46.)
+constexpr int kUnitCost = 2;
+constexpr int kLeastCost = 4;                    // of a CTA's range
+constexpr int kMostSlots = 5;
+// Ring of K and V tiles: 16-bit rows 5; 4-bit rows 4, and rings of the copy warps' coded rows.
+template <bool Q4> constexpr int kRingSlots = Q4 ? 4 : 5;
+constexpr int kRawRing = 3;                      // K or V rows of a copy warp on their way
+constexpr int kRawBytes = 32 * (kCodeBytes + 8);
 constexpr int kMaskRing = 8;
 constexpr int kSoftWarps = 8;                    // four per row tile
 constexpr int kCopier = 8, kCopiers = 4;         // copy warps
-constexpr int kIssuer = 12, kSched = 13;
+constexpr int kSched = 12, kIssuer = 13;
 constexpr int kThreads = 32 * 14;
-constexpr int kUnitRing = 2;
+constexpr int kStep = 64;                        // tokens of one S
+constexpr int kCopyRows = kTile / kCopiers;      // of a tile, per copy warp: one a lane
+static_assert(kCopyRows == 32, "a lane has one row of a tile");
+constexpr int kUnitRing = 4;
 constexpr int kUnitUsers = kSoftWarps + kCopiers + 1;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;                  // O of row tile t: kColO + 128 t; S: 128 t; P: 128 t + 64
-constexpr size_t kSmem = (size_t)(2 + kSlots) * kTileBytes + 3 * 1024;    // + Extra
+constexpr uint32_t kColO = 256;      // O of row tile t: kColO + 128 t; S, and P over it: 128 t and 128 t + 64
+constexpr size_t kSmem = (size_t)(2 + kMostSlots) * kTileBytes + 3 * 1024;    // + Extra
 
 // A unit of work, as every role reads it.
 struct Unit {
@@ -53,42 +65,58 @@ struct Unit {
     int q0;            // first row of q of the request
     int row0, rows;    // query rows of the request: row = token * G + head
     int pos0;          // position of the request's first new token
-    int limit;         // cached tokens that some row may see: positions below this
-    int low;           // and at or behind this, or below sinks
-    int sink_tiles, low_tile;
-    int tiles;         // of 128 tokens; -1: no more units
+    // The tokens that some row may see, one behind the other: the first ones (positions 0 ..
+    // first - 1), then positions low .. low + rest - 1.  Tiles are cut from this list.
+    int first, low, rest;
+    // The CTA's segment: tiles of 128 tokens from tile0 on, steps of 64; tiles -1: no more.
+    int tile0, tiles, steps;
+    int part;          // where its result goes: partial sums number `part`, -1: it is the unit's whole
+};
 
-    __device__ int tile(int j) const { return j < sink_tiles ? j : low_tile + j - sink_tiles; }
+// Where a CTA's range of tiles begins.
+struct Start {
+    int b, block, h, at;     // request, block of query rows, KV head, cost of the unit that lies before
+    int64_t left;            // cost of the range; 0: none
 };
 
 // Who arrives and who waits; a wait looks at a phase's parity, so each must come when
-// the phase before is over and before the one after can be.
-//   full     a ring slot's use: every copy thread as its copies land, and once more each copy
-//            warp, behind its word of `valid`.  The issuer waits for every one in order.
+// the phase before is over and before the one after can be.  Step number g of a row tile, over
+// units: its S and P have buffer g & 1.
+//   full     a ring slot's use: 16-bit rows: every copy thread as its copies land (then fenced by
+//            the issuer), and each copy warp behind its word of `valid`; 4-bit rows: each copy
+//            warp when its rows are written and fenced.  The issuer waits for every one in order.
 //   empty    the commit behind the MMAs that read the slot; the copy warps wait for every use.
 //   q, q_free   as full and empty, per unit.
-//   s[t]     S of row tile t.  Its softmax warps wait for every one; the next S is issued
-//            behind P V, which needs their P.
-//   p[t]     the row tile's four softmax warps; the issuer waits for every one.
-//   o[t]     P V of row tile t.  The issuer waits for every one before the next S of t, which
-//            overwrites its P; the softmax for the last one, or to rescale O, always
-//            before it hands over the P that the next one needs.
-//   unit_there, unit_free   a unit's entry, written by the scheduler and read by all others,
-//            who free it when they are done with the unit.
+//   s[t][g & 1]  S of step g of row tile t.  Its softmax warps wait for every one; S of g + 2 is
+//            issued behind P V of g, which needs their P.
+//   p[t][g & 1]  P of step g, the row tile's four softmax warps; the issuer waits for every one,
+//            and P of g + 2 needs S of g + 2.
+//   o[t]     P V of a step.  The issuer waits for that of g - 1 before it issues P V of g, so for
+//            every one (and so S of g + 1 finds P of g - 1 read).  The softmax waits for that of
+//            g - 1 to rescale O, and at a unit's last step, always before it hands over P of g:
+//            P V of g - 2 is over since S of g was issued, P V of g not issued.  Then for the
+//            unit's last one.
+//   unit_there, unit_free   a unit's entry, written by the scheduler and read by all other roles, who free
+//            it when they are done with the unit.
+// q_inv of a unit lies where that of the unit but one before did: its Q comes after q_free of the
+// unit before, which is issued behind all of the unit but one before, for which P was needed.
 struct Extra {
-    uint64_t full[kSlots], empty[kSlots];
+    uint64_t full[kMostSlots], empty[kMostSlots];
     uint64_t q, q_free;
-    uint64_t s[2], p[2], o[2];
+    uint64_t s[2][2], p[2][2], o[2];
     uint64_t unit_there[kUnitRing], unit_free[kUnitRing];
     uint64_t drain, done, never;
     Unit unit[kUnitRing];
+    Start start;
+    long long sums[kThreads / 32];
     alignas(16) uint32_t valid[kMaskRing][4];    // tokens of a tile that exist
-    float q_inv[kUnitRing][kUnitRows];           // 4-bit rows: what a row's scores are multiplied by
+    float q_inv[2][kUnitRows];                   // 4-bit rows: what a row's scores are multiplied by
     uint32_t tmem;
     Progress progress;
     Progress last_waits[kThreads / 32];
 };
-static_assert((2 + kSlots) * kTileBytes + sizeof(Extra) <= kSmem, "shared memory");
+static_assert((2 + kMostSlots) * kTileBytes + sizeof(Extra) <= kSmem, "shared memory");
+static_assert(kCopiers * kRawRing * kRawBytes <= kTileBytes, "coded rows take the fifth slot's place");
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
@@ -117,6 +145,28 @@ __device__ __forceinline__ uint32_t bits_of(int lo, int hi, int base)
 {
     const int x = max(lo - base, 0), y = min(hi - base, 32);
     return x >= y ? 0u : (0xffffffffu >> (32 - (y - x))) << x;
+}
+
+// Four neighbouring lanes' rows of four 32-byte pieces, turned: lane c of the four then has piece c
+// of row k in y[8 k ..].
+__device__ __forceinline__ void turn4(uint32_t (&y)[32], int lane)
+{
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            if (p & d)
+                continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint32_t &lo = y[8 * p + k], &hi = y[8 * (p + d) + k];
+                const uint32_t got = __shfl_xor_sync(kFull, up ? lo : hi, d);
+                lo = up ? got : lo;
+                hi = up ? hi : got;
+            }
+        }
+    }
 }
 
 // Four consecutive values of a cached row.
@@ -178,8 +228,9 @@ __device__ __noinline__ void attend_row(const PromptArgs &a, int b, int h, int p
 template <bool Q4>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __grid_constant__ PromptArgs a)
 {
+    constexpr int kSlots = kRingSlots<Q4>;
     extern __shared__ __align__(1024) unsigned char sm_raw[];
-    Extra &x = *reinterpret_cast<Extra *>(sm_raw + (2 + kSlots) * kTileBytes);
+    Extra &x = *reinterpret_cast<Extra *>(sm_raw + (2 + kMostSlots) * kTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sm_q = smem_of(sm_raw);
     const uint32_t sm_ring = sm_q + 2 * kTileBytes;
@@ -200,14 +251,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         for (int i = 0; i < kThreads / 32; ++i)
             x.last_waits[i] = Progress{};
         for (int i = 0; i < kSlots; ++i) {
-            bar_init(&x.full[i], 33 * kCopiers);
+            bar_init(&x.full[i], Q4 ? kCopiers : 33 * kCopiers);
             bar_init(&x.empty[i], 1);
         }
-        bar_init(&x.q, 32 * kCopiers);
+        bar_init(&x.q, Q4 ? kCopiers : 32 * kCopiers);
         bar_init(&x.q_free, 1);
         for (int t = 0; t < 2; ++t) {
-            bar_init(&x.s[t], 1);
-            bar_init(&x.p[t], 4);
+            for (int i = 0; i < 2; ++i) {
+                bar_init(&x.s[t][i], 1);
+                bar_init(&x.p[t][i], 4);
+            }
             bar_init(&x.o[t], 1);
         }
         for (int i = 0; i < kUnitRing; ++i) {
@@ -229,7 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     tmem_before();
     __syncthreads();
     tmem_after();
-    const uint32_t tmem = x.tmem;
+    constexpr uint32_t tmem = 0;             // all 512 columns are this CTA's, so they begin at 0
+    if (x.tmem != 0 && tid == 0)             // (cannot be)
+        x.progress.gave_up = 1;
+    __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
 
@@ -245,87 +301,196 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         bar_arrive(&x.unit_free[units % kUnitRing]);
     };
 
-    if (warp == kSched) {
-        // ---- scheduler: units by a counter, so that the CTAs end together.  Request b's blocks of
-        // 256 rows are numbers floor(cu[b] G / 256) + b and on (room for all of them; a number
-        // without a block is passed over), its last ones first: they see the most tokens.
+    // ---- the CTA's range: an equal, contiguous run of the batch's tiles, over units' borders, so that
+    // no long context and no small batch leaves SMs idle; a unit that several CTAs share is
+    // joined by prompt_join_kernel.  Units in order: request, block of 256 query rows, KV head.
+    // Request b's blocks are numbers floor(cu[b] G / 256) + b and on (room for all of them; a number
+    // without a block has no tiles).
+    auto start_of = [&](int b) { return min(max(a.cu_new[b], 0), a.num_tokens); };
+    auto number_of = [&](int b) { return (int64_t)start_of(b) * a.G / kUnitRows + b; };
+    uint32_t bad = 0;
+    struct Request {
+        int b, q0, count, n, blocks;
+    };
+    auto request = [&](int b) {
+        Request r;
+        r.b = b;
+        r.q0 = start_of(b);
+        r.count = max(0, start_of(b + 1) - r.q0);
+        r.blocks = (int)(((int64_t)r.count * a.G + kUnitRows - 1) / kUnitRows);
+        r.n = seq_len_of(a.seq_lens, b, a.Nmax, bad);
+        if (r.count > r.n)
+            bad |= kFlagSeqLenOutOfRange;
+        return r;
+    };
+    auto unit_of = [&](const Request &r, int block, int h) {
+        Unit u;
+        u.b = r.b;
+        u.h = h;
+        u.q0 = r.q0;
+        u.row0 = block * kUnitRows;
+        u.rows = min(r.count * a.G - u.row0, kUnitRows);
+        u.pos0 = r.n - r.count;                   // (below zero: those tokens see nothing)
+        const int p0 = u.pos0 + (u.row0 >> a.g_shift);
+        const int p1 = u.pos0 + ((u.row0 + u.rows - 1) >> a.g_shift);
+        u.low = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
+        u.first = min(a.sinks, u.low);
+        u.rest = max(p1 + 1 - u.low, 0);
+        u.tile0 = 0;
+        u.steps = max(1, (u.first + u.rest + kStep - 1) / kStep);
+        u.tiles = (u.steps + 1) / 2;
+        u.part = -1;
+        return u;
+    };
+    int64_t per;
+    {
         const int64_t numbers = (int64_t)a.num_tokens * a.G / kUnitRows + a.B;
-        const int64_t total = numbers * a.Hkv;
-        auto start_of = [&](int b) { return min(max(a.cu_new[b], 0), a.num_tokens); };
-        auto number_of = [&](int b) { return (int64_t)start_of(b) * a.G / kUnitRows + b; };
+        const int64_t run = (numbers + kThreads - 1) / kThreads;
+        const int64_t n0 = min(tid * run, numbers), n1 = min(n0 + run, numbers);
+        int b0 = 0;                               // the last request that begins at or before number n0
+        for (int hi = a.B; hi - b0 > 1;) {
+            const int mid = (b0 + hi) >> 1;
+            if (number_of(mid) <= n0)
+                b0 = mid;
+            else
+                hi = mid;
+        }
+        // Calls f(request, block, tiles) for the run's blocks, until it returns false.
+        auto walk = [&](auto f) {
+            if (n0 >= n1)
+                return;
+            int b = b0;
+            Request r = request(b);
+            int64_t first = number_of(b), next = number_of(b + 1);
 #pragma unroll 1
-        while (ok) {
-            Unit u{};
-            u.tiles = -1;
-            uint32_t bad = 0;
-#pragma unroll 1
-            for (;;) {
-                uint32_t at = 0;
-                if (lane == 0)
-                    at = atomicAdd(&a.ws->units, 1u);
-                at = __shfl_sync(kFull, at, 0);
-                if (at >= total)
-                    break;
-                const int64_t number = at / (uint32_t)a.Hkv;
-                int lo = 0, hi = a.B;             // the last request that begins at or before the number
-                while (hi - lo > 1) {
-                    const int step = (hi - lo + 31) / 32, b = lo + lane * step;
-                    const int n = __popc(__ballot_sync(kFull, b < hi && (lane == 0 || number_of(b) <= number)));
-                    lo += (n - 1) * step;
-                    hi = min(hi, lo + step);
+            for (int64_t n = n0; n < n1; ++n) {
+                while (b + 1 < a.B && n >= next) {
+                    r = request(++b);
+                    first = next;
+                    next = number_of(b + 1);
                 }
-                const int q0 = start_of(lo), count = max(0, start_of(lo + 1) - q0);
-                const int blocks = (int)(((int64_t)count * a.G + kUnitRows - 1) / kUnitRows);
-                const int64_t block = number - number_of(lo);
-                if (block < 0 || block >= blocks)
-                    continue;
-                u.b = lo;
-                u.h = at % (uint32_t)a.Hkv;
-                u.q0 = q0;
-                u.row0 = (blocks - 1 - (int)block) * kUnitRows;
-                u.rows = min(count * a.G - u.row0, kUnitRows);
-                const int n = seq_len_of(a.seq_lens, lo, a.Nmax, bad);
-                if (count > n)
-                    bad |= kFlagSeqLenOutOfRange;
-                u.pos0 = n - count;               // (below zero: those tokens see nothing)
-                const int p0 = u.pos0 + (u.row0 >> a.g_shift);
-                const int p1 = u.pos0 + ((u.row0 + u.rows - 1) >> a.g_shift);
-                u.limit = max(p1 + 1, 0);
-                u.low = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
-                u.low_tile = u.low / kTile;
-                u.sink_tiles = min((min(a.sinks, u.low) + kTile - 1) / kTile, u.low_tile);
-                u.tiles = u.sink_tiles + max(1, (u.limit + kTile - 1) / kTile - u.low_tile);
-                break;
+                if (n - first >= 0 && n - first < r.blocks && !f(r, (int)(n - first), unit_of(r, (int)(n - first), 0).tiles))
+                    return;
             }
-            if (bad && lane == 0)
-                atomicOr(a.status, bad);
-            if (units >= kUnitRing)
-                ok = warp_wait(&x.unit_free[units % kUnitRing], units / kUnitRing - 1);
-            if (!ok)
-                break;
-            if (lane == 0) {
-                x.unit[units % kUnitRing] = u;
-                bar_arrive(&x.unit_there[units % kUnitRing]);
+        };
+        long long mine = 0;
+        walk([&](const Request &, int, int tiles) {
+            mine += (long long)(tiles + kUnitCost) * a.Hkv;
+            return true;
+        });
+        if (bad && blockIdx.x == 0)
+            atomicOr(a.status, bad);
+        long long inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(kFull, inc, d);
+            if (lane >= d)
+                inc += y;
+        }
+        if (lane == 31)
+            x.sums[warp] = inc;
+        if (tid == 0)
+            x.start.left = 0;
+        __syncthreads();
+        long long all = 0, at = inc - mine;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp)
+                at += x.sums[i];
+            all += x.sums[i];
+        }
+        per = max((all + gridDim.x - 1) / gridDim.x, (long long)kLeastCost);
+        const long long begin = blockIdx.x * per;
+        if (begin < all && at <= begin && begin < at + mine)
+            walk([&](const Request &r, int block, int tiles) {
+                const int cost = tiles + kUnitCost;
+                if (begin >= at + (long long)cost * a.Hkv) {
+                    at += (long long)cost * a.Hkv;
+                    return true;
+                }
+                const int off = (int)(begin - at);
+                x.start = Start{r.b, block, off / cost, off % cost, min((long long)per, all - begin)};
+                return false;
+            });
+        __syncthreads();
+        if (tid == 0 && blockIdx.x > 0) {
+            // The unit that this range's begin cuts, if it is the unit's first cut: the CTA before has
+            // the unit's first tile.
+            PromptJoin j{};
+            const Start w = x.start;
+            if (w.left > 0 && w.at > kUnitCost && w.at - per <= kUnitCost) {
+                const Unit u = unit_of(request(w.b), w.block, w.h);
+                j = PromptJoin{u.b, u.h, u.q0, u.row0, u.rows, u.pos0,
+                               (int)((begin - w.at + u.tiles + kUnitCost - 1) / per), w.at < per};
+            }
+            a.ws->join[blockIdx.x] = j;
+        }
+    }
+    // Publishes the CTA's units (the scheduler, as far ahead as there are entries).
+    auto publish_all = [&] {
+        Start w = x.start;
+        Request r = w.left > 0 ? request(w.b) : Request{};
+#pragma unroll 1
+        for (uint32_t n = 0;; ++n) {
+            Unit u;
+            u.tiles = -1;
+            if (w.left > 0) {
+                // Of cost at .. end of the unit; its first kUnitCost are no tiles.
+                u = unit_of(r, w.block, w.h);
+                const int all = u.tiles;
+                const int end = (int)min((int64_t)(all + kUnitCost), w.at + w.left);
+                u.tile0 = max(w.at - kUnitCost, 0);
+                u.tiles = max(end - kUnitCost, 0) - u.tile0;
+                if (u.tiles == 0)
+                    u.tiles = -1;                 // (the range ends before the unit's first tile)
+                u.steps = min(u.steps - 2 * u.tile0, 2 * u.tiles);
+                if (u.tiles < all)
+                    u.part = 2 * blockIdx.x + (n > 0);
+                w.left -= end - w.at;
+                w.at = 0;
+                if (w.left > 0 && ++w.h == a.Hkv) {
+                    w.h = 0;
+                    if (++w.block == r.blocks) {
+                        w.block = 0;
+                        do
+                            r = request(r.b + 1);
+                        while (r.blocks == 0 && r.b + 1 < a.B);
+                    }
+                }
+            }
+            if (n >= kUnitRing)
+                ok = warp_wait(&x.unit_free[n % kUnitRing], n / kUnitRing - 1);
+            if (ok && lane == 0) {
+                x.unit[n % kUnitRing] = u;
+                bar_arrive(&x.unit_there[n % kUnitRing]);
             }
             __syncwarp();
-            ++units;
-            if (u.tiles < 0)
+            if (!ok || u.tiles < 0)
                 break;
         }
+    };
+
+    if (warp == kSched) {
+        publish_all();
     } else if (warp >= kCopier && warp < kCopier + kCopiers) {
-        // ---- copy warps: a unit's Q, then its K and V tiles, 32 rows of each per warp
+        // ---- copy warps: a unit's Q, then its K and V tiles, kCopyRows rows of each per warp
         const int me = warp - kCopier;
         uint32_t e = 0;                           // ring entries begun
         uint32_t flags = 0;
         uint32_t tile_no = 0;
+        auto arrive = [&](uint64_t *bar) {        // this warp's rows are written: the MMAs may read them
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(bar);
+        };
 #pragma unroll 1
         for (; next_unit(); ++units) {
             const Unit u = unit_entry();
-            // the row of this lane's token of tile j; a token that no row of the unit sees is
-            // none (zeros: no value of it meets a zero probability)
+            // The row of this lane's token of tile j, in three steps for later tiles while
+            // earlier ones are copied: position, page, row.
             auto position = [&](int j) {
-                const int p = u.tile(j) * kTile + 32 * me + lane;
-                return j < u.tiles && p < u.limit && (p >= u.low || p < a.sinks) ? p : -1;
+                const int t = (u.tile0 + j) * kTile + kCopyRows * me + lane;
+                return j >= u.tiles || t >= u.first + u.rest ? -1 : t < u.first ? t : t - u.first + u.low;
             };
             auto page = [&](int p) { return p >= 0 ? page_of(a.rows, u.b, p) : 0; };
             auto find = [&](int p, int pg) {
@@ -336,17 +501,35 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     flags |= kFlagPageOutOfRange;
                 return row;
             };
-            int p0 = position(0), p1 = position(1);
-            int pg0 = page(p0), pg1 = page(p1);
-            if (units > 0)
-                ok = warp_wait(&x.q_free, units - 1);
-            if (!ok)
-                break;
-            {   // Q: half a warp per row of 256 bytes
+            int p1 = position(0), p2 = position(1);
+            int pg1 = page(p1), pg2 = page(p2);
+            auto next_row = [&](int j) {          // of tile j, one after the other
+                const int row = find(p1, pg1);
+                p1 = p2, pg1 = pg2;
+                p2 = position(j + 2), pg2 = page(p2);
+                return row;
+            };
+            // Waits for the next ring slot; behind K's the tile's word of `valid`.
+            auto next_slot = [&](bool k, uint32_t there) {
+                const uint32_t slot = e % kSlots, use = e / kSlots;
+                if (use > 0)
+                    ok = ok && warp_wait(&x.empty[slot], use - 1);
+                if (ok && k && lane == 0)
+                    x.valid[tile_no % kMaskRing][me] = there;
+                ++e;
+                return slot;
+            };
+            // Q, half a warp per row of 256 bytes, behind the first K tile: its place is free only when
+            // the last S of the unit before is done.
+            auto copy_q = [&] {
+                if (units > 0)
+                    ok = warp_wait(&x.q_free, units - 1);
+                if (!ok)
+                    return;
                 const int c = lane & 15;
                 const uint16_t *src = a.q + ((size_t)u.q0 * a.Hq + (size_t)u.h * a.G) * kHeadDim + c * 8;
                 const uint32_t dst = sm_q + (c >> 3) * kHalfBytes;
-#pragma unroll 4
+#pragma unroll 8
                 for (int r = 2 * me + (lane >> 4); r < u.rows; r += 2 * kCopiers) {
                     const int row = u.row0 + r, tk = row >> a.g_shift, g = row & (a.G - 1);
                     const uint32_t to = dst + (r >> 7) * kTileBytes + (r & 127) * 128 + (((c ^ r) & 7) << 4);
@@ -374,39 +557,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                             w[k] = pack_f16(bf_lo(w[k]) * f, bf_hi(w[k]) * f);
                         sts4(to, w[0], w[1], w[2], w[3]);
                         if (c == 0)
-                            x.q_inv[units % kUnitRing][r] = __uint_as_float((uint32_t)(127 - up) << 23);
+                            x.q_inv[units & 1][r] = __uint_as_float((uint32_t)(127 - up) << 23);
                     }
                 }
-                if constexpr (!Q4) {
+                if constexpr (!Q4)
                     copies_arrive(&x.q);
-                } else {
-                    __syncwarp();
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    bar_arrive(&x.q);
-                }
-            }
+                else
+                    arrive(&x.q);
+            };
+            if constexpr (!Q4) {
 #pragma unroll 1
-            for (int j = 0; j < u.tiles; ++j, ++tile_no) {
-                const int row = find(p0, pg0);
-                p0 = p1;
-                pg0 = pg1;
-                p1 = position(j + 2);
-                pg1 = page(p1);
-                const uint32_t there = __ballot_sync(kFull, row >= 0);
-                if constexpr (!Q4) {
+                for (int j = 0; j < u.tiles && ok; ++j, ++tile_no) {
+                    const int row = next_row(j);
+                    const uint32_t there = __ballot_sync(kFull, row >= 0);
 #pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv, ++e) {
-                        const uint32_t slot = e % kSlots, use = e / kSlots;
-                        if (use > 0)
-                            ok = warp_wait(&x.empty[slot], use - 1);
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t slot = next_slot(kv == 0, there);
                         if (!ok)
                             break;
-                        if (kv == 0 && lane == 0)
-                            x.valid[tile_no % kMaskRing][me] = there;
                         const int c = lane & 15;
                         const uint8_t *src = (kv ? a.rows.v : a.rows.k) + c * 16;
-                        const uint32_t dst = sm_ring + slot * kTileBytes + (c >> 3) * kHalfBytes + 32 * me * 128;
-#pragma unroll 4
+                        const uint32_t dst = sm_ring + slot * kTileBytes + (c >> 3) * kHalfBytes + kCopyRows * me * 128;
+#pragma unroll 8
                         for (int r = lane >> 4; r < 32; r += 2) {
                             const int from = __shfl_sync(kFull, row, r);
                             copy16(dst + r * 128 + (((c ^ r) & 7) << 4),
@@ -415,56 +587,92 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                         copies_arrive(&x.full[slot]);
                         if (lane == 0)
                             bar_arrive(&x.full[slot]);
-                    }
-                } else {
-                    // a lane decodes 32 values (16 bytes, two scales) of four rows
-                    const int c = lane >> 3;
-                    uint4 w[2][4];
-                    uint32_t sc[2][4];
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const int from = __shfl_sync(kFull, row, 8 * t + (lane & 7));
-                            const size_t at = (uint32_t)max(from, 0);
-                            w[kv][t] = *reinterpret_cast<const uint4 *>((kv ? a.rows.v : a.rows.k) + at * kCodeBytes + 16 * c);
-                            sc[kv][t] = from >= 0 ? *reinterpret_cast<const uint16_t *>(a.rows.scales + at * kScaleBytes + 8 * kv + 2 * c) : 0;
-                        }
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++e) {
-                        const uint32_t slot = e % kSlots, use = e / kSlots;
-                        if (use > 0)
-                            ok = warp_wait(&x.empty[slot], use - 1);
-                        if (!ok)
-                            break;
-                        if (kv == 0 && lane == 0)
-                            x.valid[tile_no % kMaskRing][me] = there;
-                        const uint32_t dst = sm_ring + slot * kTileBytes + (c >> 1) * kHalfBytes;
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const int r = 32 * me + 8 * t + (lane & 7);
-                            uint32_t s2, two[2];
-                            asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
-                                : "=r"(s2)
-                                : "r"(sc[kv][t]));
-                            two[0] = __byte_perm(s2, s2, 0x1010);
-                            two[1] = __byte_perm(s2, s2, 0x3232);
-                            const uint32_t words[4] = {w[kv][t].x, w[kv][t].y, w[kv][t].z, w[kv][t].w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t y[4];
-                                decode8(words[k], two[k >> 1], y);
-                                const int chunk = 4 * (c & 1) + k;      // of the row's half
-                                sts4(dst + r * 128 + (((chunk ^ r) & 7) << 4), y[0], y[1], y[2], y[3]);
-                            }
-                        }
-                        __syncwarp();
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        bar_arrive_n(&x.full[slot], lane == 0 ? 2 : 1);
+                        if (j == 0 && kv == 0)
+                            copy_q();
                     }
                 }
-                if (!ok)
-                    break;
+            } else {
+                // 4-bit rows come through a ring of the warp's own, kRawRing K or V tiles ahead of
+                // where they are decoded (from registers, the loads of one tile ahead: 3000 cycles of
+                // waiting a tile).  Codes of row r, 16 bytes c: at r * 64 + (c ^ r / 2 & 3) * 16, then
+                // 8 bytes of scales a row.
+                const uint32_t raw0 = sm_ring + kSlots * kTileBytes + me * kRawRing * kRawBytes;
+                int row = -1;                     // of the tile whose copies were issued last
+                uint32_t there[3] = {0, 0, 0};    // of the tile decoded next and the two behind it
+                auto issue = [&](int n, uint32_t raw) {      // K (n even) or V rows of tile n / 2
+                    if (!(n & 1)) {
+                        row = next_row(n >> 1);
+                        there[2] = __ballot_sync(kFull, row >= 0);
+                    }
+                    const uint8_t *codes = n & 1 ? a.rows.v : a.rows.k;
+                    const int c = lane & 3;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * i + (lane >> 2), from = __shfl_sync(kFull, row, r);
+                        copy16(raw + r * kCodeBytes + ((c ^ (r >> 1 & 3)) << 4),
+                               codes + (size_t)(uint32_t)max(from, 0) * kCodeBytes + 16 * c, from >= 0);
+                    }
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(raw + 32 * kCodeBytes + 8 * lane),
+                                 "l"(a.rows.scales + (size_t)(uint32_t)max(row, 0) * kScaleBytes + 8 * (n & 1)),
+                                 "r"(row >= 0 ? 8 : 0)
+                                 : "memory");
+                };
+                const int entries = 2 * u.tiles;
+                // (K and V of tile 0, K of tile 1: behind each K the words of `valid` move up)
+#pragma unroll
+                for (int n = 0; n < kRawRing; ++n) {
+                    if (n < entries)
+                        issue(n, raw0 + n * kRawBytes);
+                    if (n == 0)
+                        there[0] = there[2];
+                    if (n == 2)
+                        there[1] = there[2];
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                }
+                uint32_t raw = raw0;
+#pragma unroll 1
+                for (int n = 0; n < entries; ++n) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kRawRing - 1) : "memory");
+                    __syncwarp();                 // (every lane's copies)
+                    const uint32_t slot = next_slot(!(n & 1), there[0]);
+                    if (!ok)
+                        break;
+                    const int c = lane >> 3;      // a lane decodes 32 values of four rows
+                    const uint32_t dst = sm_ring + slot * kTileBytes + (c >> 1) * kHalfBytes;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int r8 = 8 * t + (lane & 7), r = kCopyRows * me + r8;
+                        uint32_t w[4], s2, two[2];
+                        lds_words(raw + r8 * kCodeBytes + ((c ^ (r8 >> 1 & 3)) << 4), w);
+                        asm volatile("{\n\t.reg .b16 t;\n\tld.shared.b16 t, [%1];\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+                                     : "=r"(s2)
+                                     : "r"(raw + 32 * kCodeBytes + 8 * r8 + 2 * c)
+                                     : "memory");
+                        two[0] = __byte_perm(s2, s2, 0x1010);
+                        two[1] = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t y[4];
+                            decode8(w[k], two[k >> 1], y);
+                            const int chunk = 4 * (c & 1) + k;      // of the row's half
+                            sts4(dst + r * 128 + (((chunk ^ r) & 7) << 4), y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    arrive(&x.full[slot]);        // (with a __syncwarp: the coded rows have been read)
+                    if (n == 0)
+                        copy_q();
+                    if (n + kRawRing < entries)
+                        issue(n + kRawRing, raw);
+                    if (n & 1) {                  // (the issue above was of K)
+                        ++tile_no;
+                        there[0] = there[1];
+                        there[1] = there[2];
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    raw = raw == raw0 + (kRawRing - 1) * kRawBytes ? raw0 : raw + kRawBytes;
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
             }
             if (!ok)
                 break;
@@ -475,85 +683,114 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         if (flags)
             atomicOr(a.status, flags);
     } else if (warp == kIssuer) {
-        // ---- MMA issue, by one thread
+        // ---- MMA issue, by one thread: S of the next step of both row tiles, then P V of this
+        // one, so that the softmax finds its next scores when it is done with these.  The tensor
+        // cores queue few MMAs: every instruction between them counts.  (A wait that gave up
+        // lets the step's MMAs go, whose results nobody uses.)
         if (elect_one()) {
-            uint32_t e = 0;                       // ring entry of the unit's first K tile
-            uint32_t pv[2] = {0, 0};              // P V issued so far, per row tile
-            uint32_t done_tiles = 0;
-            auto wait = [&](uint64_t *bar, uint32_t phase) {
-                ok = ok && bar_wait(bar, phase);
-                return ok;
+            uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0;      // ring slots of the tile's K and V
+            uint32_t s_buf[2] = {0, 0}, p_buf[2] = {0, 0};    // buffers of a row tile's next S and P V
+            uint32_t p_phase[2] = {0, 0};         // bit b: phase of p[t][b]
+            uint32_t o_phase[2] = {1, 1};         // phase of the last P V that was issued
+            uint32_t done_steps = 0;
+            const uint32_t q_op = operand(sm_q, 16);
+            const uint32_t ring_k = operand(sm_ring, 16), ring_v = operand(sm_ring, kHalfBytes);
+            auto wait = [&](uint64_t *bar, uint32_t phase) { ok = bar_wait(bar, phase) && ok; };
+            // Rows copied by cp.async are read by the MMAs through the async proxy.
+            auto wait_rows = [&](uint64_t *bar, uint32_t phase) {
+                wait(bar, phase);
+                if (!Q4)
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             };
-            auto proxy_fence = [] { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); };
-            auto wait_full = [&](uint32_t entry) {
-                wait(&x.full[entry % kSlots], entry / kSlots);
-                proxy_fence();
-                return ok;
+            auto advance = [](uint32_t &slot, uint32_t &phase) {     // two slots on
+                slot += 2;
+                if (slot >= kSlots) {
+                    slot -= kSlots;
+                    phase ^= 1;
+                }
+            };
+            // S of a step, behind P V of the step before the last (which has read the P there)
+            auto issue_s = [&](int t, uint32_t k, bool after) {
+                if (after)
+                    wait(&x.o[t], o_phase[t]);
+                tmem_after();
+                const uint32_t q = q_op + t * (kTileBytes >> 4);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
+                    mma_ss<kStep, Q4>(tmem + 128 * t + 64 * s_buf[t], q + (o >> 4), k + (o >> 4), s > 0);
+                }
+                mma_commit(&x.s[t][s_buf[t]]);
+                s_buf[t] ^= 1;
+            };
+            auto issue_pv = [&](int t, uint32_t v, bool add) {
+                const uint32_t b = p_buf[t];
+                wait(&x.p[t][b], p_phase[t] >> b);
+                p_phase[t] ^= 1u << b;
+                p_buf[t] ^= 1;
+                tmem_after();
+#pragma unroll
+                for (int s = 0; s < kStep / 16; ++s)
+                    mma_ts<Q4>(tmem + kColO + 128 * t, tmem + 128 * t + 64 * b + s * 8, v + (s * 16 * 128 >> 4),
+                               add || s > 0);
+                mma_commit(&x.o[t]);
+                o_phase[t] ^= 1;
             };
 #pragma unroll 1
             for (;; ++units) {
                 wait(&x.unit_there[units % kUnitRing], units / kUnitRing);
-                if (!ok)
+                if (!ok || unit_entry().tiles < 0)
                     break;
-                const int tiles = unit_entry().tiles, parts = unit_entry().rows > kTile ? 2 : 1;
-                if (tiles < 0)
-                    break;
-                auto issue_s = [&](int t, int j) {
-                    // P V before has read the P that lies over this S (and its softmax the S before)
-                    if (pv[t] > 0 && !wait(&x.o[t], pv[t] - 1))
-                        return;
-                    tmem_after();
-                    const uint32_t q = operand(sm_q + t * kTileBytes, 16);
-                    const uint32_t k = operand(sm_ring + (e + 2 * j) % kSlots * kTileBytes, 16);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
-                        mma_ss<kTile, Q4>(tmem + 128 * t, q + (o >> 4), k + (o >> 4), s > 0);
-                    }
-                    mma_commit(&x.s[t]);
-                    if (t == parts - 1) {
-                        mma_commit(&x.empty[(e + 2 * j) % kSlots]);
-                        if (j == tiles - 1)
-                            mma_commit(&x.q_free);
-                    }
-                };
-                if (!wait(&x.q, units))
-                    break;
-                proxy_fence();
-                if (!wait_full(e))
-                    break;
-                for (int t = 0; ok && t < parts; ++t)
-                    issue_s(t, 0);
+                const int steps = unit_entry().steps;
+                const bool two = unit_entry().rows > kTile;
+                wait_rows(&x.q, units);
+                wait_rows(&x.full[k_slot], k_phase);
+                uint32_t k = ring_k + k_slot * (kTileBytes >> 4);
+                issue_s(0, k, true);              // (behind the unit before)
+                if (two)
+                    issue_s(1, k, true);
+                if (steps == 1) {
+                    mma_commit(&x.empty[k_slot]);
+                    mma_commit(&x.q_free);
+                    advance(k_slot, k_phase);
+                }
 #pragma unroll 1
-                for (int j = 0; ok && j < tiles; ++j) {
-#pragma unroll 1
-                    for (int t = 0; ok && t < parts; ++t) {
-                        const uint32_t entry = e + 2 * j + 1;
-                        if (t == 0 && !wait_full(entry))
-                            break;
-                        if (!wait(&x.p[t], pv[t]))
-                            break;
-                        tmem_after();
-                        const uint32_t v = operand(sm_ring + entry % kSlots * kTileBytes, kHalfBytes);
-#pragma unroll
-                        for (int s = 0; s < kTile / 16; ++s)
-                            mma_ts<Q4>(tmem + kColO + 128 * t, tmem + 128 * t + 64 + s * 8, v + (s * 16 * 128 >> 4),
-                                       j > 0 || s > 0);
-                        mma_commit(&x.o[t]);
-                        ++pv[t];
-                        if (t == parts - 1)
-                            mma_commit(&x.empty[entry % kSlots]);
-                        if (j + 1 < tiles) {
-                            if (t == 0 && !wait_full(entry + 1))
-                                break;
-                            issue_s(t, j + 1);
+                for (int i = 0; i < steps && ok; ++i) {
+                    const bool odd = i & 1;
+                    if (i + 1 < steps) {          // S of step i + 1
+                        if (odd) {
+                            wait_rows(&x.full[k_slot], k_phase);
+                            k = ring_k + k_slot * (kTileBytes >> 4);
                         }
+                        const uint32_t kk = k + (odd ? 0 : kStep * 128 >> 4);
+                        issue_s(0, kk, i > 0);
+                        if (two)
+                            issue_s(1, kk, i > 0);
+                        if (!odd || i + 2 == steps) {         // the tile's last one
+                            mma_commit(&x.empty[k_slot]);
+                            advance(k_slot, k_phase);
+                        }
+                        if (i + 2 == steps)
+                            mma_commit(&x.q_free);
+                    } else if (i > 0) {
+                        wait(&x.o[0], o_phase[0]);
+                        if (two)
+                            wait(&x.o[1], o_phase[1]);
                     }
-                    progress->tiles = ++done_tiles;
+                    if (!odd)
+                        wait_rows(&x.full[v_slot], v_phase);
+                    const uint32_t v = ring_v + v_slot * (kTileBytes >> 4) + (odd ? kStep * 128 >> 4 : 0);
+                    issue_pv(0, v, i > 0);
+                    if (two)
+                        issue_pv(1, v, i > 0);
+                    if (odd || i + 1 == steps) {
+                        mma_commit(&x.empty[v_slot]);
+                        advance(v_slot, v_phase);
+                    }
+                    progress->tiles = ++done_steps;
                 }
                 if (!ok)
                     break;
-                e += 2 * tiles;
                 free_unit();
             }
             // No arrival of the last commits may be left when the CTA ends.
@@ -566,12 +803,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         const int part = warp >> 2;
         const int r = tid & 127;                              // row of the row tile, and TMEM lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const uint32_t col_s = tmem + 128 * part + lanes, col_p = col_s + 64, col_o = tmem + kColO + 128 * part + lanes;
-        uint32_t count = 0, tile_no = 0;                      // tiles of this row tile; of the CTA
+        const uint32_t col_s = tmem + 128 * part + lanes, col_o = tmem + kColO + 128 * part + lanes;
+        uint32_t count = 0, tile_no = 0;                      // steps of this row tile; tiles of the CTA
 #pragma unroll 1
         for (; next_unit(); ++units) {
             const Unit &u = unit_entry();
-            const int tiles = u.tiles;
+            const int tiles = u.tiles, steps = u.steps;
             if (part * kTile >= u.rows) {                     // the unit has no such row tile
                 tile_no += tiles;
                 __syncwarp();
@@ -583,119 +820,101 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const bool live = mine < u.rows;
             const int row = u.row0 + min(mine, u.rows - 1);
             const int p = u.pos0 + (row >> a.g_shift);        // position
-            const int low = a.window > 0 ? p - a.window + 1 : 0;
+            // what the row sees of the unit's list of tokens: below its own place, and from the
+            // window's begin on or among the first ones
+            const int shift = u.first - u.low;
+            const int end = p + 1 + shift, low = a.window > 0 ? p - a.window + 1 + shift : 0;
             float sl2 = a.scale * kLog2e;
             float mref = -CUDART_INF_F, l = 0.0f;
 #pragma unroll 1
-            for (int j = 0; j < tiles; ++j, ++count, ++tile_no) {
-                ok = warp_wait(a.wait_test ? &x.never : &x.s[part], a.wait_test ? 0 : count);
+            for (int i = 0; i < steps; ++i, ++count) {
+                const uint32_t buf = count & 1;
+                ok = warp_wait(a.wait_test ? &x.never : &x.s[part][buf], a.wait_test ? 0 : count >> 1);
                 if (!ok)
                     break;
                 tmem_after();
-                if (Q4 && j == 0)                             // (written with Q, so there behind the first S)
-                    sl2 *= x.q_inv[units % kUnitRing][min(mine, u.rows - 1)];
-                uint32_t seen[4];
-                lds_words(smem_of(x.valid[tile_no % kMaskRing]), seen);
-                const int t0 = u.tile(j) * kTile;
-                // does every row of the warp see the whole tile?
-                const bool inside = p >= t0 + kTile - 1 && (t0 >= low || t0 + kTile <= a.sinks);
+                float s[kStep];                               // the row's scores
+                tmem_ld32(col_s + 64 * buf, reinterpret_cast<uint32_t *>(s));
+                tmem_ld32(col_s + 64 * buf + 32, reinterpret_cast<uint32_t *>(s) + 32);
+                if (Q4 && i == 0)                             // (written with Q, so there behind the first S)
+                    sl2 *= x.q_inv[units & 1][min(mine, u.rows - 1)];
+                const uint32_t *valid = &x.valid[(tile_no + (i >> 1)) % kMaskRing][2 * (i & 1)];
+                uint32_t w0 = valid[0], w1 = valid[1];
+                const int t0 = u.tile0 * kTile + i * kStep;
+                // does every row of the warp see all of the step's tokens?
+                const bool inside = end >= t0 + kStep && (t0 >= low || t0 + kStep <= a.sinks);
                 if (!__all_sync(kFull, inside)) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        seen[w] &= bits_of(0, p + 1 - t0, 32 * w) &
-                                   (bits_of(low - t0, kTile, 32 * w) | bits_of(0, a.sinks - t0, 32 * w));
+                    w0 &= bits_of(0, end - t0, 0) & (bits_of(low - t0, kStep, 0) | bits_of(0, a.sinks - t0, 0));
+                    w1 &= bits_of(0, end - t0, 32) & (bits_of(low - t0, kStep, 32) | bits_of(0, a.sinks - t0, 32));
                 }
-                // The row's scores pass through 64 registers, in blocks of 64 tokens: both
-                // for the maximum, then the second and again the first for the exponentials.
+                tmem_wait_ld();
+                tmem_loaded(reinterpret_cast<uint32_t *>(s));
+                tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32);
+                if (__any_sync(kFull, (w0 & w1) != kFull)) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (!(w0 >> k & 1u))
+                            s[k] = -CUDART_INF_F;
+                        if (!(w1 >> k & 1u))
+                            s[32 + k] = -CUDART_INF_F;
+                    }
+                }
                 float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-                float2 off2 = make_float2(0.0f, 0.0f);
-                float2 sum[2] = {off2, off2};
+#pragma unroll
+                for (int k = 0; k < kStep; k += 2)
+                    mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                if (mref == -CUDART_INF_F)
+                    mref = top;                      // nothing summed so far: l = 0 and O = 0
+                // The running maximum lags until a row exceeds it by 2^8: the probabilities
+                // stay below 2^8 and O is rescaled rarely.
+                const bool grow = i > 0 && top > mref + 8.0f;
+                const bool any = __any_sync(kFull, grow);
+                if (any || (i == steps - 1 && i > 0)) {
+                    ok = warp_wait(&x.o[part], count - 1);
+                    if (!ok)
+                        break;
+                }
+                if (any) {
+                    tmem_after();
+                    const float mn = grow ? top : mref;
+                    const float f = grow ? ex2(mref - mn) : 1.0f;
+                    mref = mn;
+                    l *= f;
 #pragma unroll 1
-                for (int pass = 0; pass < 3; ++pass) {
-                    const int block = pass & 1;
-                    const uint32_t w0 = block ? seen[2] : seen[0], w1 = block ? seen[3] : seen[1];
-                    float s[64];
-                    __syncwarp();
-                    tmem_ld32(col_s + 64 * block, reinterpret_cast<uint32_t *>(s));
-                    tmem_ld32(col_s + 64 * block + 32, reinterpret_cast<uint32_t *>(s) + 32);
-                    tmem_wait_ld();
-                    tmem_loaded(reinterpret_cast<uint32_t *>(s));
-                    tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32);
-                    if ((w0 & w1) != kFull) {
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t ov[32];
+                        tmem_ld32(col_o + 32 * c, ov);
+                        tmem_wait_ld();
+                        tmem_loaded(ov);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            if (!(w0 >> k & 1u))
-                                s[k] = -CUDART_INF_F;
-                            if (!(w1 >> k & 1u))
-                                s[32 + k] = -CUDART_INF_F;
-                        }
-                    }
-                    if (pass < 2) {
-#pragma unroll
-                        for (int k = 0; k < 64; k += 2)
-                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
-                    }
-                    if (pass == 1) {
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-                        if (mref == -CUDART_INF_F)
-                            mref = top;              // nothing summed so far: l = 0 and O = 0
-                        // The running maximum lags until a row exceeds it by 2^8: the
-                        // probabilities stay below 2^8 and O is rescaled rarely.
-                        const bool grow = j > 0 && top > mref + 8.0f;
-                        if (__any_sync(kFull, grow)) {
-                            ok = warp_wait(&x.o[part], count - 1);
-                            if (!ok)
-                                break;
-                            tmem_after();
-                            const float mn = grow ? top : mref;
-                            const float f = grow ? ex2(mref - mn) : 1.0f;
-                            mref = mn;
-                            l *= f;
-#pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t ov[32];
-                                tmem_ld32(col_o + 32 * c, ov);
-                                tmem_wait_ld();
-                                tmem_loaded(ov);
-#pragma unroll
-                                for (int k = 0; k < 32; k += 2)
-                                    scale2(ov + k, f);
-                                tmem_st32(col_o + 32 * c, ov);
-                            }
-                        }
-                        const float off = mref == -CUDART_INF_F ? 0.0f : -mref;
-                        off2 = make_float2(off, off);
-                    }
-                    if (pass >= 1) {
-                        const float2 sl22 = make_float2(sl2, sl2);
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float2 z = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), sl22, off2);
-                            const float2 ev = make_float2(ex2(z.x), ex2(z.y));
-                            sum[k & 1] = __fadd2_rn(sum[k & 1], ev);
-                            pk[k] = Q4 ? pack_f16(ev.x, ev.y) : pack_bf16(ev.x, ev.y);
-                        }
-                        // (over scores of the second block, which have been read)
-                        tmem_st32(col_p + 32 * block, pk);
+                        for (int k = 0; k < 32; k += 2)
+                            scale2(ov + k, f);
+                        tmem_st32(col_o + 32 * c, ov);
                     }
                 }
-                if (!ok)
-                    break;
+                const float off = mref == -CUDART_INF_F ? 0.0f : -mref;
+                const float2 off2 = make_float2(off, off), sl22 = make_float2(sl2, sl2);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float2 z = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), sl22, off2);
+                    const float2 ev = make_float2(ex2(z.x), ex2(z.y));
+                    sum[k & 1] = __fadd2_rn(sum[k & 1], ev);
+                    pk[k] = Q4 ? pack_f16(ev.x, ev.y) : pack_bf16(ev.x, ev.y);
+                }
+                tmem_st32(col_s + 64 * buf, pk);             // (over scores that have been read)
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_wait_st();
-                // P V of the tile before is waited for before this P goes: no phase is missed
-                if (j == tiles - 1 && j > 0)
-                    ok = warp_wait(&x.o[part], count - 1);
-                if (!ok)
-                    break;
                 tmem_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(&x.p[part]);
+                    bar_arrive(&x.p[part][buf]);
             }
             if (!ok)
                 break;
+            tile_no += tiles;
             // ---- the rows' results
             ok = warp_wait(&x.o[part], count - 1);
             if (!ok)
@@ -703,31 +922,59 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             tmem_after();
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const size_t q_row = ((size_t)u.q0 + (row >> a.g_shift)) * a.Hq + (size_t)u.h * a.G + (row & (a.G - 1));
+            const bool whole = u.part < 0;
             float worst = 0.0f;
+            // A lane has a row, four lanes four rows: they turn blocks of four 32-byte pieces, so that
+            // a store of the four goes to 128 bytes of one row.  (Every lane on its own: 8400
+            // cycles a unit.)
+            const int row4 = part * kTile + (warp & 3) * 32 + (lane & ~3);     // first of the four rows
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t ov[32];
+            for (int c = 0; c < (whole ? 2 : 4); ++c) {
+                uint32_t y[32];
                 __syncwarp();
-                tmem_ld32(col_o + 32 * c, ov);
-                tmem_wait_ld();
-                tmem_loaded(ov);
-                uint32_t y[16];
+                if (whole) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    scale2(ov + 2 * k, inv);
-                    const float v0 = __uint_as_float(ov[2 * k]), v1 = __uint_as_float(ov[2 * k + 1]);
-                    worst = fmaf(0.0f, v0, fmaf(0.0f, v1, worst));      // NaN where one is not finite
-                    y[k] = l == 0.0f ? 0u : pack_bf16(v0, v1);
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t ov[32];
+                        tmem_ld32(col_o + 64 * c + 32 * half, ov);
+                        tmem_wait_ld();
+                        tmem_loaded(ov);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            scale2(ov + 2 * k, inv);
+                            const float v0 = __uint_as_float(ov[2 * k]), v1 = __uint_as_float(ov[2 * k + 1]);
+                            worst = fmaf(0.0f, v0, fmaf(0.0f, v1, worst));      // NaN where one is not finite
+                            y[16 * half + k] = l == 0.0f ? 0u : pack_bf16(v0, v1);
+                        }
+                    }
+                } else {
+                    tmem_ld32(col_o + 32 * c, y);
+                    tmem_wait_ld();
+                    tmem_loaded(y);
                 }
-                if (live) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + q_row * kHeadDim + 32 * c);
+                turn4(y, lane);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                for (int k = 0; k < 4; ++k) {
+                    if (row4 + k >= u.rows)
+                        continue;
+                    if (whole) {                     // (out is 16-byte aligned)
+                        const int to = u.row0 + row4 + k;
+                        uint4 *dst = reinterpret_cast<uint4 *>(
+                            a.out + (((size_t)u.q0 + (to >> a.g_shift)) * a.Hq + (size_t)u.h * a.G + (to & (a.G - 1))) *
+                                        kHeadDim + 64 * c + 16 * (lane & 3));
+                        dst[0] = make_uint4(y[8 * k], y[8 * k + 1], y[8 * k + 2], y[8 * k + 3]);
+                        dst[1] = make_uint4(y[8 * k + 4], y[8 * k + 5], y[8 * k + 6], y[8 * k + 7]);
+                    } else {
+                        store32(&a.ws->prompt_o[u.part][row4 + k][32 * c + 8 * (lane & 3)], y + 8 * k);
+                    }
                 }
             }
+            if (!whole && live) {
+                a.ws->prompt_m[u.part][mine] = mref;
+                a.ws->prompt_l[u.part][mine] = l;
+            }
             tmem_before();
-            uint32_t again = __ballot_sync(kFull, live && l != 0.0f && !(worst == 0.0f));
+            uint32_t again = __ballot_sync(kFull, live && whole && l != 0.0f && !(worst == 0.0f));
             if (again) {
                 __syncwarp();                        // (the rows' stores come before the second ones)
                 for (; again; again &= again - 1) {
@@ -751,20 +998,83 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         }
         __syncthreads();
     }
-    if (tid == 0) {
-        if (x.progress.gave_up)
-            atomicOr(a.status, kFlagWaitTimeout);
-        // The last CTA to end leaves the counters as it found them.
-        __threadfence();
-        if (atomicAdd(&a.ws->done, 1u) == gridDim.x - 1) {
-            a.ws->units = 0;
-            a.ws->done = 0;
-        }
-    }
+    if (tid == 0 && x.progress.gave_up)
+        atomicOr(a.status, kFlagWaitTimeout);
     if (warp == kIssuer) {
         tmem_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(x.tmem), "r"(kTmemCols)
                      : "memory");
+    }
+}
+
+// Joins the parts of the units that several CTAs shared.  Block x belongs to the begin of CTA x + 1's
+// range, which left a plan of the unit that it cuts (rows 0: none, or not the unit's first cut).
+// A warp per query row: o = sum_s o_s 2^(m_s - m) / sum_s l_s 2^(m_s - m).
+constexpr int kJoinWarps = 4, kJoinBlocks = 16;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const __grid_constant__ PromptArgs a)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
+    const PromptJoin j = a.ws->join[c];
+    // part s: CTA c - 1 + s's; its second one where the unit begins inside its range
+    auto part_of = [&](int s) { return 2 * (c - 1 + s) + (s == 0 && j.late ? 1 : 0); };
+    const int parts = j.last - c + 2;
+    for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < j.rows; r += kJoinBlocks * kJoinWarps) {
+        constexpr int kAhead = 4;
+        float top = -CUDART_INF_F, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int s0 = 0; s0 < parts; s0 += kAhead) {
+            float ms[kAhead], ls[kAhead];
+            float4 x[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                ms[k] = -CUDART_INF_F;
+                ls[k] = 0.0f;
+                x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (s0 + k < parts) {
+                    const int p = part_of(s0 + k);
+                    ms[k] = a.ws->prompt_m[p][r];
+                    ls[k] = a.ws->prompt_l[p][r];
+                    x[k] = *reinterpret_cast<const float4 *>(&a.ws->prompt_o[p][r][4 * lane]);
+                }
+            }
+            float mn = top;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                mn = fmaxf(mn, ms[k]);
+            const float ref = mn == -CUDART_INF_F ? 0.0f : mn;
+            const float keep = exp2f(top - ref);
+            l *= keep;
+            o.x *= keep;
+            o.y *= keep;
+            o.z *= keep;
+            o.w *= keep;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (ls[k] == 0.0f)               // nothing of the part is seen (its sums may hold anything)
+                    continue;
+                const float f = ms[k] == -CUDART_INF_F ? 1.0f : exp2f(ms[k] - ref);
+                l += ls[k] * f;
+                o.x += x[k].x * f;
+                o.y += x[k].y * f;
+                o.z += x[k].z * f;
+                o.w += x[k].w * f;
+            }
+            top = mn;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int row = j.row0 + r;
+        const size_t q_row = ((size_t)j.q0 + (row >> a.g_shift)) * a.Hq + (size_t)j.h * a.G + (row & (a.G - 1));
+        const float worst = 0.0f * o.x + 0.0f * o.y + 0.0f * o.z + 0.0f * o.w;
+        if (__any_sync(kFull, !(worst * inv == 0.0f))) {
+            attend_row(a, j.b, j.h, j.pos0 + (row >> a.g_shift), q_row, lane);
+            continue;
+        }
+        uint2 y;
+        y.x = pack_bf16(o.x * inv, o.y * inv);
+        y.y = pack_bf16(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2 *>(a.out + q_row * kHeadDim + 4 * lane) = y;
     }
 }
 
@@ -787,9 +1097,9 @@ template <bool Q4> cudaError_t launch(const PromptArgs &a, int sms, cudaStream_t
                 ready[dev] = true;
         }
     }
-    const int64_t units = ((int64_t)a.num_tokens * a.G / kUnitRows + a.B) * a.Hkv;
+    const int ctas = sms < kMaxPromptCtas ? sms : kMaxPromptCtas;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units < sms ? units : sms));
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
@@ -798,7 +1108,13 @@ template <bool Q4> cudaError_t launch(const PromptArgs &a, int sms, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = host_pdl();
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prompt_attention_kernel<Q4>, a);
+    err = cudaLaunchKernelEx(&cfg, prompt_attention_kernel<Q4>, a);
+    if (err != cudaSuccess || ctas < 2)
+        return err;
+    cfg.gridDim = dim3(ctas - 1, kJoinBlocks);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, prompt_join_kernel, a);
 }
 
 }  // namespace
