@@ -37,12 +37,11 @@ constexpr int kMaxCacheCtas = 1024;
 constexpr int kMaxPromptCtas = 160;
 constexpr int kPromptRows = 256;
 
-// A unit whose tiles several CTAs shared, left by the CTA whose range begins at the unit's first
-// cut (rows 0: nothing to join there).
+// The unit that a CTA's range begins with (b -1: it has none).  rows: where the begin is the first
+// cut of a unit whose tiles several CTAs share, its query rows, else 0.
 struct PromptJoin {
     int b, h, q0, row0, rows, pos0;
     int last;                             // the last CTA that has a part
-    int late;                             // the first part is its CTA's second one
 };
 
 // Fixed part of the workspace, at the buffer's end whatever the shape is, so that the

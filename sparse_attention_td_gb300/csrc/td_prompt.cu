@@ -39,6 +39,9 @@ static_assert(kUnitRows == 2 * kTile, "two row tiles");
 // A unit's begin and end cost as much as two tiles: it counts as so many more.  (Prompts of 1K-6K,
 // window 1024, ranges cut by tiles alone: 230 us with 10 units per CTA, 344 with 46.)
 constexpr int kUnitCost = 2;
+// A range's begin within so much of a unit's begin or end moves there: what a cut costs (another
+// begin and end, the join) is more than the SMs would differ by.  Units of up to twice that are whole.
+constexpr int kSnap = 6;
 constexpr int kLeastCost = 4;                    // of a CTA's range
 constexpr int kMostSlots = 5;
 // Ring of K and V tiles: 16-bit rows 5; 4-bit rows 4, and rings of the copy warps' coded rows.
@@ -76,7 +79,7 @@ struct Unit {
 // Where a CTA's range of tiles begins.
 struct Start {
     int b, block, h, at;     // request, block of query rows, KV head, cost of the unit that lies before
-    int64_t left;            // cost of the range; 0: none
+    long long begin, end;    // of the range, in the batch's cost
 };
 
 // Who arrives and who waits; a wait looks at a phase's parity, so each must come when
@@ -390,72 +393,104 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         if (lane == 31)
             x.sums[warp] = inc;
         if (tid == 0)
-            x.start.left = 0;
+            x.start.begin = x.start.end = 0;
         __syncthreads();
-        long long all = 0, at = inc - mine;
+        long long all = 0, at0 = inc - mine;
         for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp)
-                at += x.sums[i];
+                at0 += x.sums[i];
             all += x.sums[i];
         }
         per = max((all + gridDim.x - 1) / gridDim.x, (long long)kLeastCost);
-        const long long begin = blockIdx.x * per;
-        if (begin < all && at <= begin && begin < at + mine)
-            walk([&](const Request &r, int block, int tiles) {
-                const int cost = tiles + kUnitCost;
-                if (begin >= at + (long long)cost * a.Hkv) {
-                    at += (long long)cost * a.Hkv;
-                    return true;
-                }
-                const int off = (int)(begin - at);
-                x.start = Start{r.b, block, off / cost, off % cost, min((long long)per, all - begin)};
-                return false;
-            });
-        __syncthreads();
-        if (tid == 0 && blockIdx.x > 0) {
-            // The unit that this range's begin cuts, if it is the unit's first cut: the CTA before has
-            // the unit's first tile.
-            PromptJoin j{};
-            const Start w = x.start;
-            if (w.left > 0 && w.at > kUnitCost && w.at - per <= kUnitCost) {
-                const Unit u = unit_of(request(w.b), w.block, w.h);
-                j = PromptJoin{u.b, u.h, u.q0, u.row0, u.rows, u.pos0,
-                               (int)((begin - w.at + u.tiles + kUnitCost - 1) / per), w.at < per};
+        // Where the range begins and ends: the unit there, the place in it, moved to its begin or end
+        // where that is near.
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const long long target = (blockIdx.x + k) * per;
+            long long at = at0;
+            if (target < all && at <= target && target < at + mine)
+                walk([&](const Request &r, int block, int tiles) {
+                    const int cost = tiles + kUnitCost;
+                    if (target >= at + (long long)cost * a.Hkv) {
+                        at += (long long)cost * a.Hkv;
+                        return true;
+                    }
+                    const int h = (int)(target - at) / cost, in = (int)(target - at) - h * cost;
+                    const int to = in <= kSnap ? 0 : cost - in <= kSnap ? cost : in;
+                    if (k == 0) {
+                        x.start.b = r.b;
+                        x.start.block = block;
+                        x.start.h = h;
+                        x.start.at = to;
+                        x.start.begin = target - in + to;
+                    } else {
+                        x.start.end = target - in + to;
+                    }
+                    return false;
+                });
+            else if (target >= all && tid == 0) {
+                if (k == 0)
+                    x.start.begin = all;
+                else
+                    x.start.end = all;
             }
-            a.ws->join[blockIdx.x] = j;
         }
+        __syncthreads();
     }
+    // The unit behind a place's.
+    auto next_unit_of = [&](Start &w, Request &r) {
+        w.at = 0;
+        if (++w.h < a.Hkv)
+            return;
+        w.h = 0;
+        if (++w.block < r.blocks)
+            return;
+        w.block = 0;
+        do
+            r = request(r.b + 1);
+        while (r.blocks == 0 && r.b + 1 < a.B);
+        w.b = r.b;
+    };
     // Publishes the CTA's units (the scheduler, as far ahead as there are entries).
     auto publish_all = [&] {
         Start w = x.start;
-        Request r = w.left > 0 ? request(w.b) : Request{};
+        long long left = w.end - w.begin;
+        Request r{};
+        PromptJoin join{-1};
+        if (left > 0) {
+            r = request(w.b);
+            const Unit u = unit_of(r, w.block, w.h);
+            if (w.at == u.tiles + kUnitCost) {
+                next_unit_of(w, r);
+                const Unit v = unit_of(r, w.block, w.h);
+                join = PromptJoin{v.b, v.h, v.q0, v.row0, 0, v.pos0, 0};
+            } else {
+                // Is this the first cut of the unit?  The last CTA that has a part of it begins at
+                // least kSnap + 1 before its end.
+                const bool cut = w.at > 0 && w.at - per <= kSnap;
+                join = PromptJoin{u.b, u.h, u.q0, u.row0, cut ? u.rows : 0, u.pos0,
+                                  (int)((w.begin - w.at + u.tiles + kUnitCost - kSnap - 1) / per)};
+            }
+        }
+        if (lane == 0)
+            a.ws->join[blockIdx.x] = join;
 #pragma unroll 1
         for (uint32_t n = 0;; ++n) {
             Unit u;
             u.tiles = -1;
-            if (w.left > 0) {
+            if (left > 0) {
                 // Of cost at .. end of the unit; its first kUnitCost are no tiles.
                 u = unit_of(r, w.block, w.h);
                 const int all = u.tiles;
-                const int end = (int)min((int64_t)(all + kUnitCost), w.at + w.left);
+                const int end = (int)min((long long)(all + kUnitCost), w.at + left);
                 u.tile0 = max(w.at - kUnitCost, 0);
-                u.tiles = max(end - kUnitCost, 0) - u.tile0;
-                if (u.tiles == 0)
-                    u.tiles = -1;                 // (the range ends before the unit's first tile)
+                u.tiles = end - kUnitCost - u.tile0;
                 u.steps = min(u.steps - 2 * u.tile0, 2 * u.tiles);
                 if (u.tiles < all)
                     u.part = 2 * blockIdx.x + (n > 0);
-                w.left -= end - w.at;
-                w.at = 0;
-                if (w.left > 0 && ++w.h == a.Hkv) {
-                    w.h = 0;
-                    if (++w.block == r.blocks) {
-                        w.block = 0;
-                        do
-                            r = request(r.b + 1);
-                        while (r.blocks == 0 && r.b + 1 < a.B);
-                    }
-                }
+                left -= end - w.at;
+                if (left > 0)
+                    next_unit_of(w, r);
             }
             if (n >= kUnitRing)
                 ok = warp_wait(&x.unit_free[n % kUnitRing], n / kUnitRing - 1);
@@ -1017,8 +1052,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const __gr
     pdl_wait();
     const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
     const PromptJoin j = a.ws->join[c];
-    // part s: CTA c - 1 + s's; its second one where the unit begins inside its range
-    auto part_of = [&](int s) { return 2 * (c - 1 + s) + (s == 0 && j.late ? 1 : 0); };
+    if (j.rows == 0)
+        return;
+    // part s: CTA c - 1 + s's; its second one where its range begins with another unit
+    const PromptJoin before = a.ws->join[c - 1];
+    const int late = before.b != j.b || before.h != j.h || before.row0 != j.row0;
+    auto part_of = [&](int s) { return 2 * (c - 1 + s) + (s == 0 ? late : 0); };
     const int parts = j.last - c + 2;
     for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < j.rows; r += kJoinBlocks * kJoinWarps) {
         constexpr int kAhead = 4;
