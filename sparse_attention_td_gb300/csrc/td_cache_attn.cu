@@ -25,6 +25,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "td_attn_common.cuh"
 #include "td_cache.h"
 
@@ -78,13 +80,6 @@ __device__ __forceinline__ uint4 load16(const void *p, bool there = true)
     return r;
 }
 
-__device__ __forceinline__ uint2 load8(const void *p)
-{
-    uint2 r;
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
-}
-
 // Four codes' worth of halves: two bytes of codes (those of byte `at` and at + 1 of x) as
 // two pairs of fp16 values, the low half of a byte first.
 __device__ __forceinline__ void decode2(uint32_t x, int at, uint32_t &lo, uint32_t &hi)
@@ -129,6 +124,13 @@ __device__ __forceinline__ uint32_t pack_b16(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
@@ -204,30 +206,72 @@ template <> struct Tokens<false> {
     __device__ static int qdim(int c, int w) { return 8 * (c + 4 * (w >> 2)) + 2 * (w & 3); }   // of q word w
 };
 
-// 4 bits.  K: dims 32 c .. + 31, two scales; V: dims 16 r .. + 15, one scale.
+// 4 bits.  K: dims 32 c .. + 31, two scales; V: dims 16 r .. + 15, one scale.  The rows of 32
+// tokens come through shared memory (a warp's own ring): K codes, 64 bytes a token; V codes, whose
+// 16-byte pieces q of token t lie at place (t & 1) * 4 + q ^ (t / 2 & 3) * 2 of their two tokens'
+// 128 bytes, so that a half warp's loads fall into all banks; the tokens' 16 bytes of scales.
+constexpr int kStageTokens = 32;
+constexpr int kStageV = kStageTokens * kCodeBytes, kStageScales = 2 * kStageV;
+constexpr int kStageValid = kStageScales + kStageTokens * kScaleBytes;      // which tokens there are
+constexpr int kStageBytes = kStageValid + 16;
+constexpr int kStages = 4;
+
+__device__ __forceinline__ uint32_t v_place(int t, int q) { return (t >> 1) * 128 + ((((t & 1) << 2) + q) ^ ((t >> 1 & 3) << 1)) * 16; }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
 template <> struct Tokens<true> {
-    uint4 k[2];
+    uint32_t k[2][4];
     uint2 v[4];
     uint32_t ks[2], vs[4];
 
-    __device__ void load_k(const RowsArgs &a, int r, int c, const int (&row)[2])
+    // The rows of a stage: lane's own token's is `row`, -1: none (zeros).
+    __device__ static void fill(const RowsArgs &a, uint32_t stage, int row, int lane)
+    {
+        const int q = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 8 * i + (lane >> 2), from = __shfl_sync(kFull, row, t);
+            const size_t at = (size_t)(uint32_t)max(from, 0) * kCodeBytes + 16 * q;
+            copy16(stage + t * kCodeBytes + 16 * q, a.k + at, from >= 0);
+            copy16(stage + kStageV + v_place(t, q), a.v + at, from >= 0);
+        }
+        copy16(stage + kStageScales + lane * kScaleBytes, a.scales + (size_t)(uint32_t)max(row, 0) * kScaleBytes, row >= 0);
+        const uint32_t there = __ballot_sync(kFull, row >= 0);
+        if (lane == 0)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + kStageValid), "r"(there) : "memory");
+    }
+    __device__ void load_k(uint32_t stage, int u, int r, int c)
     {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const size_t at = (uint32_t)max(row[t], 0);
-            k[t] = load16(a.k + at * kCodeBytes + 16 * c);
-            ks[t] = *reinterpret_cast<const uint16_t *>(a.scales + at * kScaleBytes + 2 * c);
+            const int tok = 16 * u + 8 * t + r;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(k[t][0]), "=r"(k[t][1]), "=r"(k[t][2]), "=r"(k[t][3])
+                         : "r"(stage + tok * kCodeBytes + 16 * c)
+                         : "memory");
+            asm volatile("{\n\t.reg .b16 t;\n\tld.shared.b16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}"
+                         : "=r"(ks[t])
+                         : "r"(stage + kStageScales + tok * kScaleBytes + 2 * c)
+                         : "memory");
         }
     }
-    __device__ void load_v(const RowsArgs &a, int r, int c, const int (&row)[4])
+    __device__ void load_v(uint32_t stage, int u, int r, int c)
     {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const size_t at = (uint32_t)max(row[t], 0);
-            v[t] = load8(a.v + at * kCodeBytes + 8 * r);
-            vs[t] = a.scales[at * kScaleBytes + 8 + r];
-            if (row[t] < 0)
-                vs[t] = 0;         // P of such a token is zero; V has to be finite
+            const int tok = 16 * u + 2 * c + (t & 1) + 8 * (t >> 1);
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(v[t].x), "=r"(v[t].y)
+                         : "r"(stage + kStageV + v_place(tok, r >> 1) + 8 * (r & 1))
+                         : "memory");
+            asm volatile("ld.shared.u8 %0, [%1];"
+                         : "=r"(vs[t])
+                         : "r"(stage + kStageScales + tok * kScaleBytes + 8 + r)
+                         : "memory");
         }
     }
     __device__ void s(float (&d)[4], const uint32_t (&q)[16]) const
@@ -241,8 +285,7 @@ template <> struct Tokens<true> {
             uint32_t x[2][2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const uint32_t w = (j >> 1) == 0 ? k[t].x : (j >> 1) == 1 ? k[t].y : (j >> 1) == 2 ? k[t].z : k[t].w;
-                decode2(w, 2 * (j & 1), x[t][0], x[t][1]);
+                decode2(k[t][j >> 1], 2 * (j & 1), x[t][0], x[t][1]);
                 x[t][0] = mul2(x[t][0], sc[t][j >> 2]);
                 x[t][1] = mul2(x[t][1], sc[t][j >> 2]);
             }
@@ -299,7 +342,7 @@ template <int MODE, int GT> __device__ __forceinline__ Seen seen_of(const CacheA
 }
 
 // MODE 0: a window or everything; 1: an index set; 2: everything, the logits are kept.
-// U: 16-token blocks that a warp takes at a time.
+// U: 16-token blocks that a warp takes at a time (4 bits: a stage's two).
 template <bool Q4, int MODE, int U, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const __grid_constant__ CacheAttnArgs a)
 {
@@ -308,11 +351,15 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
     __shared__ int sm_sums[kWarps];
     __shared__ int sm_start[3];                   // b, KV head, group that the CTA's range starts at
     __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
-    __shared__ __align__(16) float sm_o[kWarps][kHeads][kHeadDim];
     __shared__ int sm_last;
+    // The warps' outputs; over 4-bit rows in their rings, which are empty by then.
+    extern __shared__ __align__(128) unsigned char sm_raw[];
+    constexpr int kPerWarp = Q4 ? kStages * kStageBytes : kHeads * kHeadDim * (int)sizeof(float);
+    auto sm_o = [&](int w, int hd) { return reinterpret_cast<float *>(sm_raw + w * kPerWarp) + hd * kHeadDim; };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm_raw) + warp * kPerWarp;
     pdl_wait();
 
     // ---- the CTA's range: requests in equal runs per thread, prefix sums
@@ -401,12 +448,13 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 flags |= kFlagPageOutOfRange;
             return row;
         };
-        Block blk[U];
+        Block blk[Q4 ? 1 : U];
         auto load_k = [&](int row) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int rows[2] = {__shfl_sync(kFull, row, 16 * u + r), __shfl_sync(kFull, row, 16 * u + 8 + r)};
-                blk[u].load_k(a.rows, r, c, rows);
+                if constexpr (!Q4)
+                    blk[u].load_k(a.rows, r, c, rows);
             }
         };
         auto load_v = [&](int row) {
@@ -415,15 +463,42 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 const int at = 16 * u + 2 * c;
                 const int rows[4] = {__shfl_sync(kFull, row, at), __shfl_sync(kFull, row, at + 1),
                                      __shfl_sync(kFull, row, at + 8), __shfl_sync(kFull, row, at + 9)};
-                blk[u].load_v(a.rows, r, c, rows);
+                if constexpr (!Q4)
+                    blk[u].load_v(a.rows, r, c, rows);
             }
         };
 
+        // Positions, pages and rows of the warp's next groups: row is that of group i (16 bits), or
+        // of the next group to fill a stage with (4 bits).
         int i = warp;
         int p0 = checked(position(i)), p1 = checked(position(i + kWarps)), p2 = position(i + 2 * kWarps);
         int pg0 = page(p0), pg1 = page(p1);
-        int row = find(p0, pg0);
-        if (i < count) {
+        int row = find(p0, pg0), ahead = i;           // ahead: the group whose row `row` is
+        auto next_row = [&] {
+            p2 = checked(p2);
+            const int pg2 = page(p2), p3 = position(ahead + 3 * kWarps);
+            const int next = find(p1, pg1);
+            p1 = p2;
+            pg1 = pg2;
+            p2 = p3;
+            ahead += kWarps;
+            return next;
+        };
+        uint32_t stage = ring;                        // 4 bits: the stage of group i
+        auto fill = [&](uint32_t to) {                // with the rows of group `ahead`
+            if constexpr (Q4) {
+                if (ahead < count) {
+                    Block::fill(a.rows, to, row, lane);
+                    row = next_row();
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
+        };
+        if constexpr (Q4) {
+#pragma unroll 1
+            for (int s = 0; s < kStages - 1; ++s)
+                fill(ring + s * kStageBytes);
+        } else if (i < count) {
             load_k(row);
             load_v(row);
         }
@@ -470,20 +545,33 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 o[k][e] = 0.0f;
 
         for (; i < count; i += kWarps) {
-            const uint32_t there = __ballot_sync(kFull, row >= 0);
-            p2 = checked(p2);
-            const int pg2 = page(p2), p3 = position(i + 3 * kWarps);
-            const int next = find(p1, pg1);
+            uint32_t there;
+            int next = 0;
+            if constexpr (Q4) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+                __syncwarp();                         // (every lane's copies; and the stage before has been read)
+                fill(stage == ring ? ring + (kStages - 1) * kStageBytes : stage - kStageBytes);
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(there) : "r"(stage + kStageValid) : "memory");
+            } else {
+                there = __ballot_sync(kFull, row >= 0);
+                next = next_row();
+            }
             float s[U][4];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     s[u][e] = 0.0f;
-                blk[u].s(s[u], q);
+                if constexpr (Q4) {
+                    blk[0].load_k(stage, u, r, c);
+                    blk[0].s(s[u], q);
+                } else {
+                    blk[u].s(s[u], q);
+                }
             }
-            if (i + kWarps < count)
-                load_k(next);
+            if constexpr (!Q4)
+                if (i + kWarps < count)
+                    load_k(next);
             // s[u][2 t + e]: token 16 u + 8 t + r, head 2c + e
             float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
@@ -541,17 +629,27 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        p[t][e] = exp2f(s[u][2 * t + e] - ref[e]);
+                        p[t][e] = ex2(s[u][2 * t + e] - ref[e]);
                         l[e] += p[t][e];
                     }
-                blk[u].pv(o, p);
+                if constexpr (Q4) {
+                    blk[0].load_v(stage, u, r, c);
+                    blk[0].pv(o, p);
+                } else {
+                    blk[u].pv(o, p);
+                }
             }
-            if (i + kWarps < count)
-                load_v(next);
-            row = next;
-            p1 = p2;
-            pg1 = pg2;
-            p2 = p3;
+            if constexpr (Q4) {
+                stage = stage == ring + (kStages - 1) * kStageBytes ? ring : stage + kStageBytes;
+            } else {
+                if (i + kWarps < count)
+                    load_v(next);
+                row = next;
+            }
+        }
+        if constexpr (Q4) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
         }
 
         // ---- the segment's result: the warps' sums joined in shared memory
@@ -568,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<float2 *>(&sm_o[warp][hd][Block::dim(k, r)]) = make_float2(o[k][e], o[k][e + 2]);
+                    *reinterpret_cast<float2 *>(sm_o(warp, hd) + Block::dim(k, r)) = make_float2(o[k][e], o[k][e + 2]);
             }
         }
         __syncthreads();
@@ -589,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
             for (int w = 0; w < kWarps; ++w) {
                 const float f = weight(sm_m[w][hd], M);     // (without a maximum: zeros, or NaN)
                 L += sm_l[w][hd] * f;
-                O += sm_o[w][hd][tid] * f;
+                O += sm_o(w, hd)[tid] * f;
             }
             if (whole) {
                 a.out[(row0 + hd) * kHeadDim + tid] = f32_to_bf16_rn(L == 0.0f ? 0.0f : O / L);
@@ -685,9 +783,28 @@ cudaError_t launch(const CacheAttnArgs &a, int sms, cudaStream_t stream)
         ctas = (most + kWarps - 1) / kWarps;
     if (ctas > kMaxCacheCtas)
         ctas = kMaxCacheCtas;
+    constexpr size_t smem = (size_t)kWarps * (Q4 ? kStages * kStageBytes : kHeads * kHeadDim * sizeof(float));
+    if (smem > 48 * 1024) {
+        static std::mutex mu;
+        static bool ready[64] = {false};
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
+        if (err != cudaSuccess)
+            return err;
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev < 0 || dev >= 64 || !ready[dev]) {
+            err = cudaFuncSetAttribute(cache_attention_kernel<Q4, MODE, U, CTAS>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (err != cudaSuccess)
+                return err;
+            if (dev >= 0 && dev < 64)
+                ready[dev] = true;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -746,7 +863,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, int sms, cudaStream_t
     if (a.logits)
         return launch<false, 2, 1, 3>(a, sms, stream);
     if (a.rows.scales)
-        return a.idx ? launch<true, 1, 2, 4>(a, sms, stream) : launch<true, 0, 2, 4>(a, sms, stream);
+        return a.idx ? launch<true, 1, 2, 3>(a, sms, stream) : launch<true, 0, 2, 3>(a, sms, stream);
     return launch<false, 0, 1, 3>(a, sms, stream);
 }
 
