@@ -35,66 +35,97 @@ cudaError_t launch_behind(void (*kernel)(Args, More...), long long grid, int thr
 // where the result is that short (one step from a rounded reciprocal: the remainder
 // x - q s is exact in an fma).  The same holds for the largest value / 6 and the borders of e4m3.
 constexpr int kQuantThreads = 256;
+constexpr int kQuantPer = 2;                  // blocks of 16 values a thread has at a time
+constexpr int kQuantBlocks = kHeadDim / 16;   // of a row
 
 __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4AppendArgs a)
 {
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int kBlocks = kHeadDim / 16;
-    const int per = a.Hkv * kBlocks;              // blocks of one token's K (or V)
-    const long long total = (long long)a.tokens * 2 * per;
-    const long long limit = (long long)a.num_pages * a.page_size;
-    for (long long e = (long long)blockIdx.x * kQuantThreads + threadIdx.x; e < total;
-         e += (long long)gridDim.x * kQuantThreads) {
-        const int i = (int)(e / (2 * per));
-        int j = (int)(e - (long long)i * 2 * per);
-        const bool isv = j >= per;
-        j -= isv ? per : 0;
-        const int slot = a.slots[i];
-        if (slot < 0 || slot >= limit)
-            continue;
-        const uint4 *src = reinterpret_cast<const uint4 *>((isv ? a.v_new : a.k_new) + (size_t)i * a.new_stride + j * 16);
-        const uint4 y0 = src[0], y1 = src[1];
-        const uint32_t x[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-        uint32_t top = 0;
+    const uint32_t per = a.Hkv * kQuantBlocks;    // blocks of one token's K (or V)
+    const uint32_t total = (uint32_t)a.tokens * 2 * per;        // (below 2^31)
+    const uint32_t limit = (uint32_t)a.num_pages * a.page_size;
+    const uint32_t step = gridDim.x * kQuantThreads;
+    for (uint32_t e0 = blockIdx.x * kQuantThreads + threadIdx.x; e0 < total; e0 += kQuantPer * step) {
+        uint4 y[kQuantPer][2];
+        uint8_t *codes_at[kQuantPer], *scale_at[kQuantPer];     // null: nothing to write
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            top = __vmaxu2(top, x[k] & 0x7fff7fffu);
-        top = max(top & 0xffffu, top >> 16);
-        const float amax = __uint_as_float(top << 16);
-        uint32_t scale;                            // e4m3, saturated at 448
-        asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
-            : "=r"(scale)
-            : "f"(0.0f), "f"(__fdiv_rn(amax, 6.0f)));
-        uint32_t half;                             // its value, exact in fp16
-        asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(half) : "r"(scale));
-        float s;
-        asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.f32.f16 %0, t;\n\t}" : "=f"(s) : "r"(half));
-        uint32_t codes[2] = {0, 0};
-        if (top > 0x7f80u) {
-            scale = 0x7f;                          // a value that is not a number: none of the 16 is
-        } else if (s > 0.0f) {
-            const float inv = __frcp_rn(s), most = 8.0f * s;       // (beyond 6 s the code saturates)
-            auto quotient = [&](uint32_t bits) {
-                const float v = fmaxf(fminf(__uint_as_float(bits), most), -most);
-                const float q = v * inv;
-                return copysignf(fmaf(fmaf(-q, s, v), inv, q), v);       // (-0 keeps its sign)
-            };
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float lo = quotient(x[k] << 16), hi = quotient(x[k] & 0xffff0000u);
-                uint32_t two;
-                asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, 0, 0, 0};\n\t}"
-                    : "=r"(two)
-                    : "f"(hi), "f"(lo));
-                codes[k >> 2] |= two << 8 * (k & 3);
-            }
+        for (int p = 0; p < kQuantPer; ++p) {
+            const uint32_t e = e0 + p * step;
+            codes_at[p] = scale_at[p] = nullptr;
+            if (e >= total)
+                continue;
+            const uint32_t i = e / (2 * per);
+            uint32_t j = e - i * 2 * per;
+            const bool isv = j >= per;
+            j -= isv ? per : 0;
+            const uint32_t slot = a.slots[i];                   // (negative ones lie beyond the limit)
+            if (slot >= limit)
+                continue;
+            const uint4 *src = reinterpret_cast<const uint4 *>((isv ? a.v_new : a.k_new) + (size_t)i * a.new_stride + j * 16);
+            y[p][0] = src[0];
+            y[p][1] = src[1];
+            const uint32_t page = slot / a.page_size, r = slot - page * a.page_size, block = j % kQuantBlocks;
+            const size_t row = ((size_t)page * a.Hkv + j / kQuantBlocks) * a.page_size + r;
+            codes_at[p] = (isv ? a.v : a.k) + row * kCodeBytes + block * 8;
+            scale_at[p] = a.scales + row * kScaleBytes + (isv ? kQuantBlocks : 0) + block;
         }
-        const int page = slot / a.page_size, r = slot % a.page_size;
-        const size_t row = ((size_t)page * a.Hkv + j / kBlocks) * a.page_size + r;
-        const int block = j % kBlocks;
-        *reinterpret_cast<uint2 *>((isv ? a.v : a.k) + row * kCodeBytes + block * 8) = make_uint2(codes[0], codes[1]);
-        a.scales[row * kScaleBytes + (isv ? kBlocks : 0) + block] = (uint8_t)scale;
+#pragma unroll
+        for (int p = 0; p < kQuantPer; ++p) {
+            if (!codes_at[p])
+                continue;
+            const uint32_t x[8] = {y[p][0].x, y[p][0].y, y[p][0].z, y[p][0].w, y[p][1].x, y[p][1].y, y[p][1].z, y[p][1].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                top = __vmaxu2(top, x[k] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
+            uint32_t scale;                        // e4m3, saturated at 448
+            float s;                               // its value (exact in fp16 on the way)
+            asm("{\n\t.reg .b16 t, u, v;\n\t.reg .b32 w;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 t, %2, %3;\n\tcvt.u32.u16 %0, t;\n\t"
+                "cvt.rn.f16x2.e4m3x2 w, t;\n\tmov.b32 {u, v}, w;\n\tcvt.f32.f16 %1, u;\n\t}"
+                : "=r"(scale), "=f"(s)
+                : "f"(0.0f), "f"(__fdiv_rn(__uint_as_float(top << 16), 6.0f)));
+            uint2 codes = make_uint2(0, 0);
+            if (top > 0x7f80u) {
+                scale = 0x7f;                      // a value that is not a number: none of the 16 is
+            } else if (s > 0.0f) {
+                const float inv = __frcp_rn(s);
+                // Beyond 6 s the code saturates; 8 s stands for what is larger (only 16 values of
+                // which the largest is beyond 448 * 8 have any, as a smaller scale is at
+                // least half of the largest / 6).
+                const float most = 8.0f * s;
+                const bool clamp = __uint_as_float(top << 16) > 8.0f * 448.0f;
+                // (the remainder's sign this way round, so that -0 stays -0)
+                auto quotient = [&](uint32_t bits) {
+                    float v = __uint_as_float(bits);
+                    if (clamp)
+                        v = fmaxf(fminf(v, most), -most);
+                    const float q = v * inv;
+                    return fmaf(-fmaf(q, s, -v), inv, q);
+                };
+                float q[16];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    q[2 * k] = quotient(x[k] << 16);
+                    q[2 * k + 1] = quotient(x[k] & 0xffff0000u);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float *z = q + 8 * h;
+                    uint32_t &out = h ? codes.y : codes.x;
+                    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+                        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+                        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+                        "mov.b32 %0, {a, b, c, d};\n\t}"
+                        : "=r"(out)
+                        : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
+                }
+            }
+            *reinterpret_cast<uint2 *>(codes_at[p]) = codes;
+            *scale_at[p] = (uint8_t)scale;
+        }
     }
 }
 
@@ -150,10 +181,20 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             for (int i = tid; i < bins; i += kSelectThreads)
                 hist[i] = 0;
             __syncthreads();
-            for (int i = c0 + tid; i < c1; i += kSelectThreads) {
-                const uint32_t k = weight_key(w[i]);
-                if ((k & mask) == key)
-                    atomicAdd(&hist[k >> shift & (bins - 1)], 1u);
+            constexpr int kAhead = 8;
+            for (int i0 = c0 + tid; i0 < c1; i0 += kAhead * kSelectThreads) {
+                float v[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (i0 + k * kSelectThreads < c1)
+                        v[k] = w[i0 + k * kSelectThreads];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (i0 + k * kSelectThreads < c1) {
+                        const uint32_t y = weight_key(v[k]);
+                        if ((y & mask) == key)
+                            atomicAdd(&hist[y >> shift & (bins - 1)], 1u);
+                    }
             }
             __syncthreads();
             // Counts from the highest digit down: a thread has a run of bins.
@@ -245,13 +286,16 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 // read lies at or behind the row that it goes to: a CTA that takes its rows in order, in
 // chunks that are read before they are written, overwrites no row that is still to be read.
 // A CTA has K or V of one (request, KV head), whole rows or a slice of each, where there are
-// few; between two caches the rows are also cut into runs.  The next chunk is read before
-// this one is written.
+// few; between two caches the rows are also cut into runs.  Cache rows are looked up
+// kMoveList at a time; a chunk is read while the one before is written.
 constexpr int kMoveThreads = 256;
 constexpr int kMovePer = 4;
+constexpr int kMoveList = 1024;
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int log_slices, int runs)
+__global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const EvictArgs a, int log_slices, int runs)
 {
+    __shared__ int sm_from[kMoveList], sm_to[kMoveList];        // cache rows; to -1: nothing to move
+    __shared__ int sm_first;
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
@@ -263,58 +307,89 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     id >>= log_slices;
     const bool isv = id & 1;
     const int unit = id >> 1, b = unit / a.Hkv, h = unit % a.Hkv;
-    uint32_t bad = 0;
+    uint32_t bad = 0, flags = 0;
     const int n = seq_len_of(a.seq_lens, b, a.Nmax, bad);
     const int count = min(n, a.budget);
     if (a.place && n <= a.budget)
         return;
     const int lanes = 16 >> log_slices;            // of a row (or its slice), 16 bytes each
-    const int rows = kMoveThreads / lanes * kMovePer;           // of a chunk
+    const int step = kMoveThreads / lanes, rows = step * kMovePer;      // rows of a chunk
     const int chunks = (count + rows - 1) / rows;
-    const int first = (int)((long long)chunks * run / runs) * rows, end = min(count, (int)((long long)chunks * (run + 1) / runs) * rows);
+    const int first = (int)((long long)chunks * run / runs) * rows;
+    const int end = min(count, (int)((long long)chunks * (run + 1) / runs) * rows);
     const int32_t *kept = a.kept + (size_t)unit * a.budget;
-    const uint8_t *from = isv ? a.from.v : a.from.k;
-    uint8_t *to = (uint8_t *)(isv ? a.to_v : a.to_k);
     const int off = (slice * lanes + tid % lanes) * 16;
-    uint32_t flags = 0;
-    uint4 x[kMovePer], y[kMovePer];
-    int to_row[kMovePer], to_next[kMovePer];       // -1: nothing to write
-    auto read = [&](int base, uint4 (&v)[kMovePer], int (&dst)[kMovePer]) {
-        int p[kMovePer];
+    const uint8_t *from = (isv ? a.from.v : a.from.k) + off;
+    uint8_t *to = (uint8_t *)(isv ? a.to_v : a.to_k) + off;
+    for (int base = first; base < end; base += kMoveList) {
+        const int list = min(kMoveList, end - base);
+        if (tid == 0)
+            sm_first = list;
+        __syncthreads();                           // (the list before has been read)
+        constexpr int kFind = kMoveList / kMoveThreads;
+        int p[kFind], pages[kFind], to_pages[kFind];
 #pragma unroll
-        for (int k = 0; k < kMovePer; ++k) {
-            const int i = base + tid / lanes + k * (kMoveThreads / lanes);
-            p[k] = i < end ? kept[i] : -1;
+        for (int k = 0; k < kFind; ++k) {
+            const int i = tid + k * kMoveThreads;
+            p[k] = i < list ? kept[base + i] : -1;
         }
 #pragma unroll
-        for (int k = 0; k < kMovePer; ++k) {
-            const int i = base + tid / lanes + k * (kMoveThreads / lanes);
-            dst[k] = -1;
-            if (p[k] < 0 || p[k] >= n || (a.place && p[k] == i))
-                continue;
-            const int src = row_of(a.from, a.Hkv, h, p[k], page_of(a.from, b, p[k]));
-            dst[k] = row_of(a.to, a.Hkv, h, i, page_of(a.to, b, i));
-            if (src < 0 || dst[k] < 0) {
-                flags |= kFlagPageOutOfRange;
-                dst[k] = -1;
-                continue;
+        for (int k = 0; k < kFind; ++k) {
+            const int i = base + tid + k * kMoveThreads;
+            if (p[k] >= n || (a.place && p[k] == i))
+                p[k] = -1;
+            pages[k] = p[k] >= 0 ? page_of(a.from, b, p[k]) : 0;
+            to_pages[k] = p[k] >= 0 ? page_of(a.to, b, i) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kFind; ++k) {
+            const int i = tid + k * kMoveThreads;
+            int f = 0, t = -1;
+            if (p[k] >= 0) {
+                f = row_of(a.from, a.Hkv, h, p[k], pages[k]);
+                t = row_of(a.to, a.Hkv, h, base + i, to_pages[k]);
+                if (f < 0 || t < 0) {
+                    flags |= kFlagPageOutOfRange;
+                    t = -1;
+                } else {
+                    atomicMin(&sm_first, i);
+                }
             }
-            v[k] = __ldcg(reinterpret_cast<const uint4 *>(from + (size_t)src * (kHeadDim * 2) + off));
+            sm_from[i] = f;
+            sm_to[i] = t;
         }
-    };
-    if (first < end)
-        read(first, x, to_row);
-    for (int base = first; base < end; base += rows) {
-        if (base + rows < end)
-            read(base + rows, y, to_next);
-        if (a.place)
-            __syncthreads();                       // every row of this chunk has been read
+        __syncthreads();
+        uint4 x[2][kMovePer];
+        int row[2][kMovePer];                      // -1: nothing to write
+        auto read = [&](int i0, uint4 (&v)[kMovePer], int (&dst)[kMovePer]) {
 #pragma unroll
-        for (int k = 0; k < kMovePer; ++k) {
-            if (to_row[k] >= 0)
-                *reinterpret_cast<uint4 *>(to + (size_t)to_row[k] * (kHeadDim * 2) + off) = x[k];
-            x[k] = y[k];
-            to_row[k] = to_next[k];
+            for (int k = 0; k < kMovePer; ++k) {
+                const int i = i0 + tid / lanes + k * step;
+                dst[k] = i < list ? sm_to[i] : -1;
+                if (dst[k] >= 0)
+                    v[k] = __ldcg(reinterpret_cast<const uint4 *>(from + (size_t)sm_from[i] * (kHeadDim * 2)));
+            }
+        };
+        auto write = [&](const uint4 (&v)[kMovePer], const int (&dst)[kMovePer]) {
+            if (a.place)
+                __syncthreads();                   // every row of this chunk has been read
+#pragma unroll
+            for (int k = 0; k < kMovePer; ++k)
+                if (dst[k] >= 0)
+                    *reinterpret_cast<uint4 *>(to + (size_t)dst[k] * (kHeadDim * 2)) = v[k];
+        };
+        int i0 = sm_first / rows * rows;
+        if (i0 < list)
+            read(i0, x[0], row[0]);
+        for (; i0 < list; i0 += 2 * rows) {
+            if (i0 + rows < list)
+                read(i0 + rows, x[1], row[1]);
+            write(x[0], row[0]);
+            if (i0 + rows >= list)
+                break;
+            if (i0 + 2 * rows < list)
+                read(i0 + 2 * rows, x[0], row[0]);
+            write(x[1], row[1]);
         }
     }
     if (flags)
@@ -323,14 +398,26 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 
 }  // namespace
 
-cudaError_t launch_q4_append(const Q4AppendArgs &a, cudaStream_t stream)
+cudaError_t launch_q4_append(const Q4AppendArgs &args, cudaStream_t stream)
 {
-    const long long total = (long long)a.tokens * 2 * a.Hkv * (kHeadDim / 16);
+    const long long per = 2ll * args.Hkv * kQuantBlocks;        // blocks of a token
     const long long most = (long long)host_sm_count() * 8;
-    long long grid = (total + kQuantThreads - 1) / kQuantThreads;
-    if (grid > most)
-        grid = most;
-    return launch_behind(q4_append_kernel, grid, kQuantThreads, stream, a);
+    // (blocks are counted in 31 bits)
+    const int piece = (int)((1ll << 30) / per) > 0 ? (int)((1ll << 30) / per) : 1;
+    for (int t = 0; t < args.tokens; t += piece) {
+        Q4AppendArgs a = args;
+        a.k_new += (size_t)t * a.new_stride;
+        a.v_new += (size_t)t * a.new_stride;
+        a.slots += t;
+        a.tokens = args.tokens - t < piece ? args.tokens - t : piece;
+        long long grid = (a.tokens * per + kQuantThreads - 1) / kQuantThreads;
+        if (grid > most)
+            grid = most;
+        const cudaError_t err = launch_behind(q4_append_kernel, grid, kQuantThreads, stream, a);
+        if (err != cudaSuccess)
+            return err;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream)
