@@ -214,7 +214,7 @@ constexpr int kStageTokens = 32;
 constexpr int kStageV = kStageTokens * kCodeBytes, kStageScales = 2 * kStageV;
 constexpr int kStageValid = kStageScales + kStageTokens * kScaleBytes;      // which tokens there are
 constexpr int kStageBytes = kStageValid + 16;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 
 __device__ __forceinline__ uint32_t v_place(int t, int q) { return (t >> 1) * 128 + ((((t & 1) << 2) + q) ^ ((t >> 1 & 3) << 1)) * 16; }
 
@@ -368,9 +368,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
     {
         const int run = (a.B + kThreads - 1) / kThreads;
         const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
-        int mine = 0;
-        for (int b = b0; b < b1; ++b)
-            mine += seen_of<MODE, GT>(a, b, bad).groups * a.Hkv;
+        int mine = 0, last = 0;                   // groups of a KV head: all requests', the last one's
+        for (int b = b0; b < b1; ++b) {
+            last = seen_of<MODE, GT>(a, b, bad).groups;
+            mine += last * a.Hkv;
+        }
         if (bad && blockIdx.x == 0)
             atomicOr(a.status, bad);
         bad = 0;
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
         const int64_t start = (int64_t)blockIdx.x * per;
         if (start < total && at <= start && start < at + mine) {
             for (int b = b0; b < b1; ++b) {
-                const int g = seen_of<MODE, GT>(a, b, bad).groups;
+                const int g = run == 1 ? last : seen_of<MODE, GT>(a, b, bad).groups;
                 if (start < at + (int64_t)g * a.Hkv) {
                     sm_start[0] = b;
                     sm_start[1] = (int)(start - at) / g;
@@ -721,36 +723,51 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                     a.ws->tickets[c0] = 0;
                 // CTA c0's part is its second one where the unit starts inside its range.
                 const int late = (int64_t)c0 * per < u0 ? 1 : 0;
-                for (int hd = 0; hd < a.G; ++hd) {
-                    float M = -CUDART_INF_F, L = 0.0f, O = 0.0f;
-                    constexpr int kAhead = 8;
+                // A warp per head: 20 parts of 4 heads take two trips to memory, not ten.
+                for (int hd = warp; hd < a.G; hd += kWarps) {
+                    float M = -CUDART_INF_F, L = 0.0f;
+                    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    constexpr int kAhead = 12;
                     for (int s0 = c0; s0 <= c1; s0 += kAhead) {
-                        float ms[kAhead], ls[kAhead], os[kAhead], mn = M;
+                        float ms[kAhead], ls[kAhead], mn = M;
+                        float4 os[kAhead];
 #pragma unroll
                         for (int k = 0; k < kAhead; ++k) {
                             ms[k] = -CUDART_INF_F;
-                            ls[k] = os[k] = 0.0f;
+                            ls[k] = 0.0f;
+                            os[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                             if (s0 + k <= c1) {
                                 const int at = 2 * (s0 + k) + (s0 + k == c0 ? late : 0);
                                 ms[k] = __ldcg(&a.ws->part_m[at][hd]);
                                 ls[k] = __ldcg(&a.ws->part_l[at][hd]);
-                                os[k] = __ldcg(&a.ws->part_o[at][hd][tid]);
+                                os[k] = __ldcg(reinterpret_cast<const float4 *>(&a.ws->part_o[at][hd][4 * lane]));
                             }
-                            mn = fmaxf(mn, ms[k]);
                         }
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k)
+                            mn = fmaxf(mn, ms[k]);
                         const float keep = weight(M, mn);
                         L *= keep;
-                        O *= keep;
+                        O.x *= keep;
+                        O.y *= keep;
+                        O.z *= keep;
+                        O.w *= keep;
 #pragma unroll
                         for (int k = 0; k < kAhead; ++k) {
                             const float f = weight(ms[k], mn);
                             L += ls[k] * f;
-                            O += os[k] * f;
+                            O.x += os[k].x * f;
+                            O.y += os[k].y * f;
+                            O.z += os[k].z * f;
+                            O.w += os[k].w * f;
                         }
                         M = mn;
                     }
-                    a.out[(row0 + hd) * kHeadDim + tid] = f32_to_bf16_rn(L == 0.0f ? 0.0f : O / L);
-                    if (MODE == 2 && tid == 0) {
+                    uint2 y = make_uint2(0u, 0u);
+                    if (L != 0.0f)
+                        y = make_uint2(pack_b16(O.x / L, O.y / L), pack_b16(O.z / L, O.w / L));
+                    *reinterpret_cast<uint2 *>(a.out + (row0 + hd) * kHeadDim + 4 * lane) = y;
+                    if (MODE == 2 && lane == 0) {
                         a.stat_m[row0 + hd] = M;
                         a.stat_l[row0 + hd] = L;
                     }
@@ -863,7 +880,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, int sms, cudaStream_t
     if (a.logits)
         return launch<false, 2, 1, 3>(a, sms, stream);
     if (a.rows.scales)
-        return a.idx ? launch<true, 1, 2, 3>(a, sms, stream) : launch<true, 0, 2, 3>(a, sms, stream);
+        return a.idx ? launch<true, 1, 2, 4>(a, sms, stream) : launch<true, 0, 2, 4>(a, sms, stream);
     return launch<false, 0, 1, 3>(a, sms, stream);
 }
 
