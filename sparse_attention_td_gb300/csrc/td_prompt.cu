@@ -245,8 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         return (bool)__all_sync(kFull, bar_wait(bar, parity));
     };
     if (sm_q & 1023) {            // (cannot be: the swizzled tiles need it)
-        if (tid == 0)
+        pdl_wait();
+        if (tid == 0) {
             atomicOr(a.status, kFlagWaitTimeout);
+            a.ws->join[blockIdx.x] = PromptJoin{-1};
+        }
         return;
     }
     if (tid == 32 * kIssuer) {
