@@ -51,13 +51,13 @@ constexpr int kRawBytes = 32 * (kCodeBytes + 8);
 constexpr int kMaskRing = 8;
 constexpr int kSoftWarps = 8;                    // four per row tile
 constexpr int kCopier = 8, kCopiers = 4;         // copy warps
-constexpr int kSched = 12, kIssuer = 13;
-constexpr int kThreads = 32 * 14;
+constexpr int kSched = 12, kIssuer = 13, kIssuers = 2;      // an issuer per row tile
+constexpr int kThreads = 32 * 15;
 constexpr int kStep = 64;                        // tokens of one S
 constexpr int kCopyRows = kTile / kCopiers;      // of a tile, per copy warp: one a lane
 static_assert(kCopyRows == 32, "a lane has one row of a tile");
 constexpr int kUnitRing = 4;
-constexpr int kUnitUsers = kSoftWarps + kCopiers + 1;
+constexpr int kUnitUsers = kSoftWarps + kCopiers + kIssuers;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;      // O of row tile t: kColO + 128 t; S, and P over it: 128 t and 128 t + 64
 constexpr size_t kSmem = (size_t)(2 + kMostSlots) * kTileBytes + 3 * 1024;    // + Extra
@@ -86,15 +86,16 @@ struct Start {
 // the phase before is over and before the one after can be.  Step number g of a row tile, over
 // units: its S and P have buffer g & 1.
 //   full     a ring slot's use: 16-bit rows: every copy thread as its copies land (then fenced by
-//            the issuer), and each copy warp behind its word of `valid`; 4-bit rows: each copy
-//            warp when its rows are written and fenced.  The issuer waits for every one in order.
-//   empty    the commit behind the MMAs that read the slot; the copy warps wait for every use.
+//            the issuers), and each copy warp behind its word of `valid`; 4-bit rows: each copy
+//            warp when its rows are written and fenced.  Both issuers wait for every one in order.
+//   empty    each issuer's commit behind its MMAs that read the slot, or, in a unit without its row
+//            tile, its arrival behind `full`; the copy warps wait for every use.
 //   q, q_free   as full and empty, per unit.
 //   s[t][g & 1]  S of step g of row tile t.  Its softmax warps wait for every one; S of g + 2 is
 //            issued behind P V of g, which needs their P.
-//   p[t][g & 1]  P of step g, the row tile's four softmax warps; the issuer waits for every one,
+//   p[t][g & 1]  P of step g, the row tile's four softmax warps; its issuer waits for every one,
 //            and P of g + 2 needs S of g + 2.
-//   o[t]     P V of a step.  The issuer waits for that of g - 1 before it issues P V of g, so for
+//   o[t]     P V of a step.  Its issuer waits for that of g - 1 before it issues P V of g, so for
 //            every one (and so S of g + 1 finds P of g - 1 read).  The softmax waits for that of
 //            g - 1 to rescale O, and at a unit's last step, always before it hands over P of g:
 //            P V of g - 2 is over since S of g was issued, P V of g not issued.  Then for the
@@ -102,13 +103,14 @@ struct Start {
 //   unit_there, unit_free   a unit's entry, written by the scheduler and read by all other roles, who free
 //            it when they are done with the unit.
 // q_inv of a unit lies where that of the unit but one before did: its Q comes after q_free of the
-// unit before, which is issued behind all of the unit but one before, for which P was needed.
+// unit before, to which an issuer arrives behind all of the unit but one before, for which P was
+// needed.
 struct Extra {
     uint64_t full[kMostSlots], empty[kMostSlots];
     uint64_t q, q_free;
     uint64_t s[2][2], p[2][2], o[2];
     uint64_t unit_there[kUnitRing], unit_free[kUnitRing];
-    uint64_t drain, done, never;
+    uint64_t drain[kIssuers], done[kIssuers], never;
     Unit unit[kUnitRing];
     Start start;
     long long sums[kThreads / 32];
@@ -258,10 +260,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             x.last_waits[i] = Progress{};
         for (int i = 0; i < kSlots; ++i) {
             bar_init(&x.full[i], Q4 ? kCopiers : 33 * kCopiers);
-            bar_init(&x.empty[i], 1);
+            bar_init(&x.empty[i], kIssuers);
         }
         bar_init(&x.q, Q4 ? kCopiers : 32 * kCopiers);
-        bar_init(&x.q_free, 1);
+        bar_init(&x.q_free, kIssuers);
         for (int t = 0; t < 2; ++t) {
             for (int i = 0; i < 2; ++i) {
                 bar_init(&x.s[t][i], 1);
@@ -273,8 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             bar_init(&x.unit_there[i], 1);
             bar_init(&x.unit_free[i], kUnitUsers);
         }
-        bar_init(&x.drain, 1);
-        bar_init(&x.done, 1);
+        for (int t = 0; t < kIssuers; ++t) {
+            bar_init(&x.drain[t], 1);
+            bar_init(&x.done[t], 1);
+        }
         bar_init(&x.never, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -288,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     tmem_before();
     __syncthreads();
     tmem_after();
-    constexpr uint32_t tmem = 0;             // all 512 columns are this CTA's, so they begin at 0
+    // (all 512 columns are this CTA's, so they begin at 0)
+    constexpr uint32_t tmem = 0;
     if (x.tmem != 0 && tid == 0)             // (cannot be)
         x.progress.gave_up = 1;
     __syncthreads();
@@ -720,19 +725,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         }
         if (flags)
             atomicOr(a.status, flags);
-    } else if (warp == kIssuer) {
-        // ---- MMA issue, by one thread: S of the next step of both row tiles, then P V of this
-        // one, so that the softmax finds its next scores when it is done with these.  The tensor
-        // cores queue few MMAs: every instruction between them counts.  (A wait that gave up
-        // lets the step's MMAs go, whose results nobody uses.)
+    } else if (warp >= kIssuer) {
+        // ---- MMA issue, by one thread for each row tile: S of the next step, then P V of this one, so
+        // that the softmax finds its next scores when it is done with these.  The tensor cores
+        // queue few MMAs, so one thread's waits would leave them idle where two overlap.  (A wait
+        // that gave up lets the step's MMAs go, whose results nobody uses.)
         if (elect_one()) {
+            const int t = warp - kIssuer;
             uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0;      // ring slots of the tile's K and V
-            uint32_t s_buf[2] = {0, 0}, p_buf[2] = {0, 0};    // buffers of a row tile's next S and P V
-            uint32_t p_phase[2] = {0, 0};         // bit b: phase of p[t][b]
-            uint32_t o_phase[2] = {1, 1};         // phase of the last P V that was issued
+            uint32_t s_buf = 0, p_buf = 0;        // buffers of the next S and P V
+            uint32_t p_phase = 0;                 // bit b: phase of p[t][b]
+            uint32_t o_phase = 1;                 // phase of the last P V that was issued
             uint32_t done_steps = 0;
-            const uint32_t q_op = operand(sm_q, 16);
+            const uint32_t q = operand(sm_q + t * kTileBytes, 16);
             const uint32_t ring_k = operand(sm_ring, 16), ring_v = operand(sm_ring, kHalfBytes);
+            const uint32_t col_s = 128 * t, col_o = kColO + 128 * t;
+            uint64_t *const s_bar = x.s[t], *const p_bar = x.p[t], *const o_bar = &x.o[t];
             auto wait = [&](uint64_t *bar, uint32_t phase) { ok = bar_wait(bar, phase) && ok; };
             // Rows copied by cp.async are read by the MMAs through the async proxy.
             auto wait_rows = [&](uint64_t *bar, uint32_t phase) {
@@ -747,32 +755,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     phase ^= 1;
                 }
             };
-            // S of a step, behind P V of the step before the last (which has read the P there)
-            auto issue_s = [&](int t, uint32_t k, bool after) {
-                if (after)
-                    wait(&x.o[t], o_phase[t]);
+            // S of a step; its buffer held the P of the step before the last.
+            auto issue_s = [&](uint32_t k) {
                 tmem_after();
-                const uint32_t q = q_op + t * (kTileBytes >> 4);
 #pragma unroll
                 for (int s = 0; s < 8; ++s) {
                     const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
-                    mma_ss<kStep, Q4>(tmem + 128 * t + 64 * s_buf[t], q + (o >> 4), k + (o >> 4), s > 0);
+                    mma_ss<kStep, Q4>(col_s + 64 * s_buf, q + (o >> 4), k + (o >> 4), s > 0);
                 }
-                mma_commit(&x.s[t][s_buf[t]]);
-                s_buf[t] ^= 1;
-            };
-            auto issue_pv = [&](int t, uint32_t v, bool add) {
-                const uint32_t b = p_buf[t];
-                wait(&x.p[t][b], p_phase[t] >> b);
-                p_phase[t] ^= 1u << b;
-                p_buf[t] ^= 1;
-                tmem_after();
-#pragma unroll
-                for (int s = 0; s < kStep / 16; ++s)
-                    mma_ts<Q4>(tmem + kColO + 128 * t, tmem + 128 * t + 64 * b + s * 8, v + (s * 16 * 128 >> 4),
-                               add || s > 0);
-                mma_commit(&x.o[t]);
-                o_phase[t] ^= 1;
+                mma_commit(s_bar + s_buf);
+                s_buf ^= 1;
             };
 #pragma unroll 1
             for (;; ++units) {
@@ -780,13 +772,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 if (!ok || unit_entry().tiles < 0)
                     break;
                 const int steps = unit_entry().steps;
-                const bool two = unit_entry().rows > kTile;
                 wait_rows(&x.q, units);
+                if (t * kTile >= unit_entry().rows) {         // the unit has no such row tile
+                    bar_arrive(&x.q_free);
+#pragma unroll 1
+                    for (int i = 0; i < steps && ok; i += 2) {
+                        wait(&x.full[k_slot], k_phase);
+                        bar_arrive(&x.empty[k_slot]);
+                        wait(&x.full[v_slot], v_phase);
+                        bar_arrive(&x.empty[v_slot]);
+                        advance(k_slot, k_phase);
+                        advance(v_slot, v_phase);
+                    }
+                    if (!ok)
+                        break;
+                    free_unit();
+                    continue;
+                }
                 wait_rows(&x.full[k_slot], k_phase);
                 uint32_t k = ring_k + k_slot * (kTileBytes >> 4);
-                issue_s(0, k, true);              // (behind the unit before)
-                if (two)
-                    issue_s(1, k, true);
+                wait(o_bar, o_phase);             // (behind the unit before)
+                issue_s(k);
                 if (steps == 1) {
                     mma_commit(&x.empty[k_slot]);
                     mma_commit(&x.q_free);
@@ -795,32 +801,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
 #pragma unroll 1
                 for (int i = 0; i < steps && ok; ++i) {
                     const bool odd = i & 1;
+                    if (i > 0)
+                        wait(o_bar, o_phase);     // P V of step i - 1
                     if (i + 1 < steps) {          // S of step i + 1
                         if (odd) {
                             wait_rows(&x.full[k_slot], k_phase);
                             k = ring_k + k_slot * (kTileBytes >> 4);
                         }
-                        const uint32_t kk = k + (odd ? 0 : kStep * 128 >> 4);
-                        issue_s(0, kk, i > 0);
-                        if (two)
-                            issue_s(1, kk, i > 0);
+                        issue_s(k + (odd ? 0 : kStep * 128 >> 4));
                         if (!odd || i + 2 == steps) {         // the tile's last one
                             mma_commit(&x.empty[k_slot]);
                             advance(k_slot, k_phase);
                         }
                         if (i + 2 == steps)
                             mma_commit(&x.q_free);
-                    } else if (i > 0) {
-                        wait(&x.o[0], o_phase[0]);
-                        if (two)
-                            wait(&x.o[1], o_phase[1]);
                     }
                     if (!odd)
                         wait_rows(&x.full[v_slot], v_phase);
                     const uint32_t v = ring_v + v_slot * (kTileBytes >> 4) + (odd ? kStep * 128 >> 4 : 0);
-                    issue_pv(0, v, i > 0);
-                    if (two)
-                        issue_pv(1, v, i > 0);
+                    wait(p_bar + p_buf, p_phase >> p_buf);
+                    tmem_after();
+#pragma unroll
+                    for (int s = 0; s < kStep / 16; ++s)
+                        mma_ts<Q4>(col_o, col_s + 64 * p_buf + s * 8, v + (s * 16 * 128 >> 4), i > 0 || s > 0);
+                    mma_commit(o_bar);
+                    p_phase ^= 1u << p_buf;
+                    p_buf ^= 1;
+                    o_phase ^= 1;
                     if (odd || i + 1 == steps) {
                         mma_commit(&x.empty[v_slot]);
                         advance(v_slot, v_phase);
@@ -832,8 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 free_unit();
             }
             // No arrival of the last commits may be left when the CTA ends.
-            mma_commit(&x.done);
-            bar_wait(&x.done, 0);
+            mma_commit(&x.done[t]);
+            bar_wait(&x.done[t], 0);
         }
         __syncwarp();
     } else if (warp < kSoftWarps) {
@@ -1030,9 +1037,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     if (x.progress.gave_up) {
         // A wait gave up: leave no copy and no MMA in flight.
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (warp == kIssuer && elect_one()) {        // (the lane that issued them)
-            mma_commit(&x.drain);
-            bar_wait_for(&x.drain, 0, &x.last_waits[warp], 2000000000ll);
+        if (warp >= kIssuer && elect_one()) {        // (the lane that issued them)
+            mma_commit(&x.drain[warp - kIssuer]);
+            bar_wait_for(&x.drain[warp - kIssuer], 0, &x.last_waits[warp], 2000000000ll);
         }
         __syncthreads();
     }
