@@ -152,20 +152,20 @@ __device__ __forceinline__ uint32_t bits_of(int lo, int hi, int base)
     return x >= y ? 0u : (0xffffffffu >> (32 - (y - x))) << x;
 }
 
-// Four neighbouring lanes' rows of four 32-byte pieces, turned: lane c of the four then has piece c
-// of row k in y[8 k ..].
+// Four neighbouring lanes' rows of two times four 16-byte pieces, turned: lane c of the four then
+// has piece c of row k of the first four in y[4 k ..], of the others in y[16 + 4 k ..].
 __device__ __forceinline__ void turn4(uint32_t (&y)[32], int lane)
 {
 #pragma unroll
     for (int d = 1; d <= 2; d <<= 1) {
         const bool up = lane & d;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < 8; ++p) {
             if (p & d)
                 continue;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                uint32_t &lo = y[8 * p + k], &hi = y[8 * (p + d) + k];
+            for (int k = 0; k < 4; ++k) {
+                uint32_t &lo = y[4 * p + k], &hi = y[4 * (p + d) + k];
                 const uint32_t got = __shfl_xor_sync(kFull, up ? lo : hi, d);
                 lo = up ? got : lo;
                 hi = up ? hi : got;
@@ -869,6 +869,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             // window's begin on or among the first ones
             const int shift = u.first - u.low;
             const int end = p + 1 + shift, low = a.window > 0 ? p - a.window + 1 + shift : 0;
+            // (of the warp's rows the first one ends first, the last one's window begins last)
+            const int end0 = __shfl_sync(kFull, end, 0), low1 = __shfl_sync(kFull, low, 31);
             float sl2 = a.scale * kLog2e;
             float mref = -CUDART_INF_F, l = 0.0f;
 #pragma unroll 1
@@ -886,16 +888,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 const uint32_t *valid = &x.valid[(tile_no + (i >> 1)) % kMaskRing][2 * (i & 1)];
                 uint32_t w0 = valid[0], w1 = valid[1];
                 const int t0 = u.tile0 * kTile + i * kStep;
-                // does every row of the warp see all of the step's tokens?
-                const bool inside = end >= t0 + kStep && (t0 >= low || t0 + kStep <= a.sinks);
-                if (!__all_sync(kFull, inside)) {
-                    w0 &= bits_of(0, end - t0, 0) & (bits_of(low - t0, kStep, 0) | bits_of(0, a.sinks - t0, 0));
-                    w1 &= bits_of(0, end - t0, 32) & (bits_of(low - t0, kStep, 32) | bits_of(0, a.sinks - t0, 32));
-                }
                 tmem_wait_ld();
                 tmem_loaded(reinterpret_cast<uint32_t *>(s));
                 tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32);
-                if (__any_sync(kFull, (w0 & w1) != kFull)) {
+                // does every row of the warp see all of the step's tokens?
+                const bool inside = end0 >= t0 + kStep && (t0 >= low1 || t0 + kStep <= a.sinks);
+                if (!inside || (w0 & w1) != kFull) {
+                    w0 &= bits_of(0, end - t0, 0) & (bits_of(low - t0, kStep, 0) | bits_of(0, a.sinks - t0, 0));
+                    w1 &= bits_of(0, end - t0, 32) & (bits_of(low - t0, kStep, 32) | bits_of(0, a.sinks - t0, 32));
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         if (!(w0 >> k & 1u))
@@ -969,9 +969,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const size_t q_row = ((size_t)u.q0 + (row >> a.g_shift)) * a.Hq + (size_t)u.h * a.G + (row & (a.G - 1));
             const bool whole = u.part < 0;
             float worst = 0.0f;
-            // A lane has a row, four lanes four rows: they turn blocks of four 32-byte pieces, so that
-            // a store of the four goes to 128 bytes of one row.  (Every lane on its own: 8400
-            // cycles a unit.)
+            const int q0 = u.q0, unit_row0 = u.row0, unit_rows = u.rows, unit_b = u.b, unit_h = u.h, unit_part = u.part;
+            __syncwarp();
+            if (lane == 0)
+                free_unit();
+            // A lane has a row, four lanes four rows: they turn blocks of four 16-byte pieces, so that
+            // a store of the four goes to 64 bytes of one row.  (Every lane on its own: 8400 cycles
+            // a unit.)
             const int row4 = part * kTile + (warp & 3) * 32 + (lane & ~3);     // first of the four rows
 #pragma unroll 1
             for (int c = 0; c < (whole ? 2 : 4); ++c) {
@@ -1000,23 +1004,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 turn4(y, lane);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (row4 + k >= u.rows)
+                    if (row4 + k >= unit_rows)
                         continue;
-                    if (whole) {                     // (out is 16-byte aligned)
-                        const int to = u.row0 + row4 + k;
-                        uint4 *dst = reinterpret_cast<uint4 *>(
-                            a.out + (((size_t)u.q0 + (to >> a.g_shift)) * a.Hq + (size_t)u.h * a.G + (to & (a.G - 1))) *
-                                        kHeadDim + 64 * c + 16 * (lane & 3));
-                        dst[0] = make_uint4(y[8 * k], y[8 * k + 1], y[8 * k + 2], y[8 * k + 3]);
-                        dst[1] = make_uint4(y[8 * k + 4], y[8 * k + 5], y[8 * k + 6], y[8 * k + 7]);
-                    } else {
-                        store32(&a.ws->prompt_o[u.part][row4 + k][32 * c + 8 * (lane & 3)], y + 8 * k);
-                    }
+                    const int to = unit_row0 + row4 + k;
+                    uint16_t *const dst =
+                        whole ? a.out + (((size_t)q0 + (to >> a.g_shift)) * a.Hq + (size_t)unit_h * a.G + (to & (a.G - 1))) *
+                                            kHeadDim + 64 * c
+                              : reinterpret_cast<uint16_t *>(&a.ws->prompt_o[unit_part][row4 + k][32 * c]);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+                        reinterpret_cast<uint4 *>(dst)[4 * g + (lane & 3)] =
+                            make_uint4(y[16 * g + 4 * k], y[16 * g + 4 * k + 1], y[16 * g + 4 * k + 2], y[16 * g + 4 * k + 3]);
                 }
             }
             if (!whole && live) {
-                a.ws->prompt_m[u.part][mine] = mref;
-                a.ws->prompt_l[u.part][mine] = l;
+                a.ws->prompt_m[unit_part][mine] = mref;
+                a.ws->prompt_l[unit_part][mine] = l;
             }
             tmem_before();
             uint32_t again = __ballot_sync(kFull, live && whole && l != 0.0f && !(worst == 0.0f));
@@ -1024,12 +1027,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 __syncwarp();                        // (the rows' stores come before the second ones)
                 for (; again; again &= again - 1) {
                     const int k = __ffs(again) - 1;
-                    attend_row(a, u.b, u.h, __shfl_sync(kFull, p, k), __shfl_sync(kFull, (unsigned long long)q_row, k), lane);
+                    attend_row(a, unit_b, unit_h, __shfl_sync(kFull, p, k), __shfl_sync(kFull, (unsigned long long)q_row, k), lane);
                 }
             }
             __syncwarp();
-            if (lane == 0)
-                free_unit();
         }
     }
     tmem_before();
