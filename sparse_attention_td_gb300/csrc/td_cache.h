@@ -109,6 +109,8 @@ struct Q4AppendArgs {
     const int32_t *slots;
     int64_t new_stride;
     int tokens, Hkv, num_pages, page_size;
+    uint32_t token_magic, page_magic;   // quotients by products (set by the launcher)
+    int token_shift, page_shift;
 };
 cudaError_t launch_q4_append(const Q4AppendArgs &a, cudaStream_t stream);
 

@@ -286,7 +286,7 @@ td_status td_q4_append(const td_shape *shape, const td_q4_cache *cache, int32_t 
         return TD_ERR_INVALID_ARG;
     const td::Q4AppendArgs a{(uint8_t *)cache->k, (uint8_t *)cache->v, (uint8_t *)cache->scales,
                              (const uint16_t *)k_new, (const uint16_t *)v_new, slot_map, new_stride, num_tokens,
-                             shape->num_kv_heads, cache->num_pages, cache->page_size};
+                             shape->num_kv_heads, cache->num_pages, cache->page_size, 0, 0, 0, 0};
     return td::launch_q4_append(a, (cudaStream_t)stream) == cudaSuccess ? TD_OK : TD_ERR_CUDA;
 }
 

@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 q[w] = y.x;
                 q[w + 1] = y.y;
             }
-            x2[0] = x2[1] = a.scale * kLog2e;
+            x2[0] = x2[1] = MODE == 2 ? kLog2e : a.scale * kLog2e;
             if constexpr (Q4) {
                 uint32_t top = 0;
 #pragma unroll
@@ -574,42 +574,47 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
             if constexpr (!Q4)
                 if (i + kWarps < count)
                     load_k(next);
-            // s[u][2 t + e]: token 16 u + 8 t + r, head 2c + e
-            float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+            // s[u][2 t + e]: token 16 u + 8 t + r, head 2c + e; as exponents of 2 times x2
+            if constexpr (MODE == 2) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const bool ok = there >> (16 * u + 8 * t + r) & 1u;
+                    for (int t = 0; t < 2; ++t) {
+                        const int in = 16 * u + 8 * t + r, at = (grp + i) * GT + in;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float &x = s[u][2 * t + e];
-                        if constexpr (MODE == 2) {
-                            const float z = x * a.scale;
-                            const int at = (grp + i) * GT + 16 * u + 8 * t + r;
+                        for (int e = 0; e < 2; ++e) {
+                            float &x = s[u][2 * t + e];
+                            x *= a.scale;
                             if (2 * c + e < a.G && at < seen.count)
                                 a.logits[((size_t)b * a.Hq + (size_t)h * a.G + 2 * c + e) * a.Nmax + at] =
-                                    ok ? z : -CUDART_INF_F;
-                            x = z * kLog2e;
-                        } else {
-                            x *= x2[e];
+                                    there >> in & 1u ? x : -CUDART_INF_F;
                         }
-                        x = ok ? x : -CUDART_INF_F;
-                        top[e] = fmaxf(top[e], x);
                     }
-                }
-            float ref[2];
-            bool grows = false;
+            }
+            if (there != kFull) {                     // (16 tokens: twice in the word)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (!(there >> (16 * u + 8 * t + r) & 1u))
+                            s[u][2 * t] = s[u][2 * t + 1] = -CUDART_INF_F;
+            }
+            // The running maximum lags until a token exceeds it by 2^8: the probabilities stay below
+            // 2^8, and maxima pass between lanes and O is rescaled rarely.
+            float top[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], 4));
-                top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], 8));
-                top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], 16));
-                grows |= top[e] > m[e];
+                top[e] = fmaxf(s[0][e], s[0][2 + e]);
+                if (U == 2)
+                    top[e] = fmaxf(top[e], fmaxf(s[U - 1][e], s[U - 1][2 + e]));
+                top[e] *= x2[e];
             }
-            if (__any_sync(kFull, grows)) {
+            if (__any_sync(kFull, top[0] > m[0] + 8.0f || top[1] > m[1] + 8.0f)) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], 4));
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], 8));
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], 16));
                     const float mn = fmaxf(m[e], top[e]);
                     const float f = safe_exp2_diff(m[e], mn);
                     m[e] = mn;
@@ -621,9 +626,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                     }
                 }
             }
+            float off[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                ref[e] = m[e] == -CUDART_INF_F ? 0.0f : m[e];
+                off[e] = m[e] == -CUDART_INF_F ? 0.0f : -m[e];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float p[2][2];
@@ -631,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        p[t][e] = ex2(s[u][2 * t + e] - ref[e]);
+                        p[t][e] = ex2(fmaf(s[u][2 * t + e], x2[e], off[e]));
                         l[e] += p[t][e];
                     }
                 if constexpr (Q4) {

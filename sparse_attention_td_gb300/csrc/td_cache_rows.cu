@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
             codes_at[p] = scale_at[p] = nullptr;
             if (e >= total)
                 continue;
-            const uint32_t i = e / (2 * per);
+            const uint32_t i = (uint32_t)((uint64_t)e * a.token_magic >> a.token_shift);      // e / (2 per)
             uint32_t j = e - i * 2 * per;
             const bool isv = j >= per;
             j -= isv ? per : 0;
@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
             const uint4 *src = reinterpret_cast<const uint4 *>((isv ? a.v_new : a.k_new) + (size_t)i * a.new_stride + j * 16);
             y[p][0] = src[0];
             y[p][1] = src[1];
-            const uint32_t page = slot / a.page_size, r = slot - page * a.page_size, block = j % kQuantBlocks;
+            const uint32_t page = (uint32_t)((uint64_t)slot * a.page_magic >> a.page_shift);
+            const uint32_t r = slot - page * a.page_size, block = j % kQuantBlocks;
             const size_t row = ((size_t)page * a.Hkv + j / kQuantBlocks) * a.page_size + r;
             codes_at[p] = (isv ? a.v : a.k) + row * kCodeBytes + block * 8;
             scale_at[p] = a.scales + row * kScaleBytes + (isv ? kQuantBlocks : 0) + block;
@@ -80,23 +81,27 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
             for (int k = 0; k < 8; ++k)
                 top = __vmaxu2(top, x[k] & 0x7fff7fffu);
             top = max(top & 0xffffu, top >> 16);
+            // largest / 6, by the step that the quotients below take
+            const float amax = __uint_as_float(top << 16), sixth = amax * (1.0f / 6.0f);
+            const float want = top >= 0x7f80u ? amax : fmaf(-fmaf(sixth, 6.0f, -amax), 1.0f / 6.0f, sixth);
             uint32_t scale;                        // e4m3, saturated at 448
             float s;                               // its value (exact in fp16 on the way)
             asm("{\n\t.reg .b16 t, u, v;\n\t.reg .b32 w;\n\t"
                 "cvt.rn.satfinite.e4m3x2.f32 t, %2, %3;\n\tcvt.u32.u16 %0, t;\n\t"
                 "cvt.rn.f16x2.e4m3x2 w, t;\n\tmov.b32 {u, v}, w;\n\tcvt.f32.f16 %1, u;\n\t}"
                 : "=r"(scale), "=f"(s)
-                : "f"(0.0f), "f"(__fdiv_rn(__uint_as_float(top << 16), 6.0f)));
+                : "f"(0.0f), "f"(want));
             uint2 codes = make_uint2(0, 0);
             if (top > 0x7f80u) {
                 scale = 0x7f;                      // a value that is not a number: none of the 16 is
             } else if (s > 0.0f) {
-                const float inv = __frcp_rn(s);
+                float inv;                         // (within a step: the quotient's last step corrects it)
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
                 // Beyond 6 s the code saturates; 8 s stands for what is larger (only 16 values of
                 // which the largest is beyond 448 * 8 have any, as a smaller scale is at
                 // least half of the largest / 6).
                 const float most = 8.0f * s;
-                const bool clamp = __uint_as_float(top << 16) > 8.0f * 448.0f;
+                const bool clamp = amax > 8.0f * 448.0f;
                 // (the remainder's sign this way round, so that -0 stays -0)
                 auto quotient = [&](uint32_t bits) {
                     float v = __uint_as_float(bits);
@@ -138,7 +143,7 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
 // weights.  In place a weight moves to a lower or its own place, and every place that a
 // chunk writes lies below the next chunk's, so the block's barrier per chunk orders
 // reads before writes.
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 1024;
 constexpr int kSelectPer = 4;
 
 // A weight that is not a number counts as the largest.
@@ -398,6 +403,16 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const Evict
 
 }  // namespace
 
+// x / d = x * m >> shift for 0 <= x < 2^31.
+static void magic(uint32_t d, uint32_t &m, int &shift)
+{
+    int s = 0;
+    while ((uint64_t(1) << s) < d)
+        ++s;
+    shift = 31 + s;
+    m = (uint32_t)(((uint64_t(1) << shift) + d - 1) / d);
+}
+
 cudaError_t launch_q4_append(const Q4AppendArgs &args, cudaStream_t stream)
 {
     const long long per = 2ll * args.Hkv * kQuantBlocks;        // blocks of a token
@@ -410,6 +425,8 @@ cudaError_t launch_q4_append(const Q4AppendArgs &args, cudaStream_t stream)
         a.v_new += (size_t)t * a.new_stride;
         a.slots += t;
         a.tokens = args.tokens - t < piece ? args.tokens - t : piece;
+        magic((uint32_t)per, a.token_magic, a.token_shift);
+        magic((uint32_t)a.page_size, a.page_magic, a.page_shift);
         long long grid = (a.tokens * per + kQuantThreads - 1) / kQuantThreads;
         if (grid > most)
             grid = most;
