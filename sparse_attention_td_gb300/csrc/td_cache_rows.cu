@@ -137,23 +137,177 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
 // ------------------------------------------------------------------- eviction
 // Of request b's n > budget positions and KV head g: the first `sinks`, the last `recent`, and
 // of the others the `heavy` = budget - sinks - recent with the most weight (ties: the lower
-// position).  A CTA per (request, KV head) finds the weight of the last one kept by three
-// radix passes over order-preserving keys (11, 11 and 10 bits, counts in shared
-// memory), then walks the row once, writing the kept positions in order and their
-// weights.  In place a weight moves to a lower or its own place, and every place that a
-// chunk writes lies below the next chunk's, so the block's barrier per chunk orders
-// reads before writes.
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectPer = 4;
+// position).  A CTA per (request, KV head) finds the weight of the last one kept, then writes
+// the kept positions in order and their weights.
+//
+// The weight is found by three radix passes over order-preserving keys (11, 11 and 10 bits,
+// counts in shared memory).  Rows of up to 16384 positions stay in registers.  (Found bit by
+// bit with block-wide counts, without atomics, it takes two to three times as long.)
+constexpr int kBins = 2048;
 
 // A weight that is not a number counts as the largest.
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xffffffffu : order_key(w); }
 
+// The key of the heavy-th largest candidate (heavy > 0), and in `rest` how many of that key are among
+// the heavy ones.  each(f) calls f(key) for every candidate of the thread.
+template <int T, typename Each>
+__device__ __forceinline__ uint32_t last_key(unsigned *hist, unsigned *sums, unsigned *found, int heavy, unsigned &rest,
+                                             Each each)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t key = 0, mask = 0;
+    rest = heavy;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? kBins / 2 : kBins;
+        for (int i = tid; i < bins; i += T)
+            hist[i] = 0;
+        __syncthreads();
+        each([&](uint32_t k) {
+            if ((k & mask) == key)
+                atomicAdd(&hist[k >> shift & (bins - 1)], 1u);
+        });
+        __syncthreads();
+        // Counts from the highest digit down: a thread has a run of bins.
+        const int run = bins / T, top = bins - 1 - tid * run;
+        unsigned mine = 0;
+        for (int k = 0; k < run; ++k)
+            mine += hist[top - k];
+        unsigned inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned y = __shfl_up_sync(kFull, inc, d);
+            if (lane >= d)
+                inc += y;
+        }
+        if (lane == 31)
+            sums[warp] = inc;
+        __syncthreads();
+        unsigned before = inc - mine;
+        for (int i = 0; i < warp; ++i)
+            before += sums[i];
+        if (before < rest && rest <= before + mine) {
+            int d = top;
+            for (; before + hist[d] < rest; --d)
+                before += hist[d];
+            found[0] = d;
+            found[1] = rest - before;
+        }
+        __syncthreads();
+        key |= found[0] << shift;
+        mask |= (uint32_t)(bins - 1) << shift;
+        rest = found[1];
+    }
+    return key;
+}
+
+template <int T, int NR> __global__ void __launch_bounds__(T) evict_select_short_kernel(const EvictArgs a)
+{
+    constexpr int W = T / 32;
+    __shared__ unsigned hist[kBins], sums[W], found[2];
+    __shared__ uint32_t counts[NR * W];            // kept in any case, and (high half) of the last weight
+    pdl_wait();
+    pdl_launch_dependents();
+    const int unit = blockIdx.x, b = unit / a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t bad = 0;
+    const int n = seq_len_of(a.seq_lens, b, a.Nmax, bad);
+    const float *w = a.weights + (size_t)unit * a.Nmax;
+    float *out = a.weights_out + (size_t)unit * a.out_row;
+    int32_t *kept = a.kept + (size_t)unit * a.budget;
+    if (unit % a.Hkv == 0 && tid == 0) {
+        a.seq_lens_out[b] = min(n, a.budget);
+        if (bad)
+            atomicOr(a.status, bad);
+    }
+    if (n <= a.budget) {
+        for (int i = tid; i < a.budget; i += T) {
+            kept[i] = i < n ? i : -1;
+            if (i < n && out != w)
+                out[i] = w[i];
+        }
+        return;
+    }
+    const int c0 = a.sinks, c1 = n - a.recent;       // the candidates
+    const int heavy = a.budget - a.sinks - a.recent;
+    const int rounds = (n + T - 1) / T;              // position j T + tid
+    float v[NR];
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        const int i = j * T + tid;
+        v[j] = j < rounds && i < n ? w[i] : 0.0f;
+    }
+    auto candidate = [&](int j) { return j * T + tid >= c0 && j * T + tid < c1; };
+    uint32_t key = 0xffffffffu;
+    unsigned rest = 0;                               // how many of that key are kept, the lowest positions
+    if (heavy > 0)
+        key = last_key<T>(hist, sums, found, heavy, rest, [&](auto f) {
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+                if (j < rounds && candidate(j))
+                    f(weight_key(v[j]));
+        });
+    // Counts of every warp and round, their prefix sums in the positions' order, the places.
+    auto flags = [&](int j, uint32_t &sure, uint32_t &equal) {
+        const int i = j * T + tid;
+        const uint32_t k = weight_key(v[j]);
+        const bool in = candidate(j);
+        sure = __ballot_sync(kFull, i < n && (!in || k > key));
+        equal = __ballot_sync(kFull, i < n && in && k == key);
+    };
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        uint32_t sure, equal;
+        flags(j, sure, equal);
+        if (lane == 0)
+            counts[j * W + warp] = __popc(sure) | __popc(equal) << 16;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        constexpr int kPer = NR * W / 32;
+        uint32_t mine[kPer], all = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            mine[i] = all;
+            all += counts[lane * kPer + i];          // (at most 16384 of either)
+        }
+        uint32_t inc = all;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(kFull, inc, d);
+            if (lane >= d)
+                inc += y;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            counts[lane * kPer + i] = mine[i] + inc - all;
+    }
+    __syncthreads();                                 // (every weight has been read, too)
+    const uint32_t below = (1u << lane) - 1;
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        if (j >= rounds)
+            break;
+        uint32_t sure, equal;
+        flags(j, sure, equal);
+        const uint32_t before = counts[j * W + warp];
+        const uint32_t nsure = (before & 0xffff) + __popc(sure & below), nsame = (before >> 16) + __popc(equal & below);
+        if ((sure >> lane & 1u) || ((equal >> lane & 1u) && nsame < rest)) {
+            const uint32_t to = nsure + min(nsame, rest);
+            kept[to] = j * T + tid;
+            out[to] = v[j];
+        }
+    }
+}
+
+// Longer rows are read again for each pass, then walked over.  In place a weight moves to a lower or its own
+// place, and every place that a chunk writes lies below the next chunk's, so the block's
+// barrier per chunk orders reads before writes.
+constexpr int kSelectThreads = 512;
+constexpr int kSelectPer = 4;
+
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a)
 {
-    __shared__ unsigned hist[2048];
-    __shared__ unsigned sums[kSelectThreads / 32];
-    __shared__ unsigned sm_digit, sm_rest;
+    __shared__ unsigned hist[kBins], sums[kSelectThreads / 32], found[2];
     pdl_wait();
     pdl_launch_dependents();
     const int unit = blockIdx.x, b = unit / a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -177,15 +331,10 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     }
     const int c0 = a.sinks, c1 = n - a.recent;       // the candidates
     const int heavy = a.budget - a.sinks - a.recent;
-    // The key of the heavy-th candidate, digit by digit, and how many of that key are kept.
-    uint32_t key = 0, mask = 0;
-    unsigned rest = heavy;
-    if (heavy > 0) {
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-            for (int i = tid; i < bins; i += kSelectThreads)
-                hist[i] = 0;
-            __syncthreads();
+    uint32_t key = 0xffffffffu;
+    unsigned rest = 0;                               // how many of that key are kept
+    if (heavy > 0)
+        key = last_key<kSelectThreads>(hist, sums, found, heavy, rest, [&](auto f) {
             constexpr int kAhead = 8;
             for (int i0 = c0 + tid; i0 < c1; i0 += kAhead * kSelectThreads) {
                 float v[kAhead];
@@ -195,44 +344,10 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
                         v[k] = w[i0 + k * kSelectThreads];
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k)
-                    if (i0 + k * kSelectThreads < c1) {
-                        const uint32_t y = weight_key(v[k]);
-                        if ((y & mask) == key)
-                            atomicAdd(&hist[y >> shift & (bins - 1)], 1u);
-                    }
+                    if (i0 + k * kSelectThreads < c1)
+                        f(weight_key(v[k]));
             }
-            __syncthreads();
-            // Counts from the highest digit down: a thread has a run of bins.
-            const int run = bins / kSelectThreads, top = bins - 1 - tid * run;
-            unsigned mine = 0;
-            for (int k = 0; k < run; ++k)
-                mine += hist[top - k];
-            unsigned inc = mine;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned y = __shfl_up_sync(kFull, inc, d);
-                if (lane >= d)
-                    inc += y;
-            }
-            if (lane == 31)
-                sums[warp] = inc;
-            __syncthreads();
-            unsigned before = inc - mine;
-            for (int i = 0; i < warp; ++i)
-                before += sums[i];
-            if (before < rest && rest <= before + mine) {
-                int d = top;
-                for (; before + hist[d] < rest; --d)
-                    before += hist[d];
-                sm_digit = d;
-                sm_rest = rest - before;
-            }
-            __syncthreads();
-            key |= sm_digit << shift;
-            mask |= (uint32_t)(bins - 1) << shift;
-            rest = sm_rest;
-        }
-    }
+        });
     // ---- the kept positions in order.  Both counts pass through one scan: those kept in
     // any case in the low half, those of the last key in the high one.
     unsigned sure0 = 0, same0 = 0;                 // before this chunk
@@ -440,7 +555,9 @@ cudaError_t launch_q4_append(const Q4AppendArgs &args, cudaStream_t stream)
 cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream)
 {
     const long long units = (long long)a.B * a.Hkv;
-    const cudaError_t err = launch_behind(evict_select_kernel, units, kSelectThreads, stream, a);
+    const cudaError_t err = a.Nmax <= 8192 ? launch_behind(evict_select_short_kernel<512, 16>, units, 512, stream, a)
+                            : a.Nmax <= 16384 ? launch_behind(evict_select_short_kernel<1024, 16>, units, 1024, stream, a)
+                                              : launch_behind(evict_select_kernel, units, kSelectThreads, stream, a);
     if (err != cudaSuccess)
         return err;
     // Slices of rows (in place) or runs of them (else) until there are about four CTAs per SM.

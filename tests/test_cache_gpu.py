@@ -449,9 +449,10 @@ def test_evict(place, budget, sinks, recent, page):
 
 
 @pytest.mark.parametrize("kind", ["equal", "few", "special", "heavy end", "close"])
-@pytest.mark.parametrize("place", [True, False])
-def test_evict_weights(place, kind):
-    c = Case(11, [700, 650, 64], 1, 2, 16)
+@pytest.mark.parametrize("place,n", [(True, 700), (False, 700), (True, 9000), (True, 17000)])
+def test_evict_weights(place, n, kind):
+    """The rows' three ways through the selection, by their length."""
+    c = Case(11, [n, 650, 64], 1, 2, 16)
     w = torch.rand(c.B, c.Hkv, c.N, generator=c.gen)
     if kind == "equal":
         w = torch.full_like(w, 0.25)
@@ -470,8 +471,9 @@ def test_evict_weights(place, kind):
 def test_evict_many_requests_and_long_rows():
     c = Case(2, [1 + (i * 31) % 100 for i in range(40)], 1, 8, 8)
     run_evict(c, torch.rand(c.B, c.Hkv, c.N, generator=c.gen), 33, 2, 8, True)
-    c = Case(2, [9000], 1, 1, 0)
-    run_evict(c, torch.rand(1, 1, c.N, generator=c.gen), 5000, 2, 100, True)
+    for n, budget in ((9000, 5000), (17000, 3), (16385, 16384)):
+        c = Case(2, [n], 1, 1, 0)
+        run_evict(c, (torch.rand(1, 1, c.N, generator=c.gen) * 5000).floor(), budget, 1, 2, True)
 
 
 def test_evict_pages_that_are_none():
