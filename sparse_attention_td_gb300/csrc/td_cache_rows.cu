@@ -34,8 +34,12 @@ cudaError_t launch_behind(void (*kernel)(Args, More...), long long grid, int thr
 // or differs from it by 2^-11 relative; the quotient below is within 2^-23 and exact
 // where the result is that short (one step from a rounded reciprocal: the remainder
 // x - q s is exact in an fma).  The same holds for the largest value / 6 and the borders of e4m3.
+//
+// Bound by memory once there are enough loads in flight: 26624 tokens of 8 KV heads
+// take 32.4 us (5.3 TB/s).  One block a thread and many threads: two or four a thread, or
+// 4 to 16 CTAs per SM that walk, took 36 to 55 us.
 constexpr int kQuantThreads = 256;
-constexpr int kQuantPer = 2;                  // blocks of 16 values a thread has at a time
+constexpr int kQuantCtas = 32;                // per SM, at most
 constexpr int kQuantBlocks = kHeadDim / 16;   // of a row
 
 __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4AppendArgs a)
@@ -45,92 +49,74 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
     const uint32_t per = a.Hkv * kQuantBlocks;    // blocks of one token's K (or V)
     const uint32_t total = (uint32_t)a.tokens * 2 * per;        // (below 2^31)
     const uint32_t limit = (uint32_t)a.num_pages * a.page_size;
-    const uint32_t step = gridDim.x * kQuantThreads;
-    for (uint32_t e0 = blockIdx.x * kQuantThreads + threadIdx.x; e0 < total; e0 += kQuantPer * step) {
-        uint4 y[kQuantPer][2];
-        uint8_t *codes_at[kQuantPer], *scale_at[kQuantPer];     // null: nothing to write
+    for (uint32_t e = blockIdx.x * kQuantThreads + threadIdx.x; e < total; e += gridDim.x * kQuantThreads) {
+        const uint32_t i = (uint32_t)((uint64_t)e * a.token_magic >> a.token_shift);      // e / (2 per)
+        uint32_t j = e - i * 2 * per;
+        const bool isv = j >= per;
+        j -= isv ? per : 0;
+        const uint32_t slot = a.slots[i];                       // (negative ones lie beyond the limit)
+        if (slot >= limit)
+            continue;
+        const uint4 *src = reinterpret_cast<const uint4 *>((isv ? a.v_new : a.k_new) + (size_t)i * a.new_stride + j * 16);
+        const uint4 y0 = src[0], y1 = src[1];
+        const uint32_t x[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        uint32_t top = 0;
 #pragma unroll
-        for (int p = 0; p < kQuantPer; ++p) {
-            const uint32_t e = e0 + p * step;
-            codes_at[p] = scale_at[p] = nullptr;
-            if (e >= total)
-                continue;
-            const uint32_t i = (uint32_t)((uint64_t)e * a.token_magic >> a.token_shift);      // e / (2 per)
-            uint32_t j = e - i * 2 * per;
-            const bool isv = j >= per;
-            j -= isv ? per : 0;
-            const uint32_t slot = a.slots[i];                   // (negative ones lie beyond the limit)
-            if (slot >= limit)
-                continue;
-            const uint4 *src = reinterpret_cast<const uint4 *>((isv ? a.v_new : a.k_new) + (size_t)i * a.new_stride + j * 16);
-            y[p][0] = src[0];
-            y[p][1] = src[1];
-            const uint32_t page = (uint32_t)((uint64_t)slot * a.page_magic >> a.page_shift);
-            const uint32_t r = slot - page * a.page_size, block = j % kQuantBlocks;
-            const size_t row = ((size_t)page * a.Hkv + j / kQuantBlocks) * a.page_size + r;
-            codes_at[p] = (isv ? a.v : a.k) + row * kCodeBytes + block * 8;
-            scale_at[p] = a.scales + row * kScaleBytes + (isv ? kQuantBlocks : 0) + block;
-        }
+        for (int k = 0; k < 8; ++k)
+            top = __vmaxu2(top, x[k] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
+        // largest / 6, by the step that the quotients below take
+        const float amax = __uint_as_float(top << 16), sixth = amax * (1.0f / 6.0f);
+        const float want = top >= 0x7f80u ? amax : fmaf(-fmaf(sixth, 6.0f, -amax), 1.0f / 6.0f, sixth);
+        uint32_t scale;                        // e4m3, saturated at 448
+        float s;                               // its value (exact in fp16 on the way)
+        asm("{\n\t.reg .b16 t, u, v;\n\t.reg .b32 w;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 t, %2, %3;\n\tcvt.u32.u16 %0, t;\n\t"
+            "cvt.rn.f16x2.e4m3x2 w, t;\n\tmov.b32 {u, v}, w;\n\tcvt.f32.f16 %1, u;\n\t}"
+            : "=r"(scale), "=f"(s)
+            : "f"(0.0f), "f"(want));
+        uint2 codes = make_uint2(0, 0);
+        if (top > 0x7f80u) {
+            scale = 0x7f;                      // a value that is not a number: none of the 16 is
+        } else if (s > 0.0f) {
+            float inv;                         // (within a step: the quotient's last step corrects it)
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+            // Beyond 6 s the code saturates; 8 s stands for what is larger (only 16 values of
+            // which the largest is beyond 448 * 8 have any, as a smaller scale is at
+            // least half of the largest / 6).
+            const float most = 8.0f * s;
+            const bool clamp = amax > 8.0f * 448.0f;
+            // (the remainder's sign this way round, so that -0 stays -0)
+            auto quotient = [&](uint32_t bits) {
+                float v = __uint_as_float(bits);
+                if (clamp)
+                    v = fmaxf(fminf(v, most), -most);
+                const float q = v * inv;
+                return fmaf(-fmaf(q, s, -v), inv, q);
+            };
+            float q[16];
 #pragma unroll
-        for (int p = 0; p < kQuantPer; ++p) {
-            if (!codes_at[p])
-                continue;
-            const uint32_t x[8] = {y[p][0].x, y[p][0].y, y[p][0].z, y[p][0].w, y[p][1].x, y[p][1].y, y[p][1].z, y[p][1].w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                top = __vmaxu2(top, x[k] & 0x7fff7fffu);
-            top = max(top & 0xffffu, top >> 16);
-            // largest / 6, by the step that the quotients below take
-            const float amax = __uint_as_float(top << 16), sixth = amax * (1.0f / 6.0f);
-            const float want = top >= 0x7f80u ? amax : fmaf(-fmaf(sixth, 6.0f, -amax), 1.0f / 6.0f, sixth);
-            uint32_t scale;                        // e4m3, saturated at 448
-            float s;                               // its value (exact in fp16 on the way)
-            asm("{\n\t.reg .b16 t, u, v;\n\t.reg .b32 w;\n\t"
-                "cvt.rn.satfinite.e4m3x2.f32 t, %2, %3;\n\tcvt.u32.u16 %0, t;\n\t"
-                "cvt.rn.f16x2.e4m3x2 w, t;\n\tmov.b32 {u, v}, w;\n\tcvt.f32.f16 %1, u;\n\t}"
-                : "=r"(scale), "=f"(s)
-                : "f"(0.0f), "f"(want));
-            uint2 codes = make_uint2(0, 0);
-            if (top > 0x7f80u) {
-                scale = 0x7f;                      // a value that is not a number: none of the 16 is
-            } else if (s > 0.0f) {
-                float inv;                         // (within a step: the quotient's last step corrects it)
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-                // Beyond 6 s the code saturates; 8 s stands for what is larger (only 16 values of
-                // which the largest is beyond 448 * 8 have any, as a smaller scale is at
-                // least half of the largest / 6).
-                const float most = 8.0f * s;
-                const bool clamp = amax > 8.0f * 448.0f;
-                // (the remainder's sign this way round, so that -0 stays -0)
-                auto quotient = [&](uint32_t bits) {
-                    float v = __uint_as_float(bits);
-                    if (clamp)
-                        v = fmaxf(fminf(v, most), -most);
-                    const float q = v * inv;
-                    return fmaf(-fmaf(q, s, -v), inv, q);
-                };
-                float q[16];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    q[2 * k] = quotient(x[k] << 16);
-                    q[2 * k + 1] = quotient(x[k] & 0xffff0000u);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float *z = q + 8 * h;
-                    uint32_t &out = h ? codes.y : codes.x;
-                    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-                        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-                        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-                        "mov.b32 %0, {a, b, c, d};\n\t}"
-                        : "=r"(out)
-                        : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
-                }
+            for (int k = 0; k < 8; ++k) {
+                q[2 * k] = quotient(x[k] << 16);
+                q[2 * k + 1] = quotient(x[k] & 0xffff0000u);
             }
-            *reinterpret_cast<uint2 *>(codes_at[p]) = codes;
-            *scale_at[p] = (uint8_t)scale;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float *z = q + 8 * h;
+                uint32_t &out = h ? codes.y : codes.x;
+                asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+                    "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+                    "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+                    "mov.b32 %0, {a, b, c, d};\n\t}"
+                    : "=r"(out)
+                    : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
+            }
         }
+        const uint32_t page = (uint32_t)((uint64_t)slot * a.page_magic >> a.page_shift);
+        const uint32_t r = slot - page * a.page_size, block = j % kQuantBlocks;
+        const size_t row = ((size_t)page * a.Hkv + j / kQuantBlocks) * a.page_size + r;
+        *reinterpret_cast<uint2 *>((isv ? a.v : a.k) + row * kCodeBytes + block * 8) = codes;
+        a.scales[row * kScaleBytes + (isv ? kQuantBlocks : 0) + block] = (uint8_t)scale;
     }
 }
 
@@ -409,10 +395,10 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 // few; between two caches the rows are also cut into runs.  Cache rows are looked up
 // kMoveList at a time; a chunk is read while the one before is written.
 constexpr int kMoveThreads = 256;
-constexpr int kMovePer = 4;
+constexpr int kMovePer = 8;       // (4 with 3 or 4 CTAs per SM: 219 and 191 us where this takes 176)
 constexpr int kMoveList = 1024;
 
-__global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const EvictArgs a, int log_slices, int runs)
+__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const EvictArgs a, int log_slices, int runs)
 {
     __shared__ int sm_from[kMoveList], sm_to[kMoveList];        // cache rows; to -1: nothing to move
     __shared__ int sm_first;
@@ -531,7 +517,7 @@ static void magic(uint32_t d, uint32_t &m, int &shift)
 cudaError_t launch_q4_append(const Q4AppendArgs &args, cudaStream_t stream)
 {
     const long long per = 2ll * args.Hkv * kQuantBlocks;        // blocks of a token
-    const long long most = (long long)host_sm_count() * 8;
+    const long long most = (long long)host_sm_count() * kQuantCtas;
     // (blocks are counted in 31 bits)
     const int piece = (int)((1ll << 30) / per) > 0 ? (int)((1ll << 30) / per) : 1;
     for (int t = 0; t < args.tokens; t += piece) {
