@@ -35,7 +35,7 @@ cudaError_t launch_behind(void (*kernel)(Args, More...), long long grid, int thr
 // where the result is that short (one step from a rounded reciprocal: the remainder
 // x - q s is exact in an fma).  The same holds for the largest value / 6 and the borders of e4m3.
 //
-// Bound by memory once there are enough loads in flight: 26624 tokens of 8 KV heads
+// Bound by memory once there are enough loads in flight: 32749 tokens of 8 KV heads
 // take 32.4 us (5.3 TB/s).  One block a thread and many threads: two or four a thread, or
 // 4 to 16 CTAs per SM that walk, took 36 to 55 us.
 constexpr int kQuantThreads = 256;

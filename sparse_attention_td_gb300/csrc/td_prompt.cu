@@ -57,9 +57,12 @@ constexpr int kStep = 64;                        // tokens of one S
 constexpr int kCopyRows = kTile / kCopiers;      // of a tile, per copy warp: one a lane
 static_assert(kCopyRows == 32, "a lane has one row of a tile");
 constexpr int kUnitRing = 4;
+constexpr float kMostSum = 8192.0f;              // of a step's P of a row (fp16 ends at 65504)
+constexpr float kMostFloat = 3.402823466e38f;
 constexpr int kUnitUsers = kSoftWarps + kCopiers + kIssuers;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;      // O of row tile t: kColO + 128 t; S, and P over it: 128 t and 128 t + 64
+constexpr uint32_t kColO = 256;      // O of row tile t: kColO + 128 t; S: 128 t
+constexpr uint32_t kColP = 64;       // two P of a row tile: behind its S, 32 columns each
 constexpr size_t kSmem = (size_t)(2 + kMostSlots) * kTileBytes + 3 * 1024;    // + Extra
 
 // A unit of work, as every role reads it.
@@ -84,22 +87,21 @@ struct Start {
 
 // Who arrives and who waits; a wait looks at a phase's parity, so each must come when
 // the phase before is over and before the one after can be.  Step number g of a row tile, over
-// units: its S and P have buffer g & 1.
+// units: its P has buffer g & 1.
 //   full     a ring slot's use: 16-bit rows: every copy thread as its copies land (then fenced by
 //            the issuers), and each copy warp behind its word of `valid`; 4-bit rows: each copy
 //            warp when its rows are written and fenced.  Both issuers wait for every one in order.
 //   empty    each issuer's commit behind its MMAs that read the slot, or, in a unit without its row
 //            tile, its arrival behind `full`; the copy warps wait for every use.
 //   q, q_free   as full and empty, per unit.
-//   s[t][g & 1]  S of step g of row tile t.  Its softmax warps wait for every one; S of g + 2 is
-//            issued behind P V of g, which needs their P.
+//   s[t]     S of step g of row tile t.  Its softmax warps wait for every one.
+//   r[t]     the four softmax warps have S of step g in registers.  Its issuer waits for every one
+//            before it issues the S behind it.
 //   p[t][g & 1]  P of step g, the row tile's four softmax warps; its issuer waits for every one,
-//            and P of g + 2 needs S of g + 2.
-//   o[t]     P V of a step.  Its issuer waits for that of g - 1 before it issues P V of g, so for
-//            every one (and so S of g + 1 finds P of g - 1 read).  The softmax waits for that of
-//            g - 1 to rescale O, and at a unit's last step, always before it hands over P of g:
-//            P V of g - 2 is over since S of g was issued, P V of g not issued.  Then for the
-//            unit's last one.
+//            and P of g + 2 needs S of g + 2, which is issued behind P V of g.
+//   o[t][g & 1]  P V of a step.  The softmax waits for that of g - 2 before it writes P of g over
+//            that step's, so for every one, and that of g + 2 needs a later P.  For that of g - 1 it
+//            waits to rescale O, and behind a unit's last step.
 //   unit_there, unit_free   a unit's entry, written by the scheduler and read by all other roles, who free
 //            it when they are done with the unit.
 // q_inv of a unit lies where that of the unit but one before did: its Q comes after q_free of the
@@ -108,7 +110,7 @@ struct Start {
 struct Extra {
     uint64_t full[kMostSlots], empty[kMostSlots];
     uint64_t q, q_free;
-    uint64_t s[2][2], p[2][2], o[2];
+    uint64_t s[2], r[2], p[2][2], o[2][2];
     uint64_t unit_there[kUnitRing], unit_free[kUnitRing];
     uint64_t drain[kIssuers], done[kIssuers], never;
     Unit unit[kUnitRing];
@@ -265,11 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         bar_init(&x.q, Q4 ? kCopiers : 32 * kCopiers);
         bar_init(&x.q_free, kIssuers);
         for (int t = 0; t < 2; ++t) {
+            bar_init(&x.s[t], 1);
+            bar_init(&x.r[t], 4);
             for (int i = 0; i < 2; ++i) {
-                bar_init(&x.s[t][i], 1);
                 bar_init(&x.p[t][i], 4);
+                bar_init(&x.o[t][i], 1);
             }
-            bar_init(&x.o[t], 1);
         }
         for (int i = 0; i < kUnitRing; ++i) {
             bar_init(&x.unit_there[i], 1);
@@ -618,14 +621,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                         const uint32_t slot = next_slot(kv == 0, there);
                         if (!ok)
                             break;
+                        // half a warp per row of 256 bytes: rows 0 .. 15, and 16 .. 31
                         const int c = lane & 15;
                         const uint8_t *src = (kv ? a.rows.v : a.rows.k) + c * 16;
-                        const uint32_t dst = sm_ring + slot * kTileBytes + (c >> 3) * kHalfBytes + kCopyRows * me * 128;
-#pragma unroll 8
-                        for (int r = lane >> 4; r < 32; r += 2) {
-                            const int from = __shfl_sync(kFull, row, r);
-                            copy16(dst + r * 128 + (((c ^ r) & 7) << 4),
-                                   src + (size_t)(uint32_t)max(from, 0) * (kHeadDim * 2), from >= 0);
+                        const uint32_t dst = sm_ring + slot * kTileBytes + (c >> 3) * kHalfBytes +
+                                             (kCopyRows * me + (lane & 16)) * 128 + ((c & 7) << 4);
+                        if (there == kFull) {
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) {
+                                const int from = __shfl_sync(kFull, row, r, 16);
+                                copy16((dst ^ ((r & 7) << 4)) + r * 128, src + (size_t)(uint32_t)from * (kHeadDim * 2));
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int r = 0; r < 16; ++r) {
+                                const int from = __shfl_sync(kFull, row, r, 16);
+                                copy16((dst ^ ((r & 7) << 4)) + r * 128,
+                                       src + (size_t)(uint32_t)max(from, 0) * (kHeadDim * 2), from >= 0);
+                            }
                         }
                         copies_arrive(&x.full[slot]);
                         if (lane == 0)
@@ -647,17 +660,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                         row = next_row(n >> 1);
                         there[2] = __ballot_sync(kFull, row >= 0);
                     }
-                    const uint8_t *codes = n & 1 ? a.rows.v : a.rows.k;
-                    const int c = lane & 3;
+                    const uint8_t *codes = (n & 1 ? a.rows.v : a.rows.k) + 16 * (lane & 3);
+                    const uint8_t *scales = a.rows.scales + (size_t)(uint32_t)max(row, 0) * kScaleBytes + 8 * (n & 1);
+                    const uint32_t to = raw + (lane >> 2) * kCodeBytes + (((lane & 3) ^ (lane >> 3 & 3)) << 4);
+                    if (there[2] == kFull) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 8 * i + (lane >> 2), from = __shfl_sync(kFull, row, r);
-                        copy16(raw + r * kCodeBytes + ((c ^ (r >> 1 & 3)) << 4),
-                               codes + (size_t)(uint32_t)max(from, 0) * kCodeBytes + 16 * c, from >= 0);
+                        for (int i = 0; i < 4; ++i) {
+                            const int from = __shfl_sync(kFull, row, 8 * i + (lane >> 2));
+                            copy16(to + 8 * i * kCodeBytes, codes + (size_t)(uint32_t)from * kCodeBytes);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            const int from = __shfl_sync(kFull, row, 8 * i + (lane >> 2));
+                            copy16(to + 8 * i * kCodeBytes, codes + (size_t)(uint32_t)max(from, 0) * kCodeBytes, from >= 0);
+                        }
                     }
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(raw + 32 * kCodeBytes + 8 * lane),
-                                 "l"(a.rows.scales + (size_t)(uint32_t)max(row, 0) * kScaleBytes + 8 * (n & 1)),
-                                 "r"(row >= 0 ? 8 : 0)
+                                 "l"(scales), "r"(row >= 0 ? 8 : 0)
                                  : "memory");
                 };
                 const int entries = 2 * u.tiles;
@@ -680,16 +700,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     const uint32_t slot = next_slot(!(n & 1), there[0]);
                     if (!ok)
                         break;
-                    const int c = lane >> 3;      // a lane decodes 32 values of four rows
-                    const uint32_t dst = sm_ring + slot * kTileBytes + (c >> 1) * kHalfBytes;
+                    // a lane decodes 32 values, c, of rows 8 t + the low three bits of its number
+                    const int c = lane >> 3, low = lane & 7;
+                    const uint32_t codes = raw + low * kCodeBytes + ((c ^ (low >> 1 & 3)) << 4);
+                    const uint32_t scales = raw + 32 * kCodeBytes + 8 * low + 2 * c;
+                    const uint32_t dst = sm_ring + slot * kTileBytes + (c >> 1) * kHalfBytes +
+                                         (kCopyRows * me + low) * 128 + (((4 * (c & 1)) ^ low) << 4);
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const int r8 = 8 * t + (lane & 7), r = kCopyRows * me + r8;
                         uint32_t w[4], s2, two[2];
-                        lds_words(raw + r8 * kCodeBytes + ((c ^ (r8 >> 1 & 3)) << 4), w);
+                        lds_words(codes + 8 * t * kCodeBytes, w);
                         asm volatile("{\n\t.reg .b16 t;\n\tld.shared.b16 t, [%1];\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
                                      : "=r"(s2)
-                                     : "r"(raw + 32 * kCodeBytes + 8 * r8 + 2 * c)
+                                     : "r"(scales + 64 * t)
                                      : "memory");
                         two[0] = __byte_perm(s2, s2, 0x1010);
                         two[1] = __byte_perm(s2, s2, 0x3232);
@@ -697,8 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                         for (int k = 0; k < 4; ++k) {
                             uint32_t y[4];
                             decode8(w[k], two[k >> 1], y);
-                            const int chunk = 4 * (c & 1) + k;      // of the row's half
-                            sts4(dst + r * 128 + (((chunk ^ r) & 7) << 4), y[0], y[1], y[2], y[3]);
+                            sts4((dst ^ (k << 4)) + 1024 * t, y[0], y[1], y[2], y[3]);
                         }
                     }
                     arrive(&x.full[slot]);        // (with a __syncwarp: the coded rows have been read)
@@ -726,21 +748,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         if (flags)
             atomicOr(a.status, flags);
     } else if (warp >= kIssuer) {
-        // ---- MMA issue, by one thread for each row tile: S of the next step, then P V of this one, so
-        // that the softmax finds its next scores when it is done with these.  The tensor cores
-        // queue few MMAs, so one thread's waits would leave them idle where two overlap.  (A wait
+        // ---- MMA issue, by one thread for each row tile: S of the next step as soon as the softmax has
+        // this one's in registers, then P V of this one, so that the softmax finds its next scores
+        // when it is done with these.  The tensor cores queue few MMAs, so one thread's
+        // waits would leave them idle where two overlap.  (A wait
         // that gave up lets the step's MMAs go, whose results nobody uses.)
         if (elect_one()) {
             const int t = warp - kIssuer;
             uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0;      // ring slots of the tile's K and V
-            uint32_t s_buf = 0, p_buf = 0;        // buffers of the next S and P V
+            uint32_t p_buf = 0;                   // buffer of the next P V
             uint32_t p_phase = 0;                 // bit b: phase of p[t][b]
-            uint32_t o_phase = 1;                 // phase of the last P V that was issued
+            uint32_t r_phase = 1;                 // phase of the last S that was issued
             uint32_t done_steps = 0;
             const uint32_t q = operand(sm_q + t * kTileBytes, 16);
             const uint32_t ring_k = operand(sm_ring, 16), ring_v = operand(sm_ring, kHalfBytes);
-            const uint32_t col_s = 128 * t, col_o = kColO + 128 * t;
-            uint64_t *const s_bar = x.s[t], *const p_bar = x.p[t], *const o_bar = &x.o[t];
+            const uint32_t col_s = 128 * t, col_p = col_s + kColP, col_o = kColO + 128 * t;
+            uint64_t *const s_bar = &x.s[t], *const p_bar = x.p[t], *const o_bar = x.o[t];
             auto wait = [&](uint64_t *bar, uint32_t phase) { ok = bar_wait(bar, phase) && ok; };
             // Rows copied by cp.async are read by the MMAs through the async proxy.
             auto wait_rows = [&](uint64_t *bar, uint32_t phase) {
@@ -755,16 +778,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     phase ^= 1;
                 }
             };
-            // S of a step; its buffer held the P of the step before the last.
+            // S of a step, over the one before (which may be another unit's).
             auto issue_s = [&](uint32_t k) {
+                wait(&x.r[t], r_phase);
+                r_phase ^= 1;
                 tmem_after();
 #pragma unroll
                 for (int s = 0; s < 8; ++s) {
                     const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
-                    mma_ss<kStep, Q4>(col_s + 64 * s_buf, q + (o >> 4), k + (o >> 4), s > 0);
+                    mma_ss<kStep, Q4>(col_s, q + (o >> 4), k + (o >> 4), s > 0);
                 }
-                mma_commit(s_bar + s_buf);
-                s_buf ^= 1;
+                mma_commit(s_bar);
             };
 #pragma unroll 1
             for (;; ++units) {
@@ -791,7 +815,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
                 wait_rows(&x.full[k_slot], k_phase);
                 uint32_t k = ring_k + k_slot * (kTileBytes >> 4);
-                wait(o_bar, o_phase);             // (behind the unit before)
                 issue_s(k);
                 if (steps == 1) {
                     mma_commit(&x.empty[k_slot]);
@@ -801,8 +824,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
 #pragma unroll 1
                 for (int i = 0; i < steps && ok; ++i) {
                     const bool odd = i & 1;
-                    if (i > 0)
-                        wait(o_bar, o_phase);     // P V of step i - 1
                     if (i + 1 < steps) {          // S of step i + 1
                         if (odd) {
                             wait_rows(&x.full[k_slot], k_phase);
@@ -823,11 +844,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     tmem_after();
 #pragma unroll
                     for (int s = 0; s < kStep / 16; ++s)
-                        mma_ts<Q4>(col_o, col_s + 64 * p_buf + s * 8, v + (s * 16 * 128 >> 4), i > 0 || s > 0);
-                    mma_commit(o_bar);
+                        mma_ts<Q4>(col_o, col_p + 32 * p_buf + s * 8, v + (s * 16 * 128 >> 4), i > 0 || s > 0);
+                    mma_commit(o_bar + p_buf);
                     p_phase ^= 1u << p_buf;
                     p_buf ^= 1;
-                    o_phase ^= 1;
                     if (odd || i + 1 == steps) {
                         mma_commit(&x.empty[v_slot]);
                         advance(v_slot, v_phase);
@@ -876,21 +896,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
 #pragma unroll 1
             for (int i = 0; i < steps; ++i, ++count) {
                 const uint32_t buf = count & 1;
-                ok = warp_wait(a.wait_test ? &x.never : &x.s[part][buf], a.wait_test ? 0 : count >> 1);
+                // S of this step, and P V of the step but one before (issued before that S: over, or nearly)
+                uint64_t *const s_bar = a.wait_test ? &x.never : &x.s[part], *const o_bar = &x.o[part][buf];
+                const uint32_t s_phase = a.wait_test ? 0 : count & 1, o_phase = count >= 2 ? (count - 2) >> 1 & 1 : 1;
+                if (!__all_sync(kFull, bar_try(smem_of(s_bar), s_phase) & bar_try(smem_of(o_bar), o_phase)))
+                    ok = warp_wait(s_bar, s_phase) && warp_wait(o_bar, o_phase);
                 if (!ok)
                     break;
                 tmem_after();
                 float s[kStep];                               // the row's scores
-                tmem_ld32(col_s + 64 * buf, reinterpret_cast<uint32_t *>(s));
-                tmem_ld32(col_s + 64 * buf + 32, reinterpret_cast<uint32_t *>(s) + 32);
+                tmem_ld32(col_s, reinterpret_cast<uint32_t *>(s));
+                tmem_ld32(col_s + 32, reinterpret_cast<uint32_t *>(s) + 32);
                 if (Q4 && i == 0)                             // (written with Q, so there behind the first S)
                     sl2 *= x.q_inv[units & 1][min(mine, u.rows - 1)];
                 const uint32_t *valid = &x.valid[(tile_no + (i >> 1)) % kMaskRing][2 * (i & 1)];
                 uint32_t w0 = valid[0], w1 = valid[1];
+                float step_sum = 0.0f;
                 const int t0 = u.tile0 * kTile + i * kStep;
                 tmem_wait_ld();
                 tmem_loaded(reinterpret_cast<uint32_t *>(s));
                 tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32);
+                tmem_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(&x.r[part]);
                 // does every row of the warp see all of the step's tokens?
                 const bool inside = end0 >= t0 + kStep && (t0 >= low1 || t0 + kStep <= a.sinks);
                 if (!inside || (w0 & w1) != kFull) {
@@ -904,53 +933,66 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                             s[32 + k] = -CUDART_INF_F;
                     }
                 }
-                float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                // P = 2^(x - mref).  A row's reference is its largest score at first and stays as it is until the
+                // sum of a step's P passes kMostSum; then it becomes the largest score so far, O and
+                // l are rescaled and P is done again.  (Rows that do not exist hold anything: not theirs.)
+                bool grow = true, move = i == 0;
+#pragma unroll 1
+                for (int again = move; again < 2; ++again) {
+                    if (move) {
+                        tmem_wait_st();                      // (P goes to the same place once more)
+                        float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-                for (int k = 0; k < kStep; k += 2)
-                    mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-                if (mref == -CUDART_INF_F)
-                    mref = top;                      // nothing summed so far: l = 0 and O = 0
-                // The running maximum lags until a row exceeds it by 2^8: the probabilities
-                // stay below 2^8 and O is rescaled rarely.
-                const bool grow = i > 0 && top > mref + 8.0f;
-                const bool any = __any_sync(kFull, grow);
-                if (any || (i == steps - 1 && i > 0)) {
-                    ok = warp_wait(&x.o[part], count - 1);
-                    if (!ok)
+                        for (int k = 0; k < kStep; k += 2)
+                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                        const float mn = grow ? fmaxf(mref, top) : mref;
+                        const float f = mref == mn || mref == -CUDART_INF_F ? 1.0f : ex2(mref - mn);     // (or l = 0, O = 0)
+                        mref = mn;
+                        if (i > 0) {
+                            l *= f;
+                            ok = warp_wait(&x.o[part][buf ^ 1], (count - 1) >> 1);
+                            if (!ok)
+                                break;
+                            tmem_after();
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t ov[16];
+                                tmem_ld16(col_o + 16 * c, ov);
+                                tmem_wait_ld();
+                                tmem_loaded16(ov);
+#pragma unroll
+                                for (int k = 0; k < 16; k += 2)
+                                    scale2(ov + k, f);
+                                tmem_st16(col_o + 16 * c, ov);
+                            }
+                        }
+                    }
+                    // (a row that has seen nothing: any score that is not -inf gives at least 1)
+                    const float off = mref == -CUDART_INF_F ? kMostFloat : -mref;
+                    const float2 off2 = make_float2(off, off), sl22 = make_float2(sl2, sl2);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 z = __ffma2_rn(make_float2(s[32 * h + 2 * k], s[32 * h + 2 * k + 1]), sl22, off2);
+                            const float2 ev = make_float2(ex2(z.x), ex2(z.y));
+                            sum[k & 1] = __fadd2_rn(sum[k & 1], ev);
+                            pk[k] = Q4 ? pack_f16(ev.x, ev.y) : pack_bf16(ev.x, ev.y);
+                        }
+                        tmem_st16(col_s + kColP + 32 * buf + 16 * h, pk);
+                    }
+                    step_sum = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    grow = live && !(step_sum <= (mref == -CUDART_INF_F ? 0.0f : kMostSum));
+                    move = __any_sync(kFull, grow);
+                    if (!move)
                         break;
                 }
-                if (any) {
-                    tmem_after();
-                    const float mn = grow ? top : mref;
-                    const float f = grow ? ex2(mref - mn) : 1.0f;
-                    mref = mn;
-                    l *= f;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t ov[32];
-                        tmem_ld32(col_o + 32 * c, ov);
-                        tmem_wait_ld();
-                        tmem_loaded(ov);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2)
-                            scale2(ov + k, f);
-                        tmem_st32(col_o + 32 * c, ov);
-                    }
-                }
-                const float off = mref == -CUDART_INF_F ? 0.0f : -mref;
-                const float2 off2 = make_float2(off, off), sl22 = make_float2(sl2, sl2);
-                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                uint32_t pk[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float2 z = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), sl22, off2);
-                    const float2 ev = make_float2(ex2(z.x), ex2(z.y));
-                    sum[k & 1] = __fadd2_rn(sum[k & 1], ev);
-                    pk[k] = Q4 ? pack_f16(ev.x, ev.y) : pack_bf16(ev.x, ev.y);
-                }
-                tmem_st32(col_s + 64 * buf, pk);             // (over scores that have been read)
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                if (!ok)
+                    break;
+                l += step_sum;
                 tmem_wait_st();
                 tmem_before();
                 __syncwarp();
@@ -961,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 break;
             tile_no += tiles;
             // ---- the rows' results
-            ok = warp_wait(&x.o[part], count - 1);
+            ok = warp_wait(&x.o[part][(count - 1) & 1], (count - 1) >> 1);
             if (!ok)
                 break;
             tmem_after();
