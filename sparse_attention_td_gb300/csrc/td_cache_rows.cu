@@ -126,38 +126,62 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
 // position).  A CTA per (request, KV head) finds the weight of the last one kept, then writes
 // the kept positions in order and their weights.
 //
-// The weight is found by three radix passes over order-preserving keys (11, 11 and 10 bits,
+// The weight is found by at most three radix passes over order-preserving keys (11 bits each,
 // counts in shared memory).  Rows of up to 16384 positions stay in registers.  (Found bit by
 // bit with block-wide counts, without atomics, it takes two to three times as long.)
 constexpr int kBins = 2048;
 
-// A weight that is not a number counts as the largest.
-__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xffffffffu : order_key(w); }
+// A weight that is not a number counts as the largest, -0 as 0.  No key is 0 or kAnyCase.
+constexpr uint32_t kAnyCase = 0xffffffffu;
+__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xff800001u : order_key(w); }
 
 // The key of the heavy-th largest candidate (heavy > 0), and in `rest` how many of that key are among
-// the heavy ones.  each(f) calls f(key) for every candidate of the thread.
+// the heavy ones.  each(f) calls f(key) for every candidate of the thread; it may do so with 0, which
+// counts for nothing, and with kAnyCase, which it does `others` times in the block.  The digits begin
+// behind the bits that all candidates share: weights of a few magnitudes else meet in a few bins,
+// whose counts are then added to one after the other.
 template <int T, typename Each>
-__device__ __forceinline__ uint32_t last_key(unsigned *hist, unsigned *sums, unsigned *found, int heavy, unsigned &rest,
+__device__ __forceinline__ uint32_t last_key(unsigned *hist, unsigned *sums, unsigned *found, int heavy, int others, unsigned &rest,
                                              Each each)
 {
+    constexpr int W = T / 32, kDigit = 11, kRun = kBins / T;
+    static_assert(kBins == 1 << kDigit && kBins % T == 0 && W <= 32, "bins per thread");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint32_t key = 0, mask = 0;
-    rest = heavy;
+    uint32_t least = 0xffffffffu, most = 0;
+    each([&](uint32_t k) {
+        least = min(least, k - 1);
+        most = max(most, k + 1);
+    });
+    least = __reduce_min_sync(kFull, least);
+    most = __reduce_max_sync(kFull, most);
+    if (lane == 0) {
+        hist[warp] = least;
+        hist[W + warp] = most;
+    }
+    __syncthreads();
+    least = __reduce_min_sync(kFull, hist[lane % W]) + 1;
+    most = __reduce_max_sync(kFull, hist[W + lane % W]) - 1;
+    __syncthreads();
+    int left = 32 - __clz(least ^ most);             // bits of the key that are open
+    uint32_t mask = left == 32 ? 0u : 0xffffffffu << left, key = most & mask;
+    rest = heavy + (key == (kAnyCase & mask) ? others : 0);
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? kBins / 2 : kBins;
-        for (int i = tid; i < bins; i += T)
+    while (left > 0) {
+        const int shift = max(left - kDigit, 0);
+        const unsigned digits = (1u << (left - shift)) - 1;
+        for (int i = tid; i < kBins; i += T)
             hist[i] = 0;
         __syncthreads();
         each([&](uint32_t k) {
             if ((k & mask) == key)
-                atomicAdd(&hist[k >> shift & (bins - 1)], 1u);
+                atomicAdd(&hist[k >> shift & digits], 1u);
         });
         __syncthreads();
         // Counts from the highest digit down: a thread has a run of bins.
-        const int run = bins / T, top = bins - 1 - tid * run;
+        const int top = kBins - 1 - tid * kRun;
         unsigned mine = 0;
-        for (int k = 0; k < run; ++k)
+#pragma unroll
+        for (int k = 0; k < kRun; ++k)
             mine += hist[top - k];
         unsigned inc = mine;
 #pragma unroll
@@ -169,20 +193,28 @@ __device__ __forceinline__ uint32_t last_key(unsigned *hist, unsigned *sums, uns
         if (lane == 31)
             sums[warp] = inc;
         __syncthreads();
-        unsigned before = inc - mine;
-        for (int i = 0; i < warp; ++i)
-            before += sums[i];
+        unsigned before = inc - mine + __reduce_add_sync(kFull, lane < warp ? sums[lane] : 0u);
         if (before < rest && rest <= before + mine) {
             int d = top;
             for (; before + hist[d] < rest; --d)
                 before += hist[d];
             found[0] = d;
             found[1] = rest - before;
+            found[2] = hist[d];
         }
         __syncthreads();
         key |= found[0] << shift;
-        mask |= (uint32_t)(bins - 1) << shift;
+        mask |= digits << shift;
         rest = found[1];
+        left = shift;
+        if (left > 0 && found[2] == 1) {             // one candidate is left
+            each([&](uint32_t k) {
+                if ((k & mask) == key)
+                    found[3] = k;
+            });
+            __syncthreads();
+            return found[3];
+        }
     }
     return key;
 }
@@ -190,7 +222,7 @@ __device__ __forceinline__ uint32_t last_key(unsigned *hist, unsigned *sums, uns
 template <int T, int NR> __global__ void __launch_bounds__(T) evict_select_short_kernel(const EvictArgs a)
 {
     constexpr int W = T / 32;
-    __shared__ unsigned hist[kBins], sums[W], found[2];
+    __shared__ unsigned hist[kBins], sums[W], found[4];
     __shared__ uint32_t counts[NR * W];            // kept in any case, and (high half) of the last weight
     pdl_wait();
     pdl_launch_dependents();
@@ -217,28 +249,30 @@ template <int T, int NR> __global__ void __launch_bounds__(T) evict_select_short
     const int heavy = a.budget - a.sinks - a.recent;
     const int rounds = (n + T - 1) / T;              // position j T + tid
     float v[NR];
+    uint32_t k[NR];
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
         const int i = j * T + tid;
         v[j] = j < rounds && i < n ? w[i] : 0.0f;
     }
-    auto candidate = [&](int j) { return j * T + tid >= c0 && j * T + tid < c1; };
-    uint32_t key = 0xffffffffu;
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        const int i = j * T + tid;
+        k[j] = i >= n ? 0u : i < c0 || i >= c1 ? kAnyCase : weight_key(v[j]);
+    }
+    uint32_t key = kAnyCase - 1;
     unsigned rest = 0;                               // how many of that key are kept, the lowest positions
     if (heavy > 0)
-        key = last_key<T>(hist, sums, found, heavy, rest, [&](auto f) {
+        key = last_key<T>(hist, sums, found, heavy, a.sinks + a.recent, rest, [&](auto f) {
 #pragma unroll
             for (int j = 0; j < NR; ++j)
-                if (j < rounds && candidate(j))
-                    f(weight_key(v[j]));
+                if (j < rounds)
+                    f(k[j]);
         });
     // Counts of every warp and round, their prefix sums in the positions' order, the places.
     auto flags = [&](int j, uint32_t &sure, uint32_t &equal) {
-        const int i = j * T + tid;
-        const uint32_t k = weight_key(v[j]);
-        const bool in = candidate(j);
-        sure = __ballot_sync(kFull, i < n && (!in || k > key));
-        equal = __ballot_sync(kFull, i < n && in && k == key);
+        sure = __ballot_sync(kFull, k[j] > key);
+        equal = __ballot_sync(kFull, k[j] == key);
     };
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
@@ -293,7 +327,7 @@ constexpr int kSelectPer = 4;
 
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a)
 {
-    __shared__ unsigned hist[kBins], sums[kSelectThreads / 32], found[2];
+    __shared__ unsigned hist[kBins], sums[kSelectThreads / 32], found[4];
     pdl_wait();
     pdl_launch_dependents();
     const int unit = blockIdx.x, b = unit / a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -320,7 +354,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     uint32_t key = 0xffffffffu;
     unsigned rest = 0;                               // how many of that key are kept
     if (heavy > 0)
-        key = last_key<kSelectThreads>(hist, sums, found, heavy, rest, [&](auto f) {
+        key = last_key<kSelectThreads>(hist, sums, found, heavy, 0, rest, [&](auto f) {
             constexpr int kAhead = 8;
             for (int i0 = c0 + tid; i0 < c1; i0 += kAhead * kSelectThreads) {
                 float v[kAhead];
