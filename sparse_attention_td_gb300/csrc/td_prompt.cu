@@ -448,19 +448,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         }
         __syncthreads();
     }
-    // The unit behind a place's.
+    // The unit behind a place's.  (False: there is none, which no cu_new that ascends leads to.)
     auto next_unit_of = [&](Start &w, Request &r) {
         w.at = 0;
         if (++w.h < a.Hkv)
-            return;
+            return true;
         w.h = 0;
         if (++w.block < r.blocks)
-            return;
+            return true;
         w.block = 0;
-        do
+        do {
+            if (r.b + 1 >= a.B)
+                return false;
             r = request(r.b + 1);
-        while (r.blocks == 0 && r.b + 1 < a.B);
+        } while (r.blocks == 0);
         w.b = r.b;
+        return true;
     };
     // Publishes the CTA's units (the scheduler, as far ahead as there are entries).
     auto publish_all = [&] {
@@ -472,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             r = request(w.b);
             const Unit u = unit_of(r, w.block, w.h);
             if (w.at == u.tiles + kUnitCost) {
-                next_unit_of(w, r);
+                if (!next_unit_of(w, r))
+                    left = 0;
                 const Unit v = unit_of(r, w.block, w.h);
                 join = PromptJoin{v.b, v.h, v.q0, v.row0, 0, v.pos0, 0};
             } else {
@@ -500,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 if (u.tiles < all)
                     u.part = 2 * blockIdx.x + (n > 0);
                 left -= end - w.at;
-                if (left > 0)
-                    next_unit_of(w, r);
+                if (left > 0 && !next_unit_of(w, r))
+                    left = 0;
             }
             if (n >= kUnitRing)
                 ok = warp_wait(&x.unit_free[n % kUnitRing], n / kUnitRing - 1);

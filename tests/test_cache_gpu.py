@@ -248,6 +248,32 @@ def test_hidden_values_do_not_reach_rows(q4):
         assert (got - want)[fine].abs().max().item() <= 3e-2 if fine.any() else True
 
 
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("kind", ["up", "down", "waves", "cliff", "last"])
+def test_scores_that_rise_and_fall(kind, q4):
+    """Scores whose maximum moves by far more than the running one may lag, within and between tiles."""
+    n = 700
+    c = Case(17, [n], 4, 1, 0, q4)
+    j = torch.arange(n).float()
+    slope = {"up": j / 4, "down": -j / 4, "waves": 90 * torch.sin(j / 40), "cliff": torch.where(j < 200, -400.0, 0.0),
+             "last": torch.where(j < n - 1, 0.0, 150.0)}[kind]
+    w = torch.sign(c.rnd(D).float())
+    K = (c.K.float() + (slope[:, None] * w * D ** 0.5 / D)).to(torch.bfloat16)       # score: about the slope
+    if q4:
+        codes, scales = quantise(K)
+        c.K = values(codes, scales)
+        c.parts[0].copy_(codes), c.parts[2][..., :8].copy_(scales)
+    else:
+        c.K = K
+        c.parts[0].copy_(K)
+    plain = c.rnd
+    c.rnd = lambda *s: ((plain(*s).float() / 4 + w) / 2).to(torch.bfloat16)          # (they double it)
+    run_new(c, [n], 0, 0)
+    run_new(c, [330], 200, 3)
+    run_tokens(c, 0, 0)
+    run_tokens(c, 300, 2)
+
+
 def test_more_new_tokens_than_cached():
     c = Case(4, [5, 40], 4, 2, 0)
     q = c.rnd(30, 8, D).cuda()

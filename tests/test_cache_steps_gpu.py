@@ -296,6 +296,24 @@ def test_arguments_are_checked():
 
 # --------------------------------------------------- the failure report
 @pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("bad", [[0, 400, 0, 400], [400, 30, 200, 20], [-5, 10, 1 << 30, 7], [400, 400, 400, 0]])
+def test_wrong_borders_then_the_next_call_is_right(bad, q4):
+    """A cu_new that does not ascend: its rows are anyone's, but nothing else is touched."""
+    c = Case(71, [500, 333, 290], 4, 2, 16, q4)
+    q = c.rnd(400, 8, D).cuda()
+    run = td.td_q4_attn if q4 else td.td_window_attn
+    out = torch.zeros(402, 8, D, dtype=torch.bfloat16, device="cuda")
+    run(c.shape, c.cache, 200, 3, i32(bad), q, c.seq, out[1:401], c.ws)
+    torch.cuda.synchronize()
+    assert not out[0].any() and not out[401].any() and not c.ws.status() & td.FLAG_WAIT_TIMEOUT
+    good = i32([0, 100, 400, 400])
+    got, want = torch.zeros_like(q), torch.zeros_like(q)
+    run(c.shape, c.cache, 200, 3, good, q, c.seq, got, c.ws)
+    run(c.shape, c.cache, 200, 3, good, q, c.seq, want, td.Workspace(c.shape, 0, cache_calls=True))
+    assert torch.equal(got, want) and got[100:].any()
+
+
+@pytest.mark.parametrize("q4", [False, True])
 @pytest.mark.parametrize("new", [[100, 300], [1, 1], [700, 3]])
 def test_wait_runs_out_then_the_next_call_is_right(new, q4):
     """The softmax waits for what nothing arrives on: the CTAs give up, report it and leave, and the
