@@ -843,23 +843,25 @@ constexpr int kWeightPer = 4;
 
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightsArgs a, int chunks)
 {
-    pdl_wait();
-    pdl_launch_dependents();
+    // Lengths and sums are there when this kernel may start (the attention kernel, which does not
+    // write them, lets it behind its own wait for what came before): read ahead of the wait, past L1.
+    // (All behind it: 17.2 us where 3 requests of up to 2K positions take 16.2.)
     const int unit = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
     const int b = unit / a.Hkv, g = unit % a.Hkv;
-    uint32_t bad = 0;
-    const int n = seq_len_of(a.seq_lens, b, a.Nmax, bad);
+    const int n = min(max(__ldcg(a.seq_lens + b), 0), a.Nmax);
     const int n0 = chunk * kWeightThreads * kWeightPer + threadIdx.x;
-    if (n0 >= n)
-        return;
     const size_t row0 = (size_t)b * a.Hq + (size_t)g * a.G;
     float *w = a.weights + (size_t)unit * a.Nmax;
     float sum[kWeightPer];
 #pragma unroll
     for (int k = 0; k < kWeightPer; ++k) {
         const int at = n0 + k * kWeightThreads;
-        sum[k] = at < n - a.fresh ? w[at] : 0.0f;
+        sum[k] = at < n - a.fresh ? __ldcg(w + at) : 0.0f;
     }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (n0 >= n)
+        return;
     for (int hd = 0; hd < a.G; ++hd) {
         const float m = a.stat_m[row0 + hd], l = a.stat_l[row0 + hd];
         const float ref = m == -CUDART_INF_F ? 0.0f : m, inv = l == 0.0f ? 0.0f : 1.0f / l;
