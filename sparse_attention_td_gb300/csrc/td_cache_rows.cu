@@ -127,7 +127,9 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
 // the kept positions in order and their weights.
 //
 // The weight is found by at most three radix passes over order-preserving keys (11 bits each,
-// counts in shared memory).  Rows of up to 16384 positions stay in registers.  (Found bit by
+// counts in shared memory).  In place, 32 requests x 8 heads from up to 4224 to 4096 positions:
+// 174 us with the rows' moves, 6.2 TB/s; 7 prompts of 9K .. 16K to 2048: 36.4 us, of which the
+// selection is 14 (56 rows on as many SMs, bound by integer instructions).  Rows of up to 16384 positions stay in registers.  (Found bit by
 // bit with block-wide counts, without atomics, it takes two to three times as long.)
 constexpr int kBins = 2048;
 

@@ -15,6 +15,16 @@
 // by row, so any page size and any window edge is alike.  4-bit rows are decoded to fp16 on
 // their way into shared memory, where they are exact; q and P are then fp16 too (q times
 // a power of two per row).
+//
+// Measured on GB300 (a call in a graph; rates of the visible products alone):
+//   5 prompts of 1021 .. 6144 tokens, 32 query / 8 KV heads, window 1024: 181 us, 1.10 PFLOP/s
+//   3 chunks of 517 .. 1024 tokens on 5K .. 16K tokens in 4 bits:          393 us, 1.17 PFLOP/s
+// A step of 64 tokens is 1272 cycles of MMAs (S with N = 64 reads its Q from shared memory as often
+// as with 128: 380 cycles a row tile, not 256) and about as many of shared memory's, and takes
+// 1700: the softmax warps and the copies share the issue slots (55% taken) and wait on one another.
+// Tried and slower: S of 128 tokens (the row tiles' products fall into step: 4800 cycles where two steps
+// take 3900), S in two places with P over it (205 us), two threads per row (216 and 487 us), results
+// read out behind the next unit's first step (209 and 420), rows stored 32 bytes a lane (186 and 398).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -95,9 +105,9 @@ struct Start {
 //            tile, its arrival behind `full`; the copy warps wait for every use.
 //   q, q_free   as full and empty, per unit.
 //   s[t]     S of step g of row tile t.  Its softmax warps wait for every one.
-//   r[t]     the four softmax warps have S of step g in registers.  Its issuer waits for every one
-//            before it issues the S behind it.
-//   p[t][g & 1]  P of step g, the row tile's four softmax warps; its issuer waits for every one,
+//   r[t]     the row tile's 128 softmax threads have S of step g in registers.  Its issuer waits for
+//            every one before it issues the S behind it.
+//   p[t][g & 1]  P of step g, the row tile's softmax threads; its issuer waits for every one,
 //            and P of g + 2 needs S of g + 2, which is issued behind P V of g.
 //   o[t][g & 1]  P V of a step.  The softmax waits for that of g - 2 before it writes P of g over
 //            that step's, so for every one, and that of g + 2 needs a later P.  For that of g - 1 it
@@ -147,11 +157,12 @@ __device__ __forceinline__ void decode8(uint32_t codes, uint32_t scale, uint32_t
         : "r"(codes), "r"(scale));
 }
 
-// Bits lo .. hi - 1 of 32 that start at bit `base`.
-__device__ __forceinline__ uint32_t bits_of(int lo, int hi, int base)
+// The lowest n of 32 bits (n < 0: none, n > 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n)
 {
-    const int x = max(lo - base, 0), y = min(hi - base, 32);
-    return x >= y ? 0u : (0xffffffffu >> (32 - (y - x))) << x;
+    uint32_t r;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(r) : "r"(max(n, 0)));
+    return r;
 }
 
 // Four neighbouring lanes' rows of two times four 16-byte pieces, turned: lane c of the four then
@@ -268,9 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         bar_init(&x.q_free, kIssuers);
         for (int t = 0; t < 2; ++t) {
             bar_init(&x.s[t], 1);
-            bar_init(&x.r[t], 4);
+            bar_init(&x.r[t], kTile);
             for (int i = 0; i < 2; ++i) {
-                bar_init(&x.p[t][i], 4);
+                bar_init(&x.p[t][i], kTile);
                 bar_init(&x.o[t][i], 1);
             }
         }
@@ -874,6 +885,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t col_s = tmem + 128 * part + lanes, col_o = tmem + kColO + 128 * part + lanes;
         uint32_t count = 0, tile_no = 0;                      // steps of this row tile; tiles of the CTA
+        const uint32_t s_bar = smem_of(a.wait_test ? &x.never : &x.s[part]), s_phases = a.wait_test ? 0 : 1;
+        const uint32_t r_bar = smem_of(&x.r[part]), p_bar = smem_of(&x.p[part][0]), o_bar = smem_of(&x.o[part][0]);
+        auto wait_at = [&](uint32_t bar, uint32_t phase) {
+            return (bool)__all_sync(kFull, bar_try(bar, phase) || bar_wait_long(bar, phase, progress, a.wait_cycles));
+        };
 #pragma unroll 1
         for (; next_unit(); ++units) {
             const Unit &u = unit_entry();
@@ -897,14 +913,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const int end0 = __shfl_sync(kFull, end, 0), low1 = __shfl_sync(kFull, low, 31);
             float sl2 = a.scale * kLog2e;
             float mref = -CUDART_INF_F, l = 0.0f;
+            int t0 = u.tile0 * kTile;                         // first of the step's tokens
 #pragma unroll 1
-            for (int i = 0; i < steps; ++i, ++count) {
+            for (int i = 0; i < steps; ++i, ++count, t0 += kStep) {
                 const uint32_t buf = count & 1;
                 // S of this step, and P V of the step but one before (issued before that S: over, or nearly)
-                uint64_t *const s_bar = a.wait_test ? &x.never : &x.s[part], *const o_bar = &x.o[part][buf];
-                const uint32_t s_phase = a.wait_test ? 0 : count & 1, o_phase = count >= 2 ? (count - 2) >> 1 & 1 : 1;
-                if (!__all_sync(kFull, bar_try(smem_of(s_bar), s_phase) & bar_try(smem_of(o_bar), o_phase)))
-                    ok = warp_wait(s_bar, s_phase) && warp_wait(o_bar, o_phase);
+                const uint32_t s_phase = count & s_phases, o_phase = (count >> 1 & 1) ^ 1;
+                if (!__all_sync(kFull, bar_try(s_bar, s_phase) & bar_try(o_bar + 8 * buf, o_phase)))
+                    ok = wait_at(s_bar, s_phase) && wait_at(o_bar + 8 * buf, o_phase);
                 if (!ok)
                     break;
                 tmem_after();
@@ -915,63 +931,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     sl2 *= x.q_inv[units & 1][min(mine, u.rows - 1)];
                 const uint32_t *valid = &x.valid[(tile_no + (i >> 1)) % kMaskRing][2 * (i & 1)];
                 uint32_t w0 = valid[0], w1 = valid[1];
-                float step_sum = 0.0f;
-                const int t0 = u.tile0 * kTile + i * kStep;
                 tmem_wait_ld();
                 tmem_loaded(reinterpret_cast<uint32_t *>(s));
                 tmem_loaded(reinterpret_cast<uint32_t *>(s) + 32);
                 tmem_before();
-                __syncwarp();
-                if (lane == 0)
-                    bar_arrive(&x.r[part]);
+                arrive_at(r_bar);
                 // does every row of the warp see all of the step's tokens?
                 const bool inside = end0 >= t0 + kStep && (t0 >= low1 || t0 + kStep <= a.sinks);
                 if (!inside || (w0 & w1) != kFull) {
-                    w0 &= bits_of(0, end - t0, 0) & (bits_of(low - t0, kStep, 0) | bits_of(0, a.sinks - t0, 0));
-                    w1 &= bits_of(0, end - t0, 32) & (bits_of(low - t0, kStep, 32) | bits_of(0, a.sinks - t0, 32));
+                    w0 &= low_bits(end - t0) & (~low_bits(low - t0) | low_bits(a.sinks - t0));
+                    w1 &= low_bits(end - t0 - 32) & (~low_bits(low - t0 - 32) | low_bits(a.sinks - t0 - 32));
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (!(w0 >> k & 1u))
-                            s[k] = -CUDART_INF_F;
-                        if (!(w1 >> k & 1u))
-                            s[32 + k] = -CUDART_INF_F;
+                    for (int k0 = 0; k0 < kStep; k0 += 16) {
+                        const uint32_t m = (k0 < 32 ? w0 : w1) >> (k0 & 31);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (!(m & 1u << k))
+                                s[k0 + k] = -CUDART_INF_F;
                     }
                 }
                 // P = 2^(x - mref).  A row's reference is its largest score at first and stays as it is until the
                 // sum of a step's P passes kMostSum; then it becomes the largest score so far, O and
                 // l are rescaled and P is done again.  (Rows that do not exist hold anything: not theirs.)
-                bool grow = true, move = i == 0;
-#pragma unroll 1
-                for (int again = move; again < 2; ++again) {
-                    if (move) {
-                        tmem_wait_st();                      // (P goes to the same place once more)
-                        float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-                        for (int k = 0; k < kStep; k += 2)
-                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-                        const float mn = grow ? fmaxf(mref, top) : mref;
-                        const float f = mref == mn || mref == -CUDART_INF_F ? 1.0f : ex2(mref - mn);     // (or l = 0, O = 0)
-                        mref = mn;
-                        if (i > 0) {
-                            l *= f;
-                            ok = warp_wait(&x.o[part][buf ^ 1], (count - 1) >> 1);
-                            if (!ok)
-                                break;
-                            tmem_after();
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
-                                uint32_t ov[16];
-                                tmem_ld16(col_o + 16 * c, ov);
-                                tmem_wait_ld();
-                                tmem_loaded16(ov);
-#pragma unroll
-                                for (int k = 0; k < 16; k += 2)
-                                    scale2(ov + k, f);
-                                tmem_st16(col_o + 16 * c, ov);
-                            }
-                        }
-                    }
+                float step_sum = 0.0f;
+                auto probabilities = [&] {
                     // (a row that has seen nothing: any score that is not -inf gives at least 1)
                     const float off = mref == -CUDART_INF_F ? kMostFloat : -mref;
                     const float2 off2 = make_float2(off, off), sl22 = make_float2(sl2, sl2);
@@ -989,19 +972,47 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                         tmem_st16(col_s + kColP + 32 * buf + 16 * h, pk);
                     }
                     step_sum = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                };
+                bool grow = true, move = i == 0;
+                if (!move) {
+                    probabilities();
                     grow = live && !(step_sum <= (mref == -CUDART_INF_F ? 0.0f : kMostSum));
                     move = __any_sync(kFull, grow);
-                    if (!move)
-                        break;
                 }
-                if (!ok)
-                    break;
+                if (__builtin_expect(move, 0)) {
+                    tmem_wait_st();                      // (P goes to the same place once more)
+                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                    for (int k = 0; k < kStep; k += 2)
+                        mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], s[k], s[k + 1]);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                    const float mn = grow ? fmaxf(mref, top) : mref;
+                    const float f = mref == mn || mref == -CUDART_INF_F ? 1.0f : ex2(mref - mn);     // (or l = 0, O = 0)
+                    mref = mn;
+                    if (i > 0) {
+                        l *= f;
+                        ok = warp_wait(&x.o[part][buf ^ 1], (count - 1) >> 1);
+                        if (!ok)
+                            break;
+                        tmem_after();
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t ov[16];
+                            tmem_ld16(col_o + 16 * c, ov);
+                            tmem_wait_ld();
+                            tmem_loaded16(ov);
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2)
+                                scale2(ov + k, f);
+                            tmem_st16(col_o + 16 * c, ov);
+                        }
+                    }
+                    probabilities();
+                }
                 l += step_sum;
                 tmem_wait_st();
                 tmem_before();
-                __syncwarp();
-                if (lane == 0)
-                    bar_arrive(&x.p[part][buf]);
+                arrive_at(p_bar + 8 * buf);
             }
             if (!ok)
                 break;
@@ -1014,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const size_t q_row = ((size_t)u.q0 + (row >> a.g_shift)) * a.Hq + (size_t)u.h * a.G + (row & (a.G - 1));
             const bool whole = u.part < 0;
-            float worst = 0.0f;
+            float2 worst = make_float2(0.0f, 0.0f);           // NaN where a value is not finite
             const int q0 = u.q0, unit_row0 = u.row0, unit_rows = u.rows, unit_b = u.b, unit_h = u.h, unit_part = u.part;
             __syncwarp();
             if (lane == 0)
@@ -1038,14 +1049,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                         for (int k = 0; k < 16; ++k) {
                             scale2(ov + 2 * k, inv);
                             const float v0 = __uint_as_float(ov[2 * k]), v1 = __uint_as_float(ov[2 * k + 1]);
-                            worst = fmaf(0.0f, v0, fmaf(0.0f, v1, worst));      // NaN where one is not finite
-                            y[16 * half + k] = l == 0.0f ? 0u : pack_bf16(v0, v1);
+                            worst = __ffma2_rn(make_float2(0.0f, 0.0f), make_float2(v0, v1), worst);
+                            y[16 * half + k] = pack_bf16(v0, v1);
                         }
                     }
                 } else {
                     tmem_ld32(col_o + 32 * c, y);
                     tmem_wait_ld();
                     tmem_loaded(y);
+                }
+                if (whole && __any_sync(kFull, l == 0.0f)) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        y[k] = l == 0.0f ? 0u : y[k];
                 }
                 turn4(y, lane);
 #pragma unroll
@@ -1068,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 a.ws->prompt_l[unit_part][mine] = l;
             }
             tmem_before();
-            uint32_t again = __ballot_sync(kFull, live && whole && l != 0.0f && !(worst == 0.0f));
+            uint32_t again = __ballot_sync(kFull, live && whole && l != 0.0f && !(worst.x + worst.y == 0.0f));
             if (again) {
                 __syncwarp();                        // (the rows' stores come before the second ones)
                 for (; again; again &= again - 1) {

@@ -32,10 +32,11 @@ __device__ __forceinline__ bool elect_one()
     return yes != 0;
 }
 
-__device__ __forceinline__ void bar_arrive(uint64_t *bar)
+__device__ __forceinline__ void arrive_at(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_of(bar)) : "memory");
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) { arrive_at(smem_of(bar)); }
 
 __device__ __forceinline__ void bar_arrive_n(uint64_t *bar, unsigned n)
 {
