@@ -104,11 +104,18 @@ __device__ __forceinline__ void decode2(uint32_t x, int at, uint32_t &lo, uint32
             : "r"(x));
 }
 
-// Two e4m3 scales (low 16 bits of x) as fp16, each twice.
-__device__ __forceinline__ void scales2(uint32_t x, uint32_t &s0, uint32_t &s1)
+// Two e4m3 scales (low 16 bits of x) as fp16.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t x)
 {
     uint32_t s;
     asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s) : "r"(x));
+    return s;
+}
+
+// The same, each twice.
+__device__ __forceinline__ void scales2(uint32_t x, uint32_t &s0, uint32_t &s1)
+{
+    const uint32_t s = scale_pair(x);
     s0 = prmt(s, s, 0x1010);
     s1 = prmt(s, s, 0x3232);
 }
@@ -307,23 +314,30 @@ template <> struct Tokens<true> {
     // rounding (below 2^-14 of the largest, an absolute 2^-25).
     __device__ void pv(float (&o)[8][4], const float (&p)[2][2]) const
     {
-        uint32_t sc[4];
-        scales2(vs[0] | vs[1] << 8, sc[0], sc[1]);
-        scales2(vs[2] | vs[3] << 8, sc[2], sc[3]);
+        // Two tokens' codes of a dim meet in a byte (lower token low) before they are converted, with the
+        // two tokens' scales.
+        const uint32_t sc[2] = {scale_pair(vs[0] | vs[1] << 8), scale_pair(vs[2] | vs[3] << 8)};
         const uint32_t b0 = turned(pack_f16(p[0][0], p[0][1])), b1 = turned(pack_f16(p[1][0], p[1][1]));
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            uint32_t x[4][2];
+        for (int h = 0; h < 2; ++h) {
+            uint32_t x[2][2][4];                      // token pair, even and odd dims, dims / 2
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                decode2(i < 4 ? v[t].x : v[t].y, i & 2, x[t][0], x[t][1]);
-                x[t][0] = mul2(x[t][0], sc[t]);
-                x[t][1] = mul2(x[t][1], sc[t]);
+            for (int t = 0; t < 2; ++t) {
+                constexpr uint32_t low = 0x0f0f0f0f;
+                const uint32_t w0 = h ? v[2 * t].y : v[2 * t].x, w1 = h ? v[2 * t + 1].y : v[2 * t + 1].x;
+                const uint32_t codes[2] = {(w0 & low) | (w1 << 4 & ~low), (w0 >> 4 & low) | (w1 & ~low)};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    decode2(codes[e], 0, x[t][e][0], x[t][e][1]);
+                    decode2(codes[e], 2, x[t][e][2], x[t][e][3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[t][e][k] = mul2(x[t][e][k], sc[t]);
+                }
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                mma<true>(o[i + u], prmt(x[0][u], x[1][u], 0x5410), prmt(x[0][u], x[1][u], 0x7632),
-                          prmt(x[2][u], x[3][u], 0x5410), prmt(x[2][u], x[3][u], 0x7632), b0, b1);
+            for (int k = 0; k < 4; ++k)
+                mma<true>(o[4 * h + k], x[0][0][k], x[0][1][k], x[1][0][k], x[1][1][k], b0, b1);
         }
     }
     __device__ static int dim(int i, int r) { return 16 * r + 2 * i; }
