@@ -84,21 +84,23 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
             // Beyond 6 s the code saturates; 8 s stands for what is larger (only 16 values of
             // which the largest is beyond 448 * 8 have any, as a smaller scale is at
             // least half of the largest / 6).
-            const float most = 8.0f * s;
-            const bool clamp = amax > 8.0f * 448.0f;
-            // (the remainder's sign this way round, so that -0 stays -0)
-            auto quotient = [&](uint32_t bits) {
-                float v = __uint_as_float(bits);
-                if (clamp)
-                    v = fmaxf(fminf(v, most), -most);
-                const float q = v * inv;
-                return fmaf(-fmaf(q, s, -v), inv, q);
-            };
             float q[16];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                q[2 * k] = quotient(x[k] << 16);
-                q[2 * k + 1] = quotient(x[k] & 0xffff0000u);
+                q[2 * k] = __uint_as_float(x[k] << 16);
+                q[2 * k + 1] = __uint_as_float(x[k] & 0xffff0000u);
+            }
+            if (__builtin_expect(amax > 8.0f * 448.0f, 0)) {
+                const float most = 8.0f * s;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    q[k] = fmaxf(fminf(q[k], most), -most);
+            }
+            // (the remainder's sign this way round, so that -0 stays -0)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float v = q[k], y = v * inv;
+                q[k] = fmaf(-fmaf(y, s, -v), inv, y);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -129,8 +131,9 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
 // The weight is found by at most three radix passes over order-preserving keys (11 bits each,
 // counts in shared memory).  In place, 32 requests x 8 heads from up to 4224 to 4096 positions:
 // 174 us with the rows' moves, 6.2 TB/s; 7 prompts of 9K .. 16K to 2048: 36.4 us, of which the
-// selection is 14 (56 rows on as many SMs, bound by integer instructions).  Rows of up to 16384 positions stay in registers.  (Found bit by
-// bit with block-wide counts, without atomics, it takes two to three times as long.)
+// selection is 14 (56 rows on as many SMs, bound by integer instructions).  Rows of up to 16384
+// positions stay in registers.  (Found bit by bit with block-wide counts, without atomics, it
+// takes two to three times as long.)
 constexpr int kBins = 2048;
 
 // A weight that is not a number counts as the largest, -0 as 0.  No key is 0 or kAnyCase.
