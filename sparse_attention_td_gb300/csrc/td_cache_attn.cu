@@ -22,8 +22,8 @@
 //
 // Measured on GB300 (a call in a graph), 32 requests of 8K .. 16K tokens, 32 query / 8 KV heads:
 //   window 4096, 16-bit rows    85 us, 6.3 TB/s: bound by memory
-//   everything, 4-bit rows     101 us, 4.5 TB/s: bound by instructions, 381 for 16 tokens of a KV head
-//                              (a 4-bit value costs one to convert and scale, whatever reads it)
+//   everything, 4-bit rows      95 us, 4.8 TB/s: bound by instructions (a 4-bit value costs one to
+//                              convert and scale, whatever reads it)
 //   a set of 2048 of 32K tokens, 4 requests, 4-bit rows: 12 us, of which two thirds are one
 //                              chain of loads (length, set, page, row) and the join
 //   weights, 1025 .. 4224 tokens: 70 us with the second kernel

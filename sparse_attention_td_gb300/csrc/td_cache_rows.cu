@@ -35,11 +35,10 @@ cudaError_t launch_behind(void (*kernel)(Args, More...), long long grid, int thr
 // where the result is that short (one step from a rounded reciprocal: the remainder
 // x - q s is exact in an fma).  The same holds for the largest value / 6 and the borders of e4m3.
 //
-// Bound by memory once there are enough loads in flight: 32749 tokens of 8 KV heads
-// take 32.4 us (5.3 TB/s).  One block a thread and many threads: two or four a thread, or
-// 4 to 16 CTAs per SM that walk, took 36 to 55 us.
+// Bound by memory: 32749 tokens of 8 KV heads take 28.1 us (6.1 TB/s).  A block of 16 values a thread,
+// 16 CTAs per SM that walk (32: 28.6 us; as many as there are blocks: 31.3).
 constexpr int kQuantThreads = 256;
-constexpr int kQuantCtas = 32;                // per SM, at most
+constexpr int kQuantCtas = 16;                // per SM, at most
 constexpr int kQuantBlocks = kHeadDim / 16;   // of a row
 
 __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4AppendArgs a)
@@ -84,34 +83,34 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
             // Beyond 6 s the code saturates; 8 s stands for what is larger (only 16 values of
             // which the largest is beyond 448 * 8 have any, as a smaller scale is at
             // least half of the largest / 6).
-            float q[16];
+            float2 q[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                q[2 * k] = __uint_as_float(x[k] << 16);
-                q[2 * k + 1] = __uint_as_float(x[k] & 0xffff0000u);
-            }
+            for (int k = 0; k < 8; ++k)
+                q[k] = make_float2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u));
             if (__builtin_expect(amax > 8.0f * 448.0f, 0)) {
                 const float most = 8.0f * s;
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    q[k] = fmaxf(fminf(q[k], most), -most);
+                for (int k = 0; k < 8; ++k)
+                    q[k] = make_float2(fmaxf(fminf(q[k].x, most), -most), fmaxf(fminf(q[k].y, most), -most));
             }
-            // (the remainder's sign this way round, so that -0 stays -0)
+            // Minus the quotient, so that the zeros' signs come out right too.
+            const float2 ninv = make_float2(-inv, -inv), s2 = make_float2(s, s);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float v = q[k], y = v * inv;
-                q[k] = fmaf(-fmaf(y, s, -v), inv, y);
+            for (int k = 0; k < 8; ++k) {
+                const float2 y = __fmul2_rn(q[k], ninv);
+                q[k] = __ffma2_rn(__ffma2_rn(y, s2, q[k]), ninv, y);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float *z = q + 8 * h;
+                const float2 *z = q + 4 * h;
                 uint32_t &out = h ? codes.y : codes.x;
                 asm("{\n\t.reg .b8 a, b, c, d;\n\t"
                     "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
                     "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
                     "mov.b32 %0, {a, b, c, d};\n\t}"
                     : "=r"(out)
-                    : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
+                    : "f"(z[0].x), "f"(z[0].y), "f"(z[1].x), "f"(z[1].y), "f"(z[2].x), "f"(z[2].y), "f"(z[3].x), "f"(z[3].y));
+                out ^= 0x88888888u;
             }
         }
         const uint32_t page = (uint32_t)((uint64_t)slot * a.page_magic >> a.page_shift);
