@@ -1,5 +1,6 @@
 // td_cache_rows.cu -- rows of small caches: quantising new rows into a 4-bit cache, and
 // the eviction of the positions with the least attention weight.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -124,29 +125,51 @@ __global__ void __launch_bounds__(kQuantThreads) q4_append_kernel(const Q4Append
 // ------------------------------------------------------------------- eviction
 // Of request b's n > budget positions and KV head g: the first `sinks`, the last `recent`, and
 // of the others the `heavy` = budget - sinks - recent with the most weight (ties: the lower
-// position).  A CTA per (request, KV head) finds the weight of the last one kept, then writes
-// the kept positions in order and their weights.
+// position).  A CTA, or a cluster of them, per (request, KV head) finds the weight of the last one
+// kept, then writes the kept positions in order and their weights.
 //
 // The weight is found by at most three radix passes over order-preserving keys (11 bits each,
-// counts in shared memory).  In place, 32 requests x 8 heads from up to 4224 to 4096 positions:
-// 174 us with the rows' moves, 6.2 TB/s; 7 prompts of 9K .. 16K to 2048: 36.4 us, of which the
-// selection is 14 (56 rows on as many SMs, bound by integer instructions).  Rows of up to 16384
-// positions stay in registers.  (Found bit by bit with block-wide counts, without atomics, it
-// takes two to three times as long.)
+// counts in shared memory, a cluster's added up by each rank in order: with every thread's own
+// bins read from the other ranks four CTAs take 35 us, not 17).  Rows of up to 131072 positions
+// stay in registers.  In place, 32 requests x 8 heads from up to 4224 to 4096 positions: 174 us with
+// the rows' moves, 6.2 TB/s; 7 prompts of 9K .. 16K to 2048: 34.8 us, of which the selection
+// is 13 (integer instructions and its barriers).  (Found bit by bit with block-wide counts, without
+// atomics, it takes two to three times as long.)
 constexpr int kBins = 2048;
 
 // A weight that is not a number counts as the largest, -0 as 0.  No key is 0 or kAnyCase.
 constexpr uint32_t kAnyCase = 0xffffffffu;
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xff800001u : order_key(w); }
 
+// A row's CTAs, a cluster of C of them or one.
+template <int C> __device__ __forceinline__ void row_sync()
+{
+    if constexpr (C > 1)
+        cooperative_groups::this_cluster().sync();
+    else
+        __syncthreads();
+}
+template <int C, typename X> __device__ __forceinline__ X *of_rank(X *p, int rank)
+{
+    if constexpr (C > 1)
+        return cooperative_groups::this_cluster().map_shared_rank(p, rank);
+    else
+        return p;
+}
+
+template <int T, int C> struct SelectShared {
+    unsigned hist[C > 1 ? 3 : 1][kBins];             // a cluster: this rank's in two of them in turn, the row's
+    unsigned ends[2][T / 32], sums[T / 32], found[4];
+    unsigned totals[2][C];           // of each rank's positions: kept in any case, of the last weight
+};
+
 // The key of the heavy-th largest candidate (heavy > 0), and in `rest` how many of that key are among
 // the heavy ones.  each(f) calls f(key) for every candidate of the thread; it may do so with 0, which
-// counts for nothing, and with kAnyCase, which it does `others` times in the block.  The digits begin
+// counts for nothing, and with kAnyCase, which it does `others` times in the row.  The digits begin
 // behind the bits that all candidates share: weights of a few magnitudes else meet in a few bins,
 // whose counts are then added to one after the other.
-template <int T, typename Each>
-__device__ __forceinline__ uint32_t last_key(unsigned *hist, unsigned *sums, unsigned *found, int heavy, int others, unsigned &rest,
-                                             Each each)
+template <int T, int C, typename Each>
+__device__ __forceinline__ uint32_t last_key(SelectShared<T, C> &x, int heavy, int others, unsigned &rest, Each each)
 {
     constexpr int W = T / 32, kDigit = 11, kRun = kBins / T;
     static_assert(kBins == 1 << kDigit && kBins % T == 0 && W <= 32, "bins per thread");
@@ -159,20 +182,26 @@ __device__ __forceinline__ uint32_t last_key(unsigned *hist, unsigned *sums, uns
     least = __reduce_min_sync(kFull, least);
     most = __reduce_max_sync(kFull, most);
     if (lane == 0) {
-        hist[warp] = least;
-        hist[W + warp] = most;
+        x.ends[0][warp] = least;
+        x.ends[1][warp] = most;
     }
-    __syncthreads();
-    least = __reduce_min_sync(kFull, hist[lane % W]) + 1;
-    most = __reduce_max_sync(kFull, hist[W + lane % W]) - 1;
-    __syncthreads();
+    row_sync<C>();
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+        least = min(least, of_rank<C>(x.ends[0], q)[lane % W]);
+        most = max(most, of_rank<C>(x.ends[1], q)[lane % W]);
+    }
+    least = __reduce_min_sync(kFull, least) + 1;
+    most = __reduce_max_sync(kFull, most) - 1;
     int left = 32 - __clz(least ^ most);             // bits of the key that are open
     uint32_t mask = left == 32 ? 0u : 0xffffffffu << left, key = most & mask;
     rest = heavy + (key == (kAnyCase & mask) ? others : 0);
 #pragma unroll 1
-    while (left > 0) {
+    for (int pass = 0; left > 0; ++pass) {
         const int shift = max(left - kDigit, 0);
         const unsigned digits = (1u << (left - shift)) - 1;
+        // (In a cluster two arrays in turn: one is cleared when every rank has read it, two passes ago.)
+        unsigned *const hist = x.hist[C > 1 ? pass & 1 : 0];
         for (int i = tid; i < kBins; i += T)
             hist[i] = 0;
         __syncthreads();
@@ -180,13 +209,27 @@ __device__ __forceinline__ uint32_t last_key(unsigned *hist, unsigned *sums, uns
             if ((k & mask) == key)
                 atomicAdd(&hist[k >> shift & digits], 1u);
         });
-        __syncthreads();
+        row_sync<C>();
+        if constexpr (C > 1) {
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                unsigned sum = 0;
+#pragma unroll
+                for (int q = 0; q < C; ++q)
+                    sum += of_rank<C>(hist, q)[i * T + tid];
+                x.hist[2][i * T + tid] = sum;
+            }
+            __syncthreads();
+        }
+        const unsigned *const all = x.hist[C > 1 ? 2 : 0];
         // Counts from the highest digit down: a thread has a run of bins.
         const int top = kBins - 1 - tid * kRun;
-        unsigned mine = 0;
+        unsigned bins[kRun], mine = 0;
 #pragma unroll
-        for (int k = 0; k < kRun; ++k)
-            mine += hist[top - k];
+        for (int k = 0; k < kRun; ++k) {
+            bins[k] = all[top - k];
+            mine += bins[k];
+        }
         unsigned inc = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -195,54 +238,57 @@ __device__ __forceinline__ uint32_t last_key(unsigned *hist, unsigned *sums, uns
                 inc += y;
         }
         if (lane == 31)
-            sums[warp] = inc;
+            x.sums[warp] = inc;
         __syncthreads();
-        unsigned before = inc - mine + __reduce_add_sync(kFull, lane < warp ? sums[lane] : 0u);
-        if (before < rest && rest <= before + mine) {
-            int d = top;
-            for (; before + hist[d] < rest; --d)
-                before += hist[d];
-            found[0] = d;
-            found[1] = rest - before;
-            found[2] = hist[d];
+        unsigned before = inc - mine + __reduce_add_sync(kFull, lane < warp ? x.sums[lane] : 0u);
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            if (before < rest && rest <= before + bins[k]) {
+                x.found[0] = top - k;
+                x.found[1] = rest - before;
+                x.found[2] = bins[k];
+            }
+            before += bins[k];
         }
         __syncthreads();
-        key |= found[0] << shift;
+        key |= x.found[0] << shift;
         mask |= digits << shift;
-        rest = found[1];
+        rest = x.found[1];
         left = shift;
-        if (left > 0 && found[2] == 1) {             // one candidate is left
+        if (C == 1 && left > 0 && x.found[2] == 1) {         // one candidate is left
             each([&](uint32_t k) {
                 if ((k & mask) == key)
-                    found[3] = k;
+                    x.found[3] = k;
             });
             __syncthreads();
-            return found[3];
+            return x.found[3];
         }
     }
     return key;
 }
 
-template <int T, int NR> __global__ void __launch_bounds__(T) evict_select_short_kernel(const EvictArgs a)
+// Rows of up to C T NR positions, which stay in registers; a rank has the rank-th part of its row.
+template <int T, int NR, int C> __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(T) evict_select_short_kernel(const EvictArgs a)
 {
     constexpr int W = T / 32;
-    __shared__ unsigned hist[kBins], sums[W], found[4];
+    __shared__ SelectShared<T, C> x;
     __shared__ uint32_t counts[NR * W];            // kept in any case, and (high half) of the last weight
     pdl_wait();
     pdl_launch_dependents();
-    const int unit = blockIdx.x, b = unit / a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int unit = blockIdx.x / C, rank = blockIdx.x % C, b = unit / a.Hkv;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t bad = 0;
     const int n = seq_len_of(a.seq_lens, b, a.Nmax, bad);
     const float *w = a.weights + (size_t)unit * a.Nmax;
     float *out = a.weights_out + (size_t)unit * a.out_row;
     int32_t *kept = a.kept + (size_t)unit * a.budget;
-    if (unit % a.Hkv == 0 && tid == 0) {
+    if (unit % a.Hkv == 0 && rank == 0 && tid == 0) {
         a.seq_lens_out[b] = min(n, a.budget);
         if (bad)
             atomicOr(a.status, bad);
     }
     if (n <= a.budget) {
-        for (int i = tid; i < a.budget; i += T) {
+        for (int i = rank * T + tid; i < a.budget; i += C * T) {
             kept[i] = i < n ? i : -1;
             if (i < n && out != w)
                 out[i] = w[i];
@@ -251,23 +297,24 @@ template <int T, int NR> __global__ void __launch_bounds__(T) evict_select_short
     }
     const int c0 = a.sinks, c1 = n - a.recent;       // the candidates
     const int heavy = a.budget - a.sinks - a.recent;
-    const int rounds = (n + T - 1) / T;              // position j T + tid
+    const int part = (n + C - 1) / C, base = rank * part, count = min(part, n - base);
+    const int rounds = (part + T - 1) / T;           // position base + j T + tid
     float v[NR];
     uint32_t k[NR];
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
         const int i = j * T + tid;
-        v[j] = j < rounds && i < n ? w[i] : 0.0f;
+        v[j] = j < rounds && i < count ? w[base + i] : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
-        const int i = j * T + tid;
-        k[j] = i >= n ? 0u : i < c0 || i >= c1 ? kAnyCase : weight_key(v[j]);
+        const int i = j * T + tid, at = base + i;
+        k[j] = i >= count ? 0u : at < c0 || at >= c1 ? kAnyCase : weight_key(v[j]);
     }
     uint32_t key = kAnyCase - 1;
     unsigned rest = 0;                               // how many of that key are kept, the lowest positions
     if (heavy > 0)
-        key = last_key<T>(hist, sums, found, heavy, a.sinks + a.recent, rest, [&](auto f) {
+        key = last_key(x, heavy, a.sinks + a.recent, rest, [&](auto f) {
 #pragma unroll
             for (int j = 0; j < NR; ++j)
                 if (j < rounds)
@@ -304,8 +351,18 @@ template <int T, int NR> __global__ void __launch_bounds__(T) evict_select_short
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             counts[lane * kPer + i] = mine[i] + inc - all;
+        const uint32_t total = __shfl_sync(kFull, inc, 31);
+        if (lane < C) {
+            of_rank<C>(x.totals[0], lane)[rank] = total & 0xffff;
+            of_rank<C>(x.totals[1], lane)[rank] = total >> 16;
+        }
     }
-    __syncthreads();                                 // (every weight has been read, too)
+    row_sync<C>();                                   // (every weight of the row has been read, too)
+    unsigned sure0 = 0, same0 = 0;                   // of the ranks before
+    for (int q = 0; q < rank; ++q) {
+        sure0 += x.totals[0][q];
+        same0 += x.totals[1][q];
+    }
     const uint32_t below = (1u << lane) - 1;
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
@@ -314,10 +371,11 @@ template <int T, int NR> __global__ void __launch_bounds__(T) evict_select_short
         uint32_t sure, equal;
         flags(j, sure, equal);
         const uint32_t before = counts[j * W + warp];
-        const uint32_t nsure = (before & 0xffff) + __popc(sure & below), nsame = (before >> 16) + __popc(equal & below);
+        const uint32_t nsure = sure0 + (before & 0xffff) + __popc(sure & below);
+        const uint32_t nsame = same0 + (before >> 16) + __popc(equal & below);
         if ((sure >> lane & 1u) || ((equal >> lane & 1u) && nsame < rest)) {
             const uint32_t to = nsure + min(nsame, rest);
-            kept[to] = j * T + tid;
+            kept[to] = base + j * T + tid;
             out[to] = v[j];
         }
     }
@@ -331,7 +389,8 @@ constexpr int kSelectPer = 4;
 
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a)
 {
-    __shared__ unsigned hist[kBins], sums[kSelectThreads / 32], found[4];
+    __shared__ SelectShared<kSelectThreads, 1> x;
+    unsigned *const sums = x.sums;
     pdl_wait();
     pdl_launch_dependents();
     const int unit = blockIdx.x, b = unit / a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -358,7 +417,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     uint32_t key = 0xffffffffu;
     unsigned rest = 0;                               // how many of that key are kept
     if (heavy > 0)
-        key = last_key<kSelectThreads>(hist, sums, found, heavy, 0, rest, [&](auto f) {
+        key = last_key(x, heavy, 0, rest, [&](auto f) {
             constexpr int kAhead = 8;
             for (int i0 = c0 + tid; i0 < c1; i0 += kAhead * kSelectThreads) {
                 float v[kAhead];
@@ -579,9 +638,20 @@ cudaError_t launch_q4_append(const Q4AppendArgs &args, cudaStream_t stream)
 cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream)
 {
     const long long units = (long long)a.B * a.Hkv;
-    const cudaError_t err = a.Nmax <= 8192 ? launch_behind(evict_select_short_kernel<512, 16>, units, 512, stream, a)
-                            : a.Nmax <= 16384 ? launch_behind(evict_select_short_kernel<1024, 16>, units, 1024, stream, a)
-                                              : launch_behind(evict_select_kernel, units, kSelectThreads, stream, a);
+    // Rows are cut over a cluster where one CTA's registers do not hold them (100K positions: 24 us, walked
+    // over 121), and in two where they are long and there are SMs enough (8 rows of 16384: 13.4 us, of
+    // one CTA each 15.0; of 3000 positions 12.8 and 12.1; four CTAs a row: 13.2, but 43 for 35 with 56 rows).
+    cudaError_t err;
+    if (a.Nmax > 131072)
+        err = launch_behind(evict_select_kernel, units, kSelectThreads, stream, a);
+    else if (a.Nmax > 16384)
+        err = launch_behind(evict_select_short_kernel<1024, 16, 8>, units * 8, 1024, stream, a);
+    else if (a.Nmax > 4096 && units * 2 <= sms)
+        err = launch_behind(evict_select_short_kernel<1024, 8, 2>, units * 2, 1024, stream, a);
+    else if (a.Nmax <= 8192)
+        err = launch_behind(evict_select_short_kernel<512, 16, 1>, units, 512, stream, a);
+    else
+        err = launch_behind(evict_select_short_kernel<1024, 16, 1>, units, 1024, stream, a);
     if (err != cudaSuccess)
         return err;
     // Slices of rows (in place) or runs of them (else) until there are about four CTAs per SM.

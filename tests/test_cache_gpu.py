@@ -502,6 +502,35 @@ def test_evict_many_requests_and_long_rows():
         run_evict(c, (torch.rand(1, 1, c.N, generator=c.gen) * 5000).floor(), budget, 1, 2, True)
 
 
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("B,Hkv,N", [(10, 8, 3000), (11, 8, 8193), (3, 1, 2049), (7, 8, 16384), (10, 8, 9000),
+                                     (2, 8, 4097), (1, 2, 16385), (2, 1, 131072), (1, 1, 131073)])
+def test_evict_selection_of_many_and_of_long_rows(B, Hkv, N, few):
+    """Every way through the selection: rows few and many, up to where each way ends."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    shape = td.make_shape(B, Hkv, Hkv, N)
+    k = torch.zeros(B, Hkv, N, D, dtype=torch.bfloat16, device="cuda")
+    at = torch.arange(N, device="cuda")
+    for i, x in enumerate((at // 65536, at // 256 % 256, at % 256)):
+        k[..., i] = x                                           # (exact in bf16)
+    budget, sinks, recent = N // 3, 5, N // 7
+    to = torch.full((B, Hkv, budget, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    w = torch.rand(B, Hkv, N, generator=gen, device="cuda")
+    if few:
+        w = (w * 5).floor()
+    lens = i32([N - 17 * b for b in range(B)])
+    out, kept = torch.zeros(B, Hkv, budget).cuda(), torch.zeros(B, Hkv, budget, dtype=torch.int32).cuda()
+    seq, ws = i32([0] * B), td.Workspace(shape, 0, cache_calls=True)
+    td.td_evict(shape, td.make_cache(k, k), td.make_cache(to, to.clone()), budget, sinks, recent, w, out, lens, seq, kept, ws)
+    fixed = (at < sinks) | (at >= lens[:, None] - recent)
+    key = torch.where(fixed[:, None], 9.0, w).where(at < lens[:, None, None], -1.0)
+    want = key.sort(dim=-1, descending=True, stable=True).indices[..., :budget].sort(dim=-1).values
+    assert torch.equal(kept.long(), want) and torch.equal(out, w.gather(-1, want))
+    rows = (to[..., :3].float() * torch.tensor([65536.0, 256.0, 1.0], device="cuda")).sum(-1)
+    assert torch.equal(rows.long(), want) and ws.status() == 0
+    assert seq.tolist() == [budget] * B
+
+
 def test_evict_pages_that_are_none():
     c = Case(6, [200], 1, 1, 16)
     c.dev_table[0, 3] = -1
