@@ -24,7 +24,7 @@
 //   window 4096, 16-bit rows    85 us, 6.3 TB/s: bound by memory
 //   everything, 4-bit rows      95 us, 4.8 TB/s: bound by instructions (a 4-bit value costs one to
 //                              convert and scale, whatever reads it)
-//   a set of 2048 of 32K tokens, 4 requests, 4-bit rows: 12 us, of which two thirds are one
+//   a set of 2048 of 32K tokens, 4 requests, 4-bit rows: 10.7 us, of which two thirds are one
 //                              chain of loads (length, set, page, row) and the join
 //   weights, 1025 .. 4224 tokens: 70 us with the second kernel
 #include <cuda_bf16.h>
@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+constexpr float kJoinCost = 20.0f;
 constexpr int kHeads = 8;             // columns of the products; heads behind G are zero
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
@@ -415,8 +416,13 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 at += sm_sums[i];
             total += sm_sums[i];
         }
-        // (at least a group for each warp)
-        per = max(kWarps, (int)((uint32_t)(total + gridDim.x - 1) / gridDim.x));
+        // Few groups for many SMs: a part more costs the join (80 ns of one CTA), a group more each warp
+        // (1 us), so that sqrt(groups of a unit / kJoinCost) groups a warp cost the least; no more
+        // than one unit has.  (1 x 16000 tokens, one KV head: 13.5 us, a group a warp 26.3; 4-bit sets of
+        // 2048 10.7 and 12.0; 1 x 16 tokens, 8 KV heads: 3.9, four units a CTA 10.5.)
+        const int unit = max((int)((uint32_t)total / (uint32_t)(a.B * a.Hkv)), 1);
+        const int least = kWarps * max((int)(sqrtf((float)unit / kJoinCost) + 0.5f), 1);
+        per = max(min(least, unit), (int)((uint32_t)(total + gridDim.x - 1) / gridDim.x));
         const int64_t start = (int64_t)blockIdx.x * per;
         if (start < total && at <= start && start < at + mine) {
             for (int b = b0; b < b1; ++b) {
@@ -824,8 +830,8 @@ cudaError_t launch(const CacheAttnArgs &a, int sms, cudaStream_t stream)
         most = (int64_t)a.B * a.Hkv * ((count + 16 * U - 1) / (16 * U) + 1);
     }
     int64_t ctas = (int64_t)sms * CTAS;
-    if (ctas > (most + kWarps - 1) / kWarps)
-        ctas = (most + kWarps - 1) / kWarps;
+    if (ctas > most)
+        ctas = most;
     if (ctas > kMaxCacheCtas)
         ctas = kMaxCacheCtas;
     constexpr size_t smem = (size_t)kWarps * (Q4 ? kStages * kStageBytes : kHeads * kHeadDim * sizeof(float));
