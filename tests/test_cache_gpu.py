@@ -209,6 +209,13 @@ def test_new_many_requests(q4):
     run_new(Case(5, lens, 4, 2, 8, q4), [min(n, 1 + (i * 13) % 40) if i % 9 else 0 for i, n in enumerate(lens)], 30, 2)
 
 
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("G,new,window", [(1, [3, 0], 0), (4, [70, 9], 0), (8, [5, 40], 3001), (2, [200, 131], 0)])
+def test_few_new_tokens_on_long_contexts(G, new, window, q4):
+    """Units of many times a CTA's share: every one is cut often."""
+    run_new(Case(sum(new) + G, [5003, 4100], G, 1, 48, q4), new, window, 3)
+
+
 def test_forms_agree():
     """One token per request through both forms."""
     c = Case(9, [700, 129, 64], 4, 2, 16)
