@@ -26,7 +26,7 @@
 //                              convert and scale, whatever reads it)
 //   a set of 2048 of 32K tokens, 4 requests, 4-bit rows: 10.7 us, of which two thirds are one
 //                              chain of loads (length, set, page, row) and the join
-//   weights, 1025 .. 4224 tokens: 70 us with the second kernel
+//   weights, 1025 .. 4224 tokens: 70 us with the second kernel; 3 requests of 257 .. 2050: 15.5
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -43,7 +43,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kJoinCost = 20.0f;
+constexpr float kJoinCost = 30.0f;
 constexpr int kHeads = 8;             // columns of the products; heads behind G are zero
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
@@ -416,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 at += sm_sums[i];
             total += sm_sums[i];
         }
-        // Few groups for many SMs: a part more costs the join (80 ns of one CTA), a group more each warp
-        // (1 us), so that sqrt(groups of a unit / kJoinCost) groups a warp cost the least; no more
-        // than one unit has.  (1 x 16000 tokens, one KV head: 13.5 us, a group a warp 26.3; 4-bit sets of
+        // Few groups for many SMs: a part more costs the join (60 ns of one CTA), a group more each warp
+        // (1 to 2 us), so that sqrt(groups of a unit / kJoinCost) groups a warp cost the least; no more
+        // than one unit has.  (1 x 16000 tokens, one KV head: 11.4 us, a group a warp 26.3; 4-bit sets of
         // 2048 10.7 and 12.0; 1 x 16 tokens, 8 KV heads: 3.9, four units a CTA 10.5.)
         const int unit = max((int)((uint32_t)total / (uint32_t)(a.B * a.Hkv)), 1);
         const int least = kWarps * max((int)(sqrtf((float)unit / kJoinCost) + 0.5f), 1);
@@ -757,45 +757,58 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                     a.ws->tickets[c0] = 0;
                 // CTA c0's part is its second one where the unit starts inside its range.
                 const int late = (int64_t)c0 * per < u0 ? 1 : 0;
-                // A warp per head: 20 parts of 4 heads take two trips to memory, not ten.
+                // A warp per head; the outputs of kAhead parts are on their way at a time, the maxima
+                // and sums of 32.
                 for (int hd = warp; hd < a.G; hd += kWarps) {
                     float M = -CUDART_INF_F, L = 0.0f;
                     float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    constexpr int kAhead = 12;
-                    for (int s0 = c0; s0 <= c1; s0 += kAhead) {
-                        float ms[kAhead], ls[kAhead], mn = M;
-                        float4 os[kAhead];
+                    constexpr int kAhead = 16;
+                    for (int s0 = c0; s0 <= c1; s0 += 32) {
+                        auto slot_of = [&](int s) { return 2 * s + (s == c0 ? late : 0); };
+                        float m1 = -CUDART_INF_F, l1 = 0.0f;
+                        if (s0 + lane <= c1) {
+                            m1 = __ldcg(&a.ws->part_m[slot_of(s0 + lane)][hd]);
+                            l1 = __ldcg(&a.ws->part_l[slot_of(s0 + lane)][hd]);
+                        }
+                        float f1 = 0.0f;
+#pragma unroll 1
+                        for (int h0 = 0; h0 < 32 && s0 + h0 <= c1; h0 += kAhead) {
+                            float4 os[kAhead];
 #pragma unroll
-                        for (int k = 0; k < kAhead; ++k) {
-                            ms[k] = -CUDART_INF_F;
-                            ls[k] = 0.0f;
-                            os[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (s0 + k <= c1) {
-                                const int at = 2 * (s0 + k) + (s0 + k == c0 ? late : 0);
-                                ms[k] = __ldcg(&a.ws->part_m[at][hd]);
-                                ls[k] = __ldcg(&a.ws->part_l[at][hd]);
-                                os[k] = __ldcg(reinterpret_cast<const float4 *>(&a.ws->part_o[at][hd][4 * lane]));
+                            for (int k = 0; k < kAhead; ++k) {
+                                os[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                if (s0 + h0 + k <= c1)
+                                    os[k] = __ldcg(reinterpret_cast<const float4 *>(&a.ws->part_o[slot_of(s0 + h0 + k)][hd][4 * lane]));
+                            }
+                            if (h0 == 0) {
+                                float mn = m1;
+#pragma unroll
+                                for (int d = 16; d; d >>= 1)
+                                    mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, d));
+                                mn = fmaxf(M, mn);
+                                const float keep = weight(M, mn);
+                                M = mn;
+                                L *= keep;
+                                O.x *= keep;
+                                O.y *= keep;
+                                O.z *= keep;
+                                O.w *= keep;
+                                f1 = weight(m1, mn);
+                                float sum = l1 * f1;
+#pragma unroll
+                                for (int d = 16; d; d >>= 1)
+                                    sum += __shfl_xor_sync(kFull, sum, d);
+                                L += sum;
+                            }
+#pragma unroll
+                            for (int k = 0; k < kAhead; ++k) {
+                                const float f = __shfl_sync(kFull, f1, h0 + k);
+                                O.x += os[k].x * f;
+                                O.y += os[k].y * f;
+                                O.z += os[k].z * f;
+                                O.w += os[k].w * f;
                             }
                         }
-#pragma unroll
-                        for (int k = 0; k < kAhead; ++k)
-                            mn = fmaxf(mn, ms[k]);
-                        const float keep = weight(M, mn);
-                        L *= keep;
-                        O.x *= keep;
-                        O.y *= keep;
-                        O.z *= keep;
-                        O.w *= keep;
-#pragma unroll
-                        for (int k = 0; k < kAhead; ++k) {
-                            const float f = weight(ms[k], mn);
-                            L += ls[k] * f;
-                            O.x += os[k].x * f;
-                            O.y += os[k].y * f;
-                            O.z += os[k].z * f;
-                            O.w += os[k].w * f;
-                        }
-                        M = mn;
                     }
                     uint2 y = make_uint2(0u, 0u);
                     if (L != 0.0f)
