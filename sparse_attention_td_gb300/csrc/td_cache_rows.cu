@@ -498,7 +498,9 @@ constexpr int kMoveList = 1024;
 __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const EvictArgs a, int log_slices, int runs)
 {
     __shared__ int sm_from[kMoveList], sm_to[kMoveList];        // cache rows; to -1: nothing to move
-    __shared__ int sm_first;
+    // The first entry of a list that moves.  Two words in turn: no barrier lies between a warp's read of one
+    // and the reset for the next list, but one lies between that read and the reset after it.
+    __shared__ int sm_first[2];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
@@ -524,10 +526,10 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
     const int off = (slice * lanes + tid % lanes) * 16;
     const uint8_t *from = (isv ? a.from.v : a.from.k) + off;
     uint8_t *to = (uint8_t *)(isv ? a.to_v : a.to_k) + off;
-    for (int base = first; base < end; base += kMoveList) {
+    for (int base = first, pass = 0; base < end; base += kMoveList, pass ^= 1) {
         const int list = min(kMoveList, end - base);
         if (tid == 0)
-            sm_first = list;
+            sm_first[pass] = list;
         __syncthreads();                           // (the list before has been read)
         constexpr int kFind = kMoveList / kMoveThreads;
         int p[kFind], pages[kFind], to_pages[kFind];
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
                     flags |= kFlagPageOutOfRange;
                     t = -1;
                 } else {
-                    atomicMin(&sm_first, i);
+                    atomicMin(&sm_first[pass], i);
                 }
             }
             sm_from[i] = f;
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
                 if (dst[k] >= 0)
                     *reinterpret_cast<uint4 *>(to + (size_t)dst[k] * (kHeadDim * 2)) = v[k];
         };
-        int i0 = sm_first / rows * rows;
+        int i0 = sm_first[pass] / rows * rows;
         if (i0 < list)
             read(i0, x[0], row[0]);
         for (; i0 < list; i0 += 2 * rows) {
