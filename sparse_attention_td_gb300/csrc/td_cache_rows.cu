@@ -320,6 +320,8 @@ template <int T, int NR, int C> __global__ void __cluster_dims__(C, 1, 1) __laun
                 if (j < rounds)
                     f(k[j]);
         });
+    else
+        row_sync<C>();       // (last_key's: every rank has begun before its shared memory is written below)
     // Counts of every warp and round, their prefix sums in the positions' order, the places.
     auto flags = [&](int j, uint32_t &sure, uint32_t &equal) {
         sure = __ballot_sync(kFull, k[j] > key);

@@ -110,3 +110,24 @@ def test_many_requests_with_several_lists_each():
         kept = c.evict(td.make_cache(k, v), w, budget, 3, 100, torch.zeros(c.B, c.Hkv, budget, device="cuda"))
         assert torch.equal(kept, want)
         c.check_rows(k, v, want)
+
+
+@pytest.mark.parametrize("place", [True, False])
+@pytest.mark.parametrize("B,N", [(3, 1000), (2, 4097), (40, 9000), (2, 16385), (1, 131072), (1, 131073)])
+def test_first_and_last_positions_alone(B, N, place):
+    """budget = sinks + recent: no weight decides, on every way through the selection."""
+    c = Numbered([N - 7 * b for b in range(B)], 2, N)
+    budget, sinks = 700, 11
+    w = torch.rand(B, 2, N, device="cuda")
+    want, old = c.wanted(w, budget, sinks, budget - sinks), w.clone()
+    for b, n in enumerate(c.lens):
+        assert want[b, 0].tolist() == list(range(sinks)) + list(range(n - budget + sinks, n))
+    if place:
+        k, v, out = c.k, c.v, w
+        kept = c.evict(c.cache, w, budget, sinks, budget - sinks)
+    else:
+        k, v = (torch.zeros(B, 2, budget, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        out = torch.zeros(B, 2, budget, device="cuda")
+        kept = c.evict(td.make_cache(k, v), w, budget, sinks, budget - sinks, out)
+    assert torch.equal(kept, want) and torch.equal(out[..., :budget], old.gather(-1, want))
+    c.check_rows(k, v, want)
