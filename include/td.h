@@ -649,7 +649,10 @@ td_status td_weights_attn(const td_shape *shape, const td_cache *cache, int32_t 
  * min(seq_lens[b], budget).  A request with no more than budget positions keeps them all.  (Heads keep
  * different positions, so the rows of one position are not those of one token afterwards.)
  *   cache, to  `to` may be the same cache (in place: rows behind the last kept one are left
- *              as they were), hold other pages of the same pool, or be a cache of its own. Both
+ *              as they were), hold pages of the same pool, or be a cache of its own.  Of one pool,
+ *              each block of a request has the page that the same block of `cache` has (a shorter
+ *              copy of the table: in place, if slower than with the table itself) or one of
+ *              no block of `cache`.  Both
  *              with shape's num_kv_heads; `to` holds at least min(budget, max_seq_len)
  *              positions per request.  Requests must not share pages that are written.
  *   budget     >= 1, sinks + recent <= budget, sinks, recent >= 0.

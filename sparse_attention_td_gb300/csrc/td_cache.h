@@ -125,6 +125,7 @@ struct EvictArgs {
     uint32_t *status;
     int B, Hkv, Nmax, out_row, budget, sinks, recent;
     int place;                  // from and to are the same cache
+    int pool;                   // .. or have pages of the same pool
 };
 cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream);
 

@@ -355,6 +355,7 @@ td_status td_evict(const td_shape *shape, const td_cache *cache, const td_cache 
     a.sinks = sinks;
     a.recent = recent;
     a.place = place;
+    a.pool = pool;
     return td::launch_evict(a, td::host_sm_count(), (cudaStream_t)stream) == cudaSuccess ? TD_OK : TD_ERR_CUDA;
 }
 

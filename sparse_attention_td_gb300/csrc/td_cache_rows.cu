@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 // read lies at or behind the row that it goes to: a CTA that takes its rows in order, in
 // chunks that are read before they are written, overwrites no row that is still to be read.
 // A CTA has K or V of one (request, KV head), whole rows or a slice of each, where there are
-// few; between two caches the rows are also cut into runs.  Cache rows are looked up
+// few; between two caches, or pages, the rows are also cut into runs.  Cache rows are looked up
 // kMoveList at a time; a chunk is read while the one before is written.
 constexpr int kMoveThreads = 256;
 constexpr int kMovePer = 8;       // (4 with 3 or 4 CTAs per SM: 219 and 191 us where this takes 176)
@@ -522,8 +522,23 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
     const int lanes = 16 >> log_slices;            // of a row (or its slice), 16 bytes each
     const int step = kMoveThreads / lanes, rows = step * kMovePer;      // rows of a chunk
     const int chunks = (count + rows - 1) / rows;
-    const int first = (int)((long long)chunks * run / runs) * rows;
-    const int end = min(count, (int)((long long)chunks * (run + 1) / runs) * rows);
+    int first = (int)((long long)chunks * run / runs) * rows;
+    int end = min(count, (int)((long long)chunks * (run + 1) / runs) * rows);
+    bool ordered = a.place;
+    if (a.pool && !a.place && count > 0) {
+        // Two tables of one pool: a request with a block of the same page in both moves as in place, by
+        // its first CTA.
+        bool same = false;
+        for (int j = tid; j <= block_of(a.to, count - 1); j += kMoveThreads)
+            same = same || a.from.table[(size_t)b * a.from.max_blocks + j] == a.to.table[(size_t)b * a.to.max_blocks + j];
+        ordered = __syncthreads_or(same);
+        if (ordered) {
+            if (run > 0)
+                return;
+            first = 0;
+            end = count;
+        }
+    }
     const int32_t *kept = a.kept + (size_t)unit * a.budget;
     const int off = (slice * lanes + tid % lanes) * 16;
     const uint8_t *from = (isv ? a.from.v : a.from.k) + off;
@@ -558,6 +573,8 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
                 if (f < 0 || t < 0) {
                     flags |= kFlagPageOutOfRange;
                     t = -1;
+                } else if (a.pool && f == t) {
+                    t = -1;                        // (stays where it is)
                 } else {
                     atomicMin(&sm_first[pass], i);
                 }
@@ -578,7 +595,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
             }
         };
         auto write = [&](const uint4 (&v)[kMovePer], const int (&dst)[kMovePer]) {
-            if (a.place)
+            if (ordered)
                 __syncthreads();                   // every row of this chunk has been read
 #pragma unroll
             for (int k = 0; k < kMovePer; ++k)

@@ -131,3 +131,30 @@ def test_first_and_last_positions_alone(B, N, place):
         kept = c.evict(td.make_cache(k, v), w, budget, sinks, budget - sinks, out)
     assert torch.equal(kept, want) and torch.equal(out[..., :budget], old.gather(-1, want))
     c.check_rows(k, v, want)
+
+
+@pytest.mark.parametrize("blocks", ["same", "some", "other"])
+@pytest.mark.parametrize("B,N,page,budget", [(3, 600, 16, 100), (2, 5000, 64, 2500), (1, 9000, 48, 1025), (60, 300, 8, 64)])
+def test_two_tables_of_one_pool(B, N, page, budget, blocks):
+    """The kept rows go by a shorter copy of the cache's table, by pages of their own, or some of each."""
+    need = -(-budget // page)
+    lens = [N - 11 * (b % 20) if b % 3 < 2 else budget - b for b in range(B)]      # (some keep all they have)
+    c = Numbered(lens, 2, N, page, spare=B * need)
+    spare = c.spare.view(B, need)
+    table = c.table[:, :need].clone()
+    if blocks == "other":
+        table = spare.clone()
+    elif blocks == "some":
+        pick = torch.rand(B, need, device="cuda") < 0.5
+        pick[0] = True                                                       # (a request with none of its own)
+        table = torch.where(pick, spare, table)
+    w = torch.rand(B, 2, N, device="cuda")
+    want = c.wanted(w, budget, 2, 9)
+    before = [x.clone() for x in (c.k, c.v)]
+    out = torch.zeros(B, 2, budget, device="cuda")
+    kept = c.evict(td.make_cache(c.k, c.v, table.contiguous()), w, budget, 2, 9, out)
+    assert torch.equal(kept, want)
+    c.check_rows(c.k, c.v, want, table)
+    left = torch.ones(len(c.k), dtype=torch.bool, device="cuda")
+    left[table.long().flatten()] = False
+    assert torch.equal(c.k[left], before[0][left]) and torch.equal(c.v[left], before[1][left])
