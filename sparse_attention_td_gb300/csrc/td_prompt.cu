@@ -211,8 +211,10 @@ __device__ float4 row_values(const RowsArgs &c, bool v, int row, int lane)
 
 // One query row by a warp, a position at a time: for rows whose tiles held values that are
 // not finite, which in a product meet the zero probabilities of tokens that the row does not
-// see.  Rare, and out of line.
-__device__ __noinline__ void attend_row(const PromptArgs &a, int b, int h, int p, size_t q_row, int lane)
+// see.  Rare, and out of line.  `walked` (or null) counts on: a CTA's other roles wait for the warp, for
+// longer than a wait without progress may take.
+__device__ __noinline__ void attend_row(const PromptArgs &a, int b, int h, int p, size_t q_row, int lane,
+                                        uint32_t *walked)
 {
     const uint2 y = *reinterpret_cast<const uint2 *>(a.q + q_row * kHeadDim + 4 * lane);
     const float4 q = make_float4(bf_lo(y.x), bf_hi(y.x), bf_lo(y.y), bf_hi(y.y));
@@ -221,6 +223,8 @@ __device__ __noinline__ void attend_row(const PromptArgs &a, int b, int h, int p
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
     for (int t = 0; t < w.first + p + 1 - w.low; ++t) {
+        if (walked && (t & 63) == 0 && lane == 0)
+            atomicAdd(walked, 1u);
         const int j = t < w.first ? t : w.low + t - w.first;
         const int row = row_of(a.rows, a.Hkv, h, j, page_of(a.rows, b, j));
         if (row < 0)
@@ -1095,7 +1099,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 __syncwarp();                        // (the rows' stores come before the second ones)
                 for (; again; again &= again - 1) {
                     const int k = __ffs(again) - 1;
-                    attend_row(a, unit_b, unit_h, __shfl_sync(kFull, p, k), __shfl_sync(kFull, (unsigned long long)q_row, k), lane);
+                    attend_row(a, unit_b, unit_h, __shfl_sync(kFull, p, k), __shfl_sync(kFull, (unsigned long long)q_row, k),
+                               lane, &x.progress.walked);
                 }
             }
             __syncwarp();
@@ -1186,7 +1191,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const __gr
         const size_t q_row = ((size_t)j.q0 + (row >> a.g_shift)) * a.Hq + (size_t)j.h * a.G + (row & (a.G - 1));
         const float worst = 0.0f * o.x + 0.0f * o.y + 0.0f * o.z + 0.0f * o.w;
         if (__any_sync(kFull, !(worst * inv == 0.0f))) {
-            attend_row(a, j.b, j.h, j.pos0 + (row >> a.g_shift), q_row, lane);
+            attend_row(a, j.b, j.h, j.pos0 + (row >> a.g_shift), q_row, lane, nullptr);
             continue;
         }
         uint2 y;

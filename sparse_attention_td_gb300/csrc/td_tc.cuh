@@ -63,29 +63,31 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity)
     return done != 0;
 }
 
-// What waits look at before they give up: whether another role has, and the tiles done
-// by the CTA so far.
+// What waits look at before they give up: whether another role has, the tiles done
+// by the CTA so far, and what its warps count while they work on something longer than a tile.
 struct Progress {
     int gave_up;
     uint32_t tiles;
+    uint32_t walked;
+    __device__ uint32_t done() const volatile { return tiles + walked; }
 };
 
 // Waits for the phase of the given parity.  Gives up after `limit` cycles of the SM
-// clock without a tile done (a role may have nothing to do for most of a long unit),
+// clock without progress (a role may have nothing to do for most of a long unit),
 // or when another role has (then the CTA leaves as a whole and reports the
 // timeout).  Out of line: the roles' code has to stay in the instruction cache.
 __device__ __noinline__ bool bar_wait_long(uint32_t bar, unsigned parity, volatile Progress *at, long long limit)
 {
     long long t0 = clock64();
-    uint32_t tiles = at->tiles;
+    uint32_t done = at->done();
     for (int polls = 1;; ++polls) {
         if (bar_try(bar, parity))
             return true;
         if ((polls & 63) == 0) {
             if (at->gave_up)
                 return false;
-            if (at->tiles != tiles) {
-                tiles = at->tiles;
+            if (at->done() != done) {
+                done = at->done();
                 t0 = clock64();
             } else if (clock64() - t0 > limit) {
                 at->gave_up = 1;
