@@ -27,7 +27,6 @@
 // read out behind the next unit's first step (209 and 420), rows stored 32 bytes a lane (186 and 398).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -191,58 +190,103 @@ __device__ __forceinline__ void turn4(uint32_t (&y)[32], int lane)
     }
 }
 
-// Four consecutive values of a cached row.
-__device__ float4 row_values(const RowsArgs &c, bool v, int row, int lane)
+// Four consecutive values of a cached row, as they are held: two words of 16-bit values, or four codes and
+// their scale.
+template <bool Q4> __device__ __forceinline__ uint2 row_words(const RowsArgs &c, bool v, int row, int lane)
 {
     const uint8_t *x = v ? c.v : c.k;
-    if (!c.scales) {
-        const uint2 y = *reinterpret_cast<const uint2 *>(x + (size_t)(uint32_t)row * (kHeadDim * 2) + 8 * lane);
-        return make_float4(bf_lo(y.x), bf_hi(y.x), bf_lo(y.y), bf_hi(y.y));
-    }
-    const uint32_t codes = *reinterpret_cast<const uint16_t *>(x + (size_t)(uint32_t)row * kCodeBytes + 2 * lane);
-    const __half_raw s = __nv_cvt_fp8_to_halfraw(c.scales[(size_t)(uint32_t)row * kScaleBytes + (v ? 8 : 0) + lane / 4], __NV_E4M3);
-    const float f = __half2float(__half(s));
-    auto value = [&](uint32_t n) {
-        const float mag = (n & 7) < 2 ? 0.5f * (n & 7) : (float)(2 + (n & 1)) * 0.5f * (float)(1 << ((n >> 1 & 3) - 1));
-        return (n & 8 ? -mag : mag) * f;
-    };
-    return make_float4(value(codes & 15), value(codes >> 4 & 15), value(codes >> 8 & 15), value(codes >> 12));
+    if constexpr (!Q4)
+        return *reinterpret_cast<const uint2 *>(x + (size_t)(uint32_t)row * (kHeadDim * 2) + 8 * lane);
+    return make_uint2(*reinterpret_cast<const uint16_t *>(x + (size_t)(uint32_t)row * kCodeBytes + 2 * lane),
+                      c.scales[(size_t)(uint32_t)row * kScaleBytes + (v ? 8 : 0) + lane / 4]);
 }
 
-// One query row by a warp, a position at a time: for rows whose tiles held values that are
+template <bool Q4> __device__ __forceinline__ float4 row_values(uint2 y)
+{
+    if constexpr (!Q4)
+        return make_float4(bf_lo(y.x), bf_hi(y.x), bf_lo(y.y), bf_hi(y.y));
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .b16 t;\n\t.reg .b32 w, x, s;\n\tmov.b32 {a, b, c, d}, %2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 w, a;\n\tcvt.rn.f16x2.e2m1x2 x, b;\n\t"
+        "cvt.u16.u32 t, %3;\n\tcvt.rn.f16x2.e4m3x2 s, t;\n\t"
+        "mul.rn.f16x2 %0, w, s;\n\tmul.rn.f16x2 %1, x, s;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(y.x), "r"(y.y | y.y << 8));
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return make_float4(f0.x, f0.y, f1.x, f1.y);
+}
+
+// One query row by a warp, kWalk positions at a time: for rows whose tiles held values that are
 // not finite, which in a product meet the zero probabilities of tokens that the row does not
-// see.  Rare, and out of line.  `walked` (or null) counts on: a CTA's other roles wait for the warp, for
+// see.  Rare, and out of line: 16 prompts of 2000 tokens that all see a NaN take 218 ms, over 4-bit rows 169
+// (one position at a time 751 and 1124; without a NaN 0.45 and 0.81).  `walked` (or null) counts on: a CTA's other roles wait for the warp, for
 // longer than a wait without progress may take.
+constexpr int kWalk = 8;
+
+template <bool Q4>
 __device__ __noinline__ void attend_row(const PromptArgs &a, int b, int h, int p, size_t q_row, int lane,
                                         uint32_t *walked)
 {
     const uint2 y = *reinterpret_cast<const uint2 *>(a.q + q_row * kHeadDim + 4 * lane);
     const float4 q = make_float4(bf_lo(y.x), bf_hi(y.x), bf_lo(y.y), bf_hi(y.y));
     const Range w = window_range(p + 1, a.window, a.sinks);
+    const int count = w.first + p + 1 - w.low;
     float m = -CUDART_INF_F, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-    for (int t = 0; t < w.first + p + 1 - w.low; ++t) {
-        if (walked && (t & 63) == 0 && lane == 0)
+    for (int t0 = 0; t0 < count; t0 += kWalk) {
+        if (walked && lane == 0)
             atomicAdd(walked, 1u);
-        const int j = t < w.first ? t : w.low + t - w.first;
-        const int row = row_of(a.rows, a.Hkv, h, j, page_of(a.rows, b, j));
-        if (row < 0)
-            continue;
-        const float4 k = row_values(a.rows, false, row, lane), v = row_values(a.rows, true, row, lane);
-        float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+        // lane k has the row of the k-th position (-1: none)
+        const int t = t0 + lane % kWalk, j = t < w.first ? t : w.low + t - w.first;
+        const int mine = t < count ? row_of(a.rows, a.Hkv, h, j, page_of(a.rows, b, j)) : -1;
+        int rows[kWalk];
+        uint2 kw[kWalk], vw[kWalk];
+#pragma unroll
+        for (int k = 0; k < kWalk; ++k)
+            rows[k] = __shfl_sync(kFull, mine, k);
+#pragma unroll
+        for (int k = 0; k < kWalk; ++k) {
+            kw[k] = row_words<Q4>(a.rows, false, max(rows[k], 0), lane);
+            vw[k] = row_words<Q4>(a.rows, true, max(rows[k], 0), lane);
+        }
+        float x[kWalk], mn = m;
+#pragma unroll
+        for (int k = 0; k < kWalk; ++k) {
+            const float4 key = row_values<Q4>(kw[k]);
+            x[k] = fmaf(q.x, key.x, fmaf(q.y, key.y, fmaf(q.z, key.z, q.w * key.w)));
+        }
 #pragma unroll
         for (int d = 16; d; d >>= 1)
-            s += __shfl_xor_sync(kFull, s, d);
-        const float x = s * (a.scale * kLog2e), mn = fmaxf(m, x);
-        const float f = safe_exp2_diff(m, mn), e = exp2f(x - (mn == -CUDART_INF_F ? 0.0f : mn));
-        m = mn;
+#pragma unroll
+            for (int k = 0; k < kWalk; ++k)
+                x[k] += __shfl_xor_sync(kFull, x[k], d);
+#pragma unroll
+        for (int k = 0; k < kWalk; ++k) {
+            x[k] *= a.scale * kLog2e;
+            mn = rows[k] >= 0 ? fmaxf(mn, x[k]) : mn;
+        }
         // (a sum that is zero has nothing to keep, whatever the factor)
-        l = l * f + e;
-        o.x = o.x * f + e * v.x;
-        o.y = o.y * f + e * v.y;
-        o.z = o.z * f + e * v.z;
-        o.w = o.w * f + e * v.w;
+        const float f = safe_exp2_diff(m, mn), off = mn == -CUDART_INF_F ? 0.0f : mn;
+        m = mn;
+        l *= f;
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
+#pragma unroll
+        for (int k = 0; k < kWalk; ++k) {
+            if (rows[k] < 0)
+                continue;
+            const float e = exp2f(x[k] - off);
+            const float4 v = row_values<Q4>(vw[k]);
+            l += e;
+            o.x += e * v.x;
+            o.y += e * v.y;
+            o.z += e * v.z;
+            o.w += e * v.w;
+        }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint2 r;
@@ -1099,8 +1143,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 __syncwarp();                        // (the rows' stores come before the second ones)
                 for (; again; again &= again - 1) {
                     const int k = __ffs(again) - 1;
-                    attend_row(a, unit_b, unit_h, __shfl_sync(kFull, p, k), __shfl_sync(kFull, (unsigned long long)q_row, k),
-                               lane, &x.progress.walked);
+                    attend_row<Q4>(a, unit_b, unit_h, __shfl_sync(kFull, p, k), __shfl_sync(kFull, (unsigned long long)q_row, k),
+                                   lane, &x.progress.walked);
                 }
             }
             __syncwarp();
@@ -1191,7 +1235,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const __gr
         const size_t q_row = ((size_t)j.q0 + (row >> a.g_shift)) * a.Hq + (size_t)j.h * a.G + (row & (a.G - 1));
         const float worst = 0.0f * o.x + 0.0f * o.y + 0.0f * o.z + 0.0f * o.w;
         if (__any_sync(kFull, !(worst * inv == 0.0f))) {
-            attend_row(a, j.b, j.h, j.pos0 + (row >> a.g_shift), q_row, lane, nullptr);
+            if (a.rows.scales)
+                attend_row<true>(a, j.b, j.h, j.pos0 + (row >> a.g_shift), q_row, lane, nullptr);
+            else
+                attend_row<false>(a, j.b, j.h, j.pos0 + (row >> a.g_shift), q_row, lane, nullptr);
             continue;
         }
         uint2 y;

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import sparse_attention_td_gb300 as td
-from cache_util import D, U, attend
+from cache_util import D, U, attend, visible
 from test_cache_gpu import Case, _built, call, i32, near  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -39,3 +39,35 @@ def test_rows_done_again_outlast_no_wait(q4):
         for h in (0, 13, 31):
             ref, tol, _, _ = attend(q[rows, h], c.K[b, h // G], c.V[b, h // G], sees, 2.0 ** -11 if q4 else U, q4)
             near(out[rows, h], ref, tol)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("lens,new,window,sinks", [([203, 131, 90, 77] * 20, [50, 64, 1, 13] * 20, 37, 5),
+                                                   ([203, 131, 90, 77] * 20, [50, 64, 1, 13] * 20, 0, 0),
+                                                   ([3001, 2050], [30, 9], 0, 0), ([3001, 2050], [30, 9], 1003, 2)])
+def test_rows_done_again_are_right(lens, new, window, sinks, q4):
+    """The last token's value is a NaN that no row but its own sees: the rows beside it are computed one by one, in
+    whole units and in ones that several CTAs share, over pages of which one is none."""
+    c = Case(83, lens, 2, 1, 16, q4)
+    for b, n in enumerate(lens):
+        at = (int(c.table[b, (n - 1) // 16]), 0, (n - 1) % 16)
+        if q4:
+            c.parts[2][at][8:] = 0x7f
+        else:
+            c.parts[1][at] = float("nan")
+    gone = range(16, 32)
+    c.dev_table[:, 1] = -1
+    q = 2 * c.rnd(sum(new), 2, D)
+    out = torch.zeros_like(q).cuda()
+    cu = [0]
+    for t in new:
+        cu.append(cu[-1] + t)
+    call(c)(c.shape, c.cache, window, sinks, i32(cu), q.cuda(), c.seq, out, c.ws)
+    assert c.ws.status() == (0 if window and all(n - t - window >= 32 for n, t in zip(lens, new)) else td.FLAG_PAGE_OUT_OF_RANGE)
+    last = torch.zeros(len(q), dtype=torch.bool)
+    last[[e - 1 for e in cu[1:]]] = True
+    assert out[last].isnan().all()
+    ref, tol = c.attend(q, [(b, list(range(n - t, n))) for b, (n, t) in enumerate(zip(lens, new))],
+                        lambda b, g, p: [j for j in visible(lens[b], p, window, sinks) if j not in gone],
+                        2.0 ** -11 if q4 else U)
+    near(out[~last], ref[~last], tol[~last])
