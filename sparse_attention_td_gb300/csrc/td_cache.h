@@ -71,7 +71,7 @@ struct CacheAttnArgs {
     CacheWs *ws;
     int B, Hq, Hkv, G, Nmax, top_k;
     int window, sinks;          // window 0: every position
-    float scale;
+    float scale, scale2;        // .. and times log2(e)
 };
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, int sms, cudaStream_t stream);
 

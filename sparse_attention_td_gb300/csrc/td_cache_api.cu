@@ -119,6 +119,7 @@ td::CacheAttnArgs token_args(const td_shape &s, const td::RowsArgs &rows, const 
     a.G = s.num_q_heads / s.num_kv_heads;
     a.Nmax = s.max_seq_len;
     a.scale = td::host_scale(s);
+    a.scale2 = a.scale * 1.4426950408889634f;
     return a;
 }
 

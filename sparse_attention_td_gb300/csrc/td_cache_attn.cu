@@ -375,6 +375,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
     __shared__ int sm_start[3];                   // b, KV head, group that the CTA's range starts at
     __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
     __shared__ int sm_last;
+    // Rows of 16 bits: what a unit's end needs again, so that no register holds it through the loop over the unit's
+    // groups (there is none to spare, and no local memory).  The last one is read behind the unit's
+    // last barrier: units take two words in turn.
+    __shared__ volatile int sm_per, sm_stop, sm_begin, sm_end, sm_done[2];
     // The warps' outputs; over 4-bit rows in their rings, which are empty by then.
     extern __shared__ __align__(128) unsigned char sm_raw[];
     constexpr int kPerWarp = Q4 ? kStages * kStageBytes : kHeads * kHeadDim * (int)sizeof(float);
@@ -436,27 +440,46 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 at += g * a.Hkv;
             }
         }
+        if (!Q4 && tid == 0) {
+            sm_per = per;
+            sm_stop = (int)min(start + per, (int64_t)total);
+        }
         __syncthreads();
         if (start >= total)
             return;
     }
-    const int begin = blockIdx.x * per;
-    int left = min(per, total - begin);
+    int at = blockIdx.x * per;                    // groups done, in the whole batch's order
+    int stop = min(at + per, total);
     int b = sm_start[0], h = sm_start[1], grp = sm_start[2];
     Seen seen = seen_of<MODE, GT>(a, b, bad);
     pdl_launch_dependents();
+    // (4 bits: reported at the end, as loads behind a branch wait for it; 16 bits: no register is left for that)
     uint32_t flags = 0;
+    auto report = [&](uint32_t flag) {
+        if constexpr (Q4)
+            flags |= flag;
+        else
+            atomicOr(a.status, flag);
+    };
 
-    for (bool first_seg = true; left > 0; first_seg = false) {
-        const int count = min(left, seen.groups - grp);
+    while (at < stop) {
+        // of the unit's groups those from grp on, up to `end`; the unit's begin and end in the whole batch's order
+        const int end = grp + min(stop - at, seen.groups - grp);
+        int u0 = at - grp, u1 = u0 + seen.groups;
+        at = u0 + end;
+        if (!Q4 && tid == 0) {
+            sm_begin = u0;
+            sm_end = u1;
+            sm_done[(b * a.Hkv + h) & 1] = at;
+        }
         const int32_t *set = MODE == 1 ? a.idx + ((size_t)b * a.Hkv + h) * a.top_k : nullptr;
 
         // Where a token of group i lies, in three steps that are taken for later groups
         // while earlier ones are computed: its position, its page, its row.  A lane
         // has token lane % GT of the group.
         auto position = [&](int i) {
-            const int t = (grp + i) * GT + (lane & (GT - 1));
-            if (i >= count || t >= seen.count)
+            const int t = i * GT + (threadIdx.x & (GT - 1));
+            if (i >= end || t >= seen.count)
                 return -1;
             if (MODE == 1)
                 return set[t];
@@ -464,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
         };
         auto checked = [&](int p) {
             if (MODE == 1 && (p < -1 || p >= seen.n)) {
-                flags |= kFlagIndexOutOfRange;
+                report(kFlagIndexOutOfRange);
                 return -1;
             }
             return p;
@@ -475,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 return -1;
             const int row = row_of(a.rows, a.Hkv, h, p, pg);
             if (row < 0)
-                flags |= kFlagPageOutOfRange;
+                report(kFlagPageOutOfRange);
             return row;
         };
         Block blk[Q4 ? 1 : U];
@@ -500,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
 
         // Positions, pages and rows of the warp's next groups: row is that of group i (16 bits), or
         // of the next group to fill a stage with (4 bits).
-        int i = warp;
+        int i = grp + warp;
         int p0 = checked(position(i)), p1 = checked(position(i + kWarps)), p2 = position(i + 2 * kWarps);
         int pg0 = page(p0), pg1 = page(p1);
         int row = find(p0, pg0), ahead = i;           // ahead: the group whose row `row` is
@@ -517,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
         uint32_t stage = ring;                        // 4 bits: the stage of group i
         auto fill = [&](uint32_t to) {                // with the rows of group `ahead`
             if constexpr (Q4) {
-                if (ahead < count) {
+                if (ahead < end) {
                     Block::fill(a.rows, to, row, lane);
                     row = next_row();
                 }
@@ -528,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
 #pragma unroll 1
             for (int s = 0; s < kStages - 1; ++s)
                 fill(ring + s * kStageBytes);
-        } else if (i < count) {
+        } else if (i < end) {
             load_k(row);
             load_v(row);
         }
@@ -545,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 q[w] = y.x;
                 q[w + 1] = y.y;
             }
-            x2[0] = x2[1] = MODE == 2 ? kLog2e : a.scale * kLog2e;
+            x2[0] = x2[1] = MODE == 2 ? kLog2e : a.scale2;
             if constexpr (Q4) {
                 uint32_t top = 0;
 #pragma unroll
@@ -574,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
             for (int e = 0; e < 4; ++e)
                 o[k][e] = 0.0f;
 
-        for (; i < count; i += kWarps) {
+        for (; i < end; i += kWarps) {
             uint32_t there;
             int next = 0;
             if constexpr (Q4) {
@@ -600,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 }
             }
             if constexpr (!Q4)
-                if (i + kWarps < count)
+                if (i + kWarps < end)
                     load_k(next);
             // s[u][2 t + e]: token 16 u + 8 t + r, head 2c + e; as exponents of 2 times x2
             if constexpr (MODE == 2) {
@@ -608,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const int in = 16 * u + 8 * t + r, at = (grp + i) * GT + in;
+                        const int in = 16 * u + 8 * t + r, at = i * GT + in;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float &x = s[u][2 * t + e];
@@ -678,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
             if constexpr (Q4) {
                 stage = stage == ring + (kStages - 1) * kStageBytes ? ring : stage + kStageBytes;
             } else {
-                if (i + kWarps < count)
+                if (i + kWarps < end)
                     load_v(next);
                 row = next;
             }
@@ -706,11 +729,15 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
             }
         }
         __syncthreads();
-        // This unit's groups in the whole batch's order, and the CTAs that share them.
-        const int u0 = begin + (min(per, total - begin) - left) - grp, u1 = u0 + seen.groups;
+        // The CTAs that share this unit's groups.
+        if (!Q4) {
+            u0 = sm_begin;
+            u1 = sm_end;
+            per = sm_per;
+        }
         const int c0 = u0 / per, c1 = (u1 - 1) / per;
         const bool whole = c0 == c1;
-        const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
+        const int slot = 2 * blockIdx.x + (u0 > (int)blockIdx.x * per);     // (its first part or another)
         const size_t row0 = (size_t)b * a.Hq + (size_t)h * a.G;
         static_assert(kThreads == kHeadDim, "a thread per dim");
         auto weight = [](float ms, float M) { return ms == -CUDART_INF_F ? 1.0f : exp2f(ms - M); };
@@ -822,9 +849,12 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache_attention_kernel(const _
             }
         }
         // ---- the next unit
-        left -= count;
+        if (!Q4) {
+            at = sm_done[(b * a.Hkv + h) & 1];
+            stop = sm_stop;
+        }
         grp = 0;
-        if (left > 0 && ++h == a.Hkv) {
+        if (at < stop && ++h == a.Hkv) {
             h = 0;
             ++b;
             seen = seen_of<MODE, GT>(a, b, bad);

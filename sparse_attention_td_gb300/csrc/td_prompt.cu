@@ -957,12 +957,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             }
             const int mine = part * kTile + r;                // row of the unit
             const bool live = mine < u.rows;
-            const int row = u.row0 + min(mine, u.rows - 1);
-            const int p = u.pos0 + (row >> a.g_shift);        // position
+            auto row_at = [&](int i) { return u.row0 + min(i, u.rows - 1); };
+            auto position_at = [&](int row) { return u.pos0 + (row >> a.g_shift); };
             // what the row sees of the unit's list of tokens: below its own place, and from the
             // window's begin on or among the first ones
             const int shift = u.first - u.low;
-            const int end = p + 1 + shift, low = a.window > 0 ? p - a.window + 1 + shift : 0;
+            const int end = position_at(row_at(mine)) + 1 + shift, low = a.window > 0 ? end - a.window : 0;
             // (of the warp's rows the first one ends first, the last one's window begins last)
             const int end0 = __shfl_sync(kFull, end, 0), low1 = __shfl_sync(kFull, low, 31);
             float sl2 = a.scale * kLog2e;
@@ -1077,6 +1077,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 break;
             tmem_after();
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            // (once more: no register holds them through the steps, and no local memory)
+            const int row = row_at(opaque(mine)), p = position_at(row);
             const size_t q_row = ((size_t)u.q0 + (row >> a.g_shift)) * a.Hq + (size_t)u.h * a.G + (row & (a.G - 1));
             const bool whole = u.part < 0;
             float2 worst = make_float2(0.0f, 0.0f);           // NaN where a value is not finite
