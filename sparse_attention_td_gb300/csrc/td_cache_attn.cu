@@ -869,7 +869,7 @@ cudaError_t launch(const CacheAttnArgs &a, int sms, cudaStream_t stream)
 {
     int64_t most = 0;      // groups, if every request had the most
     {
-        const int count = MODE == 1 ? a.top_k : a.window > 0 && a.Nmax > a.window ? a.window + a.sinks : a.Nmax;
+        const int64_t count = MODE == 1 ? a.top_k : a.window > 0 && a.Nmax > a.window ? (int64_t)a.window + a.sinks : a.Nmax;
         most = (int64_t)a.B * a.Hkv * ((count + 16 * U - 1) / (16 * U) + 1);
     }
     int64_t ctas = (int64_t)sms * CTAS;

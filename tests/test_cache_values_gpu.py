@@ -71,3 +71,26 @@ def test_rows_done_again_are_right(lens, new, window, sinks, q4):
                         lambda b, g, p: [j for j in visible(lens[b], p, window, sinks) if j not in gone],
                         2.0 ** -11 if q4 else U)
     near(out[~last], ref[~last], tol[~last])
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_windows_and_sinks_of_the_largest_size(q4):
+    """max_seq_len = 2^30 over a table of one page, a window and first tokens that add up to 2^31 - 1."""
+    page, blocks, n = 1 << 16, 1 << 14, 300
+    shape = td.make_shape(1, 4, 1, page * blocks)
+    c = Case(84, [n], 4, 1, 0, q4)
+    parts = []
+    for x in c.parts:
+        big = torch.zeros(1, 1, page, x.shape[3], dtype=x.dtype, device="cuda")
+        big[:, :, :n] = x
+        parts.append(big)
+    table = torch.zeros(1, blocks, dtype=torch.int32, device="cuda")
+    cache = td.make_q4_cache(*parts, table) if q4 else td.make_cache(*parts, table)
+    ws = td.Workspace(td.make_shape(1, 4, 1, n), 0, cache_calls=True)
+    for T, cu in ((1, None), (40, i32([0, 40]))):
+        q = 2 * c.rnd(T, 4, D)
+        out = torch.zeros_like(q).cuda()
+        call(c)(shape, cache, (1 << 30) - 1, 1 << 30, cu, q.cuda(), c.seq, out, ws)
+        ref, tol = c.attend(q, [(0, list(range(n - T, n)))], lambda b, g, p: list(range(p + 1)), 2.0 ** -11 if q4 else U)
+        near(out, ref, tol)
+    assert ws.status() == 0
