@@ -497,7 +497,8 @@ constexpr int kMoveThreads = 256;
 constexpr int kMovePer = 8;       // (4 with 3 or 4 CTAs per SM: 219 and 191 us where this takes 176)
 constexpr int kMoveList = 1024;
 
-__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const EvictArgs a, int log_slices, int runs)
+// POOL: two tables of one pool (the other calls have no register for that: 174 us in place became 179).
+template <bool POOL> __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const EvictArgs a, int log_slices, int runs)
 {
     __shared__ int sm_from[kMoveList], sm_to[kMoveList];        // cache rows; to -1: nothing to move
     // The first entry of a list that moves.  Two words in turn: no barrier lies between a warp's read of one
@@ -525,9 +526,8 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
     int first = (int)((long long)chunks * run / runs) * rows;
     int end = min(count, (int)((long long)chunks * (run + 1) / runs) * rows);
     bool ordered = a.place;
-    if (a.pool && !a.place && count > 0) {
-        // Two tables of one pool: a request with a block of the same page in both moves as in place, by
-        // its first CTA.
+    if (POOL && count > 0) {
+        // A request with a block of the same page in both moves as in place, by its first CTA.
         bool same = false;
         for (int j = tid; j <= block_of(a.to, count - 1); j += kMoveThreads)
             same = same || a.from.table[(size_t)b * a.from.max_blocks + j] == a.to.table[(size_t)b * a.to.max_blocks + j];
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
                 if (f < 0 || t < 0) {
                     flags |= kFlagPageOutOfRange;
                     t = -1;
-                } else if (a.pool && f == t) {
+                } else if (POOL && f == t) {
                     t = -1;                        // (stays where it is)
                 } else {
                     atomicMin(&sm_first[pass], i);
@@ -685,7 +685,8 @@ cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream)
         while (runs < chunks && units * 2 * runs < 8ll * sms)
             ++runs;
     }
-    return launch_behind(evict_move_kernel, (units * 2 << log_slices) * runs, kMoveThreads, stream, a, log_slices, runs);
+    return launch_behind(a.pool && !a.place ? evict_move_kernel<true> : evict_move_kernel<false>,
+                         (units * 2 << log_slices) * runs, kMoveThreads, stream, a, log_slices, runs);
 }
 
 }  // namespace td
