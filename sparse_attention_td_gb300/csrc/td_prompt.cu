@@ -219,10 +219,10 @@ template <bool Q4> __device__ __forceinline__ float4 row_values(uint2 y)
 
 // One query row by a warp, kWalk positions at a time: for rows whose tiles held values that are
 // not finite, which in a product meet the zero probabilities of tokens that the row does not
-// see.  Rare, and out of line: 16 prompts of 2000 tokens that all see a NaN take 266 ms, over 4-bit rows 243
-// (one position at a time 751 and 1124, eight 218 and 169, but then the kernel takes 395 us without a
-// NaN where it takes 392; the prompts without a NaN 0.45 and 0.8 ms).  `walked` (or null) counts on: a CTA's other roles wait for the warp, for
-// longer than a wait without progress may take.
+// see.  Rare, and out of line: 16 prompts of 2000 tokens that all see a NaN in some dims take 266 ms, over
+// 4-bit rows 243 (one position at a time 751 and 1124, eight 218 and 169, but then the kernel takes 395 us
+// without a NaN where it takes 392), in all dims 3.4; without one 0.45 and 0.8.  `walked` (or
+// null) counts on: a CTA's other roles wait for the warp, for longer than a wait without progress may take.
 constexpr int kWalk = 4;
 
 template <bool Q4>
@@ -288,6 +288,10 @@ __device__ __noinline__ void attend_row(const PromptArgs &a, int b, int h, int p
             o.z += e * v.z;
             o.w += e * v.w;
         }
+        // (no later position makes a number of a NaN)
+        const float all = fminf(fminf(fabsf(o.x), fabsf(o.y)), fminf(fabsf(o.z), fabsf(o.w)));   // (of the numbers)
+        if (l != 0.0f && __all_sync(kFull, all != all))
+            break;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint2 r;

@@ -10,16 +10,17 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("q4", [False, True])
-def test_rows_done_again_outlast_no_wait(q4):
-    """Prompts between others whose every row sees a NaN: those rows are computed once more, one by one, and take
-    far longer than a wait without progress may."""
+@pytest.mark.parametrize("dims", [16, 128])
+def test_rows_done_again_outlast_no_wait(dims, q4):
+    """Prompts between others whose every row sees a value of which some or all dims are NaN: those rows are
+    computed once more, one by one, and take (in some dims) far longer than a wait without progress may."""
     n, Hkv, G = 600, 8, 4
     c = Case(81, [n] * 8, G, Hkv, 0, q4)
     for b in (0, 2, 5, 6):
         if q4:
-            c.parts[2][b, :, 3, 8:] = 0x7f
+            c.parts[2][b, :, 3, 8:8 + dims // 16] = 0x7f
         else:
-            c.parts[1][b, :, 3] = float("nan")
+            c.parts[1][b, :, 3, :dims] = float("nan")
     q = 2 * c.rnd(8 * n, Hkv * G, D)
     out = torch.zeros_like(q).cuda()
     cu = i32([n * b for b in range(9)])
@@ -34,7 +35,8 @@ def test_rows_done_again_outlast_no_wait(q4):
     for b in range(8):
         rows = slice(n * b, n * b + n)
         if b in (0, 2, 5, 6):
-            assert out[rows][3:].isnan().all() and out[rows][:3].isfinite().all()
+            assert out[rows][3:, :, :dims].isnan().all() and out[rows][:3].isfinite().all()
+            assert out[rows][3:, :, dims:].isfinite().all()
             continue
         for h in (0, 13, 31):
             ref, tol, _, _ = attend(q[rows, h], c.K[b, h // G], c.V[b, h // G], sees, 2.0 ** -11 if q4 else U, q4)
