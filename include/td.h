@@ -582,7 +582,8 @@ size_t td_cache_workspace_size(const td_shape *shape);
  * A token that sees no position (seq_lens[b] = 0; more new tokens than cached ones, which also
  * sets TD_FLAG_SEQ_LEN_OUT_OF_RANGE) gets 0.  K/V values that a token does not see never reach
  * it, whatever they hold.  (Where a unit of 256 query rows meets V values that are not
- * finite, its rows are computed again one by one: right, but slow.)  Scores, statistics and
+ * finite, its rows are computed again one by one: right, but slow, about 0.3 us per
+ * visible position and row, eight rows at a time on each SM.)  Scores, statistics and
  * sums are fp32; with cu_new the probabilities enter the second product as bf16 (relative
  * error at most 2^-8 each), without as two bf16 terms.
  *   shape      max_seq_len bounds seq_lens (a longer one is clamped and flagged); at most
@@ -770,7 +771,7 @@ td_status td_probe_layer_reads(const td_shape *shape, const void *k_cache, const
  *   "wait_limit_us": microseconds after which a staged full-layer CTA stops
  *          waiting for a bulk copy, or a tree-attention CTA (or one of td_window_attn or td_q4_attn
  *          with cu_new) that has finished no tile of 128 tokens meanwhile for its copies and products (default 1 s;
- *          such a CTA that gives up waits, with
+ *          rows that are computed again one by one count as tiles; such a CTA that gives up waits, with
  *          limits, for what it has in flight, sets TD_FLAG_WAIT_TIMEOUT and leaves:
  *          its rows are not valid, the next launch is not affected).  A CTA that gives up waits
  *          (at the default limit) for every copy it issued, then joins the

@@ -1,6 +1,6 @@
 // td_cache.h -- kernel arguments and launchers of the operators on small caches
 // (windows with sinks, 4-bit rows, attention weights and eviction), shared by
-// td_cache_attn.cu, td_prompt.cu, td_evict.cu and td_cache_api.cu (not part of the
+// td_cache_attn.cu, td_prompt.cu, td_cache_rows.cu and td_cache_api.cu (not part of the
 // public C ABI).
 #pragma once
 

@@ -22,8 +22,10 @@
 //
 // Measured on GB300 (a call in a graph), 32 requests of 8K .. 16K tokens, 32 query / 8 KV heads:
 //   window 4096, 16-bit rows    85 us, 6.3 TB/s: bound by memory
-//   everything, 4-bit rows      95 us, 4.8 TB/s: bound by instructions (a 4-bit value costs one to
-//                              convert and scale, whatever reads it)
+//   everything, 4-bit rows      95 us, 4.8 TB/s: no unit is at its limit (issue slots 61%, ALU 53%, DRAM 59%).
+//                              Of a warp's time 9% are waits for memory, 18% issue, 23% fixed latencies,
+//                              21% another warp issues, 17% the conversions' pipe is busy: 3.5
+//                              warps per scheduler, whose instructions follow on one another
 //   a set of 2048 of 32K tokens, 4 requests, 4-bit rows: 10.7 us, of which two thirds are one
 //                              chain of loads (length, set, page, row) and the join
 //   weights, 1025 .. 4224 tokens: 70 us with the second kernel; 3 requests of 257 .. 2050: 15.5

@@ -33,8 +33,8 @@ cudaError_t launch_behind(void (*kernel)(Args, More...), long long grid, int thr
 // values nearest to x / s (ties to the even code).  Exact decisions in fp32: x has 8
 // significant bits, s 4, a border between codes at most 3, so x / s either is the border
 // or differs from it by 2^-11 relative; the quotient below is within 2^-23 and exact
-// where the result is that short (one step from a rounded reciprocal: the remainder
-// x - q s is exact in an fma).  The same holds for the largest value / 6 and the borders of e4m3.
+// where the result is that short (Markstein's correction, IBM J. Res. Dev. 34 (1990) 111: one step
+// from a rounded reciprocal, as the remainder x - q s is exact in an fma).  The same holds for the largest value / 6 and the borders of e4m3.
 //
 // Bound by memory: 32749 tokens of 8 KV heads take 28.1 us (6.1 TB/s).  A block of 16 values a thread,
 // 16 CTAs per SM that walk (32: 28.6 us; as many as there are blocks: 31.3).
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 // read lies at or behind the row that it goes to: a CTA that takes its rows in order, in
 // chunks that are read before they are written, overwrites no row that is still to be read.
 // A CTA has K or V of one (request, KV head), whole rows or a slice of each, where there are
-// few; between two caches, or pages, the rows are also cut into runs.  Cache rows are looked up
+// few; between two caches, or to other pages, the rows are also cut into runs.  Cache rows are looked up
 // kMoveList at a time; a chunk is read while the one before is written.
 constexpr int kMoveThreads = 256;
 constexpr int kMovePer = 8;       // (4 with 3 or 4 CTAs per SM: 219 and 191 us where this takes 176)
@@ -675,7 +675,8 @@ cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream)
         err = launch_behind(evict_select_short_kernel<1024, 16, 1>, units, 1024, stream, a);
     if (err != cudaSuccess)
         return err;
-    // Slices of rows (in place) or runs of them (else) until there are about four CTAs per SM.
+    // In place: slices of rows, up to four, until there are two CTAs per SM, as many as are resident.  Else
+    // runs of rows, up to eight CTAs per SM: rows of different lengths end together.
     int log_slices = 0, runs = 1;
     if (a.place) {
         while (log_slices < 2 && (units * 2 << log_slices) < 2ll * sms)
